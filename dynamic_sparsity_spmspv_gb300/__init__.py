@@ -13,6 +13,10 @@ Multiplication for Dynamic GPU Workloads", ICPP '26.
     y_idx, y_val, y_nnz = spmspv(A, x_idx, x_val, ws=ws)   # per x (3.3, 4.1)
     y = spmspv_dense(A, x_dense, ws=ws)                  # decoding form (4.3)
     levels, nlev = bfs(A, src, ws=ws)                    # DB-BFS (4.2)
+
+The operators of a decoding step around that layer (4-bit linear layers,
+rotary positions, attention of drafted tokens over a cache, logit penalties)
+are in decoding.py and are exported here too.
 """
 from __future__ import annotations
 
@@ -364,6 +368,17 @@ class SpMVPlan:
             self.close()
         except Exception:
             pass
+
+
+_DECODING = ("w4_linear", "rotary_table", "rotary", "rotary_append", "tree_attention", "penalize_logits")
+
+
+def __getattr__(name):
+    """The operators of decoding.py, imported (with torch) at their first use."""
+    if name in _DECODING or (name.startswith("dbs_") and name[4:] in _DECODING):
+        from . import decoding
+        return getattr(decoding, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def library_path() -> str:

@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import _build
 
@@ -45,6 +46,12 @@ class dbs_stats(ctypes.Structure):
                 ("bfs_levels", I32), ("bfs_push_levels", I32), ("phase_ns", I64 * 3)]
 
 
+# The operators' argument structs, packed per call (names in the header, in
+# this order; native alignment).
+ROTARY_HEADS = "PP6q3i4x"
+ATTENTION_ARGS = struct.Struct("@4i2qP3q2P6q2qP2q3PfP3q2Pq")
+LOGITS_ARGS = struct.Struct("@PiqPiq2qP2q2P3P2P2qPq")
+
 # name -> (restype, argtypes)
 PROTOTYPES = {
     "dbs_build_opts_default": (None, [P]),
@@ -69,6 +76,12 @@ PROTOTYPES = {
     "dbs_spmv": (I32, [P, P, P, P]),
     "dbs_spmv_plan_info": (I32, [P, P, P]),
     "dbs_spmv_plan_destroy": (I32, [P]),
+    "dbs_w4_linear": (I32, [P, I32, I64, I64, P, I64, P, I32, I64, P, I64, I64, I64, I32, P, I64, P]),
+    "dbs_rotary_table": (I32, [I64, I32, F64, I32, F64, F64, F64, F64, P, P]),
+    "dbs_rotary": (I32, [P, I32, I32, I64, I64, I32, I32, P, I64, P, P, I64, I64, I32, I32, P]),
+    "dbs_tree_attention_scratch": (I32, [P, P]),
+    "dbs_tree_attention": (I32, [P, P]),
+    "dbs_penalize_logits": (I32, [P, P]),
     "dbs_bfs": (I32, [P, I64, P, P, ctypes.c_int, P, P]),
     "dbs_last_stats": (I32, [P, P, P]),
     "dbs_selftest_wait_timeout": (I32, [P, P]),
@@ -81,9 +94,9 @@ _lib = None
 
 
 class DbsError(RuntimeError):
-    def __init__(self, fn: str, status: int):
+    def __init__(self, fn: str, status: int, why: str = ""):
         self.status = status
-        super().__init__(f"{fn} failed: {STATUS_NAMES.get(status, status)}")
+        super().__init__(f"{fn} failed: {STATUS_NAMES.get(status, status)}" + (f" ({why})" if why else ""))
 
 
 def lib_path() -> str:

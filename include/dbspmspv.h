@@ -421,6 +421,158 @@ dbs_status dbs_spmspv_dense_noalloc(const dbs_matrix *A, const float *x, float *
  * DBS_ERR_INVALID_ARG if no call has run on this device yet. */
 dbs_status dbs_spmspv_dense_noalloc_check(void *stream);
 
+/* ---- Operators of a decoding step ----
+ *
+ * What a language model's step of one or a few (drafted) tokens needs around
+ * the DB-Decoding layer; the paper has no counterpart.  All calls are ASYNC,
+ * allocate nothing, hold no state between calls, can be captured in a CUDA
+ * graph and give identical bits when repeated.  Strides are in elements (of
+ * bytes for 4-bit codes); the innermost dimension is contiguous.  Sums,
+ * softmax statistics and rotations are fp32; every result is rounded once, to
+ * its own type. */
+typedef enum { DBS_F32 = 0, DBS_F16 = 1, DBS_BF16 = 2 } dbs_dtype;
+
+/* Linear layer with 4-bit weights and group scales, for one or a few tokens:
+ *     y[t, i] = sum_j x[t, j] * (q[i, j] - z[i, j / group]) * s[i, j / group]
+ *   x       device, `dtype`, [tokens, n], rows x_stride apart
+ *   q       device bytes, [m, ceil(n/2)], rows q_stride bytes apart: column 2c
+ *           in the low half of byte c, column 2c + 1 in the high half.  Rows
+ *           on 16-byte boundaries (q and q_stride) take the tensor-core path.
+ *   scales  device, scale_dtype, [m, ceil(n/group)], rows scale_stride apart
+ *   zeros   device bytes (0..255), the same shape, rows zero_stride apart;
+ *           NULL = 8 everywhere
+ *   group   32, 64, 128 or 256 columns; the last group may be short
+ *   y       device, `dtype`, [tokens, m], rows y_stride apart, not overlapping x
+ * fp32 x is multiplied exactly (not rounded to a shorter type).  Errors:
+ * DBS_ERR_INVALID_ARG (null pointers, sizes or strides below 0, y_stride < m,
+ * other groups or types), DBS_ERR_CUDA. */
+dbs_status dbs_w4_linear(const void *x, dbs_dtype dtype, int64_t tokens, int64_t x_stride, const uint8_t *q,
+                         int64_t q_stride, const void *scales, dbs_dtype scale_dtype, int64_t scale_stride,
+                         const uint8_t *zeros, int64_t zero_stride, int64_t m, int64_t n, int32_t group, void *y,
+                         int64_t y_stride, void *stream);
+
+/* How the angles of a rotary table are stretched for contexts longer than the
+ * model was trained on. */
+typedef enum {
+    DBS_ROTARY_PLAIN = 0,      /* f_i = base^(-2i/dim) */
+    DBS_ROTARY_LINEAR = 1,     /* f_i / factor (positions squeezed) */
+    DBS_ROTARY_NTK = 2,        /* base * factor^(dim/(dim-2)): slow pairs stretched, the fastest kept */
+    DBS_ROTARY_YARN = 3        /* pairs that turn more than beta_fast times within `trained` positions are
+                                  kept, fewer than beta_slow divided by factor, a linear ramp (over the pair
+                                  index) between; cos and sin times 0.1 ln(factor) + 1 */
+} dbs_rotary_scaling;
+
+/* Cosine and sine table of rotary positions, computed in fp64 and rounded to
+ * fp32: table[p, 0..dim/2) = cos(p f_i), table[p, dim/2..dim) = sin(p f_i).
+ *   table     device float32[positions, dim]
+ *   dim       even, 2..512; base > 1
+ *   factor    >= 1; trained, beta_fast > beta_slow > 0 only for YARN
+ * Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */
+dbs_status dbs_rotary_table(int64_t positions, int32_t dim, double base, dbs_rotary_scaling scaling, double factor,
+                            double trained, double beta_fast, double beta_slow, float *table, void *stream);
+
+/* One group of heads of a rotary call: element [b, t, h, c] is at
+ * ptr + b * batch_stride + t * token_stride + h * head_stride + c. */
+typedef struct {
+    const void *in;
+    void *out;                 /* may be `in` (in place), else must not overlap it */
+    int64_t in_batch, in_token, in_head;
+    int64_t out_batch, out_token, out_head;
+    int32_t heads;             /* 0 = absent */
+    int32_t rotate;            /* 0 = copied as it is */
+    int32_t to_slots;          /* 1 = token (b, t) goes to cache entry slots[b, t]:
+                                  out + (slot / page_size) * out_batch + (slot % page_size) * out_token */
+} dbs_rotary_heads;
+
+/* Rotates the first `dim` entries of every head by its token's position; the
+ * rest is copied.  Pairs are (i, i + dim/2), or (2i, 2i + 1) if interleaved:
+ *     a' = a cos - b sin,  b' = a sin + b cos;
+ * transposed turns the other way (sin negated), which is the gradient.
+ *   parts      1 to 3 groups of heads (q, k and, to be copied into a cache, v)
+ *   table      device float32[table_rows, dim]
+ *   positions  device int32[batch, tokens], contiguous; a token whose position
+ *              is outside the table gets NaN in its rotated entries
+ *   slots      device int32[batch, tokens], contiguous, NULL without to_slots;
+ *              tokens with a slot outside [0, pages * page_size) are not
+ *              written.  Slots in use must differ from one another.
+ *   head_dim   entries of a head, dim <= head_dim <= 1024, dim even
+ * Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */
+dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype dtype, int64_t batch, int64_t tokens,
+                      int32_t head_dim, int32_t dim, const float *table, int64_t table_rows, const int32_t *positions,
+                      const int32_t *slots, int64_t pages, int64_t page_size, int32_t interleaved,
+                      int32_t transposed, void *stream);
+
+/* Attention of drafted tokens over a cache (one token: plain decoding).
+ * Sequence b holds kv_lens[b] entries; the last tree_lens[b] of them are its
+ * drafted tokens, in the order of q's tokens.  Token t sees every earlier entry
+ * and those drafted ones whose bit is set: entry kv_lens[b] - tree_lens[b] + i
+ * is seen iff bit i % 64 of tree[b, t, i / 64] is set (tree NULL: iff i <= t).
+ *     out[b, t, h] = sum_j softmax_j(scale q[b,t,h].k[j, h / G]) v[j, h / G]
+ * over the entries it sees, G = q_heads / kv_heads.  A token that sees none
+ * gets 0 and lse -inf, and so do the tokens t >= tree_lens[b].  Entries that
+ * are not seen take no part, whatever they hold (NaN included). */
+typedef struct {
+    dbs_dtype dtype;           /* DBS_F16 or DBS_BF16, of q, caches and out */
+    int32_t head_dim;          /* 1..256 */
+    int32_t q_heads, kv_heads; /* q_heads a multiple of kv_heads */
+    int64_t batch, tokens;     /* q holds `tokens` per sequence, 0..1024 */
+    const void *q;             /* [batch, tokens, q_heads, head_dim] */
+    int64_t q_batch, q_token, q_head;
+    const void *k, *v;         /* [pages, page_size, kv_heads, head_dim] */
+    int64_t k_page, k_entry, k_head;
+    int64_t v_page, v_entry, v_head;
+    int64_t pages, page_size;
+    const int32_t *page_table; /* device [batch, max_pages], rows page_row apart: page of entry
+                                  j is page_table[b, j / page_size], clamped to [0, pages);
+                                  NULL: sequence b is page b */
+    int64_t max_pages, page_row;
+    const int32_t *kv_lens;    /* device [batch]; clamped to [0, max_pages * page_size] */
+    const int32_t *tree_lens;  /* device [batch]; clamped to [0, tokens]; NULL = tokens */
+    const int64_t *tree;       /* device [batch, tokens, ceil(tokens / 64)], contiguous, or NULL */
+    float scale;               /* finite */
+    void *out;                 /* [batch, tokens, q_heads, head_dim] */
+    int64_t o_batch, o_token, o_head;
+    float *lse;                /* device [batch, tokens, q_heads], natural logarithm, or NULL */
+    void *scratch;             /* device, 16-byte aligned, dbs_tree_attention_scratch bytes; the
+                                  call leaves nothing in it that a later call reads */
+    int64_t scratch_bytes;
+} dbs_attention_args;
+
+/* Bytes of scratch that dbs_tree_attention needs for these sizes. */
+dbs_status dbs_tree_attention_scratch(const dbs_attention_args *a, int64_t *bytes);
+/* Errors: DBS_ERR_INVALID_ARG (null pointers, sizes, strides, types),
+ * DBS_ERR_CUDA. */
+dbs_status dbs_tree_attention(const dbs_attention_args *a, void *stream);
+
+/* Penalties for repeated tokens, biases and a grammar's mask on logits; in this
+ * order for row b and token v:
+ *   v among history[b, 0..history_lens[b]):   l = l > 0 ? l / repetition : l * repetition
+ *   c times from prompt_lens[b] on, c > 0:    l = l - (frequency * c + presence)
+ *   v in bias_ids[b]:                         l = l + bias (listed again: added again, in the list's order)
+ *   bit v % 32 of allowed[b, v / 32] clear:   l = -inf
+ * Absent parts (NULL) are left out; ids outside [0, vocab) are skipped. */
+typedef struct {
+    const void *logits;        /* device [batch, vocab], rows logits_stride apart */
+    dbs_dtype dtype;
+    int64_t logits_stride;
+    void *out;                 /* device [batch, vocab], out_dtype; may be logits (same type and stride) */
+    dbs_dtype out_dtype;
+    int64_t out_stride;
+    int64_t batch, vocab;      /* vocab < 2^31 */
+    const int32_t *history;    /* device [batch, history_max], rows history_stride apart */
+    int64_t history_max, history_stride;
+    const int32_t *history_lens;  /* device [batch], clamped to [0, history_max]; NULL = history_max */
+    const int32_t *prompt_lens;   /* device [batch]; NULL = 0: everything is output */
+    const float *repetition, *presence, *frequency;   /* device [batch] each, or NULL */
+    const int32_t *bias_ids;   /* device [batch, biases], rows bias_stride apart (the values' too) */
+    const float *bias_vals;
+    int64_t biases, bias_stride;
+    const int32_t *allowed;    /* device [batch, ceil(vocab / 32)], rows allowed_stride apart */
+    int64_t allowed_stride;
+} dbs_logits_args;
+/* Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */
+dbs_status dbs_penalize_logits(const dbs_logits_args *a, void *stream);
+
 /* Test hook (the paper has no counterpart): injects one allocation failure.
  * The k-th allocation attempt from now on (k = 0: the next one) fails as if
  * memory were exhausted -- device allocations (cudaMalloc) and the host
