@@ -2,7 +2,8 @@
 
 nvcc compiles the CUDA translation unit for sm_103a only; g++ compiles the
 host builder; both run in parallel and nvcc links the shared library against
-the static CUDA runtime.
+the static CUDA runtime.  Beside it g++ builds _dbsops.so, the Python binding of
+the decoding step's operators, against the installed torch.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libdbspmspv.so")
+OPS = os.path.join(OUT, "_dbsops.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
@@ -21,6 +23,12 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 SOURCES_CU = ["kernels.cu", "spmv.cu", "build_gpu.cu", "w4.cu", "rotary.cu", "attention.cu", "logits.cu"]
 SOURCES_CPP = ["matrix.cpp"]
+
+
+def _torch_dir() -> str:
+    """Where torch is installed, without importing it."""
+    import importlib.util
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
 
 
 def _newest_input() -> float:
@@ -34,8 +42,10 @@ def _newest_input() -> float:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _newest_input() for p in (LIB, OPS)):
         return LIB
+    import sysconfig
+    torch_dir = _torch_dir()
     procs = []
     objs = []
     for src in SOURCES_CU:
@@ -52,6 +62,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
                "-I", os.path.join(CUDA_HOME, "include"), "-c", os.path.join(CSRC, src), "-o", obj]
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         objs.append(obj)
+    ops_obj = os.path.join(OUT, "binding.cpp.o")
+    cmd = ["g++", "-O1", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(torch_dir, "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(CUDA_HOME, "include"),
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", ops_obj]
+    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for cmd, p in procs:
         out, _ = p.communicate()
@@ -64,6 +79,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lpthread"])
     os.replace(tmp, LIB)
+    tmp = OPS + f".tmp{os.getpid()}"
+    subprocess.check_call(["g++", "-shared", "-o", tmp, ops_obj, "-L", OUT, "-l:libdbspmspv.so", "-Wl,-rpath,$ORIGIN",
+                           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, OPS)
     return LIB
 
 

@@ -17,6 +17,13 @@ struct W4 {
     int32_t group;
 };
 
+// 16-byte loads of x: every token's row on such a boundary.
+template <class T>
+__device__ __forceinline__ bool aligned_x(const T *x, int64_t stride)
+{
+    return (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (stride * sizeof(T) & 15u) == 0;
+}
+
 constexpr int ROWS_NT = 128;     // four warps, one row each
 constexpr int ROWS_TOK = 4;      // tokens a warp carries at a time
 
@@ -35,7 +42,7 @@ __global__ void __launch_bounds__(ROWS_NT) k_w4_rows(W4 A)
         float acc[ROWS_TOK] = {};
         for (int64_t c = lane; c < bytes; c += 32) {
             const int64_t j = 2 * c, g = j / A.group;
-            const float sc = to_f32(s[g]), zp = z ? (float)z[g] : 8.f;
+            const float sc = to_f32(s[g]), zp = z ? (float)(z[g] & 127) : 8.f;
             const unsigned b = q[c];
             const float w0 = ((float)(b & 15u) - zp) * sc, w1 = ((float)(b >> 4) - zp) * sc;
 #pragma unroll
@@ -55,20 +62,375 @@ __global__ void __launch_bounds__(ROWS_NT) k_w4_rows(W4 A)
     }
 }
 
-template <class T, class S>
-void launch(const W4 &A, cudaStream_t s)
+// ---- rows on 16-byte boundaries: tensor cores ----
+//
+// A matrix instruction takes 16 rows of codes (A, 16 x 16) and 8 columns of x
+// (B, 16 x 8): the columns are tokens, or, for fp32 x, the three 8-bit pieces
+// hi + mid + lo whose sum is x exactly (truncated splits of its 24 bits), so
+// fp32 costs three columns a token and loses nothing.  Codes become numbers in
+// registers: with a nibble in the low mantissa bits, 128 + q in bf16 (1024 + q
+// in fp16) is one AND-OR of a word's nibble pair, and subtracting 128 + z gives
+// q - z exactly.  Which column of x a fragment's slot stands for is free as long
+// as A and B agree: a lane's word holds 8 neighbouring columns, paired (0, 4),
+// (1, 5), (2, 6), (3, 7) as they lie in the word, and x is laid out to match.
+// Groups' sums are fp32 accumulators, multiplied by the scale in fp32.
+template <class T> struct Half2;
+template <> struct Half2<__half> {
+    static constexpr uint32_t magic = 0x64006400u, one = 0x00010001u;   // 1024 + q
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+    {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+template <> struct Half2<__nv_bfloat16> {
+    static constexpr uint32_t magic = 0x43004300u, one = 0x00010001u;   // 128 + q
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b)
+    {
+        // a * 1 - b in one rounding, exact here
+        uint32_t r;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+    {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+
+// The matrix type of x's type, and its columns per token.
+template <class T> struct Piece { using type = T; static constexpr int parts = 1; };
+template <> struct Piece<float> { using type = __nv_bfloat16; static constexpr int parts = 3; };
+
+constexpr int MMA_NT = 256, MMA_W = MMA_NT / 32;
+constexpr int STEP = 128;                      // columns of a stage: 64 bytes of a row
+__host__ __device__ constexpr int stages_of(int rt) { return rt == 1 ? 4 : 3; }
+
+// How a call is cut up.
+struct Cut {
+    int wk;                    // warps of a block that share a row tile and take turns of its stages
+    int steps, phase;          // stages of a row; stages whose x is in shared memory at a time
+    int cols;                  // columns of B in use: tokens of a pass * parts
+    int64_t groups;            // of rows: a block's rows at a time
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes)
 {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Eight neighbouring values of x as the pairs (0, 4), (1, 5), (2, 6), (3, 7).
+template <class T>
+__device__ __forceinline__ void lay_out(const T *x, int64_t j, int64_t n, bool wide, uint4 (&out)[1])
+{
+    uint16_t v[8];
+    if (wide && j + 8 <= n) {
+        const uint4 u = *(const uint4 *)(x + j);
+        *(uint4 *)v = u;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = j + e < n ? *(const uint16_t *)(x + j + e) : (uint16_t)0;
+    }
+    out[0] = make_uint4(v[0] | (uint32_t)v[4] << 16, v[1] | (uint32_t)v[5] << 16, v[2] | (uint32_t)v[6] << 16, v[3] | (uint32_t)v[7] << 16);
+}
+
+// The same of fp32: the upper 8 bits of each value, the next 8, the last 8, each
+// a bf16.  What is not finite goes into the first piece alone.
+__device__ __forceinline__ void lay_out(const float *x, int64_t j, int64_t n, bool wide, uint4 (&out)[3])
+{
+    float v[8];
+    if (wide && j + 8 <= n) {
+        *(float4 *)v = *(const float4 *)(x + j);
+        *(float4 *)(v + 4) = *(const float4 *)(x + j + 4);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = j + e < n ? x[j + e] : 0.f;
+    }
+    uint32_t w[3][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t hi[2], mid[2], lo[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float f = v[e + 4 * k];
+            uint32_t b = __float_as_uint(f);
+            const bool fin = (b & 0x7f800000u) != 0x7f800000u;
+            if (!fin && (b & 0x007fffffu)) b |= 0x00400000u;               // a NaN stays one
+            hi[k] = b & 0xffff0000u;
+            const float r1 = fin ? f - __uint_as_float(hi[k]) : 0.f;
+            mid[k] = __float_as_uint(r1) & 0xffff0000u;
+            lo[k] = __float_as_uint(r1 - __uint_as_float(mid[k]));
+        }
+        w[0][e] = hi[0] >> 16 | hi[1];
+        w[1][e] = mid[0] >> 16 | mid[1];
+        w[2][e] = lo[0] >> 16 | (lo[1] & 0xffff0000u);
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) out[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+
+// One block takes groups of rows in turn; each warp streams stages of RT row
+// tiles (16 rows) through its own ring of shared memory (cp.async, no
+// block-wide wait), against x in shared memory.
+template <class T, class S, int NT, int RT>
+__global__ void __launch_bounds__(MMA_NT, 2) k_w4_mma(W4 A, Cut C)
+{
+    using P = Piece<T>;
+    using H = Half2<typename P::type>;
+    constexpr int NS = stages_of(RT), TILE = 16 * STEP / 2, STAGE = RT * TILE;
+    extern __shared__ __align__(128) unsigned char sm[];
+    float *red = (float *)(sm + MMA_W * NS * STAGE);
+    uint4 *xs = (uint4 *)(sm + MMA_W * NS * STAGE + MMA_W * RT * 16 * NT * 8 * 4);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+    const int wk = warp % C.wk, wr = warp / C.wk, wrs = MMA_W / C.wk;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm) + warp * NS * STAGE;
+    const unsigned char *ringp = sm + warp * NS * STAGE;
+    const int64_t bytes = (A.n + 1) >> 1;
+    const int64_t t0 = (int64_t)blockIdx.y * (NT * 8 / P::parts);            // the pass's first token
+    const int64_t left = A.tokens - t0;
+    const int tokens = (int)(left < NT * 8 / P::parts ? left : NT * 8 / P::parts), cols = tokens * P::parts;
+    const T *x = (const T *)A.x + t0 * A.x_stride;
+    const bool wide = aligned_x(x, A.x_stride);
+    const int last_group = (int)((A.n + A.group - 1) / A.group) - 1;
+    const uint32_t apply = A.group == 32 ? 0xfu : A.group == 64 ? 0xau : 0x8u;   // words that end a group
+
+    // the stages to fetch run ahead of the stages in use, across groups of rows
+    int64_t fg = wk < C.steps ? blockIdx.x : C.groups;
+    int fs = wk, slot = 0;
+    auto fetch = [&]() {
+        if (fg < C.groups) {
+            const int64_t row0 = (fg * wrs + wr) * (16 * RT);
+            const int64_t b0 = (int64_t)fs * (STEP / 2);
+#pragma unroll
+            for (int i = 0; i < 2 * RT; ++i) {
+                const int r = i * 8 + (lane >> 2), c = lane & 3;
+                const int64_t row = row0 + r, at = b0 + c * 16;
+                const int64_t rest = bytes - at;
+                const int take = row < A.m && rest > 0 ? (rest < 16 ? (int)rest : 16) : 0;
+                cp16(ring + slot * STAGE + r * 64 + ((c ^ ((r >> 1) & 3)) << 4), A.q + (take ? row * A.q_stride + at : 0), take);
+            }
+            fs += C.wk;
+            if (fs >= C.steps) {
+                fs = wk;
+                fg += gridDim.x;
+            }
+        }
+        slot = slot + 1 == NS ? 0 : slot + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // scales and zero points of a stage: lane t4 holds those of its 32 columns
+    auto constants = [&](int64_t grp, int st, float (&s)[RT][2], uint32_t (&z)[RT][2]) {
+        const int64_t row0 = (grp * wrs + wr) * (16 * RT);
+        int gi = (int)(((int64_t)st * STEP + 32 * t4) / A.group);
+        gi = gi < last_group ? gi : last_group;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                int64_t row = row0 + 16 * r + 8 * h + g;
+                row = row < A.m ? row : A.m - 1;
+                s[r][h] = to_f32(((const S *)A.scales)[row * A.scale_stride + gi]);
+                const uint32_t zp = A.zeros ? A.zeros[row * A.zero_stride + gi] & 127u : 8u;
+                z[r][h] = H::magic + zp * H::one;
+            }
+    };
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i) fetch();
+    float sn[RT][2];
+    uint32_t zn[RT][2];
+    if (wk < C.steps && blockIdx.x < C.groups) constants(blockIdx.x, wk, sn, zn);
+
+    int use = 0;
+    bool have = false;
+    for (int64_t grp = blockIdx.x; grp < C.groups; grp += gridDim.x) {
+        float tot[RT][NT][4];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tot[r][c][e] = 0.f;
+        for (int p0 = 0; p0 < C.steps; p0 += C.phase) {
+            const int p1 = p0 + C.phase < C.steps ? p0 + C.phase : C.steps;
+            if (!have || C.phase < C.steps) {
+                // x of this phase: piece (32-column block, column, quarter) at
+                // [block][column][quarter], 16 bytes each
+                if (have) __syncthreads();
+                const int quarters = (p1 - p0) * (STEP / 8);
+                for (int i = threadIdx.x; i < quarters * tokens; i += MMA_NT) {
+                    const int tok = i / quarters, k = i % quarters;
+                    uint4 v[P::parts];
+                    lay_out(x + tok * A.x_stride, (int64_t)p0 * STEP + 8 * k, A.n, wide, v);
+#pragma unroll
+                    for (int p = 0; p < P::parts; ++p) xs[((k >> 2) * cols + tok * P::parts + p) * 4 + (k & 3)] = v[p];
+                }
+                __syncthreads();
+                have = true;
+            }
+            // phases are whole turns of the warps, so turns go on across them
+            for (int st = p0 + wk; st < p1; st += C.wk) {
+                float sc[RT][2];
+                uint32_t zc[RT][2];
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        sc[r][h] = sn[r][h];
+                        zc[r][h] = zn[r][h];
+                    }
+                fetch();
+                if (st + C.wk < C.steps) constants(grp, st + C.wk, sn, zn);
+                else if (grp + gridDim.x < C.groups) constants(grp + gridDim.x, wk, sn, zn);
+                asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
+                __syncwarp();
+                const unsigned char *w = ringp + use * STAGE;
+                use = use + 1 == NS ? 0 : use + 1;
+                float part[RT][NT][4];
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) part[r][c][e] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint4 b[NT];
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+                        b[c] = 8 * c + g < cols ? xs[(((st - p0) * 4 + j) * cols + 8 * c + g) * 4 + t4] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const int src = (lane & ~3) | j;
+                        const uint32_t za = __shfl_sync(~0u, zc[r][0], src), zb = __shfl_sync(~0u, zc[r][1], src);
+                        const int o = ((j ^ ((g >> 1) & 3)) << 4) + 4 * t4;
+                        const uint32_t wa = *(const uint32_t *)(w + r * TILE + g * 64 + o), wb = *(const uint32_t *)(w + r * TILE + (g + 8) * 64 + o);
+                        uint32_t a[4];
+                        a[0] = H::sub((wa & 0x000f000fu) | H::magic, za);
+                        a[1] = H::sub((wb & 0x000f000fu) | H::magic, zb);
+                        a[2] = H::sub((wa >> 4 & 0x000f000fu) | H::magic, za);
+                        a[3] = H::sub((wb >> 4 & 0x000f000fu) | H::magic, zb);
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) H::mma(part[r][c], a, b[c].x, b[c].y);
+                        a[0] = H::sub((wa >> 8 & 0x000f000fu) | H::magic, za);
+                        a[1] = H::sub((wb >> 8 & 0x000f000fu) | H::magic, zb);
+                        a[2] = H::sub((wa >> 12 & 0x000f000fu) | H::magic, za);
+                        a[3] = H::sub((wb >> 12 & 0x000f000fu) | H::magic, zb);
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) H::mma(part[r][c], a, b[c].z, b[c].w);
+                        if (apply >> j & 1u) {
+                            const float sa = __shfl_sync(~0u, sc[r][0], src), sb = __shfl_sync(~0u, sc[r][1], src);
+#pragma unroll
+                            for (int c = 0; c < NT; ++c) {
+                                tot[r][c][0] = fmaf(sa, part[r][c][0], tot[r][c][0]);
+                                tot[r][c][1] = fmaf(sa, part[r][c][1], tot[r][c][1]);
+                                tot[r][c][2] = fmaf(sb, part[r][c][2], tot[r][c][2]);
+                                tot[r][c][3] = fmaf(sb, part[r][c][3], tot[r][c][3]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) part[r][c][e] = 0.f;
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        // sums of the warps of a row tile and of the pieces of a token, in order
+        float *mine = red + warp * (RT * 16 * NT * 8);
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                // [column][row]
+                float *d = mine + (8 * c + 2 * t4) * (RT * 16) + 16 * r + g;
+                d[0] = tot[r][c][0];
+                d[RT * 16] = tot[r][c][1];
+                d[8] = tot[r][c][2];
+                d[RT * 16 + 8] = tot[r][c][3];
+            }
+        __syncthreads();
+        const int rows = wrs * RT * 16;
+        for (int i = threadIdx.x; i < rows * tokens; i += MMA_NT) {
+            const int tok = i / rows, rr = i % rows, wr2 = rr / (RT * 16), r = rr % (RT * 16);
+            const int64_t row = grp * rows + rr;
+            float v = 0.f;
+            for (int k = 0; k < C.wk; ++k)
+#pragma unroll
+                for (int p = 0; p < P::parts; ++p)
+                    v += red[(wr2 * C.wk + k) * (RT * 16 * NT * 8) + (tok * P::parts + p) * (RT * 16) + r];
+            if (row < A.m) ((T *)A.y)[(t0 + tok) * A.y_stride + row] = from_f32<T>(v);
+        }
+        __syncthreads();
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Shared memory of a block, so that two of them fit an SM.
+constexpr int SMEM_MAX = 113 * 1024;
+__host__ __device__ constexpr int fixed_smem(int nt, int rt) { return MMA_W * stages_of(rt) * rt * 16 * STEP / 2 + MMA_W * rt * 16 * nt * 8 * 4; }
+
+template <class T, class S, int NT, int RT>
+dbs_status launch_mma(const W4 &A, cudaStream_t s)
+{
+    constexpr int parts = Piece<T>::parts, pass = NT * 8 / parts;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(k_w4_mma<T, S, NT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess) {
+        cudaGetLastError();
+        return DBS_ERR_CUDA;
+    }
+    Cut C{};
+    C.steps = (int)((A.n + STEP - 1) / STEP);
+    C.cols = (int)((A.tokens < pass ? A.tokens : pass) * parts);
+    const int step_bytes = STEP * C.cols * 2;
+    C.wk = MMA_W;
+    C.phase = (SMEM_MAX - fixed_smem(NT, RT)) / step_bytes;
+    if (C.phase >= C.steps) {
+        C.phase = C.steps;
+    } else {
+        // x does not fit at once: few warps share a row tile, so that a phase is long for each
+        C.wk = 2;
+        C.phase = C.phase / C.wk * C.wk;
+    }
+    const int rows = MMA_W / C.wk * RT * 16;
+    C.groups = (A.m + rows - 1) / rows;
+    const int64_t grid = C.groups < 2 * sms ? C.groups : 2 * sms;
+    const int64_t passes = (A.tokens + pass - 1) / pass;
+    const int smem = fixed_smem(NT, RT) + (C.phase < C.steps ? C.phase : C.steps) * step_bytes;
+    W4 B = A;
+    for (int64_t p = 0; p < passes; p += 32768) {
+        const int64_t now = passes - p < 32768 ? passes - p : 32768;
+        B.x = (const T *)A.x + p * pass * A.x_stride;
+        B.y = (T *)A.y + p * pass * A.y_stride;
+        B.tokens = A.tokens - p * pass;
+        k_w4_mma<T, S, NT, RT><<<dim3((unsigned)grid, (unsigned)now), MMA_NT, smem, s>>>(B, C);
+    }
+    return launched();
+}
+
+template <class T, class S>
+dbs_status launch(const W4 &A, cudaStream_t s)
+{
+    if (A.n > 0 && aligned16(A.q) && (A.q_stride & 15) == 0) {
+        const int64_t cols = A.tokens * Piece<T>::parts;
+        return cols <= 8 ? launch_mma<T, S, 1, 1>(A, s) : cols <= 16 ? launch_mma<T, S, 2, 2>(A, s) : launch_mma<T, S, 3, 2>(A, s);
+    }
     const int64_t chunks = (A.tokens + ROWS_TOK - 1) / ROWS_TOK;
     const dim3 grid((unsigned)((A.m + ROWS_NT / 32 - 1) / (ROWS_NT / 32)), (unsigned)(chunks < 65535 ? chunks : 65535));
     k_w4_rows<T, S><<<grid, ROWS_NT, 0, s>>>(A);
+    return launched();
 }
 
 template <class T>
-void launch_scales(const W4 &A, dbs_dtype sd, cudaStream_t s)
+dbs_status launch_scales(const W4 &A, dbs_dtype sd, cudaStream_t s)
 {
-    if (sd == DBS_F32) launch<T, float>(A, s);
-    else if (sd == DBS_F16) launch<T, __half>(A, s);
-    else launch<T, __nv_bfloat16>(A, s);
+    return sd == DBS_F32 ? launch<T, float>(A, s) : sd == DBS_F16 ? launch<T, __half>(A, s) : launch<T, __nv_bfloat16>(A, s);
 }
 
 }  // namespace
@@ -87,8 +449,7 @@ extern "C" dbs_status dbs_w4_linear(const void *x, dbs_dtype dtype, int64_t toke
         return DBS_ERR_INVALID_ARG;
     const W4 A{x, q, scales, zeros, y, tokens, x_stride, q_stride, scale_stride, zero_stride, m, n, y_stride, group};
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == DBS_F32) launch_scales<float>(A, scale_dtype, s);
-    else if (dtype == DBS_F16) launch_scales<__half>(A, scale_dtype, s);
-    else launch_scales<__nv_bfloat16>(A, scale_dtype, s);
-    return launched();
+    return dtype == DBS_F32   ? launch_scales<float>(A, scale_dtype, s)
+           : dtype == DBS_F16 ? launch_scales<__half>(A, scale_dtype, s)
+                              : launch_scales<__nv_bfloat16>(A, scale_dtype, s);
 }

@@ -439,8 +439,8 @@ typedef enum { DBS_F32 = 0, DBS_F16 = 1, DBS_BF16 = 2 } dbs_dtype;
  *           in the low half of byte c, column 2c + 1 in the high half.  Rows
  *           on 16-byte boundaries (q and q_stride) take the tensor-core path.
  *   scales  device, scale_dtype, [m, ceil(n/group)], rows scale_stride apart
- *   zeros   device bytes (0..255), the same shape, rows zero_stride apart;
- *           NULL = 8 everywhere
+ *   zeros   device bytes, of which the low 7 bits count (0..127), the same shape,
+ *           rows zero_stride apart; NULL = 8 everywhere
  *   group   32, 64, 128 or 256 columns; the last group may be short
  *   y       device, `dtype`, [tokens, m], rows y_stride apart, not overlapping x
  * fp32 x is multiplied exactly (not rounded to a shorter type).  Errors:
