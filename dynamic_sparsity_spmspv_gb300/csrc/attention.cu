@@ -17,7 +17,7 @@ struct Attn {
 
 // What sequence b holds, with every length clamped to its range.
 struct Seq {
-    int64_t kv, first;         // entries; index of the first drafted one (may be < 0)
+    int kv, first;             // entries; index of the first drafted one (may be < 0)
     int tree;                  // drafted tokens
 };
 
@@ -27,17 +27,24 @@ __device__ __forceinline__ Seq sequence(const Attn &A, int64_t b)
     Seq s;
     const int64_t room = a.max_pages * a.page_size;
     int64_t kv = a.kv_lens[b], t = a.tree_lens ? a.tree_lens[b] : a.tokens;
-    s.kv = kv < 0 ? 0 : kv > room ? room : kv;
+    s.kv = (int)(kv < 0 ? 0 : kv > room ? room : kv);
     s.tree = (int)(t < 0 ? 0 : t > a.tokens ? a.tokens : t);
     s.first = s.kv - s.tree;
     return s;
 }
 
-__device__ __forceinline__ int64_t page_of(const dbs_attention_args &a, int64_t b, int64_t j)
+// Where entry j of sequence b lies: its page, and its place in it.
+struct Place {
+    int64_t page;
+    uint32_t in;
+};
+
+__device__ __forceinline__ Place place_of(const dbs_attention_args &a, int64_t b, int j)
 {
-    if (!a.page_table) return b;
-    const int64_t p = a.page_table[b * a.page_row + j / a.page_size];
-    return p < 0 ? 0 : p >= a.pages ? a.pages - 1 : p;
+    if (!a.page_table) return {b, (uint32_t)j};
+    const uint32_t size = (uint32_t)a.page_size, n = (uint32_t)j / size;
+    const int64_t p = a.page_table[b * a.page_row + n];
+    return {p < 0 ? 0 : p >= a.pages ? a.pages - 1 : p, (uint32_t)j - n * size};
 }
 
 // Whether token t of sequence b sees drafted entry i (0 <= i < tree).
@@ -65,32 +72,32 @@ __device__ __forceinline__ Row row_of(const Attn &A, int hk, int64_t R)
 
 // Visibility of the 32 entries from drafted index `node` on (bit k: entry
 // node + k) for token t.  Entries below 0 are the earlier part of the cache.
-__device__ __forceinline__ uint32_t sees32(const Attn &A, int64_t b, int t, int tree, int64_t node)
+__device__ __forceinline__ uint32_t sees32(const Attn &A, int64_t b, int t, int tree, int node)
 {
     if (t >= tree || node >= tree) return 0u;
     if (node <= -32) return ~0u;
     uint32_t m;
     if (!A.a.tree) {
-        const int64_t n = t - node + 1;                  // the first n entries
+        const int n = t - node + 1;                  // the first n entries
         m = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
     } else {
         const uint64_t *w = (const uint64_t *)A.a.tree + (b * A.a.tokens + t) * A.words;
         if (node < 0) {
             m = (uint32_t)(w[0] << -node) | ((1u << -node) - 1u);
         } else {
-            const int i = (int)node >> 6, sh = (int)node & 63;
+            const int i = node >> 6, sh = node & 63;
             uint64_t v = w[i] >> sh;
             if (sh > 32 && i + 1 < A.words) v |= w[i + 1] << (64 - sh);
             m = (uint32_t)v;
         }
     }
-    const int64_t left = tree - node;                    // drafted entries end here
+    const int left = tree - node;                    // drafted entries end here
     return left >= 32 ? m : m & ((1u << left) - 1u);
 }
 
 // One query row by one warp, entry by entry, touching only what the row sees.
 template <class T>
-__device__ __forceinline__ void row_by_warp(const Attn &A, int64_t b, int t, int h, int64_t j0, int step, float &m, float &l,
+__device__ __forceinline__ void row_by_warp(const Attn &A, int64_t b, int t, int h, int j0, int step, float &m, float &l,
                                          float (&o)[8])
 {
     const dbs_attention_args &a = A.a;
@@ -106,11 +113,11 @@ __device__ __forceinline__ void row_by_warp(const Attn &A, int64_t b, int t, int
         o[e] = 0.f;
     }
     if (t >= s.tree) return;
-    for (int64_t j = j0; j < s.kv; j += step) {
-        if (j >= s.first && !sees(A, b, t, (int)(j - s.first))) continue;
-        const int64_t p = page_of(a, b, j), in = a.page_table ? j % a.page_size : j;
-        const T *k = (const T *)a.k + p * a.k_page + in * a.k_entry + hk * a.k_head;
-        const T *v = (const T *)a.v + p * a.v_page + in * a.v_entry + hk * a.v_head;
+    for (int j = j0; j < s.kv; j += step) {
+        if (j >= s.first && !sees(A, b, t, j - s.first)) continue;
+        const Place at = place_of(a, b, j);
+        const T *k = (const T *)a.k + at.page * a.k_page + at.in * a.k_entry + hk * a.k_head;
+        const T *v = (const T *)a.v + at.page * a.v_page + at.in * a.v_entry + hk * a.v_head;
         float x = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -156,10 +163,10 @@ __device__ __noinline__ void add_odd(const Attn &A, int64_t b, int t, int hk, fl
     const dbs_attention_args &a = A.a;
     const int lane = threadIdx.x & 31;
     const Seq s = sequence(A, b);
-    for (int i = s.first < 0 ? (int)-s.first : 0; i < s.tree; ++i) {
+    for (int i = s.first < 0 ? -s.first : 0; i < s.tree; ++i) {
         if (!sees(A, b, t, i)) continue;
-        const int64_t j = s.first + i, p = page_of(a, b, j), in = a.page_table ? j % a.page_size : j;
-        const T *v = (const T *)a.v + p * a.v_page + in * a.v_entry + hk * a.v_head;
+        const Place at = place_of(a, b, s.first + i);
+        const T *v = (const T *)a.v + at.page * a.v_page + at.in * a.v_entry + hk * a.v_head;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (lane + 32 * e < a.head_dim) {
@@ -242,11 +249,11 @@ struct Line {
     int64_t total, at;         // tiles of all; tiles before sequence b
 };
 
-__device__ __forceinline__ int64_t tiles_of(const Attn &A, const Share &S, int64_t b)
+__device__ __forceinline__ int tiles_of(const Share &S, const Seq &s)
 {
-    const int64_t kv = sequence(A, b).kv;
-    return kv <= S.keys ? 1 : (kv + S.keys - 1) / S.keys;
+    return s.kv <= S.keys ? 1 : (int)((uint32_t)(s.kv + S.keys - 1) / (uint32_t)S.keys);
 }
+__device__ __forceinline__ int64_t tiles_of(const Attn &A, const Share &S, int64_t b) { return tiles_of(S, sequence(A, b)); }
 
 // Sum of `v` over the block (every thread gets it); `red` holds a word per warp.
 template <int NT>
@@ -338,7 +345,8 @@ __device__ __forceinline__ float *slot_of(const Attn &A, const Share &S, int64_t
 constexpr int JOIN_NT = 128;
 
 // Joins the parts of a unit that more than one block worked on; one warp per
-// row, the parts in the order of the cache.
+// row.  The parts' maxima and sums are read by the lanes at once, their outputs
+// in the order of the cache.
 template <class T>
 __global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int grid)
 {
@@ -346,37 +354,55 @@ __global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int grid
     __shared__ int64_t red[JOIN_NT / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t per = (int64_t)a.kv_heads * S.groups;
-    const int64_t b = blockIdx.x / per, u = blockIdx.x % per;
+    const uint32_t per = (uint32_t)a.kv_heads * S.groups;
+    const uint32_t b = blockIdx.x / per, u = blockIdx.x % per;
     const Line L = line_at<JOIN_NT>(A, S, b, red);
-    const int64_t n = tiles_of(A, S, b), x0 = L.at + u * n;
+    const Seq s = sequence(A, b);
+    const int n = tiles_of(S, s);
+    const int64_t x0 = L.at + (int64_t)u * n;
     const int64_t blocks = L.total < grid ? L.total : grid;
     const int64_t c0 = block_of(L.total, x0, blocks), c1 = block_of(L.total, x0 + n - 1, blocks);
     if (c0 == c1) return;
-    const int hk = (int)(u / S.groups);
-    const int64_t R0 = u % S.groups * S.rows;
-    const int tree = sequence(A, b).tree;
-    const int r = blockIdx.y * (JOIN_NT / 32) + warp;
+    const int hk = (int)(u / S.groups), r = blockIdx.y * (JOIN_NT / 32) + warp;
     if (r >= S.rows) return;
-    const Row row = row_of(A, hk, R0 + r);
+    const Row row = row_of(A, hk, (int64_t)(u % S.groups) * S.rows + r);
     if (!row.inside) return;
     float top = -INFINITY, sum = 0.f, o[8] = {};
-    if (row.t < tree) {
-        bool odd = false;
-        for (int64_t c = c0; c <= c1; ++c) {
-            const float *p = slot_of(A, S, c, piece(L.total, c, blocks) >= x0 ? 0 : 1);
-            const float *st = p + (int64_t)S.rows * a.head_dim;
-            const float m = st[r], l = st[S.rows + r];
-            odd |= st[2 * S.rows] != 0.f;
-            const float now = fmaxf(top, m);
-            const float keep = top == -INFINITY ? 0.f : exp2f(top - now), f = m == -INFINITY ? 0.f : exp2f(m - now);
-            sum = sum * keep + (l != l ? l : f * l);
-            top = now;
+    if (row.t < s.tree) {
+        const int parts = (int)(c1 - c0) + 1;
+        const int64_t size = slot_floats(S.rows, a.head_dim);
+        // the unit may be the second of its first block, and is the first of the others
+        const float *p0 = slot_of(A, S, c0, piece(L.total, c0, blocks) >= x0 ? 0 : 1), *rest = slot_of(A, S, c0, 0);
+        const int64_t stat = (int64_t)S.rows * a.head_dim;
+        for (int i = lane; i < parts; i += 32) top = fmaxf(top, (i ? rest + 2 * size * i : p0)[stat + r]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (lane + 32 * e < a.head_dim) o[e] = o[e] * keep + (f == 0.f ? 0.f : f * p[(int64_t)r * a.head_dim + lane + 32 * e]);
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        bool odd = false;
+        for (int base = 0; base < parts; base += 32) {
+            float f = 0.f, l = 0.f;
+            if (base + lane < parts) {
+                const float *st = (base + lane ? rest + 2 * size * (base + lane) : p0) + stat;
+                const float m = st[r];
+                l = st[S.rows + r];
+                odd |= st[2 * S.rows] != 0.f;
+                f = m == -INFINITY ? 0.f : exp2f(m - top);
+                l = l != l ? l : f * l;
+            }
+            const int now = parts - base < 32 ? parts - base : 32;
+#pragma unroll 4
+            for (int i = 0; i < now; ++i) {
+                const float fi = __shfl_sync(~0u, f, i), li = __shfl_sync(~0u, l, i);
+                const float *p = (base + i ? rest + 2 * size * (base + i) : p0) + (int64_t)r * a.head_dim;
+                sum += li;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (lane + 32 * e < a.head_dim) {
+                        const float v = p[lane + 32 * e];
+                        o[e] += fi == 0.f ? 0.f : fi * v;
+                    }
+            }
         }
-        if (odd) add_odd<T>(A, b, row.t, hk, o);
+        if (__any_sync(~0u, odd)) add_odd<T>(A, b, row.t, hk, o);
     }
     store_row<T>(A, b, row.t, row.h, top, sum, o);
 }
@@ -457,21 +483,21 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
         bool first_piece = true;
         while (x < end) {
             const Seq s = sequence(A, b);
-            const int64_t n = tiles_of(A, S, b), u = (x - at) / n, t0 = (x - at) % n;
-            const int64_t count = n - t0 < end - x ? n - t0 : end - x;
-            const int hk = (int)(u / S.groups);
-            const int64_t R0 = u % S.groups * FEW_ROWS;
-            const int64_t j0 = t0 * FEW_KEYS, j1 = (t0 + count) * FEW_KEYS < s.kv ? (t0 + count) * FEW_KEYS : s.kv;
-            const int steps = j1 > j0 + warp * FEW_STEP ? (int)((j1 - j0 - warp * FEW_STEP + FEW_KEYS - 1) / FEW_KEYS) : 0;
+            const int n = tiles_of(S, s);
+            const int64_t u = (x - at) / n;
+            const int t0 = (int)(x - at - u * n), count = n - t0 < end - x ? n - t0 : (int)(end - x);
+            const int hk = (int)((uint32_t)u / (uint32_t)S.groups);
+            const int64_t R0 = (int64_t)((uint32_t)u % (uint32_t)S.groups) * FEW_ROWS;
+            const int j0 = t0 * FEW_KEYS, j1 = (int64_t)(t0 + count) * FEW_KEYS < s.kv ? (t0 + count) * FEW_KEYS : s.kv;
+            const int steps = j1 > j0 + warp * FEW_STEP ? (j1 - j0 - warp * FEW_STEP + FEW_KEYS - 1) / FEW_KEYS : 0;
 
             // stage `i` of this warp: lane l < 16 finds entry l, all lanes copy
             auto fetch = [&](int i) {
                 if (i < steps) {
-                    const int64_t j = j0 + (int64_t)i * FEW_KEYS + warp * FEW_STEP + (lane & 15);
+                    const int j = j0 + i * FEW_KEYS + warp * FEW_STEP + (lane & 15);
                     const bool in = j < j1;
-                    const int64_t jj = in ? j : j1 - 1;
-                    const int64_t p = page_of(a, b, jj), e = a.page_table ? jj % a.page_size : jj;
-                    const int64_t ok = p * a.k_page + e * a.k_entry, ov = p * a.v_page + e * a.v_entry;
+                    const Place at_j = place_of(a, b, in ? j : j1 - 1);
+                    const int64_t ok = at_j.page * a.k_page + at_j.in * a.k_entry, ov = at_j.page * a.v_page + at_j.in * a.v_entry;
                     const unsigned ins = __ballot_sync(~0u, in);
                     const T *k = (const T *)a.k + hk * a.k_head, *v = (const T *)a.v + hk * a.v_head;
                     const uint32_t st = base + (i % FEW_STAGES) * (2 * HALF);
@@ -527,7 +553,7 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
                     mma16816<T>(sc[0], qf[k], r[0], r[1]);
                     mma16816<T>(sc[1], qf[k], r[2], r[3]);
                 }
-                const int64_t j = j0 + (int64_t)i * FEW_KEYS + warp * FEW_STEP;
+                const int j = j0 + i * FEW_KEYS + warp * FEW_STEP;
                 uint32_t va = ~0u, vb = ~0u;
                 if (j + FEW_STEP > s.first) {
                     bool found = false;

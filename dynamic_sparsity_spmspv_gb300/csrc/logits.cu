@@ -6,20 +6,24 @@ using namespace dbs::ops;
 
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 256, BATCH = 8;       // BATCH loads of a thread in flight
 constexpr unsigned SEEN = 0x80000000u;   // in the history; the other bits count the output part
 constexpr unsigned NONE = 0xffffffffu;
 
 // One block per (row, slice of the vocabulary).  The block reads the row's
 // whole history and keeps what falls into its slice in shared memory, so no
-// [batch, vocab] counts ever exist in global memory.
+// [batch, vocab] counts ever exist in global memory.  Bound by the latency of
+// its few dependent steps for one row, by HBM for many; loads are issued
+// BATCH at a time, since shared-memory atomics between them keep the compiler
+// from doing so.
 template <class T, class O>
 __global__ void __launch_bounds__(NT) k_logits(dbs_logits_args A, int width)
 {
     extern __shared__ unsigned smem[];
     __shared__ int listed_again;
     unsigned *count = smem, *first = smem + width;   // first: only with biases
-    const int64_t b = blockIdx.y, v0 = (int64_t)blockIdx.x * width;
+    const int64_t b = blockIdx.y;
+    const int v0 = blockIdx.x * width;
     const int w = (int)(A.vocab - v0 < width ? A.vocab - v0 : width);
     const bool bias = A.biases > 0;
     for (int i = threadIdx.x; i < w; i += NT) {
@@ -29,24 +33,30 @@ __global__ void __launch_bounds__(NT) k_logits(dbs_logits_args A, int width)
     if (threadIdx.x == 0) listed_again = 0;
     __syncthreads();
     if (A.history) {
-        int64_t len = A.history_lens ? A.history_lens[b] : A.history_max;
-        len = len < 0 ? 0 : len > A.history_max ? A.history_max : len;
-        const int64_t prompt = A.prompt_lens ? A.prompt_lens[b] : 0;
+        int len = A.history_lens ? A.history_lens[b] : (int)A.history_max;
+        len = len < 0 ? 0 : len > A.history_max ? (int)A.history_max : len;
+        const int prompt = A.prompt_lens ? A.prompt_lens[b] : 0;
         const int32_t *h = A.history + b * A.history_stride;
-        for (int64_t j = threadIdx.x; j < len; j += NT) {
-            const int64_t d = h[j] - v0;
-            if (d < 0 || d >= w) continue;
-            if (j >= prompt) atomicAdd(&count[d], 1u);
-            else atomicOr(&count[d], SEEN);
+        for (int64_t j0 = threadIdx.x; j0 < len; j0 += NT * BATCH) {
+            int32_t id[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) id[k] = j0 + k * NT < len ? h[j0 + k * NT] : -1;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                // negative ids are below every slice, ids past the vocabulary beyond the last
+                if (id[k] < v0 || id[k] - v0 >= w) continue;
+                if (j0 + k * NT >= prompt) atomicAdd(&count[id[k] - v0], 1u);
+                else atomicOr(&count[id[k] - v0], SEEN);
+            }
         }
     }
     const int32_t *ids = A.bias_ids + b * A.bias_stride;
     const float *vals = A.bias_vals + b * A.bias_stride;
     if (bias) {
         for (int64_t i = threadIdx.x; i < A.biases; i += NT) {
-            const int64_t d = ids[i] - v0;
-            if (d >= 0 && d < w) {
-                if (atomicMin(&first[d], (unsigned)i) != NONE) listed_again = 1;
+            const int32_t id = ids[i];
+            if (id >= v0 && id - v0 < w) {
+                if (atomicMin(&first[id - v0], (unsigned)i) != NONE) listed_again = 1;
             }
         }
     }
@@ -56,27 +66,44 @@ __global__ void __launch_bounds__(NT) k_logits(dbs_logits_args A, int width)
     const T *x = (const T *)A.logits + b * A.logits_stride + v0;
     O *y = (O *)A.out + b * A.out_stride + v0;
     const int32_t *allowed = A.allowed ? A.allowed + b * A.allowed_stride : nullptr;
-    for (int i = threadIdx.x; i < w; i += NT) {
-        float l = to_f32(x[i]);
-        const unsigned c = count[i], n = c & ~SEEN;
-        if (c && A.repetition) l = l > 0.f ? l / rep : l * rep;
-        if (n) l -= freq * (float)n + pres;
-        if (bias && first[i] != NONE) {
-            l += vals[first[i]];
-            if (listed_again)
-                for (int64_t k = (int64_t)first[i] + 1; k < A.biases; ++k)
-                    if (ids[k] == v0 + i) l += vals[k];
+    for (int i0 = threadIdx.x; i0 < w; i0 += NT * BATCH) {
+        T in[BATCH];
+        unsigned bits[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int i = i0 + k * NT;
+            if (i < w) {
+                in[k] = x[i];
+                bits[k] = allowed ? (unsigned)allowed[(v0 + i) >> 5] : ~0u;
+            }
         }
-        const int64_t v = v0 + i;
-        if (allowed && !((unsigned)allowed[v >> 5] >> (v & 31) & 1u)) l = -__int_as_float(0x7f800000);
-        y[i] = from_f32<O>(l);
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int i = i0 + k * NT;
+            if (i >= w) break;
+            float l = to_f32(in[k]);
+            const unsigned c = count[i], n = c & ~SEEN;
+            if (c && A.repetition) l = l > 0.f ? l / rep : l * rep;
+            if (n) l -= freq * (float)n + pres;
+            if (bias && first[i] != NONE) {
+                l += vals[first[i]];
+                if (listed_again)
+                    for (int64_t m = (int64_t)first[i] + 1; m < A.biases; ++m)
+                        if (ids[m] == v0 + i) l += vals[m];
+            }
+            if (!(bits[k] >> ((v0 + i) & 31) & 1u)) l = -__int_as_float(0x7f800000);
+            y[i] = from_f32<O>(l);
+        }
     }
 }
 
+// Slices of 512 to 4096 entries: small ones while the grid is small, so that a
+// single row spreads over the GPU (each block reads the history again, from L2).
 template <class T, class O>
 void launch(const dbs_logits_args &A, cudaStream_t s)
 {
-    const int width = 4096;
+    int width = 4096;
+    while (width > 512 && (A.vocab + width - 1) / width * A.batch < 608) width /= 2;
     const dim3 grid((unsigned)((A.vocab + width - 1) / width), (unsigned)A.batch);
     k_logits<T, O><<<grid, NT, (A.biases > 0 ? 2 : 1) * width * sizeof(unsigned), s>>>(A, width);
 }

@@ -21,57 +21,147 @@ struct Rotary {
 
 constexpr int NT = 256;
 
-// One thread per pair (or copied entry) of one head of one token.
-template <class T, bool INTERLEAVED>
-__global__ void __launch_bounds__(NT) k_rotary(Rotary A, int heads)
+// 16 bytes of a head, or one value where rows are not aligned for that.
+template <class T, bool WIDE> struct Vec {
+    static constexpr int n = WIDE ? 16 / (int)sizeof(T) : 1;
+    struct alignas(n * sizeof(T)) type {
+        T v[n];
+    };
+};
+
+// Where head h of one token goes, and where it comes from.
+template <class T>
+__device__ __forceinline__ bool head_of(const Rotary &A, int h, int64_t b, int64_t t, int64_t slot, const T *&in, T *&out, bool &rotate)
 {
-    const int half = A.dim / 2, units = half + (A.head_dim - A.dim);
-    const int64_t all = A.total * heads * units;
-    for (int64_t u = (int64_t)blockIdx.x * NT + threadIdx.x; u < all; u += (int64_t)gridDim.x * NT) {
-        const int c = (int)(u % units);
-        const int64_t th = u / units, tok = th / heads;
-        int h = (int)(th % heads), p = 0;
-        while (h >= A.part[p].heads) h -= A.part[p++].heads;
-        const dbs_rotary_heads &P = A.part[p];
-        const int64_t b = tok / A.tokens, t = tok % A.tokens;
-        const T *in = (const T *)P.in + b * P.in_batch + t * P.in_token + h * P.in_head;
-        T *out = (T *)P.out + h * P.out_head;
-        if (P.to_slots) {
-            const int64_t s = A.slots[tok];
-            if (s < 0 || s >= A.slots_end) continue;
-            out += s / A.page_size * P.out_batch + s % A.page_size * P.out_token;
-        } else {
-            out += b * P.out_batch + t * P.out_token;
-        }
-        if (c >= half) {
-            out[A.dim + c - half] = in[A.dim + c - half];
+    int p = 0;
+    while (h >= A.part[p].heads) h -= A.part[p++].heads;
+    const dbs_rotary_heads &P = A.part[p];
+    rotate = P.rotate;
+    in = (const T *)P.in + b * P.in_batch + t * P.in_token + h * P.in_head;
+    out = (T *)P.out + h * P.out_head;
+    if (!P.to_slots) {
+        out += b * P.out_batch + t * P.out_token;
+        return true;
+    }
+    if (slot < 0 || slot >= A.slots_end) return false;
+    const uint32_t size = (uint32_t)A.page_size, page = (uint32_t)slot / size;
+    out += page * P.out_batch + ((uint32_t)slot - page * size) * P.out_token;
+    return true;
+}
+
+// A unit of a head is what one thread turns at once: vectors i and i + dim/2 of
+// the half layout, one vector of pairs of the interleaved one, or one vector of
+// the copied rest.  A thread keeps its token's cosines and sines for HEADS
+// heads, whose loads are issued together.  Bound by HBM: every entry is read
+// and written once.
+template <class T, bool INTERLEAVED, bool WIDE, int HEADS>
+__global__ void __launch_bounds__(NT) k_rotary(Rotary A, int heads, int units, int turning, int64_t all)
+{
+    using V = Vec<T, WIDE>;
+    using VT = typename V::type;
+    constexpr int N = V::n;
+    // interleaved pairs of single values: two entries a unit
+    constexpr int E = INTERLEAVED && !WIDE ? 2 : N, PAIRS = INTERLEAVED ? E / 2 : N;
+    constexpr int F = !WIDE ? 1 : PAIRS < 4 ? PAIRS : 4;      // entries of the table in one load
+    const int half = A.dim / 2, blocks = (heads + HEADS - 1) / HEADS;
+    for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < all; i += (int64_t)gridDim.x * NT) {
+        const uint32_t th = all >> 32 ? (uint32_t)(i / units) : (uint32_t)i / (uint32_t)units, c = (uint32_t)(i - (int64_t)th * units);
+        const uint32_t tok = th / (uint32_t)blocks, h0 = (th - tok * blocks) * HEADS;
+        const uint32_t b = tok / (uint32_t)A.tokens, t = tok - b * (uint32_t)A.tokens;
+        const int64_t slot = A.slots ? A.slots[tok] : 0;
+        if ((int)c >= turning) {
+            const int at = A.dim + ((int)c - turning) * N;
+#pragma unroll
+            for (int k = 0; k < HEADS; ++k) {
+                const T *in;
+                T *out;
+                bool rotate;
+                if ((int)h0 + k >= heads || !head_of(A, h0 + k, b, t, slot, in, out, rotate)) continue;
+                *(VT *)(out + at) = *(const VT *)(in + at);
+            }
             continue;
         }
-        const int i = INTERLEAVED ? 2 * c : c, j = INTERLEAVED ? 2 * c + 1 : c + half;
-        if (!P.rotate) {
-            const T a = in[i], b2 = in[j];
-            out[i] = a;
-            out[j] = b2;
-            continue;
+        const int pair = (int)c * PAIRS;                      // the unit's first pair
+        const int lo = INTERLEAVED ? 2 * pair : pair, hi = INTERLEAVED ? lo + (WIDE ? 0 : 1) : lo + half;
+        constexpr bool TWO = !INTERLEAVED || !WIDE;           // a second vector at hi
+        VT x[HEADS], y[HEADS];
+        T *out[HEADS];
+        bool take[HEADS], rotate[HEADS];
+#pragma unroll
+        for (int k = 0; k < HEADS; ++k) {
+            const T *in;
+            take[k] = (int)h0 + k < heads && head_of(A, h0 + k, b, t, slot, in, out[k], rotate[k]);
+            if (take[k]) {
+                x[k] = *(const VT *)(in + lo);
+                if (TWO) y[k] = *(const VT *)(in + hi);
+            }
         }
         const int64_t pos = A.positions[tok];
         const bool ok = pos >= 0 && pos < A.table_rows;
-        const float cs = ok ? A.table[pos * A.dim + c] : nanf("");
-        const float sn = ok ? A.sign * A.table[pos * A.dim + half + c] : nanf("");
-        const float x = to_f32(in[i]), y = to_f32(in[j]);
-        out[i] = from_f32<T>(x * cs - y * sn);
-        out[j] = from_f32<T>(x * sn + y * cs);
+        float cs[PAIRS], sn[PAIRS];
+#pragma unroll
+        for (int p = 0; p < PAIRS; p += F) {
+            struct alignas(4 * F) Floats {
+                float v[F];
+            };
+            const float *row = A.table + pos * A.dim + pair + p;
+#pragma unroll
+            for (int e = 0; e < F; ++e) cs[p + e] = sn[p + e] = nanf("");
+            if (ok) {
+                const Floats c4 = *(const Floats *)row, s4 = *(const Floats *)(row + half);
+#pragma unroll
+                for (int e = 0; e < F; ++e) {
+                    cs[p + e] = c4.v[e];
+                    sn[p + e] = A.sign * s4.v[e];
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < HEADS; ++k) {
+            if (!take[k]) continue;
+            if (rotate[k]) {
+#pragma unroll
+                for (int p = 0; p < PAIRS; ++p) {
+                    T &a = TWO ? x[k].v[TWO ? p : 0] : x[k].v[TWO ? 0 : 2 * p], &d = TWO ? y[k].v[TWO ? p : 0] : x[k].v[TWO ? 0 : 2 * p + 1];
+                    const float u = to_f32(a), v = to_f32(d);
+                    a = from_f32<T>(u * cs[p] - v * sn[p]);
+                    d = from_f32<T>(u * sn[p] + v * cs[p]);
+                }
+            }
+            *(VT *)(out[k] + lo) = x[k];
+            if (TWO) *(VT *)(out[k] + hi) = y[k];
+        }
     }
+}
+
+template <class T, bool INTERLEAVED, bool WIDE>
+void launch_heads(const Rotary &A, int heads, cudaStream_t s)
+{
+    constexpr int N = Vec<T, WIDE>::n, E = INTERLEAVED ? (WIDE ? N : 2) : 2 * N;
+    const int turning = A.dim / E, units = turning + (A.head_dim - A.dim) / N;
+    // four heads a thread once that still fills the GPU
+    const int64_t four = A.total * ((heads + 3) / 4) * units;
+    const bool many = four >= 152 * 2048;
+    const int64_t all = many ? four : A.total * heads * units;
+    const int64_t blocks = (all + NT - 1) / NT;
+    const unsigned grid = (unsigned)(blocks < (int64_t(1) << 30) ? blocks : (int64_t(1) << 30));
+    if (many) k_rotary<T, INTERLEAVED, WIDE, 4><<<grid, NT, 0, s>>>(A, heads, units, turning, all);
+    else k_rotary<T, INTERLEAVED, WIDE, 1><<<grid, NT, 0, s>>>(A, heads, units, turning, all);
 }
 
 template <class T>
 void launch(const Rotary &A, int heads, bool interleaved, cudaStream_t s)
 {
-    const int64_t all = A.total * heads * (A.head_dim - A.dim / 2);
-    const int64_t blocks = (all + NT - 1) / NT;
-    const unsigned grid = (unsigned)(blocks < (int64_t(1) << 30) ? blocks : (int64_t(1) << 30));
-    if (interleaved) k_rotary<T, true><<<grid, NT, 0, s>>>(A, heads);
-    else k_rotary<T, false><<<grid, NT, 0, s>>>(A, heads);
+    // 16-byte accesses: all heads on such boundaries, and whole vectors in each part of a head
+    constexpr int N = 16 / (int)sizeof(T);
+    bool wide = A.dim % (interleaved ? N : 2 * N) == 0 && A.head_dim % N == 0 && aligned16(A.table);
+    for (int p = 0; p < A.nparts; ++p) {
+        const dbs_rotary_heads &P = A.part[p];
+        wide = wide && aligned16(P.in) && aligned16(P.out) &&
+               ((P.in_batch | P.in_token | P.in_head | P.out_batch | P.out_token | P.out_head) & (N - 1)) == 0;
+    }
+    if (interleaved) wide ? launch_heads<T, true, true>(A, heads, s) : launch_heads<T, true, false>(A, heads, s);
+    else wide ? launch_heads<T, false, true>(A, heads, s) : launch_heads<T, false, false>(A, heads, s);
 }
 
 struct Freqs {
@@ -155,6 +245,7 @@ dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype d
         heads += P.heads;
     }
     if (!work || heads == 0) return DBS_OK;
+    if (batch * tokens * heads >= (int64_t(1) << 32)) return DBS_ERR_INVALID_ARG;
     A.head_dim = head_dim;
     A.dim = dim;
     A.tokens = tokens;

@@ -68,15 +68,16 @@ __global__ void __launch_bounds__(ROWS_NT) k_w4_rows(W4 A)
 // (B, 16 x 8): the columns are tokens, or, for fp32 x, the three 8-bit pieces
 // hi + mid + lo whose sum is x exactly (truncated splits of its 24 bits), so
 // fp32 costs three columns a token and loses nothing.  Codes become numbers in
-// registers: with a nibble in the low mantissa bits, 128 + q in bf16 (1024 + q
-// in fp16) is one AND-OR of a word's nibble pair, and subtracting 128 + z gives
-// q - z exactly.  Which column of x a fragment's slot stands for is free as long
+// registers: with a nibble in the low mantissa bits, (128 + q) / 256 in bf16 (1024
+// + q in fp16) is one AND-OR of a word's nibble pair, and subtracting the same
+// of z gives q - z (by the unit 1/256) exactly.  Which column of x a fragment's slot stands for is free as long
 // as A and B agree: a lane's word holds 8 neighbouring columns, paired (0, 4),
 // (1, 5), (2, 6), (3, 7) as they lie in the word, and x is laid out to match.
 // Groups' sums are fp32 accumulators, multiplied by the scale in fp32.
 template <class T> struct Half2;
 template <> struct Half2<__half> {
     static constexpr uint32_t magic = 0x64006400u, one = 0x00010001u;   // 1024 + q
+    static constexpr float unit = 1.f;
     static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b)
     {
         uint32_t r;
@@ -90,10 +91,11 @@ template <> struct Half2<__half> {
     }
 };
 template <> struct Half2<__nv_bfloat16> {
-    static constexpr uint32_t magic = 0x43004300u, one = 0x00010001u;   // 128 + q
+    // (128 + q) / 256: sums stay below the largest fp32 for the largest x
+    static constexpr uint32_t magic = 0x3f003f00u, one = 0x00010001u;
+    static constexpr float unit = 256.f;
     static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b)
     {
-        // a * 1 - b in one rounding, exact here
         uint32_t r;
         asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(MMA_NT, 2) k_w4_mma(W4 A, Cut C)
 #pragma unroll
                 for (int p = 0; p < P::parts; ++p)
                     v += red[(wr2 * C.wk + k) * (RT * 16 * NT * 8) + (tok * P::parts + p) * (RT * 16) + r];
-            if (row < A.m) ((T *)A.y)[(t0 + tok) * A.y_stride + row] = from_f32<T>(v);
+            if (row < A.m) ((T *)A.y)[(t0 + tok) * A.y_stride + row] = from_f32<T>(v * H::unit);
         }
         __syncthreads();
     }

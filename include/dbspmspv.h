@@ -496,6 +496,7 @@ typedef struct {
  *              tokens with a slot outside [0, pages * page_size) are not
  *              written.  Slots in use must differ from one another.
  *   head_dim   entries of a head, dim <= head_dim <= 1024, dim even
+ *   batch * tokens < 2^31, and times all heads < 2^32
  * Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */
 dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype dtype, int64_t batch, int64_t tokens,
                       int32_t head_dim, int32_t dim, const float *table, int64_t table_rows, const int32_t *positions,
