@@ -157,8 +157,13 @@ __device__ __forceinline__ bool clear_odd(uint32_t &w)
     return lo || hi;
 }
 
+struct Eight {
+    float v[8];
+};
+
+// (by value, so that the caller's sums stay in registers)
 template <class T>
-__device__ __noinline__ void add_odd(const Attn &A, int64_t b, int t, int hk, float (&o)[8])
+__device__ __noinline__ Eight add_odd(const Attn &A, int64_t b, int t, int hk, Eight o)
 {
     const dbs_attention_args &a = A.a;
     const int lane = threadIdx.x & 31;
@@ -171,9 +176,10 @@ __device__ __noinline__ void add_odd(const Attn &A, int64_t b, int t, int hk, fl
         for (int e = 0; e < 8; ++e)
             if (lane + 32 * e < a.head_dim) {
                 const float x = to_f32(v[lane + 32 * e]);
-                if (!isfinite(x)) o[e] += x;
+                if (!isfinite(x)) o.v[e] += x;
             }
     }
+    return o;
 }
 
 // Writes a row from its sums: out = o / l, lse = (m + log2 l) ln 2.
@@ -389,20 +395,33 @@ __global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int grid
                 l = l != l ? l : f * l;
             }
             const int now = parts - base < 32 ? parts - base : 32;
-#pragma unroll 4
-            for (int i = 0; i < now; ++i) {
-                const float fi = __shfl_sync(~0u, f, i), li = __shfl_sync(~0u, l, i);
-                const float *p = (base + i ? rest + 2 * size * (base + i) : p0) + (int64_t)r * a.head_dim;
-                sum += li;
+            for (int i = 0; i < now; i += 4) {
+                float v[4][8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (lane + 32 * e < a.head_dim) {
-                        const float v = p[lane + 32 * e];
-                        o[e] += fi == 0.f ? 0.f : fi * v;
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const int c = base + (i + k < now ? i + k : i);
+                    const float *p = (c ? rest + 2 * size * c : p0) + (int64_t)r * a.head_dim;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[k][e] = lane + 32 * e < a.head_dim ? p[lane + 32 * e] : 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (i + k >= now) break;
+                    const float fi = __shfl_sync(~0u, f, i + k);
+                    sum += __shfl_sync(~0u, l, i + k);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] += fi == 0.f ? 0.f : fi * v[k][e];
+                }
             }
         }
-        if (__any_sync(~0u, odd)) add_odd<T>(A, b, row.t, hk, o);
+        if (__any_sync(~0u, odd)) {
+            Eight w;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w.v[e] = o[e];
+            w = add_odd<T>(A, b, row.t, hk, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = w.v[e];
+        }
     }
     store_row<T>(A, b, row.t, row.h, top, sum, o);
 }
@@ -667,8 +686,16 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
                     for (int e = 0; e < DP / 32; ++e) oo[e] += f == 0.f ? 0.f : f * po[lane + 32 * e];
                 }
                 if (whole) {
-                    if (row.t >= s.tree) sum = 0.f;
-                    else if (odd) add_odd<T>(A, b, row.t, hk, oo);
+                    if (row.t >= s.tree) {
+                        sum = 0.f;
+                    } else if (odd) {
+                        Eight w;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w.v[e] = oo[e];
+                        w = add_odd<T>(A, b, row.t, hk, w);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) oo[e] = w.v[e];
+                    }
                     store_row<T>(A, b, row.t, row.h, top, sum, oo);
                 } else {
 #pragma unroll

@@ -6,106 +6,156 @@ using namespace dbs::ops;
 
 namespace {
 
-constexpr int NT = 256, BATCH = 8;       // BATCH loads of a thread in flight
-constexpr unsigned SEEN = 0x80000000u;   // in the history; the other bits count the output part
+constexpr int NT = 512;
+constexpr int RUN = 8;                   // neighbouring entries of a thread: 16 bytes of 16-bit logits
+constexpr int BATCH = 8;                 // history entries of a thread in flight
+constexpr unsigned SEEN = 0x80000000u;   // in the history; the low bits count the output part
+constexpr unsigned BIAS = 0x40000000u;   // in the bias list
 constexpr unsigned NONE = 0xffffffffu;
+
+template <class T, int N> struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Run {
+    T v[N];
+};
 
 // One block per (row, slice of the vocabulary).  The block reads the row's
 // whole history and keeps what falls into its slice in shared memory, so no
-// [batch, vocab] counts ever exist in global memory.  Bound by the latency of
-// its few dependent steps for one row, by HBM for many; loads are issued
-// BATCH at a time, since shared-memory atomics between them keep the compiler
-// from doing so.
+// [batch, vocab] counts ever exist in global memory.  A slice's first logits
+// and history entries are under way before the first wait.  Slices are cut at
+// `lead` entries before the row, the distance to the 16-byte boundary below it,
+// so that runs of eight are aligned whatever the vocabulary's size.
 template <class T, class O>
-__global__ void __launch_bounds__(NT) k_logits(dbs_logits_args A, int width)
+__global__ void __launch_bounds__(NT, 2) k_logits(dbs_logits_args A, int width)
 {
-    extern __shared__ unsigned smem[];
+    extern __shared__ __align__(16) unsigned smem[];
     __shared__ int listed_again;
-    unsigned *count = smem, *first = smem + width;   // first: only with biases
+    unsigned *count = smem, *first = smem + width;   // first: only with biases, and of flagged entries
     const int64_t b = blockIdx.y;
-    const int v0 = blockIdx.x * width;
-    const int w = (int)(A.vocab - v0 < width ? A.vocab - v0 : width);
-    const bool bias = A.biases > 0;
-    for (int i = threadIdx.x; i < w; i += NT) {
-        count[i] = 0;
-        if (bias) first[i] = NONE;
+    const T *x = (const T *)A.logits + b * A.logits_stride;
+    O *y = (O *)A.out + b * A.out_stride;
+    const int lead = (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T)) % RUN);
+    const bool whole_runs = (reinterpret_cast<uintptr_t>(y) / sizeof(O)) % RUN == lead;
+    const int v0 = (int)blockIdx.x * width - lead;   // the slice's first entry, below 0 in the first slice
+    if (v0 >= A.vocab) return;
+    const int v1 = A.vocab - v0 < width ? (int)A.vocab : v0 + width;
+    const int32_t *h = A.history + b * A.history_stride;
+    int len = 0, prompt = 0;
+    if (A.history) {
+        len = A.history_lens ? A.history_lens[b] : (int)A.history_max;
+        prompt = A.prompt_lens ? A.prompt_lens[b] : 0;
     }
+    int32_t id[BATCH];
+    auto ahead = [&](int j0) {
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) id[k] = j0 + k * NT < (int)A.history_max ? h[j0 + k * NT] : -1;
+    };
+    Run<T, RUN> in;
+    auto fetch = [&](int v) {
+        if (v >= 0 && v + RUN <= v1) {
+            in = *(const Run<T, RUN> *)(x + v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < RUN; ++e)
+                if (v + e >= 0 && v + e < v1) in.v[e] = x[v + e];
+        }
+    };
+    if (A.history) ahead(threadIdx.x);
+    fetch(v0 + (int)threadIdx.x * RUN);
+    for (int i = threadIdx.x; i < width / 4; i += NT) ((uint4 *)count)[i] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) listed_again = 0;
     __syncthreads();
-    if (A.history) {
-        int len = A.history_lens ? A.history_lens[b] : (int)A.history_max;
-        len = len < 0 ? 0 : len > A.history_max ? (int)A.history_max : len;
-        const int prompt = A.prompt_lens ? A.prompt_lens[b] : 0;
-        const int32_t *h = A.history + b * A.history_stride;
-        for (int64_t j0 = threadIdx.x; j0 < len; j0 += NT * BATCH) {
-            int32_t id[BATCH];
+    len = len < 0 ? 0 : len > A.history_max ? (int)A.history_max : len;
+    for (int j0 = threadIdx.x; j0 < len; j0 += NT * BATCH) {
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) id[k] = j0 + k * NT < len ? h[j0 + k * NT] : -1;
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                // negative ids are below every slice, ids past the vocabulary beyond the last
-                if (id[k] < v0 || id[k] - v0 >= w) continue;
-                if (j0 + k * NT >= prompt) atomicAdd(&count[id[k] - v0], 1u);
-                else atomicOr(&count[id[k] - v0], SEEN);
-            }
+        for (int k = 0; k < BATCH; ++k) {
+            const int j = j0 + k * NT;
+            if (j >= len || id[k] < 0 || id[k] < v0 || id[k] >= v1) continue;
+            if (j >= prompt) atomicAdd(&count[id[k] - v0], 1u);
+            else atomicOr(&count[id[k] - v0], SEEN);
         }
+        if (j0 + NT * BATCH < len) ahead(j0 + NT * BATCH);
     }
+    const int nb = (int)A.biases;
     const int32_t *ids = A.bias_ids + b * A.bias_stride;
     const float *vals = A.bias_vals + b * A.bias_stride;
-    if (bias) {
-        for (int64_t i = threadIdx.x; i < A.biases; i += NT) {
-            const int32_t id = ids[i];
-            if (id >= v0 && id - v0 < w) {
-                if (atomicMin(&first[id - v0], (unsigned)i) != NONE) listed_again = 1;
+    if (nb) {
+        // flag the listed entries, then find the first place of each in the list
+        for (int i = threadIdx.x; i < nb; i += NT)
+            if (ids[i] >= 0 && ids[i] >= v0 && ids[i] < v1) {
+                atomicOr(&count[ids[i] - v0], BIAS);
+                first[ids[i] - v0] = NONE;
             }
-        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < nb; i += NT)
+            if (ids[i] >= 0 && ids[i] >= v0 && ids[i] < v1)
+                if (atomicMin(&first[ids[i] - v0], (unsigned)i) != NONE) listed_again = 1;
     }
-    __syncthreads();
     const float rep = A.repetition ? A.repetition[b] : 1.f, pres = A.presence ? A.presence[b] : 0.f;
     const float freq = A.frequency ? A.frequency[b] : 0.f;
-    const T *x = (const T *)A.logits + b * A.logits_stride + v0;
-    O *y = (O *)A.out + b * A.out_stride + v0;
-    const int32_t *allowed = A.allowed ? A.allowed + b * A.allowed_stride : nullptr;
-    for (int i0 = threadIdx.x; i0 < w; i0 += NT * BATCH) {
-        T in[BATCH];
-        unsigned bits[BATCH];
+    const unsigned *allowed = A.allowed ? (const unsigned *)A.allowed + b * A.allowed_stride : nullptr;
+    const int last_word = (int)((A.vocab - 1) >> 5);
+    __syncthreads();
+    for (int i = threadIdx.x * RUN; i < v1 - v0; i += NT * RUN) {
+        const int v = v0 + i;
+        if (i >= NT * RUN) fetch(v);
+        unsigned bits = ~0u;                         // of entries v .. v + 7
+        if (allowed) {
+            const int at = v < 0 ? 0 : v;
+            const unsigned a0 = allowed[at >> 5], a1 = (at >> 5) < last_word ? allowed[(at >> 5) + 1] : 0u;
+            bits = __funnelshift_r(a0, a1, at & 31) << (at - v);
+        }
+        float l[RUN];
+        unsigned c[RUN];
+        *(uint4 *)c = *(const uint4 *)(count + i);
+        *(uint4 *)(c + 4) = *(const uint4 *)(count + i + 4);
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            const int i = i0 + k * NT;
-            if (i < w) {
-                in[k] = x[i];
-                bits[k] = allowed ? (unsigned)allowed[(v0 + i) >> 5] : ~0u;
+        for (int e = 0; e < RUN; ++e) l[e] = to_f32(in.v[e]);
+        if (c[0] | c[1] | c[2] | c[3] | c[4] | c[5] | c[6] | c[7]) {
+#pragma unroll
+            for (int e = 0; e < RUN; ++e) {
+                if (c[e] == 0) continue;
+                const unsigned n = c[e] & ~(SEEN | BIAS);
+                if ((c[e] & ~BIAS) && A.repetition) l[e] = l[e] > 0.f ? l[e] / rep : l[e] * rep;
+                if (n) l[e] -= freq * (float)n + pres;
+                if (c[e] & BIAS) {
+                    const unsigned k = first[i + e];
+                    l[e] += vals[k];
+                    if (listed_again)
+                        for (int m = (int)k + 1; m < nb; ++m)
+                            if (ids[m] == v + e) l[e] += vals[m];
+                }
             }
         }
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            const int i = i0 + k * NT;
-            if (i >= w) break;
-            float l = to_f32(in[k]);
-            const unsigned c = count[i], n = c & ~SEEN;
-            if (c && A.repetition) l = l > 0.f ? l / rep : l * rep;
-            if (n) l -= freq * (float)n + pres;
-            if (bias && first[i] != NONE) {
-                l += vals[first[i]];
-                if (listed_again)
-                    for (int64_t m = (int64_t)first[i] + 1; m < A.biases; ++m)
-                        if (ids[m] == v0 + i) l += vals[m];
+        for (int e = 0; e < RUN; ++e) l[e] = bits >> e & 1u ? l[e] : -__int_as_float(0x7f800000);
+        if (whole_runs && v >= 0 && v + RUN <= v1) {
+            constexpr int N = 16 / sizeof(O) < RUN ? 16 / sizeof(O) : RUN;
+#pragma unroll
+            for (int e = 0; e < RUN; e += N) {
+                Run<O, N> r;
+#pragma unroll
+                for (int k = 0; k < N; ++k) r.v[k] = from_f32<O>(l[e + k]);
+                *(Run<O, N> *)(y + v + e) = r;
             }
-            if (!(bits[k] >> ((v0 + i) & 31) & 1u)) l = -__int_as_float(0x7f800000);
-            y[i] = from_f32<O>(l);
+        } else {
+#pragma unroll
+            for (int e = 0; e < RUN; ++e)
+                if (v + e >= 0 && v + e < v1) y[v + e] = from_f32<O>(l[e]);
         }
     }
 }
 
-// Slices of 512 to 4096 entries: small ones while the grid is small, so that a
-// single row spreads over the GPU (each block reads the history again, from L2).
+// Slices of 1024 to 8192 entries: small ones while the grid is small, so that a
+// single row spreads over the GPU; large ones otherwise, since each block reads
+// the history again (from L2) and meets the memory's latency once.
 template <class T, class O>
 void launch(const dbs_logits_args &A, cudaStream_t s)
 {
-    int width = 4096;
-    while (width > 512 && (A.vocab + width - 1) / width * A.batch < 608) width /= 2;
-    const dim3 grid((unsigned)((A.vocab + width - 1) / width), (unsigned)A.batch);
-    k_logits<T, O><<<grid, NT, (A.biases > 0 ? 2 : 1) * width * sizeof(unsigned), s>>>(A, width);
+    int width = 8192;
+    while (width > 1024 && (A.vocab + RUN - 2 + width) / width * A.batch < 2 * 152) width /= 2;
+    const dim3 grid((unsigned)((A.vocab + RUN - 2 + width) / width), (unsigned)A.batch);
+    const int smem = (A.biases > 0 ? 2 : 1) * width * (int)sizeof(unsigned);
+    cudaFuncSetAttribute(k_logits<T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 8192 * (int)sizeof(unsigned));
+    k_logits<T, O><<<grid, NT, smem, s>>>(A, width);
 }
 
 template <class T>
@@ -121,7 +171,7 @@ void launch_out(const dbs_logits_args &A, cudaStream_t s)
 extern "C" dbs_status dbs_penalize_logits(const dbs_logits_args *a, void *stream)
 {
     if (!a || !dtype_ok(a->dtype) || !dtype_ok(a->out_dtype) || a->batch < 0 || a->vocab < 0 ||
-        a->vocab >= (int64_t(1) << 31) || a->batch > 65535 || a->history_max < 0 || a->history_max >= (int64_t(1) << 31) ||
+        a->vocab >= (int64_t(1) << 31) - 8192 || a->batch > 65535 || a->history_max < 0 || a->history_max >= (int64_t(1) << 30) ||
         a->biases < 0 || a->biases >= (int64_t(1) << 31))
         return DBS_ERR_INVALID_ARG;
     if (a->batch == 0 || a->vocab == 0) return DBS_OK;

@@ -29,128 +29,119 @@ template <class T, bool WIDE> struct Vec {
     };
 };
 
-// Where head h of one token goes, and where it comes from.
-template <class T>
-__device__ __forceinline__ bool head_of(const Rotary &A, int h, int64_t b, int64_t t, int64_t slot, const T *&in, T *&out, bool &rotate)
-{
-    int p = 0;
-    while (h >= A.part[p].heads) h -= A.part[p++].heads;
-    const dbs_rotary_heads &P = A.part[p];
-    rotate = P.rotate;
-    in = (const T *)P.in + b * P.in_batch + t * P.in_token + h * P.in_head;
-    out = (T *)P.out + h * P.out_head;
-    if (!P.to_slots) {
-        out += b * P.out_batch + t * P.out_token;
-        return true;
-    }
-    if (slot < 0 || slot >= A.slots_end) return false;
-    const uint32_t size = (uint32_t)A.page_size, page = (uint32_t)slot / size;
-    out += page * P.out_batch + ((uint32_t)slot - page * size) * P.out_token;
-    return true;
-}
-
 // A unit of a head is what one thread turns at once: vectors i and i + dim/2 of
 // the half layout, one vector of pairs of the interleaved one, or one vector of
-// the copied rest.  A thread keeps its token's cosines and sines for HEADS
-// heads, whose loads are issued together.  Bound by HBM: every entry is read
-// and written once.
-template <class T, bool INTERLEAVED, bool WIDE, int HEADS>
-__global__ void __launch_bounds__(NT) k_rotary(Rotary A, int heads, int units, int turning, int64_t all)
+// the copied rest.  A thread keeps its token's cosines and sines for up to
+// `span` heads of one group (blockIdx.y), four of whose loads are issued
+// together.  Bound by HBM: every entry is read and written once.
+template <class T, bool INTERLEAVED, bool WIDE>
+__global__ void __launch_bounds__(NT) k_rotary(Rotary A, uint32_t units, uint32_t turning, uint32_t threads, int span)
 {
     using V = Vec<T, WIDE>;
     using VT = typename V::type;
     constexpr int N = V::n;
     // interleaved pairs of single values: two entries a unit
-    constexpr int E = INTERLEAVED && !WIDE ? 2 : N, PAIRS = INTERLEAVED ? E / 2 : N;
+    constexpr int PAIRS = INTERLEAVED ? (WIDE ? N / 2 : 1) : N;
     constexpr int F = !WIDE ? 1 : PAIRS < 4 ? PAIRS : 4;      // entries of the table in one load
-    const int half = A.dim / 2, blocks = (heads + HEADS - 1) / HEADS;
-    for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < all; i += (int64_t)gridDim.x * NT) {
-        const uint32_t th = all >> 32 ? (uint32_t)(i / units) : (uint32_t)i / (uint32_t)units, c = (uint32_t)(i - (int64_t)th * units);
-        const uint32_t tok = th / (uint32_t)blocks, h0 = (th - tok * blocks) * HEADS;
-        const uint32_t b = tok / (uint32_t)A.tokens, t = tok - b * (uint32_t)A.tokens;
-        const int64_t slot = A.slots ? A.slots[tok] : 0;
-        if ((int)c >= turning) {
-            const int at = A.dim + ((int)c - turning) * N;
-#pragma unroll
-            for (int k = 0; k < HEADS; ++k) {
-                const T *in;
-                T *out;
-                bool rotate;
-                if ((int)h0 + k >= heads || !head_of(A, h0 + k, b, t, slot, in, out, rotate)) continue;
-                *(VT *)(out + at) = *(const VT *)(in + at);
-            }
-            continue;
-        }
-        const int pair = (int)c * PAIRS;                      // the unit's first pair
-        const int lo = INTERLEAVED ? 2 * pair : pair, hi = INTERLEAVED ? lo + (WIDE ? 0 : 1) : lo + half;
-        constexpr bool TWO = !INTERLEAVED || !WIDE;           // a second vector at hi
-        VT x[HEADS], y[HEADS];
-        T *out[HEADS];
-        bool take[HEADS], rotate[HEADS];
-#pragma unroll
-        for (int k = 0; k < HEADS; ++k) {
-            const T *in;
-            take[k] = (int)h0 + k < heads && head_of(A, h0 + k, b, t, slot, in, out[k], rotate[k]);
-            if (take[k]) {
-                x[k] = *(const VT *)(in + lo);
-                if (TWO) y[k] = *(const VT *)(in + hi);
-            }
-        }
+    constexpr bool TWO = !INTERLEAVED || !WIDE;               // a second vector at hi
+    const uint32_t i = blockIdx.x * NT + threadIdx.x;
+    if (i >= threads) return;
+    // this block's heads
+    int y = blockIdx.y, p = 0;
+    while (p + 1 < A.nparts && y >= (A.part[p].heads + span - 1) / span) y -= (A.part[p++].heads + span - 1) / span;
+    const dbs_rotary_heads &P = A.part[p];
+    const int h0 = y * span, heads = P.heads - h0 < span ? P.heads - h0 : span;
+
+    const uint32_t tok = i / units, c = i - tok * units;
+    const uint32_t b = tok / (uint32_t)A.tokens, t = tok - b * (uint32_t)A.tokens;
+    const T *in = (const T *)P.in + b * P.in_batch + t * P.in_token + h0 * P.in_head;
+    T *out = (T *)P.out + h0 * P.out_head;
+    if (P.to_slots) {
+        const int64_t slot = A.slots[tok];
+        if (slot < 0 || slot >= A.slots_end) return;
+        const uint32_t size = (uint32_t)A.page_size, page = (uint32_t)slot / size;
+        out += page * P.out_batch + ((uint32_t)slot - page * size) * P.out_token;
+    } else {
+        out += b * P.out_batch + t * P.out_token;
+    }
+    const bool turn = c < turning && P.rotate;
+    const bool two = TWO && c < turning;
+    const int half = A.dim / 2, pair = (int)c * PAIRS;        // the unit's first pair
+    const int lo = c >= turning ? A.dim + (int)(c - turning) * N : INTERLEAVED ? 2 * pair : pair;
+    const int apart = INTERLEAVED ? 1 : half;
+    in += lo;
+    out += lo;
+    float cs[PAIRS], sn[PAIRS];
+    if (turn) {
         const int64_t pos = A.positions[tok];
         const bool ok = pos >= 0 && pos < A.table_rows;
-        float cs[PAIRS], sn[PAIRS];
 #pragma unroll
-        for (int p = 0; p < PAIRS; p += F) {
+        for (int q = 0; q < PAIRS; q += F) {
             struct alignas(4 * F) Floats {
                 float v[F];
             };
-            const float *row = A.table + pos * A.dim + pair + p;
-#pragma unroll
-            for (int e = 0; e < F; ++e) cs[p + e] = sn[p + e] = nanf("");
+            Floats c4, s4;
+            const float *row = A.table + pos * A.dim + pair + q;
             if (ok) {
-                const Floats c4 = *(const Floats *)row, s4 = *(const Floats *)(row + half);
+                c4 = *(const Floats *)row;
+                s4 = *(const Floats *)(row + half);
+            }
 #pragma unroll
-                for (int e = 0; e < F; ++e) {
-                    cs[p + e] = c4.v[e];
-                    sn[p + e] = A.sign * s4.v[e];
-                }
+            for (int e = 0; e < F; ++e) {
+                cs[q + e] = ok ? c4.v[e] : nanf("");
+                sn[q + e] = ok ? A.sign * s4.v[e] : nanf("");
             }
         }
+    }
+    for (int h = 0; h < heads; h += 4) {
+        VT x[4], z[4];
 #pragma unroll
-        for (int k = 0; k < HEADS; ++k) {
-            if (!take[k]) continue;
-            if (rotate[k]) {
-#pragma unroll
-                for (int p = 0; p < PAIRS; ++p) {
-                    T &a = TWO ? x[k].v[TWO ? p : 0] : x[k].v[TWO ? 0 : 2 * p], &d = TWO ? y[k].v[TWO ? p : 0] : x[k].v[TWO ? 0 : 2 * p + 1];
-                    const float u = to_f32(a), v = to_f32(d);
-                    a = from_f32<T>(u * cs[p] - v * sn[p]);
-                    d = from_f32<T>(u * sn[p] + v * cs[p]);
-                }
+        for (int k = 0; k < 4; ++k)
+            if (h + k < heads) {
+                x[k] = *(const VT *)(in + k * P.in_head);
+                if (two) z[k] = *(const VT *)(in + k * P.in_head + apart);
             }
-            *(VT *)(out[k] + lo) = x[k];
-            if (TWO) *(VT *)(out[k] + hi) = y[k];
-        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (h + k < heads) {
+                if (turn) {
+#pragma unroll
+                    for (int q = 0; q < PAIRS; ++q) {
+                        T &a = x[k].v[TWO ? q : 2 * q], &d = TWO ? z[k].v[q] : x[k].v[TWO ? 0 : 2 * q + 1];
+                        const float u = to_f32(a), v = to_f32(d);
+                        a = from_f32<T>(u * cs[q] - v * sn[q]);
+                        d = from_f32<T>(u * sn[q] + v * cs[q]);
+                    }
+                }
+                *(VT *)(out + k * P.out_head) = x[k];
+                if (two) *(VT *)(out + k * P.out_head + apart) = z[k];
+            }
+        in += 4 * P.in_head;
+        out += 4 * P.out_head;
     }
 }
 
 template <class T, bool INTERLEAVED, bool WIDE>
-void launch_heads(const Rotary &A, int heads, cudaStream_t s)
+dbs_status launch_units(const Rotary &A, cudaStream_t s)
 {
     constexpr int N = Vec<T, WIDE>::n, E = INTERLEAVED ? (WIDE ? N : 2) : 2 * N;
     const int turning = A.dim / E, units = turning + (A.head_dim - A.dim) / N;
-    // four heads a thread once that still fills the GPU
-    const int64_t four = A.total * ((heads + 3) / 4) * units;
-    const bool many = four >= 152 * 2048;
-    const int64_t all = many ? four : A.total * heads * units;
-    const int64_t blocks = (all + NT - 1) / NT;
-    const unsigned grid = (unsigned)(blocks < (int64_t(1) << 30) ? blocks : (int64_t(1) << 30));
-    if (many) k_rotary<T, INTERLEAVED, WIDE, 4><<<grid, NT, 0, s>>>(A, heads, units, turning, all);
-    else k_rotary<T, INTERLEAVED, WIDE, 1><<<grid, NT, 0, s>>>(A, heads, units, turning, all);
+    const int64_t threads = A.total * units;
+    // Heads of a thread: eight, so that a token's angles are read once for all of
+    // them, and fewer while that leaves the GPU's 152 x 2048 threads idle.
+    int span = 8, chunks = 0;
+    for (;; span /= 2) {
+        chunks = 0;
+        for (int p = 0; p < A.nparts; ++p) chunks += (A.part[p].heads + span - 1) / span;
+        if (span == 1 || threads * chunks >= 152 * 2048) break;
+    }
+    k_rotary<T, INTERLEAVED, WIDE><<<dim3((unsigned)((threads + NT - 1) / NT), (unsigned)chunks), NT, 0, s>>>(
+        A, (uint32_t)units, (uint32_t)turning, (uint32_t)threads, span);
+    return launched();
 }
 
 template <class T>
-void launch(const Rotary &A, int heads, bool interleaved, cudaStream_t s)
+dbs_status launch(const Rotary &A, bool interleaved, cudaStream_t s)
 {
     // 16-byte accesses: all heads on such boundaries, and whole vectors in each part of a head
     constexpr int N = 16 / (int)sizeof(T);
@@ -160,8 +151,8 @@ void launch(const Rotary &A, int heads, bool interleaved, cudaStream_t s)
         wide = wide && aligned16(P.in) && aligned16(P.out) &&
                ((P.in_batch | P.in_token | P.in_head | P.out_batch | P.out_token | P.out_head) & (N - 1)) == 0;
     }
-    if (interleaved) wide ? launch_heads<T, true, true>(A, heads, s) : launch_heads<T, true, false>(A, heads, s);
-    else wide ? launch_heads<T, false, true>(A, heads, s) : launch_heads<T, false, false>(A, heads, s);
+    if (interleaved) return wide ? launch_units<T, true, true>(A, s) : launch_units<T, true, false>(A, s);
+    return wide ? launch_units<T, false, true>(A, s) : launch_units<T, false, false>(A, s);
 }
 
 struct Freqs {
@@ -230,13 +221,13 @@ dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype d
         head_dim > 1024 || dim < 0 || dim > head_dim || (dim & 1) || table_rows < 0)
         return DBS_ERR_INVALID_ARG;
     Rotary A{};
-    int heads = 0;
+    int64_t heads = 0;
     const bool work = batch > 0 && tokens > 0;
     if (work && (batch > (int64_t(1) << 31) || tokens > (int64_t(1) << 31) || batch * tokens >= (int64_t(1) << 31)))
         return DBS_ERR_INVALID_ARG;
     for (int p = 0; p < nparts; ++p) {
         const dbs_rotary_heads &P = parts[p];
-        if (P.heads < 0 || P.heads > 65536) return DBS_ERR_INVALID_ARG;
+        if (P.heads < 0 || P.heads > 16384) return DBS_ERR_INVALID_ARG;
         if (P.heads == 0) continue;
         if (work && (!P.in || !P.out || (P.rotate && dim > 0 && (!table || !positions)) ||
                      (P.to_slots && (!slots || pages < 0 || page_size < 1 || pages > (int64_t(1) << 31) / page_size))))
@@ -245,7 +236,7 @@ dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype d
         heads += P.heads;
     }
     if (!work || heads == 0) return DBS_OK;
-    if (batch * tokens * heads >= (int64_t(1) << 32)) return DBS_ERR_INVALID_ARG;
+    if (batch * tokens * head_dim >= (int64_t(1) << 32) - NT) return DBS_ERR_INVALID_ARG;
     A.head_dim = head_dim;
     A.dim = dim;
     A.tokens = tokens;
@@ -258,10 +249,9 @@ dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype d
     A.slots_end = slots ? pages * page_size : 0;
     A.sign = transposed ? -1.f : 1.f;
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == DBS_F32) launch<float>(A, heads, interleaved != 0, s);
-    else if (dtype == DBS_F16) launch<__half>(A, heads, interleaved != 0, s);
-    else launch<__nv_bfloat16>(A, heads, interleaved != 0, s);
-    return launched();
+    return dtype == DBS_F32   ? launch<float>(A, interleaved != 0, s)
+           : dtype == DBS_F16 ? launch<__half>(A, interleaved != 0, s)
+                              : launch<__nv_bfloat16>(A, interleaved != 0, s);
 }
 
 }  // extern "C"

@@ -24,25 +24,30 @@ __device__ __forceinline__ bool aligned_x(const T *x, int64_t stride)
     return (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (stride * sizeof(T) & 15u) == 0;
 }
 
+__device__ __forceinline__ float scale_at(const W4 &A, int sd, int64_t i)
+{
+    if (sd == DBS_F32) return ((const float *)A.scales)[i];
+    return sd == DBS_F16 ? to_f32(((const __half *)A.scales)[i]) : to_f32(((const __nv_bfloat16 *)A.scales)[i]);
+}
+
 constexpr int ROWS_NT = 128;     // four warps, one row each
 constexpr int ROWS_TOK = 4;      // tokens a warp carries at a time
 
 // Any alignment: one warp per row and ROWS_TOK tokens, two columns per byte.
-template <class T, class S>
-__global__ void __launch_bounds__(ROWS_NT) k_w4_rows(W4 A)
+template <class T>
+__global__ void __launch_bounds__(ROWS_NT) k_w4_rows(W4 A, int sd)
 {
     const int lane = threadIdx.x & 31;
     const int64_t i = (int64_t)blockIdx.x * (ROWS_NT / 32) + (threadIdx.x >> 5);
     if (i >= A.m) return;
     const uint8_t *q = A.q + i * A.q_stride;
-    const S *s = (const S *)A.scales + i * A.scale_stride;
     const uint8_t *z = A.zeros ? A.zeros + i * A.zero_stride : nullptr;
     const int64_t bytes = (A.n + 1) >> 1;
     for (int64_t t0 = (int64_t)blockIdx.y * ROWS_TOK; t0 < A.tokens; t0 += (int64_t)gridDim.y * ROWS_TOK) {
         float acc[ROWS_TOK] = {};
         for (int64_t c = lane; c < bytes; c += 32) {
             const int64_t j = 2 * c, g = j / A.group;
-            const float sc = to_f32(s[g]), zp = z ? (float)(z[g] & 127) : 8.f;
+            const float sc = scale_at(A, sd, i * A.scale_stride + g), zp = z ? (float)(z[g] & 127) : 8.f;
             const unsigned b = q[c];
             const float w0 = ((float)(b & 15u) - zp) * sc, w1 = ((float)(b >> 4) - zp) * sc;
 #pragma unroll
@@ -111,16 +116,18 @@ template <> struct Half2<__nv_bfloat16> {
 template <class T> struct Piece { using type = T; static constexpr int parts = 1; };
 template <> struct Piece<float> { using type = __nv_bfloat16; static constexpr int parts = 3; };
 
-constexpr int MMA_NT = 256, MMA_W = MMA_NT / 32;
-constexpr int STEP = 128;                      // columns of a stage: 64 bytes of a row
-__host__ __device__ constexpr int stages_of(int rt) { return rt == 1 ? 4 : 3; }
+constexpr int MMA_NT = 512, MMA_W = MMA_NT / 32;   // one block an SM
+constexpr int STAGES = 3, STAGE = 2048;           // of a warp's ring; bytes
+// A stage is RT tiles of 16 rows: 256 columns of one, or 128 of two.
+template <int RT> constexpr int STEP_V = RT == 1 ? 256 : 128;
 
 // How a call is cut up.
 struct Cut {
     int wk;                    // warps of a block that share a row tile and take turns of its stages
     int steps, phase;          // stages of a row; stages whose x is in shared memory at a time
-    int cols;                  // columns of B in use: tokens of a pass * parts
+    int shift;                 // log2 of the group
     int64_t groups;            // of rows: a block's rows at a time
+    int sd;                    // type of the scales
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes)
@@ -178,45 +185,50 @@ __device__ __forceinline__ void lay_out(const float *x, int64_t j, int64_t n, bo
     for (int p = 0; p < 3; ++p) out[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
 
-// One block takes groups of rows in turn; each warp streams stages of RT row
-// tiles (16 rows) through its own ring of shared memory (cp.async, no
-// block-wide wait), against x in shared memory.
-template <class T, class S, int NT, int RT>
-__global__ void __launch_bounds__(MMA_NT, 2) k_w4_mma(W4 A, Cut C)
+// One block takes groups of rows in turn; each warp streams stages of weights
+// through its own ring of shared memory (cp.async, no block-wide wait) against
+// x in shared memory: all of it, laid out once, or, where it does not fit, a
+// phase at a time.
+template <class T, int NT, int RT>
+__global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
 {
     using P = Piece<T>;
     using H = Half2<typename P::type>;
-    constexpr int NS = stages_of(RT), TILE = 16 * STEP / 2, STAGE = RT * TILE;
+    constexpr int STEP = STEP_V<RT>, ROWB = STEP / 2, CH = ROWB / 16, WORDS = STEP / 32;
+    constexpr int RED = RT * 16 * NT * 8;                                    // floats of a warp's sums
     extern __shared__ __align__(128) unsigned char sm[];
-    float *red = (float *)(sm + MMA_W * NS * STAGE);
-    uint4 *xs = (uint4 *)(sm + MMA_W * NS * STAGE + MMA_W * RT * 16 * NT * 8 * 4);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
-    const int wk = warp % C.wk, wr = warp / C.wk, wrs = MMA_W / C.wk;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm) + warp * NS * STAGE;
-    const unsigned char *ringp = sm + warp * NS * STAGE;
+    const int wk = warp & (C.wk - 1), wr = warp / C.wk, wrs = MMA_W / C.wk;
+    unsigned char *ringp = sm + warp * STAGES * STAGE;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ringp);
+    uint4 *const none = (uint4 *)(sm + MMA_W * STAGES * STAGE);              // 16 bytes of zeros
+    float *const red = (float *)(none + 8);          // (128 bytes on)
+    uint4 *const xs = (uint4 *)(red + (C.wk > 1 || P::parts > 1 ? MMA_W * RED : 0));
     const int64_t bytes = (A.n + 1) >> 1;
     const int64_t t0 = (int64_t)blockIdx.y * (NT * 8 / P::parts);            // the pass's first token
     const int64_t left = A.tokens - t0;
     const int tokens = (int)(left < NT * 8 / P::parts ? left : NT * 8 / P::parts), cols = tokens * P::parts;
     const T *x = (const T *)A.x + t0 * A.x_stride;
     const bool wide = aligned_x(x, A.x_stride);
-    const int last_group = (int)((A.n + A.group - 1) / A.group) - 1;
-    const uint32_t apply = A.group == 32 ? 0xfu : A.group == 64 ? 0xau : 0x8u;   // words that end a group
+    const int last_group = (int)((A.n - 1) >> C.shift);
+    const uint32_t per = (1u << C.shift) / 32u;                              // words of a group
 
     // the stages to fetch run ahead of the stages in use, across groups of rows
     int64_t fg = wk < C.steps ? blockIdx.x : C.groups;
     int fs = wk, slot = 0;
     auto fetch = [&]() {
         if (fg < C.groups) {
-            const int64_t row0 = (fg * wrs + wr) * (16 * RT);
-            const int64_t b0 = (int64_t)fs * (STEP / 2);
+            const int64_t row0 = (fg * wrs + wr) * (16 * RT) + lane / CH;
+            const int64_t at = (int64_t)fs * ROWB + (lane % CH) * 16, rest = bytes - at;
+            const int most = rest >= 16 ? 16 : rest > 0 ? (int)rest : 0;
+            const uint8_t *p = A.q + row0 * A.q_stride + at;
 #pragma unroll
-            for (int i = 0; i < 2 * RT; ++i) {
-                const int r = i * 8 + (lane >> 2), c = lane & 3;
-                const int64_t row = row0 + r, at = b0 + c * 16;
-                const int64_t rest = bytes - at;
-                const int take = row < A.m && rest > 0 ? (rest < 16 ? (int)rest : 16) : 0;
-                cp16(ring + slot * STAGE + r * 64 + ((c ^ ((r >> 1) & 3)) << 4), A.q + (take ? row * A.q_stride + at : 0), take);
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * (32 / CH) + lane / CH;
+                const int take = row0 + i * (32 / CH) < A.m ? most : 0;
+                const int c = (lane % CH) ^ (CH == 8 ? r & 7 : (r >> 1) & 3);
+                cp16(ring + slot * STAGE + r * ROWB + (c << 4), take ? p : A.q, take);
+                p += (32 / CH) * A.q_stride;
             }
             fs += C.wk;
             if (fs >= C.steps) {
@@ -224,118 +236,149 @@ __global__ void __launch_bounds__(MMA_NT, 2) k_w4_mma(W4 A, Cut C)
                 fg += gridDim.x;
             }
         }
-        slot = slot + 1 == NS ? 0 : slot + 1;
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // scales and zero points of a stage: lane t4 holds those of its 32 columns
-    auto constants = [&](int64_t grp, int st, float (&s)[RT][2], uint32_t (&z)[RT][2]) {
-        const int64_t row0 = (grp * wrs + wr) * (16 * RT);
-        int gi = (int)(((int64_t)st * STEP + 32 * t4) / A.group);
-        gi = gi < last_group ? gi : last_group;
+    // scales and zero points of a stage: those of word j of a row are in lane
+    // j % 4 of the row's four, set j / 4; of each row tile rows g and g + 8
+    float sn[2][2];
+    uint32_t zn[2][2];
+    auto constants = [&](int64_t grp, int st) {
+        const int64_t row0 = (grp * wrs + wr) * (16 * RT) + g;
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                int64_t row = row0 + 16 * r + 8 * h + g;
+                const int word = t4 + (RT == 1 ? 4 * i : 0);
+                int gi = (st * STEP + 32 * word) >> C.shift;
+                gi = gi < last_group ? gi : last_group;
+                int64_t row = row0 + (RT == 1 ? 0 : 16 * i) + 8 * h;
                 row = row < A.m ? row : A.m - 1;
-                s[r][h] = to_f32(((const S *)A.scales)[row * A.scale_stride + gi]);
-                const uint32_t zp = A.zeros ? A.zeros[row * A.zero_stride + gi] & 127u : 8u;
-                z[r][h] = H::magic + zp * H::one;
+                sn[i][h] = scale_at(A, C.sd, row * A.scale_stride + gi);
+                zn[i][h] = A.zeros ? A.zeros[row * A.zero_stride + gi] & 127u : 8u;
             }
     };
+    // x of a phase: piece (32-column block, column of B, quarter) at
+    // [block][column][quarter], 16 bytes each
+    auto place = [&](int i, int quarters, const uint4 (&v)[P::parts]) {
+        const int tok = i / quarters, k = i - tok * quarters;
 #pragma unroll
-    for (int i = 0; i < NS - 1; ++i) fetch();
-    float sn[RT][2];
-    uint32_t zn[RT][2];
-    if (wk < C.steps && blockIdx.x < C.groups) constants(blockIdx.x, wk, sn, zn);
+        for (int p = 0; p < P::parts; ++p) xs[((k >> 2) * cols + tok * P::parts + p) * 4 + (k & 3)] = v[p];
+    };
+    auto stage_x = [&](int p0, int p1) {
+        const int quarters = (p1 - p0) * (STEP / 8), all = quarters * tokens;
+        for (int i = threadIdx.x; i < all; i += 2 * MMA_NT) {
+            uint4 v[2][P::parts];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int at = i + k * MMA_NT < all ? i + k * MMA_NT : i, tok = at / quarters;
+                lay_out(x + tok * A.x_stride, (int64_t)p0 * STEP + 8 * (at - tok * quarters), A.n, wide, v[k]);
+            }
+            place(i, quarters, v[0]);
+            if (i + MMA_NT < all) place(i + MMA_NT, quarters, v[1]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fetch();
+    if (wk < C.steps && blockIdx.x < C.groups) constants(blockIdx.x, wk);
+    if (threadIdx.x < 8) none[threadIdx.x] = make_uint4(0, 0, 0, 0);
+
+    // this lane's pieces of B: column 8 c + g of each block, or zeros
+    int step_b[NT];
+    const uint4 *from[NT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+        const bool in = 8 * c + g < cols;
+        from[c] = in ? xs + (8 * c + g) * 4 + t4 : none;
+        step_b[c] = in ? cols * 4 : 0;
+    }
 
     int use = 0;
     bool have = false;
     for (int64_t grp = blockIdx.x; grp < C.groups; grp += gridDim.x) {
-        float tot[RT][NT][4];
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) tot[r][c][e] = 0.f;
+        float tot[RT][NT][4] = {};
         for (int p0 = 0; p0 < C.steps; p0 += C.phase) {
             const int p1 = p0 + C.phase < C.steps ? p0 + C.phase : C.steps;
             if (!have || C.phase < C.steps) {
-                // x of this phase: piece (32-column block, column, quarter) at
-                // [block][column][quarter], 16 bytes each
                 if (have) __syncthreads();
-                const int quarters = (p1 - p0) * (STEP / 8);
-                for (int i = threadIdx.x; i < quarters * tokens; i += MMA_NT) {
-                    const int tok = i / quarters, k = i % quarters;
-                    uint4 v[P::parts];
-                    lay_out(x + tok * A.x_stride, (int64_t)p0 * STEP + 8 * k, A.n, wide, v);
-#pragma unroll
-                    for (int p = 0; p < P::parts; ++p) xs[((k >> 2) * cols + tok * P::parts + p) * 4 + (k & 3)] = v[p];
-                }
+                stage_x(p0, p1);
                 __syncthreads();
                 have = true;
             }
             // phases are whole turns of the warps, so turns go on across them
             for (int st = p0 + wk; st < p1; st += C.wk) {
-                float sc[RT][2];
-                uint32_t zc[RT][2];
+                float sc[2][2];
+                uint32_t zc[2][2];
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        sc[r][h] = sn[r][h];
-                        zc[r][h] = zn[r][h];
+                        sc[i][h] = sn[i][h];
+                        zc[i][h] = H::magic + zn[i][h] * H::one;
                     }
                 fetch();
-                if (st + C.wk < C.steps) constants(grp, st + C.wk, sn, zn);
-                else if (grp + gridDim.x < C.groups) constants(grp + gridDim.x, wk, sn, zn);
-                asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
+                if (st + C.wk < C.steps) constants(grp, st + C.wk);
+                else if (grp + gridDim.x < C.groups) constants(grp + gridDim.x, wk);
+                asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
                 __syncwarp();
-                const unsigned char *w = ringp + use * STAGE;
-                use = use + 1 == NS ? 0 : use + 1;
+                const unsigned char *w = ringp + use * STAGE + g * ROWB + 4 * t4;
+                use = use + 1 == STAGES ? 0 : use + 1;
+                const uint4 *bx[NT];
+#pragma unroll
+                for (int c = 0; c < NT; ++c) bx[c] = from[c] + (st - p0) * WORDS * step_b[c];
                 float part[RT][NT][4];
+                uint32_t za[RT], zb[RT];
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int c = 0; c < NT; ++c)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) part[r][c][e] = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < WORDS; ++j) {
+                    const int src = (lane & ~3) | (j & 3);
                     uint4 b[NT];
 #pragma unroll
-                    for (int c = 0; c < NT; ++c)
-                        b[c] = 8 * c + g < cols ? xs[(((st - p0) * 4 + j) * cols + 8 * c + g) * 4 + t4] : make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < NT; ++c) {
+                        b[c] = *bx[c];
+                        bx[c] += step_b[c];
+                    }
+                    const bool begins = j == 0 || (j & (per - 1)) == 0, ends = j == WORDS - 1 || ((j + 1) & (per - 1)) == 0;
+                    if (begins) {
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            const int i = RT == 1 ? j >> 2 : r;
+                            za[r] = __shfl_sync(~0u, zc[i][0], src);
+                            zb[r] = __shfl_sync(~0u, zc[i][1], src);
+#pragma unroll
+                            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) part[r][c][e] = 0.f;
+                        }
+                    }
+                    const int o = (j ^ (CH == 8 ? g : g >> 1 & 3)) << 4;
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        const int src = (lane & ~3) | j;
-                        const uint32_t za = __shfl_sync(~0u, zc[r][0], src), zb = __shfl_sync(~0u, zc[r][1], src);
-                        const int o = ((j ^ ((g >> 1) & 3)) << 4) + 4 * t4;
-                        const uint32_t wa = *(const uint32_t *)(w + r * TILE + g * 64 + o), wb = *(const uint32_t *)(w + r * TILE + (g + 8) * 64 + o);
+                        const uint32_t wa = *(const uint32_t *)(w + r * 16 * ROWB + o), wb = *(const uint32_t *)(w + (r * 16 + 8) * ROWB + o);
                         uint32_t a[4];
-                        a[0] = H::sub((wa & 0x000f000fu) | H::magic, za);
-                        a[1] = H::sub((wb & 0x000f000fu) | H::magic, zb);
-                        a[2] = H::sub((wa >> 4 & 0x000f000fu) | H::magic, za);
-                        a[3] = H::sub((wb >> 4 & 0x000f000fu) | H::magic, zb);
+                        a[0] = H::sub((wa & 0x000f000fu) | H::magic, za[r]);
+                        a[1] = H::sub((wb & 0x000f000fu) | H::magic, zb[r]);
+                        a[2] = H::sub((wa >> 4 & 0x000f000fu) | H::magic, za[r]);
+                        a[3] = H::sub((wb >> 4 & 0x000f000fu) | H::magic, zb[r]);
 #pragma unroll
                         for (int c = 0; c < NT; ++c) H::mma(part[r][c], a, b[c].x, b[c].y);
-                        a[0] = H::sub((wa >> 8 & 0x000f000fu) | H::magic, za);
-                        a[1] = H::sub((wb >> 8 & 0x000f000fu) | H::magic, zb);
-                        a[2] = H::sub((wa >> 12 & 0x000f000fu) | H::magic, za);
-                        a[3] = H::sub((wb >> 12 & 0x000f000fu) | H::magic, zb);
+                        a[0] = H::sub((wa >> 8 & 0x000f000fu) | H::magic, za[r]);
+                        a[1] = H::sub((wb >> 8 & 0x000f000fu) | H::magic, zb[r]);
+                        a[2] = H::sub((wa >> 12 & 0x000f000fu) | H::magic, za[r]);
+                        a[3] = H::sub((wb >> 12 & 0x000f000fu) | H::magic, zb[r]);
 #pragma unroll
                         for (int c = 0; c < NT; ++c) H::mma(part[r][c], a, b[c].z, b[c].w);
-                        if (apply >> j & 1u) {
-                            const float sa = __shfl_sync(~0u, sc[r][0], src), sb = __shfl_sync(~0u, sc[r][1], src);
+                    }
+                    if (ends) {
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            const int i = RT == 1 ? j >> 2 : r;
+                            const float sa = __shfl_sync(~0u, sc[i][0], src), sb = __shfl_sync(~0u, sc[i][1], src);
 #pragma unroll
                             for (int c = 0; c < NT; ++c) {
                                 tot[r][c][0] = fmaf(sa, part[r][c][0], tot[r][c][0]);
                                 tot[r][c][1] = fmaf(sa, part[r][c][1], tot[r][c][1]);
                                 tot[r][c][2] = fmaf(sb, part[r][c][2], tot[r][c][2]);
                                 tot[r][c][3] = fmaf(sb, part[r][c][3], tot[r][c][3]);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) part[r][c][e] = 0.f;
                             }
                         }
                     }
@@ -343,8 +386,22 @@ __global__ void __launch_bounds__(MMA_NT, 2) k_w4_mma(W4 A, Cut C)
                 __syncwarp();
             }
         }
+        if (C.wk == 1 && P::parts == 1) {
+            // the warp has its rows' whole sums
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int64_t row = (grp * wrs + wr) * (16 * RT) + 16 * r + g + (e >> 1) * 8;
+                        const int tok = 8 * c + 2 * t4 + (e & 1);
+                        if (tok < tokens && row < A.m) ((T *)A.y)[(t0 + tok) * A.y_stride + row] = from_f32<T>(tot[r][c][e] * H::unit);
+                    }
+            continue;
+        }
         // sums of the warps of a row tile and of the pieces of a token, in order
-        float *mine = red + warp * (RT * 16 * NT * 8);
+        float *mine = red + warp * RED;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -359,13 +416,14 @@ __global__ void __launch_bounds__(MMA_NT, 2) k_w4_mma(W4 A, Cut C)
         __syncthreads();
         const int rows = wrs * RT * 16;
         for (int i = threadIdx.x; i < rows * tokens; i += MMA_NT) {
-            const int tok = i / rows, rr = i % rows, wr2 = rr / (RT * 16), r = rr % (RT * 16);
+            const int tok = i / rows, rr = i - tok * rows, wr2 = rr / (RT * 16), r = rr % (RT * 16);
             const int64_t row = grp * rows + rr;
+            const float *f = red + wr2 * C.wk * RED + tok * P::parts * (RT * 16) + r;
             float v = 0.f;
+#pragma unroll 4
             for (int k = 0; k < C.wk; ++k)
 #pragma unroll
-                for (int p = 0; p < P::parts; ++p)
-                    v += red[(wr2 * C.wk + k) * (RT * 16 * NT * 8) + (tok * P::parts + p) * (RT * 16) + r];
+                for (int p = 0; p < P::parts; ++p) v += f[k * RED + p * (RT * 16)];
             if (row < A.m) ((T *)A.y)[(t0 + tok) * A.y_stride + row] = from_f32<T>(v * H::unit);
         }
         __syncthreads();
@@ -373,66 +431,75 @@ __global__ void __launch_bounds__(MMA_NT, 2) k_w4_mma(W4 A, Cut C)
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Shared memory of a block, so that two of them fit an SM.
-constexpr int SMEM_MAX = 113 * 1024;
-__host__ __device__ constexpr int fixed_smem(int nt, int rt) { return MMA_W * stages_of(rt) * rt * 16 * STEP / 2 + MMA_W * rt * 16 * nt * 8 * 4; }
+constexpr int SMEM_MAX = 227 * 1024;
 
-template <class T, class S, int NT, int RT>
-dbs_status launch_mma(const W4 &A, cudaStream_t s)
+template <class T, int NT, int RT>
+dbs_status launch_mma(const W4 &A, dbs_dtype sd, cudaStream_t s)
 {
-    constexpr int parts = Piece<T>::parts, pass = NT * 8 / parts;
+    constexpr int parts = Piece<T>::parts, pass = NT * 8 / parts, STEP = STEP_V<RT>;
+    constexpr int ring = MMA_W * STAGES * STAGE + 128, red = MMA_W * RT * 16 * NT * 8 * 4;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(k_w4_mma<T, S, NT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess) {
+        cudaFuncSetAttribute(k_w4_mma<T, NT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess) {
         cudaGetLastError();
         return DBS_ERR_CUDA;
     }
     Cut C{};
     C.steps = (int)((A.n + STEP - 1) / STEP);
-    C.cols = (int)((A.tokens < pass ? A.tokens : pass) * parts);
-    const int step_bytes = STEP * C.cols * 2;
-    C.wk = MMA_W;
-    C.phase = (SMEM_MAX - fixed_smem(NT, RT)) / step_bytes;
-    if (C.phase >= C.steps) {
-        C.phase = C.steps;
-    } else {
-        // x does not fit at once: few warps share a row tile, so that a phase is long for each
-        C.wk = 2;
-        C.phase = C.phase / C.wk * C.wk;
+    C.sd = sd;
+    while (1 << C.shift < A.group) ++C.shift;
+    const int step_bytes = STEP * (int)((A.tokens < pass ? A.tokens : pass) * parts) * 2;
+    // Warps per row tile: the time of a block, counted in instructions of a
+    // warp: rounds of (its stages, about 300 + 64 NT for each row tile; the join
+    // of the warps' sums; laying out x again, if it does not fit at once, about
+    // 30 for 16 bytes of a piece).
+    double best = 0;
+    int smem = 0;
+    for (int wk = 1; wk <= MMA_W; wk *= 2) {
+        const int room = SMEM_MAX - ring - (wk > 1 || parts > 1 ? red : 0);
+        int phase = room / step_bytes;
+        if (phase >= C.steps) phase = C.steps;
+        else phase = phase / wk * wk;
+        if (phase < 1) continue;
+        const int rows = MMA_W / wk * RT * 16;
+        const int64_t groups = (A.m + rows - 1) / rows, rounds = (groups + sms - 1) / sms;
+        const double stages = (C.steps + wk - 1) / wk * (300. + 64 * NT) , join = wk > 1 ? 100. + 10 * NT * RT * wk : 60.;
+        const double lay = (double)C.steps * step_bytes / 16 / parts / MMA_NT * 30;
+        const double cost = rounds * (stages + join + (phase < C.steps ? lay + 1000. * ((C.steps + phase - 1) / phase) : 0.)) + lay;
+        if (smem == 0 || cost < best) {
+            best = cost;
+            C.wk = wk;
+            C.phase = phase;
+            C.groups = groups;
+            smem = ring + (wk > 1 || parts > 1 ? red : 0) + phase * step_bytes;
+        }
     }
-    const int rows = MMA_W / C.wk * RT * 16;
-    C.groups = (A.m + rows - 1) / rows;
-    const int64_t grid = C.groups < 2 * sms ? C.groups : 2 * sms;
+    const int64_t grid = C.groups < sms ? C.groups : sms;
     const int64_t passes = (A.tokens + pass - 1) / pass;
-    const int smem = fixed_smem(NT, RT) + (C.phase < C.steps ? C.phase : C.steps) * step_bytes;
     W4 B = A;
     for (int64_t p = 0; p < passes; p += 32768) {
         const int64_t now = passes - p < 32768 ? passes - p : 32768;
         B.x = (const T *)A.x + p * pass * A.x_stride;
         B.y = (T *)A.y + p * pass * A.y_stride;
         B.tokens = A.tokens - p * pass;
-        k_w4_mma<T, S, NT, RT><<<dim3((unsigned)grid, (unsigned)now), MMA_NT, smem, s>>>(B, C);
+        k_w4_mma<T, NT, RT><<<dim3((unsigned)grid, (unsigned)now), MMA_NT, smem, s>>>(B, C);
     }
-    return launched();
-}
-
-template <class T, class S>
-dbs_status launch(const W4 &A, cudaStream_t s)
-{
-    if (A.n > 0 && aligned16(A.q) && (A.q_stride & 15) == 0) {
-        const int64_t cols = A.tokens * Piece<T>::parts;
-        return cols <= 8 ? launch_mma<T, S, 1, 1>(A, s) : cols <= 16 ? launch_mma<T, S, 2, 2>(A, s) : launch_mma<T, S, 3, 2>(A, s);
-    }
-    const int64_t chunks = (A.tokens + ROWS_TOK - 1) / ROWS_TOK;
-    const dim3 grid((unsigned)((A.m + ROWS_NT / 32 - 1) / (ROWS_NT / 32)), (unsigned)(chunks < 65535 ? chunks : 65535));
-    k_w4_rows<T, S><<<grid, ROWS_NT, 0, s>>>(A);
     return launched();
 }
 
 template <class T>
-dbs_status launch_scales(const W4 &A, dbs_dtype sd, cudaStream_t s)
+dbs_status launch(const W4 &A, dbs_dtype sd, cudaStream_t s)
 {
-    return sd == DBS_F32 ? launch<T, float>(A, s) : sd == DBS_F16 ? launch<T, __half>(A, s) : launch<T, __nv_bfloat16>(A, s);
+    if (A.n > 0 && aligned16(A.q) && (A.q_stride & 15) == 0) {
+        // columns of B, in eights
+        const int64_t cols = A.tokens * Piece<T>::parts;
+        return cols <= 8 ? launch_mma<T, 1, 1>(A, sd, s) : cols <= 16 ? launch_mma<T, 2, 2>(A, sd, s) 
+                                                                           : cols <= 24 ? launch_mma<T, 3, 2>(A, sd, s) : launch_mma<T, 4, 2>(A, sd, s);
+    }
+    const int64_t chunks = (A.tokens + ROWS_TOK - 1) / ROWS_TOK;
+    const dim3 grid((unsigned)((A.m + ROWS_NT / 32 - 1) / (ROWS_NT / 32)), (unsigned)(chunks < 65535 ? chunks : 65535));
+    k_w4_rows<T><<<grid, ROWS_NT, 0, s>>>(A, sd);
+    return launched();
 }
 
 }  // namespace
@@ -451,7 +518,7 @@ extern "C" dbs_status dbs_w4_linear(const void *x, dbs_dtype dtype, int64_t toke
         return DBS_ERR_INVALID_ARG;
     const W4 A{x, q, scales, zeros, y, tokens, x_stride, q_stride, scale_stride, zero_stride, m, n, y_stride, group};
     cudaStream_t s = (cudaStream_t)stream;
-    return dtype == DBS_F32   ? launch_scales<float>(A, scale_dtype, s)
-           : dtype == DBS_F16 ? launch_scales<__half>(A, scale_dtype, s)
-                              : launch_scales<__nv_bfloat16>(A, scale_dtype, s);
+    return dtype == DBS_F32   ? launch<float>(A, scale_dtype, s)
+           : dtype == DBS_F16 ? launch<__half>(A, scale_dtype, s)
+                              : launch<__nv_bfloat16>(A, scale_dtype, s);
 }

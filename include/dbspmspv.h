@@ -496,7 +496,8 @@ typedef struct {
  *              tokens with a slot outside [0, pages * page_size) are not
  *              written.  Slots in use must differ from one another.
  *   head_dim   entries of a head, dim <= head_dim <= 1024, dim even
- *   batch * tokens < 2^31, and times all heads < 2^32
+ *   batch * tokens < 2^31, and times head_dim < 2^32 - 256; at most 16384 heads
+ *   in a group
  * Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */
 dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype dtype, int64_t batch, int64_t tokens,
                       int32_t head_dim, int32_t dim, const float *table, int64_t table_rows, const int32_t *positions,
@@ -559,9 +560,9 @@ typedef struct {
     void *out;                 /* device [batch, vocab], out_dtype; may be logits (same type and stride) */
     dbs_dtype out_dtype;
     int64_t out_stride;
-    int64_t batch, vocab;      /* vocab < 2^31 */
+    int64_t batch, vocab;      /* batch < 2^16, vocab < 2^31 - 8192 */
     const int32_t *history;    /* device [batch, history_max], rows history_stride apart */
-    int64_t history_max, history_stride;
+    int64_t history_max, history_stride;   /* history_max < 2^30 */
     const int32_t *history_lens;  /* device [batch], clamped to [0, history_max]; NULL = history_max */
     const int32_t *prompt_lens;   /* device [batch]; NULL = 0: everything is output */
     const float *repetition, *presence, *frequency;   /* device [batch] each, or NULL */
