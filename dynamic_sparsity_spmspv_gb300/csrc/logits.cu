@@ -90,6 +90,8 @@ __global__ void __launch_bounds__(NT, 2) k_logits(dbs_logits_args A, int width)
                 if (atomicMin(&first[ids[i] - v0], (unsigned)i) != NONE) listed_again = 1;
     }
     const float rep = A.repetition ? A.repetition[b] : 1.f, pres = A.presence ? A.presence[b] : 0.f;
+    // (a row's reciprocal once, instead of a division for each repeated token: 2 roundings for 1)
+    const float down = 1.f / rep;
     const float freq = A.frequency ? A.frequency[b] : 0.f;
     const unsigned *allowed = A.allowed ? (const unsigned *)A.allowed + b * A.allowed_stride : nullptr;
     const int last_word = (int)((A.vocab - 1) >> 5);
@@ -109,20 +111,28 @@ __global__ void __launch_bounds__(NT, 2) k_logits(dbs_logits_args A, int width)
         *(uint4 *)(c + 4) = *(const uint4 *)(count + i + 4);
 #pragma unroll
         for (int e = 0; e < RUN; ++e) l[e] = to_f32(in.v[e]);
-        if (c[0] | c[1] | c[2] | c[3] | c[4] | c[5] | c[6] | c[7]) {
+        const unsigned any = c[0] | c[1] | c[2] | c[3] | c[4] | c[5] | c[6] | c[7];
+        if (any) {
 #pragma unroll
             for (int e = 0; e < RUN; ++e) {
-                if (c[e] == 0) continue;
                 const unsigned n = c[e] & ~(SEEN | BIAS);
-                if ((c[e] & ~BIAS) && A.repetition) l[e] = l[e] > 0.f ? l[e] / rep : l[e] * rep;
-                if (n) l[e] -= freq * (float)n + pres;
-                if (c[e] & BIAS) {
-                    const unsigned k = first[i + e];
-                    l[e] += vals[k];
-                    if (listed_again)
-                        for (int m = (int)k + 1; m < nb; ++m)
-                            if (ids[m] == v + e) l[e] += vals[m];
-                }
+                if (c[e] & ~BIAS) l[e] *= l[e] > 0.f ? down : rep;
+                if (n) l[e] -= fmaf(freq, (float)n, pres);
+            }
+            if (any & BIAS) {
+                for (int e = 0; e < RUN; ++e)
+                    if (count[i + e] & BIAS) {
+                        const unsigned k = first[i + e];
+                        float add = l[0];
+#pragma unroll
+                        for (int m = 1; m < RUN; ++m) add = e == m ? l[m] : add;
+                        add += vals[k];
+                        if (listed_again)
+                            for (int m = (int)k + 1; m < nb; ++m)
+                                if (ids[m] == v + e) add += vals[m];
+#pragma unroll
+                        for (int m = 0; m < RUN; ++m) l[m] = e == m ? add : l[m];
+                    }
             }
         }
 #pragma unroll

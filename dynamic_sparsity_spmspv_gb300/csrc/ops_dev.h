@@ -20,7 +20,37 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-inline int dtype_size(int32_t d) { return d == DBS_F32 ? 4 : 2; }
+// Two 16-bit values of a word (or one fp32) to fp32, values 2i and 2i + 1 (or
+// i) of an array, and back, rounded once.
+template <class T, int N> __device__ __forceinline__ void open2(uint32_t w, float (&v)[N], int i)
+{
+    if constexpr (sizeof(T) == 4) {
+        v[i] = __uint_as_float(w);
+    } else if constexpr (__is_same(T, __nv_bfloat16)) {
+        v[2 * i] = __uint_as_float(w << 16);
+        v[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+template <class T> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if constexpr (__is_same(T, __nv_bfloat16)) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+template <class T, int N> __device__ __forceinline__ uint32_t shut2(const float (&v)[N], int i)
+{
+    if constexpr (sizeof(T) == 4) return __float_as_uint(v[i]);
+    else return pack2<T>(v[2 * i], v[2 * i + 1]);
+}
+
 inline bool dtype_ok(int32_t d) { return d == DBS_F32 || d == DBS_F16 || d == DBS_BF16; }
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

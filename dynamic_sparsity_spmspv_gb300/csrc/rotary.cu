@@ -21,21 +21,55 @@ struct Rotary {
 
 constexpr int NT = 256;
 
-// 16 bytes of a head, or one value where rows are not aligned for that.
+// What a thread moves of a head at once: 16 bytes, or one value where rows are
+// not aligned for that.
 template <class T, bool WIDE> struct Vec {
     static constexpr int n = WIDE ? 16 / (int)sizeof(T) : 1;
-    struct alignas(n * sizeof(T)) type {
-        T v[n];
-    };
+    using type = uint4;
+};
+template <> struct Vec<float, false> {
+    static constexpr int n = 1;
+    using type = uint32_t;
+};
+template <> struct Vec<__half, false> {
+    static constexpr int n = 1;
+    using type = uint16_t;
+};
+template <> struct Vec<__nv_bfloat16, false> {
+    static constexpr int n = 1;
+    using type = uint16_t;
 };
 
+// The values of a vector in fp32, and back with their one rounding.
+template <class T> __device__ __forceinline__ void open(const uint4 &w, float (&v)[16 / sizeof(T)])
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) open2<T>(u[i], v, i);
+}
+template <class T> __device__ __forceinline__ uint4 shut(const float (&v)[16 / sizeof(T)])
+{
+    return make_uint4(shut2<T>(v, 0), shut2<T>(v, 1), shut2<T>(v, 2), shut2<T>(v, 3));
+}
+template <class T> __device__ __forceinline__ void open(uint16_t w, float (&v)[1]) { v[0] = to_f32(*reinterpret_cast<const T *>(&w)); }
+template <class T> __device__ __forceinline__ void open(uint32_t w, float (&v)[1]) { v[0] = __uint_as_float(w); }
+template <class T> __device__ __forceinline__ void shut(const float (&v)[1], uint16_t &w)
+{
+    const T t = from_f32<T>(v[0]);
+    w = *reinterpret_cast<const uint16_t *>(&t);
+}
+template <class T> __device__ __forceinline__ void shut(const float (&v)[1], uint32_t &w) { w = __float_as_uint(v[0]); }
+template <class T, int N> __device__ __forceinline__ void shut(const float (&v)[N], uint4 &w) { w = shut<T>(v); }
+
 // A unit of a head is what one thread turns at once: vectors i and i + dim/2 of
-// the half layout, one vector of pairs of the interleaved one, or one vector of
-// the copied rest.  A thread keeps its token's cosines and sines for up to
-// `span` heads of one group (blockIdx.y), four of whose loads are issued
-// together.  Bound by HBM: every entry is read and written once.
-template <class T, bool INTERLEAVED, bool WIDE>
-__global__ void __launch_bounds__(NT) k_rotary(Rotary A, uint32_t units, uint32_t turning, uint32_t threads, int span)
+// the half layout, or one vector of pairs of the interleaved one.  A thread
+// keeps its token's cosines and sines for up to `span` heads of one group
+// (blockIdx.y), four of whose loads are issued together.  The copied rest of the
+// heads (and all of a group that is not turned) has blocks of its own, COPY, so
+// that no warp does both.  Bound by HBM: every entry is read and written once.
+template <class T, bool INTERLEAVED, bool WIDE, bool COPY>
+__device__ __forceinline__ void turn_heads(const Rotary &A, const dbs_rotary_heads &P, int h0, int heads, uint32_t units, uint32_t threads,
+                                           int from)
 {
     using V = Vec<T, WIDE>;
     using VT = typename V::type;
@@ -43,19 +77,16 @@ __global__ void __launch_bounds__(NT) k_rotary(Rotary A, uint32_t units, uint32_
     // interleaved pairs of single values: two entries a unit
     constexpr int PAIRS = INTERLEAVED ? (WIDE ? N / 2 : 1) : N;
     constexpr int F = !WIDE ? 1 : PAIRS < 4 ? PAIRS : 4;      // entries of the table in one load
-    constexpr bool TWO = !INTERLEAVED || !WIDE;               // a second vector at hi
+    constexpr bool TWO = !COPY && (!INTERLEAVED || !WIDE);    // a second vector
     const uint32_t i = blockIdx.x * NT + threadIdx.x;
     if (i >= threads) return;
-    // this block's heads
-    int y = blockIdx.y, p = 0;
-    while (p + 1 < A.nparts && y >= (A.part[p].heads + span - 1) / span) y -= (A.part[p++].heads + span - 1) / span;
-    const dbs_rotary_heads &P = A.part[p];
-    const int h0 = y * span, heads = P.heads - h0 < span ? P.heads - h0 : span;
-
     const uint32_t tok = i / units, c = i - tok * units;
     const uint32_t b = tok / (uint32_t)A.tokens, t = tok - b * (uint32_t)A.tokens;
-    const T *in = (const T *)P.in + b * P.in_batch + t * P.in_token + h0 * P.in_head;
-    T *out = (T *)P.out + h0 * P.out_head;
+    const int half = A.dim / 2, pair = (int)c * PAIRS;        // the unit's first pair
+    const int lo = COPY ? from + (int)c * N : INTERLEAVED ? 2 * pair : pair;
+    const int apart = INTERLEAVED ? 1 : half;
+    const T *in = (const T *)P.in + b * P.in_batch + t * P.in_token + h0 * P.in_head + lo;
+    T *out = (T *)P.out + h0 * P.out_head + lo;
     if (P.to_slots) {
         const int64_t slot = A.slots[tok];
         if (slot < 0 || slot >= A.slots_end) return;
@@ -64,15 +95,8 @@ __global__ void __launch_bounds__(NT) k_rotary(Rotary A, uint32_t units, uint32_
     } else {
         out += b * P.out_batch + t * P.out_token;
     }
-    const bool turn = c < turning && P.rotate;
-    const bool two = TWO && c < turning;
-    const int half = A.dim / 2, pair = (int)c * PAIRS;        // the unit's first pair
-    const int lo = c >= turning ? A.dim + (int)(c - turning) * N : INTERLEAVED ? 2 * pair : pair;
-    const int apart = INTERLEAVED ? 1 : half;
-    in += lo;
-    out += lo;
     float cs[PAIRS], sn[PAIRS];
-    if (turn) {
+    if (!COPY) {
         const int64_t pos = A.positions[tok];
         const bool ok = pos >= 0 && pos < A.table_rows;
 #pragma unroll
@@ -99,44 +123,86 @@ __global__ void __launch_bounds__(NT) k_rotary(Rotary A, uint32_t units, uint32_
         for (int k = 0; k < 4; ++k)
             if (h + k < heads) {
                 x[k] = *(const VT *)(in + k * P.in_head);
-                if (two) z[k] = *(const VT *)(in + k * P.in_head + apart);
+                if (TWO) z[k] = *(const VT *)(in + k * P.in_head + apart);
             }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (h + k < heads) {
-                if (turn) {
+                if (!COPY) {
+                    float u[N], v[N];
+                    open<T>(x[k], u);
+                    if (TWO) open<T>(z[k], v);
 #pragma unroll
                     for (int q = 0; q < PAIRS; ++q) {
-                        T &a = x[k].v[TWO ? q : 2 * q], &d = TWO ? z[k].v[q] : x[k].v[TWO ? 0 : 2 * q + 1];
-                        const float u = to_f32(a), v = to_f32(d);
-                        a = from_f32<T>(u * cs[q] - v * sn[q]);
-                        d = from_f32<T>(u * sn[q] + v * cs[q]);
+                        float &a = u[TWO ? q : 2 * q], &d = TWO ? v[q] : u[TWO ? 0 : 2 * q + 1];
+                        const float a0 = a, d0 = d;
+                        a = a0 * cs[q] - d0 * sn[q];
+                        d = a0 * sn[q] + d0 * cs[q];
                     }
+                    shut<T>(u, x[k]);
+                    if (TWO) shut<T>(v, z[k]);
                 }
                 *(VT *)(out + k * P.out_head) = x[k];
-                if (two) *(VT *)(out + k * P.out_head + apart) = z[k];
+                if (TWO) *(VT *)(out + k * P.out_head + apart) = z[k];
             }
         in += 4 * P.in_head;
         out += 4 * P.out_head;
     }
 }
 
+// blockIdx.y: the chunks of `span` heads of every turned group, then those of
+// every copied part.
+template <class T, bool INTERLEAVED, bool WIDE>
+__global__ void __launch_bounds__(NT) k_rotary(Rotary A, uint32_t turning, int span)
+{
+    constexpr int N = Vec<T, WIDE>::n;
+    int y = blockIdx.y;
+    for (int copy = 0; copy < 2; ++copy)
+        for (int p = 0; p < A.nparts; ++p) {
+            const dbs_rotary_heads &P = A.part[p];
+            const int from = P.rotate ? A.dim : 0;
+            if (copy ? from == A.head_dim : !P.rotate || turning == 0) continue;
+            const int chunks = (P.heads + span - 1) / span;
+            if (y >= chunks) {
+                y -= chunks;
+                continue;
+            }
+            const int h0 = y * span, heads = P.heads - h0 < span ? P.heads - h0 : span;
+            if (!copy) {
+                turn_heads<T, INTERLEAVED, WIDE, false>(A, P, h0, heads, turning, (uint32_t)A.total * turning, 0);
+            } else {
+                const uint32_t units = (uint32_t)(A.head_dim - from) / N;
+                turn_heads<T, INTERLEAVED, WIDE, true>(A, P, h0, heads, units, (uint32_t)A.total * units, from);
+            }
+            return;
+        }
+}
+
 template <class T, bool INTERLEAVED, bool WIDE>
 dbs_status launch_units(const Rotary &A, cudaStream_t s)
 {
     constexpr int N = Vec<T, WIDE>::n, E = INTERLEAVED ? (WIDE ? N : 2) : 2 * N;
-    const int turning = A.dim / E, units = turning + (A.head_dim - A.dim) / N;
-    const int64_t threads = A.total * units;
+    const int turning = A.dim / E;
     // Heads of a thread: eight, so that a token's angles are read once for all of
     // them, and fewer while that leaves the GPU's 152 x 2048 threads idle.
+    int64_t most = 0;
     int span = 8, chunks = 0;
     for (;; span /= 2) {
+        int64_t threads = 0;
         chunks = 0;
-        for (int p = 0; p < A.nparts; ++p) chunks += (A.part[p].heads + span - 1) / span;
-        if (span == 1 || threads * chunks >= 152 * 2048) break;
+        for (int copy = 0; copy < 2; ++copy)
+            for (int p = 0; p < A.nparts; ++p) {
+                const int from = A.part[p].rotate ? A.dim : 0;
+                if (copy ? from == A.head_dim : !A.part[p].rotate || turning == 0) continue;
+                const int64_t units = copy ? (A.head_dim - from) / N : turning;
+                const int n = (A.part[p].heads + span - 1) / span;
+                chunks += n;
+                threads += A.total * units * n;
+                most = most > A.total * units ? most : A.total * units;
+            }
+        if (span == 1 || threads >= 152 * 2048) break;
     }
-    k_rotary<T, INTERLEAVED, WIDE><<<dim3((unsigned)((threads + NT - 1) / NT), (unsigned)chunks), NT, 0, s>>>(
-        A, (uint32_t)units, (uint32_t)turning, (uint32_t)threads, span);
+    k_rotary<T, INTERLEAVED, WIDE><<<dim3((unsigned)((most + NT - 1) / NT), (unsigned)chunks), NT, 0, s>>>(A, (uint32_t)turning, span);
     return launched();
 }
 

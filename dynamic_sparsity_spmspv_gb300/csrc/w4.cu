@@ -24,18 +24,12 @@ __device__ __forceinline__ bool aligned_x(const T *x, int64_t stride)
     return (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (stride * sizeof(T) & 15u) == 0;
 }
 
-__device__ __forceinline__ float scale_at(const W4 &A, int sd, int64_t i)
-{
-    if (sd == DBS_F32) return ((const float *)A.scales)[i];
-    return sd == DBS_F16 ? to_f32(((const __half *)A.scales)[i]) : to_f32(((const __nv_bfloat16 *)A.scales)[i]);
-}
-
 constexpr int ROWS_NT = 128;     // four warps, one row each
 constexpr int ROWS_TOK = 4;      // tokens a warp carries at a time
 
 // Any alignment: one warp per row and ROWS_TOK tokens, two columns per byte.
-template <class T>
-__global__ void __launch_bounds__(ROWS_NT) k_w4_rows(W4 A, int sd)
+template <class T, class S>
+__global__ void __launch_bounds__(ROWS_NT) k_w4_rows(W4 A)
 {
     const int lane = threadIdx.x & 31;
     const int64_t i = (int64_t)blockIdx.x * (ROWS_NT / 32) + (threadIdx.x >> 5);
@@ -47,7 +41,7 @@ __global__ void __launch_bounds__(ROWS_NT) k_w4_rows(W4 A, int sd)
         float acc[ROWS_TOK] = {};
         for (int64_t c = lane; c < bytes; c += 32) {
             const int64_t j = 2 * c, g = j / A.group;
-            const float sc = scale_at(A, sd, i * A.scale_stride + g), zp = z ? (float)(z[g] & 127) : 8.f;
+            const float sc = to_f32(((const S *)A.scales)[i * A.scale_stride + g]), zp = z ? (float)(z[g] & 127) : 8.f;
             const unsigned b = q[c];
             const float w0 = ((float)(b & 15u) - zp) * sc, w1 = ((float)(b >> 4) - zp) * sc;
 #pragma unroll
@@ -127,7 +121,6 @@ struct Cut {
     int steps, phase;          // stages of a row; stages whose x is in shared memory at a time
     int shift;                 // log2 of the group
     int64_t groups;            // of rows: a block's rows at a time
-    int sd;                    // type of the scales
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes)
@@ -163,33 +156,56 @@ __device__ __forceinline__ void lay_out(const float *x, int64_t j, int64_t n, bo
         for (int e = 0; e < 8; ++e) v[e] = j + e < n ? x[j + e] : 0.f;
     }
     uint32_t w[3][4];
+    float odd = 0.f;                     // NaN if a value is not finite
+#pragma unroll
+    for (int e = 0; e < 8; ++e) odd = fmaf(v[e], 0.f, odd);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        uint32_t hi[2], mid[2], lo[2];
+        float r[2], q[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const float f = v[e + 4 * k];
-            uint32_t b = __float_as_uint(f);
-            const bool fin = (b & 0x7f800000u) != 0x7f800000u;
-            if (!fin && (b & 0x007fffffu)) b |= 0x00400000u;               // a NaN stays one
-            hi[k] = b & 0xffff0000u;
-            const float r1 = fin ? f - __uint_as_float(hi[k]) : 0.f;
-            mid[k] = __float_as_uint(r1) & 0xffff0000u;
-            lo[k] = __float_as_uint(r1 - __uint_as_float(mid[k]));
+            r[k] = f - __uint_as_float(__float_as_uint(f) & 0xffff0000u);
+            q[k] = r[k] - __uint_as_float(__float_as_uint(r[k]) & 0xffff0000u);
         }
-        w[0][e] = hi[0] >> 16 | hi[1];
-        w[1][e] = mid[0] >> 16 | mid[1];
-        w[2][e] = lo[0] >> 16 | (lo[1] & 0xffff0000u);
+        // the upper halves of two words
+        w[0][e] = __byte_perm(__float_as_uint(v[e]), __float_as_uint(v[e + 4]), 0x7632);
+        w[1][e] = __byte_perm(__float_as_uint(r[0]), __float_as_uint(r[1]), 0x7632);
+        w[2][e] = __byte_perm(__float_as_uint(q[0]), __float_as_uint(q[1]), 0x7632);
+    }
+    if (odd != odd) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t mask = e < 4 ? 0xffff0000u : 0x0000ffffu;         // of the other value of the word
+            if (v[e] != v[e]) w[0][e & 3] = (w[0][e & 3] & mask) | (0x7fc07fc0u & ~mask);   // a NaN stays one
+            if (!isfinite(v[e])) {
+                w[1][e & 3] &= mask;
+                w[2][e & 3] &= mask;
+            }
+        }
     }
 #pragma unroll
     for (int p = 0; p < 3; ++p) out[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+
+__device__ __forceinline__ uint4 ld16(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld4(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
 }
 
 // One block takes groups of rows in turn; each warp streams stages of weights
 // through its own ring of shared memory (cp.async, no block-wide wait) against
 // x in shared memory: all of it, laid out once, or, where it does not fit, a
 // phase at a time.
-template <class T, int NT, int RT>
+template <class T, class S, int NT, int RT>
 __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
 {
     using P = Piece<T>;
@@ -199,8 +215,7 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
     extern __shared__ __align__(128) unsigned char sm[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
     const int wk = warp & (C.wk - 1), wr = warp / C.wk, wrs = MMA_W / C.wk;
-    unsigned char *ringp = sm + warp * STAGES * STAGE;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ringp);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + warp * STAGES * STAGE);
     uint4 *const none = (uint4 *)(sm + MMA_W * STAGES * STAGE);              // 16 bytes of zeros
     float *const red = (float *)(none + 8);          // (128 bytes on)
     uint4 *const xs = (uint4 *)(red + (C.wk > 1 || P::parts > 1 ? MMA_W * RED : 0));
@@ -213,50 +228,76 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
     const int last_group = (int)((A.n - 1) >> C.shift);
     const uint32_t per = (1u << C.shift) / 32u;                              // words of a group
 
-    // the stages to fetch run ahead of the stages in use, across groups of rows
+    // The stages to fetch run ahead of the stages in use, across groups of rows.
+    // A lane copies 16 bytes of every (32 / CH)-th row of a stage.
+    constexpr int RS = 32 / CH;
+    const int fr = lane / CH, fc = lane % CH;
     int64_t fg = wk < C.steps ? blockIdx.x : C.groups;
-    int fs = wk, slot = 0;
+    int fs = wk, slot = 0, rows_left;
+    const uint8_t *fp;
+    auto fetch_from = [&]() {
+        const int64_t row0 = (fg * wrs + wr) * (16 * RT) + fr;
+        fp = A.q + row0 * A.q_stride + (int64_t)wk * ROWB + fc * 16;
+        rows_left = (int)(A.m - row0 < 64 ? A.m - row0 : 64);
+    };
+    if (fg < C.groups) fetch_from();
+    uint32_t to[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * RS + fr;
+        to[i] = ring + r * ROWB + ((fc ^ (CH == 8 ? r & 7 : (r >> 1) & 3)) << 4);
+    }
+    const int64_t down = RS * A.q_stride;
     auto fetch = [&]() {
         if (fg < C.groups) {
-            const int64_t row0 = (fg * wrs + wr) * (16 * RT) + lane / CH;
-            const int64_t at = (int64_t)fs * ROWB + (lane % CH) * 16, rest = bytes - at;
-            const int most = rest >= 16 ? 16 : rest > 0 ? (int)rest : 0;
-            const uint8_t *p = A.q + row0 * A.q_stride + at;
+            const int rest = (int)bytes - fs * ROWB - fc * 16;
+            const int most = rest >= 16 ? 16 : rest > 0 ? rest : 0;
+            const uint8_t *p = fp;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = i * (32 / CH) + lane / CH;
-                const int take = row0 + i * (32 / CH) < A.m ? most : 0;
-                const int c = (lane % CH) ^ (CH == 8 ? r & 7 : (r >> 1) & 3);
-                cp16(ring + slot * STAGE + r * ROWB + (c << 4), take ? p : A.q, take);
-                p += (32 / CH) * A.q_stride;
+                const int take = i * RS < rows_left ? most : 0;
+                cp16(to[i] + slot * STAGE, take ? p : A.q, take);
+                p += down;
             }
             fs += C.wk;
+            fp += C.wk * ROWB;
             if (fs >= C.steps) {
                 fs = wk;
                 fg += gridDim.x;
+                if (fg < C.groups) fetch_from();
             }
         }
         slot = slot + 1 == STAGES ? 0 : slot + 1;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // scales and zero points of a stage: those of word j of a row are in lane
-    // j % 4 of the row's four, set j / 4; of each row tile rows g and g + 8
-    float sn[2][2];
-    uint32_t zn[2][2];
-    auto constants = [&](int64_t grp, int st) {
+    // Scales and zero points of a stage: those of word j of a row are in lane
+    // j % 4 of the row's four, set j / 4; of each row tile rows g and g + 8.
+    // (Offsets fit 32 bits: the launch sees to it.)
+    S sn[2][2];
+    uint32_t zn[2][2], so[2][2], zo[2][2];
+    auto constants_from = [&](int64_t grp) {
         const int64_t row0 = (grp * wrs + wr) * (16 * RT) + g;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int word = t4 + (RT == 1 ? 4 * i : 0);
-                int gi = (st * STEP + 32 * word) >> C.shift;
-                gi = gi < last_group ? gi : last_group;
                 int64_t row = row0 + (RT == 1 ? 0 : 16 * i) + 8 * h;
                 row = row < A.m ? row : A.m - 1;
-                sn[i][h] = scale_at(A, C.sd, row * A.scale_stride + gi);
-                zn[i][h] = A.zeros ? A.zeros[row * A.zero_stride + gi] & 127u : 8u;
+                so[i][h] = (uint32_t)(row * A.scale_stride);
+                zo[i][h] = (uint32_t)(row * A.zero_stride);
             }
+    };
+    auto constants = [&](int st) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            int gi = (st * STEP + 32 * (t4 + (RT == 1 ? 4 * i : 0))) >> C.shift;
+            gi = gi < last_group ? gi : last_group;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                sn[i][h] = ((const S *)A.scales)[so[i][h] + (uint32_t)gi];
+                zn[i][h] = A.zeros ? A.zeros[zo[i][h] + (uint32_t)gi] : 8u;
+            }
+        }
     };
     // x of a phase: piece (32-column block, column of B, quarter) at
     // [block][column][quarter], 16 bytes each
@@ -280,17 +321,19 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
     };
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) fetch();
-    if (wk < C.steps && blockIdx.x < C.groups) constants(blockIdx.x, wk);
+    if (wk < C.steps && blockIdx.x < C.groups) {
+        constants_from(blockIdx.x);
+        constants(wk);
+    }
     if (threadIdx.x < 8) none[threadIdx.x] = make_uint4(0, 0, 0, 0);
 
     // this lane's pieces of B: column 8 c + g of each block, or zeros
-    int step_b[NT];
-    const uint4 *from[NT];
+    uint32_t step_b[NT], from[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         const bool in = 8 * c + g < cols;
-        from[c] = in ? xs + (8 * c + g) * 4 + t4 : none;
-        step_b[c] = in ? cols * 4 : 0;
+        from[c] = (uint32_t)__cvta_generic_to_shared(in ? xs + (8 * c + g) * 4 + t4 : none);
+        step_b[c] = in ? cols * 64 : 0;
     }
 
     int use = 0;
@@ -313,17 +356,21 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        sc[i][h] = sn[i][h];
-                        zc[i][h] = H::magic + zn[i][h] * H::one;
+                        sc[i][h] = to_f32(sn[i][h]);
+                        zc[i][h] = H::magic + (zn[i][h] & 127u) * H::one;
                     }
                 fetch();
-                if (st + C.wk < C.steps) constants(grp, st + C.wk);
-                else if (grp + gridDim.x < C.groups) constants(grp + gridDim.x, wk);
+                if (st + C.wk < C.steps) {
+                    constants(st + C.wk);
+                } else if (grp + gridDim.x < C.groups) {
+                    constants_from(grp + gridDim.x);
+                    constants(wk);
+                }
                 asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
                 __syncwarp();
-                const unsigned char *w = ringp + use * STAGE + g * ROWB + 4 * t4;
+                const uint32_t w = ring + use * STAGE + g * ROWB + 4 * t4;
                 use = use + 1 == STAGES ? 0 : use + 1;
-                const uint4 *bx[NT];
+                uint32_t bx[NT];
 #pragma unroll
                 for (int c = 0; c < NT; ++c) bx[c] = from[c] + (st - p0) * WORDS * step_b[c];
                 float part[RT][NT][4];
@@ -334,7 +381,7 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
                     uint4 b[NT];
 #pragma unroll
                     for (int c = 0; c < NT; ++c) {
-                        b[c] = *bx[c];
+                        b[c] = ld16(bx[c]);
                         bx[c] += step_b[c];
                     }
                     const bool begins = j == 0 || (j & (per - 1)) == 0, ends = j == WORDS - 1 || ((j + 1) & (per - 1)) == 0;
@@ -353,7 +400,7 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
                     const int o = (j ^ (CH == 8 ? g : g >> 1 & 3)) << 4;
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        const uint32_t wa = *(const uint32_t *)(w + r * 16 * ROWB + o), wb = *(const uint32_t *)(w + (r * 16 + 8) * ROWB + o);
+                        const uint32_t wa = ld4(w + r * 16 * ROWB + o), wb = ld4(w + (r * 16 + 8) * ROWB + o);
                         uint32_t a[4];
                         a[0] = H::sub((wa & 0x000f000fu) | H::magic, za[r]);
                         a[1] = H::sub((wb & 0x000f000fu) | H::magic, zb[r]);
@@ -433,20 +480,19 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
 
 constexpr int SMEM_MAX = 227 * 1024;
 
-template <class T, int NT, int RT>
-dbs_status launch_mma(const W4 &A, dbs_dtype sd, cudaStream_t s)
+template <class T, class S, int NT, int RT>
+dbs_status launch_mma(const W4 &A, cudaStream_t s)
 {
     constexpr int parts = Piece<T>::parts, pass = NT * 8 / parts, STEP = STEP_V<RT>;
     constexpr int ring = MMA_W * STAGES * STAGE + 128, red = MMA_W * RT * 16 * NT * 8 * 4;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(k_w4_mma<T, NT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess) {
+        cudaFuncSetAttribute(k_w4_mma<T, S, NT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess) {
         cudaGetLastError();
         return DBS_ERR_CUDA;
     }
     Cut C{};
     C.steps = (int)((A.n + STEP - 1) / STEP);
-    C.sd = sd;
     while (1 << C.shift < A.group) ++C.shift;
     const int step_bytes = STEP * (int)((A.tokens < pass ? A.tokens : pass) * parts) * 2;
     // Warps per row tile: the time of a block, counted in instructions of a
@@ -482,24 +528,30 @@ dbs_status launch_mma(const W4 &A, dbs_dtype sd, cudaStream_t s)
         B.x = (const T *)A.x + p * pass * A.x_stride;
         B.y = (T *)A.y + p * pass * A.y_stride;
         B.tokens = A.tokens - p * pass;
-        k_w4_mma<T, NT, RT><<<dim3((unsigned)grid, (unsigned)now), MMA_NT, smem, s>>>(B, C);
+        k_w4_mma<T, S, NT, RT><<<dim3((unsigned)grid, (unsigned)now), MMA_NT, smem, s>>>(B, C);
     }
     return launched();
 }
 
-template <class T>
-dbs_status launch(const W4 &A, dbs_dtype sd, cudaStream_t s)
+template <class T, class S>
+dbs_status launch(const W4 &A, cudaStream_t s)
 {
-    if (A.n > 0 && aligned16(A.q) && (A.q_stride & 15) == 0) {
-        // columns of B, in eights
-        const int64_t cols = A.tokens * Piece<T>::parts;
-        return cols <= 8 ? launch_mma<T, 1, 1>(A, sd, s) : cols <= 16 ? launch_mma<T, 2, 2>(A, sd, s) 
-                                                                           : cols <= 24 ? launch_mma<T, 3, 2>(A, sd, s) : launch_mma<T, 4, 2>(A, sd, s);
+    constexpr int64_t LIMIT = int64_t(1) << 32;
+    if (A.n > 0 && aligned16(A.q) && (A.q_stride & 15) == 0 && (A.m + 1) * A.scale_stride < LIMIT && (A.m + 1) * A.zero_stride < LIMIT) {
+        const int64_t cols = A.tokens * Piece<T>::parts;         // of B, in eights
+        return cols <= 8 ? launch_mma<T, S, 1, 1>(A, s) : cols <= 16 ? launch_mma<T, S, 2, 2>(A, s)
+               : cols <= 24 ? launch_mma<T, S, 3, 2>(A, s) : launch_mma<T, S, 4, 2>(A, s);
     }
     const int64_t chunks = (A.tokens + ROWS_TOK - 1) / ROWS_TOK;
     const dim3 grid((unsigned)((A.m + ROWS_NT / 32 - 1) / (ROWS_NT / 32)), (unsigned)(chunks < 65535 ? chunks : 65535));
-    k_w4_rows<T><<<grid, ROWS_NT, 0, s>>>(A, sd);
+    k_w4_rows<T, S><<<grid, ROWS_NT, 0, s>>>(A);
     return launched();
+}
+
+template <class T>
+dbs_status launch_scales(const W4 &A, dbs_dtype sd, cudaStream_t s)
+{
+    return sd == DBS_F32 ? launch<T, float>(A, s) : sd == DBS_F16 ? launch<T, __half>(A, s) : launch<T, __nv_bfloat16>(A, s);
 }
 
 }  // namespace
@@ -518,7 +570,7 @@ extern "C" dbs_status dbs_w4_linear(const void *x, dbs_dtype dtype, int64_t toke
         return DBS_ERR_INVALID_ARG;
     const W4 A{x, q, scales, zeros, y, tokens, x_stride, q_stride, scale_stride, zero_stride, m, n, y_stride, group};
     cudaStream_t s = (cudaStream_t)stream;
-    return dtype == DBS_F32   ? launch<float>(A, scale_dtype, s)
-           : dtype == DBS_F16 ? launch<__half>(A, scale_dtype, s)
-                              : launch<__nv_bfloat16>(A, scale_dtype, s);
+    return dtype == DBS_F32   ? launch_scales<float>(A, scale_dtype, s)
+           : dtype == DBS_F16 ? launch_scales<__half>(A, scale_dtype, s)
+                              : launch_scales<__nv_bfloat16>(A, scale_dtype, s);
 }
