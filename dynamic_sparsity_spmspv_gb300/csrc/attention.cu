@@ -13,6 +13,7 @@ struct Attn {
     dbs_attention_args a;
     float scale_log2;          // scale * log2(e): probabilities are powers of two
     int words;                 // 64-bit mask words per token
+    bool wide_out;             // heads of out start on 16-byte boundaries
 };
 
 // What sequence b holds, with every length clamped to its range.
@@ -240,26 +241,39 @@ __global__ void __launch_bounds__(ROW_NT) k_attn_rows(Attn A)
 
 // ---- how the work is shared out ----
 //
-// A unit is one kv head of one sequence and up to `rows` of its query rows;
-// its work is its tiles of `keys` entries (one at least).  All units' tiles lie
-// in one line, of which every block takes an equal, contiguous piece, whatever
-// the lengths: a piece covers whole units and at most two in part (the first
-// and the last).  Whole ones are written at once, parts go to the block's two
-// slots of scratch and are joined by k_attn_join.
+// A unit is one kv head of one sequence and up to `rows` of its query rows; its
+// work is its tiles of `keys` entries (one at least), each weighing as many as
+// the 128-row blocks that the unit fills.  All units lie in one line, of which
+// every block takes an equal, contiguous piece, whatever the lengths: a piece
+// covers whole units and at most two in part (the first and the last).  Whole
+// ones are written at once, parts go to the block's two slots of scratch and are
+// joined by k_attn_join.
 struct Share {
     int keys, rows, groups;    // entries of a tile; query rows of a unit; units of a kv head
+    int heavy, last;           // weight of a tile: of a kv head's units but the last, of the last
     float *scratch;
+
+    __host__ __device__ int per_head() const { return heavy * (groups - 1) + last; }
+    // Blocks that get a piece: none of them shorter than a tile.
+    __device__ int64_t blocks(int64_t total, int64_t grid) const
+    {
+        const int64_t most = total / (heavy > last ? heavy : last);
+        return most < grid ? most : grid;
+    }
 };
 
 struct Line {
-    int64_t total, at;         // tiles of all; tiles before sequence b
+    int64_t total, at;         // weight of all; weight before sequence b
 };
 
 __device__ __forceinline__ int tiles_of(const Share &S, const Seq &s)
 {
     return s.kv <= S.keys ? 1 : (int)((uint32_t)(s.kv + S.keys - 1) / (uint32_t)S.keys);
 }
-__device__ __forceinline__ int64_t tiles_of(const Attn &A, const Share &S, int64_t b) { return tiles_of(S, sequence(A, b)); }
+__device__ __forceinline__ int64_t weight_of(const Attn &A, const Share &S, int64_t b)
+{
+    return (int64_t)tiles_of(S, sequence(A, b)) * A.a.kv_heads * S.per_head();
+}
 
 // Sum of `v` over the block (every thread gets it); `red` holds a word per warp.
 template <int NT>
@@ -275,19 +289,18 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red)
     return v;
 }
 
-// Tiles before sequence `b`, and of all.
+// Weight before sequence `b`, and of all.
 template <int NT>
 __device__ Line line_at(const Attn &A, const Share &S, int64_t b, int64_t *red)
 {
-    const int64_t per = (int64_t)A.a.kv_heads * S.groups;
     Line L{0, 0};
     if (A.a.batch == 1) {
-        L.total = tiles_of(A, S, 0) * per;
+        L.total = weight_of(A, S, 0);
         return L;
     }
     int64_t all = 0, before = 0;
     for (int64_t i = threadIdx.x; i < A.a.batch; i += NT) {
-        const int64_t n = tiles_of(A, S, i) * per;
+        const int64_t n = weight_of(A, S, i);
         all += n;
         if (i < b) before += n;
     }
@@ -296,17 +309,16 @@ __device__ Line line_at(const Attn &A, const Share &S, int64_t b, int64_t *red)
     return L;
 }
 
-// The sequence that holds tile x, and the tiles before it.
+// The sequence that holds position x of the line, and the weight before it.
 template <int NT>
 __device__ int64_t sequence_of(const Attn &A, const Share &S, int64_t x, int64_t &at, int64_t *red)
 {
-    const int64_t per = (int64_t)A.a.kv_heads * S.groups;
     at = 0;
     if (A.a.batch == 1) return 0;
     __shared__ int64_t hit, hit_at;
     for (int64_t base = 0; base < A.a.batch; base += NT) {
         const int64_t i = base + threadIdx.x;
-        const int64_t n = i < A.a.batch ? tiles_of(A, S, i) * per : 0;
+        const int64_t n = i < A.a.batch ? weight_of(A, S, i) : 0;
         int64_t inc = n;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -337,7 +349,7 @@ __device__ int64_t sequence_of(const Attn &A, const Share &S, int64_t x, int64_t
 }
 
 __device__ __forceinline__ int64_t piece(int64_t total, int64_t c, int64_t blocks) { return c * total / blocks; }
-// The block whose piece holds tile x.
+// The block whose piece holds position x.
 __device__ __forceinline__ int64_t block_of(int64_t total, int64_t x, int64_t blocks) { return ((x + 1) * blocks - 1) / total; }
 
 // A slot of scratch: rows x head_dim sums, the rows' maxima and sums, and the
@@ -346,6 +358,68 @@ __host__ __device__ __forceinline__ int64_t slot_floats(int rows, int head_dim) 
 __device__ __forceinline__ float *slot_of(const Attn &A, const Share &S, int64_t block, int slot)
 {
     return S.scratch + (block * 2 + slot) * slot_floats(S.rows, A.a.head_dim);
+}
+
+// A piece's part of one unit.
+struct Segment {
+    Seq s;
+    int64_t b;
+    int hk, group;             // kv head, group of its rows
+    int j0, j1;                // entries
+    int tiles;                 // 0: the piece ends within the unit's next tile, which the following block has
+    bool whole;                // the unit's only part
+    int slot;                  // of scratch, if not
+};
+
+// Walks a block's piece.
+struct Walk {
+    int64_t x, end, at, b, first;
+    __device__ __forceinline__ bool next(const Attn &A, const Share &S, Segment &g)
+    {
+        while (x < end) {
+            g.s = sequence(A, b);
+            const int n = tiles_of(S, g.s), per = S.per_head();
+            const uint64_t in = (uint64_t)(x - at), head = (uint64_t)n * (uint32_t)per;
+            g.b = b;
+            // (32-bit divisions where they do)
+            g.hk = (in | head) >> 32 ? (int)(in / head) : (int)((uint32_t)in / (uint32_t)head);
+            const int64_t rest = (int64_t)(in - g.hk * head), big = (int64_t)n * S.heavy;
+            g.group = S.groups == 1 ? 0 : (rest >> 31) ? (int)(rest / big) : (int)((uint32_t)rest / (uint32_t)big);
+            if (g.group > S.groups - 1) g.group = S.groups - 1;
+            const int w = g.group == S.groups - 1 ? S.last : S.heavy;
+            const int64_t u0 = x - rest + g.group * big, u1 = u0 + (int64_t)n * w;      // the unit in the line
+            const int64_t e = end < u1 ? end : u1;
+            const int t0 = (int)((x - u0 + w - 1) / w), t1 = (int)((e - u0 + w - 1) / w);
+            g.tiles = t1 - t0;
+            g.whole = g.tiles == n;
+            g.slot = first >= u0 ? 0 : 1;
+            g.j0 = t0 * S.keys;
+            g.j1 = (int64_t)t1 * S.keys < g.s.kv ? t1 * S.keys : g.s.kv;
+            x = e;
+            if (x - at == (int64_t)head * A.a.kv_heads) {
+                at = x;
+                ++b;
+            }
+            if (g.tiles > 0) return true;
+        }
+        return false;
+    }
+};
+
+template <int NT>
+__device__ __forceinline__ Walk start(const Attn &A, const Share &S, int64_t *red)
+{
+    Walk w;
+    const int64_t total = line_at<NT>(A, S, 0, red).total;
+    const int64_t blocks = S.blocks(total, gridDim.x);
+    if (blockIdx.x >= blocks) {
+        w.x = w.end = 0;
+        return w;
+    }
+    w.x = w.first = piece(total, blockIdx.x, blocks);
+    w.end = piece(total, blockIdx.x + 1, blocks);
+    w.b = sequence_of<NT>(A, S, w.x, w.at, red);
+    return w;
 }
 
 constexpr int JOIN_NT = 128;
@@ -362,16 +436,20 @@ __global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t per = (uint32_t)a.kv_heads * S.groups;
     const uint32_t b = blockIdx.x / per, u = blockIdx.x % per;
+    const int hk = (int)(u / S.groups), group = (int)(u % S.groups), w = group == S.groups - 1 ? S.last : S.heavy;
     const Line L = line_at<JOIN_NT>(A, S, b, red);
     const Seq s = sequence(A, b);
     const int n = tiles_of(S, s);
-    const int64_t x0 = L.at + (int64_t)u * n;
-    const int64_t blocks = L.total < grid ? L.total : grid;
-    const int64_t c0 = block_of(L.total, x0, blocks), c1 = block_of(L.total, x0 + n - 1, blocks);
+    const int64_t x0 = L.at + (int64_t)n * ((int64_t)hk * S.per_head() + group * S.heavy), x1 = x0 + (int64_t)n * w;
+    const int64_t blocks = S.blocks(L.total, grid);
+    const int64_t c0 = block_of(L.total, x0, blocks);
+    int64_t c1 = block_of(L.total, x1 - 1, blocks);
+    // the last block has no tile if its piece begins within the last one
+    while (c1 > c0 && (piece(L.total, c1, blocks) - x0 + w - 1) / w >= n) --c1;
     if (c0 == c1) return;
-    const int hk = (int)(u / S.groups), r = blockIdx.y * (JOIN_NT / 32) + warp;
+    const int r = blockIdx.y * (JOIN_NT / 32) + warp;
     if (r >= S.rows) return;
-    const Row row = row_of(A, hk, (int64_t)(u % S.groups) * S.rows + r);
+    const Row row = row_of(A, hk, (int64_t)group * S.rows + r);
     if (!row.inside) return;
     float top = -INFINITY, sum = 0.f, o[8] = {};
     if (row.t < s.tree) {
@@ -481,22 +559,14 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
     unsigned char *mine = ring + warp * (FEW_STAGES * 2 * HALF);
     const uint32_t base = smem_addr(mine);
     const int chunks = a.head_dim / 8;
-    const int64_t per = (int64_t)a.kv_heads * S.groups;
-    const int64_t total = line_at<FEW_NT>(A, S, 0, red).total;
-    const int64_t blocks = total < gridDim.x ? total : gridDim.x;      // no empty pieces
-    if (blockIdx.x < blocks) {
-        int64_t x = piece(total, blockIdx.x, blocks);
-        const int64_t end = piece(total, blockIdx.x + 1, blocks);
-        int64_t at, b = sequence_of<FEW_NT>(A, S, x, at, red);
-        bool first_piece = true;
-        while (x < end) {
-            const Seq s = sequence(A, b);
-            const int n = tiles_of(S, s);
-            const int64_t u = (x - at) / n;
-            const int t0 = (int)(x - at - u * n), count = n - t0 < end - x ? n - t0 : (int)(end - x);
-            const int hk = (int)((uint32_t)u / (uint32_t)S.groups);
-            const int64_t R0 = (int64_t)((uint32_t)u % (uint32_t)S.groups) * FEW_ROWS;
-            const int j0 = t0 * FEW_KEYS, j1 = (int64_t)(t0 + count) * FEW_KEYS < s.kv ? (t0 + count) * FEW_KEYS : s.kv;
+    Walk walk = start<FEW_NT>(A, S, red);
+    Segment seg;
+    {
+        while (walk.next(A, S, seg)) {
+            const Seq &s = seg.s;
+            const int64_t b = seg.b;
+            const int hk = seg.hk, j0 = seg.j0, j1 = seg.j1;
+            const int64_t R0 = (int64_t)seg.group * FEW_ROWS;
             const int steps = j1 > j0 + warp * FEW_STEP ? (j1 - j0 - warp * FEW_STEP + FEW_KEYS - 1) / FEW_KEYS : 0;
 
             // stage `i` of this warp: lane l < 16 finds entry l, all lanes copy
@@ -657,9 +727,9 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
                 s_l[warp][g + 8] = lb;
             }
             __syncthreads();
-            const bool whole = count == n;
+            const bool whole = seg.whole;
             odd = (s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3]) != 0;
-            float *part = slot_of(A, S, blockIdx.x, first_piece ? 0 : 1);
+            float *part = slot_of(A, S, blockIdx.x, seg.slot);
             for (int r = warp; r < FEW_ROWS; r += FEW_W) {
                 const Row row = row_of(A, hk, R0 + r);
                 if (!row.inside) break;
@@ -698,13 +768,496 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
                 }
             }
             __syncthreads();       // the rings are free again
-            first_piece = false;
-            x += count;
-            if (x - at == n * per) {
-                at = x;
-                ++b;
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ---- many rows: tcgen05 ----
+//
+// 128 query rows against tiles of entries on the fifth-generation tensor cores:
+// S = Q K^T and O += P V with both accumulators in tensor memory (a row per
+// lane), Q, K and V in shared memory in the 128-byte swizzle (K row by row, V
+// as it lies, its entries as the contraction's dimension), and P, rounded to
+// the caches' type, written over S for the second product.  Warps have roles:
+// four fetch K and V (16-byte asynchronous copies, since pages may be of any
+// size), one issues the matrix instructions, and four for each 128 rows do the
+// softmax, a thread a row.  With two row tiles (TILES = 2) a tile of K and V
+// serves both, and the products of one run under the softmax of the other; with
+// one, the scores of the next tile of entries do.
+//
+// Every wait has a limit; a block whose wait runs out stops and leaves NaN in
+// its rows.
+
+template <int DP, int TILES> struct Many {
+    static constexpr int KEYS = DP == 256 ? 64 : 128;
+    static constexpr int STAGES = TILES == 1 && DP != 256 ? 3 : 2;        // of K, and of V
+    static constexpr int SB = TILES == 1 ? 2 : 1;                         // score buffers of a row tile
+    static constexpr int SUBQ = 128 * 128, SUBK = KEYS * 128;             // 64 columns of a tile, in bytes
+    static constexpr int Q = DP / 64 * SUBQ, KV = DP / 64 * SUBK;
+    static constexpr int NT = 32 * (4 * TILES + 4 + 1);
+    static constexpr int FETCH = 4 * TILES, ISSUE = FETCH + 4;            // first warps of the roles
+    static constexpr int S_COL = 0, O_COL = TILES * SB * KEYS;
+    static constexpr int SMEM = TILES * Q + STAGES * 2 * KV + 1024;
+};
+static_assert(Many<128, 2>::O_COL + 2 * 128 <= 512 && Many<256, 1>::O_COL + 256 <= 512, "tensor memory");
+
+constexpr unsigned long long WAIT_NS = 2000000000ull;
+
+__device__ __forceinline__ void bar_init(uint32_t bar, int count) { asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory"); }
+__device__ __forceinline__ void bar_arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(bar) : "memory"); }
+// Waits for the phase of that parity to end; false when the limit ran out, here or in another warp.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *stop)
+{
+    unsigned long long began = 0;
+    for (int i = 0;; ++i) {
+        uint32_t done;
+        asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done) return true;
+        if ((i & 31) != 31) continue;
+        if (*stop) return false;
+        unsigned long long now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (began == 0) began = now;
+        else if (now - began > WAIT_NS) break;
+    }
+    *stop = 1;
+    return false;
+}
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t more)
+{
+    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(more) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t more)
+{
+    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(more) : "memory");
+}
+// (the wait belongs to the load: nothing may use the registers before it)
+__device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t a)
+{
+    uint32_t r[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+                 "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                   "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+                   "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+                   "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(a) : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+                 "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t a, const float (&v)[32])
+{
+    uint32_t lo[16], hi[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        lo[i] = __float_as_uint(v[i]);
+        hi[i] = __float_as_uint(v[16 + i]);
+    }
+    tc_st16(a, lo);
+    tc_st16(a + 16, hi);
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float pow2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Shared-memory descriptor of a 128-byte-swizzled tile: `lead` bytes between
+// 64-column parts (used where the columns are not the contraction's
+// dimension), 1024 between groups of eight rows.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead)
+{
+    return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)((lead >> 4) & 0x3fffu) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+template <class T, int DP, int TILES>
+__global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Share S)
+{
+    using M = Many<DP, TILES>;
+    constexpr int KEYS = M::KEYS, ST = M::STAGES, SB = M::SB, CH = DP / 8;
+    const dbs_attention_args &a = A.a;
+    extern __shared__ unsigned char raw[];
+    __shared__ int64_t red[M::NT / 32];
+    __shared__ __align__(8) uint64_t bars[4 * ST + TILES * (SB + 3) + 1];
+    __shared__ uint32_t tmem_at;
+    __shared__ int stop;
+    __shared__ int odd_seg[8];                       // segments (their number + 1) whose V is not finite somewhere
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t sq = base, sk = base + TILES * M::Q, sv = sk + ST * M::KV;
+    const uint32_t bar0 = smem_addr(bars);
+    const uint32_t k_full = bar0, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST;
+    const uint32_t s_full = v_empty + 8 * ST, q_full = s_full + 8 * TILES * SB, p_ready = q_full + 8 * TILES, o_done = p_ready + 8 * TILES;
+    const uint32_t last_bar = o_done + 8 * TILES;
+    Walk walk = start<M::NT>(A, S, red);
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            bar_init(k_full + 8 * i, 128);
+            bar_init(k_empty + 8 * i, 1);
+            bar_init(v_full + 8 * i, 128);
+            bar_init(v_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < TILES * SB; ++i) bar_init(s_full + 8 * i, 1);
+        for (int i = 0; i < TILES; ++i) {
+            bar_init(q_full + 8 * i, 128);
+            bar_init(p_ready + 8 * i, 128);
+            bar_init(o_done + 8 * i, 1);
+        }
+        bar_init(last_bar, 1);
+        stop = 0;
+        for (int i = 0; i < 8; ++i) odd_seg[i] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == M::ISSUE) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_at)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = tmem_at;
+    // row tiles in use of a unit
+    const int G = a.q_heads / a.kv_heads;
+    const int64_t all_rows = a.tokens * G;
+    auto tiles_in = [&](const Segment &g) {
+        const int64_t left = all_rows - (int64_t)g.group * (128 * TILES);
+        return TILES == 1 || left <= 128 ? 1 : 2;
+    };
+    Segment seg;
+
+    if (warp >= M::FETCH && warp < M::ISSUE) {
+        // ---- fetch K and V ----
+        // each warp has a quarter of a tile's entries: a lane finds one, all copy
+        constexpr int RW = KEYS / 4, RS = 32 / CH;                         // entries of a warp; of one copy of all lanes
+        const int w0 = (warp - M::FETCH) * RW, chunks = a.head_dim / 8, c = lane % CH, r0 = w0 + lane / CH;
+        const uint32_t sub = (c >> 3) * M::SUBK;
+        int n = 0, number = 0;                                             // tiles fetched; segments
+        bool ok = true;
+        // what has been issued but not yet announced: K and V of tiles done .. n
+        int announced = 0;                                                 // groups (2 a tile) announced
+        struct Mark { int first, j0, number; };
+        Mark marks[ST + 1] = {};                                              // of the last tiles, by tile % (ST + 1)
+        auto announce = [&]() {
+            const int tile = announced >> 1, st = tile % ST;
+            if (announced & 1) {
+                Mark m = marks[0];
+#pragma unroll
+                for (int i = 1; i <= ST; ++i)
+                    if (tile % (ST + 1) == i) m = marks[i];
+                if (m.j0 + KEYS > m.first) {
+                    bool found = false;
+#pragma unroll 4
+                    for (int i = 0; i < RW / RS; ++i) {
+                        const int row = r0 + i * RS;
+                        const uint32_t at = sv + st * M::KV + sub + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                        uint4 x;
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+                        const bool any = (int)clear_odd<T>(x.x) | (int)clear_odd<T>(x.y) | (int)clear_odd<T>(x.z) | (int)clear_odd<T>(x.w);
+                        if (any && m.j0 + row >= m.first) {
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+                            found = true;
+                        }
+                    }
+                    if (found) *(volatile int *)&odd_seg[m.number & 7] = m.number + 1;
+                }
+            }
+            async_fence();
+            bar_arrive((announced & 1 ? v_full : k_full) + 8 * st);
+            ++announced;
+        };
+        constexpr int LAG = 2 * (ST - 1);                                  // groups in flight behind the newest
+        while (ok && walk.next(A, S, seg)) {
+            const T *k = (const T *)a.k + seg.hk * a.k_head + c * 8, *v = (const T *)a.v + seg.hk * a.v_head + c * 8;
+            for (int t = 0; t < seg.tiles && ok; ++t, ++n) {
+                const int j0 = seg.j0 + t * KEYS, st = n % ST;
+                const uint32_t parity = (n / ST + 1) & 1;                  // of the stage's release; the first round finds it free
+                const int j = j0 + w0 + (lane & (RW - 1));
+                const Place at = place_of(a, seg.b, j < seg.j1 ? j : 0);
+                const unsigned in = __ballot_sync(~0u, j < seg.j1);
+                const int64_t off_k = at.page * a.k_page + at.in * a.k_entry, off_v = at.page * a.v_page + at.in * a.v_entry;
+#pragma unroll
+                for (int i = 0; i <= ST; ++i)
+                    if (n % (ST + 1) == i) marks[i] = {seg.s.first, j0, number};
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (ok) ok = __all_sync(~0u, bar_wait((kv ? v_empty : k_empty) + 8 * st, parity, &stop));
+                    if (ok) {
+                        const uint32_t to = (kv ? sv : sk) + st * M::KV + sub;
+#pragma unroll
+                        for (int i = 0; i < RW / RS; ++i) {
+                            const int rw = i * RS + lane / CH, row = w0 + rw;
+                            const int64_t off = __shfl_sync(~0u, kv ? off_v : off_k, rw);
+                            const bool take = (in >> rw & 1u) && c < chunks;
+                            cp16(to + row * 128 + (((c & 7) ^ (row & 7)) << 4), take ? (const void *)((kv ? v : k) + off) : (const void *)a.k, take);
+                        }
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (ok && 2 * n + kv >= LAG) {
+                        asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
+                        announce();
+                    }
+                }
+            }
+            ++number;
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (ok)
+            while (announced < 2 * n) announce();
+    } else if (warp == M::ISSUE) {
+        // ---- issue the products ----
+        constexpr uint32_t FMT = __is_same(T, __nv_bfloat16) ? 1u : 0u;
+        constexpr uint32_t DESC = 1u << 4 | FMT << 7 | FMT << 10 | (128u >> 4) << 24;
+        constexpr uint32_t DESC_S = DESC | (uint32_t)(KEYS >> 3) << 17, DESC_O = DESC | 1u << 16 | (uint32_t)(DP >> 3) << 17;
+        int n0 = 0, it[TILES] = {}, units[TILES] = {};                     // first tile; of a row tile: score tiles, segments
+        bool ok = true;
+        while (ok && walk.next(A, S, seg)) {
+            const int used = tiles_in(seg);
+            // scores of row tile r against tile t of the segment
+            auto scores = [&](int r, int t) {
+                const int st = (n0 + t) % ST;
+                if (r == 0 && ok) ok = __all_sync(~0u, bar_wait(k_full + 8 * st, (n0 + t) / ST & 1, &stop));
+                if (!ok) return;
+                tc_after();
+                if (lane == 0) {
+                    const uint32_t d = tmem + M::S_COL + (r * SB + (SB == 2 ? it[r] & 1 : 0)) * KEYS;
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) {
+                        const uint32_t in = (k & 3) * 32;
+                        tc_mma_ss(d, tile_desc(sq + r * M::Q + (k >> 2) * M::SUBQ + in, 16), tile_desc(sk + st * M::KV + (k >> 2) * M::SUBK + in, 16),
+                                  DESC_S, k > 0);
+                    }
+                    tc_commit(s_full + 8 * (r * SB + (SB == 2 ? it[r] & 1 : 0)));
+                    if (r == used - 1) tc_commit(k_empty + 8 * st);
+                }
+                ++it[r];
+                __syncwarp();
+            };
+            auto outputs = [&](int r, int t) {
+                const int st = (n0 + t) % ST, done = SB == 2 ? it[r] - (t + 1 < seg.tiles ? 2 : 1) : it[r] - 1;   // this tile's number
+                if (r == 0 && ok) ok = __all_sync(~0u, bar_wait(v_full + 8 * st, (n0 + t) / ST & 1, &stop));
+                if (ok) ok = __all_sync(~0u, bar_wait(p_ready + 8 * r, done & 1, &stop));
+                if (!ok) return;
+                tc_after();
+                if (lane == 0) {
+                    const uint32_t d = tmem + M::O_COL + r * DP, pa = tmem + M::S_COL + (r * SB + (SB == 2 ? done & 1 : 0)) * KEYS;
+#pragma unroll
+                    for (int k = 0; k < KEYS / 16; ++k)
+                        tc_mma_ts(d, pa + 8 * k, tile_desc(sv + st * M::KV + k * 2048, M::SUBK), DESC_O, t > 0 || k > 0);
+                    tc_commit(o_done + 8 * r);
+                    if (r == used - 1) tc_commit(v_empty + 8 * st);
+                }
+                __syncwarp();
+            };
+#pragma unroll
+            for (int r = 0; r < TILES; ++r)
+                if (r < used && ok) {
+                    ok = __all_sync(~0u, bar_wait(q_full + 8 * r, units[r]++ & 1, &stop));
+                    if (ok) scores(r, 0);
+                }
+            for (int t = 0; t < seg.tiles && ok; ++t) {
+                if (SB == 2 && t + 1 < seg.tiles) scores(0, t + 1);
+#pragma unroll
+                for (int r = 0; r < TILES; ++r)
+                    if (r < used && ok) {
+                        outputs(r, t);
+                        if (SB == 1 && ok && t + 1 < seg.tiles) scores(r, t + 1);
+                    }
+            }
+            n0 += seg.tiles;
+        }
+        if (!ok) {
+            // products under way end before their memory is given back
+            if (lane == 0) tc_commit(last_bar);
+            __syncwarp();
+            int ignored = 0;
+            bar_wait(last_bar, 0, &ignored);
+        }
+    } else {
+        // ---- softmax: a thread has a row ----
+        const int r = warp >> 2, row = (warp & 3) * 32 + lane;             // row tile, row in it
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+        const uint32_t o_at = tmem + lanes + M::O_COL + r * DP;
+        int it = 0, number = 0;                                            // tiles done; segments
+        bool ok = true;
+        while (ok && walk.next(A, S, seg)) {
+            const int number_now = number++;
+            if (r >= tiles_in(seg)) continue;                              // the unit has one row tile: the other's barriers rest
+            const int64_t b = seg.b;
+            const Seq s = seg.s;
+            const Row me = row_of(A, seg.hk, (int64_t)seg.group * (128 * TILES) + r * 128 + row);
+            const bool busy = __any_sync(~0u, me.inside);
+            {
+                // this row of Q
+                const T *q = (const T *)a.q + b * a.q_batch + me.t * a.q_token + me.h * a.q_head;
+#pragma unroll 8
+                for (int c = 0; c < CH; ++c) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (me.inside && 8 * c < a.head_dim) x = *(const uint4 *)(q + 8 * c);
+                    const uint32_t at = sq + r * M::Q + (c >> 3) * M::SUBQ + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+                }
+                async_fence();
+                bar_arrive(q_full + 8 * r);
+            }
+            float m = -INFINITY, l = 0.f;
+            for (int t = 0; t < seg.tiles; ++t, ++it) {
+                const int buf = SB == 2 ? it & 1 : 0;
+                ok = __all_sync(~0u, bar_wait(s_full + 8 * (r * SB + buf), (SB == 2 ? it >> 1 : it) & 1, &stop));
+                if (!ok) break;
+                tc_after();
+                const uint32_t s_at = tmem + lanes + M::S_COL + (r * SB + buf) * KEYS;
+                const int j0 = seg.j0 + t * KEYS;
+                const bool masked = j0 + KEYS > s.first;
+                bool settled = t == 0;                                     // the product before this one is known to be in O
+                if (busy) {
+                    uint32_t see[KEYS / 32];
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < KEYS / 32; ++c) {
+                        float v[32];
+                        tc_ld32(v, s_at + 32 * c);
+                        see[c] = masked ? sees32(A, b, me.t, s.tree, j0 + 32 * c - s.first) : ~0u;
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) top = fmaxf(top, see[c] >> e & 1u ? v[e] * A.scale_log2 : -INFINITY);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e] * A.scale_log2);
+                        }
+                    }
+                    // replace the maximum only when it grew by more than 2^8
+                    const bool grew = top > m + 8.f || (m == -INFINITY && top > m);
+                    if (__any_sync(~0u, grew)) {
+                        const float f = grew ? (m == -INFINITY ? 0.f : exp2f(m - top)) : 1.f;
+                        if (grew) m = top;
+                        l *= f;
+                        if (t > 0) {
+                            // the output so far, once the product before this one is in it
+                            ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
+                            if (!ok) break;
+                            settled = true;
+                            tc_after();
+#pragma unroll 1
+                            for (int c = 0; c < DP / 32; ++c) {
+                                float v[32];
+                                tc_ld32(v, o_at + 32 * c);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] *= f;
+                                tc_st32(o_at + 32 * c, v);
+                            }
+                            tc_wait_st();
+                        }
+                    }
+                    const float shift = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                    for (int c = 0; c < KEYS / 32; ++c) {
+                        float v[32];
+                        tc_ld32(v, s_at + 32 * c);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            v[e] = pow2(fmaf(v[e], A.scale_log2, -shift));
+                            if (masked) v[e] = see[c] >> e & 1u ? v[e] : 0.f;
+                            l += v[e];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = pack2<T>(v[2 * e], v[2 * e + 1]);
+                        tc_st16(s_at + 16 * c, w);
+                    }
+                    tc_wait_st();
+                }
+                // (every phase of o_done is waited for while the next cannot end)
+                if (!settled) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
+                if (!ok) break;
+                tc_before();
+                bar_arrive(p_ready + 8 * r);
+            }
+            // the unit's (or the part's) output
+            if (ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
+            tc_after();
+            const bool odd = ok && *(volatile int *)&odd_seg[number_now & 7] == number_now + 1;
+            if (!busy) continue;
+            float *part = slot_of(A, S, blockIdx.x, seg.slot);
+            const int slot_row = r * 128 + row;
+            const bool none = me.t >= s.tree || l == 0.f;
+            const float fine = ok ? 1.f : nanf("");
+            const float by = seg.whole ? (none ? 0.f : 1.f / l) * fine : fine;
+            T *out = (T *)a.out + b * a.o_batch + me.t * a.o_token + me.h * a.o_head;
+#pragma unroll 1
+            for (int c = 0; c < DP / 32; ++c) {
+                float v[32];
+                tc_ld32(v, o_at + 32 * c);
+                if (!me.inside) continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = seg.whole && none && ok ? 0.f : v[e] * by;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    const int d = 32 * c + e;
+                    if (d >= a.head_dim) break;
+                    if (!seg.whole) {
+                        float4 *to = (float4 *)(part + (int64_t)slot_row * a.head_dim + d);
+                        to[0] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        to[1] = make_float4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+                    } else if (A.wide_out) {
+                        *(uint4 *)(out + d) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]), pack2<T>(v[e + 4], v[e + 5]),
+                                                         pack2<T>(v[e + 6], v[e + 7]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) out[d + k] = from_f32<T>(v[e + k]);
+                    }
+                }
+            }
+            tc_before();
+            if (me.inside) {
+                if (!seg.whole) {
+                    float *st = part + (int64_t)S.rows * a.head_dim;
+                    st[slot_row] = m;
+                    st[S.rows + slot_row] = l * fine;
+                    if (slot_row == 0) st[2 * S.rows] = odd;
+                } else if (a.lse) {
+                    a.lse[(b * a.tokens + me.t) * a.q_heads + me.h] = none ? -INFINITY : (m + log2f(l * fine)) * 0.6931471805599453f;
+                }
+            }
+            if (odd && seg.whole) {
+                __syncwarp();
+                for (int i = 0; i < 32; ++i) {
+                    const Row other = row_of(A, seg.hk, (int64_t)seg.group * (128 * TILES) + r * 128 + (warp & 3) * 32 + i);
+                    if (!other.inside || other.t >= s.tree) continue;
+                    T *o = (T *)a.out + b * a.o_batch + other.t * a.o_token + other.h * a.o_head;
+                    Eight w;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w.v[e] = lane + 32 * e < a.head_dim ? to_f32(o[lane + 32 * e]) : 0.f;
+                    w = add_odd<T>(A, b, other.t, seg.hk, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (lane + 32 * e < a.head_dim) o[lane + 32 * e] = from_f32<T>(w.v[e]);
+                }
             }
         }
+    }
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    if (warp == M::ISSUE) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -713,7 +1266,7 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
 
 // How a call runs: the kernel, its grid and its scratch.
 struct Plan {
-    bool rows;                 // any alignment
+    bool rows, many;           // any alignment; 128 rows at a time
     int dp, blocks;
     Share share;
     int64_t scratch;
@@ -724,7 +1277,7 @@ bool aligned8(int64_t v) { return (v & 7) == 0; }
 dbs_status plan_of(const dbs_attention_args &a, Plan &P)
 {
     P = Plan{};
-    const int64_t entries = a.max_pages * a.page_size;
+    const int64_t entries = a.max_pages * a.page_size, rows = a.tokens * (a.q_heads / a.kv_heads);
     // 16-byte copies of heads: every head starts on such a boundary
     P.rows = a.head_dim % 8 || !aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned8(a.q_batch) ||
              !aligned8(a.q_token) || !aligned8(a.q_head) || !aligned8(a.k_page) || !aligned8(a.k_entry) ||
@@ -736,13 +1289,27 @@ dbs_status plan_of(const dbs_attention_args &a, Plan &P)
         return DBS_ERR_CUDA;
     }
     P.dp = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256;
-    P.share.keys = FEW_KEYS;
-    P.share.rows = FEW_ROWS;
-    P.share.groups = (int)((a.tokens * (a.q_heads / a.kv_heads) + FEW_ROWS - 1) / FEW_ROWS);
-    const int per_sm = P.dp == 64 ? 4 : P.dp == 128 ? 2 : 1;
-    const int64_t most = a.batch * a.kv_heads * P.share.groups * (entries < FEW_KEYS ? 1 : (entries + FEW_KEYS - 1) / FEW_KEYS);
+    // up to 16 rows of a kv head fit one instruction of k_attn_few, which reads
+    // the cache once for each 16
+    P.many = rows > FEW_ROWS;
+    Share &S = P.share;
+    int per_sm = P.dp == 64 ? 4 : P.dp == 128 ? 2 : 1;
+    if (P.many) {
+        const int tiles = P.dp == 256 || rows <= 128 ? 1 : 2;
+        S.keys = P.dp == 256 ? 64 : 128;
+        S.rows = 128 * tiles;
+        S.heavy = tiles;
+        per_sm = 1;
+    } else {
+        S.keys = FEW_KEYS;
+        S.rows = FEW_ROWS;
+        S.heavy = 1;
+    }
+    S.groups = (int)((rows + S.rows - 1) / S.rows);
+    S.last = P.many ? (int)((rows - (int64_t)(S.groups - 1) * S.rows + 127) / 128) : 1;
+    const int64_t most = a.batch * a.kv_heads * S.groups * (entries < S.keys ? 1 : (entries + S.keys - 1) / S.keys);
     P.blocks = (int)(most < sms * per_sm ? most : sms * per_sm);
-    P.scratch = (int64_t)P.blocks * 2 * slot_floats(FEW_ROWS, a.head_dim) * 4;
+    P.scratch = (int64_t)P.blocks * 2 * slot_floats(S.rows, a.head_dim) * 4;
     return DBS_OK;
 }
 
@@ -774,6 +1341,19 @@ dbs_status launch_few(const Attn &A, const Plan &P, cudaStream_t s)
     return st == DBS_OK ? launch_join<T>(A, P, s) : st;
 }
 
+template <class T, int DP, int TILES>
+dbs_status launch_many(const Attn &A, const Plan &P, cudaStream_t s)
+{
+    using M = Many<DP, TILES>;
+    if (cudaFuncSetAttribute(k_attn_many<T, DP, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::SMEM) != cudaSuccess) {
+        cudaGetLastError();
+        return DBS_ERR_CUDA;
+    }
+    k_attn_many<T, DP, TILES><<<P.blocks, M::NT, M::SMEM, s>>>(A, P.share);
+    const dbs_status st = launched();
+    return st == DBS_OK ? launch_join<T>(A, P, s) : st;
+}
+
 template <class T>
 dbs_status launch(const Attn &A, const Plan &P, cudaStream_t s)
 {
@@ -781,6 +1361,11 @@ dbs_status launch(const Attn &A, const Plan &P, cudaStream_t s)
         const int64_t rows = A.a.batch * A.a.tokens * A.a.q_heads;
         k_attn_rows<T><<<(unsigned)(rows < (1 << 30) ? rows : (1 << 30)), ROW_NT, 0, s>>>(A);
         return launched();
+    }
+    if (P.many) {
+        if (P.dp == 256) return launch_many<T, 256, 1>(A, P, s);
+        if (P.share.heavy == 1) return P.dp == 64 ? launch_many<T, 64, 1>(A, P, s) : launch_many<T, 128, 1>(A, P, s);
+        return P.dp == 64 ? launch_many<T, 64, 2>(A, P, s) : launch_many<T, 128, 2>(A, P, s);
     }
     return P.dp == 64 ? launch_few<T, 64>(A, P, s) : P.dp == 128 ? launch_few<T, 128>(A, P, s) : launch_few<T, 256>(A, P, s);
 }
@@ -825,7 +1410,8 @@ dbs_status dbs_tree_attention(const dbs_attention_args *a, void *stream)
     const dbs_status st = plan_of(*a, P);
     if (st != DBS_OK) return st;
     if (P.scratch > 0 && (!a->scratch || !aligned16(a->scratch) || a->scratch_bytes < P.scratch)) return DBS_ERR_INVALID_ARG;
-    Attn A{*a, a->scale * 1.4426950408889634f, (int)((a->tokens + 63) / 64)};
+    const bool wide_out = aligned16(a->out) && aligned8(a->o_batch) && aligned8(a->o_token) && aligned8(a->o_head);
+    const Attn A{*a, a->scale * 1.4426950408889634f, (int)((a->tokens + 63) / 64), wide_out};
     P.share.scratch = (float *)a->scratch;
     return a->dtype == DBS_F16 ? launch<__half>(A, P, (cudaStream_t)stream) : launch<__nv_bfloat16>(A, P, (cudaStream_t)stream);
 }
