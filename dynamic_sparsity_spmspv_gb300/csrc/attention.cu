@@ -348,9 +348,14 @@ __device__ int64_t sequence_of(const Attn &A, const Share &S, int64_t x, int64_t
     return A.a.batch - 1;      // not reached: x < total
 }
 
-__device__ __forceinline__ int64_t piece(int64_t total, int64_t c, int64_t blocks) { return c * total / blocks; }
+// (32-bit divisions where they do)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+__device__ __forceinline__ int64_t piece(int64_t total, int64_t c, int64_t blocks) { return quotient(c * total, blocks); }
 // The block whose piece holds position x.
-__device__ __forceinline__ int64_t block_of(int64_t total, int64_t x, int64_t blocks) { return ((x + 1) * blocks - 1) / total; }
+__device__ __forceinline__ int64_t block_of(int64_t total, int64_t x, int64_t blocks) { return quotient((x + 1) * blocks - 1, total); }
 
 // A slot of scratch: rows x head_dim sums, the rows' maxima and sums, and the
 // mark of a V that is not finite.
@@ -422,16 +427,19 @@ __device__ __forceinline__ Walk start(const Attn &A, const Share &S, int64_t *re
     return w;
 }
 
-constexpr int JOIN_NT = 128;
+constexpr int JOIN_NT = 128, JOIN_W = JOIN_NT / 32;
 
-// Joins the parts of a unit that more than one block worked on; one warp per
-// row.  The parts' maxima and sums are read by the lanes at once, their outputs
-// in the order of the cache.
+// Joins the parts of a unit that more than one block worked on; a row by `split`
+// warps (all four of a block while there are few rows, else one).  A row's
+// warps read the parts' maxima and sums (a lane a part), each adds up its share
+// of the parts' outputs, several loads at a time, and the warps' sums are added
+// in order.  Bound by the latency of that chain.
 template <class T>
-__global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int grid)
+__global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int grid, int rows, int split)
 {
     const dbs_attention_args &a = A.a;
-    __shared__ int64_t red[JOIN_NT / 32];
+    __shared__ int64_t red[JOIN_W];
+    __shared__ float s_o[JOIN_W][256];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t per = (uint32_t)a.kv_heads * S.groups;
@@ -445,63 +453,82 @@ __global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int grid
     const int64_t c0 = block_of(L.total, x0, blocks);
     int64_t c1 = block_of(L.total, x1 - 1, blocks);
     // the last block has no tile if its piece begins within the last one
-    while (c1 > c0 && (piece(L.total, c1, blocks) - x0 + w - 1) / w >= n) --c1;
+    while (w > 1 && c1 > c0 && (piece(L.total, c1, blocks) - x0 + w - 1) / w >= n) --c1;
     if (c0 == c1) return;
-    const int r = blockIdx.y * (JOIN_NT / 32) + warp;
-    if (r >= S.rows) return;
-    const Row row = row_of(A, hk, (int64_t)group * S.rows + r);
-    if (!row.inside) return;
-    float top = -INFINITY, sum = 0.f, o[8] = {};
-    if (row.t < s.tree) {
-        const int parts = (int)(c1 - c0) + 1;
-        const int64_t size = slot_floats(S.rows, a.head_dim);
-        // the unit may be the second of its first block, and is the first of the others
-        const float *p0 = slot_of(A, S, c0, piece(L.total, c0, blocks) >= x0 ? 0 : 1), *rest = slot_of(A, S, c0, 0);
-        const int64_t stat = (int64_t)S.rows * a.head_dim;
-        for (int i = lane; i < parts; i += 32) top = fmaxf(top, (i ? rest + 2 * size * i : p0)[stat + r]);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    const int parts = (int)(c1 - c0) + 1, mine = warp % split;
+    const int64_t size = slot_floats(S.rows, a.head_dim), stat = (int64_t)S.rows * a.head_dim;
+    // the unit may be the second of its first block, and is the first of the others
+    const float *p0 = slot_of(A, S, c0, piece(L.total, c0, blocks) >= x0 ? 0 : 1), *rest = slot_of(A, S, c0, 0);
+    for (int r0 = blockIdx.y * (JOIN_W / split); r0 < rows; r0 += gridDim.y * (JOIN_W / split)) {
+        const int r = r0 + warp / split;
+        const Row row = row_of(A, hk, (int64_t)group * S.rows + r);
+        const bool here = r < rows && row.inside;
+        float top = -INFINITY, sum = 0.f, o[8] = {};
         bool odd = false;
-        for (int base = 0; base < parts; base += 32) {
-            float f = 0.f, l = 0.f;
-            if (base + lane < parts) {
-                const float *st = (base + lane ? rest + 2 * size * (base + lane) : p0) + stat;
-                const float m = st[r];
-                l = st[S.rows + r];
-                odd |= st[2 * S.rows] != 0.f;
-                f = m == -INFINITY ? 0.f : exp2f(m - top);
+        if (here && row.t < s.tree) {
+            for (int base = 0; base < parts; base += 32) {
+                float m = -INFINITY, l = 0.f;
+                if (base + lane < parts) {
+                    const float *st = (base + lane ? rest + 2 * size * (base + lane) : p0) + stat;
+                    m = st[r];
+                    l = st[S.rows + r];
+                    odd |= st[2 * S.rows] != 0.f;
+                }
+                float now = fmaxf(top, m);
+#pragma unroll
+                for (int d = 16; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(~0u, now, d));
+                const float keep = top == -INFINITY ? 0.f : exp2f(top - now);
+                top = now;
+                const float f = m == -INFINITY ? 0.f : exp2f(m - top);
                 l = l != l ? l : f * l;
-            }
-            const int now = parts - base < 32 ? parts - base : 32;
-            for (int i = 0; i < now; i += 4) {
-                float v[4][8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int c = base + (i + k < now ? i + k : i);
-                    const float *p = (c ? rest + 2 * size * c : p0) + (int64_t)r * a.head_dim;
+                for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+                sum = sum * keep + l;
+                const int now_parts = parts - base < 32 ? parts - base : 32;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[k][e] = lane + 32 * e < a.head_dim ? p[lane + 32 * e] : 0.f;
-                }
+                for (int e = 0; e < 8; ++e) o[e] *= keep;
+                for (int i = mine; i < now_parts; i += 4 * split) {
+                    float v[4][8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (i + k >= now) break;
-                    const float fi = __shfl_sync(~0u, f, i + k);
-                    sum += __shfl_sync(~0u, l, i + k);
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = base + (i + k * split < now_parts ? i + k * split : i);
+                        const float *p = (c ? rest + 2 * size * c : p0) + (int64_t)r * a.head_dim;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] += fi == 0.f ? 0.f : fi * v[k][e];
+                        for (int e = 0; e < 8; ++e) v[k][e] = lane + 32 * e < a.head_dim ? p[lane + 32 * e] : 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float fi = __shfl_sync(~0u, f, (i + k * split) & 31);
+                        if (i + k * split >= now_parts) break;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] += fi == 0.f ? 0.f : fi * v[k][e];
+                    }
                 }
             }
         }
+        if (split > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (lane + 32 * e < a.head_dim) s_o[warp][lane + 32 * e] = o[e];
+            __syncthreads();
+            if (mine == 0)
+                for (int k = 1; k < split; ++k)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (lane + 32 * e < a.head_dim) o[e] += s_o[warp + k][lane + 32 * e];
+        }
+        if (!here || mine != 0) continue;
         if (__any_sync(~0u, odd)) {
-            Eight w;
+            Eight q;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w.v[e] = o[e];
-            w = add_odd<T>(A, b, row.t, hk, w);
+            for (int e = 0; e < 8; ++e) q.v[e] = o[e];
+            q = add_odd<T>(A, b, row.t, hk, q);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = w.v[e];
+            for (int e = 0; e < 8; ++e) o[e] = q.v[e];
         }
+        store_row<T>(A, b, row.t, row.h, top, sum, o);
     }
-    store_row<T>(A, b, row.t, row.h, top, sum, o);
 }
 
 // ---- few rows: every warp streams its own entries ----
@@ -781,7 +808,7 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
 // as it lies, its entries as the contraction's dimension), and P, rounded to
 // the caches' type, written over S for the second product.  Warps have roles:
 // four fetch K and V (16-byte asynchronous copies, since pages may be of any
-// size), one issues the matrix instructions, and four for each 128 rows do the
+// size), two each, so that neither waits for the other; one issues the matrix instructions, and four for each 128 rows do the
 // softmax, a thread a row.  With two row tiles (TILES = 2) a tile of K and V
 // serves both, and the products of one run under the softmax of the other; with
 // one, the scores of the next tile of entries do.
@@ -824,6 +851,12 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     *stop = 1;
     return false;
 }
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done;
+}
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -840,11 +873,11 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
     asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(more) : "memory");
 }
 // (the wait belongs to the load: nothing may use the registers before it)
-__device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t a)
+__device__ __forceinline__ void tc_ld(float (&v)[32], uint32_t a)
 {
     uint32_t r[32];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
-                 "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+                 "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
                  "tcgen05.wait::ld.sync.aligned;"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
                    "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
@@ -854,22 +887,32 @@ __device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t a)
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16])
+__device__ __forceinline__ void tc_ld(float (&v)[64], uint32_t a)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-                 "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
-}
-__device__ __forceinline__ void tc_st32(uint32_t a, const float (&v)[32])
-{
-    uint32_t lo[16], hi[16];
+    uint32_t r[64];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+                 "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,"
+                 "%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                   "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+                   "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+                   "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
+                   "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]),
+                   "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]),
+                   "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+                 : "r"(a) : "memory");
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        lo[i] = __float_as_uint(v[i]);
-        hi[i] = __float_as_uint(v[16 + i]);
-    }
-    tc_st16(a, lo);
-    tc_st16(a + 16, hi);
+    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_st(uint32_t a, const uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+                 ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                   "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+                   "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+                   "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float pow2(float x)
@@ -909,9 +952,9 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
     Walk walk = start<M::NT>(A, S, red);
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            bar_init(k_full + 8 * i, 128);
+            bar_init(k_full + 8 * i, 64);
             bar_init(k_empty + 8 * i, 1);
-            bar_init(v_full + 8 * i, 128);
+            bar_init(v_full + 8 * i, 64);
             bar_init(v_empty + 8 * i, 1);
         }
         for (int i = 0; i < TILES * SB; ++i) bar_init(s_full + 8 * i, 1);
@@ -943,83 +986,94 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
     Segment seg;
 
     if (warp >= M::FETCH && warp < M::ISSUE) {
-        // ---- fetch K and V ----
-        // each warp has a quarter of a tile's entries: a lane finds one, all copy
-        constexpr int RW = KEYS / 4, RS = 32 / CH;                         // entries of a warp; of one copy of all lanes
-        const int w0 = (warp - M::FETCH) * RW, chunks = a.head_dim / 8, c = lane % CH, r0 = w0 + lane / CH;
-        const uint32_t sub = (c >> 3) * M::SUBK;
-        int n = 0, number = 0;                                             // tiles fetched; segments
-        bool ok = true;
-        // what has been issued but not yet announced: K and V of tiles done .. n
-        int announced = 0;                                                 // groups (2 a tile) announced
+        // ---- fetch: two warps K, two V, each with half of a tile's entries ----
+        // A lane finds one entry in 32, all copy.  Stages are filled as they come
+        // free, and announced in order, as soon as they have arrived.
+        constexpr int RW = KEYS / 2, RS = 32 / CH, PL = RW / 32;           // entries of a warp; of one copy of all lanes; of a lane
+        const int role = warp - M::FETCH;
+        const bool is_v = role >= 2;
+        const int w0 = (role & 1) * RW, chunks = a.head_dim / 8, c = lane % CH, r0 = w0 + lane / CH;
+        const uint32_t sub = (c >> 3) * M::SUBK, store = (is_v ? sv : sk) + sub;
+        const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
+        const int64_t st_page = is_v ? a.v_page : a.k_page, st_entry = is_v ? a.v_entry : a.k_entry, st_head = is_v ? a.v_head : a.k_head;
+        const T *const src = (const T *)(is_v ? a.v : a.k) + c * 8;
+        int n = 0, announced = 0, number = 0;                              // tiles fetched, announced; segments
         struct Mark { int first, j0, number; };
-        Mark marks[ST + 1] = {};                                              // of the last tiles, by tile % (ST + 1)
-        auto announce = [&]() {
-            const int tile = announced >> 1, st = tile % ST;
-            if (announced & 1) {
-                Mark m = marks[0];
+        Mark marks[ST];                                                    // of the tiles under way
 #pragma unroll
-                for (int i = 1; i <= ST; ++i)
-                    if (tile % (ST + 1) == i) m = marks[i];
-                if (m.j0 + KEYS > m.first) {
-                    bool found = false;
+        for (int i = 0; i < ST; ++i) marks[i] = {0, 0, 0};
+        auto announce = [&]() {
+            // all but the (n - announced - 1) newest copies have arrived
+            if (n - announced == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
+            else if (ST == 2 || n - announced == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.wait_group 2;" ::: "memory");
+            const int st = announced % ST;
+            Mark m = marks[0];
+#pragma unroll
+            for (int i = 1; i < ST; ++i)
+                if (st == i) m = marks[i];
+            if (is_v && m.j0 + KEYS > m.first) {
+                bool found = false;
 #pragma unroll 4
-                    for (int i = 0; i < RW / RS; ++i) {
-                        const int row = r0 + i * RS;
-                        const uint32_t at = sv + st * M::KV + sub + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-                        uint4 x;
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
-                        const bool any = (int)clear_odd<T>(x.x) | (int)clear_odd<T>(x.y) | (int)clear_odd<T>(x.z) | (int)clear_odd<T>(x.w);
-                        if (any && m.j0 + row >= m.first) {
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
-                            found = true;
-                        }
+                for (int i = 0; i < RW / RS; ++i) {
+                    const int row = r0 + i * RS;
+                    const uint32_t at = store + st * M::KV + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                    uint4 x;
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+                    const bool any = (int)clear_odd<T>(x.x) | (int)clear_odd<T>(x.y) | (int)clear_odd<T>(x.z) | (int)clear_odd<T>(x.w);
+                    if (any && m.j0 + row >= m.first) {
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+                        found = true;
                     }
-                    if (found) *(volatile int *)&odd_seg[m.number & 7] = m.number + 1;
                 }
+                if (found) *(volatile int *)&odd_seg[m.number & 7] = m.number + 1;
             }
             async_fence();
-            bar_arrive((announced & 1 ? v_full : k_full) + 8 * st);
+            bar_arrive(full + 8 * st);
             ++announced;
         };
-        constexpr int LAG = 2 * (ST - 1);                                  // groups in flight behind the newest
+        bool ok = true;
         while (ok && walk.next(A, S, seg)) {
-            const T *k = (const T *)a.k + seg.hk * a.k_head + c * 8, *v = (const T *)a.v + seg.hk * a.v_head + c * 8;
-            for (int t = 0; t < seg.tiles && ok; ++t, ++n) {
-                const int j0 = seg.j0 + t * KEYS, st = n % ST;
-                const uint32_t parity = (n / ST + 1) & 1;                  // of the stage's release; the first round finds it free
-                const int j = j0 + w0 + (lane & (RW - 1));
-                const Place at = place_of(a, seg.b, j < seg.j1 ? j : 0);
-                const unsigned in = __ballot_sync(~0u, j < seg.j1);
-                const int64_t off_k = at.page * a.k_page + at.in * a.k_entry, off_v = at.page * a.v_page + at.in * a.v_entry;
+            const T *const from = src + seg.hk * st_head;
+            int64_t off[PL];                                               // of this lane's entries of the next tile
+            unsigned in[PL];
+            auto find = [&](int t) {
 #pragma unroll
-                for (int i = 0; i <= ST; ++i)
-                    if (n % (ST + 1) == i) marks[i] = {seg.s.first, j0, number};
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (ok) ok = __all_sync(~0u, bar_wait((kv ? v_empty : k_empty) + 8 * st, parity, &stop));
-                    if (ok) {
-                        const uint32_t to = (kv ? sv : sk) + st * M::KV + sub;
-#pragma unroll
-                        for (int i = 0; i < RW / RS; ++i) {
-                            const int rw = i * RS + lane / CH, row = w0 + rw;
-                            const int64_t off = __shfl_sync(~0u, kv ? off_v : off_k, rw);
-                            const bool take = (in >> rw & 1u) && c < chunks;
-                            cp16(to + row * 128 + (((c & 7) ^ (row & 7)) << 4), take ? (const void *)((kv ? v : k) + off) : (const void *)a.k, take);
-                        }
-                    }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (ok && 2 * n + kv >= LAG) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
-                        announce();
-                    }
+                for (int i = 0; i < PL; ++i) {
+                    const int j = seg.j0 + t * KEYS + w0 + 32 * i + lane;
+                    const Place at = place_of(a, seg.b, j < seg.j1 ? j : 0);
+                    in[i] = __ballot_sync(~0u, j < seg.j1);
+                    off[i] = at.page * st_page + at.in * st_entry;
                 }
+            };
+            find(0);
+            for (int t = 0; t < seg.tiles && ok; ++t) {
+                const int st = n % ST;
+                const uint32_t parity = (n / ST + 1) & 1;                  // of the stage's release; the first round finds it free
+                // what has been fetched is announced before this warp waits for a stage
+                while (announced < n && !__all_sync(~0u, bar_test(empty + 8 * st, parity))) announce();
+                ok = __all_sync(~0u, bar_wait(empty + 8 * st, parity, &stop));
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < ST; ++i)
+                    if (st == i) marks[i] = {seg.s.first, seg.j0 + t * KEYS, number};
+                const uint32_t to = store + st * M::KV;
+#pragma unroll
+                for (int i = 0; i < RW / RS; ++i) {
+                    const int rw = i * RS + lane / CH, row = w0 + rw;
+                    const int64_t o = __shfl_sync(~0u, off[i * RS / 32], rw & 31);
+                    const bool take = (in[i * RS / 32] >> (rw & 31) & 1u) && c < chunks;
+                    cp16(to + row * 128 + (((c & 7) ^ (row & 7)) << 4), take ? (const void *)(from + o) : (const void *)a.k, take);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                ++n;
+                if (t + 1 < seg.tiles) find(t + 1);
             }
             ++number;
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (ok)
-            while (announced < 2 * n) announce();
+            while (announced < n) announce();
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else if (warp == M::ISSUE) {
         // ---- issue the products ----
         constexpr uint32_t FMT = __is_same(T, __nv_bfloat16) ? 1u : 0u;
@@ -1033,6 +1087,8 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             auto scores = [&](int r, int t) {
                 const int st = (n0 + t) % ST;
                 if (r == 0 && ok) ok = __all_sync(~0u, bar_wait(k_full + 8 * st, (n0 + t) / ST & 1, &stop));
+                // the scores' columns are free once the product that read P from them is done
+                if (t > 0 && ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it[r] - SB) & 1, &stop));
                 if (!ok) return;
                 tc_after();
                 if (lane == 0) {
@@ -1127,21 +1183,29 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 const bool masked = j0 + KEYS > s.first;
                 bool settled = t == 0;                                     // the product before this one is known to be in O
                 if (busy) {
-                    uint32_t see[KEYS / 32];
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < KEYS / 32; ++c) {
-                        float v[32];
-                        tc_ld32(v, s_at + 32 * c);
-                        see[c] = masked ? sees32(A, b, me.t, s.tree, j0 + 32 * c - s.first) : ~0u;
+                    // 64 entries at a time, read twice: first for the maximum, then for P
+                    // (loops kept rolled: the roles share the instruction cache)
+                    auto load = [&](float (&v)[64], int c) {
+                        tc_ld(v, s_at + 64 * c);
                         if (masked) {
+                            const uint32_t lo = sees32(A, b, me.t, s.tree, j0 + 64 * c - s.first);
+                            const uint32_t hi = sees32(A, b, me.t, s.tree, j0 + 64 * c + 32 - s.first);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) top = fmaxf(top, see[c] >> e & 1u ? v[e] * A.scale_log2 : -INFINITY);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e] * A.scale_log2);
+                            for (int e = 0; e < 32; ++e) {
+                                v[e] = lo >> e & 1u ? v[e] : -INFINITY;
+                                v[e + 32] = hi >> e & 1u ? v[e + 32] : -INFINITY;
+                            }
                         }
+                    };
+                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int c = 0; c < KEYS / 64; ++c) {
+                        float v[64];
+                        load(v, c);
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) t4[e & 3] = fmaxf(t4[e & 3], v[e]);
                     }
+                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * A.scale_log2;      // (scale > 0 here)
                     // replace the maximum only when it grew by more than 2^8
                     const bool grew = top > m + 8.f || (m == -INFINITY && top > m);
                     if (__any_sync(~0u, grew)) {
@@ -1157,30 +1221,32 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
 #pragma unroll 1
                             for (int c = 0; c < DP / 32; ++c) {
                                 float v[32];
-                                tc_ld32(v, o_at + 32 * c);
+                                uint32_t w[32];
+                                tc_ld(v, o_at + 32 * c);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) v[e] *= f;
-                                tc_st32(o_at + 32 * c, v);
+                                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(v[e] * f);
+                                tc_st(o_at + 32 * c, w);
                             }
                             tc_wait_st();
                         }
                     }
                     const float shift = m == -INFINITY ? 0.f : m;
+                    float l4[4] = {l, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int c = 0; c < KEYS / 64; ++c) {
+                        float v[64];
+                        uint32_t w[32];
+                        load(v, c);
 #pragma unroll
-                    for (int c = 0; c < KEYS / 32; ++c) {
-                        float v[32];
-                        tc_ld32(v, s_at + 32 * c);
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
+                        for (int e = 0; e < 64; ++e) {
                             v[e] = pow2(fmaf(v[e], A.scale_log2, -shift));
-                            if (masked) v[e] = see[c] >> e & 1u ? v[e] : 0.f;
-                            l += v[e];
+                            l4[e & 3] += v[e];
                         }
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = pack2<T>(v[2 * e], v[2 * e + 1]);
-                        tc_st16(s_at + 16 * c, w);
+                        for (int e = 0; e < 32; ++e) w[e] = pack2<T>(v[2 * e], v[2 * e + 1]);
+                        tc_st(s_at + 32 * c, w);
                     }
+                    l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
                     tc_wait_st();
                 }
                 // (every phase of o_done is waited for while the next cannot end)
@@ -1203,7 +1269,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
 #pragma unroll 1
             for (int c = 0; c < DP / 32; ++c) {
                 float v[32];
-                tc_ld32(v, o_at + 32 * c);
+                tc_ld(v, o_at + 32 * c);
                 if (!me.inside) continue;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = seg.whole && none && ok ? 0.f : v[e] * by;
@@ -1291,7 +1357,7 @@ dbs_status plan_of(const dbs_attention_args &a, Plan &P)
     P.dp = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256;
     // up to 16 rows of a kv head fit one instruction of k_attn_few, which reads
     // the cache once for each 16
-    P.many = rows > FEW_ROWS;
+    P.many = rows > FEW_ROWS && a.scale > 0;
     Share &S = P.share;
     int per_sm = P.dp == 64 ? 4 : P.dp == 128 ? 2 : 1;
     if (P.many) {
@@ -1313,12 +1379,24 @@ dbs_status plan_of(const dbs_attention_args &a, Plan &P)
     return DBS_OK;
 }
 
+// Rows of a call's largest unit.
+int64_t rows_of_unit(const Attn &A, const Plan &P)
+{
+    const int64_t rows = A.a.tokens * (A.a.q_heads / A.a.kv_heads);
+    return rows < P.share.rows ? rows : P.share.rows;
+}
+
 // The joining kernel, started while the first one ends.
 template <class T>
 dbs_status launch_join(const Attn &A, const Plan &P, cudaStream_t s)
 {
+    // whole blocks for a row while all rows find room on the GPU at once (8 blocks
+    // an SM), and no more blocks than that: each finds its unit's place anew
+    const int64_t units = A.a.batch * A.a.kv_heads * P.share.groups, rows = rows_of_unit(A, P), room = 152 * 8;
+    const int split = units * rows <= room ? JOIN_W : 1;
+    const int64_t turns = (rows + JOIN_W / split - 1) / (JOIN_W / split), most = room / units > 0 ? room / units : 1;
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)(A.a.batch * A.a.kv_heads * P.share.groups), (unsigned)((P.share.rows + JOIN_NT / 32 - 1) / (JOIN_NT / 32)));
+    c.gridDim = dim3((unsigned)units, (unsigned)(turns < most ? turns : most));
     c.blockDim = JOIN_NT;
     c.stream = s;
     cudaLaunchAttribute at[1];
@@ -1326,7 +1404,7 @@ dbs_status launch_join(const Attn &A, const Plan &P, cudaStream_t s)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     c.attrs = at;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, k_attn_join<T>, A, P.share, P.blocks) == cudaSuccess ? DBS_OK : (cudaGetLastError(), DBS_ERR_CUDA);
+    return cudaLaunchKernelEx(&c, k_attn_join<T>, A, P.share, P.blocks, (int)rows, split) == cudaSuccess ? DBS_OK : (cudaGetLastError(), DBS_ERR_CUDA);
 }
 
 template <class T, int DP>
