@@ -807,11 +807,16 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
 // lane), Q, K and V in shared memory in the 128-byte swizzle (K row by row, V
 // as it lies, its entries as the contraction's dimension), and P, rounded to
 // the caches' type, written over S for the second product.  Warps have roles:
-// four fetch K and V (16-byte asynchronous copies, since pages may be of any
-// size), two each, so that neither waits for the other; one issues the matrix instructions, and four for each 128 rows do the
-// softmax, a thread a row.  With two row tiles (TILES = 2) a tile of K and V
-// serves both, and the products of one run under the softmax of the other; with
-// one, the scores of the next tile of entries do.
+// four fetch K and V, one issues the matrix instructions, and four for each 128
+// rows do the softmax, a thread a row.  With two row tiles (TILES = 2) a tile of
+// K and V serves both, and the products of one run under the softmax of the
+// other; with one, the scores of the next tile of entries do.
+//
+// K and V come by tiled copies (TMA) of boxes of as many entries as divide a
+// page, eight at least; caches whose pages do not split into eights come by
+// 16-byte asynchronous copies, which reach about half of the memory's rate (a
+// batch of 16 trees over 2300 entries each: 57 us for 150 MB, an SM's copies in
+// flight being the limit).
 //
 // Every wait has a limit; a block whose wait runs out stops and leaves NaN in
 // its rows.
@@ -930,15 +935,32 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead)
     return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)((lead >> 4) & 0x3fffu) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-template <class T, int DP, int TILES>
-__global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Share S)
+// Tensor maps of K and V: [pages, entries, heads, head_dim], boxes of 64 columns
+// of one head of `box` entries.
+struct Maps {
+    CUtensorMap k, v;
+    int box;
+};
+
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap *map, int d, int head, int entry, int page, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+                 "l"(map), "r"(bar), "r"(d), "r"(head), "r"(entry), "r"(page) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+template <class T, int DP, int TILES, bool BOXES>
+__global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Share S, const __grid_constant__ Maps maps)
 {
     using M = Many<DP, TILES>;
     constexpr int KEYS = M::KEYS, ST = M::STAGES, SB = M::SB, CH = DP / 8;
     const dbs_attention_args &a = A.a;
     extern __shared__ unsigned char raw[];
     __shared__ int64_t red[M::NT / 32];
-    __shared__ __align__(8) uint64_t bars[4 * ST + TILES * (SB + 3) + 1];
+    __shared__ __align__(8) uint64_t bars[6 * ST + TILES * (SB + 3) + 1];
     __shared__ uint32_t tmem_at;
     __shared__ int stop;
     __shared__ int odd_seg[8];                       // segments (their number + 1) whose V is not finite somewhere
@@ -948,13 +970,15 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
     const uint32_t bar0 = smem_addr(bars);
     const uint32_t k_full = bar0, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST;
     const uint32_t s_full = v_empty + 8 * ST, q_full = s_full + 8 * TILES * SB, p_ready = q_full + 8 * TILES, o_done = p_ready + 8 * TILES;
-    const uint32_t last_bar = o_done + 8 * TILES;
+    const uint32_t last_bar = o_done + 8 * TILES, v_fixed = last_bar + 8, v_odd = v_fixed + 8 * ST;
     Walk walk = start<M::NT>(A, S, red);
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            bar_init(k_full + 8 * i, 64);
+            bar_init(k_full + 8 * i, BOXES ? 1 : 64);
             bar_init(k_empty + 8 * i, 1);
-            bar_init(v_full + 8 * i, 64);
+            bar_init(v_full + 8 * i, BOXES ? 1 : 64);
+            bar_init(v_fixed + 8 * i, 64);
+            bar_init(v_odd + 8 * i, 1);
             bar_init(v_empty + 8 * i, 1);
         }
         for (int i = 0; i < TILES * SB; ++i) bar_init(s_full + 8 * i, 1);
@@ -985,7 +1009,81 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
     };
     Segment seg;
 
-    if (warp >= M::FETCH && warp < M::ISSUE) {
+    if (BOXES && warp >= M::FETCH && warp < M::FETCH + 2) {
+        // ---- fetch: one warp K, one V, a lane a box ----
+        const bool is_v = warp > M::FETCH;
+        const uint32_t store = is_v ? sv : sk, full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
+        const CUtensorMap *const map = is_v ? &maps.v : &maps.k;
+        const int box = maps.box, boxes = KEYS / box;                      // (8 to 128 entries; 1 to 16 boxes)
+        int n = 0;
+        bool ok = true;
+        while (ok && walk.next(A, S, seg)) {
+            Place at = {0, 0};
+            auto find = [&](int t) {
+                const int j = seg.j0 + t * KEYS + lane * box;
+                if (lane < boxes && j < seg.j1) at = place_of(a, seg.b, j);
+            };
+            find(0);
+            for (int t = 0; t < seg.tiles && ok; ++t, ++n) {
+                const int st = n % ST, j = seg.j0 + t * KEYS;
+                ok = __all_sync(~0u, bar_wait(empty + 8 * st, (n / ST + 1) & 1, &stop));   // the first round finds it free
+                if (!ok) break;
+                const bool mine = lane < boxes && j + lane * box < seg.j1;
+                const int count = __popc(__ballot_sync(~0u, mine));
+                if (lane == 0) bar_expect(full + 8 * st, (uint32_t)(count * box * 128 * (DP / 64)));
+                __syncwarp();
+                if (mine)
+#pragma unroll
+                    for (int c = 0; c < DP / 64; ++c)
+                        box_load(store + st * M::KV + c * M::SUBK + lane * box * 128, map, 64 * c, seg.hk, (int)at.in, (int)at.page, full + 8 * st);
+                __syncwarp();
+                if (is_v && lane == 0 && j + KEYS > seg.s.first) bar_arrive(v_odd + 8 * st);      // a tile to look through
+                if (t + 1 < seg.tiles) find(t + 1);
+            }
+        }
+        // copies under way end before their memory is given back
+        if (!ok)
+            for (int i = n > ST ? n - ST : 0; i < n; ++i) {
+                int ignored = 0;
+                bar_wait(full + 8 * (i % ST), i / ST & 1, &ignored);
+            }
+    } else if (BOXES && warp >= M::FETCH + 2 && warp < M::ISSUE) {
+        // ---- the tiles with drafted entries: what lies behind the last entry of V
+        // becomes 0, and so does what is not finite in drafted ones ----
+        const int p = tid - 32 * (M::FETCH + 2), c = p % CH, r0 = p / CH;
+        constexpr int RS = 64 / CH;
+        int n = 0, number = 0;
+        uint32_t seen = 0;                                                 // parity of v_odd of a stage, a bit each
+        bool ok = true;
+        while (ok && walk.next(A, S, seg)) {
+            for (int t = 0; t < seg.tiles; ++t, ++n) {
+                const int j0 = seg.j0 + t * KEYS, st = n % ST;
+                if (j0 + KEYS <= seg.s.first) continue;
+                // (first that the stage's copies are this tile's, then that they have arrived)
+                ok = __all_sync(~0u, bar_wait(v_odd + 8 * st, seen >> st & 1u, &stop));
+                seen ^= 1u << st;
+                if (ok) ok = __all_sync(~0u, bar_wait(v_full + 8 * st, n / ST & 1, &stop));
+                if (!ok) break;
+                bool found = false;
+#pragma unroll 4
+                for (int row = r0; row < KEYS; row += RS) {
+                    const uint32_t at = sv + st * M::KV + (c >> 3) * M::SUBK + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                    uint4 x;
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+                    const bool behind = j0 + row >= seg.s.kv;
+                    const bool any = (int)clear_odd<T>(x.x) | (int)clear_odd<T>(x.y) | (int)clear_odd<T>(x.z) | (int)clear_odd<T>(x.w);
+                    if (behind) x = make_uint4(0, 0, 0, 0);
+                    if (behind || (any && j0 + row >= seg.s.first))
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+                    found |= any && !behind && j0 + row >= seg.s.first;
+                }
+                if (found) *(volatile int *)&odd_seg[number & 7] = number + 1;
+                async_fence();
+                bar_arrive(v_fixed + 8 * st);
+            }
+            ++number;
+        }
+    } else if (!BOXES && warp >= M::FETCH && warp < M::ISSUE) {
         // ---- fetch: two warps K, two V, each with half of a tile's entries ----
         // A lane finds one entry in 32, all copy.  Stages are filled as they come
         // free, and announced in order, as soon as they have arrived.
@@ -1079,6 +1177,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
         constexpr uint32_t FMT = __is_same(T, __nv_bfloat16) ? 1u : 0u;
         constexpr uint32_t DESC = 1u << 4 | FMT << 7 | FMT << 10 | (128u >> 4) << 24;
         constexpr uint32_t DESC_S = DESC | (uint32_t)(KEYS >> 3) << 17, DESC_O = DESC | 1u << 16 | (uint32_t)(DP >> 3) << 17;
+        uint32_t fixes = 0;                                                // parity of the repairs of a stage, a bit each
         int n0 = 0, it[TILES] = {}, units[TILES] = {};                     // first tile; of a row tile: score tiles, segments
         bool ok = true;
         while (ok && walk.next(A, S, seg)) {
@@ -1108,6 +1207,10 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             auto outputs = [&](int r, int t) {
                 const int st = (n0 + t) % ST, done = SB == 2 ? it[r] - (t + 1 < seg.tiles ? 2 : 1) : it[r] - 1;   // this tile's number
                 if (r == 0 && ok) ok = __all_sync(~0u, bar_wait(v_full + 8 * st, (n0 + t) / ST & 1, &stop));
+                if (BOXES && r == 0 && ok && seg.j0 + (t + 1) * KEYS > seg.s.first) {
+                    ok = __all_sync(~0u, bar_wait(v_fixed + 8 * st, fixes >> st & 1u, &stop));
+                    fixes ^= 1u << st;
+                }
                 if (ok) ok = __all_sync(~0u, bar_wait(p_ready + 8 * r, done & 1, &stop));
                 if (!ok) return;
                 tc_after();
@@ -1419,17 +1522,53 @@ dbs_status launch_few(const Attn &A, const Plan &P, cudaStream_t s)
     return st == DBS_OK ? launch_join<T>(A, P, s) : st;
 }
 
-template <class T, int DP, int TILES>
-dbs_status launch_many(const Attn &A, const Plan &P, cudaStream_t s)
+// Boxes of the caches, or false where pages or strides do not allow them.
+bool make_maps(const dbs_attention_args &a, int keys, Maps &M)
+{
+    const encode_tiled_fn encode = encode_tiled();
+    if (!encode || a.page_size < 1 || a.pages < 1) return false;
+    // a sequence's own page is one run of entries; pages of a table split into boxes
+    M.box = keys;
+    if (a.page_table)
+        while (M.box >= 8 && a.page_size % M.box) M.box /= 2;
+    if (M.box < 8) return false;
+    for (int i = 0; i < 2; ++i) {
+        const cuuint64_t dims[4] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.kv_heads, (cuuint64_t)a.page_size, (cuuint64_t)a.pages};
+        const int64_t by[3] = {i ? a.v_head : a.k_head, i ? a.v_entry : a.k_entry, i ? a.v_page : a.k_page};
+        const cuuint32_t box[4] = {64, 1, (cuuint32_t)M.box, 1}, ones[4] = {1, 1, 1, 1};
+        cuuint64_t strides[3];
+        for (int d = 0; d < 3; ++d) {
+            // (a dimension of one entry has any stride)
+            const int64_t bytes = dims[d + 1] == 1 ? 16 * a.head_dim : by[d] * 2;
+            if (bytes <= 0 || bytes >= int64_t(1) << 40 || dims[d + 1] >= cuuint64_t(1) << 31) return false;
+            strides[d] = (cuuint64_t)bytes;
+        }
+        if (encode(i ? &M.v : &M.k, a.dtype == DBS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                   const_cast<void *>(i ? a.v : a.k), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
+    return true;
+}
+
+template <class T, int DP, int TILES, bool BOXES>
+dbs_status launch_kind(const Attn &A, const Plan &P, const Maps &maps, cudaStream_t s)
 {
     using M = Many<DP, TILES>;
-    if (cudaFuncSetAttribute(k_attn_many<T, DP, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::SMEM) != cudaSuccess) {
+    if (cudaFuncSetAttribute(k_attn_many<T, DP, TILES, BOXES>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::SMEM) != cudaSuccess) {
         cudaGetLastError();
         return DBS_ERR_CUDA;
     }
-    k_attn_many<T, DP, TILES><<<P.blocks, M::NT, M::SMEM, s>>>(A, P.share);
+    k_attn_many<T, DP, TILES, BOXES><<<P.blocks, M::NT, M::SMEM, s>>>(A, P.share, maps);
     const dbs_status st = launched();
     return st == DBS_OK ? launch_join<T>(A, P, s) : st;
+}
+
+template <class T, int DP, int TILES>
+dbs_status launch_many(const Attn &A, const Plan &P, cudaStream_t s)
+{
+    Maps maps{};
+    return make_maps(A.a, P.share.keys, maps) ? launch_kind<T, DP, TILES, true>(A, P, maps, s) : launch_kind<T, DP, TILES, false>(A, P, maps, s);
 }
 
 template <class T>

@@ -1,6 +1,7 @@
 // Device helpers shared by the decoding-step operators (w4.cu, rotary.cu,
 // attention.cu, logits.cu).
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -49,6 +50,26 @@ template <class T, int N> __device__ __forceinline__ uint32_t shut2(const float 
 {
     if constexpr (sizeof(T) == 4) return __float_as_uint(v[i]);
     else return pack2<T>(v[2 * i], v[2 * i + 1]);
+}
+
+// Tensor maps for tiled copies, made by the driver (whose entry point is looked
+// up once; no library is linked for it).
+typedef CUresult (*encode_tiled_fn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                    const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline encode_tiled_fn encode_tiled()
+{
+    static const encode_tiled_fn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return (encode_tiled_fn)p;
+    }();
+    return fn;
 }
 
 inline bool dtype_ok(int32_t d) { return d == DBS_F32 || d == DBS_F16 || d == DBS_BF16; }
