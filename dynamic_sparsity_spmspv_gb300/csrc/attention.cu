@@ -252,6 +252,7 @@ struct Share {
     int keys, rows, groups;    // entries of a tile; query rows of a unit; units of a kv head
     int heavy, last;           // weight of a tile: of a kv head's units but the last, of the last
     float *scratch;
+    int4 *units;               // of every unit: the first block that works on it, its slot there, the number of blocks
 
     __host__ __device__ int per_head() const { return heavy * (groups - 1) + last; }
     // Blocks that get a piece: none of them shorter than a tile.
@@ -260,10 +261,6 @@ struct Share {
         const int64_t most = total / (heavy > last ? heavy : last);
         return most < grid ? most : grid;
     }
-};
-
-struct Line {
-    int64_t total, at;         // weight of all; weight before sequence b
 };
 
 __device__ __forceinline__ int tiles_of(const Share &S, const Seq &s)
@@ -289,24 +286,14 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red)
     return v;
 }
 
-// Weight before sequence `b`, and of all.
+// Weight of all.
 template <int NT>
-__device__ Line line_at(const Attn &A, const Share &S, int64_t b, int64_t *red)
+__device__ int64_t line_total(const Attn &A, const Share &S, int64_t *red)
 {
-    Line L{0, 0};
-    if (A.a.batch == 1) {
-        L.total = weight_of(A, S, 0);
-        return L;
-    }
-    int64_t all = 0, before = 0;
-    for (int64_t i = threadIdx.x; i < A.a.batch; i += NT) {
-        const int64_t n = weight_of(A, S, i);
-        all += n;
-        if (i < b) before += n;
-    }
-    L.total = block_sum<NT>(all, red);
-    L.at = block_sum<NT>(before, red);
-    return L;
+    if (A.a.batch == 1) return weight_of(A, S, 0);
+    int64_t all = 0;
+    for (int64_t i = threadIdx.x; i < A.a.batch; i += NT) all += weight_of(A, S, i);
+    return block_sum<NT>(all, red);
 }
 
 // The sequence that holds position x of the line, and the weight before it.
@@ -374,32 +361,47 @@ struct Segment {
     int tiles;                 // 0: the piece ends within the unit's next tile, which the following block has
     bool whole;                // the unit's only part
     int slot;                  // of scratch, if not
+    int64_t u0;                // the unit in the line, and its weight
+    int weight;
+};
+
+// Lengths of the first sequences, kept in shared memory by a block.
+constexpr int NEAR = 128;
+struct Near {
+    int kv[NEAR], tree[NEAR];
 };
 
 // Walks a block's piece.
 struct Walk {
-    int64_t x, end, at, b, first;
-    __device__ __forceinline__ bool next(const Attn &A, const Share &S, Segment &g)
+    int64_t x, end, at, b, first, total, blocks;
+    __device__ __forceinline__ bool next(const Attn &A, const Share &S, const Near &near, Segment &g)
     {
         while (x < end) {
-            g.s = sequence(A, b);
+            if (b < NEAR) {
+                g.s.kv = near.kv[b];
+                g.s.tree = near.tree[b];
+                g.s.first = g.s.kv - g.s.tree;
+            } else {
+                g.s = sequence(A, b);
+            }
             const int n = tiles_of(S, g.s), per = S.per_head();
             const uint64_t in = (uint64_t)(x - at), head = (uint64_t)n * (uint32_t)per;
             g.b = b;
-            // (32-bit divisions where they do)
-            g.hk = (in | head) >> 32 ? (int)(in / head) : (int)((uint32_t)in / (uint32_t)head);
+            g.hk = (int)quotient((int64_t)in, (int64_t)head);
             const int64_t rest = (int64_t)(in - g.hk * head), big = (int64_t)n * S.heavy;
-            g.group = S.groups == 1 ? 0 : (rest >> 31) ? (int)(rest / big) : (int)((uint32_t)rest / (uint32_t)big);
+            g.group = S.groups == 1 ? 0 : (int)quotient(rest, big);
             if (g.group > S.groups - 1) g.group = S.groups - 1;
             const int w = g.group == S.groups - 1 ? S.last : S.heavy;
             const int64_t u0 = x - rest + g.group * big, u1 = u0 + (int64_t)n * w;      // the unit in the line
             const int64_t e = end < u1 ? end : u1;
-            const int t0 = (int)((x - u0 + w - 1) / w), t1 = (int)((e - u0 + w - 1) / w);
+            const int t0 = w == 1 ? (int)(x - u0) : (int)((x - u0 + w - 1) / w), t1 = w == 1 ? (int)(e - u0) : (int)((e - u0 + w - 1) / w);
             g.tiles = t1 - t0;
             g.whole = g.tiles == n;
             g.slot = first >= u0 ? 0 : 1;
             g.j0 = t0 * S.keys;
             g.j1 = (int64_t)t1 * S.keys < g.s.kv ? t1 * S.keys : g.s.kv;
+            g.u0 = u0;
+            g.weight = n * w;
             x = e;
             if (x - at == (int64_t)head * A.a.kv_heads) {
                 at = x;
@@ -409,20 +411,36 @@ struct Walk {
         }
         return false;
     }
+    // For the join, by the block with the unit's first tile: who works on it.
+    __device__ __forceinline__ void record(const Attn &A, const Share &S, const Segment &g) const
+    {
+        if (g.j0 != 0) return;
+        const int w = g.group == S.groups - 1 ? S.last : S.heavy;
+        int64_t c1 = g.whole ? blockIdx.x : block_of(total, g.u0 + g.weight - 1, blocks);
+        // the last block has no tile if its piece begins within the last one
+        while (w > 1 && c1 > blockIdx.x && (piece(total, c1, blocks) - g.u0 + w - 1) / w >= g.weight / w) --c1;
+        S.units[(g.b * A.a.kv_heads + g.hk) * S.groups + g.group] = make_int4((int)blockIdx.x, g.slot, (int)(c1 - blockIdx.x) + 1, 0);
+    }
 };
 
 template <int NT>
-__device__ __forceinline__ Walk start(const Attn &A, const Share &S, int64_t *red)
+__device__ __forceinline__ Walk start(const Attn &A, const Share &S, int64_t *red, Near &near)
 {
     Walk w;
-    const int64_t total = line_at<NT>(A, S, 0, red).total;
-    const int64_t blocks = S.blocks(total, gridDim.x);
-    if (blockIdx.x >= blocks) {
+    for (int i = threadIdx.x; i < NEAR && i < A.a.batch; i += NT) {
+        const Seq s = sequence(A, i);
+        near.kv[i] = s.kv;
+        near.tree[i] = s.tree;
+    }
+    w.total = line_total<NT>(A, S, red);
+    w.blocks = S.blocks(w.total, gridDim.x);
+    __syncthreads();
+    if (blockIdx.x >= w.blocks) {
         w.x = w.end = 0;
         return w;
     }
-    w.x = w.first = piece(total, blockIdx.x, blocks);
-    w.end = piece(total, blockIdx.x + 1, blocks);
+    w.x = w.first = piece(w.total, blockIdx.x, w.blocks);
+    w.end = piece(w.total, blockIdx.x + 1, w.blocks);
     w.b = sequence_of<NT>(A, S, w.x, w.at, red);
     return w;
 }
@@ -435,30 +453,22 @@ constexpr int JOIN_NT = 128, JOIN_W = JOIN_NT / 32;
 // of the parts' outputs, several loads at a time, and the warps' sums are added
 // in order.  Bound by the latency of that chain.
 template <class T>
-__global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int grid, int rows, int split)
+__global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int rows, int split)
 {
     const dbs_attention_args &a = A.a;
-    __shared__ int64_t red[JOIN_W];
     __shared__ float s_o[JOIN_W][256];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t per = (uint32_t)a.kv_heads * S.groups;
     const uint32_t b = blockIdx.x / per, u = blockIdx.x % per;
-    const int hk = (int)(u / S.groups), group = (int)(u % S.groups), w = group == S.groups - 1 ? S.last : S.heavy;
-    const Line L = line_at<JOIN_NT>(A, S, b, red);
+    const int hk = (int)(u / S.groups), group = (int)(u % S.groups);
+    const int4 unit = S.units[blockIdx.x];
     const Seq s = sequence(A, b);
-    const int n = tiles_of(S, s);
-    const int64_t x0 = L.at + (int64_t)n * ((int64_t)hk * S.per_head() + group * S.heavy), x1 = x0 + (int64_t)n * w;
-    const int64_t blocks = S.blocks(L.total, grid);
-    const int64_t c0 = block_of(L.total, x0, blocks);
-    int64_t c1 = block_of(L.total, x1 - 1, blocks);
-    // the last block has no tile if its piece begins within the last one
-    while (w > 1 && c1 > c0 && (piece(L.total, c1, blocks) - x0 + w - 1) / w >= n) --c1;
-    if (c0 == c1) return;
-    const int parts = (int)(c1 - c0) + 1, mine = warp % split;
+    const int parts = unit.z, mine = warp % split;
+    if (parts == 1) return;
     const int64_t size = slot_floats(S.rows, a.head_dim), stat = (int64_t)S.rows * a.head_dim;
     // the unit may be the second of its first block, and is the first of the others
-    const float *p0 = slot_of(A, S, c0, piece(L.total, c0, blocks) >= x0 ? 0 : 1), *rest = slot_of(A, S, c0, 0);
+    const float *p0 = slot_of(A, S, unit.x, unit.y), *rest = slot_of(A, S, unit.x, 0);
     for (int r0 = blockIdx.y * (JOIN_W / split); r0 < rows; r0 += gridDim.y * (JOIN_W / split)) {
         const int r = r0 + warp / split;
         const Row row = row_of(A, hk, (int64_t)group * S.rows + r);
@@ -578,6 +588,7 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
     const dbs_attention_args &a = A.a;
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ int64_t red[FEW_W];
+    __shared__ Near near;
     __shared__ float s_m[FEW_W][FEW_ROWS], s_l[FEW_W][FEW_ROWS];
     __shared__ int s_odd[FEW_W];
     constexpr int RB = DP * 2, CH = DP / 8, HALF = FEW_STEP * RB;   // bytes and 16-byte chunks of an entry; of a stage's K
@@ -586,10 +597,12 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
     unsigned char *mine = ring + warp * (FEW_STAGES * 2 * HALF);
     const uint32_t base = smem_addr(mine);
     const int chunks = a.head_dim / 8;
-    Walk walk = start<FEW_NT>(A, S, red);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // (the join waits for this grid's end)
+    Walk walk = start<FEW_NT>(A, S, red, near);
     Segment seg;
     {
-        while (walk.next(A, S, seg)) {
+        while (walk.next(A, S, near, seg)) {
+            if (threadIdx.x == 0) walk.record(A, S, seg);
             const Seq &s = seg.s;
             const int64_t b = seg.b;
             const int hk = seg.hk, j0 = seg.j0, j1 = seg.j1;
@@ -797,7 +810,6 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
             __syncthreads();       // the rings are free again
         }
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---- many rows: tcgen05 ----
@@ -960,6 +972,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
     const dbs_attention_args &a = A.a;
     extern __shared__ unsigned char raw[];
     __shared__ int64_t red[M::NT / 32];
+    __shared__ Near near;
     __shared__ __align__(8) uint64_t bars[6 * ST + TILES * (SB + 3) + 1];
     __shared__ uint32_t tmem_at;
     __shared__ int stop;
@@ -971,7 +984,8 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
     const uint32_t k_full = bar0, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST;
     const uint32_t s_full = v_empty + 8 * ST, q_full = s_full + 8 * TILES * SB, p_ready = q_full + 8 * TILES, o_done = p_ready + 8 * TILES;
     const uint32_t last_bar = o_done + 8 * TILES, v_fixed = last_bar + 8, v_odd = v_fixed + 8 * ST;
-    Walk walk = start<M::NT>(A, S, red);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // (the join waits for this grid's end)
+    Walk walk = start<M::NT>(A, S, red, near);
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             bar_init(k_full + 8 * i, BOXES ? 1 : 64);
@@ -1017,7 +1031,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
         const int box = maps.box, boxes = KEYS / box;                      // (8 to 128 entries; 1 to 16 boxes)
         int n = 0;
         bool ok = true;
-        while (ok && walk.next(A, S, seg)) {
+        while (ok && walk.next(A, S, near, seg)) {
             Place at = {0, 0};
             auto find = [&](int t) {
                 const int j = seg.j0 + t * KEYS + lane * box;
@@ -1055,7 +1069,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
         int n = 0, number = 0;
         uint32_t seen = 0;                                                 // parity of v_odd of a stage, a bit each
         bool ok = true;
-        while (ok && walk.next(A, S, seg)) {
+        while (ok && walk.next(A, S, near, seg)) {
             for (int t = 0; t < seg.tiles; ++t, ++n) {
                 const int j0 = seg.j0 + t * KEYS, st = n % ST;
                 if (j0 + KEYS <= seg.s.first) continue;
@@ -1131,7 +1145,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             ++announced;
         };
         bool ok = true;
-        while (ok && walk.next(A, S, seg)) {
+        while (ok && walk.next(A, S, near, seg)) {
             const T *const from = src + seg.hk * st_head;
             int64_t off[PL];                                               // of this lane's entries of the next tile
             unsigned in[PL];
@@ -1180,8 +1194,9 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
         uint32_t fixes = 0;                                                // parity of the repairs of a stage, a bit each
         int n0 = 0, it[TILES] = {}, units[TILES] = {};                     // first tile; of a row tile: score tiles, segments
         bool ok = true;
-        while (ok && walk.next(A, S, seg)) {
+        while (ok && walk.next(A, S, near, seg)) {
             const int used = tiles_in(seg);
+            if (lane == 0) walk.record(A, S, seg);
             // scores of row tile r against tile t of the segment
             auto scores = [&](int r, int t) {
                 const int st = (n0 + t) % ST;
@@ -1255,7 +1270,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
         const uint32_t o_at = tmem + lanes + M::O_COL + r * DP;
         int it = 0, number = 0;                                            // tiles done; segments
         bool ok = true;
-        while (ok && walk.next(A, S, seg)) {
+        while (ok && walk.next(A, S, near, seg)) {
             const int number_now = number++;
             if (r >= tiles_in(seg)) continue;                              // the unit has one row tile: the other's barriers rest
             const int64_t b = seg.b;
@@ -1263,14 +1278,26 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             const Row me = row_of(A, seg.hk, (int64_t)seg.group * (128 * TILES) + r * 128 + row);
             const bool busy = __any_sync(~0u, me.inside);
             {
-                // this row of Q
+                // Q: the warp copies its 32 rows, 32 / CH of them at a time
+                constexpr int RS = 32 / CH;
                 const T *q = (const T *)a.q + b * a.q_batch + me.t * a.q_token + me.h * a.q_head;
-#pragma unroll 8
-                for (int c = 0; c < CH; ++c) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (me.inside && 8 * c < a.head_dim) x = *(const uint4 *)(q + 8 * c);
-                    const uint32_t at = sq + r * M::Q + (c >> 3) * M::SUBQ + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+                const uint64_t from = me.inside ? (uint64_t)q : 0;
+                const int c = lane % CH;
+#pragma unroll
+                for (int i0 = 0; i0 < 32 / RS; i0 += 16) {
+                    uint4 x[16];
+#pragma unroll
+                    for (int i = 0; i < 16 && i0 + i < 32 / RS; ++i) {
+                        const uint64_t p = __shfl_sync(~0u, from, (i0 + i) * RS + lane / CH);
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (p && 8 * c < a.head_dim) x[i] = *(const uint4 *)((const T *)p + 8 * c);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16 && i0 + i < 32 / RS; ++i) {
+                        const int to = (warp & 3) * 32 + (i0 + i) * RS + lane / CH;
+                        const uint32_t at = sq + r * M::Q + (c >> 3) * M::SUBQ + to * 128 + (((c & 7) ^ (to & 7)) << 4);
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w) : "memory");
+                    }
                 }
                 async_fence();
                 bar_arrive(q_full + 8 * r);
@@ -1428,7 +1455,6 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---- host ----
@@ -1438,7 +1464,7 @@ struct Plan {
     bool rows, many;           // any alignment; 128 rows at a time
     int dp, blocks;
     Share share;
-    int64_t scratch;
+    int64_t slots, scratch;    // bytes of scratch: the slots, and all
 };
 
 bool aligned8(int64_t v) { return (v & 7) == 0; }
@@ -1478,7 +1504,8 @@ dbs_status plan_of(const dbs_attention_args &a, Plan &P)
     S.last = P.many ? (int)((rows - (int64_t)(S.groups - 1) * S.rows + 127) / 128) : 1;
     const int64_t most = a.batch * a.kv_heads * S.groups * (entries < S.keys ? 1 : (entries + S.keys - 1) / S.keys);
     P.blocks = (int)(most < sms * per_sm ? most : sms * per_sm);
-    P.scratch = (int64_t)P.blocks * 2 * slot_floats(S.rows, a.head_dim) * 4;
+    P.slots = (int64_t)P.blocks * 2 * slot_floats(S.rows, a.head_dim) * 4;
+    P.scratch = P.slots + a.batch * a.kv_heads * S.groups * (int64_t)sizeof(int4);
     return DBS_OK;
 }
 
@@ -1507,7 +1534,7 @@ dbs_status launch_join(const Attn &A, const Plan &P, cudaStream_t s)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     c.attrs = at;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, k_attn_join<T>, A, P.share, P.blocks, (int)rows, split) == cudaSuccess ? DBS_OK : (cudaGetLastError(), DBS_ERR_CUDA);
+    return cudaLaunchKernelEx(&c, k_attn_join<T>, A, P.share, (int)rows, split) == cudaSuccess ? DBS_OK : (cudaGetLastError(), DBS_ERR_CUDA);
 }
 
 template <class T, int DP>
@@ -1630,6 +1657,7 @@ dbs_status dbs_tree_attention(const dbs_attention_args *a, void *stream)
     const bool wide_out = aligned16(a->out) && aligned8(a->o_batch) && aligned8(a->o_token) && aligned8(a->o_head);
     const Attn A{*a, a->scale * 1.4426950408889634f, (int)((a->tokens + 63) / 64), wide_out};
     P.share.scratch = (float *)a->scratch;
+    P.share.units = (int4 *)((char *)a->scratch + P.slots);
     return a->dtype == DBS_F16 ? launch<__half>(A, P, (cudaStream_t)stream) : launch<__nv_bfloat16>(A, P, (cudaStream_t)stream);
 }
 
