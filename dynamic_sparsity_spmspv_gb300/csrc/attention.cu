@@ -14,6 +14,7 @@ struct Attn {
     float scale_log2;          // scale * log2(e): probabilities are powers of two
     int words;                 // 64-bit mask words per token
     bool wide_out;             // heads of out start on 16-byte boundaries
+    int group;                 // query heads of a kv head
 };
 
 // What sequence b holds, with every length clamped to its range.
@@ -63,10 +64,10 @@ struct Row {
 
 __device__ __forceinline__ Row row_of(const Attn &A, int hk, int64_t R)
 {
-    const int G = A.a.q_heads / A.a.kv_heads;
+    const uint32_t G = (uint32_t)A.group, t = (uint32_t)R / G;             // (tokens * G < 2^27)
     Row r;
-    r.t = (int)(R / G);
-    r.h = hk * G + (int)(R % G);
+    r.t = (int)t;
+    r.h = hk * (int)G + (int)((uint32_t)R - t * G);
     r.inside = R < A.a.tokens * G;
     return r;
 }
@@ -267,74 +268,6 @@ __device__ __forceinline__ int tiles_of(const Share &S, const Seq &s)
 {
     return s.kv <= S.keys ? 1 : (int)((uint32_t)(s.kv + S.keys - 1) / (uint32_t)S.keys);
 }
-__device__ __forceinline__ int64_t weight_of(const Attn &A, const Share &S, int64_t b)
-{
-    return (int64_t)tiles_of(S, sequence(A, b)) * A.a.kv_heads * S.per_head();
-}
-
-// Sum of `v` over the block (every thread gets it); `red` holds a word per warp.
-template <int NT>
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red)
-{
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0;
-    for (int w = 0; w < NT / 32; ++w) v += red[w];
-    return v;
-}
-
-// Weight of all.
-template <int NT>
-__device__ int64_t line_total(const Attn &A, const Share &S, int64_t *red)
-{
-    if (A.a.batch == 1) return weight_of(A, S, 0);
-    int64_t all = 0;
-    for (int64_t i = threadIdx.x; i < A.a.batch; i += NT) all += weight_of(A, S, i);
-    return block_sum<NT>(all, red);
-}
-
-// The sequence that holds position x of the line, and the weight before it.
-template <int NT>
-__device__ int64_t sequence_of(const Attn &A, const Share &S, int64_t x, int64_t &at, int64_t *red)
-{
-    at = 0;
-    if (A.a.batch == 1) return 0;
-    __shared__ int64_t hit, hit_at;
-    for (int64_t base = 0; base < A.a.batch; base += NT) {
-        const int64_t i = base + threadIdx.x;
-        const int64_t n = i < A.a.batch ? weight_of(A, S, i) : 0;
-        int64_t inc = n;
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(~0u, inc, d);
-            if (lane >= d) inc += o;
-        }
-        __syncthreads();
-        if (lane == 31) red[warp] = inc;
-        __syncthreads();
-        int64_t add = at, sum = 0;
-        for (int w = 0; w < NT / 32; ++w) {
-            if (w < warp) add += red[w];
-            sum += red[w];
-        }
-        if (x < at + sum) {
-            if (x >= add + inc - n && x < add + inc) {
-                hit = i;
-                hit_at = add + inc - n;
-            }
-            __syncthreads();
-            at = hit_at;
-            return hit;
-        }
-        at += sum;
-    }
-    return A.a.batch - 1;      // not reached: x < total
-}
-
 // (32-bit divisions where they do)
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 {
@@ -371,30 +304,26 @@ struct Near {
     int kv[NEAR], tree[NEAR];
 };
 
-// Walks a block's piece.
+__device__ __forceinline__ Seq sequence(const Attn &A, const Near &near, int64_t b)
+{
+    if (b >= NEAR) return sequence(A, b);
+    return {near.kv[b], near.kv[b] - near.tree[b], near.tree[b]};
+}
+
+// Walks a block's piece, unit by unit.
 struct Walk {
-    int64_t x, end, at, b, first, total, blocks;
+    int64_t x, end, b, u0, first, total, blocks;
+    int hk, group;
     __device__ __forceinline__ bool next(const Attn &A, const Share &S, const Near &near, Segment &g)
     {
         while (x < end) {
-            if (b < NEAR) {
-                g.s.kv = near.kv[b];
-                g.s.tree = near.tree[b];
-                g.s.first = g.s.kv - g.s.tree;
-            } else {
-                g.s = sequence(A, b);
-            }
-            const int n = tiles_of(S, g.s), per = S.per_head();
-            const uint64_t in = (uint64_t)(x - at), head = (uint64_t)n * (uint32_t)per;
+            g.s = sequence(A, near, b);
+            const int n = tiles_of(S, g.s), w = group == S.groups - 1 ? S.last : S.heavy;
+            const int64_t u1 = u0 + (int64_t)n * w, e = end < u1 ? end : u1;
+            const int t0 = w == 1 ? (int)(x - u0) : (int)((x - u0 + w - 1) >> 1), t1 = w == 1 ? (int)(e - u0) : (int)((e - u0 + w - 1) >> 1);
             g.b = b;
-            g.hk = (int)quotient((int64_t)in, (int64_t)head);
-            const int64_t rest = (int64_t)(in - g.hk * head), big = (int64_t)n * S.heavy;
-            g.group = S.groups == 1 ? 0 : (int)quotient(rest, big);
-            if (g.group > S.groups - 1) g.group = S.groups - 1;
-            const int w = g.group == S.groups - 1 ? S.last : S.heavy;
-            const int64_t u0 = x - rest + g.group * big, u1 = u0 + (int64_t)n * w;      // the unit in the line
-            const int64_t e = end < u1 ? end : u1;
-            const int t0 = w == 1 ? (int)(x - u0) : (int)((x - u0 + w - 1) / w), t1 = w == 1 ? (int)(e - u0) : (int)((e - u0 + w - 1) / w);
+            g.hk = hk;
+            g.group = group;
             g.tiles = t1 - t0;
             g.whole = g.tiles == n;
             g.slot = first >= u0 ? 0 : 1;
@@ -403,9 +332,15 @@ struct Walk {
             g.u0 = u0;
             g.weight = n * w;
             x = e;
-            if (x - at == (int64_t)head * A.a.kv_heads) {
-                at = x;
-                ++b;
+            if (x == u1) {
+                u0 = u1;
+                if (++group == S.groups) {
+                    group = 0;
+                    if (++hk == A.a.kv_heads) {
+                        hk = 0;
+                        ++b;
+                    }
+                }
             }
             if (g.tiles > 0) return true;
         }
@@ -423,25 +358,90 @@ struct Walk {
     }
 };
 
+// Where this block's piece begins.  Up to NEAR sequences every warp finds out
+// for itself from the lengths in shared memory, a few sequences a lane; of more
+// the block adds up the lengths in turns.
 template <int NT>
 __device__ __forceinline__ Walk start(const Attn &A, const Share &S, int64_t *red, Near &near)
 {
+    const int64_t B = A.a.batch;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Walk w;
-    for (int i = threadIdx.x; i < NEAR && i < A.a.batch; i += NT) {
+    for (int i = threadIdx.x; i < NEAR && i < B; i += NT) {
         const Seq s = sequence(A, i);
         near.kv[i] = s.kv;
         near.tree[i] = s.tree;
     }
-    w.total = line_total<NT>(A, S, red);
-    w.blocks = S.blocks(w.total, gridDim.x);
     __syncthreads();
-    if (blockIdx.x >= w.blocks) {
-        w.x = w.end = 0;
-        return w;
+    const int64_t per = (int64_t)A.a.kv_heads * S.per_head();
+    auto tiles = [&](int64_t i) { return i < B ? (int64_t)tiles_of(S, sequence(A, near, i)) * per : 0; };
+    auto scan = [&](int64_t v) {                             // sums up to and with each lane
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(~0u, v, d);
+            if (lane >= d) v += o;
+        }
+        return v;
+    };
+    int64_t at = 0;
+    if (B <= NEAR) {
+        constexpr int E = NEAR / 32;
+        int64_t n[E], sum = 0;
+#pragma unroll
+        for (int k = 0; k < E; ++k) sum += n[k] = tiles(lane * E + k);
+        int64_t upto = scan(sum);
+        w.total = __shfl_sync(~0u, upto, 31);
+        w.blocks = S.blocks(w.total, gridDim.x);
+        w.x = blockIdx.x < w.blocks ? piece(w.total, blockIdx.x, w.blocks) : w.total;
+        w.b = 0;
+        if (w.x < w.total) {
+            const int who = __ffs(__ballot_sync(~0u, w.x < upto)) - 1;
+            upto -= sum;                                     // before this lane's
+            int64_t mine = lane * E;
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+                if (mine == lane * E + k && w.x >= upto + n[k]) {
+                    upto += n[k];
+                    ++mine;
+                }
+            at = __shfl_sync(~0u, upto, who);
+            w.b = __shfl_sync(~0u, mine, who);
+        }
+    } else {
+        int64_t sum = 0;
+        for (int64_t i = threadIdx.x; i < B; i += NT) sum += tiles(i);
+        sum = __shfl_sync(~0u, scan(sum), 31);
+        if (lane == 0) red[warp] = sum;
+        __syncthreads();
+        w.total = 0;
+        for (int k = 0; k < NT / 32; ++k) w.total += red[k];
+        w.blocks = S.blocks(w.total, gridDim.x);
+        w.x = blockIdx.x < w.blocks ? piece(w.total, blockIdx.x, w.blocks) : w.total;
+        w.b = 0;
+        // (every warp for itself, 32 sequences at a time)
+        if (w.x < w.total)
+            for (;; w.b += 32) {
+                const int64_t n = tiles(w.b + lane), upto = scan(n), all = __shfl_sync(~0u, upto, 31);
+                if (w.x < at + all) {
+                    const int who = __ffs(__ballot_sync(~0u, w.x < at + upto)) - 1;
+                    at += __shfl_sync(~0u, upto - n, who);
+                    w.b += who;
+                    break;
+                }
+                at += all;
+            }
     }
-    w.x = w.first = piece(w.total, blockIdx.x, w.blocks);
-    w.end = piece(w.total, blockIdx.x + 1, w.blocks);
-    w.b = sequence_of<NT>(A, S, w.x, w.at, red);
+    w.first = w.x;
+    w.end = blockIdx.x < w.blocks ? piece(w.total, blockIdx.x + 1, w.blocks) : w.x;
+    if (w.x < w.end) {
+        const int n = tiles_of(S, sequence(A, near, w.b));
+        const int64_t head = (int64_t)n * S.per_head(), big = (int64_t)n * S.heavy;
+        w.hk = (int)quotient(w.x - at, head);
+        const int64_t rest = w.x - at - w.hk * head;
+        w.group = S.groups == 1 ? 0 : (int)quotient(rest, big);
+        if (w.group > S.groups - 1) w.group = S.groups - 1;
+        w.u0 = at + w.hk * head + w.group * big;
+    }
     return w;
 }
 
@@ -973,7 +973,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
     extern __shared__ unsigned char raw[];
     __shared__ int64_t red[M::NT / 32];
     __shared__ Near near;
-    __shared__ __align__(8) uint64_t bars[6 * ST + TILES * (SB + 3) + 1];
+    __shared__ __align__(8) uint64_t bars[6 * ST + TILES * (SB + 4) + 1];
     __shared__ uint32_t tmem_at;
     __shared__ int stop;
     __shared__ int odd_seg[8];                       // segments (their number + 1) whose V is not finite somewhere
@@ -983,21 +983,21 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
     const uint32_t bar0 = smem_addr(bars);
     const uint32_t k_full = bar0, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST;
     const uint32_t s_full = v_empty + 8 * ST, q_full = s_full + 8 * TILES * SB, p_ready = q_full + 8 * TILES, o_done = p_ready + 8 * TILES;
-    const uint32_t last_bar = o_done + 8 * TILES, v_fixed = last_bar + 8, v_odd = v_fixed + 8 * ST;
+    const uint32_t last_bar = o_done + 8 * TILES, v_fixed = last_bar + 8, v_odd = v_fixed + 8 * ST, q_empty = v_odd + 8 * ST;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // (the join waits for this grid's end)
-    Walk walk = start<M::NT>(A, S, red, near);
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            bar_init(k_full + 8 * i, BOXES ? 1 : 64);
+            bar_init(k_full + 8 * i, BOXES ? 1 : 32);
             bar_init(k_empty + 8 * i, 1);
-            bar_init(v_full + 8 * i, BOXES ? 1 : 64);
+            bar_init(v_full + 8 * i, BOXES ? 1 : 32);
             bar_init(v_fixed + 8 * i, 64);
             bar_init(v_odd + 8 * i, 1);
             bar_init(v_empty + 8 * i, 1);
         }
         for (int i = 0; i < TILES * SB; ++i) bar_init(s_full + 8 * i, 1);
         for (int i = 0; i < TILES; ++i) {
-            bar_init(q_full + 8 * i, 128);
+            bar_init(q_full + 8 * i, 64);
+            bar_init(q_empty + 8 * i, 1);
             bar_init(p_ready + 8 * i, 128);
             bar_init(o_done + 8 * i, 1);
         }
@@ -1010,6 +1010,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_at)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    Walk walk = start<M::NT>(A, S, red, near);
     tc_before();
     __syncthreads();
     tc_after();
@@ -1061,16 +1062,43 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 int ignored = 0;
                 bar_wait(full + 8 * (i % ST), i / ST & 1, &ignored);
             }
-    } else if (BOXES && warp >= M::FETCH + 2 && warp < M::ISSUE) {
-        // ---- the tiles with drafted entries: what lies behind the last entry of V
-        // becomes 0, and so does what is not finite in drafted ones ----
+    } else if (warp >= M::FETCH + 2 && warp < M::ISSUE) {
+        // ---- Q; and of the tiles with drafted entries: what lies behind the last
+        // entry of V becomes 0, and so does what is not finite in drafted ones ----
         const int p = tid - 32 * (M::FETCH + 2), c = p % CH, r0 = p / CH;
         constexpr int RS = 64 / CH;
-        int n = 0, number = 0;
+        int n = 0, number = 0, units[TILES] = {};
         uint32_t seen = 0;                                                 // parity of v_odd of a stage, a bit each
         bool ok = true;
         while (ok && walk.next(A, S, near, seg)) {
-            for (int t = 0; t < seg.tiles; ++t, ++n) {
+            const int used = tiles_in(seg);
+#pragma unroll
+            for (int r = 0; r < TILES; ++r) {
+                if (r >= used || !ok) continue;
+                // free once the segment before has its scores
+                ok = __all_sync(~0u, bar_wait(q_empty + 8 * r, (units[r]++ + 1) & 1, &stop));
+                const int64_t R0 = (int64_t)seg.group * (128 * TILES) + r * 128;
+                const T *q = (const T *)a.q + seg.b * a.q_batch + 8 * c;
+#pragma unroll 1
+                for (int i0 = 0; i0 < 128; i0 += 8 * RS) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const Row row = row_of(A, seg.hk, R0 + i0 + i * RS + r0);
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (row.inside && 8 * c < a.head_dim) x[i] = *(const uint4 *)(q + row.t * a.q_token + row.h * a.q_head);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int to = i0 + i * RS + r0;
+                        const uint32_t at = sq + r * M::Q + (c >> 3) * M::SUBQ + to * 128 + (((c & 7) ^ (to & 7)) << 4);
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w) : "memory");
+                    }
+                }
+                async_fence();
+                bar_arrive(q_full + 8 * r);
+            }
+            if constexpr (BOXES) for (int t = 0; t < seg.tiles && ok; ++t, ++n) {
                 const int j0 = seg.j0 + t * KEYS, st = n % ST;
                 if (j0 + KEYS <= seg.s.first) continue;
                 // (first that the stage's copies are this tile's, then that they have arrived)
@@ -1098,13 +1126,11 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             ++number;
         }
     } else if (!BOXES && warp >= M::FETCH && warp < M::ISSUE) {
-        // ---- fetch: two warps K, two V, each with half of a tile's entries ----
-        // A lane finds one entry in 32, all copy.  Stages are filled as they come
+        // ---- fetch: one warp K, one V.  A lane finds one entry in 32, all copy.  Stages are filled as they come
         // free, and announced in order, as soon as they have arrived.
-        constexpr int RW = KEYS / 2, RS = 32 / CH, PL = RW / 32;           // entries of a warp; of one copy of all lanes; of a lane
-        const int role = warp - M::FETCH;
-        const bool is_v = role >= 2;
-        const int w0 = (role & 1) * RW, chunks = a.head_dim / 8, c = lane % CH, r0 = w0 + lane / CH;
+        constexpr int RS = 32 / CH, PL = KEYS / 32;                        // entries of one copy of all lanes; of a lane
+        const bool is_v = warp > M::FETCH;
+        const int chunks = a.head_dim / 8, c = lane % CH, r0 = lane / CH;
         const uint32_t sub = (c >> 3) * M::SUBK, store = (is_v ? sv : sk) + sub;
         const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
         const int64_t st_page = is_v ? a.v_page : a.k_page, st_entry = is_v ? a.v_entry : a.k_entry, st_head = is_v ? a.v_head : a.k_head;
@@ -1127,7 +1153,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             if (is_v && m.j0 + KEYS > m.first) {
                 bool found = false;
 #pragma unroll 4
-                for (int i = 0; i < RW / RS; ++i) {
+                for (int i = 0; i < KEYS / RS; ++i) {
                     const int row = r0 + i * RS;
                     const uint32_t at = store + st * M::KV + row * 128 + (((c & 7) ^ (row & 7)) << 4);
                     uint4 x;
@@ -1152,7 +1178,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             auto find = [&](int t) {
 #pragma unroll
                 for (int i = 0; i < PL; ++i) {
-                    const int j = seg.j0 + t * KEYS + w0 + 32 * i + lane;
+                    const int j = seg.j0 + t * KEYS + 32 * i + lane;
                     const Place at = place_of(a, seg.b, j < seg.j1 ? j : 0);
                     in[i] = __ballot_sync(~0u, j < seg.j1);
                     off[i] = at.page * st_page + at.in * st_entry;
@@ -1171,10 +1197,10 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                     if (st == i) marks[i] = {seg.s.first, seg.j0 + t * KEYS, number};
                 const uint32_t to = store + st * M::KV;
 #pragma unroll
-                for (int i = 0; i < RW / RS; ++i) {
-                    const int rw = i * RS + lane / CH, row = w0 + rw;
-                    const int64_t o = __shfl_sync(~0u, off[i * RS / 32], rw & 31);
-                    const bool take = (in[i * RS / 32] >> (rw & 31) & 1u) && c < chunks;
+                for (int i = 0; i < KEYS / RS; ++i) {
+                    const int row = i * RS + lane / CH;
+                    const int64_t o = __shfl_sync(~0u, off[i * RS / 32], row & 31);
+                    const bool take = (in[i * RS / 32] >> (row & 31) & 1u) && c < chunks;
                     cp16(to + row * 128 + (((c & 7) ^ (row & 7)) << 4), take ? (const void *)(from + o) : (const void *)a.k, take);
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
@@ -1202,7 +1228,9 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 const int st = (n0 + t) % ST;
                 if (r == 0 && ok) ok = __all_sync(~0u, bar_wait(k_full + 8 * st, (n0 + t) / ST & 1, &stop));
                 // the scores' columns are free once the product that read P from them is done
-                if (t > 0 && ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it[r] - SB) & 1, &stop));
+                // (the next segment waits for the last one's: two phases of a barrier are
+                // never told apart)
+                if (it[r] > 0 && ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it[r] - (t > 0 ? SB : 1)) & 1, &stop));
                 if (!ok) return;
                 tc_after();
                 if (lane == 0) {
@@ -1215,6 +1243,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                     }
                     tc_commit(s_full + 8 * (r * SB + (SB == 2 ? it[r] & 1 : 0)));
                     if (r == used - 1) tc_commit(k_empty + 8 * st);
+                    if (t == seg.tiles - 1) tc_commit(q_empty + 8 * r);
                 }
                 ++it[r];
                 __syncwarp();
@@ -1277,31 +1306,6 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             const Seq s = seg.s;
             const Row me = row_of(A, seg.hk, (int64_t)seg.group * (128 * TILES) + r * 128 + row);
             const bool busy = __any_sync(~0u, me.inside);
-            {
-                // Q: the warp copies its 32 rows, 32 / CH of them at a time
-                constexpr int RS = 32 / CH;
-                const T *q = (const T *)a.q + b * a.q_batch + me.t * a.q_token + me.h * a.q_head;
-                const uint64_t from = me.inside ? (uint64_t)q : 0;
-                const int c = lane % CH;
-#pragma unroll
-                for (int i0 = 0; i0 < 32 / RS; i0 += 16) {
-                    uint4 x[16];
-#pragma unroll
-                    for (int i = 0; i < 16 && i0 + i < 32 / RS; ++i) {
-                        const uint64_t p = __shfl_sync(~0u, from, (i0 + i) * RS + lane / CH);
-                        x[i] = make_uint4(0, 0, 0, 0);
-                        if (p && 8 * c < a.head_dim) x[i] = *(const uint4 *)((const T *)p + 8 * c);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16 && i0 + i < 32 / RS; ++i) {
-                        const int to = (warp & 3) * 32 + (i0 + i) * RS + lane / CH;
-                        const uint32_t at = sq + r * M::Q + (c >> 3) * M::SUBQ + to * 128 + (((c & 7) ^ (to & 7)) << 4);
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w) : "memory");
-                    }
-                }
-                async_fence();
-                bar_arrive(q_full + 8 * r);
-            }
             float m = -INFINITY, l = 0.f;
             for (int t = 0; t < seg.tiles; ++t, ++it) {
                 const int buf = SB == 2 ? it & 1 : 0;
@@ -1655,7 +1659,7 @@ dbs_status dbs_tree_attention(const dbs_attention_args *a, void *stream)
     if (st != DBS_OK) return st;
     if (P.scratch > 0 && (!a->scratch || !aligned16(a->scratch) || a->scratch_bytes < P.scratch)) return DBS_ERR_INVALID_ARG;
     const bool wide_out = aligned16(a->out) && aligned8(a->o_batch) && aligned8(a->o_token) && aligned8(a->o_head);
-    const Attn A{*a, a->scale * 1.4426950408889634f, (int)((a->tokens + 63) / 64), wide_out};
+    const Attn A{*a, a->scale * 1.4426950408889634f, (int)((a->tokens + 63) / 64), wide_out, a->q_heads / a->kv_heads};
     P.share.scratch = (float *)a->scratch;
     P.share.units = (int4 *)((char *)a->scratch + P.slots);
     return a->dtype == DBS_F16 ? launch<__half>(A, P, (cudaStream_t)stream) : launch<__nv_bfloat16>(A, P, (cudaStream_t)stream);
