@@ -279,7 +279,7 @@ __device__ __forceinline__ int64_t block_of(int64_t total, int64_t x, int64_t bl
 
 // A slot of scratch: rows x head_dim sums, the rows' maxima and sums, and the
 // mark of a V that is not finite.
-__host__ __device__ __forceinline__ int64_t slot_floats(int rows, int head_dim) { return (int64_t)rows * (head_dim + 2) + 4; }
+__host__ __device__ __forceinline__ int64_t slot_floats(int rows, int head_dim) { return (int64_t)rows * (head_dim + 2) + 8; }
 __device__ __forceinline__ float *slot_of(const Attn &A, const Share &S, int64_t block, int slot)
 {
     return S.scratch + (block * 2 + slot) * slot_floats(S.rows, A.a.head_dim);
@@ -819,8 +819,9 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
 // lane), Q, K and V in shared memory in the 128-byte swizzle (K row by row, V
 // as it lies, its entries as the contraction's dimension), and P, rounded to
 // the caches' type, written over S for the second product.  Warps have roles:
-// four fetch K and V, one issues the matrix instructions, and four for each 128
-// rows do the softmax, a thread a row.  With two row tiles (TILES = 2) a tile of
+// two fetch K and V, two load Q, one issues the matrix instructions, two look
+// through the drafted part of V, and four for each 128 rows do the softmax, a
+// thread a row.  With two row tiles (TILES = 2) a tile of
 // K and V serves both, and the products of one run under the softmax of the
 // other; with one, the scores of the next tile of entries do.
 //
@@ -839,8 +840,8 @@ template <int DP, int TILES> struct Many {
     static constexpr int SB = TILES == 1 ? 2 : 1;                         // score buffers of a row tile
     static constexpr int SUBQ = 128 * 128, SUBK = KEYS * 128;             // 64 columns of a tile, in bytes
     static constexpr int Q = DP / 64 * SUBQ, KV = DP / 64 * SUBK;
-    static constexpr int NT = 32 * (4 * TILES + 4 + 1);
-    static constexpr int FETCH = 4 * TILES, ISSUE = FETCH + 4;            // first warps of the roles
+    static constexpr int NT = 32 * (4 * TILES + 4 + 1 + 2);
+    static constexpr int FETCH = 4 * TILES, LOAD = FETCH + 2, ISSUE = FETCH + 4, MEND = ISSUE + 1;   // first warps of the roles
     static constexpr int S_COL = 0, O_COL = TILES * SB * KEYS;
     static constexpr int SMEM = TILES * Q + STAGES * 2 * KV + 1024;
 };
@@ -932,6 +933,11 @@ __device__ __forceinline__ void tc_st(uint32_t a, const uint32_t (&r)[32])
                  : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 32 bytes, a whole sector, at once.
+__device__ __forceinline__ void store32(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g, uint32_t h)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
+}
 __device__ __forceinline__ float pow2(float x)
 {
     float y;
@@ -939,12 +945,22 @@ __device__ __forceinline__ float pow2(float x)
     return y;
 }
 
-// Shared-memory descriptor of a 128-byte-swizzled tile: `lead` bytes between
-// 64-column parts (used where the columns are not the contraction's
-// dimension), 1024 between groups of eight rows.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead)
+// Shared-memory descriptors of 128-byte-swizzled tiles: the lower word has the
+// address and, where the columns are not the contraction's dimension, the bytes
+// between 64-column parts; the upper one 1024 bytes between groups of eight rows.
+// The lower words of a product's instructions are made ready, in registers that
+// all lanes agree on, before the first of them: an instruction whose descriptor
+// is made between two others delays both (112 instead of 69 cycles for 128 x 128
+// x 16, measured alone).
+constexpr uint32_t DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) { return __shfl_sync(~0u, (addr >> 4) | (lead >> 4) << 16, 0); }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return (uint64_t)DESC_HI << 32 | lo; }
+// One lane of a warp, in a way that the compiler knows to be one.
+__device__ __forceinline__ bool elected()
 {
-    return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)((lead >> 4) & 0x3fffu) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e != 0;
 }
 
 // Tensor maps of K and V: [pages, entries, heads, head_dim], boxes of 64 columns
@@ -1062,43 +1078,60 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 int ignored = 0;
                 bar_wait(full + 8 * (i % ST), i / ST & 1, &ignored);
             }
-    } else if (warp >= M::FETCH + 2 && warp < M::ISSUE) {
-        // ---- Q; and of the tiles with drafted entries: what lies behind the last
-        // entry of V becomes 0, and so does what is not finite in drafted ones ----
-        const int p = tid - 32 * (M::FETCH + 2), c = p % CH, r0 = p / CH;
+    } else if (warp >= M::LOAD && warp < M::ISSUE) {
+        // ---- Q ----
+        const int p = tid - 32 * M::LOAD, c = p % CH, r0 = p / CH;
         constexpr int RS = 64 / CH;
-        int n = 0, number = 0, units[TILES] = {};
-        uint32_t seen = 0;                                                 // parity of v_odd of a stage, a bit each
+        int units[TILES] = {};
         bool ok = true;
         while (ok && walk.next(A, S, near, seg)) {
             const int used = tiles_in(seg);
 #pragma unroll
             for (int r = 0; r < TILES; ++r) {
                 if (r >= used || !ok) continue;
-                // free once the segment before has its scores
-                ok = __all_sync(~0u, bar_wait(q_empty + 8 * r, (units[r]++ + 1) & 1, &stop));
+                // rows past the call's are left as they are: a row's results depend on it alone
                 const int64_t R0 = (int64_t)seg.group * (128 * TILES) + r * 128;
+                const int rows = all_rows - R0 < 128 ? (int)(all_rows - R0) : 128;
                 const T *q = (const T *)a.q + seg.b * a.q_batch + 8 * c;
+                bool free = false;
 #pragma unroll 1
-                for (int i0 = 0; i0 < 128; i0 += 8 * RS) {
-                    uint4 x[8];
+                for (int i0 = 0; i0 < rows; i0 += 16 * RS) {
+                    uint4 x[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const Row row = row_of(A, seg.hk, R0 + i0 + i * RS + r0);
+                    for (int i = 0; i < 16; ++i) {
+                        const int to = i0 + i * RS + r0;
+                        const Row row = row_of(A, seg.hk, R0 + to);
                         x[i] = make_uint4(0, 0, 0, 0);
-                        if (row.inside && 8 * c < a.head_dim) x[i] = *(const uint4 *)(q + row.t * a.q_token + row.h * a.q_head);
+                        if (to < rows && 8 * c < a.head_dim) x[i] = *(const uint4 *)(q + row.t * a.q_token + row.h * a.q_head);
+                    }
+                    if (!free) {
+                        // free once the segment before has its scores
+                        ok = __all_sync(~0u, bar_wait(q_empty + 8 * r, (units[r]++ + 1) & 1, &stop));
+                        free = true;
+                        if (!ok) break;
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                         const int to = i0 + i * RS + r0;
                         const uint32_t at = sq + r * M::Q + (c >> 3) * M::SUBQ + to * 128 + (((c & 7) ^ (to & 7)) << 4);
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w) : "memory");
+                        if (to < rows)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w) : "memory");
                     }
                 }
                 async_fence();
                 bar_arrive(q_full + 8 * r);
             }
-            if constexpr (BOXES) for (int t = 0; t < seg.tiles && ok; ++t, ++n) {
+        }
+    } else if (warp >= M::MEND) {
+        // ---- of the tiles with drafted entries: what lies behind the last entry of V
+        // becomes 0, and so does what is not finite in drafted ones ----
+        const int p = tid - 32 * M::MEND, c = p % CH, r0 = p / CH;
+        constexpr int RS = 64 / CH;
+        int n = 0, number = 0;
+        uint32_t seen = 0;                                                 // parity of v_odd of a stage, a bit each
+        bool ok = BOXES;                                                   // (else the fetching warps do it)
+        while (ok && walk.next(A, S, near, seg)) {
+            for (int t = 0; t < seg.tiles && ok; ++t, ++n) {
                 const int j0 = seg.j0 + t * KEYS, st = n % ST;
                 if (j0 + KEYS <= seg.s.first) continue;
                 // (first that the stage's copies are this tile's, then that they have arrived)
@@ -1233,14 +1266,17 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 if (it[r] > 0 && ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it[r] - (t > 0 ? SB : 1)) & 1, &stop));
                 if (!ok) return;
                 tc_after();
-                if (lane == 0) {
-                    const uint32_t d = tmem + M::S_COL + (r * SB + (SB == 2 ? it[r] & 1 : 0)) * KEYS;
+                const uint32_t d = __shfl_sync(~0u, tmem + M::S_COL + (r * SB + (SB == 2 ? it[r] & 1 : 0)) * KEYS, 0);
+                const uint32_t qa = desc_lo(sq + r * M::Q, 16), ka = desc_lo(sk + st * M::KV, 16);
+                uint64_t qd[DP / 16], kd[DP / 16];
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        const uint32_t in = (k & 3) * 32;
-                        tc_mma_ss(d, tile_desc(sq + r * M::Q + (k >> 2) * M::SUBQ + in, 16), tile_desc(sk + st * M::KV + (k >> 2) * M::SUBK + in, 16),
-                                  DESC_S, k > 0);
-                    }
+                for (int k = 0; k < DP / 16; ++k) {
+                    qd[k] = desc_of(qa + ((k >> 2) * M::SUBQ + (k & 3) * 32) / 16);
+                    kd[k] = desc_of(ka + ((k >> 2) * M::SUBK + (k & 3) * 32) / 16);
+                }
+                if (elected()) {
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) tc_mma_ss(d, qd[k], kd[k], DESC_S, k > 0);
                     tc_commit(s_full + 8 * (r * SB + (SB == 2 ? it[r] & 1 : 0)));
                     if (r == used - 1) tc_commit(k_empty + 8 * st);
                     if (t == seg.tiles - 1) tc_commit(q_empty + 8 * r);
@@ -1258,11 +1294,15 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 if (ok) ok = __all_sync(~0u, bar_wait(p_ready + 8 * r, done & 1, &stop));
                 if (!ok) return;
                 tc_after();
-                if (lane == 0) {
-                    const uint32_t d = tmem + M::O_COL + r * DP, pa = tmem + M::S_COL + (r * SB + (SB == 2 ? done & 1 : 0)) * KEYS;
+                const uint32_t d = __shfl_sync(~0u, tmem + M::O_COL + r * DP, 0);
+                const uint32_t pa = __shfl_sync(~0u, tmem + M::S_COL + (r * SB + (SB == 2 ? done & 1 : 0)) * KEYS, 0);
+                const uint32_t va = desc_lo(sv + st * M::KV, M::SUBK), more = __shfl_sync(~0u, t, 0) > 0;
+                uint64_t vd[KEYS / 16];
 #pragma unroll
-                    for (int k = 0; k < KEYS / 16; ++k)
-                        tc_mma_ts(d, pa + 8 * k, tile_desc(sv + st * M::KV + k * 2048, M::SUBK), DESC_O, t > 0 || k > 0);
+                for (int k = 0; k < KEYS / 16; ++k) vd[k] = desc_of(va + k * 2048 / 16);
+                if (elected()) {
+#pragma unroll
+                    for (int k = 0; k < KEYS / 16; ++k) tc_mma_ts(d, pa + 8 * k, vd[k], DESC_O, k > 0 ? 1u : more);
                     tc_commit(o_done + 8 * r);
                     if (r == used - 1) tc_commit(v_empty + 8 * st);
                 }
@@ -1412,9 +1452,9 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                     const int d = 32 * c + e;
                     if (d >= a.head_dim) break;
                     if (!seg.whole) {
-                        float4 *to = (float4 *)(part + (int64_t)slot_row * a.head_dim + d);
-                        to[0] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                        to[1] = make_float4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+                        store32(part + (int64_t)slot_row * a.head_dim + d, __float_as_uint(v[e]), __float_as_uint(v[e + 1]), __float_as_uint(v[e + 2]),
+                                __float_as_uint(v[e + 3]), __float_as_uint(v[e + 4]), __float_as_uint(v[e + 5]), __float_as_uint(v[e + 6]),
+                                __float_as_uint(v[e + 7]));
                     } else if (A.wide_out) {
                         *(uint4 *)(out + d) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]), pack2<T>(v[e + 4], v[e + 5]),
                                                          pack2<T>(v[e + 6], v[e + 7]));
@@ -1657,7 +1697,7 @@ dbs_status dbs_tree_attention(const dbs_attention_args *a, void *stream)
     Plan P;
     const dbs_status st = plan_of(*a, P);
     if (st != DBS_OK) return st;
-    if (P.scratch > 0 && (!a->scratch || !aligned16(a->scratch) || a->scratch_bytes < P.scratch)) return DBS_ERR_INVALID_ARG;
+    if (P.scratch > 0 && (!a->scratch || (reinterpret_cast<uintptr_t>(a->scratch) & 31u) || a->scratch_bytes < P.scratch)) return DBS_ERR_INVALID_ARG;
     const bool wide_out = aligned16(a->out) && aligned8(a->o_batch) && aligned8(a->o_token) && aligned8(a->o_head);
     const Attn A{*a, a->scale * 1.4426950408889634f, (int)((a->tokens + 63) / 64), wide_out, a->q_heads / a->kv_heads};
     P.share.scratch = (float *)a->scratch;

@@ -535,7 +535,7 @@ typedef struct {
     void *out;                 /* [batch, tokens, q_heads, head_dim] */
     int64_t o_batch, o_token, o_head;
     float *lse;                /* device [batch, tokens, q_heads], natural logarithm, or NULL */
-    void *scratch;             /* device, 16-byte aligned, dbs_tree_attention_scratch bytes; the
+    void *scratch;             /* device, 32-byte aligned, dbs_tree_attention_scratch bytes; the
                                   call leaves nothing in it that a later call reads */
     int64_t scratch_bytes;
 } dbs_attention_args;
