@@ -543,7 +543,6 @@ __global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int rows
 
 // ---- few rows: every warp streams its own entries ----
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
@@ -847,28 +846,6 @@ template <int DP, int TILES> struct Many {
 };
 static_assert(Many<128, 2>::O_COL + 2 * 128 <= 512 && Many<256, 1>::O_COL + 256 <= 512, "tensor memory");
 
-constexpr unsigned long long WAIT_NS = 2000000000ull;
-
-__device__ __forceinline__ void bar_init(uint32_t bar, int count) { asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory"); }
-__device__ __forceinline__ void bar_arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(bar) : "memory"); }
-// Waits for the phase of that parity to end; false when the limit ran out, here or in another warp.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *stop)
-{
-    unsigned long long began = 0;
-    for (int i = 0;; ++i) {
-        uint32_t done;
-        asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-        if (done) return true;
-        if ((i & 31) != 31) continue;
-        if (*stop) return false;
-        unsigned long long now;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        if (began == 0) began = now;
-        else if (now - began > WAIT_NS) break;
-    }
-    *stop = 1;
-    return false;
-}
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
 {
     uint32_t done;
@@ -955,14 +932,6 @@ __device__ __forceinline__ float pow2(float x)
 constexpr uint32_t DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) { return __shfl_sync(~0u, (addr >> 4) | (lead >> 4) << 16, 0); }
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return (uint64_t)DESC_HI << 32 | lo; }
-// One lane of a warp, in a way that the compiler knows to be one.
-__device__ __forceinline__ bool elected()
-{
-    uint32_t e;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
-    return e != 0;
-}
-
 // Tensor maps of K and V: [pages, entries, heads, head_dim], boxes of 64 columns
 // of one head of `box` entries.
 struct Maps {
@@ -975,11 +944,6 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap *map, i
     asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
                  "l"(map), "r"(bar), "r"(d), "r"(head), "r"(entry), "r"(page) : "memory");
 }
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
 template <class T, int DP, int TILES, bool BOXES>
 __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Share S, const __grid_constant__ Maps maps)
 {

@@ -52,6 +52,46 @@ template <class T, int N> __device__ __forceinline__ uint32_t shut2(const float 
     else return pack2<T>(v[2 * i], v[2 * i + 1]);
 }
 
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// ---- barriers in shared memory ----
+
+// Every wait ends: after this long it gives up.
+constexpr unsigned long long WAIT_NS = 2000000000ull;
+
+__device__ __forceinline__ void bar_init(uint32_t bar, int count) { asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory"); }
+__device__ __forceinline__ void bar_arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(bar) : "memory"); }
+// Waits for the phase of that parity to end; false when the limit ran out, here or in another warp.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *stop)
+{
+    unsigned long long began = 0;
+    for (int i = 0;; ++i) {
+        uint32_t done;
+        asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done) return true;
+        if ((i & 31) != 31) continue;
+        if (*stop) return false;
+        unsigned long long now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (began == 0) began = now;
+        else if (now - began > WAIT_NS) break;
+    }
+    *stop = 1;
+    return false;
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// One lane of a warp, in a way that the compiler knows to be one.
+__device__ __forceinline__ bool elected()
+{
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e != 0;
+}
+
 // Tensor maps for tiled copies, made by the driver (whose entry point is looked
 // up once; no library is linked for it).
 typedef CUresult (*encode_tiled_fn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,

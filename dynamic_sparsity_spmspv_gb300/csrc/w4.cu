@@ -121,11 +121,14 @@ struct Cut {
     int steps, phase;          // stages of a row; stages whose x is in shared memory at a time
     int shift;                 // log2 of the group
     int64_t groups;            // of rows: a block's rows at a time
+    bool bf16_scales;          // of 16-bit ones
+    uint32_t magic;            // of the codes' numbers
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes)
+__device__ __forceinline__ void stage_load(uint32_t dst, const CUtensorMap *map, int byte, int row, uint32_t bar)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst), "l"(map),
+                 "r"(bar), "r"(byte), "r"(row) : "memory");
 }
 
 // Eight neighbouring values of x as the pairs (0, 4), (1, 5), (2, 6), (3, 7).
@@ -188,6 +191,13 @@ __device__ __forceinline__ void lay_out(const float *x, int64_t j, int64_t n, bo
     for (int p = 0; p < 3; ++p) out[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
 
+// (v & 0x000f000f) | magic as one instruction: as an expression it is two.
+__device__ __forceinline__ uint32_t nibbles(uint32_t v, uint32_t magic)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(v), "n"(0x000f000f), "r"(magic));
+    return r;
+}
 __device__ __forceinline__ uint4 ld16(uint32_t a)
 {
     uint4 v;
@@ -202,78 +212,71 @@ __device__ __forceinline__ uint32_t ld4(uint32_t a)
 }
 
 // One block takes groups of rows in turn; each warp streams stages of weights
-// through its own ring of shared memory (cp.async, no block-wide wait) against
-// x in shared memory: all of it, laid out once, or, where it does not fit, a
-// phase at a time.
-template <class T, class S, int NT, int RT>
-__global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
+// through its own ring of shared memory, a tiled copy (TMA) a stage, with no
+// block-wide wait, against x in shared memory: all of it, laid out once, or,
+// where it does not fit, a phase at a time.  S16: scales of 16 bits; FINE: groups
+// of 32 or 64 columns.  A wait that runs out leaves NaN.
+template <class T, bool S16, int NT, int RT, bool FINE>
+__global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C, const __grid_constant__ CUtensorMap map)
 {
     using P = Piece<T>;
     using H = Half2<typename P::type>;
-    constexpr int STEP = STEP_V<RT>, ROWB = STEP / 2, CH = ROWB / 16, WORDS = STEP / 32;
+    constexpr int STEP = STEP_V<RT>, ROWB = STEP / 2, WORDS = STEP / 32;
     constexpr int RED = RT * 16 * NT * 8;                                    // floats of a warp's sums
-    extern __shared__ __align__(128) unsigned char sm[];
+    extern __shared__ unsigned char raw[];
+    unsigned char *const sm = raw + (-smem_addr(raw) & 1023u);               // (the swizzle counts from 1024-byte boundaries)
+    __shared__ __align__(8) uint64_t bars[MMA_W * STAGES];
+    __shared__ int stop;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
     const int wk = warp & (C.wk - 1), wr = warp / C.wk, wrs = MMA_W / C.wk;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + warp * STAGES * STAGE);
+    const uint32_t ring = smem_addr(sm + warp * STAGES * STAGE), bar = smem_addr(bars + warp * STAGES);
     uint4 *const none = (uint4 *)(sm + MMA_W * STAGES * STAGE);              // 16 bytes of zeros
-    float *const red = (float *)(none + 8);          // (128 bytes on)
+    float *const red = (float *)(none + 8);                                  // (128 bytes on)
     uint4 *const xs = (uint4 *)(red + (C.wk > 1 || P::parts > 1 ? MMA_W * RED : 0));
-    const int64_t bytes = (A.n + 1) >> 1;
     const int64_t t0 = (int64_t)blockIdx.y * (NT * 8 / P::parts);            // the pass's first token
     const int64_t left = A.tokens - t0;
     const int tokens = (int)(left < NT * 8 / P::parts ? left : NT * 8 / P::parts), cols = tokens * P::parts;
     const T *x = (const T *)A.x + t0 * A.x_stride;
     const bool wide = aligned_x(x, A.x_stride);
     const int last_group = (int)((A.n - 1) >> C.shift);
-    const uint32_t per = (1u << C.shift) / 32u;                              // words of a group
+    const uint32_t magic = C.magic;                                          // H::magic, from a register
+    const uint32_t per = FINE ? (1u << C.shift) / 32u : 4u;                  // words of a group (or of half of one)
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < MMA_W * STAGES; ++i) bar_init(smem_addr(bars + i), 1);
+        stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (threadIdx.x < 8) none[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
 
     // The stages to fetch run ahead of the stages in use, across groups of rows.
-    // A lane copies 16 bytes of every (32 / CH)-th row of a stage.
-    constexpr int RS = 32 / CH;
-    const int fr = lane / CH, fc = lane % CH;
     int64_t fg = wk < C.steps ? blockIdx.x : C.groups;
-    int fs = wk, slot = 0, rows_left;
-    const uint8_t *fp;
-    auto fetch_from = [&]() {
-        const int64_t row0 = (fg * wrs + wr) * (16 * RT) + fr;
-        fp = A.q + row0 * A.q_stride + (int64_t)wk * ROWB + fc * 16;
-        rows_left = (int)(A.m - row0 < 64 ? A.m - row0 : 64);
-    };
-    if (fg < C.groups) fetch_from();
-    uint32_t to[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * RS + fr;
-        to[i] = ring + r * ROWB + ((fc ^ (CH == 8 ? r & 7 : (r >> 1) & 3)) << 4);
-    }
-    const int64_t down = RS * A.q_stride;
+    int fs = wk, slot = 0;
     auto fetch = [&]() {
         if (fg < C.groups) {
-            const int rest = (int)bytes - fs * ROWB - fc * 16;
-            const int most = rest >= 16 ? 16 : rest > 0 ? rest : 0;
-            const uint8_t *p = fp;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int take = i * RS < rows_left ? most : 0;
-                cp16(to[i] + slot * STAGE, take ? p : A.q, take);
-                p += down;
+            if (elected()) {
+                bar_expect(bar + 8 * slot, STAGE);
+                stage_load(ring + slot * STAGE, &map, fs * ROWB, (int)((fg * wrs + wr) * (16 * RT)), bar + 8 * slot);
             }
             fs += C.wk;
-            fp += C.wk * ROWB;
             if (fs >= C.steps) {
                 fs = wk;
                 fg += gridDim.x;
-                if (fg < C.groups) fetch_from();
             }
         }
         slot = slot + 1 == STAGES ? 0 : slot + 1;
-        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // Scales and zero points of a stage: those of word j of a row are in lane
-    // j % 4 of the row's four, set j / 4; of each row tile rows g and g + 8.
+    // Scales and zero points, of rows g and g + 8 of a row tile, lie in the four
+    // lanes that share those rows and two sets of registers.
+    //   FINE: of one stage; word j in lane j % 4, set j / 4 (RT = 1) or of row
+    //   tile `set` (RT = 2);
+    //   else a stage has one group (RT = 2) or two (RT = 1, its halves), and they
+    //   are read for four of the warp's stages at once: stage k in lane k, set =
+    //   row tile; or in lane 2 (k % 2) + half, set k / 2.
     // (Offsets fit 32 bits: the launch sees to it.)
-    S sn[2][2];
+    constexpr int ROUND = FINE ? 1 : 4;
+    float sn[2][2];
     uint32_t zn[2][2], so[2][2], zo[2][2];
     auto constants_from = [&](int64_t grp) {
         const int64_t row0 = (grp * wrs + wr) * (16 * RT) + g;
@@ -290,33 +293,42 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
     auto constants = [&](int st) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            int gi = (st * STEP + 32 * (t4 + (RT == 1 ? 4 * i : 0))) >> C.shift;
+            const int col = FINE      ? st * STEP + 32 * (t4 + (RT == 1 ? 4 * i : 0))
+                            : RT == 2 ? (st + t4 * C.wk) * STEP
+                                      : (st + (2 * i + (t4 >> 1)) * C.wk) * STEP + 128 * (t4 & 1);
+            int gi = col >> C.shift;
             gi = gi < last_group ? gi : last_group;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                sn[i][h] = ((const S *)A.scales)[so[i][h] + (uint32_t)gi];
+                if (S16) {
+                    const uint16_t u = ((const uint16_t *)A.scales)[so[i][h] + (uint32_t)gi];
+                    sn[i][h] = __uint_as_float(u);
+                } else {
+                    sn[i][h] = ((const float *)A.scales)[so[i][h] + (uint32_t)gi];
+                }
                 zn[i][h] = A.zeros ? A.zeros[zo[i][h] + (uint32_t)gi] : 8u;
             }
         }
     };
     // x of a phase: piece (32-column block, column of B, quarter) at
     // [block][column][quarter], 16 bytes each
-    auto place = [&](int i, int quarters, const uint4 (&v)[P::parts]) {
-        const int tok = i / quarters, k = i - tok * quarters;
-#pragma unroll
-        for (int p = 0; p < P::parts; ++p) xs[((k >> 2) * cols + tok * P::parts + p) * 4 + (k & 3)] = v[p];
-    };
     auto stage_x = [&](int p0, int p1) {
-        const int quarters = (p1 - p0) * (STEP / 8), all = quarters * tokens;
-        for (int i = threadIdx.x; i < all; i += 2 * MMA_NT) {
-            uint4 v[2][P::parts];
+        const int quarters = (p1 - p0) * (STEP / 8);
+        for (int k = threadIdx.x; k < quarters; k += MMA_NT) {
+            uint4 *to = xs + (k >> 2) * cols * 4 + (k & 3);
+            const T *from = x;
+            for (int tok = 0; tok < tokens; tok += 2) {
+                uint4 v[2][P::parts];
+                lay_out(from, (int64_t)p0 * STEP + 8 * k, A.n, wide, v[0]);
+                if (tok + 1 < tokens) lay_out(from + A.x_stride, (int64_t)p0 * STEP + 8 * k, A.n, wide, v[1]);
+                from += 2 * A.x_stride;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int at = i + k * MMA_NT < all ? i + k * MMA_NT : i, tok = at / quarters;
-                lay_out(x + tok * A.x_stride, (int64_t)p0 * STEP + 8 * (at - tok * quarters), A.n, wide, v[k]);
+                for (int p = 0; p < P::parts; ++p) {
+                    to[4 * p] = v[0][p];
+                    if (tok + 1 < tokens) to[4 * (P::parts + p)] = v[1][p];
+                }
+                to += 8 * P::parts;
             }
-            place(i, quarters, v[0]);
-            if (i + MMA_NT < all) place(i + MMA_NT, quarters, v[1]);
         }
     };
 #pragma unroll
@@ -325,7 +337,6 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
         constants_from(blockIdx.x);
         constants(wk);
     }
-    if (threadIdx.x < 8) none[threadIdx.x] = make_uint4(0, 0, 0, 0);
 
     // this lane's pieces of B: column 8 c + g of each block, or zeros
     uint32_t step_b[NT], from[NT];
@@ -336,10 +347,16 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
         step_b[c] = in ? cols * 64 : 0;
     }
 
+    uint32_t at_word[WORDS];                                                 // of this lane's word of each 32 columns in a stage
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j) at_word[j] = g * ROWB + 4 * t4 + ((j ^ (RT == 1 ? g : g >> 1 & 3)) << 4);
     int use = 0;
-    bool have = false;
+    uint32_t parity = 0;
+    bool have = false, ok = true;
     for (int64_t grp = blockIdx.x; grp < C.groups; grp += gridDim.x) {
-        float tot[RT][NT][4] = {};
+        float tot[RT][NT][4] = {}, sc[2][2];
+        uint32_t zc[2][2];
+        int turn = 0;
         for (int p0 = 0; p0 < C.steps; p0 += C.phase) {
             const int p1 = p0 + C.phase < C.steps ? p0 + C.phase : C.steps;
             if (!have || C.phase < C.steps) {
@@ -350,76 +367,80 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
             }
             // phases are whole turns of the warps, so turns go on across them
             for (int st = p0 + wk; st < p1; st += C.wk) {
-                float sc[2][2];
-                uint32_t zc[2][2];
+                if (FINE || (turn & 3) == 0) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        sc[i][h] = to_f32(sn[i][h]);
-                        zc[i][h] = H::magic + (zn[i][h] & 127u) * H::one;
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t u = __float_as_uint(sn[i][h]);
+                            sc[i][h] = !S16 ? sn[i][h] : C.bf16_scales ? __uint_as_float(u << 16) : __half2float(__ushort_as_half((uint16_t)u));
+                            zc[i][h] = H::magic + (zn[i][h] & 127u) * H::one;
+                        }
+                    if (st + ROUND * C.wk < C.steps) {
+                        constants(st + ROUND * C.wk);
+                    } else if (grp + gridDim.x < C.groups) {
+                        constants_from(grp + gridDim.x);
+                        constants(wk);
                     }
-                fetch();
-                if (st + C.wk < C.steps) {
-                    constants(st + C.wk);
-                } else if (grp + gridDim.x < C.groups) {
-                    constants_from(grp + gridDim.x);
-                    constants(wk);
                 }
-                asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-                __syncwarp();
-                const uint32_t w = ring + use * STAGE + g * ROWB + 4 * t4;
-                use = use + 1 == STAGES ? 0 : use + 1;
+                const int k4 = turn++ & 3;
+                fetch();
+                ok = ok && bar_wait(bar + 8 * use, parity, &stop);
+                const uint32_t w = ring + use * STAGE;
+                if (++use == STAGES) {
+                    use = 0;
+                    parity ^= 1;
+                }
                 uint32_t bx[NT];
 #pragma unroll
                 for (int c = 0; c < NT; ++c) bx[c] = from[c] + (st - p0) * WORDS * step_b[c];
-                float part[RT][NT][4];
-                uint32_t za[RT], zb[RT];
+                float part[RT][NT][4] = {};
+                uint32_t za[RT] = {}, zb[RT] = {};
 #pragma unroll
                 for (int j = 0; j < WORDS; ++j) {
-                    const int src = (lane & ~3) | (j & 3);
+                    const int src = (lane & ~3) | (FINE ? j & 3 : RT == 2 ? k4 : 2 * (k4 & 1) + (j >> 2));
                     uint4 b[NT];
 #pragma unroll
                     for (int c = 0; c < NT; ++c) {
                         b[c] = ld16(bx[c]);
                         bx[c] += step_b[c];
                     }
-                    const bool begins = j == 0 || (j & (per - 1)) == 0, ends = j == WORDS - 1 || ((j + 1) & (per - 1)) == 0;
+                    const bool begins = FINE ? (j & (per - 1)) == 0 : (j & 3) == 0, ends = FINE ? ((j + 1) & (per - 1)) == 0 : (j & 3) == 3;
                     if (begins) {
 #pragma unroll
                         for (int r = 0; r < RT; ++r) {
-                            const int i = RT == 1 ? j >> 2 : r;
-                            za[r] = __shfl_sync(~0u, zc[i][0], src);
-                            zb[r] = __shfl_sync(~0u, zc[i][1], src);
+                            const bool second = FINE ? j >> 2 : RT == 1 ? k4 >> 1 : false;
+                            za[r] = __shfl_sync(~0u, RT == 2 ? zc[r][0] : second ? zc[1][0] : zc[0][0], src);
+                            zb[r] = __shfl_sync(~0u, RT == 2 ? zc[r][1] : second ? zc[1][1] : zc[0][1], src);
 #pragma unroll
                             for (int c = 0; c < NT; ++c)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) part[r][c][e] = 0.f;
                         }
                     }
-                    const int o = (j ^ (CH == 8 ? g : g >> 1 & 3)) << 4;
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        const uint32_t wa = ld4(w + r * 16 * ROWB + o), wb = ld4(w + (r * 16 + 8) * ROWB + o);
+                        const uint32_t wa = ld4(w + at_word[j] + r * 16 * ROWB), wb = ld4(w + at_word[j] + (r * 16 + 8) * ROWB);
                         uint32_t a[4];
-                        a[0] = H::sub((wa & 0x000f000fu) | H::magic, za[r]);
-                        a[1] = H::sub((wb & 0x000f000fu) | H::magic, zb[r]);
-                        a[2] = H::sub((wa >> 4 & 0x000f000fu) | H::magic, za[r]);
-                        a[3] = H::sub((wb >> 4 & 0x000f000fu) | H::magic, zb[r]);
+                        a[0] = H::sub(nibbles(wa, magic), za[r]);
+                        a[1] = H::sub(nibbles(wb, magic), zb[r]);
+                        a[2] = H::sub(nibbles(wa >> 4, magic), za[r]);
+                        a[3] = H::sub(nibbles(wb >> 4, magic), zb[r]);
 #pragma unroll
                         for (int c = 0; c < NT; ++c) H::mma(part[r][c], a, b[c].x, b[c].y);
-                        a[0] = H::sub((wa >> 8 & 0x000f000fu) | H::magic, za[r]);
-                        a[1] = H::sub((wb >> 8 & 0x000f000fu) | H::magic, zb[r]);
-                        a[2] = H::sub((wa >> 12 & 0x000f000fu) | H::magic, za[r]);
-                        a[3] = H::sub((wb >> 12 & 0x000f000fu) | H::magic, zb[r]);
+                        a[0] = H::sub(nibbles(wa >> 8, magic), za[r]);
+                        a[1] = H::sub(nibbles(wb >> 8, magic), zb[r]);
+                        a[2] = H::sub(nibbles(wa >> 12, magic), za[r]);
+                        a[3] = H::sub(nibbles(wb >> 12, magic), zb[r]);
 #pragma unroll
                         for (int c = 0; c < NT; ++c) H::mma(part[r][c], a, b[c].z, b[c].w);
                     }
                     if (ends) {
 #pragma unroll
                         for (int r = 0; r < RT; ++r) {
-                            const int i = RT == 1 ? j >> 2 : r;
-                            const float sa = __shfl_sync(~0u, sc[i][0], src), sb = __shfl_sync(~0u, sc[i][1], src);
+                            const bool second = FINE ? j >> 2 : RT == 1 ? k4 >> 1 : false;
+                            const float sa = __shfl_sync(~0u, RT == 2 ? sc[r][0] : second ? sc[1][0] : sc[0][0], src);
+                            const float sb = __shfl_sync(~0u, RT == 2 ? sc[r][1] : second ? sc[1][1] : sc[0][1], src);
 #pragma unroll
                             for (int c = 0; c < NT; ++c) {
                                 tot[r][c][0] = fmaf(sa, part[r][c][0], tot[r][c][0]);
@@ -433,6 +454,9 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
                 __syncwarp();
             }
         }
+        if (!ok)
+#pragma unroll
+            for (int e = 0; e < RT * NT * 4; ++e) (&tot[0][0][0])[e] = nanf("");
         if (C.wk == 1 && P::parts == 1) {
             // the warp has its rows' whole sums
 #pragma unroll
@@ -475,24 +499,25 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C)
         }
         __syncthreads();
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-constexpr int SMEM_MAX = 227 * 1024;
+constexpr int SMEM_MAX = 226 * 1024;      // (and the barriers)
 
-template <class T, class S, int NT, int RT>
-dbs_status launch_mma(const W4 &A, cudaStream_t s)
+template <class T, bool S16, int NT, int RT, bool FINE>
+dbs_status launch_mma(const W4 &A, dbs_dtype sd, const CUtensorMap &map, cudaStream_t s)
 {
     constexpr int parts = Piece<T>::parts, pass = NT * 8 / parts, STEP = STEP_V<RT>;
     constexpr int ring = MMA_W * STAGES * STAGE + 128, red = MMA_W * RT * 16 * NT * 8 * 4;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(k_w4_mma<T, S, NT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess) {
+        cudaFuncSetAttribute(k_w4_mma<T, S16, NT, RT, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess) {
         cudaGetLastError();
         return DBS_ERR_CUDA;
     }
     Cut C{};
     C.steps = (int)((A.n + STEP - 1) / STEP);
+    C.bf16_scales = sd == DBS_BF16;
+    C.magic = Half2<typename Piece<T>::type>::magic;
     while (1 << C.shift < A.group) ++C.shift;
     const int step_bytes = STEP * (int)((A.tokens < pass ? A.tokens : pass) * parts) * 2;
     // Warps per row tile: the time of a block, counted in instructions of a
@@ -502,7 +527,7 @@ dbs_status launch_mma(const W4 &A, cudaStream_t s)
     double best = 0;
     int smem = 0;
     for (int wk = 1; wk <= MMA_W; wk *= 2) {
-        const int room = SMEM_MAX - ring - (wk > 1 || parts > 1 ? red : 0);
+        const int room = SMEM_MAX - 1024 - ring - (wk > 1 || parts > 1 ? red : 0);
         int phase = room / step_bytes;
         if (phase >= C.steps) phase = C.steps;
         else phase = phase / wk * wk;
@@ -517,7 +542,7 @@ dbs_status launch_mma(const W4 &A, cudaStream_t s)
             C.wk = wk;
             C.phase = phase;
             C.groups = groups;
-            smem = ring + (wk > 1 || parts > 1 ? red : 0) + phase * step_bytes;
+            smem = 1024 + ring + (wk > 1 || parts > 1 ? red : 0) + phase * step_bytes;
         }
     }
     const int64_t grid = C.groups < sms ? C.groups : sms;
@@ -528,20 +553,47 @@ dbs_status launch_mma(const W4 &A, cudaStream_t s)
         B.x = (const T *)A.x + p * pass * A.x_stride;
         B.y = (T *)A.y + p * pass * A.y_stride;
         B.tokens = A.tokens - p * pass;
-        k_w4_mma<T, S, NT, RT><<<dim3((unsigned)grid, (unsigned)now), MMA_NT, smem, s>>>(B, C);
+        k_w4_mma<T, S16, NT, RT, FINE><<<dim3((unsigned)grid, (unsigned)now), MMA_NT, smem, s>>>(B, C, map);
     }
     return launched();
 }
 
+// The weights as rows of bytes, in stages of `columns` bytes of `rows` rows.
+bool make_map(const W4 &A, int columns, int rows, CUtensorMap &map)
+{
+    const encode_tiled_fn encode = encode_tiled();
+    const int64_t bytes = (A.n + 1) / 2, stride = A.m == 1 ? (bytes + 15) / 16 * 16 : A.q_stride;
+    if (!encode || stride < bytes || stride >= int64_t(1) << 40) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)A.m}, strides[1] = {(cuuint64_t)stride};
+    const cuuint32_t box[2] = {(cuuint32_t)columns, (cuuint32_t)rows}, ones[2] = {1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(A.q), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  columns == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, bool S16, int NT, int RT>
+dbs_status launch_tiles(const W4 &A, dbs_dtype sd, const CUtensorMap &map, cudaStream_t s)
+{
+    return A.group < 128 ? launch_mma<T, S16, NT, RT, true>(A, sd, map, s) : launch_mma<T, S16, NT, RT, false>(A, sd, map, s);
+}
+
+template <class T, bool S16>
+dbs_status launch_cols(const W4 &A, dbs_dtype sd, const CUtensorMap &map, cudaStream_t s)
+{
+    const int64_t cols = A.tokens * Piece<T>::parts;             // of B, in eights
+    return cols <= 8 ? launch_tiles<T, S16, 1, 1>(A, sd, map, s) : cols <= 16 ? launch_tiles<T, S16, 2, 2>(A, sd, map, s)
+           : cols <= 24 ? launch_tiles<T, S16, 3, 2>(A, sd, map, s) : launch_tiles<T, S16, 4, 2>(A, sd, map, s);
+}
+
 template <class T, class S>
-dbs_status launch(const W4 &A, cudaStream_t s)
+dbs_status launch(const W4 &A, dbs_dtype sd, cudaStream_t s)
 {
     constexpr int64_t LIMIT = int64_t(1) << 32;
-    if (A.n > 0 && aligned16(A.q) && (A.q_stride & 15) == 0 && (A.m + 1) * A.scale_stride < LIMIT && (A.m + 1) * A.zero_stride < LIMIT) {
-        const int64_t cols = A.tokens * Piece<T>::parts;         // of B, in eights
-        return cols <= 8 ? launch_mma<T, S, 1, 1>(A, s) : cols <= 16 ? launch_mma<T, S, 2, 2>(A, s)
-               : cols <= 24 ? launch_mma<T, S, 3, 2>(A, s) : launch_mma<T, S, 4, 2>(A, s);
-    }
+    CUtensorMap map;
+    const bool one = A.tokens * Piece<T>::parts <= 8;
+    if (A.n > 0 && aligned16(A.q) && (A.q_stride & 15) == 0 && (A.m + 1) * A.scale_stride < LIMIT && (A.m + 1) * A.zero_stride < LIMIT &&
+        make_map(A, one ? 128 : 64, one ? 16 : 32, map))
+        return launch_cols<T, sizeof(S) == 2>(A, sd, map, s);
     const int64_t chunks = (A.tokens + ROWS_TOK - 1) / ROWS_TOK;
     const dim3 grid((unsigned)((A.m + ROWS_NT / 32 - 1) / (ROWS_NT / 32)), (unsigned)(chunks < 65535 ? chunks : 65535));
     k_w4_rows<T, S><<<grid, ROWS_NT, 0, s>>>(A);
@@ -551,7 +603,7 @@ dbs_status launch(const W4 &A, cudaStream_t s)
 template <class T>
 dbs_status launch_scales(const W4 &A, dbs_dtype sd, cudaStream_t s)
 {
-    return sd == DBS_F32 ? launch<T, float>(A, s) : sd == DBS_F16 ? launch<T, __half>(A, s) : launch<T, __nv_bfloat16>(A, s);
+    return sd == DBS_F32 ? launch<T, float>(A, sd, s) : sd == DBS_F16 ? launch<T, __half>(A, sd, s) : launch<T, __nv_bfloat16>(A, sd, s);
 }
 
 }  // namespace
