@@ -1486,11 +1486,8 @@ dbs_status plan_of(const dbs_attention_args &a, Plan &P)
              !aligned8(a.q_token) || !aligned8(a.q_head) || !aligned8(a.k_page) || !aligned8(a.k_entry) ||
              !aligned8(a.k_head) || !aligned8(a.v_page) || !aligned8(a.v_entry) || !aligned8(a.v_head);
     if (P.rows) return DBS_OK;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return DBS_ERR_CUDA;
-    }
+    const int sms = multiprocessors();
+    if (sms == 0) return DBS_ERR_CUDA;
     P.dp = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256;
     // up to 16 rows of a kv head fit one instruction of k_attn_few, which reads
     // the cache once for each 16
@@ -1548,10 +1545,8 @@ dbs_status launch_join(const Attn &A, const Plan &P, cudaStream_t s)
 template <class T, int DP>
 dbs_status launch_few(const Attn &A, const Plan &P, cudaStream_t s)
 {
-    if (cudaFuncSetAttribute(k_attn_few<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem<DP>()) != cudaSuccess) {
-        cudaGetLastError();
-        return DBS_ERR_CUDA;
-    }
+    static Once once;
+    if (!room_for(once, k_attn_few<T, DP>, few_smem<DP>())) return DBS_ERR_CUDA;
     k_attn_few<T, DP><<<P.blocks, FEW_NT, few_smem<DP>(), s>>>(A, P.share);
     const dbs_status st = launched();
     return st == DBS_OK ? launch_join<T>(A, P, s) : st;
@@ -1590,10 +1585,8 @@ template <class T, int DP, int TILES, bool BOXES>
 dbs_status launch_kind(const Attn &A, const Plan &P, const Maps &maps, cudaStream_t s)
 {
     using M = Many<DP, TILES>;
-    if (cudaFuncSetAttribute(k_attn_many<T, DP, TILES, BOXES>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::SMEM) != cudaSuccess) {
-        cudaGetLastError();
-        return DBS_ERR_CUDA;
-    }
+    static Once once;
+    if (!room_for(once, k_attn_many<T, DP, TILES, BOXES>, M::SMEM)) return DBS_ERR_CUDA;
     k_attn_many<T, DP, TILES, BOXES><<<P.blocks, M::NT, M::SMEM, s>>>(A, P.share, maps);
     const dbs_status st = launched();
     return st == DBS_OK ? launch_join<T>(A, P, s) : st;

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/dbspmspv.h"
 
 namespace dbs::ops {
@@ -114,6 +116,40 @@ inline encode_tiled_fn encode_tiled()
 
 inline bool dtype_ok(int32_t d) { return d == DBS_F32 || d == DBS_F16 || d == DBS_BF16; }
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Multiprocessors of the current device; 0 if there is none.
+inline int multiprocessors()
+{
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+// Room for a kernel's dynamic shared memory, asked for once on a device (noted when
+// it is there, so that another thread's launch never comes before it).
+using Once = std::atomic<uint64_t>;
+template <class K> inline bool room_for(Once &once, K kernel, int bytes)
+{
+    int dev = 0;
+    const bool known = cudaGetDevice(&dev) == cudaSuccess && dev < 64;
+    const uint64_t bit = uint64_t(known) << (dev & 63);
+    if (once.load(std::memory_order_acquire) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    once.fetch_or(bit, std::memory_order_release);
+    return true;
+}
 
 // Status of the launches since the last check.
 inline dbs_status launched() { return cudaGetLastError() == cudaSuccess ? DBS_OK : DBS_ERR_CUDA; }

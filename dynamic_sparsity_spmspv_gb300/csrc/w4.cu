@@ -508,12 +508,9 @@ dbs_status launch_mma(const W4 &A, dbs_dtype sd, const CUtensorMap &map, cudaStr
 {
     constexpr int parts = Piece<T>::parts, pass = NT * 8 / parts, STEP = STEP_V<RT>;
     constexpr int ring = MMA_W * STAGES * STAGE + 128, red = MMA_W * RT * 16 * NT * 8 * 4;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(k_w4_mma<T, S16, NT, RT, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess) {
-        cudaGetLastError();
-        return DBS_ERR_CUDA;
-    }
+    static Once once;
+    const int sms = multiprocessors();
+    if (sms == 0 || !room_for(once, k_w4_mma<T, S16, NT, RT, FINE>, SMEM_MAX)) return DBS_ERR_CUDA;
     Cut C{};
     C.steps = (int)((A.n + STEP - 1) / STEP);
     C.bf16_scales = sd == DBS_BF16;

@@ -562,7 +562,7 @@ typedef struct {
     int64_t out_stride;
     int64_t batch, vocab;      /* batch < 2^16, vocab < 2^31 - 8192 */
     const int32_t *history;    /* device [batch, history_max], rows history_stride apart */
-    int64_t history_max, history_stride;   /* history_max < 2^30 */
+    int64_t history_max, history_stride;   /* history_max < 2^29 */
     const int32_t *history_lens;  /* device [batch], clamped to [0, history_max]; NULL = history_max */
     const int32_t *prompt_lens;   /* device [batch]; NULL = 0: everything is output */
     const float *repetition, *presence, *frequency;   /* device [batch] each, or NULL */

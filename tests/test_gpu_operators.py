@@ -520,7 +520,10 @@ def logits_ref(x, hist, hl, pl, rep, pres, freq, ids, vals, allowed):
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("B,V,L,NB,mask", [(1, 1, 1, 0, False), (1, 32000, 700, 16, True), (3, 4097, 33, 5, True), (2, 1000, 0, 3, False),
                                            (5, 50021, 9000, 300, True), (17, 333, 100, 0, True), (2, 12288, 2000, 64, False),
-                                           (1, 100003, 20011, 0, False), (70, 5000, 64, 7, True)])
+                                           (1, 100003, 20011, 0, False), (70, 5000, 64, 7, True),
+                                           # more rows than run at once: slices of other widths, ranks instead of words
+                                           (310, 5001, 200, 9, True), (311, 7, 30, 3, False), (64, 40003, 3001, 40, True),
+                                           (30, 90007, 20011, 0, True), (31, 90001, 9000, 300, False), (320, 1031, 0, 0, True)])
 def test_penalize_logits(dt, B, V, L, NB, mask):
     rng = np.random.default_rng(V + L)
     x = rnd(rng, dt, B, V) * 4
