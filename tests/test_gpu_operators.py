@@ -13,7 +13,9 @@ rounded to: 2^-24 fp32, 2^-11 fp16, 2^-8 bf16):
              1.6e-4 at 256 for N(0,1) inputs), twice (numerator and sum)
   logits     8 * 2^-24 times the sum of the magnitudes that meet, + u |y|
 """
+import importlib.util
 import math
+import os
 
 import numpy as np
 import pytest
@@ -664,3 +666,17 @@ def test_refusals_of_shapes_and_types(call):
     with pytest.raises(dbs.DbsError) as e:
         call()
     assert e.value.status == 1
+
+
+def test_example_of_drafted_steps():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "draft_step.py")
+    spec = importlib.util.spec_from_file_location("draft_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    text, got, steps, logits, got_logits = example.main(24)
+    assert steps < 24
+    # logits of order 1 from some ten roundings to 2^-11 of them, each by its own order of sums; where two of them are as
+    # near as that, the texts may part
+    same = next((i for i, (a, b) in enumerate(zip(text, got)) if a != b), 24)
+    assert (logits - got_logits)[:same + 1].abs().max() < 0.05
+    assert same == 24 or (logits[same, text[same]] - logits[same, got[same]]).abs() < 0.1
