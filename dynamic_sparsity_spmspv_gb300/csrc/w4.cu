@@ -2,6 +2,8 @@
 // (dbs_w4_linear, sm_103a):
 //     y[t, i] = sum_g s[i, g] * sum_{j in g} x[t, j] (q[i, j] - z[i, g]).
 #include "ops_dev.h"
+#include "tc_dev.h"
+#include <type_traits>
 
 using namespace dbs::ops;
 
@@ -131,19 +133,28 @@ __device__ __forceinline__ void stage_load(uint32_t dst, const CUtensorMap *map,
                  "r"(bar), "r"(byte), "r"(row) : "memory");
 }
 
-// Eight neighbouring values of x as the pairs (0, 4), (1, 5), (2, 6), (3, 7).
+// Eight neighbouring values of x, zeros behind the row's end, and the same as the
+// pairs (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __noinline__ uint4 eight_by_one(const uint16_t *x, int64_t j, int64_t n)
+{
+    uint16_t v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = j + e < n ? x[j + e] : (uint16_t)0;
+    return make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16, v[4] | (uint32_t)v[5] << 16, v[6] | (uint32_t)v[7] << 16);
+}
+template <class T>
+__device__ __forceinline__ uint4 eight(const T *x, int64_t j, int64_t n, bool wide)
+{
+    return wide && j + 8 <= n ? *(const uint4 *)(x + j) : eight_by_one((const uint16_t *)x, j, n);
+}
+__device__ __forceinline__ uint4 paired(uint4 u)
+{
+    return make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632));
+}
 template <class T>
 __device__ __forceinline__ void lay_out(const T *x, int64_t j, int64_t n, bool wide, uint4 (&out)[1])
 {
-    uint16_t v[8];
-    if (wide && j + 8 <= n) {
-        const uint4 u = *(const uint4 *)(x + j);
-        *(uint4 *)v = u;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = j + e < n ? *(const uint16_t *)(x + j + e) : (uint16_t)0;
-    }
-    out[0] = make_uint4(v[0] | (uint32_t)v[4] << 16, v[1] | (uint32_t)v[5] << 16, v[2] | (uint32_t)v[6] << 16, v[3] | (uint32_t)v[7] << 16);
+    out[0] = paired(eight(x, j, n, wide));
 }
 
 // The same of fp32: the upper 8 bits of each value, the next 8, the last 8, each
@@ -555,6 +566,402 @@ dbs_status launch_mma(const W4 &A, dbs_dtype sd, const CUtensorMap &map, cudaStr
     return launched();
 }
 
+// ---- many rows and several tokens: tcgen05 ----
+//
+// 128 rows of codes and N columns of x (tokens) on the fifth-generation tensor
+// cores: the codes' numbers, made as above, go from registers into tensor memory (a
+// row a lane, two numbers a column), x into shared memory in the 128-byte swizzle,
+// and the sums of each group, in tensor memory, come back to be scaled in fp32.
+// Warps have roles: two or three fours make numbers, half a chunk of 256 columns at
+// a time; four scale (a thread a row); four bring x's columns into the order of the
+// numbers, in place; one fetches codes and one x, by tiled copies; one issues the
+// products.  Fours of warps that need few registers leave theirs to those that scale.
+//
+// 24 tokens, 128000 x 4096: 91 us, against 144 with k_w4_mma, whose warps spend their
+// instructions on fragments of x.  A block's chunk takes 0.8 us, of which memory
+// would take 0.4: the chain of the products' issue and the scaling of their sums
+// bounds it (half of the issue slots are used).
+template <int N> struct Many {
+    static constexpr int MG = N == 32 ? 3 : 2;                               // fours of warps that make numbers
+    static constexpr int XS = MG, RA = 2 * MG, WS = 6;                // stages: of x, of numbers (half a chunk), of codes
+    static constexpr int CODES = 128 * 128, X = N * 512;                     // bytes of a stage
+    static constexpr int SCALE = 4 * MG, LAY = SCALE + 4, FETCH = LAY + 4, ISSUE = FETCH + 2, NT = 32 * (FETCH + 4);
+    // registers of a thread: at launch, and after the fours of warps have shared them out
+    static constexpr int REGS = MG == 3 ? 80 : 96, FEW = 56, SOME = 64, MANY = REGS + (REGS - FEW) + (REGS - SOME);
+    static constexpr int SUMS = 0, NUMBERS = 4 * N;                          // columns of tensor memory
+    static constexpr int SMEM = 1024 + WS * CODES + XS * X;
+};
+template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+static_assert(Many<32>::NUMBERS + Many<32>::RA * 64 <= 512 && Many<64>::NUMBERS + Many<64>::RA * 64 <= 512, "tensor memory");
+
+struct Walk {
+    int steps, shift;          // chunks of a row; log2 of the group
+    int passes;                // of N tokens
+    int units;                 // of 128 rows and N tokens; a block takes every gridDim.x-th, or
+    int split;                 // so many blocks, a cluster, one, a part of its columns each
+    int scales;                // their type
+};
+
+template <class T, int N>
+__global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap xmap)
+{
+    using M = Many<N>;
+    using H = Half2<T>;
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(8) uint64_t bars[2 * M::WS + 3 * M::XS + 2 * M::RA + 5];
+    __shared__ uint32_t tmem_at;
+    __shared__ int stop;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t codes = smem_addr(raw) + (-smem_addr(raw) & 1023u), xs = codes + M::WS * M::CODES;
+    const uint32_t w_full = smem_addr(bars), w_empty = w_full + 8 * M::WS, x_full = w_empty + 8 * M::WS, x_empty = x_full + 8 * M::XS;
+    const uint32_t a_full = x_empty + 8 * M::XS, a_empty = a_full + 8 * M::RA, d_full = a_empty + 8 * M::RA, d_empty = d_full + 16;
+    const uint32_t x_here = d_empty + 16, last_bar = x_here + 8 * M::XS;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < M::WS; ++i) {
+            bar_init(w_full + 8 * i, 1);
+            bar_init(w_empty + 8 * i, 8);
+        }
+        for (int i = 0; i < M::XS; ++i) {
+            bar_init(x_full + 8 * i, 128);
+            bar_init(x_empty + 8 * i, 1);
+            bar_init(x_here + 8 * i, 1);
+        }
+        for (int i = 0; i < M::RA; ++i) {
+            bar_init(a_full + 8 * i, 4);
+            bar_init(a_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(d_full + 8 * i, 1);
+            bar_init(d_empty + 8 * i, 4);
+        }
+        bar_init(last_bar, 1);
+        stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == M::ISSUE) tc_alloc(smem_addr(&tmem_at));
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = tmem_at;
+    const int last_group = (int)((A.n - 1) >> C.shift);
+    const int rank = (int)blockIdx.x % C.split, first = (int)blockIdx.x / C.split;
+    const int c0 = C.steps * rank / C.split;                                 // of the first unit; the launch sees that all chunks fit an int
+    const int chunks = C.split > 1 ? C.steps * (rank + 1) / C.split - c0 : (C.units - first + (int)gridDim.x - 1) / (int)gridDim.x * C.steps;
+
+    // The unit and chunk (or group) that a role is at; a unit's row tile and pass.
+    struct At {
+        int unit, tile, pass, at;
+    };
+    auto begin = [&](int each) { return At{first, first / C.passes, first % C.passes, c0 * each}; };        // each: a chunk's share of `at`
+    auto step = [&](At &p, int of) {
+        if (++p.at < of) return;
+        p.at = 0;
+        p.unit += gridDim.x;
+        p.tile = p.unit / C.passes;
+        p.pass = p.unit - p.tile * C.passes;
+    };
+
+    // All threads of the cluster.
+    auto meet = [&] {
+        asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+    };
+
+    if (warp < M::SCALE) {
+        // ---- numbers: a thread has a row's 128 codes of half a chunk, the halves in turns ----
+        const int r = threadIdx.x & 127;
+        const int parts = C.shift == 5 ? 4 : C.shift == 6 ? 2 : 1;           // groups among them
+        At ahead = begin(2);                                                 // (in halves)
+        auto skip = [&](int by) {
+            ahead.at += by;
+            while (ahead.at >= 2 * C.steps) {
+                ahead.at -= 2 * C.steps;
+                ahead.unit += gridDim.x;
+                ahead.tile = ahead.unit / C.passes;
+            }
+        };
+        uint32_t zn[4] = {8, 8, 8, 8};                                       // zero points of the next half
+        auto zero_points = [&] {
+            if (A.zeros && ahead.unit < C.units) {
+                const int64_t row = (int64_t)ahead.tile * 128 + r;
+                const uint8_t *from = A.zeros + (row < A.m ? row : A.m - 1) * A.zero_stride;
+                const int g = ahead.at * 128 >> C.shift;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < parts) zn[i] = from[g + i < last_group ? g + i : last_group];
+            }
+            skip(M::MG);
+        };
+        skip(warp >> 2);
+        zero_points();
+        const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + M::NUMBERS;
+        int ws = warp >> 3, as = warp >> 2;
+        uint32_t wp = 0, ap = 1;
+        bool ok = true;
+#pragma unroll 1
+        for (int u = warp >> 2; u < 2 * chunks && ok; u += M::MG) {
+            uint32_t z[4];                                                   // as numbers, of 32 codes each
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = H::magic + ((parts == 4 ? zn[i] : parts == 2 ? zn[i >> 1] : zn[0]) & 127u) * H::one;
+            zero_points();
+            ok = ok && __all_sync(~0u, bar_wait(w_full + 8 * ws, wp, &stop));
+            const int half = u & 1;
+            uint4 q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = ld16(codes + ws * M::CODES + r * 128 + (((half * 4 + i) ^ (r & 7)) << 4));
+            __syncwarp();
+            if (lane == 0) bar_arrive(w_empty + 8 * ws);
+            ws += ((u + M::MG) >> 1) - (u >> 1);
+            if (ws >= M::WS) {
+                ws -= M::WS;
+                wp ^= 1;
+            }
+            ok = ok && __all_sync(~0u, bar_wait(a_empty + 8 * as, ap, &stop));
+            if (!ok) break;
+            tc_after();
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                uint32_t out[32];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t w[4] = {q[2 * p + i].x, q[2 * p + i].y, q[2 * p + i].z, q[2 * p + i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) out[16 * i + 4 * e + b] = H::sub(nibbles(w[e] >> 4 * b, H::magic), z[2 * p + i]);
+                }
+                tc_st(to + as * 64 + 32 * p, out);
+            }
+            tc_wait_st();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(a_full + 8 * as);
+            if ((as += M::MG) >= M::RA) {
+                as -= M::RA;
+                ap ^= 1;
+            }
+        }
+    } else if (warp < M::LAY) {
+        // ---- groups' sums, scaled: a thread has a row ----
+        more_registers<M::MANY>();
+        // (a set of sums: two neighbouring groups, or one of 256 columns)
+        const int r = threadIdx.x & 127, two = C.shift < 8 ? 2 : 1, of = C.steps * (256 >> C.shift) / two;
+        At ahead = begin(of / C.steps), now = ahead;
+        auto row_of = [&](const At &p) {
+            const int64_t row = (int64_t)p.tile * 128 + r;
+            return row < A.m ? row : A.m - 1;
+        };
+        int64_t from = row_of(ahead) * A.scale_stride;
+        uint32_t sn[2] = {};                                                 // scales of the next set
+        auto scales = [&] {
+            if (ahead.unit < C.units) {
+                if (ahead.at == 0) from = row_of(ahead) * A.scale_stride;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int g = ahead.at * two + i;
+                    if (i < two && g <= last_group) sn[i] = C.scales == DBS_F32 ? ((const uint32_t *)A.scales)[from + g] : ((const uint16_t *)A.scales)[from + g];
+                    else sn[i] = 0;                                          // (behind the row's end, where the sums are 0)
+                }
+            }
+            step(ahead, of);
+        };
+        scales();
+        float acc[N] = {};
+        bool ok = true;
+        const int all = chunks * (of / C.steps);
+        auto store = [&](const At &p) {
+            const int64_t row = (int64_t)p.tile * 128 + r, t0 = (int64_t)p.pass * N;
+            T *y = (T *)A.y + t0 * A.y_stride + row;
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                if (t0 + t < A.tokens && row < A.m) *y = from_f32<T>(ok ? acc[t] * H::unit : nanf(""));
+                y += A.y_stride;
+            }
+        };
+#pragma unroll 1
+        for (int g = 0; g < all; ++g) {
+            ok = ok && __all_sync(~0u, bar_wait(d_full + 8 * (g & 1), g >> 1 & 1, &stop));
+            if (ok) {
+                tc_after();
+                const uint32_t sums = tmem + ((uint32_t)(warp & 3) << 21) + M::SUMS + (g & 1) * (2 * N);
+                uint32_t part[32];
+                tc_ld_begin(part, sums);
+                float f[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) f[i] = C.scales == DBS_F32 ? __uint_as_float(sn[i]) : C.scales == DBS_BF16 ? __uint_as_float(sn[i] << 16) : __half2float(__ushort_as_half((uint16_t)sn[i]));
+                scales();
+#pragma unroll
+                for (int t = 0; t < 2 * N; t += 32) {
+                    if (t == N && two == 1) break;
+                    tc_ld_end(part);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) acc[t % N + e] = fmaf(f[t / N], __uint_as_float(part[e]), acc[t % N + e]);
+                    if (t + 32 < 2 * N && (two == 2 || t + 32 < N)) tc_ld_begin(part, sums + t + 32);
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(d_empty + 8 * (g & 1));
+            }
+            if (C.split == 1 && now.at == of - 1) {
+                store(now);
+#pragma unroll
+                for (int t = 0; t < N; ++t) acc[t] = 0.f;
+            }
+            step(now, of);
+        }
+        if (C.split > 1) {
+            // the parts of the columns, in order, in the first block's shared memory
+            meet();
+            const uint32_t at = codes + r * 16;
+            if (!ok)
+#pragma unroll
+                for (int t = 0; t < N; ++t) acc[t] = nanf("");
+            if (rank > 0) {
+                uint32_t to;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(at + (rank - 1) * (N * 512)));
+#pragma unroll
+                for (int t = 0; t < N; t += 4)
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(to + t * 512), "f"(acc[t]), "f"(acc[t + 1]), "f"(acc[t + 2]),
+                                 "f"(acc[t + 3]) : "memory");
+            }
+            meet();
+            if (rank == 0) {
+                for (int i = 0; i < C.split - 1; ++i)
+#pragma unroll
+                    for (int t = 0; t < N; t += 4) {
+                        const uint4 v = ld16(at + i * (N * 512) + t * 512);
+                        acc[t] += __uint_as_float(v.x);
+                        acc[t + 1] += __uint_as_float(v.y);
+                        acc[t + 2] += __uint_as_float(v.z);
+                        acc[t + 3] += __uint_as_float(v.w);
+                    }
+                store(begin(0));
+            }
+        }
+    } else if (warp < M::FETCH) {
+        // ---- x: pairs of its columns in their places ----
+        fewer_registers<M::SOME>();
+        int st = 0;
+        uint32_t parity = 0;
+        bool ok = true;
+        for (int n = 0; n < chunks && ok; ++n) {
+            ok = __all_sync(~0u, bar_wait(x_here + 8 * st, parity, &stop));
+            if (!ok) break;
+            const uint32_t at = xs + st * M::X + (threadIdx.x & 127) * 16;
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < N / 4; i += 8) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = ld16(at + (i + e) * 2048);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint4 u = paired(v[e]);
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (i + e) * 2048), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
+                }
+            }
+            async_fence();
+            bar_arrive(x_full + 8 * st);
+            if (++st == M::XS) {
+                st = 0;
+                parity ^= 1;
+            }
+        }
+    } else if (fewer_registers<M::FEW>(), warp < M::ISSUE) {
+        // ---- fetch: one warp codes, one x; tiled copies a chunk ----
+        const bool is_x = warp > M::FETCH;
+        const int stages = is_x ? M::XS : M::WS, bytes = is_x ? M::X : M::CODES;
+        const uint32_t full = is_x ? x_here : w_full, empty = is_x ? x_empty : w_empty, store = is_x ? xs : codes;
+        At p = begin(1);
+        int st = 0;
+        uint32_t parity = 1;
+        for (int n = 0; n < chunks; ++n) {
+            if (!__all_sync(~0u, bar_wait(empty + 8 * st, parity, &stop))) break;
+            if (elected()) {
+                bar_expect(full + 8 * st, bytes);
+                if (is_x) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) stage_load(store + st * bytes + i * (N * 128), &xmap, p.at * 256 + 64 * i, p.pass * N, full + 8 * st);
+                } else {
+                    stage_load(store + st * bytes, &map, p.at * 128, p.tile * 128, full + 8 * st);
+                }
+            }
+            __syncwarp();
+            step(p, C.steps);
+            if (++st == stages) {
+                st = 0;
+                parity ^= 1;
+            }
+        }
+    } else if (warp == M::ISSUE) {
+        // ---- products ----
+        constexpr uint32_t FMT = __is_same(T, __nv_bfloat16) ? 1u : 0u;
+        constexpr uint32_t DESC = 1u << 4 | FMT << 7 | FMT << 10 | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
+        int q = 0;
+        bool ok = true;
+        // LEN: instructions of a group, at most those of half a chunk.  A turn goes
+        // once through all stages of x and of numbers, so that the descriptors are
+        // sums of constants.  (Tensor memory begins at 0: the block has all of it.)
+        auto issue = [&](auto length) {
+            constexpr int LEN = decltype(length)::value;
+            uint32_t turn = 0;
+            for (int n0 = 0; n0 < chunks && ok; n0 += M::XS, turn ^= 1) {
+#pragma unroll
+                for (int u = 0; u < 2 * M::XS; ++u) {
+                    const int half = u & 1;
+                    if (n0 + u / 2 >= chunks) break;
+                    if (half == 0) ok = ok && __all_sync(~0u, bar_wait(x_full + 8 * (u / 2), turn, &stop));
+                    ok = ok && __all_sync(~0u, bar_wait(a_full + 8 * u, turn, &stop));
+                    const uint32_t lo = (xs + u / 2 * M::X + half * (2 * N * 128)) >> 4 | 1u << 16, a = M::NUMBERS + u * 64;
+                    uint64_t b[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) b[k] = desc_of(lo + ((k >> 2) * (N * 128) + (k & 3) * 32) / 16);
+#pragma unroll
+                    for (int k0 = 0; k0 < 8; k0 += LEN) {
+                        // the group's place in its set, and whether the set begins or ends here
+                        const bool second = LEN == 8 ? half == 1 && C.shift < 8 : k0 / LEN & 1;
+                        const bool begins = LEN == 8 ? half == 0 : !second, ends = LEN == 8 ? half == 1 : second;
+                        if (begins) ok = ok && __all_sync(~0u, bar_wait(d_empty + 8 * (q & 1), (q >> 1 & 1) ^ 1, &stop));
+                        if (!ok) break;
+                        tc_after();
+                        const uint32_t d = M::SUMS + (q & 1) * (2 * N) + (second ? N : 0), full = d_full + 8 * (q & 1);
+                        const bool more = LEN == 8 && half == 1 && !second;  // (a group of 256 goes on)
+                        if (elected()) {
+#pragma unroll
+                            for (int k = k0; k < k0 + LEN; ++k) tc_mma_ts(d, a + 8 * k, b[k], DESC, k > k0 || more);
+                            if (ends) tc_commit(full);
+                            if (k0 + LEN == 8) {
+                                tc_commit(a_empty + 8 * u);
+                                if (half == 1) tc_commit(x_empty + 8 * (u / 2));
+                            }
+                        }
+                        if (ends) ++q;
+                        __syncwarp();
+                    }
+                }
+            }
+        };
+        if (C.shift >= 7) issue(std::integral_constant<int, 8>());
+        else if (C.shift == 6) issue(std::integral_constant<int, 4>());
+        else issue(std::integral_constant<int, 2>());
+        // the instructions under way, before tensor memory is given back
+        if (elected()) tc_commit(last_bar);
+        __syncwarp();
+        bar_wait(last_bar, 0, &stop);
+    }
+    if (C.split > 1 && (warp < M::SCALE || warp >= M::LAY)) {
+        __syncwarp();
+        meet();
+        meet();
+    }
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    if (warp == M::ISSUE) {
+        tc_after();
+        tc_free(tmem);
+    }
+}
+
 // The weights as rows of bytes, in stages of `columns` bytes of `rows` rows.
 bool make_map(const W4 &A, int columns, int rows, CUtensorMap &map)
 {
@@ -566,6 +973,70 @@ bool make_map(const W4 &A, int columns, int rows, CUtensorMap &map)
     return encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(A.q), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   columns == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// x (of 16 bits) in boxes of 64 columns of `rows` tokens.
+bool make_x_map(const W4 &A, int rows, CUtensorMap &map)
+{
+    const encode_tiled_fn encode = encode_tiled();
+    const int64_t stride = A.tokens == 1 ? (2 * A.n + 15) / 16 * 16 : 2 * A.x_stride;
+    if (!encode || !aligned16(A.x) || (stride & 15) != 0 || stride < 2 * A.n || stride >= int64_t(1) << 40) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)A.n, (cuuint64_t)A.tokens}, strides[1] = {(cuuint64_t)stride};
+    const cuuint32_t box[2] = {64, (cuuint32_t)rows}, ones[2] = {1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(A.x), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// From 13 tokens of 16-bit x on, where x's rows are on 16-byte boundaries.  Fewer,
+// where k_w4_mma takes two matrix instructions for a fragment, cost it less or the
+// same (12 tokens, 32000 x 4096: 42 and 50 us; 16 tokens: 48 and 50; 24 tokens: 72
+// and 50; 4096 x 11008: 27 and 21, 42 and 21, 103 and 21).
+constexpr int64_t MANY_TOKENS = 12;
+
+struct Tall {
+    CUtensorMap codes, x;
+    Walk walk;
+};
+// How such a call is cut up; false if it does not fit.
+template <int N>
+bool plan_many(const W4 &A, dbs_dtype sd, int sms, Tall &t)
+{
+    const int64_t passes = (A.tokens + N - 1) / N, units = (A.m + 127) / 128 * passes, steps = (A.n + 255) / 256;
+    // (counts of groups of 32 columns of a block, and of columns, are ints)
+    if (passes >= int64_t(1) << 31 || units >= int64_t(1) << 31 || (units / sms + 1) * steps >= int64_t(1) << 27) return false;
+    if (!make_map(A, 128, 128, t.codes) || !make_x_map(A, N, t.x)) return false;
+    t.walk = {(int)steps, 0, (int)passes, (int)units, 1, sd};
+    while (1 << t.walk.shift < A.group) ++t.walk.shift;
+    // few units: blocks of a cluster share one's columns (4096 x 11008, 24 tokens: 21
+    // us with four, 40 with one)
+    while (t.walk.split < (N == 32 ? 8 : 4) && units * 2 * t.walk.split <= sms && steps >= 4 * t.walk.split) t.walk.split *= 2;
+    return true;
+}
+template <class T, int N>
+dbs_status launch_many(const W4 &A, const Tall &t, int sms, cudaStream_t s)
+{
+    // (a block's fours of warps share out the registers that it starts with, so there
+    // have to be that many, or their waits for them would not end)
+    static const bool shares = [] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, k_w4_many<T, N>) == cudaSuccess && f.numRegs == Many<N>::REGS;
+    }();
+    static Once once;
+    if (!shares || !room_for(once, k_w4_many<T, N>, Many<N>::SMEM)) return DBS_ERR_CUDA;
+    const Walk &w = t.walk;
+    cudaLaunchConfig_t how{};
+    how.gridDim = dim3((unsigned)(w.split > 1 ? w.units * w.split : w.units < sms ? w.units : sms));
+    how.blockDim = dim3(Many<N>::NT);
+    how.dynamicSmemBytes = Many<N>::SMEM;
+    how.stream = s;
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = (unsigned)w.split;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    how.attrs = &cluster;
+    how.numAttrs = 1;
+    cudaLaunchKernelEx(&how, k_w4_many<T, N>, A, w, t.codes, t.x);
+    return launched();
 }
 
 template <class T, bool S16, int NT, int RT>
@@ -586,9 +1057,18 @@ template <class T, class S>
 dbs_status launch(const W4 &A, dbs_dtype sd, cudaStream_t s)
 {
     constexpr int64_t LIMIT = int64_t(1) << 32;
+    const bool rows16 = A.n > 0 && aligned16(A.q) && (A.q_stride & 15) == 0;
+    if constexpr (sizeof(T) == 2)
+        if (rows16 && A.tokens > MANY_TOKENS) {
+            Tall t;
+            const int sms = multiprocessors();
+            if (sms == 0) return DBS_ERR_CUDA;
+            if (A.tokens <= 32 && plan_many<32>(A, sd, sms, t)) return launch_many<T, 32>(A, t, sms, s);
+            if (A.tokens > 32 && plan_many<64>(A, sd, sms, t)) return launch_many<T, 64>(A, t, sms, s);
+        }
     CUtensorMap map;
     const bool one = A.tokens * Piece<T>::parts <= 8;
-    if (A.n > 0 && aligned16(A.q) && (A.q_stride & 15) == 0 && (A.m + 1) * A.scale_stride < LIMIT && (A.m + 1) * A.zero_stride < LIMIT &&
+    if (rows16 && (A.m + 1) * A.scale_stride < LIMIT && (A.m + 1) * A.zero_stride < LIMIT &&
         make_map(A, one ? 128 : 64, one ? 16 : 32, map))
         return launch_cols<T, sizeof(S) == 2>(A, sd, map, s);
     const int64_t chunks = (A.tokens + ROWS_TOK - 1) / ROWS_TOK;

@@ -140,6 +140,41 @@ def test_w4_infinities_stay_with_their_token():
     close(y[3:4], big, 1e-5 * bm)
 
 
+@pytest.mark.parametrize("dt,sd", [("f16", "f32"), ("bf16", "bf16"), ("bf16", "f16"), ("f16", "f16")])
+@pytest.mark.parametrize("T,m,n,group,zeros", [
+    (13, 128, 256, 128, True), (17, 129, 2051, 64, True), (32, 1, 4096, 256, False), (33, 640, 1000, 32, True), (64, 130, 3001, 128, True),
+    (65, 257, 513, 32, False), (24, 19461, 300, 64, True), (200, 1000, 777, 256, True), (31, 2500, 5000, 32, True), (40, 300, 1, 64, True)])
+def test_w4_of_several_tokens(dt, sd, T, m, n, group, zeros):
+    """Rows and tokens in tiles, columns shared out among blocks or not; x's rows on and off 16-byte boundaries."""
+    rng = np.random.default_rng(T + m + n + group)
+    x, q, s, z = w4_inputs(rng, T, m, n, dt, sd, group, zeros)
+    ref, mag = w4_ref(x, q, s, z, group)
+    bound = 1e-5 * mag + U[dt] * np.abs(ref) + ETA[dt] + 1e-30
+    for pad, at in ((-n % 8 + 8, 0), (-n % 8 + 9, 1)):
+        wide = torch.full((T, n + pad), NAN, dtype=x.dtype, device=DEV)
+        wide[:, at:at + n] = x
+        out = torch.full((T, m + 3), 7.0, dtype=x.dtype, device=DEV)
+        y = dbs.w4_linear(wide[:, at:at + n], q, s, z, group=group, y=out[:, :m])
+        close(y, ref, bound)
+        assert (out[:, m:] == 7).all()
+        assert torch.equal(y, dbs.w4_linear(wide[:, at:at + n], q, s, z, group=group))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_w4_infinities_stay_with_their_token_among_several(dt):
+    rng = np.random.default_rng(7)
+    x, q, s, z = w4_inputs(rng, 20, 200, 600, dt, "f32", 64, True)
+    ref, mag = w4_ref(x, q, s, z, 64)
+    x[3, 100], x[11, 599] = INF, NAN
+    y = dbs.w4_linear(x, q, s, z, group=64)
+    rest = [t for t in range(20) if t not in (3, 11)]
+    close(y[rest], ref[rest], 1e-5 * mag[rest] + U[dt] * np.abs(ref[rest]) + ETA[dt])
+    w = np.stack([f64(q) % 16, f64(q) // 16], -1).reshape(200, -1)[:, 100] - (f64(z)[:, 100 // 64] % 128)
+    assert torch.isnan(y[11]).all()
+    got = f64(y[3])
+    assert (np.isnan(got) == (w == 0)).all() and (got[w > 0] == INF).all() and (got[w < 0] == -INF).all()
+
+
 def test_w4_exact_on_whole_numbers():
     """Small whole x and power-of-two scales: every sum is exact in fp32."""
     rng = np.random.default_rng(6)
