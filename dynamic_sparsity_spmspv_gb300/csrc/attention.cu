@@ -573,6 +573,7 @@ constexpr int FEW_ROWS = 16;               // one matrix instruction's rows
 constexpr int FEW_STEP = 16;               // entries of a stage of a warp
 constexpr int FEW_KEYS = FEW_W * FEW_STEP;
 constexpr int FEW_STAGES = 3;
+constexpr int FEW_SPLIT = 16;      // blocks of a cluster, at most
 
 template <int DP> constexpr int few_smem() { return FEW_W * FEW_STAGES * 2 * FEW_STEP * DP * 2; }
 
@@ -582,8 +583,12 @@ template <int DP> constexpr int few_smem() { return FEW_W * FEW_STAGES * 2 * FEW
 // a unit.  A maximum is replaced only when it grew by more than 2^8, so the
 // output is hardly ever rescaled (probabilities stay below 2^8, exact in
 // proportion).
-template <class T, int DP>
-__global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
+//
+// Two ways to share out the work: pieces of the line (CLUSTER = false), or, for few
+// units, the blocks of a cluster for each, which take equal parts of its entries and
+// join them through their shared memory, in the same launch.
+template <class T, int DP, bool CLUSTER>
+__global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
 {
     const dbs_attention_args &a = A.a;
     extern __shared__ __align__(128) unsigned char ring[];
@@ -591,18 +596,38 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
     __shared__ Near near;
     __shared__ float s_m[FEW_W][FEW_ROWS], s_l[FEW_W][FEW_ROWS];
     __shared__ int s_odd[FEW_W];
+    __shared__ float j_m[CLUSTER ? FEW_ROWS : 1], j_l[CLUSTER ? FEW_ROWS : 1];                 // of the block's rows, for the cluster
+    __shared__ int j_odd;
     constexpr int RB = DP * 2, CH = DP / 8, HALF = FEW_STEP * RB;   // bytes and 16-byte chunks of an entry; of a stage's K
     constexpr int KK = DP / 16, NN = DP / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
     unsigned char *mine = ring + warp * (FEW_STAGES * 2 * HALF);
+    // a row's joined sums, in the ring of the warp that joins it, behind that warp's own
+    auto joined = [&](int r) { return r % FEW_W * (FEW_STAGES * 2 * HALF) + (FEW_ROWS + r / FEW_W) * DP * 4; };
+    static_assert((FEW_ROWS + FEW_ROWS / FEW_W) * DP * 4 <= FEW_STAGES * 2 * HALF, "room behind a warp's sums");
     const uint32_t base = smem_addr(mine);
     const int chunks = a.head_dim / 8;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // (the join waits for this grid's end)
-    Walk walk = start<FEW_NT>(A, S, red, near);
+    const int rank = CLUSTER ? (int)(blockIdx.x % split) : 0;
+    Walk walk;
     Segment seg;
+    if constexpr (CLUSTER) {
+        const uint32_t unit = blockIdx.x / split, per = (uint32_t)a.kv_heads * S.groups, u = unit % per;
+        seg.b = unit / per;
+        seg.hk = (int)(u / S.groups);
+        seg.group = (int)(u % S.groups);
+        seg.s = sequence(A, seg.b);
+        const int n = tiles_of(S, seg.s);
+        seg.j0 = (int)((int64_t)n * rank / split) * S.keys;
+        seg.j1 = (int)((int64_t)n * (rank + 1) / split) * S.keys;
+        seg.j1 = seg.j1 < seg.s.kv ? seg.j1 : seg.s.kv;
+        seg.whole = false;
+    } else {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the join waits for this grid's end)
+        walk = start<FEW_NT>(A, S, red, near);
+    }
     {
-        while (walk.next(A, S, near, seg)) {
-            if (threadIdx.x == 0) walk.record(A, S, seg);
+        while (CLUSTER || walk.next(A, S, near, seg)) {
+            if (!CLUSTER && threadIdx.x == 0) walk.record(A, S, seg);
             const Seq &s = seg.s;
             const int64_t b = seg.b;
             const int hk = seg.hk, j0 = seg.j0, j1 = seg.j1;
@@ -769,7 +794,7 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
             __syncthreads();
             const bool whole = seg.whole;
             odd = (s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3]) != 0;
-            float *part = slot_of(A, S, blockIdx.x, seg.slot);
+            float *part = CLUSTER ? nullptr : slot_of(A, S, blockIdx.x, seg.slot);
             for (int r = warp; r < FEW_ROWS; r += FEW_W) {
                 const Row row = row_of(A, hk, R0 + r);
                 if (!row.inside) break;
@@ -784,7 +809,14 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
 #pragma unroll
                     for (int e = 0; e < DP / 32; ++e) oo[e] += f == 0.f ? 0.f : f * po[lane + 32 * e];
                 }
-                if (whole) {
+                if (CLUSTER) {
+#pragma unroll
+                    for (int e = 0; e < DP / 32; ++e) ((float *)(ring + joined(r)))[lane + 32 * e] = oo[e];
+                    if (lane == 0) {
+                        j_m[r] = top;
+                        j_l[r] = sum;
+                    }
+                } else if (whole) {
                     if (row.t >= s.tree) {
                         sum = 0.f;
                     } else if (odd) {
@@ -806,6 +838,57 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S)
                         if (r == 0) part[(int64_t)FEW_ROWS * a.head_dim + 2 * FEW_ROWS] = odd;
                     }
                 }
+            }
+            if constexpr (CLUSTER) {
+                if (threadIdx.x == 0) j_odd = odd;
+                asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+                // 32 columns of a row for each of the cluster's warps in turn
+                auto from = [&](const void *p, int block) {
+                    uint32_t at;
+                    float v;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(block));
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+                    return v;
+                };
+                const int64_t left = (int64_t)a.tokens * A.group - R0;
+                const int rows = (int)(left < FEW_ROWS ? left : FEW_ROWS);
+                for (int i = rank * FEW_W + warp; i < rows * (DP / 32); i += split * FEW_W) {
+                    const int r = i / (DP / 32), e0 = i % (DP / 32);
+                    const Row row = row_of(A, hk, R0 + r);
+                    const bool in = lane < split;
+                    const float m = in ? from(j_m + r, lane) : -INFINITY;
+                    float l = in ? from(j_l + r, lane) : 0.f;
+                    const bool found = in && __float_as_int(from(&j_odd, lane)) != 0;
+                    float v[FEW_SPLIT], o = 0.f, top = m;
+#pragma unroll
+                    for (int k = 0; k < FEW_SPLIT; ++k) v[k] = k < split ? from((const float *)(ring + joined(r)) + lane + 32 * e0, k) : 0.f;
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                    const float f = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2f(m - top);
+                    l = f == 0.f ? 0.f : f * l;
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+#pragma unroll
+                    for (int k = 0; k < FEW_SPLIT; ++k) {
+                        const float fk = __shfl_sync(~0u, f, k);
+                        o += fk == 0.f ? 0.f : fk * v[k];
+                    }
+                    if (row.t >= s.tree) {
+                        l = 0.f;
+                    } else if (__any_sync(~0u, found)) {
+                        Eight w;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w.v[e] = e == e0 ? o : 0.f;
+                        w = add_odd<T>(A, b, row.t, hk, w);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o = e == e0 ? w.v[e] : o;
+                    }
+                    if (lane + 32 * e0 < a.head_dim) ((T *)a.out + b * a.o_batch + row.t * a.o_token + row.h * a.o_head)[lane + 32 * e0] = from_f32<T>(l == 0.f ? 0.f : o / l);
+                    if (a.lse && e0 == 0 && lane == 0) a.lse[(b * a.tokens + row.t) * a.q_heads + row.h] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+                }
+                // (no block ends while another one reads its shared memory)
+                asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+                break;
             }
             __syncthreads();       // the rings are free again
         }
@@ -1397,6 +1480,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
 struct Plan {
     bool rows, many;           // any alignment; 128 rows at a time
     int dp, blocks;
+    int split;                 // blocks of a cluster for each unit of few rows; 0: pieces of the line
     Share share;
     int64_t slots, scratch;    // bytes of scratch: the slots, and all
 };
@@ -1435,6 +1519,22 @@ dbs_status plan_of(const dbs_attention_args &a, Plan &P)
     S.last = P.many ? (int)((rows - (int64_t)(S.groups - 1) * S.rows + 127) / 128) : 1;
     const int64_t most = a.batch * a.kv_heads * S.groups * (entries < S.keys ? 1 : (entries + S.keys - 1) / S.keys);
     P.blocks = (int)(most < sms * per_sm ? most : sms * per_sm);
+    // Few units of few rows: a cluster for each, as large as all find room at once,
+    // instead of a second launch that joins the line's pieces (one token, 8 kv heads:
+    // 2000 entries 11 and 14 us, 8192 entries 17 and 20; four sequences of 2000: 14 and
+    // 20).  Where a block would have 2048 entries or more the line's even pieces are
+    // faster (32768 entries: 44 and 40 us).  Blocks that fill an SM make clusters of
+    // sixteen hard to place (head_dim 256, 3000 entries: 24 us, of eight 19).
+    const int64_t units = a.batch * a.kv_heads * S.groups;
+    if (!P.many) {
+        int c = 1;
+        while (c < (per_sm == 1 ? 8 : FEW_SPLIT) && units * 2 * c <= sms * per_sm) c *= 2;
+        if (c > 1 && entries < (int64_t)c * 2048) {
+            P.split = c;
+            P.blocks = (int)(units * c);
+            return DBS_OK;
+        }
+    }
     P.slots = (int64_t)P.blocks * 2 * slot_floats(S.rows, a.head_dim) * 4;
     P.scratch = P.slots + a.batch * a.kv_heads * S.groups * (int64_t)sizeof(int4);
     return DBS_OK;
@@ -1471,9 +1571,25 @@ dbs_status launch_join(const Attn &A, const Plan &P, cudaStream_t s)
 template <class T, int DP>
 dbs_status launch_few(const Attn &A, const Plan &P, cudaStream_t s)
 {
-    static Once once;
-    if (!room_for(once, k_attn_few<T, DP>, few_smem<DP>())) return DBS_ERR_CUDA;
-    k_attn_few<T, DP><<<P.blocks, FEW_NT, few_smem<DP>(), s>>>(A, P.share);
+    static Once once, once_cluster;
+    if (P.split) {
+        if (!room_for(once_cluster, k_attn_few<T, DP, true>, few_smem<DP>(), true)) return DBS_ERR_CUDA;
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3((unsigned)P.blocks);
+        c.blockDim = FEW_NT;
+        c.dynamicSmemBytes = few_smem<DP>();
+        c.stream = s;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = (unsigned)P.split;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        c.attrs = &at;
+        c.numAttrs = 1;
+        cudaLaunchKernelEx(&c, k_attn_few<T, DP, true>, A, P.share, P.split);
+        return launched();
+    }
+    if (!room_for(once, k_attn_few<T, DP, false>, few_smem<DP>())) return DBS_ERR_CUDA;
+    k_attn_few<T, DP, false><<<P.blocks, FEW_NT, few_smem<DP>(), s>>>(A, P.share, 0);
     const dbs_status st = launched();
     return st == DBS_OK ? launch_join<T>(A, P, s) : st;
 }

@@ -134,16 +134,18 @@ inline int multiprocessors()
     if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
-// Room for a kernel's dynamic shared memory, asked for once on a device (noted when
+// Room for a kernel's dynamic shared memory, and leave for clusters of more than eight
+// blocks, asked for once on a device (noted when
 // it is there, so that another thread's launch never comes before it).
 using Once = std::atomic<uint64_t>;
-template <class K> inline bool room_for(Once &once, K kernel, int bytes)
+template <class K> inline bool room_for(Once &once, K kernel, int bytes, bool large_clusters = false)
 {
     int dev = 0;
     const bool known = cudaGetDevice(&dev) == cudaSuccess && dev < 64;
     const uint64_t bit = uint64_t(known) << (dev & 63);
     if (once.load(std::memory_order_acquire) & bit) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+        (large_clusters && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)) {
         cudaGetLastError();
         return false;
     }

@@ -399,7 +399,8 @@ ATTN = [(1, 1, 1, 1, 64, 1, 0), (1, 1, 8, 8, 128, 5, 0), (1, 1, 32, 8, 128, 2001
         (3, 16, 8, 1, 64, 130, 24), (2, 33, 4, 4, 96, 513, 64), (5, 3, 10, 2, 256, 77, 7), (4, 64, 8, 1, 128, 700, 256),
         (1, 64, 16, 2, 256, 190, 16), (7, 12, 12, 4, 128, 1000, 1), (2, 100, 2, 2, 64, 400, 16), (2, 7, 6, 3, 80, 129, 0),
         (2, 9, 4, 2, 36, 150, 5), (3, 4, 2, 1, 33, 65, 0), (1, 1, 5, 5, 1, 9, 0), (40, 1, 16, 4, 128, 260, 16),
-        (1, 200, 8, 2, 128, 333, 16), (1, 3, 71, 1, 128, 128, 64)]
+        (1, 200, 8, 2, 128, 333, 16), (1, 3, 71, 1, 128, 128, 64), (60, 2, 8, 4, 64, 300, 16), (170, 1, 8, 4, 64, 100, 16),
+        (24, 2, 16, 8, 128, 500, 64), (9, 3, 4, 4, 256, 500, 32), (40, 1, 8, 4, 256, 200, 16)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -474,6 +475,31 @@ def test_tree_attention_what_is_not_seen_takes_no_part(dt, T, hq, hk, D):
     if hk > 1:
         head = got[:, last, hq // hk:, 1]       # the second kv head's k is finite
         assert torch.isinf(head).all() and torch.equal(got[:, last, hq // hk:, 2:], clean[:, last, hq // hk:, 2:])
+
+
+@pytest.mark.parametrize("T,hq,hk,D", [(1, 8, 2, 128), (5, 4, 2, 128), (9, 8, 4, 64), (3, 2, 1, 256)])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_tree_attention_of_few_rows_with_room_for_a_long_text(dt, T, hq, hk, D):
+    """A page table for many more entries than there are: the work is shared out by the lengths."""
+    rng = np.random.default_rng(15)
+    B, S, page = 6, 900, 16
+    q, k, v, pages, kv, tl = attn_case(rng, dt, B, T, hq, hk, D, S, page)
+    pages = np.concatenate([pages, np.full((B, 4200), -5)], 1)
+    kv[:] = [0, 50, T, S, 1, 700]
+    tl[:] = [T, 0, T, T, T, 1]
+    bits = tree_bits(rng, B, T)
+    bits[2, T // 2] = 0
+    attn_check(dt, q, k, v, pages, kv, tl, bits, page)
+    table = dev(pages, np.int32)
+    clean = dbs.tree_attention(q, k, v, dev(kv), dev(bits.view(np.int64)), tree_lens=dev(tl), page_table=table)
+    e = S - 1                                   # seen by the last token alone
+    v[int(pages[3][e // page]), e % page, :, 0] = NAN
+    v[int(pages[3][e // page]), e % page, :, 1] = INF
+    got = dbs.tree_attention(q, k, v, dev(kv), dev(bits.view(np.int64)), tree_lens=dev(tl), page_table=table)
+    rest = [b for b in range(B) if b != 3]
+    assert torch.equal(got[rest], clean[rest]) and torch.equal(got[3, :T - 1], clean[3, :T - 1])
+    assert torch.isnan(got[3, T - 1, :, 0]).all() and torch.isinf(got[3, T - 1, :, 1]).all()
+    assert torch.equal(got[3, T - 1, :, 2:], clean[3, T - 1, :, 2:])
 
 
 def test_tree_attention_large_scores_and_views():
