@@ -201,7 +201,8 @@ __device__ __forceinline__ void store_row(const Attn &A, int64_t b, int t, int h
 constexpr int ROW_NT = 128;
 
 // Any head size and alignment: one block per query row, its warps take every
-// fourth entry.
+// fourth entry, a lane every 32nd value.  Every row reads the cache again, from L2
+// (one token, 32 heads, 2001 entries: 426 us; k_attn_few 10).
 template <class T>
 __global__ void __launch_bounds__(ROW_NT) k_attn_rows(Attn A)
 {
@@ -910,9 +911,19 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
 //
 // K and V come by tiled copies (TMA) of boxes of as many entries as divide a
 // page, eight at least; caches whose pages do not split into eights come by
-// 16-byte asynchronous copies, which reach about half of the memory's rate (a
-// batch of 16 trees over 2300 entries each: 57 us for 150 MB, an SM's copies in
-// flight being the limit).
+// 16-byte asynchronous copies, which reach about half of the memory's rate (an SM's
+// copies in flight are the limit).
+//
+// 16 trees of 12 tokens, 8 kv heads, 128 MB of caches: 53 us.  A tile of 128 entries
+// takes 1.15 us, less than its copy at the memory's rate; what is lost is the start
+// (9 us until the first scores, of which 4 the first copies) and 5 us for each of a
+// block's two or three units (masked tile, last product, output, first scores).
+// 4 trees of 48 tokens over 32768 entries, 384 rows to a kv head: 172 us, 31% of the
+// tensor cores' rate: 1.9 us for two row tiles against 128 entries, 1.15 of them
+// products; scores wait for the product that reads P from their columns.  What did
+// not help: tiles of 64 entries with two score buffers a row tile (177 us), a warp
+// of its own for each row tile's products (177), a share of the powers of two by
+// polynomial (186 to 247).
 //
 // Every wait has a limit; a block whose wait runs out stops and leaves NaN in
 // its rows.

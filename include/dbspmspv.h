@@ -437,7 +437,8 @@ typedef enum { DBS_F32 = 0, DBS_F16 = 1, DBS_BF16 = 2 } dbs_dtype;
  *   x       device, `dtype`, [tokens, n], rows x_stride apart
  *   q       device bytes, [m, ceil(n/2)], rows q_stride bytes apart: column 2c
  *           in the low half of byte c, column 2c + 1 in the high half.  Rows
- *           on 16-byte boundaries (q and q_stride) take the tensor-core path.
+ *           on 16-byte boundaries (q and q_stride) take the tensor-core paths,
+ *           and so should those of x, from 13 tokens of 16-bit x on.
  *   scales  device, scale_dtype, [m, ceil(n/group)], rows scale_stride apart
  *   zeros   device bytes, of which the low 7 bits count (0..127), the same shape,
  *           rows zero_stride apart; NULL = 8 everywhere
