@@ -584,7 +584,7 @@ dbs_status launch_mma(const W4 &A, dbs_dtype sd, const CUtensorMap &map, cudaStr
 // 24 tokens, 128000 x 4096: 91 us, against 144 with k_w4_mma, whose warps spend their
 // instructions on fragments of x.  A block's chunk takes 0.8 us, of which memory
 // would take 0.4: the chain of the products' issue and the scaling of their sums
-// bounds it (half of the issue slots are used).
+// bounds it (two thirds of the issue slots are used).
 template <int N> struct Many {
     static constexpr int MG = N == 32 ? 3 : 2;                               // fours of warps that make numbers
     static constexpr int XS = MG, RA = 2 * MG, WS = 6;                // stages: of x, of numbers (half a chunk), of codes
