@@ -901,13 +901,15 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
 // 128 query rows against tiles of entries on the fifth-generation tensor cores:
 // S = Q K^T and O += P V with both accumulators in tensor memory (a row per
 // lane), Q, K and V in shared memory in the 128-byte swizzle (K row by row, V
-// as it lies, its entries as the contraction's dimension), and P, rounded to
-// the caches' type, written over S for the second product.  Warps have roles:
-// two fetch K and V, two load Q, one issues the matrix instructions, two look
-// through the drafted part of V, and four for each 128 rows do the softmax, a
-// thread a row.  With two row tiles (TILES = 2) a tile of
-// K and V serves both, and the products of one run under the softmax of the
-// other; with one, the scores of the next tile of entries do.
+// as it lies, its entries as the contraction's dimension), and P rounded to the
+// caches' type.  Warps have roles: two fetch K and V, two load Q, one for each 128
+// rows issues the matrix instructions, two look through the drafted part of V, and
+// four for each 128 rows do the softmax, a thread a row.  S has two buffers, so the
+// scores of the next tile of entries are made under the softmax of one.
+// With one row tile P is written over S.  With two (TILES = 2), which share a tile
+// of K and V, tensor memory holds scores of 64 entries for each, P goes to shared
+// memory, so that scores wait for no product, and the warps that fetch and issue
+// leave registers to those of the softmax, which then read S once.
 //
 // K and V come by tiled copies (TMA) of boxes of as many entries as divide a
 // page, eight at least; caches whose pages do not split into eights come by
@@ -918,27 +920,32 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
 // takes 1.15 us, less than its copy at the memory's rate; what is lost is the start
 // (9 us until the first scores, of which 4 the first copies) and 5 us for each of a
 // block's two or three units (masked tile, last product, output, first scores).
-// 4 trees of 48 tokens over 32768 entries, 384 rows to a kv head: 172 us, 31% of the
-// tensor cores' rate: 1.9 us for two row tiles against 128 entries, 1.15 of them
-// products; scores wait for the product that reads P from their columns.  What did
-// not help: tiles of 64 entries with two score buffers a row tile (177 us), a warp
-// of its own for each row tile's products (177), a share of the powers of two by
-// polynomial (186 to 247).
+// 4 trees of 48 tokens over 32768 entries, 384 rows to a kv head: 169 us, 32% of the
+// tensor cores' rate; 1024 tokens over 8192 entries: 43%.  Two row tiles take 0.95 us
+// for 64 entries, 0.6 of them products: the softmax's own chain (scores, maximum,
+// powers, sum, stores) bounds it.  With P over S and tiles of 128 entries 173 us; P
+// over S and tiles of 64: 177; one warp issuing for both row tiles: 179.  A share of
+// the powers of two by polynomial made it slower (186 us and more).
 //
 // Every wait has a limit; a block whose wait runs out stops and leaves NaN in
 // its rows.
 
 template <int DP, int TILES> struct Many {
-    static constexpr int KEYS = DP == 256 ? 64 : 128;
-    static constexpr int STAGES = TILES == 1 && DP != 256 ? 3 : 2;        // of K, and of V
-    static constexpr int SB = TILES == 1 ? 2 : 1;                         // score buffers of a row tile
+    static constexpr int KEYS = DP == 256 || TILES == 2 ? 64 : 128;
+    static constexpr int STAGES = DP == 256 ? 2 : TILES == 2 ? 4 : 3;       // of K, and of V
+    static constexpr int SB = 2;                                          // score buffers of a row tile
     static constexpr int SUBQ = 128 * 128, SUBK = KEYS * 128;             // 64 columns of a tile, in bytes
-    static constexpr int Q = DP / 64 * SUBQ, KV = DP / 64 * SUBK;
-    static constexpr int NT = 32 * (4 * TILES + 4 + 1 + 2);
-    static constexpr int FETCH = 4 * TILES, LOAD = FETCH + 2, ISSUE = FETCH + 4, MEND = ISSUE + 1;   // first warps of the roles
+    static constexpr bool PS = TILES == 2;                                // P in shared memory, not over S
+    static constexpr int Q = DP / 64 * SUBQ, KV = DP / 64 * SUBK, P = PS ? 128 * KEYS * 2 : 0;
+    static constexpr int NT = 32 * (4 * TILES + 4 + TILES + 2);
+    static constexpr int FETCH = 4 * TILES, LOAD = FETCH + 2, ISSUE = FETCH + 4, MEND = ISSUE + TILES;   // first warps of the roles
+    // registers of a thread at launch (TILES = 2), and once the warps that fetch and
+    // issue have left some to those of the softmax, two fours of warps each
+    static constexpr int REGS = 128, FEW = 112, MANY = 2 * REGS - FEW;
     static constexpr int S_COL = 0, O_COL = TILES * SB * KEYS;
-    static constexpr int SMEM = TILES * Q + STAGES * 2 * KV + 1024;
+    static constexpr int SMEM = TILES * (Q + P) + STAGES * 2 * KV + 1024;
 };
+static_assert(!Many<128, 2>::PS || Many<128, 2>::KEYS == 64, "a row of P is a row of the swizzle");
 static_assert(Many<128, 2>::O_COL + 2 * 128 <= 512 && Many<256, 1>::O_COL + 256 <= 512, "tensor memory");
 
 // 32 bytes, a whole sector, at once.
@@ -974,26 +981,26 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
     extern __shared__ unsigned char raw[];
     __shared__ int64_t red[M::NT / 32];
     __shared__ Near near;
-    __shared__ __align__(8) uint64_t bars[6 * ST + TILES * (SB + 4) + 1];
+    __shared__ __align__(8) uint64_t bars[6 * ST + TILES * (SB + 5)];
     __shared__ uint32_t tmem_at;
     __shared__ int stop;
     __shared__ int odd_seg[8];                       // segments (their number + 1) whose V is not finite somewhere
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-    const uint32_t sq = base, sk = base + TILES * M::Q, sv = sk + ST * M::KV;
+    const uint32_t sq = base, sk = base + TILES * M::Q, sv = sk + ST * M::KV, sp = sv + ST * M::KV;
     const uint32_t bar0 = smem_addr(bars);
     const uint32_t k_full = bar0, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST;
     const uint32_t s_full = v_empty + 8 * ST, q_full = s_full + 8 * TILES * SB, p_ready = q_full + 8 * TILES, o_done = p_ready + 8 * TILES;
-    const uint32_t last_bar = o_done + 8 * TILES, v_fixed = last_bar + 8, v_odd = v_fixed + 8 * ST, q_empty = v_odd + 8 * ST;
+    const uint32_t last_bar = o_done + 8 * TILES, v_fixed = last_bar + 8 * TILES, v_odd = v_fixed + 8 * ST, q_empty = v_odd + 8 * ST;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // (the join waits for this grid's end)
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             bar_init(k_full + 8 * i, BOXES ? 1 : 32);
-            bar_init(k_empty + 8 * i, 1);
+            bar_init(k_empty + 8 * i, TILES);
             bar_init(v_full + 8 * i, BOXES ? 1 : 32);
             bar_init(v_fixed + 8 * i, 64);
             bar_init(v_odd + 8 * i, 1);
-            bar_init(v_empty + 8 * i, 1);
+            bar_init(v_empty + 8 * i, TILES);
         }
         for (int i = 0; i < TILES * SB; ++i) bar_init(s_full + 8 * i, 1);
         for (int i = 0; i < TILES; ++i) {
@@ -1001,8 +1008,8 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             bar_init(q_empty + 8 * i, 1);
             bar_init(p_ready + 8 * i, 128);
             bar_init(o_done + 8 * i, 1);
+            bar_init(last_bar + 8 * i, 1);
         }
-        bar_init(last_bar, 1);
         stop = 0;
         for (int i = 0; i < 8; ++i) odd_seg[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1024,7 +1031,181 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
     };
     Segment seg;
 
-    if (BOXES && warp >= M::FETCH && warp < M::FETCH + 2) {
+    if (warp < M::FETCH) {
+        // ---- softmax: a thread has a row ----
+        more_registers<TILES == 2 ? M::MANY : 0>();
+        const int r = warp >> 2, row = (warp & 3) * 32 + lane;             // row tile, row in it
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+        const uint32_t o_at = tmem + lanes + M::O_COL + r * DP;
+        int it = 0, number = 0;                                            // tiles done; segments
+        bool ok = true;
+        while (ok && walk.next(A, S, near, seg)) {
+            const int number_now = number++;
+            if (r >= tiles_in(seg)) continue;                              // the unit has one row tile: the other's barriers rest
+            const int64_t b = seg.b;
+            const Seq s = seg.s;
+            const Row me = row_of(A, seg.hk, (int64_t)seg.group * (128 * TILES) + r * 128 + row);
+            const bool busy = __any_sync(~0u, me.inside);
+            float m = -INFINITY, l = 0.f;
+            for (int t = 0; t < seg.tiles; ++t, ++it) {
+                const int buf = it & 1;
+                ok = __all_sync(~0u, bar_wait(s_full + 8 * (r * SB + buf), it >> 1 & 1, &stop));
+                if (!ok) break;
+                tc_after();
+                const uint32_t s_at = tmem + lanes + M::S_COL + (r * SB + buf) * KEYS;
+                const int j0 = seg.j0 + t * KEYS;
+                const bool masked = j0 + KEYS > s.first;
+                bool settled = t == 0;                                     // the product before this one is known to be in O
+                if (busy) {
+                    // 64 entries at a time; of more, read twice: first for the maximum, then for P
+                    // (loops kept rolled: the roles share the instruction cache)
+                    auto load = [&](float (&v)[64], int c) {
+                        tc_ld(v, s_at + 64 * c);
+                        if (masked) {
+                            const uint32_t lo = sees32(A, b, me.t, s.tree, j0 + 64 * c - s.first);
+                            const uint32_t hi = sees32(A, b, me.t, s.tree, j0 + 64 * c + 32 - s.first);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                v[e] = lo >> e & 1u ? v[e] : -INFINITY;
+                                v[e + 32] = hi >> e & 1u ? v[e + 32] : -INFINITY;
+                            }
+                        }
+                    };
+                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float v[64];
+#pragma unroll 1
+                    for (int c = 0; c < KEYS / 64; ++c) {
+                        load(v, c);
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) t4[e & 3] = fmaxf(t4[e & 3], v[e]);
+                    }
+                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * A.scale_log2;      // (scale > 0 here)
+                    // replace the maximum only when it grew by more than 2^8
+                    const bool grew = top > m + 8.f || (m == -INFINITY && top > m);
+                    if (__any_sync(~0u, grew)) {
+                        const float f = grew ? (m == -INFINITY ? 0.f : exp2f(m - top)) : 1.f;
+                        if (grew) m = top;
+                        l *= f;
+                        if (t > 0) {
+                            // the output so far, once the product before this one is in it
+                            ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
+                            if (!ok) break;
+                            settled = true;
+                            tc_after();
+#pragma unroll 1
+                            for (int c = 0; c < DP / 32; ++c) {
+                                float o[32];
+                                uint32_t w[32];
+                                tc_ld(o, o_at + 32 * c);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
+                                tc_st(o_at + 32 * c, w);
+                            }
+                            tc_wait_st();
+                        }
+                    }
+                    const float shift = m == -INFINITY ? 0.f : m;
+                    if (M::PS && !settled) {
+                        // P's place is free once the product before this one is done
+                        ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
+                        if (!ok) break;
+                        settled = true;
+                    }
+                    float l4[4] = {l, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int c = 0; c < KEYS / 64; ++c) {
+                        uint32_t w[32];
+                        if (KEYS > 64) load(v, c);
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) {
+                            v[e] = pow2(fmaf(v[e], A.scale_log2, -shift));
+                            l4[e & 3] += v[e];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) w[e] = pack2<T>(v[2 * e], v[2 * e + 1]);
+                        if constexpr (M::PS) {
+                            const uint32_t at = sp + r * M::P + row * 128;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((e ^ (row & 7)) << 4)), "r"(w[4 * e]), "r"(w[4 * e + 1]),
+                                             "r"(w[4 * e + 2]), "r"(w[4 * e + 3]) : "memory");
+                        } else {
+                            tc_st(s_at + 32 * c, w);
+                        }
+                    }
+                    l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    if constexpr (M::PS) async_fence();
+                    else tc_wait_st();
+                }
+                // (every phase of o_done is waited for while the next cannot end)
+                if (!settled) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
+                if (!ok) break;
+                tc_before();
+                bar_arrive(p_ready + 8 * r);
+            }
+            // the unit's (or the part's) output
+            if (ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
+            tc_after();
+            const bool odd = ok && *(volatile int *)&odd_seg[number_now & 7] == number_now + 1;
+            if (!busy) continue;
+            float *part = slot_of(A, S, blockIdx.x, seg.slot);
+            const int slot_row = r * 128 + row;
+            const bool none = me.t >= s.tree || l == 0.f;
+            const float fine = ok ? 1.f : nanf("");
+            const float by = seg.whole ? (none ? 0.f : 1.f / l) * fine : fine;
+            T *out = (T *)a.out + b * a.o_batch + me.t * a.o_token + me.h * a.o_head;
+#pragma unroll 1
+            for (int c = 0; c < DP / 32; ++c) {
+                float v[32];
+                tc_ld(v, o_at + 32 * c);
+                if (!me.inside) continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = seg.whole && none && ok ? 0.f : v[e] * by;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    const int d = 32 * c + e;
+                    if (d >= a.head_dim) break;
+                    if (!seg.whole) {
+                        store32(part + (int64_t)slot_row * a.head_dim + d, __float_as_uint(v[e]), __float_as_uint(v[e + 1]), __float_as_uint(v[e + 2]),
+                                __float_as_uint(v[e + 3]), __float_as_uint(v[e + 4]), __float_as_uint(v[e + 5]), __float_as_uint(v[e + 6]),
+                                __float_as_uint(v[e + 7]));
+                    } else if (A.wide_out) {
+                        *(uint4 *)(out + d) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]), pack2<T>(v[e + 4], v[e + 5]),
+                                                         pack2<T>(v[e + 6], v[e + 7]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) out[d + k] = from_f32<T>(v[e + k]);
+                    }
+                }
+            }
+            tc_before();
+            if (me.inside) {
+                if (!seg.whole) {
+                    float *st = part + (int64_t)S.rows * a.head_dim;
+                    st[slot_row] = m;
+                    st[S.rows + slot_row] = l * fine;
+                    if (slot_row == 0) st[2 * S.rows] = odd;
+                } else if (a.lse) {
+                    a.lse[(b * a.tokens + me.t) * a.q_heads + me.h] = none ? -INFINITY : (m + log2f(l * fine)) * 0.6931471805599453f;
+                }
+            }
+            if (odd && seg.whole) {
+                __syncwarp();
+                for (int i = 0; i < 32; ++i) {
+                    const Row other = row_of(A, seg.hk, (int64_t)seg.group * (128 * TILES) + r * 128 + (warp & 3) * 32 + i);
+                    if (!other.inside || other.t >= s.tree) continue;
+                    T *o = (T *)a.out + b * a.o_batch + other.t * a.o_token + other.h * a.o_head;
+                    Eight w;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w.v[e] = lane + 32 * e < a.head_dim ? to_f32(o[lane + 32 * e]) : 0.f;
+                    w = add_odd<T>(A, b, other.t, seg.hk, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (lane + 32 * e < a.head_dim) o[lane + 32 * e] = from_f32<T>(w.v[e]);
+                }
+            }
+        }
+    } else if (fewer_registers<TILES == 2 ? M::FEW : 0>(), BOXES && warp < M::FETCH + 2) {
         // ---- fetch: one warp K, one V, a lane a box ----
         const bool is_v = warp > M::FETCH;
         const uint32_t store = is_v ? sv : sk, full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
@@ -1161,7 +1342,8 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             // all but the (n - announced - 1) newest copies have arrived
             if (n - announced == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
             else if (ST == 2 || n - announced == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-            else asm volatile("cp.async.wait_group 2;" ::: "memory");
+            else if (ST == 3 || n - announced == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+            else asm volatile("cp.async.wait_group 3;" ::: "memory");
             const int st = announced % ST;
             Mark m = marks[0];
 #pragma unroll
@@ -1229,28 +1411,29 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
         if (ok)
             while (announced < n) announce();
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-    } else if (warp == M::ISSUE) {
-        // ---- issue the products ----
+    } else if (warp >= M::ISSUE && warp < M::MEND) {
+        // ---- issue the products: a warp for each row tile ----
+        const int r = warp - M::ISSUE;
         constexpr uint32_t FMT = __is_same(T, __nv_bfloat16) ? 1u : 0u;
         constexpr uint32_t DESC = 1u << 4 | FMT << 7 | FMT << 10 | (128u >> 4) << 24;
         constexpr uint32_t DESC_S = DESC | (uint32_t)(KEYS >> 3) << 17, DESC_O = DESC | 1u << 16 | (uint32_t)(DP >> 3) << 17;
         uint32_t fixes = 0;                                                // parity of the repairs of a stage, a bit each
-        int n0 = 0, it[TILES] = {}, units[TILES] = {};                     // first tile; of a row tile: score tiles, segments
+        int n0 = 0, it = 0, units = 0;                                     // first tile; score tiles, segments
         bool ok = true;
         while (ok && walk.next(A, S, near, seg)) {
-            const int used = tiles_in(seg);
-            if (lane == 0) walk.record(A, S, seg);
-            // scores of row tile r against tile t of the segment
-            auto scores = [&](int r, int t) {
+            if (r == 0 && lane == 0) walk.record(A, S, seg);
+            // scores against tile t of the segment
+            auto scores = [&](int t) {
                 const int st = (n0 + t) % ST;
-                if (r == 0 && ok) ok = __all_sync(~0u, bar_wait(k_full + 8 * st, (n0 + t) / ST & 1, &stop));
+                if (ok) ok = __all_sync(~0u, bar_wait(k_full + 8 * st, (n0 + t) / ST & 1, &stop));
                 // the scores' columns are free once the product that read P from them is done
                 // (the next segment waits for the last one's: two phases of a barrier are
                 // never told apart)
-                if (it[r] > 0 && ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it[r] - (t > 0 ? SB : 1)) & 1, &stop));
+                // (with P elsewhere: once the softmax has read them, which the product before waited for)
+                if (!M::PS && it > 0 && ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - (t > 0 ? SB : 1)) & 1, &stop));
                 if (!ok) return;
                 tc_after();
-                const uint32_t d = __shfl_sync(~0u, tmem + M::S_COL + (r * SB + (SB == 2 ? it[r] & 1 : 0)) * KEYS, 0);
+                const uint32_t d = __shfl_sync(~0u, tmem + M::S_COL + (r * SB + (it & 1)) * KEYS, 0);
                 const uint32_t qa = desc_lo(sq + r * M::Q, 16), ka = desc_lo(sk + st * M::KV, 16);
                 uint64_t qd[DP / 16], kd[DP / 16];
 #pragma unroll
@@ -1261,17 +1444,17 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 if (elected()) {
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k) tc_mma_ss(d, qd[k], kd[k], DESC_S, k > 0);
-                    tc_commit(s_full + 8 * (r * SB + (SB == 2 ? it[r] & 1 : 0)));
-                    if (r == used - 1) tc_commit(k_empty + 8 * st);
+                    tc_commit(s_full + 8 * (r * SB + (it & 1)));
+                    tc_commit(k_empty + 8 * st);
                     if (t == seg.tiles - 1) tc_commit(q_empty + 8 * r);
                 }
-                ++it[r];
+                ++it;
                 __syncwarp();
             };
-            auto outputs = [&](int r, int t) {
-                const int st = (n0 + t) % ST, done = SB == 2 ? it[r] - (t + 1 < seg.tiles ? 2 : 1) : it[r] - 1;   // this tile's number
-                if (r == 0 && ok) ok = __all_sync(~0u, bar_wait(v_full + 8 * st, (n0 + t) / ST & 1, &stop));
-                if (BOXES && r == 0 && ok && seg.j0 + (t + 1) * KEYS > seg.s.first) {
+            auto outputs = [&](int t) {
+                const int st = (n0 + t) % ST, done = it - (t + 1 < seg.tiles ? 2 : 1);   // this tile's number
+                if (ok) ok = __all_sync(~0u, bar_wait(v_full + 8 * st, (n0 + t) / ST & 1, &stop));
+                if (BOXES && ok && seg.j0 + (t + 1) * KEYS > seg.s.first) {
                     ok = __all_sync(~0u, bar_wait(v_fixed + 8 * st, fixes >> st & 1u, &stop));
                     fixes ^= 1u << st;
                 }
@@ -1279,201 +1462,54 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 if (!ok) return;
                 tc_after();
                 const uint32_t d = __shfl_sync(~0u, tmem + M::O_COL + r * DP, 0);
-                const uint32_t pa = __shfl_sync(~0u, tmem + M::S_COL + (r * SB + (SB == 2 ? done & 1 : 0)) * KEYS, 0);
+                const uint32_t pa = __shfl_sync(~0u, tmem + M::S_COL + (r * SB + (done & 1)) * KEYS, 0);
                 const uint32_t va = desc_lo(sv + st * M::KV, M::SUBK), more = __shfl_sync(~0u, t, 0) > 0;
-                uint64_t vd[KEYS / 16];
+                const uint32_t pl = desc_lo(sp + r * M::P, 16);
+                uint64_t vd[KEYS / 16], pd[KEYS / 16];
 #pragma unroll
-                for (int k = 0; k < KEYS / 16; ++k) vd[k] = desc_of(va + k * 2048 / 16);
+                for (int k = 0; k < KEYS / 16; ++k) {
+                    vd[k] = desc_of(va + k * 2048 / 16);
+                    pd[k] = desc_of(pl + k * 32 / 16);
+                }
                 if (elected()) {
 #pragma unroll
-                    for (int k = 0; k < KEYS / 16; ++k) tc_mma_ts(d, pa + 8 * k, vd[k], DESC_O, k > 0 ? 1u : more);
+                    for (int k = 0; k < KEYS / 16; ++k) {
+                        if (M::PS) tc_mma_ss(d, pd[k], vd[k], DESC_O, k > 0 ? 1u : more);
+                        else tc_mma_ts(d, pa + 8 * k, vd[k], DESC_O, k > 0 ? 1u : more);
+                    }
                     tc_commit(o_done + 8 * r);
-                    if (r == used - 1) tc_commit(v_empty + 8 * st);
+                    tc_commit(v_empty + 8 * st);
                 }
                 __syncwarp();
             };
-#pragma unroll
-            for (int r = 0; r < TILES; ++r)
-                if (r < used && ok) {
-                    ok = __all_sync(~0u, bar_wait(q_full + 8 * r, units[r]++ & 1, &stop));
-                    if (ok) scores(r, 0);
+            if (r < tiles_in(seg)) {
+                ok = __all_sync(~0u, bar_wait(q_full + 8 * r, units++ & 1, &stop));
+                if (ok) scores(0);
+                for (int t = 0; t < seg.tiles && ok; ++t) {
+                    if (t + 1 < seg.tiles) scores(t + 1);
+                    if (ok) outputs(t);
                 }
-            for (int t = 0; t < seg.tiles && ok; ++t) {
-                if (SB == 2 && t + 1 < seg.tiles) scores(0, t + 1);
-#pragma unroll
-                for (int r = 0; r < TILES; ++r)
-                    if (r < used && ok) {
-                        outputs(r, t);
-                        if (SB == 1 && ok && t + 1 < seg.tiles) scores(r, t + 1);
+            } else {
+                // the unit has one row tile: the stages are released as they come
+                for (int t = 0; t < seg.tiles && ok; ++t) {
+                    const int st = (n0 + t) % ST;
+                    ok = __all_sync(~0u, bar_wait(k_full + 8 * st, (n0 + t) / ST & 1, &stop) && bar_wait(v_full + 8 * st, (n0 + t) / ST & 1, &stop));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        bar_arrive(k_empty + 8 * st);
+                        bar_arrive(v_empty + 8 * st);
                     }
+                    if (BOXES && seg.j0 + (t + 1) * KEYS > seg.s.first) fixes ^= 1u << st;
+                }
             }
             n0 += seg.tiles;
         }
         if (!ok) {
             // products under way end before their memory is given back
-            if (lane == 0) tc_commit(last_bar);
+            if (lane == 0) tc_commit(last_bar + 8 * r);
             __syncwarp();
             int ignored = 0;
-            bar_wait(last_bar, 0, &ignored);
-        }
-    } else {
-        // ---- softmax: a thread has a row ----
-        const int r = warp >> 2, row = (warp & 3) * 32 + lane;             // row tile, row in it
-        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
-        const uint32_t o_at = tmem + lanes + M::O_COL + r * DP;
-        int it = 0, number = 0;                                            // tiles done; segments
-        bool ok = true;
-        while (ok && walk.next(A, S, near, seg)) {
-            const int number_now = number++;
-            if (r >= tiles_in(seg)) continue;                              // the unit has one row tile: the other's barriers rest
-            const int64_t b = seg.b;
-            const Seq s = seg.s;
-            const Row me = row_of(A, seg.hk, (int64_t)seg.group * (128 * TILES) + r * 128 + row);
-            const bool busy = __any_sync(~0u, me.inside);
-            float m = -INFINITY, l = 0.f;
-            for (int t = 0; t < seg.tiles; ++t, ++it) {
-                const int buf = SB == 2 ? it & 1 : 0;
-                ok = __all_sync(~0u, bar_wait(s_full + 8 * (r * SB + buf), (SB == 2 ? it >> 1 : it) & 1, &stop));
-                if (!ok) break;
-                tc_after();
-                const uint32_t s_at = tmem + lanes + M::S_COL + (r * SB + buf) * KEYS;
-                const int j0 = seg.j0 + t * KEYS;
-                const bool masked = j0 + KEYS > s.first;
-                bool settled = t == 0;                                     // the product before this one is known to be in O
-                if (busy) {
-                    // 64 entries at a time, read twice: first for the maximum, then for P
-                    // (loops kept rolled: the roles share the instruction cache)
-                    auto load = [&](float (&v)[64], int c) {
-                        tc_ld(v, s_at + 64 * c);
-                        if (masked) {
-                            const uint32_t lo = sees32(A, b, me.t, s.tree, j0 + 64 * c - s.first);
-                            const uint32_t hi = sees32(A, b, me.t, s.tree, j0 + 64 * c + 32 - s.first);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                v[e] = lo >> e & 1u ? v[e] : -INFINITY;
-                                v[e + 32] = hi >> e & 1u ? v[e + 32] : -INFINITY;
-                            }
-                        }
-                    };
-                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                    for (int c = 0; c < KEYS / 64; ++c) {
-                        float v[64];
-                        load(v, c);
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) t4[e & 3] = fmaxf(t4[e & 3], v[e]);
-                    }
-                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * A.scale_log2;      // (scale > 0 here)
-                    // replace the maximum only when it grew by more than 2^8
-                    const bool grew = top > m + 8.f || (m == -INFINITY && top > m);
-                    if (__any_sync(~0u, grew)) {
-                        const float f = grew ? (m == -INFINITY ? 0.f : exp2f(m - top)) : 1.f;
-                        if (grew) m = top;
-                        l *= f;
-                        if (t > 0) {
-                            // the output so far, once the product before this one is in it
-                            ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
-                            if (!ok) break;
-                            settled = true;
-                            tc_after();
-#pragma unroll 1
-                            for (int c = 0; c < DP / 32; ++c) {
-                                float v[32];
-                                uint32_t w[32];
-                                tc_ld(v, o_at + 32 * c);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(v[e] * f);
-                                tc_st(o_at + 32 * c, w);
-                            }
-                            tc_wait_st();
-                        }
-                    }
-                    const float shift = m == -INFINITY ? 0.f : m;
-                    float l4[4] = {l, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                    for (int c = 0; c < KEYS / 64; ++c) {
-                        float v[64];
-                        uint32_t w[32];
-                        load(v, c);
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) {
-                            v[e] = pow2(fmaf(v[e], A.scale_log2, -shift));
-                            l4[e & 3] += v[e];
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) w[e] = pack2<T>(v[2 * e], v[2 * e + 1]);
-                        tc_st(s_at + 32 * c, w);
-                    }
-                    l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-                    tc_wait_st();
-                }
-                // (every phase of o_done is waited for while the next cannot end)
-                if (!settled) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
-                if (!ok) break;
-                tc_before();
-                bar_arrive(p_ready + 8 * r);
-            }
-            // the unit's (or the part's) output
-            if (ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
-            tc_after();
-            const bool odd = ok && *(volatile int *)&odd_seg[number_now & 7] == number_now + 1;
-            if (!busy) continue;
-            float *part = slot_of(A, S, blockIdx.x, seg.slot);
-            const int slot_row = r * 128 + row;
-            const bool none = me.t >= s.tree || l == 0.f;
-            const float fine = ok ? 1.f : nanf("");
-            const float by = seg.whole ? (none ? 0.f : 1.f / l) * fine : fine;
-            T *out = (T *)a.out + b * a.o_batch + me.t * a.o_token + me.h * a.o_head;
-#pragma unroll 1
-            for (int c = 0; c < DP / 32; ++c) {
-                float v[32];
-                tc_ld(v, o_at + 32 * c);
-                if (!me.inside) continue;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = seg.whole && none && ok ? 0.f : v[e] * by;
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    const int d = 32 * c + e;
-                    if (d >= a.head_dim) break;
-                    if (!seg.whole) {
-                        store32(part + (int64_t)slot_row * a.head_dim + d, __float_as_uint(v[e]), __float_as_uint(v[e + 1]), __float_as_uint(v[e + 2]),
-                                __float_as_uint(v[e + 3]), __float_as_uint(v[e + 4]), __float_as_uint(v[e + 5]), __float_as_uint(v[e + 6]),
-                                __float_as_uint(v[e + 7]));
-                    } else if (A.wide_out) {
-                        *(uint4 *)(out + d) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]), pack2<T>(v[e + 4], v[e + 5]),
-                                                         pack2<T>(v[e + 6], v[e + 7]));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) out[d + k] = from_f32<T>(v[e + k]);
-                    }
-                }
-            }
-            tc_before();
-            if (me.inside) {
-                if (!seg.whole) {
-                    float *st = part + (int64_t)S.rows * a.head_dim;
-                    st[slot_row] = m;
-                    st[S.rows + slot_row] = l * fine;
-                    if (slot_row == 0) st[2 * S.rows] = odd;
-                } else if (a.lse) {
-                    a.lse[(b * a.tokens + me.t) * a.q_heads + me.h] = none ? -INFINITY : (m + log2f(l * fine)) * 0.6931471805599453f;
-                }
-            }
-            if (odd && seg.whole) {
-                __syncwarp();
-                for (int i = 0; i < 32; ++i) {
-                    const Row other = row_of(A, seg.hk, (int64_t)seg.group * (128 * TILES) + r * 128 + (warp & 3) * 32 + i);
-                    if (!other.inside || other.t >= s.tree) continue;
-                    T *o = (T *)a.out + b * a.o_batch + other.t * a.o_token + other.h * a.o_head;
-                    Eight w;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w.v[e] = lane + 32 * e < a.head_dim ? to_f32(o[lane + 32 * e]) : 0.f;
-                    w = add_odd<T>(A, b, other.t, seg.hk, w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (lane + 32 * e < a.head_dim) o[lane + 32 * e] = from_f32<T>(w.v[e]);
-                }
-            }
+            bar_wait(last_bar + 8 * r, 0, &ignored);
         }
     }
     __syncwarp();
@@ -1517,7 +1553,7 @@ dbs_status plan_of(const dbs_attention_args &a, Plan &P)
     int per_sm = P.dp == 64 ? 4 : P.dp == 128 ? 2 : 1;
     if (P.many) {
         const int tiles = P.dp == 256 || rows <= 128 ? 1 : 2;
-        S.keys = P.dp == 256 ? 64 : 128;
+        S.keys = P.dp == 256 || tiles == 2 ? 64 : 128;
         S.rows = 128 * tiles;
         S.heavy = tiles;
         per_sm = 1;
@@ -1639,7 +1675,13 @@ dbs_status launch_kind(const Attn &A, const Plan &P, const Maps &maps, cudaStrea
 {
     using M = Many<DP, TILES>;
     static Once once;
-    if (!room_for(once, k_attn_many<T, DP, TILES, BOXES>, M::SMEM)) return DBS_ERR_CUDA;
+    // (the warps share out the registers that a block starts with, so there have to be
+    // that many, or their waits for them would not end)
+    static const bool shares = [] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, k_attn_many<T, DP, TILES, BOXES>) == cudaSuccess && (TILES == 1 || f.numRegs == M::REGS);
+    }();
+    if (!shares || !room_for(once, k_attn_many<T, DP, TILES, BOXES>, M::SMEM)) return DBS_ERR_CUDA;
     k_attn_many<T, DP, TILES, BOXES><<<P.blocks, M::NT, M::SMEM, s>>>(A, P.share, maps);
     const dbs_status st = launched();
     return st == DBS_OK ? launch_join<T>(A, P, s) : st;

@@ -99,6 +99,16 @@ __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sy
 constexpr uint32_t DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) { return __shfl_sync(~0u, (addr >> 4) | (lead >> 4) << 16, 0); }
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return (uint64_t)DESC_HI << 32 | lo; }
+// Registers of the threads of four warps from here on (0: as they are); all of a
+// block's have to be within those that it was launched with.
+template <int R> __device__ __forceinline__ void fewer_registers()
+{
+    if constexpr (R > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R> __device__ __forceinline__ void more_registers()
+{
+    if constexpr (R > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
 // Tensor memory of a block, all 512 columns; by one warp.
 __device__ __forceinline__ void tc_alloc(uint32_t at)
 {

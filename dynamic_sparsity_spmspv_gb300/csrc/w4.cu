@@ -595,8 +595,6 @@ template <int N> struct Many {
     static constexpr int SUMS = 0, NUMBERS = 4 * N;                          // columns of tensor memory
     static constexpr int SMEM = 1024 + WS * CODES + XS * X;
 };
-template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 static_assert(Many<32>::NUMBERS + Many<32>::RA * 64 <= 512 && Many<64>::NUMBERS + Many<64>::RA * 64 <= 512, "tensor memory");
 
 struct Walk {
