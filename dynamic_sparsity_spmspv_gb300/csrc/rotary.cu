@@ -262,11 +262,14 @@ dbs_status dbs_rotary_table(int64_t positions, int32_t dim, double base, dbs_rot
     if (scaling == DBS_ROTARY_NTK) base *= std::pow(factor, (double)dim / (dim - 2));
     for (int i = 0; i < half; ++i) F.f[i] = std::pow(base, -2.0 * i / dim) / (scaling == DBS_ROTARY_LINEAR ? factor : 1);
     if (scaling == DBS_ROTARY_YARN) {
-        // pair index at which a pair turns beta times within the trained positions
+        // pair index at which a pair turns beta times within the trained positions; the ends of the
+        // ramp, rounded outwards, are kept within 0 and dim - 1 as in the published method, not within
+        // the pairs there are: where the slowest pair still turns more than beta_slow times, the ramp
+        // ends behind it
         const double pi = 3.14159265358979323846;
         auto at = [&](double beta) { return dim * std::log(trained / (beta * 2 * pi)) / (2 * std::log(base)); };
         const double lo = std::fmax(0, std::floor(at(beta_fast)));
-        double hi = std::fmin(half - 1, std::ceil(at(beta_slow)));
+        double hi = std::fmin(dim - 1, std::ceil(at(beta_slow)));
         if (hi <= lo) hi = lo + 0.001;
         for (int i = 0; i < half; ++i) {
             const double r = std::fmin(1, std::fmax(0, (i - lo) / (hi - lo)));   // 0: kept, 1: divided

@@ -460,7 +460,8 @@ typedef enum {
     DBS_ROTARY_NTK = 2,        /* base * factor^(dim/(dim-2)): slow pairs stretched, the fastest kept */
     DBS_ROTARY_YARN = 3        /* pairs that turn more than beta_fast times within `trained` positions are
                                   kept, fewer than beta_slow divided by factor, a linear ramp (over the pair
-                                  index) between; cos and sin times 0.1 ln(factor) + 1 */
+                                  index, its ends rounded outwards and kept within 0 and dim - 1) between;
+                                  cos and sin times 0.1 ln(factor) + 1 */
 } dbs_rotary_scaling;
 
 /* Cosine and sine table of rotary positions, computed in fp64 and rounded to

@@ -1,0 +1,47 @@
+"""The decoding step's operators at the ends of their ranges, against plain 64-bit forms."""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import __graft_entry__  # noqa: E402
+
+__graft_entry__.build()
+import dynamic_sparsity_spmspv_gb300 as dbs  # noqa: E402
+
+DEV = "cuda"
+
+
+def yarn_table(P, R, base, factor, trained, fast=32.0, slow=1.0):
+    """The published formula: between the pairs that turn `fast` and `slow` times within the trained positions, rounded
+    outwards and kept within 0 and R - 1, the share of the divided frequency grows linearly with the pair's index."""
+    def pair(turns):
+        return R * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
+    lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), R - 1)
+    i = np.arange(R // 2)
+    f = base ** (-2.0 * i / R)
+    share = np.clip((i - lo) / (hi - lo if hi > lo else 0.001), 0, 1)
+    f = share * f / factor + (1 - share) * f
+    a = np.arange(P)[:, None] * f
+    return np.concatenate([np.cos(a), np.sin(a)], 1) * (0.1 * math.log(factor) + 1), f
+
+
+@pytest.mark.parametrize("R,base,factor,trained", [
+    (128, 1e4, 4.0, 131072), (128, 1e4, 8.0, 65536), (64, 1e4, 2.0, 1 << 20), (96, 500.0, 16.0, 8192), (8, 1e4, 4.0, 1 << 24),
+    (128, 1e4, 16.0, 4096), (2, 1e4, 4.0, 4096), (128, 1e6, 4.0, 100.0)])
+def test_yarn_table_of_any_trained_length(R, base, factor, trained):
+    """Trained lengths at which the slowest pairs still turn more than once, and others."""
+    P = 3000
+    ref, f = yarn_table(P, R, base, factor, trained)
+    t = dbs.rotary_table(P, R, base=base, scaling="yarn", factor=factor, trained=trained).double().cpu().numpy()
+    # angles in 64 bits (roundings of the frequency and of the product, 2^-50 of the angle), then one to 32
+    assert (np.abs(t - ref) <= 2.0**-24 * 1.5 + P * 2.0**-50).all()
+    # a pair that turns more than once within the trained positions is never divided by the whole factor
+    i = np.arange(R // 2)
+    plain = base ** (-2.0 * i / R)
+    turns = trained * plain / (2 * math.pi)
+    assert (f[turns > 1.001] > plain[turns > 1.001] / factor).all()
