@@ -1378,7 +1378,8 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
 #pragma unroll
                 for (int i = 0; i < PL; ++i) {
                     const int j = seg.j0 + t * KEYS + 32 * i + lane;
-                    const Place at = place_of(a, seg.b, j < seg.j1 ? j : 0);
+                    Place at = {0, 0};                                     // (a cache without entries has no place, and may have no page table)
+                    if (j < seg.j1) at = place_of(a, seg.b, j);
                     in[i] = __ballot_sync(~0u, j < seg.j1);
                     off[i] = at.page * st_page + at.in * st_entry;
                 }
@@ -1400,7 +1401,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                     const int row = i * RS + lane / CH;
                     const int64_t o = __shfl_sync(~0u, off[i * RS / 32], row & 31);
                     const bool take = (in[i * RS / 32] >> (row & 31) & 1u) && c < chunks;
-                    cp16(to + row * 128 + (((c & 7) ^ (row & 7)) << 4), take ? (const void *)(from + o) : (const void *)a.k, take);
+                    cp16(to + row * 128 + (((c & 7) ^ (row & 7)) << 4), take ? (const void *)(from + o) : a.q, take);   // (some address to read nothing from)
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
                 ++n;

@@ -45,3 +45,17 @@ def test_yarn_table_of_any_trained_length(R, base, factor, trained):
     plain = base ** (-2.0 * i / R)
     turns = trained * plain / (2 * math.pi)
     assert (f[turns > 1.001] > plain[turns > 1.001] / factor).all()
+
+
+@pytest.mark.parametrize("T,hq", [(1, 4), (3, 4), (40, 4), (300, 4)])
+def test_attention_over_caches_without_entries(T, hq):
+    """Pages of no entry, no pages at all, a table of no pages: nothing is seen."""
+    f = dict(device=DEV, dtype=torch.bfloat16)
+    q = torch.ones((2, T, hq, 64), **f)
+    lens = torch.full((2,), 7, dtype=torch.int32, device=DEV)
+    for pages, size, table in ((5, 0, 4), (0, 0, 4), (5, 16, 0), (5, 0, 0), (0, 16, 0)):
+        c = torch.zeros((pages, size, 2, 64), **f)
+        o, lse = dbs.tree_attention(q, c, c, lens, page_table=torch.zeros((2, table), dtype=torch.int32, device=DEV), return_lse=True)
+        assert (o == 0).all() and (lse == -math.inf).all()
+    c = torch.zeros((2, 0, 2, 64), **f)
+    assert (dbs.tree_attention(q, c, c, lens) == 0).all()
