@@ -386,9 +386,10 @@ PyObject *rotary_append(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyO
         const at::Tensor qo = turned(c, q, qg);
         const dbs_rotary_heads parts[3] = {part(q, Q, qo.data_ptr(), heads_of(c, "q_out", qo, q.scalar_type()), true, false),
                                            part(k, K, kc.data_ptr(), KC, true, true), part(v, V, vc.data_ptr(), VC, false, true)};
+        const bool room = KC.n > 0;                    // (pages of no entry are like no pages)
         check(c.fn, dbs_rotary(parts, 3, dt, Q.b, Q.n, (int32_t)Q.d, (int32_t)table.size(1), table.data_ptr<float>(), table.size(0),
-                               pos.data_ptr<int32_t>(), slots.data_ptr<int32_t>(), KC.b, KC.n > 0 ? KC.n : 1, truth(a.v[8], false),
-                               0, c.stream));
+                               pos.data_ptr<int32_t>(), slots.data_ptr<int32_t>(), room ? KC.b : 0, room ? KC.n : 1,
+                               truth(a.v[8], false), 0, c.stream));
         return wrap(qo);
     });
 }

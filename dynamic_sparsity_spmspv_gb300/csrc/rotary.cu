@@ -300,9 +300,11 @@ dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype d
         const dbs_rotary_heads &P = parts[p];
         if (P.heads < 0 || P.heads > 16384) return DBS_ERR_INVALID_ARG;
         if (P.heads == 0) continue;
-        if (work && (!P.in || !P.out || (P.rotate && dim > 0 && (!table || !positions)) ||
+        if (work && (!P.in || (P.rotate && dim > 0 && (!table || !positions)) ||
                      (P.to_slots && (!slots || pages < 0 || page_size < 1 || pages > (int64_t(1) << 31) / page_size))))
             return DBS_ERR_INVALID_ARG;
+        if (work && P.to_slots && pages == 0) continue;                        // no slot is inside: nothing is written
+        if (work && !P.out) return DBS_ERR_INVALID_ARG;
         A.part[A.nparts++] = P;
         heads += P.heads;
     }

@@ -496,7 +496,8 @@ typedef struct {
  *              is outside the table gets NaN in its rotated entries
  *   slots      device int32[batch, tokens], contiguous, NULL without to_slots;
  *              tokens with a slot outside [0, pages * page_size) are not
- *              written.  Slots in use must differ from one another.
+ *              written (pages = 0: none, and `out` may be NULL).  Slots in use
+ *              must differ from one another.
  *   head_dim   entries of a head, dim <= head_dim <= 1024, dim even
  *   batch * tokens < 2^31, and times head_dim < 2^32 - 256; at most 16384 heads
  *   in a group

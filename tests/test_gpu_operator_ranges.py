@@ -59,3 +59,15 @@ def test_attention_over_caches_without_entries(T, hq):
         assert (o == 0).all() and (lse == -math.inf).all()
     c = torch.zeros((2, 0, 2, 64), **f)
     assert (dbs.tree_attention(q, c, c, lens) == 0).all()
+
+
+def test_appending_to_caches_without_entries():
+    """Every slot is outside of them: only q is turned."""
+    f = dict(device=DEV, dtype=torch.bfloat16)
+    q = torch.ones((5, 4, 64), **f)
+    n = q[:, :2]
+    pos = torch.zeros(5, dtype=torch.int32, device=DEV)
+    table = dbs.rotary_table(3, 64)
+    for pages, size in ((5, 0), (0, 16), (0, 0)):
+        c = torch.zeros((pages, size, 2, 64), **f)
+        assert torch.equal(dbs.rotary_append(q, n, n, table, pos, c, c.clone(), pos), dbs.rotary(q, None, table, pos)[0])
