@@ -16,6 +16,7 @@ struct Attn {
     int words;                 // 64-bit mask words per token
     bool wide_out;             // heads of out start on 16-byte boundaries
     int group;                 // query heads of a kv head
+    Waits waits;
 };
 
 // What sequence b holds, with every length clamped to its range.
@@ -927,8 +928,8 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
 // over S and tiles of 64: 177; one warp issuing for both row tiles: 179.  A share of
 // the powers of two by polynomial made it slower (186 us and more).
 //
-// Every wait has a limit; a block whose wait runs out stops and leaves NaN in
-// its rows.
+// Every wait on a barrier has a limit; a block whose wait runs out stops and leaves NaN
+// in the rows of all units, or parts of units, that it had not finished.
 
 template <int DP, int TILES> struct Many {
     static constexpr int KEYS = DP == 256 || TILES == 2 ? 64 : 128;
@@ -972,6 +973,39 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap *map, i
     asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
                  "l"(map), "r"(bar), "r"(d), "r"(head), "r"(entry), "r"(page) : "memory");
 }
+// After a wait ran out, for the units that are left of a block's piece: who works on
+// them, for the join, by one warp; and NaN in their rows, or, of a part, sums that the
+// join makes NaN of, a row by each softmax thread (row `row` of row tile `r`).  (The first is
+// inlined: the issuing warps have given registers away, a call might need them.)
+__device__ __forceinline__ void record_rest(const Attn &A, const Share &S, const Near &near, Walk walk)
+{
+    Segment seg;
+    while (walk.next(A, S, near, seg))
+        if ((threadIdx.x & 31) == 0) walk.record(A, S, seg);
+}
+template <class T, int TILES>
+__device__ __noinline__ void leave_nan(const Attn &A, const Share &S, const Near &near, Walk walk, int r, int row)
+{
+    const dbs_attention_args &a = A.a;
+    const float nan = nanf("");
+    Segment seg;
+    while (walk.next(A, S, near, seg)) {
+        const int slot_row = r * 128 + row;
+        const Row me = row_of(A, seg.hk, (int64_t)seg.group * (128 * TILES) + slot_row);
+        if (!me.inside) continue;
+        if (seg.whole) {
+            T *out = (T *)a.out + seg.b * a.o_batch + me.t * a.o_token + me.h * a.o_head;
+            for (int d = 0; d < a.head_dim; ++d) out[d] = from_f32<T>(nan);
+            if (a.lse) a.lse[(seg.b * a.tokens + me.t) * a.q_heads + me.h] = nan;
+        } else {
+            float *st = slot_of(A, S, blockIdx.x, seg.slot) + (int64_t)S.rows * a.head_dim;
+            st[slot_row] = -INFINITY;
+            st[S.rows + slot_row] = nan;
+            if (slot_row == 0) st[2 * S.rows] = 0.f;
+        }
+    }
+}
+
 template <class T, int DP, int TILES, bool BOXES>
 __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Share S, const __grid_constant__ Maps maps)
 {
@@ -1049,7 +1083,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             float m = -INFINITY, l = 0.f;
             for (int t = 0; t < seg.tiles; ++t, ++it) {
                 const int buf = it & 1;
-                ok = __all_sync(~0u, bar_wait(s_full + 8 * (r * SB + buf), it >> 1 & 1, &stop));
+                ok = __all_sync(~0u, bar_wait(s_full + 8 * (r * SB + buf), it >> 1 & 1, &stop, A.waits.limit));
                 if (!ok) break;
                 tc_after();
                 const uint32_t s_at = tmem + lanes + M::S_COL + (r * SB + buf) * KEYS;
@@ -1088,7 +1122,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                         l *= f;
                         if (t > 0) {
                             // the output so far, once the product before this one is in it
-                            ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
+                            ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop, A.waits.limit));
                             if (!ok) break;
                             settled = true;
                             tc_after();
@@ -1107,7 +1141,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                     const float shift = m == -INFINITY ? 0.f : m;
                     if (M::PS && !settled) {
                         // P's place is free once the product before this one is done
-                        ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
+                        ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop, A.waits.limit));
                         if (!ok) break;
                         settled = true;
                     }
@@ -1138,13 +1172,13 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                     else tc_wait_st();
                 }
                 // (every phase of o_done is waited for while the next cannot end)
-                if (!settled) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
+                if (!settled) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop, A.waits.limit));
                 if (!ok) break;
                 tc_before();
                 bar_arrive(p_ready + 8 * r);
             }
             // the unit's (or the part's) output
-            if (ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop));
+            if (ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - 1) & 1, &stop, A.waits.limit));
             tc_after();
             const bool odd = ok && *(volatile int *)&odd_seg[number_now & 7] == number_now + 1;
             if (!busy) continue;
@@ -1186,7 +1220,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                     st[S.rows + slot_row] = l * fine;
                     if (slot_row == 0) st[2 * S.rows] = odd;
                 } else if (a.lse) {
-                    a.lse[(b * a.tokens + me.t) * a.q_heads + me.h] = none ? -INFINITY : (m + log2f(l * fine)) * 0.6931471805599453f;
+                    a.lse[(b * a.tokens + me.t) * a.q_heads + me.h] = !ok ? fine : none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                 }
             }
             if (odd && seg.whole) {
@@ -1205,12 +1239,14 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 }
             }
         }
+        if (!ok) leave_nan<T, TILES>(A, S, near, walk, r, row);
     } else if (fewer_registers<TILES == 2 ? M::FEW : 0>(), BOXES && warp < M::FETCH + 2) {
         // ---- fetch: one warp K, one V, a lane a box ----
         const bool is_v = warp > M::FETCH;
         const uint32_t store = is_v ? sv : sk, full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
         const CUtensorMap *const map = is_v ? &maps.v : &maps.k;
         const int box = maps.box, boxes = KEYS / box;                      // (8 to 128 entries; 1 to 16 boxes)
+        const uint32_t vain = vain_bytes(A.waits);
         int n = 0;
         bool ok = true;
         while (ok && walk.next(A, S, near, seg)) {
@@ -1222,11 +1258,11 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             find(0);
             for (int t = 0; t < seg.tiles && ok; ++t, ++n) {
                 const int st = n % ST, j = seg.j0 + t * KEYS;
-                ok = __all_sync(~0u, bar_wait(empty + 8 * st, (n / ST + 1) & 1, &stop));   // the first round finds it free
+                ok = __all_sync(~0u, bar_wait(empty + 8 * st, (n / ST + 1) & 1, &stop, A.waits.limit));   // the first round finds it free
                 if (!ok) break;
                 const bool mine = lane < boxes && j + lane * box < seg.j1;
                 const int count = __popc(__ballot_sync(~0u, mine));
-                if (lane == 0) bar_expect(full + 8 * st, (uint32_t)(count * box * 128 * (DP / 64)));
+                if (lane == 0) bar_expect(full + 8 * st, (uint32_t)(count * box * 128 * (DP / 64)) + vain);
                 __syncwarp();
                 if (mine)
 #pragma unroll
@@ -1238,11 +1274,10 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             }
         }
         // copies under way end before their memory is given back
-        if (!ok)
-            for (int i = n > ST ? n - ST : 0; i < n; ++i) {
-                int ignored = 0;
-                bar_wait(full + 8 * (i % ST), i / ST & 1, &ignored);
-            }
+        for (int i = n > ST ? n - ST : 0; i < n; ++i) {
+            int last = 0;
+            bar_wait(full + 8 * (i % ST), i / ST & 1, &last, A.waits.limit);
+        }
     } else if (warp >= M::LOAD && warp < M::ISSUE) {
         // ---- Q ----
         const int p = tid - 32 * M::LOAD, c = p % CH, r0 = p / CH;
@@ -1271,7 +1306,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                     }
                     if (!free) {
                         // free once the segment before has its scores
-                        ok = __all_sync(~0u, bar_wait(q_empty + 8 * r, (units[r]++ + 1) & 1, &stop));
+                        ok = __all_sync(~0u, bar_wait(q_empty + 8 * r, (units[r]++ + 1) & 1, &stop, A.waits.limit));
                         free = true;
                         if (!ok) break;
                     }
@@ -1300,9 +1335,9 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 const int j0 = seg.j0 + t * KEYS, st = n % ST;
                 if (j0 + KEYS <= seg.s.first) continue;
                 // (first that the stage's copies are this tile's, then that they have arrived)
-                ok = __all_sync(~0u, bar_wait(v_odd + 8 * st, seen >> st & 1u, &stop));
+                ok = __all_sync(~0u, bar_wait(v_odd + 8 * st, seen >> st & 1u, &stop, A.waits.limit));
                 seen ^= 1u << st;
-                if (ok) ok = __all_sync(~0u, bar_wait(v_full + 8 * st, n / ST & 1, &stop));
+                if (ok) ok = __all_sync(~0u, bar_wait(v_full + 8 * st, n / ST & 1, &stop, A.waits.limit));
                 if (!ok) break;
                 bool found = false;
 #pragma unroll 4
@@ -1333,6 +1368,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
         const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
         const int64_t st_page = is_v ? a.v_page : a.k_page, st_entry = is_v ? a.v_entry : a.k_entry, st_head = is_v ? a.v_head : a.k_head;
         const T *const src = (const T *)(is_v ? a.v : a.k) + c * 8;
+        const bool vain = vain_bytes(A.waits) != 0;
         int n = 0, announced = 0, number = 0;                              // tiles fetched, announced; segments
         struct Mark { int first, j0, number; };
         Mark marks[ST];                                                    // of the tiles under way
@@ -1366,7 +1402,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 if (found) *(volatile int *)&odd_seg[m.number & 7] = m.number + 1;
             }
             async_fence();
-            bar_arrive(full + 8 * st);
+            if (!vain) bar_arrive(full + 8 * st);
             ++announced;
         };
         bool ok = true;
@@ -1390,7 +1426,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 const uint32_t parity = (n / ST + 1) & 1;                  // of the stage's release; the first round finds it free
                 // what has been fetched is announced before this warp waits for a stage
                 while (announced < n && !__all_sync(~0u, bar_test(empty + 8 * st, parity))) announce();
-                ok = __all_sync(~0u, bar_wait(empty + 8 * st, parity, &stop));
+                ok = __all_sync(~0u, bar_wait(empty + 8 * st, parity, &stop, A.waits.limit));
                 if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < ST; ++i)
@@ -1426,12 +1462,12 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             // scores against tile t of the segment
             auto scores = [&](int t) {
                 const int st = (n0 + t) % ST;
-                if (ok) ok = __all_sync(~0u, bar_wait(k_full + 8 * st, (n0 + t) / ST & 1, &stop));
+                if (ok) ok = __all_sync(~0u, bar_wait(k_full + 8 * st, (n0 + t) / ST & 1, &stop, A.waits.limit));
                 // the scores' columns are free once the product that read P from them is done
                 // (the next segment waits for the last one's: two phases of a barrier are
                 // never told apart)
                 // (with P elsewhere: once the softmax has read them, which the product before waited for)
-                if (!M::PS && it > 0 && ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - (t > 0 ? SB : 1)) & 1, &stop));
+                if (!M::PS && it > 0 && ok) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (it - (t > 0 ? SB : 1)) & 1, &stop, A.waits.limit));
                 if (!ok) return;
                 tc_after();
                 const uint32_t d = __shfl_sync(~0u, tmem + M::S_COL + (r * SB + (it & 1)) * KEYS, 0);
@@ -1454,12 +1490,12 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             };
             auto outputs = [&](int t) {
                 const int st = (n0 + t) % ST, done = it - (t + 1 < seg.tiles ? 2 : 1);   // this tile's number
-                if (ok) ok = __all_sync(~0u, bar_wait(v_full + 8 * st, (n0 + t) / ST & 1, &stop));
+                if (ok) ok = __all_sync(~0u, bar_wait(v_full + 8 * st, (n0 + t) / ST & 1, &stop, A.waits.limit));
                 if (BOXES && ok && seg.j0 + (t + 1) * KEYS > seg.s.first) {
-                    ok = __all_sync(~0u, bar_wait(v_fixed + 8 * st, fixes >> st & 1u, &stop));
+                    ok = __all_sync(~0u, bar_wait(v_fixed + 8 * st, fixes >> st & 1u, &stop, A.waits.limit));
                     fixes ^= 1u << st;
                 }
-                if (ok) ok = __all_sync(~0u, bar_wait(p_ready + 8 * r, done & 1, &stop));
+                if (ok) ok = __all_sync(~0u, bar_wait(p_ready + 8 * r, done & 1, &stop, A.waits.limit));
                 if (!ok) return;
                 tc_after();
                 const uint32_t d = __shfl_sync(~0u, tmem + M::O_COL + r * DP, 0);
@@ -1484,7 +1520,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 __syncwarp();
             };
             if (r < tiles_in(seg)) {
-                ok = __all_sync(~0u, bar_wait(q_full + 8 * r, units++ & 1, &stop));
+                ok = __all_sync(~0u, bar_wait(q_full + 8 * r, units++ & 1, &stop, A.waits.limit));
                 if (ok) scores(0);
                 for (int t = 0; t < seg.tiles && ok; ++t) {
                     if (t + 1 < seg.tiles) scores(t + 1);
@@ -1494,7 +1530,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                 // the unit has one row tile: the stages are released as they come
                 for (int t = 0; t < seg.tiles && ok; ++t) {
                     const int st = (n0 + t) % ST;
-                    ok = __all_sync(~0u, bar_wait(k_full + 8 * st, (n0 + t) / ST & 1, &stop) && bar_wait(v_full + 8 * st, (n0 + t) / ST & 1, &stop));
+                    ok = __all_sync(~0u, bar_wait(k_full + 8 * st, (n0 + t) / ST & 1, &stop, A.waits.limit) && bar_wait(v_full + 8 * st, (n0 + t) / ST & 1, &stop, A.waits.limit));
                     if (!ok) break;
                     if (lane == 0) {
                         bar_arrive(k_empty + 8 * st);
@@ -1506,11 +1542,12 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
             n0 += seg.tiles;
         }
         if (!ok) {
+            if (r == 0) record_rest(A, S, near, walk);
             // products under way end before their memory is given back
             if (lane == 0) tc_commit(last_bar + 8 * r);
             __syncwarp();
-            int ignored = 0;
-            bar_wait(last_bar + 8 * r, 0, &ignored);
+            int last = 0;
+            bar_wait(last_bar + 8 * r, 0, &last, A.waits.limit);
         }
     }
     __syncwarp();
@@ -1732,6 +1769,14 @@ bool args_ok(const dbs_attention_args *a)
 
 extern "C" {
 
+dbs_status dbs_debug_operator_waits(int64_t limit_ns, int32_t block)
+{
+    if (limit_ns < 1 || limit_ns > 2000000000 || block < -2) return DBS_ERR_INVALID_ARG;
+    wait_limit.store((uint32_t)limit_ns, std::memory_order_relaxed);
+    wait_vain.store(block, std::memory_order_relaxed);
+    return DBS_OK;
+}
+
 dbs_status dbs_tree_attention_scratch(const dbs_attention_args *a, int64_t *bytes)
 {
     if (!bytes || !args_ok(a)) return DBS_ERR_INVALID_ARG;
@@ -1752,7 +1797,7 @@ dbs_status dbs_tree_attention(const dbs_attention_args *a, void *stream)
     if (st != DBS_OK) return st;
     if (P.scratch > 0 && (!a->scratch || (reinterpret_cast<uintptr_t>(a->scratch) & 31u) || a->scratch_bytes < P.scratch)) return DBS_ERR_INVALID_ARG;
     const bool wide_out = aligned16(a->out) && aligned8(a->o_batch) && aligned8(a->o_token) && aligned8(a->o_head);
-    const Attn A{*a, a->scale * 1.4426950408889634f, (int)((a->tokens + 63) / 64), wide_out, a->q_heads / a->kv_heads};
+    const Attn A{*a, a->scale * 1.4426950408889634f, (int)((a->tokens + 63) / 64), wide_out, a->q_heads / a->kv_heads, waits()};
     P.share.scratch = (float *)a->scratch;
     P.share.units = (int4 *)((char *)a->scratch + P.slots);
     return a->dtype == DBS_F16 ? launch<__half>(A, P, (cudaStream_t)stream) : launch<__nv_bfloat16>(A, P, (cudaStream_t)stream);

@@ -17,6 +17,7 @@ struct W4 {
     void *y;
     int64_t tokens, x_stride, q_stride, scale_stride, zero_stride, m, n, y_stride;
     int32_t group;
+    Waits waits;
 };
 
 // 16-byte loads of x: every token's row on such a boundary.
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C, const __grid_
                 }
                 const int k4 = turn++ & 3;
                 fetch();
-                ok = ok && bar_wait(bar + 8 * use, parity, &stop);
+                ok = ok && bar_wait(bar + 8 * use, parity, &stop, A.waits.limit);
                 const uint32_t w = ring + use * STAGE;
                 if (++use == STAGES) {
                     use = 0;
@@ -706,7 +707,7 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
 #pragma unroll
             for (int i = 0; i < 4; ++i) z[i] = H::magic + ((parts == 4 ? zn[i] : parts == 2 ? zn[i >> 1] : zn[0]) & 127u) * H::one;
             zero_points();
-            ok = ok && __all_sync(~0u, bar_wait(w_full + 8 * ws, wp, &stop));
+            ok = ok && __all_sync(~0u, bar_wait(w_full + 8 * ws, wp, &stop, A.waits.limit));
             const int half = u & 1;
             uint4 q[4];
 #pragma unroll
@@ -718,7 +719,7 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
                 ws -= M::WS;
                 wp ^= 1;
             }
-            ok = ok && __all_sync(~0u, bar_wait(a_empty + 8 * as, ap, &stop));
+            ok = ok && __all_sync(~0u, bar_wait(a_empty + 8 * as, ap, &stop, A.waits.limit));
             if (!ok) break;
             tc_after();
 #pragma unroll
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
         };
 #pragma unroll 1
         for (int g = 0; g < all; ++g) {
-            ok = ok && __all_sync(~0u, bar_wait(d_full + 8 * (g & 1), g >> 1 & 1, &stop));
+            ok = ok && __all_sync(~0u, bar_wait(d_full + 8 * (g & 1), g >> 1 & 1, &stop, A.waits.limit));
             if (ok) {
                 tc_after();
                 const uint32_t sums = tmem + ((uint32_t)(warp & 3) << 21) + M::SUMS + (g & 1) * (2 * N);
@@ -847,7 +848,7 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
         uint32_t parity = 0;
         bool ok = true;
         for (int n = 0; n < chunks && ok; ++n) {
-            ok = __all_sync(~0u, bar_wait(x_here + 8 * st, parity, &stop));
+            ok = __all_sync(~0u, bar_wait(x_here + 8 * st, parity, &stop, A.waits.limit));
             if (!ok) break;
             const uint32_t at = xs + st * M::X + (threadIdx.x & 127) * 16;
             uint4 v[8];
@@ -877,7 +878,7 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
         int st = 0;
         uint32_t parity = 1;
         for (int n = 0; n < chunks; ++n) {
-            if (!__all_sync(~0u, bar_wait(empty + 8 * st, parity, &stop))) break;
+            if (!__all_sync(~0u, bar_wait(empty + 8 * st, parity, &stop, A.waits.limit))) break;
             if (elected()) {
                 bar_expect(full + 8 * st, bytes);
                 if (is_x) {
@@ -911,8 +912,8 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
                 for (int u = 0; u < 2 * M::XS; ++u) {
                     const int half = u & 1;
                     if (n0 + u / 2 >= chunks) break;
-                    if (half == 0) ok = ok && __all_sync(~0u, bar_wait(x_full + 8 * (u / 2), turn, &stop));
-                    ok = ok && __all_sync(~0u, bar_wait(a_full + 8 * u, turn, &stop));
+                    if (half == 0) ok = ok && __all_sync(~0u, bar_wait(x_full + 8 * (u / 2), turn, &stop, A.waits.limit));
+                    ok = ok && __all_sync(~0u, bar_wait(a_full + 8 * u, turn, &stop, A.waits.limit));
                     const uint32_t lo = (xs + u / 2 * M::X + half * (2 * N * 128)) >> 4 | 1u << 16, a = M::NUMBERS + u * 64;
                     uint64_t b[8];
 #pragma unroll
@@ -922,7 +923,7 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
                         // the group's place in its set, and whether the set begins or ends here
                         const bool second = LEN == 8 ? half == 1 && C.shift < 8 : k0 / LEN & 1;
                         const bool begins = LEN == 8 ? half == 0 : !second, ends = LEN == 8 ? half == 1 : second;
-                        if (begins) ok = ok && __all_sync(~0u, bar_wait(d_empty + 8 * (q & 1), (q >> 1 & 1) ^ 1, &stop));
+                        if (begins) ok = ok && __all_sync(~0u, bar_wait(d_empty + 8 * (q & 1), (q >> 1 & 1) ^ 1, &stop, A.waits.limit));
                         if (!ok) break;
                         tc_after();
                         const uint32_t d = M::SUMS + (q & 1) * (2 * N) + (second ? N : 0), full = d_full + 8 * (q & 1);
@@ -948,7 +949,7 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
         // the instructions under way, before tensor memory is given back
         if (elected()) tc_commit(last_bar);
         __syncwarp();
-        bar_wait(last_bar, 0, &stop);
+        bar_wait(last_bar, 0, &stop, A.waits.limit);
     }
     if (C.split > 1 && (warp < M::SCALE || warp >= M::LAY)) {
         __syncwarp();
@@ -1099,7 +1100,7 @@ extern "C" dbs_status dbs_w4_linear(const void *x, dbs_dtype dtype, int64_t toke
     if (!y || (n > 0 && (!x || !q || !scales)) || x_stride < 0 || q_stride < 0 || scale_stride < 0 ||
         (zeros && zero_stride < 0) || (tokens > 1 && y_stride < m))
         return DBS_ERR_INVALID_ARG;
-    const W4 A{x, q, scales, zeros, y, tokens, x_stride, q_stride, scale_stride, zero_stride, m, n, y_stride, group};
+    const W4 A{x, q, scales, zeros, y, tokens, x_stride, q_stride, scale_stride, zero_stride, m, n, y_stride, group, waits()};
     cudaStream_t s = (cudaStream_t)stream;
     return dtype == DBS_F32   ? launch_scales<float>(A, scale_dtype, s)
            : dtype == DBS_F16 ? launch_scales<__half>(A, scale_dtype, s)

@@ -590,6 +590,13 @@ dbs_status dbs_penalize_logits(const dbs_logits_args *a, void *stream);
  * not thread-safe with respect to concurrent builds; for tests. */
 dbs_status dbs_debug_fail_alloc(int64_t k, int64_t *previous);
 
+/* Test hook: the limit of the waits inside the operators' kernels (2 s to begin
+ * with), and the block of each later launch whose waits are made to run out
+ * (-1: none, -2: all).  No GPU fault is involved: the block gives up and
+ * leaves NaN.  Process-wide; DBS_ERR_INVALID_ARG for limits below 1 ns or above
+ * 2 s and other blocks below 0. */
+dbs_status dbs_debug_operator_waits(int64_t limit_ns, int32_t block);
+
 /* Human-readable name of a status. */
 const char *dbs_status_string(dbs_status s);
 

@@ -71,3 +71,59 @@ def test_appending_to_caches_without_entries():
     for pages, size in ((5, 0), (0, 16), (0, 0)):
         c = torch.zeros((pages, size, 2, 64), **f)
         assert torch.equal(dbs.rotary_append(q, n, n, table, pos, c, c.clone(), pos), dbs.rotary(q, None, table, pos)[0])
+
+
+class waits_run_out:
+    """Waits of one block of each launch (-2: of all blocks) run out, after a millisecond."""
+
+    def __init__(self, block):
+        self.block = block
+
+    def __enter__(self):
+        assert dbs._lib.load().dbs_debug_operator_waits(1_000_000, self.block) == 0
+
+    def __exit__(self, *_):
+        torch.cuda.synchronize()
+        assert dbs._lib.load().dbs_debug_operator_waits(2_000_000_000, -1) == 0
+
+
+@pytest.mark.parametrize("page", [16, 1])                                  # tiled copies, and others
+@pytest.mark.parametrize("B,T,hq,hk,D,S", [
+    (3, 12, 16, 2, 128, 700), (2, 96, 12, 2, 64, 1500), (5, 40, 8, 1, 128, 900), (2, 80, 2, 1, 256, 300), (190, 20, 8, 4, 64, 60)])
+def test_attention_that_gives_up_leaves_nan(B, T, hq, hk, D, S, page):
+    """All rows of the units that a block whose wait ran out had in hand or still ahead are NaN, the others as ever, and so
+    is the next call."""
+    g = torch.Generator(device=DEV).manual_seed(B + T)
+    per = -(-S // page)
+    q = torch.randn((B, T, hq, D), generator=g, device=DEV).half()
+    k, v = (torch.randn((B * per, page, hk, D), generator=g, device=DEV).half() for _ in range(2))
+    pages = torch.randperm(B * per, generator=g, device=DEV).to(torch.int32).view(B, per)
+    lens = torch.randint(S // 2, S + 1, (B,), generator=g, device=DEV).to(torch.int32)
+
+    def call():
+        # (memory that the scratch is likely to be given holds numbers that nobody may use)
+        junk = torch.full((1 << 24,), 0x7f7f7f7f, dtype=torch.int32, device=DEV)
+        del junk
+        out = torch.full_like(q, 5.0)
+        return dbs.tree_attention(q, k, v, lens, page_table=pages, out=out, return_lse=True)
+
+    clean, lse = call()
+    rows = min(256 if D <= 128 and T * hq // hk > 128 else 128, T * hq // hk)     # of a unit
+    for block in (-2, 0, 7):
+        with waits_run_out(block):
+            got, gl = call()
+        nan = torch.isnan(got)
+        assert (nan.all(3) == nan.any(3)).all() and (nan.any(3) == torch.isnan(gl)).all()
+        nan = nan.any(3)
+        if block == -2:
+            assert nan.all()
+        else:
+            assert nan.any()
+            keep = ~nan
+            assert torch.equal(got[keep], clean[keep]) and torch.equal(gl[keep], lse[keep])
+            # whole units: rows are tokens times the heads of a kv head
+            by_unit = nan.view(B, T, hk, hq // hk).transpose(1, 2).reshape(B, hk, -1)
+            for u in by_unit.split(rows, 2):
+                assert (u.all(2) == u.any(2)).all()
+        again, al = call()
+        assert torch.equal(again, clean) and torch.equal(al, lse)
