@@ -224,11 +224,26 @@ __device__ __forceinline__ uint32_t ld4(uint32_t a)
     return v;
 }
 
+// The copies of a warp's ring that are under way have ended, from the stage in use on.
+// (A call, so that the loop that it is left from keeps its registers.)
+__device__ __noinline__ void land(uint32_t bar, int use, uint32_t parity, uint32_t limit)
+{
+    for (int i = 0; i < STAGES; ++i) {
+        int last = 0;
+        bar_wait(bar + 8 * use, parity, &last, limit);
+        if (++use == STAGES) {
+            use = 0;
+            parity ^= 1;
+        }
+    }
+    __syncwarp();
+}
+
 // One block takes groups of rows in turn; each warp streams stages of weights
 // through its own ring of shared memory, a tiled copy (TMA) a stage, with no
 // block-wide wait, against x in shared memory: all of it, laid out once, or,
 // where it does not fit, a phase at a time.  S16: scales of 16 bits; FINE: groups
-// of 32 or 64 columns.  A wait that runs out leaves NaN.
+// of 32 or 64 columns.  A warp whose wait runs out fetches no more and leaves NaN.
 // One token, 4096 x 11008, fp32: 12.3 us for 24 MB, whose copies alone would take 3.5.
 // Bound by the warps' instructions, half of which turn codes into numbers, and, with a
 // start and a join of 4 us, by latency.
@@ -272,7 +287,7 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C, const __grid_
     auto fetch = [&]() {
         if (fg < C.groups) {
             if (elected()) {
-                bar_expect(bar + 8 * slot, STAGE);
+                bar_expect(bar + 8 * slot, STAGE + vain_bytes(A.waits));
                 stage_load(ring + slot * STAGE, &map, fs * ROWB, (int)((fg * wrs + wr) * (16 * RT)), bar + 8 * slot);
             }
             fs += C.wk;
@@ -401,7 +416,11 @@ __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C, const __grid_
                 }
                 const int k4 = turn++ & 3;
                 fetch();
-                ok = ok && bar_wait(bar + 8 * use, parity, &stop, A.waits.limit);
+                if (ok && !__all_sync(~0u, bar_wait(bar + 8 * use, parity, &stop, A.waits.limit))) {
+                    ok = false;
+                    fg = C.groups;                       // nothing more is fetched
+                    land(bar, use, parity, A.waits.limit);
+                }
                 const uint32_t w = ring + use * STAGE;
                 if (++use == STAGES) {
                     use = 0;
@@ -707,7 +726,8 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
 #pragma unroll
             for (int i = 0; i < 4; ++i) z[i] = H::magic + ((parts == 4 ? zn[i] : parts == 2 ? zn[i >> 1] : zn[0]) & 127u) * H::one;
             zero_points();
-            ok = ok && __all_sync(~0u, bar_wait(w_full + 8 * ws, wp, &stop, A.waits.limit));
+            ok = __all_sync(~0u, bar_wait(w_full + 8 * ws, wp, &stop, A.waits.limit));
+            if (!ok) break;                              // (codes that have not come are not given back)
             const int half = u & 1;
             uint4 q[4];
 #pragma unroll
@@ -719,7 +739,7 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
                 ws -= M::WS;
                 wp ^= 1;
             }
-            ok = ok && __all_sync(~0u, bar_wait(a_empty + 8 * as, ap, &stop, A.waits.limit));
+            ok = __all_sync(~0u, bar_wait(a_empty + 8 * as, ap, &stop, A.waits.limit));
             if (!ok) break;
             tc_after();
 #pragma unroll
@@ -875,12 +895,12 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
         const int stages = is_x ? M::XS : M::WS, bytes = is_x ? M::X : M::CODES;
         const uint32_t full = is_x ? x_here : w_full, empty = is_x ? x_empty : w_empty, store = is_x ? xs : codes;
         At p = begin(1);
-        int st = 0;
+        int st = 0, fetched = 0;
         uint32_t parity = 1;
         for (int n = 0; n < chunks; ++n) {
             if (!__all_sync(~0u, bar_wait(empty + 8 * st, parity, &stop, A.waits.limit))) break;
             if (elected()) {
-                bar_expect(full + 8 * st, bytes);
+                bar_expect(full + 8 * st, bytes + vain_bytes(A.waits));
                 if (is_x) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) stage_load(store + st * bytes + i * (N * 128), &xmap, p.at * 256 + 64 * i, p.pass * N, full + 8 * st);
@@ -894,6 +914,12 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
                 st = 0;
                 parity ^= 1;
             }
+            fetched = n + 1;
+        }
+        // copies under way end before their memory is given back, or taken for sums of other blocks
+        for (int n = fetched > stages ? fetched - stages : 0; n < fetched; ++n) {
+            int last = 0;
+            bar_wait(full + 8 * (n % stages), n / stages & 1, &last, A.waits.limit);
         }
     } else if (warp == M::ISSUE) {
         // ---- products ----
@@ -949,7 +975,8 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
         // the instructions under way, before tensor memory is given back
         if (elected()) tc_commit(last_bar);
         __syncwarp();
-        bar_wait(last_bar, 0, &stop, A.waits.limit);
+        int last = 0;
+        bar_wait(last_bar, 0, &last, A.waits.limit);
     }
     if (C.split > 1 && (warp < M::SCALE || warp >= M::LAY)) {
         __syncwarp();

@@ -127,3 +127,29 @@ def test_attention_that_gives_up_leaves_nan(B, T, hq, hk, D, S, page):
                 assert (u.all(2) == u.any(2)).all()
         again, al = call()
         assert torch.equal(again, clean) and torch.equal(al, lse)
+
+
+@pytest.mark.parametrize("T,m,n,dt,group", [
+    (1, 4096, 1024, torch.float32, 128), (1, 9000, 700, torch.bfloat16, 32), (7, 3000, 2050, torch.float16, 64), (9, 500, 20000, torch.float32, 256),
+    (25, 700, 3000, torch.float32, 128), (20, 4096, 4096, torch.bfloat16, 128), (24, 40000, 600, torch.float16, 64),
+    (70, 1000, 8192, torch.float16, 128), (150, 9000, 304, torch.bfloat16, 32)])
+def test_w4_that_gives_up_leaves_nan(T, m, n, dt, group):
+    """Rows of one matrix instruction's tiles, rows of clusters that share columns, rows of blocks with several units."""
+    g = torch.Generator(device=DEV).manual_seed(T + m)
+    x = torch.randn((T, n), generator=g, device=DEV).to(dt)
+    q = torch.randint(0, 256, (m, -(-n // 32) * 16), generator=g, device=DEV, dtype=torch.uint8)[:, :(n + 1) // 2]
+    s = torch.rand((m, -(-n // group)), generator=g, device=DEV)
+
+    def call():
+        return dbs.w4_linear(x, q, s, group=group, y=torch.full((T, m), 5.0, dtype=dt, device=DEV))
+
+    clean = call()
+    for block in (-2, 0, 3):
+        with waits_run_out(block):
+            y = call()
+        nan = torch.isnan(y)
+        if block == -2:
+            assert nan.all()
+        else:
+            assert nan.any() and not nan.all() and torch.equal(y[~nan], clean[~nan])
+        assert torch.equal(call(), clean)
