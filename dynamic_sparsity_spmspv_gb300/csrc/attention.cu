@@ -1318,6 +1318,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w) : "memory");
                     }
                 }
+                if (!ok) continue;                                         // (no queries came)
                 async_fence();
                 bar_arrive(q_full + 8 * r);
             }

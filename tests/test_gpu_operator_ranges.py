@@ -153,3 +153,24 @@ def test_w4_that_gives_up_leaves_nan(T, m, n, dt, group):
         else:
             assert nan.any() and not nan.all() and torch.equal(y[~nan], clean[~nan])
         assert torch.equal(call(), clean)
+
+
+def test_attention_whose_queries_wait_too_long():
+    """A limit that only the warps which load queries reach, as they wait for all scores of the unit before: what comes out is
+    right or NaN."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    B, T, hq, D, S, page = 400, 30, 4, 64, 1 << 19, 4
+    q = torch.randn((B, T, hq, D), generator=g, device=DEV).half()
+    k, v = (torch.randn((S // page, page, 1, D), generator=g, device=DEV).half() for _ in range(2))
+    pages = torch.arange(S // page, dtype=torch.int32, device=DEV).expand(B, -1).contiguous()
+    lens = torch.full((B,), S, dtype=torch.int32, device=DEV)
+    clean = dbs.tree_attention(q, k, v, lens, page_table=pages)
+    lib = dbs._lib.load()
+    assert lib.dbs_debug_operator_waits(20_000, -1) == 0
+    try:
+        got = dbs.tree_attention(q, k, v, lens, page_table=pages)
+        torch.cuda.synchronize()
+    finally:
+        lib.dbs_debug_operator_waits(2_000_000_000, -1)
+    nan = torch.isnan(got)
+    assert (nan | (got == clean)).all()
