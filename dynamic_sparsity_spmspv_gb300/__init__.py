@@ -370,6 +370,16 @@ class SpMVPlan:
             pass
 
 
+def dbs_operators_check(stream=None) -> int:
+    """dbs_operators_check: synchronizes the stream and returns 4
+    (DBS_ERR_TIMEOUT), once, if a wait inside a kernel of w4_linear or
+    tree_attention ran out since the last check (its results are NaN), else 0."""
+    return int(_lib.load().dbs_operators_check(_stream_handle(stream)))
+
+
+operators_check = dbs_operators_check
+
+
 _DECODING = ("w4_linear", "rotary_table", "rotary", "rotary_append", "tree_attention", "penalize_logits")
 
 

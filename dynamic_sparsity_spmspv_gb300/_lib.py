@@ -83,6 +83,7 @@ PROTOTYPES = {
     "dbs_tree_attention_scratch": (I32, [P, P]),
     "dbs_tree_attention": (I32, [P, P]),
     "dbs_penalize_logits": (I32, [P, P]),
+    "dbs_operators_check": (I32, [P]),
     "dbs_bfs": (I32, [P, I64, P, P, ctypes.c_int, P, P]),
     "dbs_last_stats": (I32, [P, P, P]),
     "dbs_selftest_wait_timeout": (I32, [P, P]),

@@ -928,8 +928,8 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
 // over S and tiles of 64: 177; one warp issuing for both row tiles: 179.  A share of
 // the powers of two by polynomial made it slower (186 us and more).
 //
-// Every wait on a barrier has a limit; a block whose wait runs out stops and leaves NaN
-// in the rows of all units, or parts of units, that it had not finished.
+// Every wait on a barrier has a limit; a block whose wait runs out stops, leaves NaN in
+// the rows of all units, or parts of units, that it had not finished, and says so.
 
 template <int DP, int TILES> struct Many {
     static constexpr int KEYS = DP == 256 || TILES == 2 ? 64 : 128;
@@ -1558,6 +1558,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
         tc_after();
         tc_free(tmem);
     }
+    if (tid == 0 && stop) ran_out = 1;
 }
 
 // ---- host ----
@@ -1769,6 +1770,12 @@ bool args_ok(const dbs_attention_args *a)
 }  // namespace
 
 extern "C" {
+
+dbs_status dbs_operators_check(void *stream)
+{
+    const dbs_status here = waits_since((cudaStream_t)stream), w4 = w4_waits_since((cudaStream_t)stream);
+    return here == DBS_ERR_CUDA ? here : w4 != DBS_OK ? w4 : here;
+}
 
 dbs_status dbs_debug_operator_waits(int64_t limit_ns, int32_t block)
 {

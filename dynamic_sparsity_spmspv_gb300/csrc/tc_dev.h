@@ -5,6 +5,23 @@
 
 namespace dbs::ops {
 
+// A wait of this file's kernels ran out since it was last asked for.
+static __device__ int ran_out;
+static dbs_status waits_since(cudaStream_t s)
+{
+    int was = 0;
+    const int none = 0;
+    if (cudaMemcpyFromSymbolAsync(&was, ran_out, sizeof was, 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess ||
+        (was && (cudaMemcpyToSymbolAsync(ran_out, &none, sizeof none, 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+                 cudaStreamSynchronize(s) != cudaSuccess))) {
+        cudaGetLastError();
+        return DBS_ERR_CUDA;
+    }
+    return was ? DBS_ERR_TIMEOUT : DBS_OK;
+}
+dbs_status w4_waits_since(cudaStream_t s);
+
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
 {
     uint32_t done;

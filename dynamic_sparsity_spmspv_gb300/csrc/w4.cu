@@ -224,10 +224,11 @@ __device__ __forceinline__ uint32_t ld4(uint32_t a)
     return v;
 }
 
-// The copies of a warp's ring that are under way have ended, from the stage in use on.
+// After a wait ran out: the copies of a warp's ring that are under way have ended, from the stage in use on.
 // (A call, so that the loop that it is left from keeps its registers.)
 __device__ __noinline__ void land(uint32_t bar, int use, uint32_t parity, uint32_t limit)
 {
+    ran_out = 1;
     for (int i = 0; i < STAGES; ++i) {
         int last = 0;
         bar_wait(bar + 8 * use, parity, &last, limit);
@@ -990,6 +991,7 @@ __global__ void __launch_bounds__(Many<N>::NT, 1) k_w4_many(W4 A, Walk C, const 
         tc_after();
         tc_free(tmem);
     }
+    if (threadIdx.x == 0 && stop) ran_out = 1;
 }
 
 // The weights as rows of bytes, in stages of `columns` bytes of `rows` rows.
@@ -1114,6 +1116,8 @@ dbs_status launch_scales(const W4 &A, dbs_dtype sd, cudaStream_t s)
 }
 
 }  // namespace
+
+dbs_status dbs::ops::w4_waits_since(cudaStream_t s) { return waits_since(s); }
 
 extern "C" dbs_status dbs_w4_linear(const void *x, dbs_dtype dtype, int64_t tokens, int64_t x_stride, const uint8_t *q,
                                     int64_t q_stride, const void *scales, dbs_dtype scale_dtype, int64_t scale_stride,

@@ -12,8 +12,9 @@ library's kernels, and the binding (csrc/binding.cpp) only checks and marshals
 them.  An argument that does not fit raises DbsError (DBS_ERR_INVALID_ARG).
 Calls are asynchronous on `stream` (a torch stream or a cudaStream_t; default:
 the current stream); what they return is allocated on that stream, and the
-caller orders its own use of tensors on other streams.  Nothing is recorded for
-autograd.
+caller orders its own use of tensors on other streams.  A kernel whose wait runs
+out (after two seconds) leaves NaN, and operators_check reports it.  Nothing is
+recorded for autograd.
 """
 from __future__ import annotations
 

@@ -429,7 +429,17 @@ dbs_status dbs_spmspv_dense_noalloc_check(void *stream);
  * graph and give identical bits when repeated.  Strides are in elements (of
  * bytes for 4-bit codes); the innermost dimension is contiguous.  Sums,
  * softmax statistics and rotations are fp32; every result is rounded once, to
- * its own type. */
+ * its own type.
+ *
+ * Waits inside the kernels of dbs_w4_linear and dbs_tree_attention end after two
+ * seconds: the block gives up and leaves NaN in what it had not finished (in lse
+ * too). */
+
+/* Whether such a wait ran out on the current device since the last check, in
+ * calls on `stream` or calls that have ended: synchronizes the stream and returns
+ * DBS_ERR_TIMEOUT, once, or DBS_OK.  DBS_ERR_CUDA. */
+dbs_status dbs_operators_check(void *stream);
+
 typedef enum { DBS_F32 = 0, DBS_F16 = 1, DBS_BF16 = 2 } dbs_dtype;
 
 /* Linear layer with 4-bit weights and group scales, for one or a few tokens:

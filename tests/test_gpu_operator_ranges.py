@@ -174,3 +174,25 @@ def test_attention_whose_queries_wait_too_long():
         lib.dbs_debug_operator_waits(2_000_000_000, -1)
     nan = torch.isnan(got)
     assert (nan | (got == clean)).all()
+
+
+def test_waits_that_run_out_are_reported_once():
+    f = dict(device=DEV)
+    codes = torch.zeros((4096, 512), dtype=torch.uint8, **f)
+    scales, q = torch.ones((4096, 8), **f), torch.ones((2, 40, 8, 64), dtype=torch.float16, **f)
+    cache, lens = torch.ones((2, 300, 2, 64), dtype=torch.float16, **f), torch.full((2,), 300, dtype=torch.int32, **f)
+    calls = [lambda: dbs.w4_linear(torch.ones((1, 1024), **f), codes, scales), lambda: dbs.w4_linear(torch.ones((20, 1024), **f).half(), codes, scales),
+             lambda: dbs.w4_linear(torch.ones((50, 1024), **f).half(), codes, scales), lambda: dbs.tree_attention(q, cache, cache, lens)]
+    side = torch.cuda.Stream()
+    dbs.operators_check()                                                  # (what earlier tests left)
+    for call in calls:
+        call()
+        assert dbs.operators_check() == 0
+        with waits_run_out(0):
+            call()
+        assert dbs.operators_check() == 4 and dbs.operators_check(side) == 0
+        with waits_run_out(-2), torch.cuda.stream(side):
+            call()
+        assert dbs.operators_check(side) == 4 and dbs.operators_check() == 0
+        call()
+        assert dbs.operators_check() == 0
