@@ -202,7 +202,7 @@ dbs_status launch_units(const Rotary &A, cudaStream_t s)
                 threads += A.total * units * n;
                 most = most > A.total * units ? most : A.total * units;
             }
-        if (span == 1 || threads >= 152 * 2048) break;
+        if (span == 1 || threads >= 152 * 2048 || 2 * chunks > 65535) break;      // (the grid's limit in y)
     }
     k_rotary<T, INTERLEAVED, WIDE><<<dim3((unsigned)((most + NT - 1) / NT), (unsigned)chunks), NT, 0, s>>>(A, (uint32_t)turning, span);
     return launched();

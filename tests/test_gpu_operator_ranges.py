@@ -196,3 +196,26 @@ def test_waits_that_run_out_are_reported_once():
         assert dbs.operators_check(side) == 4 and dbs.operators_check() == 0
         call()
         assert dbs.operators_check() == 0
+
+
+@pytest.mark.parametrize("tokens,D,R", [(1, 64, 32), (3, 4, 2), (1, 8, 8)])
+def test_rotary_of_as_many_heads_as_there_may_be(tokens, D, R):
+    """16384 heads in each group, of which parts are turned and parts copied."""
+    rng = np.random.default_rng(D)
+    H = 16384
+    table = torch.from_numpy(rng.standard_normal((9, R)).astype(np.float32)).to(DEV)
+    q, k, v = (torch.from_numpy(rng.standard_normal((tokens, H, D)).astype(np.float32)).to(DEV) for _ in range(3))
+    pos = torch.arange(tokens, dtype=torch.int32, device=DEV)
+    kc, vc = torch.zeros((tokens, 2, H, D), device=DEV), torch.zeros((tokens, 2, H, D), device=DEV)
+    qo = dbs.rotary_append(q, k, v, table, pos, kc, vc, 2 * pos + 1)
+    c, s = (t.double()[pos.long()][:, None] for t in table.split(R // 2, 1))
+
+    def turned(x):
+        a, b, rest = x.double().split([R // 2, R // 2, D - R], 2)
+        return torch.cat([a * c - b * s, a * s + b * c, rest], 2), torch.cat([(a * c).abs() + (b * s).abs(), (a * s).abs() + (b * c).abs(), rest * 0], 2)
+
+    for got, x in ((qo, q), (kc[:, 1], k)):
+        ref, size = turned(x)
+        # two products and a sum, rounded to 32 bits
+        assert ((got.double() - ref).abs() <= 3 * 2.0**-24 * size).all()
+    assert torch.equal(vc[:, 1], v) and (kc[:, 0] == 0).all() and (vc[:, 0] == 0).all()
