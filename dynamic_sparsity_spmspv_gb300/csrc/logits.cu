@@ -35,7 +35,7 @@ constexpr int WIDTH_MAX = 65536, COUNTS_MAX = 16384;
 // Narrow slices, for calls whose blocks all run at once: a word of shared memory
 // for each entry.  A slice's first logits and history entries are under way before
 // the first wait; what is left is a chain of a few waits (one row of 32,000 with 700
-// tokens: 6 us back to back), or, where the history is long, its atomics (12 rows of
+// tokens: 6.1 us back to back), or, where the history is long, its atomics (12 rows of
 // 100,003 with 20,000 tokens: 10.2 us; k_logits_wide takes 19.4).
 template <class T, class O>
 __global__ void __launch_bounds__(NT, 2) k_logits_narrow(dbs_logits_args A, int width)
@@ -104,8 +104,6 @@ __global__ void __launch_bounds__(NT, 2) k_logits_narrow(dbs_logits_args A, int 
                 if (atomicMin(&first[ids[i] - v0], (unsigned)i) != NONE) listed_again = 1;
     }
     const float rep = A.repetition ? A.repetition[b] : 1.f, pres = A.presence ? A.presence[b] : 0.f;
-    // (a row's reciprocal once, instead of a division for each repeated token: 2 roundings for 1)
-    const float down = 1.f / rep;
     const float freq = A.frequency ? A.frequency[b] : 0.f;
     const unsigned *allowed = A.allowed ? (const unsigned *)A.allowed + b * A.allowed_stride : nullptr;
     const int last_word = (int)((A.vocab - 1) >> 5);
@@ -129,8 +127,10 @@ __global__ void __launch_bounds__(NT, 2) k_logits_narrow(dbs_logits_args A, int 
         if (any) {
 #pragma unroll
             for (int e = 0; e < RUN; ++e) {
+                // (a division, not a product with the row's reciprocal: that is rounded twice, and infinite for
+                // penalties below 2^-128; it took 5.9 us for one row of 32,000, this takes 6.1)
                 const unsigned n = c[e] & ~(SEEN | BIAS);
-                if (c[e] & ~BIAS) l[e] *= l[e] > 0.f ? down : rep;
+                if (c[e] & ~BIAS) l[e] = l[e] > 0.f ? l[e] / rep : l[e] * rep;
                 if (n) l[e] -= fmaf(freq, (float)n, pres);
             }
             if (any & BIAS) {
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(NT, 2) k_logits_narrow(dbs_logits_args A, int 
 // table, whose words are claimed by compare and swap, took 15 us for 4096 tokens
 // of four warps), and there is room for a slice of 65536 entries.  The others read, mask and write every
 // entry as it is, in runs of eight, and the first ones help them then: bound by
-// HBM (96 rows of 128,000 with 4096 tokens: 26.7 us; k_logits_narrow takes 38.1, in
+// HBM (96 rows of 128,000 with 4096 tokens: 27.5 us; k_logits_narrow takes 38.1, in
 // six waves of blocks).  Last the marked entries, few against the slice, are computed again with
 // penalties and biases and written over.  Their logits are read a second time:
 // where out is the logits themselves, an entry that the first part changed is a
@@ -364,8 +364,6 @@ __global__ void __launch_bounds__(NT, 2) k_logits_wide(dbs_logits_args A, Cut C)
     __syncthreads();
 
     // ---- the marked entries ----
-    // (a row's reciprocal once, instead of a division for each repeated token: 2 roundings for 1)
-    const float down = 1.f / rep;
     for (int i = threadIdx.x; i < listed; i += NT) {
         const int v = low + (int)list[i];
         const unsigned c = count[i], n = c & ~(SEEN | BIAS), k = c & BIAS ? first[i] : 0u;
@@ -373,7 +371,7 @@ __global__ void __launch_bounds__(NT, 2) k_logits_wide(dbs_logits_args A, Cut C)
         const float add = c & BIAS ? vals[k] : 0.f;
         float l = to_f32(x[v]);
         if (!(mask >> (v & 31) & 1u)) continue;
-        if (c & ~BIAS) l *= l > 0.f ? down : rep;
+        if (c & ~BIAS) l = l > 0.f ? l / rep : l * rep;
         if (n) l -= fmaf(freq, (float)n, pres);
         if (c & BIAS) {
             l += add;

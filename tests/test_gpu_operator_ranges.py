@@ -219,3 +219,22 @@ def test_rotary_of_as_many_heads_as_there_may_be(tokens, D, R):
         # two products and a sum, rounded to 32 bits
         assert ((got.double() - ref).abs() <= 3 * 2.0**-24 * size).all()
     assert torch.equal(vc[:, 1], v) and (kc[:, 0] == 0).all() and (vc[:, 0] == 0).all()
+
+
+@pytest.mark.parametrize("B", [2, 200])
+def test_penalize_logits_of_any_repetition(B):
+    """Penalties whose reciprocal is no normal number, or none at all; a quotient is rounded once.  B: slices of both kinds."""
+    V, L = 40001, 64
+    rng = np.random.default_rng(B)
+    x = (rng.standard_normal((B, V)) * 4).astype(np.float32)
+    hist = np.stack([rng.choice(V, L, replace=False) for _ in range(B)]).astype(np.int32)
+    rep = np.resize(np.array([1e-39, 3e38, 1.1, 3.0, 1.3, 7e-42, 2.0**127], np.float32), B)
+    x[rep < 1e-30] *= np.float32(1e-12)
+    y = dbs.penalize_logits(torch.from_numpy(x).to(DEV), history=torch.from_numpy(hist).to(DEV), repetition=torch.from_numpy(rep).to(DEV))
+    ref = x.copy()
+    for b in range(B):
+        l = x[b, hist[b]]
+        with np.errstate(over="ignore", under="ignore"):
+            ref[b, hist[b]] = np.where(l > 0, (l.astype(np.float64) / np.float64(rep[b])).astype(np.float32),
+                                       (l.astype(np.float64) * np.float64(rep[b])).astype(np.float32))
+    assert np.array_equal(y.cpu().numpy(), ref)
