@@ -1760,7 +1760,7 @@ bool args_ok(const dbs_attention_args *a)
         return false;
     if (a->batch == 0 || a->tokens == 0) return true;
     const int64_t entries = a->max_pages * a->page_size;
-    if (entries >= (int64_t(1) << 31)) return false;
+    if (entries > (int64_t(1) << 31) - 1024) return false;               // (an entry's number and a tile's end are ints)
     if (!a->q || !a->out || !a->kv_lens) return false;
     if (entries > 0 && (!a->k || !a->v || a->pages < 1)) return false;
     if (!a->page_table && (a->max_pages > 1 || (entries > 0 && a->pages < a->batch))) return false;

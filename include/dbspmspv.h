@@ -540,7 +540,7 @@ typedef struct {
     const int32_t *page_table; /* device [batch, max_pages], rows page_row apart: page of entry
                                   j is page_table[b, j / page_size], clamped to [0, pages);
                                   NULL: sequence b is page b */
-    int64_t max_pages, page_row;
+    int64_t max_pages, page_row;  /* max_pages * page_size at most 2^31 - 1024 */
     const int32_t *kv_lens;    /* device [batch]; clamped to [0, max_pages * page_size] */
     const int32_t *tree_lens;  /* device [batch]; clamped to [0, tokens]; NULL = tokens */
     const int64_t *tree;       /* device [batch, tokens, ceil(tokens / 64)], contiguous, or NULL */
