@@ -1763,6 +1763,13 @@ bool args_ok(const dbs_attention_args *a)
     if (entries > (int64_t(1) << 31) - 1024) return false;               // (an entry's number and a tile's end are ints)
     if (!a->q || !a->out || !a->kv_lens) return false;
     if (entries > 0 && (!a->k || !a->v || a->pages < 1)) return false;
+    for (int64_t stride : {a->q_batch, a->q_token, a->q_head, a->k_page, a->k_entry, a->k_head, a->v_page, a->v_entry, a->v_head,
+                           a->page_row, a->o_batch, a->o_token, a->o_head})
+        if (stride < 0) return false;
+    // heads of out that share memory
+    if ((a->q_heads > 1 && a->o_head < a->head_dim) || (a->tokens > 1 && a->o_token < a->head_dim) ||
+        (a->batch > 1 && a->o_batch < a->head_dim))
+        return false;
     if (!a->page_table && (a->max_pages > 1 || (entries > 0 && a->pages < a->batch))) return false;
     return true;
 }

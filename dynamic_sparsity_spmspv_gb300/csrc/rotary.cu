@@ -305,6 +305,13 @@ dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype d
             return DBS_ERR_INVALID_ARG;
         if (work && P.to_slots && pages == 0) continue;                        // no slot is inside: nothing is written
         if (work && !P.out) return DBS_ERR_INVALID_ARG;
+        // heads of the output that share memory, or another head's place of the input
+        const int64_t n_batch = P.to_slots ? pages : batch, n_token = P.to_slots ? page_size : tokens;
+        const bool apart = (P.heads == 1 || P.out_head >= head_dim) && (n_token == 1 || P.out_token >= head_dim) &&
+                           (n_batch == 1 || P.out_batch >= head_dim);
+        const bool placed = P.in != P.out || (!P.to_slots && (P.heads == 1 || P.in_head == P.out_head) &&
+                                              (tokens == 1 || P.in_token == P.out_token) && (batch == 1 || P.in_batch == P.out_batch));
+        if (work && (P.in_head < 0 || P.in_token < 0 || P.in_batch < 0 || !apart || !placed)) return DBS_ERR_INVALID_ARG;
         A.part[A.nparts++] = P;
         heads += P.heads;
     }

@@ -427,9 +427,9 @@ dbs_status dbs_spmspv_dense_noalloc_check(void *stream);
  * the DB-Decoding layer; the paper has no counterpart.  All calls are ASYNC,
  * allocate nothing, hold no state between calls, can be captured in a CUDA
  * graph and give identical bits when repeated.  Strides are in elements (of
- * bytes for 4-bit codes); the innermost dimension is contiguous.  Sums,
- * softmax statistics and rotations are fp32; every result is rounded once, to
- * its own type.
+ * bytes for 4-bit codes) and not negative; the innermost dimension is contiguous.
+ * Sums, softmax statistics and rotations are fp32; every result is rounded once,
+ * to its own type.
  *
  * Waits inside the kernels of dbs_w4_linear and dbs_tree_attention end after two
  * seconds: the block gives up and leaves NaN in what it had not finished (in lse
@@ -487,7 +487,7 @@ dbs_status dbs_rotary_table(int64_t positions, int32_t dim, double base, dbs_rot
  * ptr + b * batch_stride + t * token_stride + h * head_stride + c. */
 typedef struct {
     const void *in;
-    void *out;                 /* may be `in` (in place), else must not overlap it */
+    void *out;                 /* may be `in` (in place, with its strides), else must not overlap it */
     int64_t in_batch, in_token, in_head;
     int64_t out_batch, out_token, out_head;
     int32_t heads;             /* 0 = absent */
@@ -511,7 +511,8 @@ typedef struct {
  *   head_dim   entries of a head, dim <= head_dim <= 1024, dim even
  *   batch * tokens < 2^31, and times head_dim < 2^32 - 256; at most 16384 heads
  *   in a group
- * Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */
+ * Errors: DBS_ERR_INVALID_ARG (heads of an output that share memory among
+ * them), DBS_ERR_CUDA. */
 dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype dtype, int64_t batch, int64_t tokens,
                       int32_t head_dim, int32_t dim, const float *table, int64_t table_rows, const int32_t *positions,
                       const int32_t *slots, int64_t pages, int64_t page_size, int32_t interleaved,
@@ -545,7 +546,7 @@ typedef struct {
     const int32_t *tree_lens;  /* device [batch]; clamped to [0, tokens]; NULL = tokens */
     const int64_t *tree;       /* device [batch, tokens, ceil(tokens / 64)], contiguous, or NULL */
     float scale;               /* finite */
-    void *out;                 /* [batch, tokens, q_heads, head_dim] */
+    void *out;                 /* [batch, tokens, q_heads, head_dim], each head in a place of its own */
     int64_t o_batch, o_token, o_head;
     float *lse;                /* device [batch, tokens, q_heads], natural logarithm, or NULL */
     void *scratch;             /* device, 32-byte aligned, dbs_tree_attention_scratch bytes; the

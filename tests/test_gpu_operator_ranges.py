@@ -238,3 +238,18 @@ def test_penalize_logits_of_any_repetition(B):
             ref[b, hist[b]] = np.where(l > 0, (l.astype(np.float64) / np.float64(rep[b])).astype(np.float32),
                                        (l.astype(np.float64) * np.float64(rep[b])).astype(np.float32))
     assert np.array_equal(y.cpu().numpy(), ref)
+
+
+def test_outputs_that_share_memory_are_refused():
+    f = dict(dtype=torch.float16, device=DEV)
+    h, cache, ids = torch.ones((4, 2, 64), **f), torch.ones((4, 2, 2, 64), **f), torch.zeros(4, dtype=torch.int32, device=DEV)
+    table, same = torch.zeros((9, 64), device=DEV), torch.zeros((1, 1, 64), **f)
+    for call in (lambda: dbs.rotary(h, h, table, ids, q_out=same.expand(4, 2, 64)), lambda: dbs.rotary(h, h, table, ids, k_out=same.expand(4, 2, 64)),
+                 lambda: dbs.rotary_append(h, h, h, table, ids, same.expand(4, 2, 2, 64), cache, ids),
+                 lambda: dbs.tree_attention(h[None], cache[:1], cache[:1], ids[:1], out=same.expand(1, 4, 2, 64)),
+                 lambda: dbs.penalize_logits(h[0], out=same[0].expand(2, 64)),
+                 lambda: dbs.w4_linear(h[:, 0], torch.zeros((8, 32), dtype=torch.uint8, device=DEV), torch.ones((8, 1), device=DEV), group=64,
+                                       y=same[0, :, :8].expand(4, 8))):
+        with pytest.raises(dbs.DbsError) as e:
+            call()
+        assert e.value.status == 1
