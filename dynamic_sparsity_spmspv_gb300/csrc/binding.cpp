@@ -7,6 +7,7 @@
 #include <cmath>
 #include <string>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -126,6 +127,8 @@ struct Call {
         if (!THPVariable_Check(o)) bad(fn, std::string(name) + " has to be a CUDA tensor");
         const at::Tensor &t = THPVariable_Unpack(o);
         if (!t.is_cuda()) bad(fn, std::string(name) + " has to be a CUDA tensor");
+        if (t.requires_grad() && at::GradMode::is_enabled())
+            bad(fn, std::string(name) + " requires a gradient, and nothing is recorded for autograd: detach it, or call under torch.no_grad()");
         const int d = t.get_device();
         if (dev < 0) {
             dev = d;
@@ -194,6 +197,12 @@ struct Call {
 
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
 
+// A tensor of the caller's that the call writes: autograd has to know if it was saved for a gradient.
+void written(const at::Tensor &t)
+{
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Runs a binding's body; a C++ exception becomes a Python one.
 template <class F>
 PyObject *guarded(F f)
@@ -254,6 +263,7 @@ PyObject *w4_linear(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObjec
         check(c.fn, dbs_w4_linear(x.data_ptr(), dt, tokens, one ? n : x.stride(0), (const uint8_t *)q.data_ptr(), qs, s.data_ptr(), sd,
                                   ss, z ? (const uint8_t *)z->data_ptr() : nullptr, zs, m, n, (int32_t)group, y.data_ptr(), ys,
                                   c.stream));
+        if (given) written(y);
         return wrap(y);
     });
 }
@@ -358,6 +368,8 @@ PyObject *rotary(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObject *
         check(c.fn, dbs_rotary(parts, k ? 2 : 1, dt, Q.b, Q.n, (int32_t)Q.d, (int32_t)table.size(1), table.data_ptr<float>(),
                                table.size(0), pos.data_ptr<int32_t>(), nullptr, 0, 1, truth(a.v[4], false), truth(a.v[5], false),
                                c.stream));
+        if (qg) written(qo);
+        if (k && kg) written(ko);
         PyObject *r = PyTuple_New(2);
         if (!r) throw Failed();
         PyTuple_SET_ITEM(r, 0, wrap(qo));
@@ -390,6 +402,9 @@ PyObject *rotary_append(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyO
         check(c.fn, dbs_rotary(parts, 3, dt, Q.b, Q.n, (int32_t)Q.d, (int32_t)table.size(1), table.data_ptr<float>(), table.size(0),
                                pos.data_ptr<int32_t>(), slots.data_ptr<int32_t>(), room ? KC.b : 0, room ? KC.n : 1,
                                truth(a.v[8], false), 0, c.stream));
+        if (qg) written(qo);
+        written(kc);
+        written(vc);
         return wrap(qo);
     });
 }
@@ -468,6 +483,7 @@ PyObject *tree_attention(PyObject *, PyObject *const *args, Py_ssize_t nargs, Py
             A.scratch = scratch.data_ptr();
         }
         check(c.fn, dbs_tree_attention(&A, c.stream));
+        if (given) written(out);
         if (!want_lse) return wrap(out);
         PyObject *r = PyTuple_New(2);
         if (!r) throw Failed();
@@ -531,6 +547,7 @@ PyObject *penalize_logits(PyObject *, PyObject *const *args, Py_ssize_t nargs, P
         A.out_stride = c.rows("out", out, B, V, out.scalar_type());
         A.out = out.data_ptr();
         check(c.fn, dbs_penalize_logits(&A, c.stream));
+        if (given) written(out);
         return wrap(out);
     });
 }

@@ -14,7 +14,8 @@ Calls are asynchronous on `stream` (a torch stream or a cudaStream_t; default:
 the current stream); what they return is allocated on that stream, and the
 caller orders its own use of tensors on other streams.  A kernel whose wait runs
 out (after two seconds) leaves NaN, and operators_check reports it.  Nothing is
-recorded for autograd.
+recorded for autograd: a tensor that requires a gradient is refused where
+gradients are recorded, and tensors written in place count as changed.
 """
 from __future__ import annotations
 

@@ -253,3 +253,54 @@ def test_outputs_that_share_memory_are_refused():
         with pytest.raises(dbs.DbsError) as e:
             call()
         assert e.value.status == 1
+
+
+def test_gradients_are_never_lost_in_silence():
+    """What would need a gradient is refused where autograd records, and what is written in place counts as changed."""
+    f = dict(device=DEV)
+    x, codes, scales = torch.ones((2, 64), **f), torch.zeros((8, 32), dtype=torch.uint8, **f), torch.ones((8, 1), **f)
+    h, cache = torch.ones((4, 2, 64), dtype=torch.float16, **f), torch.zeros((2, 16, 2, 64), dtype=torch.float16, **f)
+    ids, table = torch.zeros(4, dtype=torch.int32, **f), torch.zeros((9, 64), **f)
+    slots = torch.arange(4, dtype=torch.int32, **f)
+    one = torch.ones(2, **f)
+    calls = [lambda g: dbs.w4_linear(g(x), codes, scales, group=64), lambda g: dbs.w4_linear(x, codes, g(scales), group=64),
+             lambda g: dbs.rotary(g(h), None, table, ids), lambda g: dbs.rotary(h, g(h), table, ids), lambda g: dbs.rotary(h, h, g(table), ids),
+             lambda g: dbs.rotary_append(h, h, g(h), table, ids, cache, cache.clone(), slots),
+             lambda g: dbs.tree_attention(g(h[None]), cache[:1], cache[:1], ids[:1]),
+             lambda g: dbs.tree_attention(h[None], cache[:1], g(cache[:1]), ids[:1]),
+             lambda g: dbs.penalize_logits(g(x)), lambda g: dbs.penalize_logits(x, history=codes[:2, :3].int(), repetition=g(one))]
+    for call in calls:
+        with pytest.raises(dbs.DbsError) as e:
+            call(lambda t: t.clone().requires_grad_())
+        assert e.value.status == 1
+        call(lambda t: t)
+        with torch.no_grad():
+            call(lambda t: t.clone().requires_grad_())
+    with torch.inference_mode():
+        t, y = torch.ones((2, 64), **f), torch.empty((2, 8), **f)
+        dbs.w4_linear(t, codes, scales, group=64, y=y)
+    assert torch.equal(dbs.w4_linear(t, codes, scales, group=64), dbs.w4_linear(x, codes, scales, group=64))
+
+    def changed(t, call):
+        before = t._version
+        call()
+        assert t._version > before
+
+    y, kc, vc, q = torch.empty((2, 8), **f), cache.clone(), cache.clone(), h.clone()
+    changed(y, lambda: dbs.w4_linear(x, codes, scales, group=64, y=y))
+    for t in (q, kc, vc):
+        changed(t, lambda: dbs.rotary_append(q, h, h, table, ids, kc, vc, slots, q_out=q))
+    changed(q, lambda: dbs.rotary(h, h, table, ids, q_out=q))
+    k2 = h.clone()
+    changed(k2, lambda: dbs.rotary(h, h, table, ids, k_out=k2))
+    o = h[None].clone()
+    changed(o, lambda: dbs.tree_attention(h[None], cache[:1], cache[:1], ids[:1], out=o))
+    l = x.clone()
+    changed(l, lambda: dbs.penalize_logits(l, out=l))
+    # a saved tensor that was overwritten
+    w = torch.ones((2, 64), requires_grad=True, **f)
+    s = x.clone()
+    z = (w * s).sum()
+    dbs.penalize_logits(s, out=s)
+    with pytest.raises(RuntimeError):
+        z.backward()
