@@ -1715,13 +1715,7 @@ dbs_status launch_kind(const Attn &A, const Plan &P, const Maps &maps, cudaStrea
 {
     using M = Many<DP, TILES>;
     static Once once;
-    // (the warps share out the registers that a block starts with, so there have to be
-    // that many, or their waits for them would not end)
-    static const bool shares = [] {
-        cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, k_attn_many<T, DP, TILES, BOXES>) == cudaSuccess && (TILES == 1 || f.numRegs == M::REGS);
-    }();
-    if (!shares || !room_for(once, k_attn_many<T, DP, TILES, BOXES>, M::SMEM)) return DBS_ERR_CUDA;
+    if (!room_for(once, k_attn_many<T, DP, TILES, BOXES>, M::SMEM, false, TILES == 2 ? M::REGS : 0)) return DBS_ERR_CUDA;
     k_attn_many<T, DP, TILES, BOXES><<<P.blocks, M::NT, M::SMEM, s>>>(A, P.share, maps);
     const dbs_status st = launched();
     return st == DBS_OK ? launch_join<T>(A, P, s) : st;

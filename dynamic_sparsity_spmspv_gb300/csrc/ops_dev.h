@@ -108,23 +108,23 @@ __device__ __forceinline__ bool elected()
 }
 
 // Tensor maps for tiled copies, made by the driver (whose entry point is looked
-// up once; no library is linked for it).
+// up until it is found; no library is linked for it).
 typedef CUresult (*encode_tiled_fn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                     const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                     CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 inline encode_tiled_fn encode_tiled()
 {
-    static const encode_tiled_fn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            p = nullptr;
-        }
-        return (encode_tiled_fn)p;
-    }();
-    return fn;
+    static std::atomic<encode_tiled_fn> found{nullptr};
+    if (const encode_tiled_fn fn = found.load(std::memory_order_relaxed)) return fn;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    found.store((encode_tiled_fn)p, std::memory_order_relaxed);
+    return (encode_tiled_fn)p;
 }
 
 inline bool dtype_ok(int32_t d) { return d == DBS_F32 || d == DBS_F16 || d == DBS_BF16; }
@@ -148,20 +148,25 @@ inline int multiprocessors()
     return n;
 }
 // Room for a kernel's dynamic shared memory, and leave for clusters of more than eight
-// blocks, asked for once on a device (noted when
-// it is there, so that another thread's launch never comes before it).
+// blocks, asked for once on a device (noted when it is there, so that another thread's
+// launch never comes before it; a failure is not kept).  `registers`, if not 0: what the
+// kernel's threads have to start with, as its warps share them out (a share above that
+// would be waited for without end).
 using Once = std::atomic<uint64_t>;
-template <class K> inline bool room_for(Once &once, K kernel, int bytes, bool large_clusters = false)
+template <class K> inline bool room_for(Once &once, K kernel, int bytes, bool large_clusters = false, int registers = 0)
 {
     int dev = 0;
     const bool known = cudaGetDevice(&dev) == cudaSuccess && dev < 64;
     const uint64_t bit = uint64_t(known) << (dev & 63);
     if (once.load(std::memory_order_acquire) & bit) return true;
+    cudaFuncAttributes has{};
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
-        (large_clusters && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)) {
+        (large_clusters && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+        (registers && cudaFuncGetAttributes(&has, kernel) != cudaSuccess)) {
         cudaGetLastError();
         return false;
     }
+    if (registers && has.numRegs != registers) return false;
     once.fetch_or(bit, std::memory_order_release);
     return true;
 }

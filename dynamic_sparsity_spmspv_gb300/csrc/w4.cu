@@ -1047,14 +1047,8 @@ bool plan_many(const W4 &A, dbs_dtype sd, int sms, Tall &t)
 template <class T, int N>
 dbs_status launch_many(const W4 &A, const Tall &t, int sms, cudaStream_t s)
 {
-    // (a block's fours of warps share out the registers that it starts with, so there
-    // have to be that many, or their waits for them would not end)
-    static const bool shares = [] {
-        cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, k_w4_many<T, N>) == cudaSuccess && f.numRegs == Many<N>::REGS;
-    }();
     static Once once;
-    if (!shares || !room_for(once, k_w4_many<T, N>, Many<N>::SMEM)) return DBS_ERR_CUDA;
+    if (!room_for(once, k_w4_many<T, N>, Many<N>::SMEM, false, Many<N>::REGS)) return DBS_ERR_CUDA;
     const Walk &w = t.walk;
     cudaLaunchConfig_t how{};
     how.gridDim = dim3((unsigned)(w.split > 1 ? w.units * w.split : w.units < sms ? w.units : sms));
