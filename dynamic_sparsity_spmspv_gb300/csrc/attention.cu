@@ -1640,7 +1640,7 @@ dbs_status launch_join(const Attn &A, const Plan &P, cudaStream_t s)
 {
     // whole blocks for a row while all rows find room on the GPU at once (8 blocks
     // an SM), and no more blocks than that: each finds its unit's place anew
-    const int64_t units = A.a.batch * A.a.kv_heads * P.share.groups, rows = rows_of_unit(A, P), room = 152 * 8;
+    const int64_t units = A.a.batch * A.a.kv_heads * P.share.groups, rows = rows_of_unit(A, P), room = (int64_t)multiprocessors() * 8;
     const int split = units * rows <= room ? JOIN_W : 1;
     const int64_t turns = (rows + JOIN_W / split - 1) / (JOIN_W / split), most = room / units > 0 ? room / units : 1;
     cudaLaunchConfig_t c{};

@@ -186,7 +186,10 @@ dbs_status launch_units(const Rotary &A, cudaStream_t s)
     constexpr int N = Vec<T, WIDE>::n, E = INTERLEAVED ? (WIDE ? N : 2) : 2 * N;
     const int turning = A.dim / E;
     // Heads of a thread: eight, so that a token's angles are read once for all of
-    // them, and fewer while that leaves the GPU's 152 x 2048 threads idle.
+    // them, and fewer while that leaves some of the GPU's threads (2048 a
+    // multiprocessor) idle.
+    const int64_t room = (int64_t)multiprocessors() * 2048;
+    if (room == 0) return DBS_ERR_CUDA;
     int64_t most = 0;
     int span = 8, chunks = 0;
     for (;; span /= 2) {
@@ -202,7 +205,7 @@ dbs_status launch_units(const Rotary &A, cudaStream_t s)
                 threads += A.total * units * n;
                 most = most > A.total * units ? most : A.total * units;
             }
-        if (span == 1 || threads >= 152 * 2048 || 2 * chunks > 65535) break;      // (the grid's limit in y)
+        if (span == 1 || threads >= room || 2 * chunks > 65535) break;      // (the grid's limit in y)
     }
     k_rotary<T, INTERLEAVED, WIDE><<<dim3((unsigned)((most + NT - 1) / NT), (unsigned)chunks), NT, 0, s>>>(A, (uint32_t)turning, span);
     return launched();
