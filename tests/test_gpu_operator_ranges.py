@@ -304,3 +304,62 @@ def test_gradients_are_never_lost_in_silence():
     dbs.penalize_logits(s, out=s)
     with pytest.raises(RuntimeError):
         z.backward()
+
+
+def attention64(q, k, v, lens, tree_lens, bits, table):
+    """Attention in 64 bits, with the sums of p |v|; bits: a bool [B, T, T] of what a drafted token sees, or None."""
+    B, T, hq, D = q.shape
+    out, size = torch.zeros((2, *q.shape), dtype=torch.float64, device=DEV)
+    for b in range(B):
+        n, t = int(lens[b]), int(tree_lens[b])
+        kb, vb = ((c[table[b].long()].flatten(0, 1)[:n] if table is not None else c[b, :n]).double().repeat_interleave(hq // c.shape[2], 1) for c in (k, v))
+        node = torch.arange(n, device=DEV) - (n - t)
+        see = (node < 0) | (node[None] <= torch.arange(t, device=DEV)[:, None]) if bits is None else (node < 0) | bits[b, :t][:, node.clamp(min=0)]
+        for h in range(hq):
+            p = torch.softmax((q[b, :t, h].double() @ kb[:, h].t() * D**-0.5).masked_fill(~see, -math.inf), 1).nan_to_num(0.0)
+            seen = torch.where(torch.isfinite(vb[:, h]), vb[:, h], 0.0)    # (those that are not: see the callers)
+            out[b, :t, h], size[b, :t, h] = p @ seen, p @ seen.abs()
+    return out, size
+
+
+# head sizes of each kernel; up to 128 rows of a kv head, and more; pages that eight does not divide, and others
+@pytest.mark.parametrize("page", [12, 5, 32, 0])
+@pytest.mark.parametrize("D", [40, 64, 72, 128, 200, 256])
+@pytest.mark.parametrize("B,T,hq,hk,S", [(5, 23, 10, 2, 900), (3, 70, 6, 1, 1500), (150, 20, 2, 2, 90)])
+def test_attention_of_many_rows_over_caches_of_any_page(B, T, hq, hk, S, D, page):
+    g = torch.Generator(device=DEV).manual_seed(B + D + page)
+    dt, u = (torch.float16, 2.0**-11) if D in (40, 128, 200) else (torch.bfloat16, 2.0**-8)
+    size = page or S
+    per = -(-S // size)
+    q = torch.randn((B, T, hq, D), generator=g, device=DEV).to(dt)
+    k, v = (torch.randn((B * per, size, hk, D), generator=g, device=DEV).to(dt) for _ in range(2))
+    if not page:
+        k = k[:, :, :1].expand(-1, -1, hk, -1)                             # (heads that share keys: no tiled copies)
+    table = torch.randperm(B * per, generator=g, device=DEV).to(torch.int32).view(B, per) if page else None
+    tl = torch.randint(1, T + 1, (B,), generator=g, device=DEV).to(torch.int32)
+    lens = torch.maximum(torch.randint(1, S + 1, (B,), generator=g, device=DEV), tl).clamp(max=S).to(torch.int32)
+    lens[0], tl[0] = S, T
+    bits = torch.rand((B, T, T), generator=g, device=DEV) < 0.3
+    bits |= torch.eye(T, dtype=torch.bool, device=DEV)
+    bits[:, :-1, T - 1] = False                                            # the last drafted token: seen by itself alone
+    tree = torch.zeros((B, T, -(-T // 64)), dtype=torch.int64, device=DEV)
+    for i in range(T):
+        tree[:, :, i // 64] |= bits[:, :, i].long() << (i % 64)
+    for mask, words in ((bits, tree), (None, None)):
+        def call():
+            return dbs.tree_attention(q, k, v, lens, words, tree_lens=tl, page_table=table)
+
+        got = call()
+        ref, mag = attention64(q, k, v, lens, tl, mask, table)
+        # probabilities rounded once to the caches' type, scores in 32 bits (3e-4 for head sizes to 256), the result rounded
+        assert ((got.double() - ref).abs() <= (u + 3e-4) * mag + u * ref.abs() + 1e-7).all()
+        assert torch.equal(got, call())
+    # a NaN in the last drafted token's value reaches that token alone
+    e = int(lens[0]) - 1
+    at = (int(table[0, e // page]), e % page) if page else (0, e)
+    clean = dbs.tree_attention(q, k, v, lens, tree, tree_lens=tl, page_table=table)
+    v[at[0], at[1], :, 0] = math.nan
+    got = dbs.tree_attention(q, k, v, lens, tree, tree_lens=tl, page_table=table)
+    assert torch.isnan(got[0, T - 1, :, 0]).all()
+    got[0, T - 1, :, 0] = clean[0, T - 1, :, 0]
+    assert torch.equal(got, clean)
