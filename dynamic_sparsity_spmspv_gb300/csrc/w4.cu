@@ -1123,7 +1123,7 @@ extern "C" dbs_status dbs_w4_linear(const void *x, dbs_dtype dtype, int64_t toke
         return DBS_ERR_INVALID_ARG;
     if (tokens == 0 || m == 0) return DBS_OK;
     if (!y || (n > 0 && (!x || !q || !scales)) || x_stride < 0 || q_stride < 0 || scale_stride < 0 ||
-        (zeros && zero_stride < 0) || (tokens > 1 && y_stride < m))
+        (zeros && zero_stride < 0) || (tokens > 1 && y_stride < m) || (n > 0 && x == y))
         return DBS_ERR_INVALID_ARG;
     const W4 A{x, q, scales, zeros, y, tokens, x_stride, q_stride, scale_stride, zero_stride, m, n, y_stride, group, waits()};
     cudaStream_t s = (cudaStream_t)stream;

@@ -456,7 +456,7 @@ typedef enum { DBS_F32 = 0, DBS_F16 = 1, DBS_BF16 = 2 } dbs_dtype;
  *   y       device, `dtype`, [tokens, m], rows y_stride apart, not overlapping x
  * fp32 x is multiplied exactly (not rounded to a shorter type).  Errors:
  * DBS_ERR_INVALID_ARG (null pointers, sizes or strides below 0, y_stride < m,
- * other groups or types), DBS_ERR_CUDA. */
+ * y at x's address, other groups or types), DBS_ERR_CUDA. */
 dbs_status dbs_w4_linear(const void *x, dbs_dtype dtype, int64_t tokens, int64_t x_stride, const uint8_t *q,
                          int64_t q_stride, const void *scales, dbs_dtype scale_dtype, int64_t scale_stride,
                          const uint8_t *zeros, int64_t zero_stride, int64_t m, int64_t n, int32_t group, void *y,
@@ -554,7 +554,8 @@ typedef struct {
     int64_t scratch_bytes;
 } dbs_attention_args;
 
-/* Bytes of scratch that dbs_tree_attention needs for these sizes. */
+/* Bytes of scratch that dbs_tree_attention needs for this call (whose fields are
+ * checked, and set but for lse and scratch: sizes, addresses and strides count). */
 dbs_status dbs_tree_attention_scratch(const dbs_attention_args *a, int64_t *bytes);
 /* Errors: DBS_ERR_INVALID_ARG (null pointers, sizes, strides, types),
  * DBS_ERR_CUDA. */

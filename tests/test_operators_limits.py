@@ -71,3 +71,8 @@ def test_rotary_takes_any_stride_of_a_single_head():
     for kw in (dict(), dict(out=A), dict(heads=1, tokens=1, batch=1, strides=(0, 0, 0) * 2), dict(slots=1, pages=1, strides=(512, 128, 64, 0, 128, 64)),
                dict(out=A, heads=1, tokens=1, batch=1, strides=(1, 2, 3, 4, 5, 6))):
         assert torch.cuda.is_available() or rotary(**kw) != BAD             # (where there is no GPU that would run it)
+
+
+def test_w4_does_not_write_over_its_input():
+    lib = _lib.load()
+    assert lib.dbs_w4_linear(A, 2, 2, 64, 2 * A, 32, 3 * A, 0, 1, 0, 0, 64, 64, 64, A, 64, None) == BAD
