@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(ROW_NT) k_attn_rows(Attn A)
 //
 // A unit is one kv head of one sequence and up to `rows` of its query rows; its
 // work is its tiles of `keys` entries (one at least), each weighing as many as
-// the 128-row blocks that the unit fills.  All units lie in one line, of which
+// the 128-row blocks that the unit fills (a count, not a time: see k_attn_many).  All units lie in one line, of which
 // every block takes an equal, contiguous piece, whatever the lengths: a piece
 // covers whole units and at most two in part (the first and the last).  Whole
 // ones are written at once, parts go to the block's two slots of scratch and are
@@ -758,7 +758,9 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
                         la += sc[h][e];
                         lb += sc[h][e + 2];
                     }
-                // probabilities rounded once to the caches' type for the second product
+                // probabilities rounded once to the caches' type, the type of V in the matrix instruction (the
+                // sums take them as they are); two pieces of each would cost a second product.  Error against 64
+                // bits, relative: one token of 2001 entries, bf16, 0.0022 (0.0016 with fp32 probabilities)
                 const uint32_t pf[4] = {pack2<T>(sc[0][0], sc[0][1]), pack2<T>(sc[0][2], sc[0][3]), pack2<T>(sc[1][0], sc[1][1]),
                                         pack2<T>(sc[1][2], sc[1][3])};
 #pragma unroll
@@ -903,7 +905,8 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
 // S = Q K^T and O += P V with both accumulators in tensor memory (a row per
 // lane), Q, K and V in shared memory in the 128-byte swizzle (K row by row, V
 // as it lies, its entries as the contraction's dimension), and P rounded to the
-// caches' type.  Warps have roles: two fetch K and V, two load Q, one for each 128
+// caches' type, as the matrix instruction has one type for both operands (error against
+// 64 bits: trees of 48, f16, 0.00029, with fp32 probabilities 0.00021).  Warps have roles: two fetch K and V, two load Q, one for each 128
 // rows issues the matrix instructions, two look through the drafted part of V, and
 // four for each 128 rows do the softmax, a thread a row.  S has two buffers, so the
 // scores of the next tile of entries are made under the softmax of one.
@@ -917,16 +920,21 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
 // 16-byte asynchronous copies, which reach about half of the memory's rate (an SM's
 // copies in flight are the limit).
 //
-// 16 trees of 12 tokens, 8 kv heads, 128 MB of caches: 53 us.  A tile of 128 entries
+// 16 trees of 12 tokens, 8 kv heads, 128 MB of caches: 54 us.  A tile of 128 entries
 // takes 1.15 us, less than its copy at the memory's rate; what is lost is the start
 // (9 us until the first scores, of which 4 the first copies) and 5 us for each of a
 // block's two or three units (masked tile, last product, output, first scores).
 // 4 trees of 48 tokens over 32768 entries, 384 rows to a kv head: 169 us, 32% of the
-// tensor cores' rate; 1024 tokens over 8192 entries: 43%.  Two row tiles take 0.95 us
-// for 64 entries, 0.6 of them products: the softmax's own chain (scores, maximum,
-// powers, sum, stores) bounds it.  With P over S and tiles of 128 entries 173 us; P
-// over S and tiles of 64: 177; one warp issuing for both row tiles: 179.  A share of
-// the powers of two by polynomial made it slower (186 us and more).
+// tensor cores' rate.  Two row tiles take 1.1 us for 64 entries where a block has 862
+// such tiles (2 x 1024 tokens over 32768 entries, 32/8 heads: 950 us, 61%); the products
+// alone would take 0.67: the softmax's own chain (scores, maximum, powers, sum, stores)
+// bounds it.  With 108 a block the start, the units' ends and the join cost a third
+// (1024 tokens over 8192 entries: 34%).  A lone row tile, the rest of a kv head's rows,
+// has the same chain: 384 rows (48 tokens, 32/4 heads) take longer than 512 (L2 flushed:
+// 185 us and 168), although the line gives it half of a pair's weight.  With P over S and
+// tiles of 128 entries 173 us; P over S and tiles of 64: 177; one warp issuing for both
+// row tiles: 179.  A share of the powers of two by polynomial made it slower (186 us and
+// more).
 //
 // Every wait on a barrier has a limit; a block whose wait runs out stops, leaves NaN in
 // the rows of all units, or parts of units, that it had not finished, and says so.
@@ -954,6 +962,7 @@ __device__ __forceinline__ void store32(void *p, uint32_t a, uint32_t b, uint32_
 {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
 }
+// (to 2 units of the last place, and 0 below 2^-126: far below the 16 bits that P keeps)
 __device__ __forceinline__ float pow2(float x)
 {
     float y;

@@ -247,7 +247,8 @@ __device__ __noinline__ void land(uint32_t bar, int use, uint32_t parity, uint32
 // of 32 or 64 columns.  A warp whose wait runs out fetches no more and leaves NaN.
 // One token, 4096 x 11008, fp32: 12.3 us for 24 MB, whose copies alone would take 3.5.
 // Bound by the warps' instructions, half of which turn codes into numbers, and, with a
-// start and a join of 4 us, by latency.
+// start and a join of 4 us, by latency.  (bf16 x, a column of the instruction instead of
+// three of the same eight, takes 12.6.)
 template <class T, bool S16, int NT, int RT, bool FINE>
 __global__ void __launch_bounds__(MMA_NT, 1) k_w4_mma(W4 A, Cut C, const __grid_constant__ CUtensorMap map)
 {
@@ -602,7 +603,7 @@ dbs_status launch_mma(const W4 &A, dbs_dtype sd, const CUtensorMap &map, cudaStr
 // numbers, in place; one fetches codes and one x, by tiled copies; one issues the
 // products.  Fours of warps that need few registers leave theirs to those that scale.
 //
-// 24 tokens, 128000 x 4096: 91 us, against 144 with k_w4_mma, whose warps spend their
+// 24 tokens, 128000 x 4096: 92.5 us, against 150 with k_w4_mma, whose warps spend their
 // instructions on fragments of x.  A block's chunk takes 0.8 us, of which memory
 // would take 0.4: the chain of the products' issue and the scaling of their sums
 // bounds it (two thirds of the issue slots are used).
@@ -1019,10 +1020,16 @@ bool make_x_map(const W4 &A, int rows, CUtensorMap &map)
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// From 13 tokens of 16-bit x on, where x's rows are on 16-byte boundaries.  Fewer,
-// where k_w4_mma takes two matrix instructions for a fragment, cost it less or the
-// same (12 tokens, 32000 x 4096: 42 and 50 us; 16 tokens: 48 and 50; 24 tokens: 72
-// and 50; 4096 x 11008: 27 and 21, 42 and 21, 103 and 21).
+// From 13 tokens of 16-bit x on, where x's rows are on 16-byte boundaries: k_w4_mma takes
+// a matrix instruction for each eight tokens, this one the same time up to 32.  k_w4_mma
+// and this one, us, bf16, groups of 128, zeros:
+//                   8 tokens       12          13          16          24
+//    4096 x 11008  20.8  18.6   24.5  18.6   35.1  18.7   37.3  18.7   98   18.7
+//   11008 x  4096  16.6  18.8   18.7  18.8   23.0  18.8   24.8  18.7   41   18.7
+//   32000 x  4096  25.2  33.3   30.0  33.3   34.7  33.3   35.7  33.3   58   33.3
+//  128000 x  4096  74.8  93.9   87.9  94.1   89.1  93.6   90.2  93.7  150   93.8
+// So the right place is between 5 tokens and 16, later for more rows; 13 costs at most 32%
+// (4096 rows, 12 tokens) and 5% (128000 rows, 13).
 constexpr int64_t MANY_TOKENS = 12;
 
 struct Tall {
@@ -1039,8 +1046,8 @@ bool plan_many(const W4 &A, dbs_dtype sd, int sms, Tall &t)
     if (!make_map(A, 128, 128, t.codes) || !make_x_map(A, N, t.x)) return false;
     t.walk = {(int)steps, 0, (int)passes, (int)units, 1, sd};
     while (1 << t.walk.shift < A.group) ++t.walk.shift;
-    // few units: blocks of a cluster share one's columns (4096 x 11008, 24 tokens: 21
-    // us with four, 40 with one)
+    // few units: blocks of a cluster share one's columns (4096 x 11008, 24 tokens: 18.7
+    // us with four, 39.1 with one)
     while (t.walk.split < (N == 32 ? 8 : 4) && units * 2 * t.walk.split <= sms && steps >= 4 * t.walk.split) t.walk.split *= 2;
     return true;
 }

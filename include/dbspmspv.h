@@ -429,7 +429,7 @@ dbs_status dbs_spmspv_dense_noalloc_check(void *stream);
  * graph and give identical bits when repeated.  Strides are in elements (of
  * bytes for 4-bit codes) and not negative; the innermost dimension is contiguous.
  * Sums, softmax statistics and rotations are fp32; every result is rounded once,
- * to its own type.
+ * to its own type (and attention's probabilities to the caches', see there).
  *
  * Waits inside the kernels of dbs_w4_linear and dbs_tree_attention end after two
  * seconds: the block gives up and leaves NaN in what it had not finished (in lse
@@ -526,7 +526,9 @@ dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype d
  *     out[b, t, h] = sum_j softmax_j(scale q[b,t,h].k[j, h / G]) v[j, h / G]
  * over the entries it sees, G = q_heads / kv_heads.  A token that sees none
  * gets 0 and lse -inf, and so do the tokens t >= tree_lens[b].  Entries that
- * are not seen take no part, whatever they hold (NaN included). */
+ * are not seen take no part, whatever they hold (NaN included).  Where the
+ * products run on tensor cores each probability is rounded once to `dtype`
+ * before it meets v (their sum, and so lse, takes them in fp32). */
 typedef struct {
     dbs_dtype dtype;           /* DBS_F16 or DBS_BF16, of q, caches and out */
     int32_t head_dim;          /* 1..256 */
