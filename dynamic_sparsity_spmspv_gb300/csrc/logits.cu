@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(NT, 2) k_logits_narrow(dbs_logits_args A, int 
 // table, whose words are claimed by compare and swap, took 15 us for 4096 tokens
 // of four warps), and there is room for a slice of 65536 entries.  The others read, mask and write every
 // entry as it is, in runs of eight, and the first ones help them then: bound by
-// HBM (96 rows of 128,000 with 4096 tokens: 27.9 us; k_logits_narrow takes 38.1, in
+// HBM (96 rows of 128,000 with 4096 tokens: 27 us; k_logits_narrow takes 38.1, in
 // six waves of blocks).  Last the marked entries, few against the slice, are computed again with
 // penalties and biases and written over.  Their logits are read a second time:
 // where out is the logits themselves, an entry that the first part changed is a

@@ -425,11 +425,12 @@ dbs_status dbs_spmspv_dense_noalloc_check(void *stream);
  *
  * What a language model's step of one or a few (drafted) tokens needs around
  * the DB-Decoding layer; the paper has no counterpart.  All calls are ASYNC,
- * allocate nothing, hold no state between calls, can be captured in a CUDA
- * graph and give identical bits when repeated.  Strides are in elements (of
- * bytes for 4-bit codes) and not negative; the innermost dimension is contiguous.
- * Sums, softmax statistics and rotations are fp32; every result is rounded once,
- * to its own type (and attention's probabilities to the caches', see there).
+ * allocate nothing, hold no state between calls (but the word that
+ * dbs_operators_check reads), can be captured in a CUDA graph and give identical
+ * bits when repeated.  Strides are in elements (of bytes for 4-bit codes) and not
+ * negative; the innermost dimension is contiguous.  Sums, softmax
+ * statistics and rotations are fp32; every result is rounded once, to its own type
+ * (and attention's probabilities to the caches', see there).
  *
  * Waits inside the kernels of dbs_w4_linear and dbs_tree_attention end after two
  * seconds: the block gives up and leaves NaN in what it had not finished (in lse
