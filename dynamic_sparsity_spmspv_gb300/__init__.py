@@ -15,8 +15,9 @@ Multiplication for Dynamic GPU Workloads", ICPP '26.
     levels, nlev = bfs(A, src, ws=ws)                    # DB-BFS (4.2)
 
 The operators of a decoding step around that layer (4-bit linear layers,
-rotary positions, attention of drafted tokens over a cache, logit penalties)
-are in decoding.py and are exported here too.
+rotary positions, norms with rotation, attention of drafted tokens or with a
+sliding window over a cache, the cache's pages, logit penalties) are in
+decoding.py and are exported here too.
 """
 from __future__ import annotations
 
@@ -372,15 +373,17 @@ class SpMVPlan:
 
 def dbs_operators_check(stream=None) -> int:
     """dbs_operators_check: synchronizes the stream and returns 4
-    (DBS_ERR_TIMEOUT), once, if a wait inside a kernel of w4_linear or
-    tree_attention ran out since the last check (its results are NaN), else 0."""
+    (DBS_ERR_TIMEOUT), once, if a wait inside a kernel of w4_linear,
+    tree_attention or window_attention ran out since the last check (its results
+    are NaN), else 0."""
     return int(_lib.load().dbs_operators_check(_stream_handle(stream)))
 
 
 operators_check = dbs_operators_check
 
 
-_DECODING = ("w4_linear", "rotary_table", "rotary", "rotary_append", "tree_attention", "penalize_logits")
+_DECODING = ("w4_linear", "rotary_table", "rotary", "rotary_append", "tree_attention", "penalize_logits", "norm_rotary",
+             "norm_rotary_append", "norm_rotary_gradient", "window_attention", "cache_resize", "cache_fork", "cache_compact")
 
 
 def __getattr__(name):

@@ -552,6 +552,329 @@ PyObject *penalize_logits(PyObject *, PyObject *const *args, Py_ssize_t nargs, P
     });
 }
 
+// ---- norms with rotation ----
+
+// A head's weight: [head_dim] of any floating type, or none.
+dbs_norm_heads normed(Call &c, const char *name, const dbs_rotary_heads &heads, const at::Tensor *w, int64_t d)
+{
+    dbs_norm_heads H{heads, nullptr, DBS_F32};
+    if (w) {
+        H.weight_dtype = c.type(name, *w);
+        H.weight = c.vector(name, w, d, w->scalar_type());
+    }
+    return H;
+}
+
+PyObject *pair(const at::Tensor &a, const at::Tensor &b)
+{
+    PyObject *r = PyTuple_New(2);
+    if (!r) throw Failed();
+    PyTuple_SET_ITEM(r, 0, a.defined() ? wrap(a) : Py_NewRef(Py_None));
+    PyTuple_SET_ITEM(r, 1, b.defined() ? wrap(b) : Py_NewRef(Py_None));
+    return r;
+}
+
+PyObject *norm_rotary(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
+{
+    static const Names<11> N({"q", "k", "q_weight", "k_weight", "table", "positions", "eps", "interleaved", "q_out", "k_out", "stream"});
+    return guarded([&]() -> PyObject * {
+        Call c{"dbs_norm_rotary"};
+        const Args<11> a(c.fn, N.v, 6, 6, args, nargs, kw);
+        const at::Tensor &q = c.need("q", a.v[0]), &table = c.need("table", a.v[4]), &pos = c.need("positions", a.v[5]);
+        const at::Tensor *k = c.tensor("k", a.v[1]), *qw = c.tensor("q_weight", a.v[2]), *kw_ = c.tensor("k_weight", a.v[3]);
+        const at::Tensor *qg = c.tensor("q_out", a.v[8]), *kg = c.tensor("k_out", a.v[9]);
+        const dbs_dtype dt = c.type("q", q);
+        const Heads Q = turning(c, q, table, pos, nullptr);
+        const Heads K = k ? like(c, "k", *k, q, Q) : Q;
+        if (!k && (kw_ || kg)) bad(c.fn, "k_weight and k_out need k");
+        c.on(a.v[10]);
+        const at::Tensor qo = turned(c, q, qg), ko = k ? turned(c, *k, kg) : at::Tensor();
+        dbs_norm_heads parts[2] = {normed(c, "q_weight", part(q, Q, qo.data_ptr(), heads_of(c, "q_out", qo, q.scalar_type()), true, false), qw, Q.d)};
+        if (k) parts[1] = normed(c, "k_weight", part(*k, K, ko.data_ptr(), heads_of(c, "k_out", ko, q.scalar_type()), true, false), kw_, Q.d);
+        check(c.fn, dbs_norm_rotary(parts, k ? 2 : 1, dt, Q.b, Q.n, (int32_t)Q.d, (int32_t)table.size(1), (float)real(a.v[6], 1e-6),
+                                    table.data_ptr<float>(), table.size(0), pos.data_ptr<int32_t>(), nullptr, 0, 1, truth(a.v[7], false), c.stream));
+        if (qg) written(qo);
+        if (kg) written(ko);
+        return pair(qo, ko);
+    });
+}
+
+PyObject *norm_rotary_append(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
+{
+    static const Names<14> N({"q", "k", "v", "q_weight", "k_weight", "table", "positions", "k_cache", "v_cache", "slots", "eps", "interleaved",
+                              "q_out", "stream"});
+    return guarded([&]() -> PyObject * {
+        Call c{"dbs_norm_rotary_append"};
+        const Args<14> a(c.fn, N.v, 10, 10, args, nargs, kw);
+        const at::Tensor &q = c.need("q", a.v[0]), &k = c.need("k", a.v[1]), &v = c.need("v", a.v[2]);
+        const at::Tensor *qw = c.tensor("q_weight", a.v[3]), *kw_ = c.tensor("k_weight", a.v[4]);
+        const at::Tensor &table = c.need("table", a.v[5]), &pos = c.need("positions", a.v[6]);
+        const at::Tensor &kc = c.need("k_cache", a.v[7]), &vc = c.need("v_cache", a.v[8]), &slots = c.need("slots", a.v[9]);
+        const at::Tensor *qg = c.tensor("q_out", a.v[12]);
+        const dbs_dtype dt = c.type("q", q);
+        const Heads Q = turning(c, q, table, pos, &slots), K = like(c, "k", k, q, Q), V = like(c, "v", v, q, Q);
+        if (kc.dim() != 4 || vc.sizes() != kc.sizes() || K.h != V.h)
+            bad(c.fn, "caches have to be [pages, page_size, kv_heads, head_dim]");
+        const Heads KC = heads_of(c, "k_cache", kc, q.scalar_type()), VC = heads_of(c, "v_cache", vc, q.scalar_type());
+        if (KC.h != K.h || KC.d != Q.d) bad(c.fn, "caches have to have k's heads");
+        c.on(a.v[13]);
+        const at::Tensor qo = turned(c, q, qg);
+        const dbs_norm_heads parts[3] = {
+            normed(c, "q_weight", part(q, Q, qo.data_ptr(), heads_of(c, "q_out", qo, q.scalar_type()), true, false), qw, Q.d),
+            normed(c, "k_weight", part(k, K, kc.data_ptr(), KC, true, true), kw_, Q.d),
+            {part(v, V, vc.data_ptr(), VC, false, true), nullptr, DBS_F32}};
+        const bool room = KC.n > 0;                    // (pages of no entry are like no pages)
+        check(c.fn, dbs_norm_rotary(parts, 3, dt, Q.b, Q.n, (int32_t)Q.d, (int32_t)table.size(1), (float)real(a.v[10], 1e-6),
+                                    table.data_ptr<float>(), table.size(0), pos.data_ptr<int32_t>(), slots.data_ptr<int32_t>(),
+                                    room ? KC.b : 0, room ? KC.n : 1, truth(a.v[11], false), c.stream));
+        if (qg) written(qo);
+        written(kc);
+        written(vc);
+        return wrap(qo);
+    });
+}
+
+PyObject *norm_rotary_gradient(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
+{
+    static const Names<11> N({"q_grad", "k_grad", "q", "k", "q_weight", "k_weight", "table", "positions", "eps", "interleaved", "stream"});
+    return guarded([&]() -> PyObject * {
+        Call c{"dbs_norm_rotary_gradient"};
+        const Args<11> a(c.fn, N.v, 8, 8, args, nargs, kw);
+        const at::Tensor &qg = c.need("q_grad", a.v[0]), &q = c.need("q", a.v[2]);
+        const at::Tensor *kg = c.tensor("k_grad", a.v[1]), *k = c.tensor("k", a.v[3]);
+        const at::Tensor *qw = c.tensor("q_weight", a.v[4]), *kw_ = c.tensor("k_weight", a.v[5]);
+        const at::Tensor &table = c.need("table", a.v[6]), &pos = c.need("positions", a.v[7]);
+        const dbs_dtype dt = c.type("q", q);
+        const Heads Q = turning(c, q, table, pos, nullptr);
+        if (!k != !kg) bad(c.fn, "k and k_grad come together");
+        if (!k && kw_) bad(c.fn, "k_weight needs k");
+        c.on(a.v[10]);
+        dbs_norm_gradient_heads parts[2] = {};
+        at::Tensor dx[2], dw[2];
+        for (int p = 0; p < (k ? 2 : 1); ++p) {
+            const at::Tensor &x = p ? *k : q, &g = p ? *kg : qg;
+            const at::Tensor *w = p ? kw_ : qw;
+            const char *name = p ? "k_grad" : "q_grad";
+            const Heads X = p ? like(c, "k", x, q, Q) : Q, G = like(c, name, g, q, Q);
+            if (G.h != X.h) bad(c.fn, std::string(name) + " has to have its input's heads");
+            dx[p] = c.empty(x.sizes(), x.scalar_type());
+            dw[p] = c.empty({Q.d}, at::kFloat);
+            const Heads O = heads_of(c, "out", dx[p], x.scalar_type());
+            const dbs_norm_heads W = normed(c, p ? "k_weight" : "q_weight", dbs_rotary_heads{}, w, Q.d);
+            parts[p] = {g.data_ptr(), x.data_ptr(), dx[p].data_ptr(), G.sb, G.sn, G.sh, X.sb, X.sn, X.sh, O.sb, O.sn, O.sh,
+                        (int32_t)X.h, W.weight_dtype, W.weight, dw[p].data_ptr<float>()};
+        }
+        int64_t bytes = 0;
+        check(c.fn, dbs_norm_rotary_gradient_scratch(k ? 2 : 1, (int32_t)Q.d, &bytes));
+        const at::Tensor scratch = c.empty({bytes}, at::kByte);
+        check(c.fn, dbs_norm_rotary_gradient(parts, k ? 2 : 1, dt, Q.b, Q.n, (int32_t)Q.d, (int32_t)table.size(1), (float)real(a.v[8], 1e-6),
+                                             table.data_ptr<float>(), table.size(0), pos.data_ptr<int32_t>(), truth(a.v[9], false),
+                                             scratch.data_ptr(), bytes, c.stream));
+        PyObject *r = PyTuple_New(4);
+        if (!r) throw Failed();
+        const at::Tensor all[4] = {dx[0], dx[1], dw[0], dw[1]};
+        for (int i = 0; i < 4; ++i) PyTuple_SET_ITEM(r, i, all[i].defined() ? wrap(all[i]) : Py_NewRef(Py_None));
+        return r;
+    });
+}
+
+// ---- attention with a window ----
+
+PyObject *window_attention(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
+{
+    static const Names<12> N({"q", "k_cache", "v_cache", "kv_lens", "window", "sinks", "q_lens", "page_table", "scale", "out", "return_lse",
+                              "stream"});
+    return guarded([&]() -> PyObject * {
+        Call c{"dbs_window_attention"};
+        const Args<12> a(c.fn, N.v, 5, 5, args, nargs, kw);
+        const at::Tensor &q = c.need("q", a.v[0]), &k = c.need("k_cache", a.v[1]), &v = c.need("v_cache", a.v[2]);
+        const at::Tensor &lens = c.need("kv_lens", a.v[3]);
+        const at::Tensor *ql = c.tensor("q_lens", a.v[6]), *pt = c.tensor("page_table", a.v[7]), *given = c.tensor("out", a.v[9]);
+        const bool want_lse = truth(a.v[10], false);
+        if ((q.scalar_type() != at::kHalf && q.scalar_type() != at::kBFloat16) || q.dim() != 4)
+            bad(c.fn, "q has to be float16 or bfloat16 [batch, tokens, q_heads, head_dim]");
+        const Heads Q = heads_of(c, "q", q, q.scalar_type());
+        if (k.dim() != 4 || k.sizes() != v.sizes()) bad(c.fn, "caches have to be [pages, page_size, kv_heads, head_dim]");
+        const Heads K = heads_of(c, "k_cache", k, q.scalar_type()), V = heads_of(c, "v_cache", v, q.scalar_type());
+        if (K.d != Q.d || Q.d > 256 || Q.d < 1) bad(c.fn, "the caches' heads have to be like q's, of at most 256 entries");
+        if (K.h == 0 || Q.h == 0 || Q.h % K.h) bad(c.fn, "q_heads has to be a multiple of kv_heads");
+        dbs_window_args A{};
+        A.dtype = c.type("q", q);
+        A.head_dim = (int32_t)Q.d;
+        A.q_heads = (int32_t)Q.h;
+        A.kv_heads = (int32_t)K.h;
+        A.batch = Q.b;
+        A.tokens = Q.n;
+        A.q = q.data_ptr();
+        A.q_batch = Q.sb; A.q_token = Q.sn; A.q_head = Q.sh;
+        A.k = k.data_ptr();
+        A.v = v.data_ptr();
+        A.k_page = K.sb; A.k_entry = K.sn; A.k_head = K.sh;
+        A.v_page = V.sb; A.v_entry = V.sn; A.v_head = V.sh;
+        A.pages = K.b;
+        A.page_size = K.n;
+        if (pt) {
+            if (pt->dim() != 2) bad(c.fn, "page_table has to be int32 [batch, max_pages]");
+            A.max_pages = pt->size(1);
+            A.page_row = c.rows("page_table", *pt, Q.b, A.max_pages, at::kInt);
+            A.page_table = pt->data_ptr<int32_t>();
+        } else {
+            if (K.b < Q.b) bad(c.fn, "without a page_table the caches are [batch, entries, kv_heads, head_dim]");
+            A.max_pages = 1;
+        }
+        A.kv_lens = (const int32_t *)c.vector("kv_lens", &lens, Q.b, at::kInt);
+        A.q_lens = (const int32_t *)c.vector("q_lens", ql, Q.b, at::kInt);
+        A.window = whole(a.v[4], 0);
+        A.sinks = whole(a.v[5], 0);
+        if (A.window < 1 || A.sinks < 0) bad(c.fn, "window has to be at least 1, sinks at least 0");
+        A.scale = (float)real(a.v[8], 1.0 / std::sqrt((double)Q.d));
+        c.on(a.v[11]);
+        at::Tensor out, lse;
+        if (given) {
+            out = *given;
+            if (out.sizes() != q.sizes()) bad(c.fn, "out has to have q's shape");
+        } else {
+            out = c.empty(q.sizes(), q.scalar_type());
+        }
+        const Heads O = heads_of(c, "out", out, q.scalar_type());
+        A.out = out.data_ptr();
+        A.o_batch = O.sb; A.o_token = O.sn; A.o_head = O.sh;
+        if (want_lse) {
+            lse = c.empty({Q.b, Q.n, Q.h}, at::kFloat);
+            A.lse = lse.data_ptr<float>();
+        }
+        check(c.fn, dbs_window_attention(&A, c.stream));
+        if (given) written(out);
+        return want_lse ? pair(out, lse) : wrap(out);
+    });
+}
+
+// ---- pages of a cache ----
+
+// K and V: [pages, page_size, kv_heads, head_dim] of one layer, or with a dimension of layers before.
+dbs_cache_data cache_of(const Call &c, const at::Tensor &k, const at::Tensor &v, int64_t &pages, int64_t &page_size)
+{
+    const int64_t n = k.dim(), size = (int64_t)k.element_size();
+    if ((n != 4 && n != 5) || v.sizes() != k.sizes() || v.scalar_type() != k.scalar_type())
+        bad(c.fn, "caches have to be two tensors [pages, page_size, kv_heads, head_dim] or [layers, pages, page_size, kv_heads, head_dim] of one type");
+    if (size != 1 && size != 2 && size != 4 && size != 8) bad(c.fn, "entries of caches have to be of 1, 2, 4 or 8 bytes");
+    if (k.size(n - 1) > 1 && (k.stride(n - 1) != 1 || v.stride(n - 1) != 1)) bad(c.fn, "caches: the last dimension has to be contiguous");
+    pages = k.size(n - 4);
+    page_size = k.size(n - 3);
+    auto at = [&](const at::Tensor &t, int64_t i) { return t.stride(n - i); };
+    const bool layers = n == 5;
+    return {k.data_ptr(), v.data_ptr(), layers ? k.size(0) : 1, k.numel() ? k.size(n - 2) : 0, k.size(n - 1), (int32_t)size,   // (without entries: no heads)
+            layers ? k.stride(0) : 0, at(k, 4), at(k, 3), at(k, 2), layers ? v.stride(0) : 0, at(v, 4), at(v, 3), at(v, 2)};
+}
+
+dbs_page_state state_of(Call &c, const at::Tensor *table, const at::Tensor &lens, const at::Tensor *refs)
+{
+    dbs_page_state S{};
+    if (lens.dim() != 1) bad(c.fn, "kv_lens has to be int32 [batch]");
+    S.batch = lens.size(0);
+    S.kv_lens = (int32_t *)const_cast<void *>(c.vector("kv_lens", &lens, S.batch, at::kInt));
+    if (table) {
+        if (table->dim() != 2) bad(c.fn, "page_table has to be int32 [batch, max_pages]");
+        S.max_pages = table->size(1);
+        S.page_row = c.rows("page_table", *table, S.batch, S.max_pages, at::kInt);
+        S.page_table = table->data_ptr<int32_t>();
+    }
+    if (refs) {
+        if (refs->dim() != 1) bad(c.fn, "refs has to be int32 [pages]");
+        S.pages = refs->size(0);
+        S.refs = (int32_t *)const_cast<void *>(c.vector("refs", refs, S.pages, at::kInt));
+    }
+    return S;
+}
+
+PyObject *cache_resize(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
+{
+    static const Names<7> N({"page_table", "kv_lens", "refs", "lens", "page_size", "columns", "stream"});
+    return guarded([&]() -> PyObject * {
+        Call c{"dbs_cache_resize"};
+        const Args<7> a(c.fn, N.v, 5, 5, args, nargs, kw);
+        const at::Tensor &table = c.need("page_table", a.v[0]), &kv = c.need("kv_lens", a.v[1]), &refs = c.need("refs", a.v[2]);
+        const at::Tensor &lens = c.need("lens", a.v[3]);
+        dbs_page_state S = state_of(c, &table, kv, &refs);
+        S.page_size = whole(a.v[4], 0);
+        const int64_t columns = whole(a.v[5], 0);
+        if (S.page_size < 1 || columns < 0) bad(c.fn, "page_size has to be at least 1, columns at least 0");
+        const int32_t *want = (const int32_t *)c.vector("lens", &lens, S.batch, at::kInt);
+        c.on(a.v[6]);
+        int64_t bytes = 0;
+        check(c.fn, dbs_cache_resize_scratch(&S, &bytes));
+        const at::Tensor status = c.empty({S.batch}, at::kInt), scratch = c.empty({bytes}, at::kByte);
+        at::Tensor slots;
+        if (a.v[5]) slots = c.empty({S.batch, columns}, at::kInt);
+        check(c.fn, dbs_cache_resize(&S, want, status.data_ptr<int32_t>(), slots.defined() ? slots.data_ptr<int32_t>() : nullptr, columns,
+                                     scratch.data_ptr(), bytes, c.stream));
+        written(table);
+        written(kv);
+        written(refs);
+        return pair(status, slots);
+    });
+}
+
+PyObject *cache_fork(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
+{
+    static const Names<8> N({"k_cache", "v_cache", "page_table", "kv_lens", "refs", "parents", "children", "stream"});
+    return guarded([&]() -> PyObject * {
+        Call c{"dbs_cache_fork"};
+        const Args<8> a(c.fn, N.v, 7, 7, args, nargs, kw);
+        const at::Tensor &k = c.need("k_cache", a.v[0]), &v = c.need("v_cache", a.v[1]);
+        const at::Tensor &table = c.need("page_table", a.v[2]), &kv = c.need("kv_lens", a.v[3]), &refs = c.need("refs", a.v[4]);
+        const at::Tensor &from = c.need("parents", a.v[5]), &to = c.need("children", a.v[6]);
+        int64_t pages = 0, page_size = 0;
+        const dbs_cache_data D = cache_of(c, k, v, pages, page_size);
+        dbs_page_state S = state_of(c, &table, kv, &refs);
+        if (S.pages != pages) bad(c.fn, "refs has to have a count for each page of the caches");
+        if (page_size < 1) bad(c.fn, "pages have to hold an entry at least");
+        S.page_size = page_size;
+        if (from.dim() != 1) bad(c.fn, "parents and children have to be int32 [n]");
+        const int64_t n = from.size(0);
+        const int32_t *p = (const int32_t *)c.vector("parents", &from, n, at::kInt), *ch = (const int32_t *)c.vector("children", &to, n, at::kInt);
+        c.on(a.v[7]);
+        int64_t bytes = 0;
+        check(c.fn, dbs_cache_fork_scratch(&S, n, &bytes));
+        const at::Tensor status = c.empty({n}, at::kInt), scratch = c.empty({bytes}, at::kByte);
+        check(c.fn, dbs_cache_fork(&D, &S, p, ch, n, status.data_ptr<int32_t>(), scratch.data_ptr(), bytes, c.stream));
+        for (const at::Tensor *t : {&k, &v, &table, &kv, &refs}) written(*t);
+        return wrap(status);
+    });
+}
+
+PyObject *cache_compact(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
+{
+    static const Names<8> N({"k_cache", "v_cache", "kv_lens", "tree_lens", "accepted", "accepted_lens", "page_table", "stream"});
+    return guarded([&]() -> PyObject * {
+        Call c{"dbs_cache_compact"};
+        const Args<8> a(c.fn, N.v, 6, 5, args, nargs, kw);
+        const at::Tensor &k = c.need("k_cache", a.v[0]), &v = c.need("v_cache", a.v[1]), &kv = c.need("kv_lens", a.v[2]);
+        const at::Tensor &tree = c.need("tree_lens", a.v[3]), &acc = c.need("accepted", a.v[4]);
+        const at::Tensor *al = c.tensor("accepted_lens", a.v[5]), *table = c.tensor("page_table", a.v[6]);
+        int64_t pages = 0, page_size = 0;
+        const dbs_cache_data D = cache_of(c, k, v, pages, page_size);
+        dbs_page_state S = state_of(c, table, kv, nullptr);
+        S.pages = pages;
+        if (!table) {
+            if (pages < S.batch) bad(c.fn, "without a page_table the caches are [batch, entries, kv_heads, head_dim]");
+            S.max_pages = 1;
+        }
+        if (page_size == 0 || pages == 0) S.max_pages = 0;              // (no room, whatever the table says)
+        S.page_size = page_size > 0 ? page_size : 1;
+        if (acc.dim() != 2) bad(c.fn, "accepted has to be int32 [batch, n]");
+        const int64_t stride = c.rows("accepted", acc, S.batch, acc.size(1), at::kInt);
+        const int32_t *tl = (const int32_t *)c.vector("tree_lens", &tree, S.batch, at::kInt);
+        const int32_t *n = (const int32_t *)c.vector("accepted_lens", al, S.batch, at::kInt);
+        c.on(a.v[7]);
+        const at::Tensor lens = c.empty({S.batch}, at::kInt);
+        check(c.fn, dbs_cache_compact(&D, &S, tl, acc.data_ptr<int32_t>(), acc.size(1), stride, n, lens.data_ptr<int32_t>(), c.stream));
+        written(k);
+        written(v);
+        return wrap(lens);
+    });
+}
+
 PyObject *set_error(PyObject *, PyObject *e)
 {
     Py_XDECREF(g_error);
@@ -610,6 +933,53 @@ PyMethodDef g_methods[] = {
      "-inf where bit v % 32 of allowed int32 [batch, ceil(vocab / 32)] is clear.\n"
      "repetition, presence and frequency: float32 [batch].  Returns float32, or\n"
      "`out` (which may be logits: in place)."},
+    {"norm_rotary", FAST(norm_rotary),
+     "norm_rotary(q, k, q_weight, k_weight, table, positions, *, eps=1e-6, interleaved=False, q_out=None, k_out=None, stream=None)\n--\n\n"
+     "dbs_norm_rotary: rotary of heads that are divided by the root of their mean\n"
+     "square (plus eps) and multiplied by a weight [head_dim] (float32, float16 or\n"
+     "bfloat16; None: ones), each head of q and k (or None) by its own.  Returns\n"
+     "(q, k) as rotary does."},
+    {"norm_rotary_append", FAST(norm_rotary_append),
+     "norm_rotary_append(q, k, v, q_weight, k_weight, table, positions, k_cache, v_cache, slots, *, eps=1e-6, interleaved=False, "
+     "q_out=None, stream=None)\n--\n\n"
+     "dbs_norm_rotary with a cache: rotary_append of normed q and k; v is copied."},
+    {"norm_rotary_gradient", FAST(norm_rotary_gradient),
+     "norm_rotary_gradient(q_grad, k_grad, q, k, q_weight, k_weight, table, positions, *, eps=1e-6, interleaved=False, stream=None)\n--\n\n"
+     "dbs_norm_rotary_gradient: from the gradients of norm_rotary's results and its\n"
+     "inputs (k_grad and k may be None) the gradients of q, k (in their type),\n"
+     "q_weight and k_weight (float32 [head_dim])."},
+    {"window_attention", FAST(window_attention),
+     "window_attention(q, k_cache, v_cache, kv_lens, window, *, sinks=0, q_lens=None, page_table=None, scale=None, out=None, "
+     "return_lse=False, stream=None)\n--\n\n"
+     "dbs_window_attention: q [batch, tokens, q_heads, head_dim] (float16 or\n"
+     "bfloat16), one token or a whole prompt, against caches as tree_attention takes\n"
+     "them.  The last q_lens[b] (None: all of q's tokens) of a sequence's kv_lens[b]\n"
+     "entries are its tokens; one at position p sees the entries j <= p with\n"
+     "p - j < window or j < sinks.  Returns out like q, and with return_lse the\n"
+     "float32 [batch, tokens, q_heads] logarithm of each row's sum."},
+    {"cache_resize", FAST(cache_resize),
+     "cache_resize(page_table, kv_lens, refs, lens, page_size, *, columns=None, stream=None)\n--\n\n"
+     "dbs_cache_resize: sequence b gets length lens[b] (below 0: as it is) by giving\n"
+     "back pages or taking free ones, lowest numbers first.  page_table int32 [batch,\n"
+     "max_pages], kv_lens int32 [batch] and refs int32 [pages] (how many sequences own\n"
+     "a page) are changed in place.  Returns (status, slots): status int32 [batch], 0\n"
+     "or why a sequence kept its length (1 no free page, 2 its last page is shared, 3\n"
+     "too long for its row); slots int32 [batch, columns], where the first `columns`\n"
+     "new entries go (-1: nowhere), or None."},
+    {"cache_fork", FAST(cache_fork),
+     "cache_fork(k_cache, v_cache, page_table, kv_lens, refs, parents, children, *, stream=None)\n--\n\n"
+     "dbs_cache_fork: the empty sequences children (int32 [n]) become copies of\n"
+     "parents: full pages are shared, the entries of a last page that is not full are\n"
+     "copied to a free one.  Caches [pages, page_size, kv_heads, head_dim], or with a\n"
+     "first dimension of layers.  Returns status int32 [n]: 0, 1 no free page, 2 not\n"
+     "an empty sequence, or listed before."},
+    {"cache_compact", FAST(cache_compact),
+     "cache_compact(k_cache, v_cache, kv_lens, tree_lens, accepted, accepted_lens=None, *, page_table=None, stream=None)\n--\n\n"
+     "dbs_cache_compact: of a sequence's last tree_lens[b] entries, its drafted\n"
+     "tokens, those numbered accepted[b] (int32 [batch, n], ascending; accepted_lens[b]\n"
+     "of them, the first that does not ascend ends the list) move to the front.  Caches\n"
+     "as of cache_fork, or without a page_table [batch, entries, kv_heads, head_dim].\n"
+     "Returns the new lengths; kv_lens and the pages stay (cache_resize takes both on)."},
     {"_set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -1,0 +1,511 @@
+// Pages of a cache (dbs_cache_resize, dbs_cache_fork, dbs_cache_compact, sm_103a).
+#include "ops_dev.h"
+
+using namespace dbs::ops;
+
+namespace {
+
+constexpr int PLAN_NT = 1024, PLAN_W = PLAN_NT / 32;
+static_assert(PLAN_W == 32, "a lane for each warp's sum");
+
+struct Sums {
+    int64_t warp[PLAN_W], total;
+};
+
+// Sum of the values of the threads before this one, and of all in S.total; by the whole block.
+__device__ __forceinline__ int64_t before(int64_t v, Sums &S)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int64_t in = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(~0u, in, d);
+        if (lane >= d) in += o;
+    }
+    __syncthreads();                               // (the sums of the turn before have been read)
+    if (lane == 31) S.warp[w] = in;
+    __syncthreads();
+    if (w == 0) {
+        const int64_t mine = S.warp[lane];
+        int64_t all = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(~0u, all, d);
+            if (lane >= d) all += o;
+        }
+        S.warp[lane] = all - mine;
+        if (lane == 31) S.total = all;
+    }
+    __syncthreads();
+    return S.warp[w] + in - v;
+}
+
+__device__ __forceinline__ int pages_of(int entries, int page) { return (int)(((int64_t)entries + page - 1) / page); }
+__device__ __forceinline__ int length(const dbs_page_state &s, int64_t b)
+{
+    const int n = __ldcg(s.kv_lens + b);
+    const int64_t room = s.max_pages * s.page_size;
+    return n < 0 ? 0 : n > room ? (int)room : n;
+}
+__device__ __forceinline__ bool is_page(const dbs_page_state &s, int p) { return p >= 0 && p < s.pages; }
+// (what other threads of the block changed is read behind the first-level cache)
+__device__ __forceinline__ int refs_of(const dbs_page_state &s, int p) { return __ldcg(s.refs + p); }
+
+// The numbers of the first `want` free pages, ascending, into `list`; returns how many there
+// are (at most `want`, or a turn's more).  By the whole block.
+constexpr int RUN = 16;                            // pages of a thread in a turn
+__device__ __forceinline__ int find_free(const dbs_page_state &s, int64_t want, int *list, Sums &S)
+{
+    int found = 0;
+    for (int64_t p0 = 0; p0 < s.pages && found < want; p0 += PLAN_NT * RUN) {
+        const int64_t mine = p0 + (int64_t)threadIdx.x * RUN;
+        unsigned free = 0;
+#pragma unroll
+        for (int i = 0; i < RUN; ++i)
+            if (mine + i < s.pages && refs_of(s, (int)(mine + i)) == 0) free |= 1u << i;
+        int at = found + (int)before(__popc(free), S);
+        for (; free && at < want; free &= free - 1) list[at++] = (int)mine + __ffs(free) - 1;
+        found += (int)S.total;
+    }
+    __syncthreads();
+    return found;
+}
+
+// ---- lengths ----
+
+struct Resize {
+    dbs_page_state s;
+    const int32_t *lens;
+    int32_t *status, *slots;
+    int64_t columns;
+    // of every sequence: its length before; the pages that it asks for, and those that it and all before it ask for
+    int32_t *old, *need, *end;
+    int32_t *list;
+};
+
+// Slots of the new entries u, u + step, ... of all sequences.
+__device__ __forceinline__ void write_slots(const Resize &A, int64_t u, int64_t step)
+{
+    const dbs_page_state &s = A.s;
+    const int64_t all = s.batch * A.columns;
+    const int page = (int)s.page_size;
+    for (; u < all; u += step) {
+        const int64_t b = u / A.columns;
+        const int i = (int)(u - b * A.columns), old = __ldcg(A.old + b), n = length(s, b);
+        int slot = -1;
+        if (i < n - old) {
+            const int j = old + i, p = __ldcg(s.page_table + b * s.page_row + j / page);
+            if (is_page(s, p)) slot = p * page + j % page;
+        }
+        A.slots[u] = slot;
+    }
+}
+
+__global__ void __launch_bounds__(256) k_slots(Resize A) { write_slots(A, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256); }
+
+// One block does all: cuts, a sum over what the sequences ask for, a walk over refs
+// that ends when enough pages are found, growth.  Bound by the latency of those steps.
+__global__ void __launch_bounds__(PLAN_NT) k_resize(Resize A, int slots_here)
+{
+    __shared__ Sums S;
+    const dbs_page_state &s = A.s;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, page = (int)s.page_size;
+    const int64_t room = s.max_pages * s.page_size;
+    // a warp a sequence: what is cut off
+    for (int64_t b = warp; b < s.batch; b += PLAN_W) {
+        const int old = length(s, b), n = A.lens[b];
+        if (n >= 0 && n < old)
+            for (int c = pages_of(n, page) + lane; c < pages_of(old, page); c += 32) {
+                const int p = s.page_table[b * s.page_row + c];
+                if (is_page(s, p)) atomicSub(s.refs + p, 1);
+            }
+        if (lane == 0) {
+            A.old[b] = old;
+            if (n >= 0 && n <= old) s.kv_lens[b] = n;
+        }
+    }
+    __syncthreads();
+    int64_t asked = 0;
+    for (int64_t b0 = 0; b0 < s.batch; b0 += PLAN_NT) {
+        const int64_t b = b0 + threadIdx.x;
+        int need = 0;
+        if (b < s.batch) {
+            const int old = __ldcg(A.old + b), n = A.lens[b];
+            int status = 0;
+            if (n > room) {
+                status = 3;
+            } else if (n > old) {
+                need = pages_of(n, page) - pages_of(old, page);
+                if (old % page) {
+                    const int p = s.page_table[b * s.page_row + old / page];
+                    if (is_page(s, p) && refs_of(s, p) > 1) {
+                        status = 2;
+                        need = 0;
+                    }
+                }
+            }
+            A.need[b] = need;
+            A.status[b] = status;
+        }
+        // (what is above 2^31 - 1 is above the number of pages too)
+        const int64_t end = asked + before(need, S) + need;
+        if (b < s.batch) A.end[b] = end > 0x7fffffff ? 0x7fffffff : (int)end;
+        asked += S.total;
+    }
+    __syncthreads();
+    const int found = asked > 0 ? find_free(s, asked < s.pages ? asked : s.pages, A.list, S) : 0;
+    for (int64_t b = warp; b < s.batch; b += PLAN_W) {
+        const int old = __ldcg(A.old + b), n = A.lens[b], need = __ldcg(A.need + b), end = __ldcg(A.end + b);
+        if (n <= old || __ldcg(A.status + b) != 0) continue;
+        if (need > 0 && end > found) {
+            if (lane == 0) A.status[b] = 1;
+            continue;
+        }
+        for (int i = lane; i < need; i += 32) {
+            const int p = __ldcg(A.list + end - need + i);
+            s.page_table[b * s.page_row + pages_of(old, page) + i] = p;
+            s.refs[p] = 1;
+        }
+        if (lane == 0) s.kv_lens[b] = n;
+    }
+    if (!slots_here) return;
+    __syncthreads();
+    write_slots(A, threadIdx.x, PLAN_NT);
+}
+
+// ---- copies of entries ----
+
+// Bytes of a row of one entry that lie together, and where rows lie.
+struct Data {
+    char *k, *v;
+    int64_t heads, row;                // rows of an entry, and their units of V bytes
+    int64_t k_layer, k_page, k_entry, k_head, v_layer, v_page, v_entry, v_head;   // in units
+};
+
+struct Fork {
+    int from, to;                      // pages; to: -1 where there is nothing to copy
+    int entries;                       // of that page
+    int parent, child, full;           // sequences and full pages; child: -1 if it stayed empty
+};
+
+// One block: lengths before the call, the children that are taken, pages for those parents'
+// entries that do not fill a page.  A child is claimed by the first that names it: the least of
+// the marks i - n that the claimants leave in its length.
+__global__ void __launch_bounds__(PLAN_NT) k_fork_plan(dbs_page_state s, const int32_t *parents, const int32_t *children, int n,
+                                                       int32_t *status, Fork *forks, int32_t *list)
+{
+    __shared__ Sums S;
+    const int page = (int)s.page_size;
+    for (int i = threadIdx.x; i < n; i += PLAN_NT) {
+        const int p = parents[i], c = children[i];
+        Fork f{0, -1, 0, p, -1, 0};
+        if (p >= 0 && p < s.batch && c >= 0 && c < s.batch) {
+            const int len = length(s, p);
+            f.full = len / page;
+            f.entries = len % page;
+            if (length(s, c) == 0) f.child = c;
+        }
+        forks[i] = f;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += PLAN_NT)
+        if (forks[i].child >= 0) s.kv_lens[forks[i].child] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += PLAN_NT)
+        if (forks[i].child >= 0) atomicMin(s.kv_lens + forks[i].child, i - n);
+    __syncthreads();
+    int asked = 0;
+    for (int i0 = 0; i0 < n; i0 += PLAN_NT) {
+        const int i = i0 + threadIdx.x;
+        int need = 0;
+        if (i < n) {
+            Fork &f = forks[i];
+            const bool won = f.child >= 0 && __ldcg(s.kv_lens + f.child) == i - n;
+            status[i] = won ? 0 : 2;
+            need = won && f.entries > 0;
+            if (won && need) {
+                f.from = s.page_table[f.parent * s.page_row + f.full];
+                if (!is_page(s, f.from)) f.from = -1;
+            }
+        }
+        const int at = asked + (int)before(need, S);
+        if (need) forks[i].to = at;                // its place among the free pages
+        asked += (int)S.total;
+    }
+    __syncthreads();
+    const int found = asked > 0 ? find_free(s, asked, list, S) : 0;
+    for (int i = threadIdx.x; i < n; i += PLAN_NT) {
+        Fork &f = forks[i];
+        if (status[i] != 0) {
+            f.child = f.to = -1;
+            continue;
+        }
+        if (f.to >= found) {
+            status[i] = 1;
+            s.kv_lens[f.child] = 0;
+            f.child = f.to = -1;
+            continue;
+        }
+        s.kv_lens[f.child] = f.full * page + f.entries;
+        if (f.to >= 0) {
+            f.to = __ldcg(list + f.to);
+            s.page_table[f.child * s.page_row + f.full] = f.to;
+            s.refs[f.to] = 1;
+            if (f.from < 0) f.to = -1;             // (nothing to copy from)
+        }
+    }
+}
+
+// blockIdx.z: the fork; y: K and V of each layer, and before them the names of the
+// shared pages; x: the page's entries.
+template <class V>
+__global__ void __launch_bounds__(256) k_fork_copy(Data D, dbs_page_state s, const Fork *forks)
+{
+    const Fork f = forks[blockIdx.z];
+    if (f.child < 0) return;
+    const int64_t u0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    if (blockIdx.y == 0) {
+        for (int64_t c = u0; c < f.full; c += step) {
+            const int p = s.page_table[f.parent * s.page_row + c];
+            s.page_table[f.child * s.page_row + c] = p;
+            if (is_page(s, p)) atomicAdd(s.refs + p, 1);
+        }
+        return;
+    }
+    if (f.to < 0) return;
+    const int layer = (int)(blockIdx.y - 1) >> 1, is_v = (int)(blockIdx.y - 1) & 1;
+    V *base = (V *)(is_v ? D.v : D.k) + layer * (is_v ? D.v_layer : D.k_layer);
+    const int64_t by_page = is_v ? D.v_page : D.k_page, by_entry = is_v ? D.v_entry : D.k_entry, by_head = is_v ? D.v_head : D.k_head;
+    const int64_t per = D.heads * D.row, all = f.entries * per;
+    for (int64_t u = u0; u < all; u += step) {
+        const int64_t e = u / per, r = u - e * per, h = r / D.row, at = e * by_entry + h * by_head + (r - h * D.row);
+        base[f.to * by_page + at] = base[f.from * by_page + at];
+    }
+}
+
+// ---- accepted drafted tokens ----
+
+struct Compact {
+    Data d;
+    dbs_page_state s;
+    const int32_t *tree_lens, *accepted, *accepted_lens;
+    int64_t max_accepted, stride;
+    int32_t *new_lens;
+};
+
+constexpr int MOVE_NT = 256;
+
+// blockIdx.z: the sequence; y: K or V of a layer; x: units of an entry, one a thread.
+// Numbers ascend, so place i is behind no number that comes later: a thread may load any of its
+// units before it stores those of earlier places, in the list's order.
+template <class V>
+__global__ void __launch_bounds__(MOVE_NT) k_compact(Compact A)
+{
+    const dbs_page_state &s = A.s;
+    __shared__ int64_t from[MOVE_NT], to[MOVE_NT];         // units
+    __shared__ int ends;
+    const int64_t b = blockIdx.z;
+    const int layer = (int)blockIdx.y >> 1, is_v = (int)blockIdx.y & 1;
+    const Data &D = A.d;
+    V *base = (V *)(is_v ? D.v : D.k) + layer * (is_v ? D.v_layer : D.k_layer);
+    const int64_t by_page = is_v ? D.v_page : D.k_page, by_entry = is_v ? D.v_entry : D.k_entry, by_head = is_v ? D.v_head : D.k_head;
+    const int kv = length(s, b);
+    int tree = A.tree_lens[b];
+    tree = tree < 0 ? 0 : tree > kv ? kv : tree;
+    const int first = kv - tree;
+    const int64_t given = A.accepted_lens ? A.accepted_lens[b] : A.max_accepted;
+    const int n = (int)(given < 0 ? 0 : given > A.max_accepted ? A.max_accepted : given);
+    const int32_t *list = A.accepted + b * A.stride;
+    const int64_t u = (int64_t)blockIdx.x * MOVE_NT + threadIdx.x, per = D.heads * D.row;
+    const int64_t h = u / D.row, mine = h * by_head + (u - h * D.row);
+    int kept = 0;
+    auto place = [&](int j) {
+        int64_t page = b;
+        int in = j;
+        if (s.page_table) {
+            const int size = (int)s.page_size;
+            const int64_t p = s.page_table[b * s.page_row + j / size];
+            page = p < 0 ? 0 : p >= s.pages ? s.pages - 1 : p;
+            in = j % size;
+        }
+        return page * by_page + in * by_entry;
+    };
+    for (int i0 = 0; i0 < n; i0 += MOVE_NT) {
+        const int i = i0 + threadIdx.x, most = n - i0 < MOVE_NT ? n - i0 : MOVE_NT;
+        if (threadIdx.x == 0) ends = most;
+        __syncthreads();
+        if (i < n) {
+            const int a = list[i], prior = i ? list[i - 1] : -1;
+            if (a < 0 || a >= tree || a <= prior) {
+                atomicMin(&ends, (int)threadIdx.x);
+            } else {
+                from[threadIdx.x] = a == i ? -1 : place(first + a);
+                to[threadIdx.x] = place(first + i);        // (an ascending list: i <= a < tree)
+            }
+        }
+        __syncthreads();
+        const int m = ends;
+        if (u < per)
+            for (int k0 = 0; k0 < m; k0 += 8) {
+                V x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k0 + k < m && from[k0 + k] >= 0) x[k] = base[from[k0 + k] + mine];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k0 + k < m && from[k0 + k] >= 0) base[to[k0 + k] + mine] = x[k];
+            }
+        kept += m;
+        if (m < most) break;
+        __syncthreads();                                   // the list has been read
+    }
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) A.new_lens[b] = first + kept;
+}
+
+// ---- host ----
+
+bool state_ok(const dbs_page_state *s, bool table)
+{
+    return s && s->batch >= 0 && s->batch < (int64_t(1) << 24) && s->max_pages >= 0 && s->pages >= 0 && s->page_size >= 1 &&
+           s->page_size < (int64_t(1) << 31) && s->pages < 0x7fffffff && s->max_pages < (int64_t(1) << 31) &&
+           s->pages * s->page_size < (int64_t(1) << 31) && s->max_pages * s->page_size < (int64_t(1) << 31) &&
+           (s->batch == 0 || (s->kv_lens && (!table || ((s->page_table || s->max_pages == 0) && (s->batch == 1 || s->page_row >= s->max_pages)))));
+}
+
+// Rows as long as they lie together, and the width of a unit: 16 bytes where everything is a
+// multiple of that, else an element.
+bool data_of(const dbs_cache_data &c, Data &D, int &unit)
+{
+    const int64_t e = c.element_bytes;
+    int64_t k[4] = {c.k_layer, c.k_page, c.k_entry, c.k_head}, v[4] = {c.v_layer, c.v_page, c.v_entry, c.v_head};
+    int64_t heads = c.heads, row = c.head_dim;
+    if (heads == 1 || (k[3] == row && v[3] == row)) {
+        row *= heads;
+        heads = 1;
+        k[3] = v[3] = 0;
+    }
+    bool wide = aligned16(c.k) && aligned16(c.v) && row * e % 16 == 0;
+    for (int i = 0; i < 4; ++i) wide = wide && k[i] * e % 16 == 0 && v[i] * e % 16 == 0;
+    unit = wide ? 16 : (int)e;
+    const int64_t by = unit / e;
+    D = {(char *)c.k, (char *)c.v, heads, row / by, k[0] / by, k[1] / by, k[2] / by, k[3] / by, v[0] / by, v[1] / by, v[2] / by, v[3] / by};
+    return true;
+}
+
+bool data_ok(const dbs_cache_data *c, const dbs_page_state *s, bool work)
+{
+    if (!c || c->layers < 0 || c->layers >= 32768 || c->heads < 0 || c->heads >= (int64_t(1) << 31) || c->head_dim < 0 ||
+        c->head_dim >= (int64_t(1) << 31) || c->heads * c->head_dim >= (int64_t(1) << 31) ||
+        (c->element_bytes != 1 && c->element_bytes != 2 && c->element_bytes != 4 && c->element_bytes != 8))
+        return false;
+    if (!work || c->layers == 0 || c->heads == 0 || c->head_dim == 0) return true;
+    if (!c->k || !c->v) return false;
+    const int64_t entry[2][4] = {{c->k_layer, c->k_page, c->k_entry, c->k_head}, {c->v_layer, c->v_page, c->v_entry, c->v_head}};
+    const int64_t count[4] = {c->layers, s->pages, s->page_size, c->heads};
+    for (auto &by : entry)
+        for (int i = 0; i < 4; ++i)
+            if (by[i] < 0 || (count[i] > 1 && by[i] < c->head_dim) || by[i] >= int64_t(1) << 50) return false;
+    return true;
+}
+
+// f(V) with V the unit's type.
+template <class F> dbs_status by_unit(int unit, F f)
+{
+    return unit == 16 ? f(uint4{}) : unit == 8 ? f(uint64_t{}) : unit == 4 ? f(uint32_t{}) : unit == 2 ? f(uint16_t{}) : f(uint8_t{});
+}
+
+constexpr int64_t up16(int64_t n) { return (n + 15) & ~int64_t(15); }
+
+}  // namespace
+
+extern "C" {
+
+dbs_status dbs_cache_resize_scratch(const dbs_page_state *s, int64_t *bytes)
+{
+    if (!bytes || !state_ok(s, false)) return DBS_ERR_INVALID_ARG;
+    *bytes = up16(4 * (3 * s->batch + s->pages));
+    return DBS_OK;
+}
+
+dbs_status dbs_cache_resize(const dbs_page_state *s, const int32_t *lens, int32_t *status, int32_t *slots, int64_t columns, void *scratch,
+                            int64_t scratch_bytes, void *stream)
+{
+    if (!state_ok(s, true) || columns < 0 || columns >= (int64_t(1) << 31)) return DBS_ERR_INVALID_ARG;
+    if (s->batch == 0) return DBS_OK;
+    int64_t need = 0;
+    if (dbs_cache_resize_scratch(s, &need) != DBS_OK || !lens || !status || (s->pages > 0 && !s->refs) || !scratch || !aligned16(scratch) ||
+        scratch_bytes < need || lens == s->kv_lens)
+        return DBS_ERR_INVALID_ARG;
+    int32_t *at = (int32_t *)scratch;
+    const Resize A{*s, lens, status, columns ? slots : nullptr, columns, at, at + s->batch, at + 2 * s->batch, at + 3 * s->batch};
+    // Slots by the one block while it is through with them before a second launch would
+    // be.
+    const int64_t all = A.slots ? s->batch * columns : 0;
+    const bool here = all > 0 && all <= 8 * PLAN_NT;
+    cudaStream_t st = (cudaStream_t)stream;
+    k_resize<<<1, PLAN_NT, 0, st>>>(A, here);
+    if (all > 0 && !here) {
+        const int64_t blocks = (all + 255) / 256;
+        k_slots<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(A);
+    }
+    return launched();
+}
+
+dbs_status dbs_cache_fork_scratch(const dbs_page_state *s, int64_t n, int64_t *bytes)
+{
+    if (!bytes || !state_ok(s, false) || n < 0 || n >= 65536) return DBS_ERR_INVALID_ARG;
+    *bytes = up16(n * (int64_t)(sizeof(Fork) + 4));
+    return DBS_OK;
+}
+
+dbs_status dbs_cache_fork(const dbs_cache_data *data, const dbs_page_state *s, const int32_t *parents, const int32_t *children, int64_t n,
+                          int32_t *status, void *scratch, int64_t scratch_bytes, void *stream)
+{
+    if (!state_ok(s, true) || n < 0 || n >= 65536 || !data_ok(data, s, n > 0)) return DBS_ERR_INVALID_ARG;
+    if (n == 0) return DBS_OK;
+    int64_t need = 0;
+    if (dbs_cache_fork_scratch(s, n, &need) != DBS_OK || !parents || !children || !status || (s->pages > 0 && !s->refs) || !scratch ||
+        !aligned16(scratch) || scratch_bytes < need)
+        return DBS_ERR_INVALID_ARG;
+    Fork *forks = (Fork *)scratch;
+    int32_t *list = (int32_t *)(forks + n);
+    cudaStream_t st = (cudaStream_t)stream;
+    k_fork_plan<<<1, PLAN_NT, 0, st>>>(*s, parents, children, (int)n, status, forks, list);
+    dbs_status got = launched();
+    if (got != DBS_OK || s->batch == 0) return got;
+    Data D{};
+    int unit = 16;
+    const bool any = data->layers > 0 && data->heads > 0 && data->head_dim > 0;
+    if (any) data_of(*data, D, unit);
+    const int64_t most = any ? s->page_size * D.heads * D.row : 1, blocks = (most + 1023) / 1024;
+    const dim3 grid((unsigned)(blocks < 256 ? blocks : 256), any ? (unsigned)(1 + 2 * data->layers) : 1u, (unsigned)n);
+    return by_unit(unit, [&](auto v) {
+        k_fork_copy<decltype(v)><<<grid, 256, 0, st>>>(D, *s, forks);
+        return launched();
+    });
+}
+
+dbs_status dbs_cache_compact(const dbs_cache_data *data, const dbs_page_state *s, const int32_t *tree_lens, const int32_t *accepted,
+                             int64_t max_accepted, int64_t accepted_stride, const int32_t *accepted_lens, int32_t *new_lens, void *stream)
+{
+    if (!state_ok(s, s && s->page_table) || s->batch >= 65536 || max_accepted < 0 || max_accepted >= (int64_t(1) << 31) ||
+        !data_ok(data, s, s->batch > 0))
+        return DBS_ERR_INVALID_ARG;
+    if (s->batch == 0) return DBS_OK;
+    if (!tree_lens || !new_lens || new_lens == s->kv_lens || (max_accepted > 0 && (!accepted || accepted_stride < 0)) ||
+        (!s->page_table && (s->max_pages > 1 || s->pages < s->batch)) || (s->max_pages > 0 && s->pages < 1))
+        return DBS_ERR_INVALID_ARG;
+    Compact A{{}, *s, tree_lens, accepted, accepted_lens, max_accepted, accepted_stride, new_lens};
+    int unit = 16;
+    const bool any = data->layers > 0 && data->heads > 0 && data->head_dim > 0;
+    if (any) data_of(*data, A.d, unit);
+    else A.d.row = 1;
+    const int64_t per = any ? A.d.heads * A.d.row : 1;
+    const dim3 grid((unsigned)((per + MOVE_NT - 1) / MOVE_NT), any ? (unsigned)(2 * data->layers) : 1u, (unsigned)s->batch);
+    return by_unit(unit, [&](auto v) {
+        k_compact<decltype(v)><<<grid, MOVE_NT, 0, (cudaStream_t)stream>>>(A);
+        return launched();
+    });
+}
+
+}  // extern "C"

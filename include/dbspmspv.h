@@ -593,6 +593,155 @@ typedef struct {
 /* Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */
 dbs_status dbs_penalize_logits(const dbs_logits_args *a, void *stream);
 
+/* ---- Around a paged cache: norms with rotation, windows, pages ----
+ *
+ * As above: ASYNC, nothing allocated, no state between calls, capturable, the same
+ * bits when repeated; strides in elements, not negative, innermost dimension
+ * contiguous. */
+
+/* Norms of queries and keys, each head's own, and their rotation in the same pass:
+ *     n = x * (sum_c x[c]^2 / head_dim + eps)^(-1/2) * weight
+ * over all head_dim entries, then the first `dim` of n turned as by dbs_rotary; fp32
+ * until the result's one rounding.  Groups with rotate = 0 are copied as they are (v,
+ * into a cache). */
+typedef struct {
+    dbs_rotary_heads heads;
+    const void *weight;        /* device [head_dim] of weight_dtype; NULL: ones */
+    dbs_dtype weight_dtype;
+} dbs_norm_heads;
+/* Arguments, limits and errors as of dbs_rotary (dim may be 0: norms alone, without table
+ * and positions); eps >= 0 and finite. */
+dbs_status dbs_norm_rotary(const dbs_norm_heads *parts, int32_t nparts, dbs_dtype dtype, int64_t batch, int64_t tokens,
+                           int32_t head_dim, int32_t dim, float eps, const float *table, int64_t table_rows,
+                           const int32_t *positions, const int32_t *slots, int64_t pages, int64_t page_size,
+                           int32_t interleaved, void *stream);
+
+/* Its gradient, for one or two groups of heads.  With g the result's gradient turned
+ * back, r the head's (sum x^2 / head_dim + eps)^(-1/2) and n = x r:
+ *     x' = r (weight g - n sum_c(weight g n)[c] / head_dim),   weight' = sum over heads of g n
+ * (a token whose position is outside the table: NaN in x' and weight'). */
+typedef struct {
+    const void *grad, *in;     /* [batch, tokens, heads, head_dim] each */
+    void *out;                 /* x'; may be grad or in (with its strides), else must not overlap them */
+    int64_t grad_batch, grad_token, grad_head;
+    int64_t in_batch, in_token, in_head;
+    int64_t out_batch, out_token, out_head;
+    int32_t heads;             /* 0 = absent (its weight' becomes 0) */
+    dbs_dtype weight_dtype;
+    const void *weight;        /* NULL: ones */
+    float *weight_grad;        /* device float32[head_dim], or NULL */
+} dbs_norm_gradient_heads;
+/* Bytes of scratch of a call (of the current device). */
+dbs_status dbs_norm_rotary_gradient_scratch(int32_t nparts, int32_t head_dim, int64_t *bytes);
+/*   scratch  device, 16-byte aligned; nothing in it is read by a later call
+ * Other arguments, limits and errors as of dbs_norm_rotary. */
+dbs_status dbs_norm_rotary_gradient(const dbs_norm_gradient_heads *parts, int32_t nparts, dbs_dtype dtype, int64_t batch,
+                                    int64_t tokens, int32_t head_dim, int32_t dim, float eps, const float *table,
+                                    int64_t table_rows, const int32_t *positions, int32_t interleaved, void *scratch,
+                                    int64_t scratch_bytes, void *stream);
+
+/* Attention with a sliding window and sinks over a cache, for one token or a prompt.
+ * Sequence b holds kv_lens[b] entries, the last q_lens[b] of them its tokens of this
+ * call; token t is at p = kv_lens[b] - q_lens[b] + t and sees the entries j <= p with
+ * p - j < window or j < sinks:
+ *     out[b, t, h] = sum_j softmax_j(scale q[b,t,h].k[j, h / G]) v[j, h / G]
+ * G = q_heads / kv_heads.  A token that sees none gets 0 and lse -inf, and so do the tokens
+ * t >= q_lens[b].  Entries that a token does not see take no part in its row, whatever they
+ * hold (NaN included).  Each probability is rounded once to `dtype` before it meets v where the products
+ * run on tensor cores (their sum, and so lse, takes them in fp32). */
+typedef struct {
+    dbs_dtype dtype;           /* DBS_F16 or DBS_BF16, of q, caches and out */
+    int32_t head_dim;          /* 1..256 */
+    int32_t q_heads, kv_heads; /* q_heads a multiple of kv_heads */
+    int64_t batch, tokens;     /* batch * tokens * q_heads < 2^31 */
+    const void *q;             /* [batch, tokens, q_heads, head_dim] */
+    int64_t q_batch, q_token, q_head;
+    const void *k, *v;         /* [pages, page_size, kv_heads, head_dim] */
+    int64_t k_page, k_entry, k_head;
+    int64_t v_page, v_entry, v_head;
+    int64_t pages, page_size;
+    const int32_t *page_table; /* as of dbs_tree_attention; pages that no token sees an entry of are not read */
+    int64_t max_pages, page_row;  /* max_pages * page_size at most 2^31 - 1024 */
+    const int32_t *kv_lens;    /* device [batch]; clamped to [0, max_pages * page_size] */
+    const int32_t *q_lens;     /* device [batch]; clamped to [0, tokens]; NULL = tokens */
+    int64_t window, sinks;     /* window >= 1, sinks >= 0 */
+    float scale;               /* finite */
+    void *out;                 /* [batch, tokens, q_heads, head_dim], each head in a place of its own */
+    int64_t o_batch, o_token, o_head;
+    float *lse;                /* device [batch, tokens, q_heads], natural logarithm, or NULL */
+} dbs_window_args;
+/* Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA.  Waits inside its kernels end after two seconds
+ * (dbs_operators_check). */
+dbs_status dbs_window_attention(const dbs_window_args *a, void *stream);
+
+/* Pages of a cache.  Sequence b owns the pages page_table[b, c], c < ceil(kv_lens[b] /
+ * page_size); refs[p] counts the owned entries of page_table that name page p (0: free).
+ * These calls keep that, in place; what page_table holds behind a sequence's pages stays
+ * as it is.  Page numbers outside [0, pages) are passed over.  What a call does is a
+ * function of its inputs alone: free pages are taken in the order of their numbers. */
+typedef struct {
+    int32_t *page_table;       /* device [batch, max_pages], rows page_row apart (>= max_pages) */
+    int64_t batch, max_pages, page_row;
+    int32_t *kv_lens;          /* device [batch], read as clamped to [0, max_pages * page_size] */
+    int32_t *refs;             /* device [pages] */
+    int64_t pages, page_size;  /* pages < 2^31 - 1, pages * page_size and max_pages * page_size < 2^31,
+                                  batch < 2^24 */
+} dbs_page_state;
+
+/* Gives every sequence a new length: cut (pages that it no longer owns lose a
+ * reference; 0 frees it), or grown by free pages.  All cuts come before all growth;
+ * then pages go to the sequences in their order.
+ *   lens     device int32[batch]; below 0: the sequence stays as it is
+ *   status   device int32[batch]: 0, or why a sequence kept its length: 1 the free pages
+ *            do not suffice for it and those before it that asked for pages, 2 it would
+ *            grow into a page that others own too (fork it first), 3 it is longer than
+ *            max_pages * page_size
+ *   slots    device int32[batch, columns], contiguous, or NULL: of the i-th new entry of b the slot
+ *            (page * page_size + its place in the page), as dbs_rotary takes it; -1 where there is none
+ *   scratch  device, 16-byte aligned, dbs_cache_resize_scratch bytes
+ * Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */
+dbs_status dbs_cache_resize_scratch(const dbs_page_state *state, int64_t *bytes);
+dbs_status dbs_cache_resize(const dbs_page_state *state, const int32_t *lens, int32_t *status, int32_t *slots,
+                            int64_t columns, void *scratch, int64_t scratch_bytes, void *stream);
+
+/* K and V of all layers: entry e of page p in layer l begins at l * layer + p * page +
+ * e * entry, its heads `head` apart. */
+typedef struct {
+    void *k, *v;               /* device [layers, pages, page_size, heads, head_dim], places apart from one another */
+    int64_t layers, heads, head_dim;
+    int32_t element_bytes;     /* 1, 2, 4 or 8: entries are copied as they are */
+    int64_t k_layer, k_page, k_entry, k_head;
+    int64_t v_layer, v_page, v_entry, v_head;
+} dbs_cache_data;
+
+/* Makes sequence children[i] a copy of parents[i]: it shares the full pages, and gets
+ * one of its own for the entries of a last page that is not full, which are copied in all layers.
+ * Lengths are those before the call.
+ *   parents, children  device int32[n]
+ *   status   device int32[n]: 0, or why children[i] stayed empty: 1 the free pages do not suffice
+ *            for it and those before it, 2 a number outside [0, batch), a child that is not
+ *            empty (kv_lens above 0), or one listed before
+ *   scratch  device, 16-byte aligned, dbs_cache_fork_scratch bytes
+ * n < 2^16, layers < 2^15.  Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */
+dbs_status dbs_cache_fork_scratch(const dbs_page_state *state, int64_t n, int64_t *bytes);
+dbs_status dbs_cache_fork(const dbs_cache_data *data, const dbs_page_state *state, const int32_t *parents,
+                          const int32_t *children, int64_t n, int32_t *status, void *scratch, int64_t scratch_bytes,
+                          void *stream);
+
+/* Keeps the accepted ones of drafted tokens: the last tree_lens[b] (clamped to
+ * [0, kv_lens[b]]) entries of sequence b are its drafted tokens, and entry accepted[b, i]
+ * of them moves to place i, in all layers.
+ *   accepted       device int32[batch, max_accepted], rows accepted_stride apart: ascending
+ *                  numbers below tree_lens[b]; the first that is not (-1, say) ends the list
+ *   accepted_lens  device int32[batch], or NULL = max_accepted
+ *   new_lens       device int32[batch]: kv_lens[b] - tree_lens[b] + those kept (kv_lens stays; not its address)
+ * Of `state` refs is not used; page_table may be NULL: sequence b is page b.  Drafted
+ * entries have to lie in pages that b alone owns.  batch < 2^16, layers < 2^15.
+ * Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */
+dbs_status dbs_cache_compact(const dbs_cache_data *data, const dbs_page_state *state, const int32_t *tree_lens,
+                             const int32_t *accepted, int64_t max_accepted, int64_t accepted_stride,
+                             const int32_t *accepted_lens, int32_t *new_lens, void *stream);
+
 /* Test hook (the paper has no counterpart): injects one allocation failure.
  * The k-th allocation attempt from now on (k = 0: the next one) fails as if
  * memory were exhausted -- device allocations (cudaMalloc) and the host

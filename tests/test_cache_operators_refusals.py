@@ -1,0 +1,216 @@
+"""Refusals of the operators around a paged cache: through the C ABI, whose checks
+run on the host before anything is launched, with addresses that are never
+read; and through the Python binding, without a GPU."""
+import ctypes
+import struct
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import __graft_entry__  # noqa: E402
+
+__graft_entry__.build()
+import dynamic_sparsity_spmspv_gb300 as dbs  # noqa: E402
+from dynamic_sparsity_spmspv_gb300 import _lib  # noqa: E402
+
+A = 4096                                     # an address; nothing behind it is touched
+OK, BAD = 0, 1
+NO_GPU = not torch.cuda.is_available()
+
+
+def part(inp=A, out=2 * A, strides=(512, 128, 64) * 2, heads=2, rotate=1, slots=0, weight=A, wtype=0):
+    return struct.pack("@" + _lib.NORM_HEADS, inp, out, *strides, heads, rotate, slots, weight, wtype)
+
+
+def norm(parts=None, n=1, **kw):
+    a = dict(dtype=2, batch=1, tokens=4, d=64, dim=64, eps=1e-6, table=A, rows=10, pos=A, slots=0, pages=0, page=1, il=0)
+    a.update(kw)
+    return _lib.load().dbs_norm_rotary(parts if parts is not None else part() * n, n, *a.values(), None)
+
+
+@pytest.mark.parametrize("kw", [dict(n=0), dict(n=4), dict(dtype=9), dict(batch=-1), dict(tokens=-1), dict(d=0), dict(d=1025), dict(dim=65),
+                                dict(dim=66), dict(dim=-2), dict(table=0), dict(pos=0), dict(rows=-1), dict(eps=-1e-9), dict(eps=float("nan")),
+                                dict(eps=float("inf")), dict(batch=1 << 20, tokens=1 << 20), dict(batch=1 << 12, tokens=1 << 14),
+                                dict(parts=part(inp=0)), dict(parts=part(out=0)), dict(parts=part(heads=-1)), dict(parts=part(heads=16385)),
+                                dict(parts=part(wtype=3)), dict(parts=part(slots=1)), dict(parts=part(slots=1), slots=A, pages=-1),
+                                dict(parts=part(slots=1), slots=A, pages=4, page=0), dict(parts=part(slots=1), slots=A, pages=1 << 30, page=64),
+                                dict(parts=part(strides=(512, 128, 64, 512, 128, 63))), dict(parts=part(strides=(512, 128, 64, 512, 0, 64))),
+                                dict(parts=part(strides=(512, -128, 64, 512, 128, 64))), dict(parts=part(out=A, strides=(512, 64, 256, 512, 128, 64))),
+                                dict(parts=part(out=A, slots=1), slots=A, pages=4, page=16)])
+def test_norm_refusals(kw):
+    assert norm(**kw) == BAD
+
+
+def test_norm_nothing_to_do():
+    assert norm(tokens=0) == OK and norm(batch=0, parts=part(inp=0)) == OK and norm(parts=part(heads=0, inp=0)) == OK
+    assert norm(parts=part(slots=1, out=0), slots=A, pages=0) == OK
+    assert _lib.load().dbs_norm_rotary(None, 1, 2, 1, 4, 64, 64, 1e-6, A, 10, A, 0, 0, 1, 0, None) == BAD
+
+
+GRAD = dict(grad=A, inp=2 * A, out=3 * A, strides=(512, 128, 64) * 3, heads=2, wtype=0, weight=A, dw=A)
+
+
+def gpart(**kw):
+    a = dict(GRAD)
+    a.update(kw)
+    return struct.pack("@" + _lib.NORM_GRADIENT_HEADS, a["grad"], a["inp"], a["out"], *a["strides"], a["heads"], a["wtype"], a["weight"], a["dw"])
+
+
+def gradient(parts=None, n=1, **kw):
+    a = dict(dtype=2, batch=1, tokens=4, d=64, dim=64, eps=1e-6, table=A, rows=10, pos=A, il=0, scratch=0, bytes=0)
+    a.update(kw)
+    return _lib.load().dbs_norm_rotary_gradient(parts if parts is not None else gpart() * n, n, *a.values(), None)
+
+
+@pytest.mark.parametrize("kw", [dict(n=0), dict(n=3), dict(dtype=9), dict(batch=-1), dict(tokens=-1), dict(d=0), dict(d=1025), dict(dim=65),
+                                dict(dim=-2), dict(table=0), dict(pos=0), dict(rows=-1), dict(eps=-1.0), dict(parts=gpart(grad=0)),
+                                dict(parts=gpart(inp=0)), dict(parts=gpart(out=0)), dict(parts=gpart(heads=-1)), dict(parts=gpart(wtype=5)),
+                                dict(parts=gpart(strides=(512, 128, 64, 512, 128, 64, 512, 128, 63))),
+                                dict(parts=gpart(strides=(-512, 128, 64, 512, 128, 64, 512, 128, 64))),
+                                dict(parts=gpart(strides=(512, 128, 64, 512, -128, 64, 512, 128, 64))),
+                                dict(parts=gpart(out=A, strides=(512, 64, 256, 512, 128, 64, 512, 128, 64))),
+                                dict(parts=gpart(out=2 * A, strides=(512, 128, 64, 512, 64, 256, 512, 128, 64)))])
+def test_norm_gradient_refusals(kw):
+    assert gradient(**kw) == BAD
+
+
+def test_norm_gradient_nothing_to_do_and_scratch():
+    assert gradient(parts=gpart(dw=0), tokens=0) == OK and gradient(parts=gpart(dw=0, heads=0, grad=0)) == OK
+    need = ctypes.c_int64(-1)
+    size = _lib.load().dbs_norm_rotary_gradient_scratch
+    assert size(0, 64, ctypes.byref(need)) == BAD and size(3, 64, ctypes.byref(need)) == BAD and size(1, 0, ctypes.byref(need)) == BAD
+    assert size(1, 1025, ctypes.byref(need)) == BAD and size(1, 64, None) == BAD
+    if not NO_GPU:
+        assert size(2, 64, ctypes.byref(need)) == OK and need.value > 0
+        assert gradient(scratch=0, bytes=1 << 30) == BAD and gradient(scratch=A, bytes=need.value // 4) == BAD and gradient(scratch=A + 8, bytes=1 << 30) == BAD
+
+
+WIN = dict(dtype=2, d=64, hq=8, hk=2, batch=2, tokens=3, q=A, q0=1536, q1=512, q2=64, k=A, v=A, k0=64, k1=64, k2=64, v0=64, v1=64, v2=64, pages=9,
+           page=16, pt=A, maxp=4, prow=4, kv=A, ql=0, window=5, sinks=0, scale=0.125, out=A, o0=1536, o1=512, o2=64, lse=0)
+
+
+def window(**kw):
+    a = dict(WIN)
+    a.update(kw)
+    return _lib.load().dbs_window_attention(_lib.WINDOW_ARGS.pack(*a.values()), None)
+
+
+@pytest.mark.parametrize("kw", [dict(dtype=0), dict(dtype=4), dict(d=0), dict(d=257), dict(hk=0), dict(hk=3), dict(hq=0), dict(hq=1), dict(hq=65538),
+                                dict(batch=-1), dict(tokens=-1), dict(q=0), dict(k=0), dict(v=0), dict(out=0), dict(kv=0), dict(pages=-1), dict(pages=0),
+                                dict(page=-1), dict(maxp=-1), dict(window=0), dict(window=-3), dict(sinks=-1), dict(scale=float("nan")),
+                                dict(scale=float("inf")), dict(q0=-1), dict(q1=-1), dict(q2=-1), dict(k0=-1), dict(k1=-1), dict(k2=-1), dict(v0=-1),
+                                dict(v1=-1), dict(v2=-1), dict(prow=-1), dict(o2=63), dict(o1=0), dict(o0=0), dict(pt=0), dict(pt=0, maxp=1, pages=1),
+                                dict(batch=1 << 31), dict(tokens=1 << 31), dict(batch=1 << 16, tokens=1 << 15), dict(batch=1 << 14, tokens=1 << 14),
+                                dict(page=64, maxp=(1 << 25) - 1), dict(page=1 << 30, maxp=2), dict(page=(1 << 31) - 1, maxp=1), dict(pages=1 << 31)])
+def test_window_refusals(kw):
+    assert window(**kw) == BAD
+
+
+def test_window_nothing_to_do():
+    assert window(batch=0, q=0, out=0, kv=0) == OK and window(tokens=0, q=0, out=0) == OK
+    assert _lib.load().dbs_window_attention(None, None) == BAD
+
+
+STATE = dict(table=A, batch=3, maxp=4, prow=4, kv=A, refs=A, pages=9, page=16)
+
+
+def state(**kw):
+    a = dict(STATE)
+    a.update(kw)
+    return _lib.PAGE_STATE.pack(*a.values())
+
+
+BAD_STATES = [dict(batch=-1), dict(batch=1 << 24), dict(maxp=-1), dict(prow=3), dict(kv=0), dict(pages=-1), dict(page=0), dict(page=-4),
+              dict(pages=1 << 28), dict(maxp=1 << 28, prow=1 << 28), dict(pages=0x7fffffff, page=1), dict(page=1 << 31, pages=0, maxp=0), dict(table=0)]
+
+
+@pytest.mark.parametrize("kw", BAD_STATES)
+def test_page_state_refusals(kw):
+    lib, big = _lib.load(), 1 << 40
+    assert lib.dbs_cache_resize(state(**kw), 2 * A, A, 0, 0, A, big, None) == BAD
+    assert lib.dbs_cache_fork(data(), state(**kw), A, A, 2, A, A, big, None) == BAD
+
+
+def data(k=A, v=A, layers=2, heads=2, d=64, e=2, strides=(18432, 2048, 128, 64) * 2):
+    return _lib.CACHE_DATA.pack(k, v, layers, heads, d, e, *strides)
+
+
+def test_resize_refusals():
+    lib, big = _lib.load(), 1 << 40
+
+    def resize(s=state(), lens=2 * A, status=A, slots=0, columns=0, scratch=A, size=big):
+        return lib.dbs_cache_resize(s, lens, status, slots, columns, scratch, size, None)
+
+    for kw in (dict(s=None), dict(lens=0), dict(status=0), dict(columns=-1), dict(columns=1 << 31), dict(scratch=0), dict(scratch=A + 4), dict(size=16),
+               dict(s=state(refs=0)), dict(lens=A)):
+        assert resize(**kw) == BAD, kw
+    assert resize(s=state(batch=0, kv=0, table=0), lens=0, status=0, scratch=0) == OK
+    need = ctypes.c_int64(-1)
+    assert lib.dbs_cache_resize_scratch(state(), ctypes.byref(need)) == OK and need.value >= 4 * (3 * 3 + 9)
+    assert lib.dbs_cache_resize_scratch(state(), None) == BAD and lib.dbs_cache_resize_scratch(None, ctypes.byref(need)) == BAD
+
+
+def test_fork_refusals():
+    lib, big = _lib.load(), 1 << 40
+
+    def fork(d=data(), s=state(), parents=A, children=A, n=2, status=A, scratch=A, size=big):
+        return lib.dbs_cache_fork(d, s, parents, children, n, status, scratch, size, None)
+
+    cases = [dict(d=None), dict(s=None), dict(parents=0), dict(children=0), dict(n=-1), dict(n=65536), dict(status=0), dict(scratch=0),
+             dict(scratch=A + 8), dict(size=8), dict(s=state(refs=0))]
+    cases += [dict(d=data(**kw)) for kw in BAD_DATA]
+    for kw in cases:
+        assert fork(**kw) == BAD, kw
+    assert fork(n=0, parents=0, children=0, status=0, scratch=0) == OK
+    need = ctypes.c_int64(-1)
+    assert lib.dbs_cache_fork_scratch(state(), 3, ctypes.byref(need)) == OK and need.value > 0
+    assert lib.dbs_cache_fork_scratch(state(), -1, ctypes.byref(need)) == BAD and lib.dbs_cache_fork_scratch(state(), 3, None) == BAD
+
+
+BAD_DATA = [dict(k=0), dict(v=0), dict(layers=-1), dict(layers=32768), dict(heads=-1), dict(heads=1 << 31), dict(d=-1), dict(d=1 << 31),
+            dict(heads=1 << 16, d=1 << 16), dict(e=3), dict(e=0), dict(e=16), dict(strides=(18432, 2048, 128, 63) + (18432, 2048, 128, 64)),
+            dict(strides=(18432, 2048, 128, 64) + (18432, 2048, 0, 64)), dict(strides=(18432, 0, 128, 64) + (18432, 2048, 128, 64)),
+            dict(strides=(0, 2048, 128, 64) * 2), dict(strides=(-18432, 2048, 128, 64) * 2)]
+
+
+def test_compact_refusals():
+    lib = _lib.load()
+
+    def compact(d=data(), s=state(), tree=A, acc=A, most=4, stride=4, lens=0, new=2 * A):
+        return lib.dbs_cache_compact(d, s, tree, acc, most, stride, lens, new, None)
+
+    cases = [dict(d=None), dict(s=None), dict(tree=0), dict(acc=0), dict(most=-1), dict(most=1 << 31), dict(stride=-1), dict(new=0), dict(new=A),
+             dict(s=state(batch=65536)), dict(s=state(table=0)), dict(s=state(table=0, maxp=1, pages=2)), dict(s=state(pages=0))]
+    cases += [dict(d=data(**kw)) for kw in BAD_DATA]
+    for kw in cases:
+        assert compact(**kw) == BAD, kw
+    assert compact(s=state(batch=0, kv=0, table=0), tree=0, acc=0, new=0) == OK
+
+
+@pytest.mark.skipif(not NO_GPU, reason="host tensors are refused before anything else")
+def test_binding_refuses_host_tensors_and_wrong_arguments():
+    t, i = torch.zeros(2, 3, 2, 64, dtype=torch.float16), torch.zeros(2, dtype=torch.int32)
+    calls = [lambda: dbs.norm_rotary(t, None, None, None, t, i), lambda: dbs.norm_rotary_append(t, t, t, None, None, t, i, t, t, i),
+             lambda: dbs.norm_rotary_gradient(t, None, t, None, None, None, t, i), lambda: dbs.window_attention(t, t, t, i, 4),
+             lambda: dbs.cache_resize(i, i, i, i, 16), lambda: dbs.cache_fork(t, t, i, i, i, i, i), lambda: dbs.cache_compact(t, t, i, i, i)]
+    for call in calls:
+        with pytest.raises(dbs.DbsError):
+            call()
+    for name in ("norm_rotary", "norm_rotary_append", "norm_rotary_gradient", "window_attention", "cache_resize", "cache_fork", "cache_compact"):
+        with pytest.raises(TypeError):
+            getattr(dbs, name)(t)
+        assert getattr(dbs, "dbs_" + name) is getattr(dbs, name) and getattr(dbs, name).__doc__
+    with pytest.raises(TypeError):
+        dbs.window_attention(t, t, t, i, 4, windows=3)
+
+
+def test_argument_structs_have_the_header_s_size():
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sizes = {"dbs_norm_heads": struct.calcsize("@" + _lib.NORM_HEADS), "dbs_norm_gradient_heads": struct.calcsize("@" + _lib.NORM_GRADIENT_HEADS),
+             "dbs_window_args": _lib.WINDOW_ARGS.size, "dbs_page_state": _lib.PAGE_STATE.size, "dbs_cache_data": _lib.CACHE_DATA.size}
+    src = '#include <stddef.h>\n#include "include/dbspmspv.h"\n' + "".join(f'_Static_assert(sizeof({k}) == {v}, "size");\n' for k, v in sizes.items())
+    src += '_Static_assert(offsetof(dbs_window_args, scale) == 192 && offsetof(dbs_cache_data, k_layer) == 48, "places");\n'
+    assert subprocess.run(["gcc", "-x", "c", "-fsyntax-only", "-I", root, "-"], input=src.encode(), cwd=root).returncode == 0

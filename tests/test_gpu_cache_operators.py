@@ -1,0 +1,702 @@
+"""GPU parity of the operators around a paged cache against plain 64-bit forms:
+norms with rotation and their gradient, attention with a window and sinks, pages.
+
+Tolerances, from the formulas (u = unit roundoff of the type that a result is
+rounded to: 2^-24 fp32, 2^-11 fp16, 2^-8 bf16; e = 2^-24):
+  norm       a head's sum of squares: at most 32 terms a lane and 5 exchanges, each
+             rounded once, and the squares, so 38 e relative; its root halves that; with the division,
+             root, two products and a turn (3 e of |a cos| + |b sin|) at most 28 e:
+             32 e (|a cos| + |b sin|) + u |y|, and half the spacing of fp16's subnormals
+  gradient   x': the same root, a dot product of the same shape (38 e of the sum of its
+             magnitudes), products: 64 e r (|w g| + |n| mean |w g n|) + u |x'|, |g| taken as
+             |a cos| + |b sin|; w': chains of at most 64 + 64 terms here:
+             192 e sum |g n| + u |w'|
+  attention  (u + 3e-4) * sum p |v| + u |out|: probabilities rounded once to the
+             caches' type, and fp32 scores, whose error is at most
+             head_dim * 2^-23 * scale * sum |q k| (1.1e-4 at head_dim 128,
+             1.6e-4 at 256 for N(0,1) inputs), twice (numerator and sum)
+  pages      whole numbers and copies: equal
+"""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import __graft_entry__  # noqa: E402
+
+__graft_entry__.build()
+import dynamic_sparsity_spmspv_gb300 as dbs  # noqa: E402
+
+DEV = "cuda"
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+U = {"f32": 2.0**-24, "f16": 2.0**-11, "bf16": 2.0**-8}
+ETA = {"f32": 2.0**-140, "f16": 2.0**-25, "bf16": 2.0**-133}
+E = 2.0**-24
+NAN, INF = float("nan"), float("inf")
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def close(got, ref, tol):
+    got = f64(got)
+    assert got.shape == ref.shape
+    same = (got == ref) | (np.isnan(got) & np.isnan(ref))
+    with np.errstate(invalid="ignore"):
+        ok = same | (np.abs(got - ref) <= tol)
+    assert ok.all(), f"{(~ok).sum()} of {ok.size} off, worst {np.nanmax(np.abs(got - ref)[~ok] / np.broadcast_to(tol, ok.shape)[~ok])} x tolerance"
+
+
+def rnd(rng, dt, *shape):
+    return torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(DT[dt]).to(DEV)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+# ---- norms with rotation ----
+
+
+def turned(x, table, pos, il, back=False):
+    """Turned heads and |a cos| + |b sin|; x [..., tokens, heads, D], pos [..., tokens]."""
+    dim = table.shape[1]
+    c, s = table[pos][..., None, : dim // 2], table[pos][..., None, dim // 2:] * (-1 if back else 1)
+    y, mag = x.copy(), np.abs(x)
+    lo, hi = (slice(0, dim, 2), slice(1, dim, 2)) if il else (slice(0, dim // 2), slice(dim // 2, dim))
+    a, b = x[..., lo], x[..., hi]
+    y[..., lo], y[..., hi] = a * c - b * s, a * s + b * c
+    mag[..., lo], mag[..., hi] = np.abs(a * c) + np.abs(b * s), np.abs(a * s) + np.abs(b * c)
+    return y, mag
+
+
+def norm_ref(x, w, table, pos, il, eps):
+    n = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    return turned(n if w is None else n * w, table, pos, il)
+
+
+def grad_ref(g, x, w, table, pos, il, eps):
+    w = np.ones(x.shape[-1]) if w is None else w
+    r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    n = x * r
+    g, mag = turned(g, table, pos, il, back=True)
+    dx = r * (w * g - n * (w * g * n).mean(-1, keepdims=True))
+    dx_mag = r * (np.abs(w) * mag + np.abs(n) * (np.abs(w * n) * mag).mean(-1, keepdims=True))
+    axes = tuple(range(x.ndim - 1))
+    return dx, dx_mag, (g * n).sum(axes), (mag * np.abs(n)).sum(axes)
+
+
+def heads_of(rng, dt, lead, heads, D, layout, size=1.0):
+    """[*lead, heads, D] in one of several layouts."""
+    t = (size * torch.from_numpy(rng.standard_normal((*lead, heads, D)).astype(np.float32))).to(DT[dt]).to(DEV)
+    if layout == "first" and len(lead) == 2:
+        return t.transpose(1, 2).contiguous().transpose(1, 2)
+    if layout == "odd":
+        wide = torch.full((*lead, heads, D + 5), NAN, dtype=DT[dt], device=DEV)
+        wide[..., 3:3 + D] = t
+        return wide[..., 3:3 + D]
+    return t
+
+
+NORM_CASES = [
+    # tokens, heads, head_dim, dim, interleaved, layout
+    ((1,), 1, 2, 2, False, "plain"), ((1,), 1, 1, 0, False, "plain"), ((3,), 2, 7, 4, True, "plain"), ((5,), 40, 128, 128, False, "plain"),
+    ((2, 9), 4, 64, 64, True, "plain"), ((2, 9), 4, 128, 64, False, "first"), ((1, 33), 3, 96, 96, True, "first"),
+    ((1, 33), 3, 96, 48, False, "plain"), ((2, 5), 2, 80, 80, False, "plain"), ((2, 5), 2, 80, 40, True, "plain"), ((7,), 3, 256, 256, False, "plain"),
+    ((4,), 2, 256, 24, True, "odd"), ((3,), 1, 1024, 512, False, "plain"), ((3,), 2, 1024, 512, True, "odd"), ((2, 3), 1, 1000, 510, False, "plain"),
+    ((17,), 9, 72, 8, True, "plain"), ((0,), 2, 64, 64, False, "plain"), ((2, 0), 2, 64, 64, False, "plain"), ((6,), 5, 520, 512, False, "plain"),
+    ((400,), 12, 128, 128, False, "plain")]
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("lead,heads,D,dim,il,layout", NORM_CASES)
+def test_norm_rotary(dt, lead, heads, D, dim, il, layout):
+    rng = np.random.default_rng(len(lead) * 7 + heads * 1000 + D + dim)
+    q, k = heads_of(rng, dt, lead, heads, D, layout, 2.0), heads_of(rng, dt, lead, max(1, heads // 3), D, layout, 0.5)
+    qw, kw = rnd(rng, dt, D), rnd(rng, "f32", D)
+    table = dbs.rotary_table(50, dim) if dim else torch.zeros((50, 0), device=DEV)
+    pos = torch.from_numpy(rng.integers(0, 50, lead).astype(np.int32)).to(DEV)
+    qo, ko = dbs.norm_rotary(q, k, qw, kw, table, pos, eps=1e-5, interleaved=il)
+    assert qo.dtype == q.dtype and ko.shape == k.shape
+    for got, x, w in ((qo, q, qw), (ko, k, kw)):
+        ref, mag = norm_ref(f64(x), f64(w), f64(table), pos.cpu().numpy(), il, np.float64(np.float32(1e-5)))
+        close(got, ref, 32 * E * mag + U[dt] * np.abs(ref) + ETA[dt])
+    again = dbs.norm_rotary(q, k, qw, kw, table, pos, eps=1e-5, interleaved=il)
+    assert torch.equal(again[0], qo) and torch.equal(again[1], ko)
+    # in place, and without weights and keys
+    x = q.clone()
+    r = dbs.norm_rotary(x, None, qw, None, table, pos, eps=1e-5, interleaved=il, q_out=x)
+    assert r[0].data_ptr() == x.data_ptr() and r[1] is None
+    if layout == "odd":                                                    # (the copy lies on other boundaries: sums in another order)
+        ref, mag = norm_ref(f64(q), f64(qw), f64(table), pos.cpu().numpy(), il, np.float64(np.float32(1e-5)))
+        close(x, ref, 32 * E * mag + U[dt] * np.abs(ref) + ETA[dt])
+    else:
+        assert torch.equal(x, qo)
+    bare = dbs.norm_rotary(q, None, None, None, table, pos, eps=1e-5, interleaved=il)[0]
+    ref, mag = norm_ref(f64(q), None, f64(table), pos.cpu().numpy(), il, np.float64(np.float32(1e-5)))
+    close(bare, ref, 32 * E * mag + U[dt] * np.abs(ref) + ETA[dt])
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("lead,heads,D,dim,il,layout", NORM_CASES)
+def test_norm_rotary_gradient(dt, lead, heads, D, dim, il, layout):
+    rng = np.random.default_rng(len(lead) * 11 + heads * 1000 + D + dim)
+    kv = max(1, heads // 3)
+    q, k = heads_of(rng, dt, lead, heads, D, layout, 2.0), heads_of(rng, dt, lead, kv, D, layout, 0.5)
+    qg, kg = heads_of(rng, dt, lead, heads, D, layout), heads_of(rng, dt, lead, kv, D, "plain")
+    qw, kw = rnd(rng, "f32", D), rnd(rng, dt, D)
+    table = dbs.rotary_table(50, dim) if dim else torch.zeros((50, 0), device=DEV)
+    pos = torch.from_numpy(rng.integers(0, 50, lead).astype(np.int32)).to(DEV)
+    got = dbs.norm_rotary_gradient(qg, kg, q, k, qw, kw, table, pos, eps=1e-5, interleaved=il)
+    eps, t, p = np.float64(np.float32(1e-5)), f64(table), pos.cpu().numpy()
+    for dx, dw, g, x, w in ((got[0], got[2], qg, q, qw), (got[1], got[3], kg, k, kw)):
+        assert dx.dtype == x.dtype and dw.dtype == torch.float32
+        ref, mag, wref, wmag = grad_ref(f64(g), f64(x), f64(w), t, p, il, eps)
+        close(dx, ref, 64 * E * mag + U[dt] * np.abs(ref) + ETA[dt])
+        close(dw, wref, 192 * E * wmag + E * np.abs(wref) + 1e-30)
+    again = dbs.norm_rotary_gradient(qg, kg, q, k, qw, kw, table, pos, eps=1e-5, interleaved=il)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    alone = dbs.norm_rotary_gradient(qg, None, q, None, None, None, table, pos, eps=1e-5, interleaved=il)
+    assert alone[1] is None and alone[3] is None
+    ref, mag, wref, wmag = grad_ref(f64(qg), f64(q), None, t, p, il, eps)
+    close(alone[0], ref, 64 * E * mag + U[dt] * np.abs(ref) + ETA[dt])
+    close(alone[2], wref, 192 * E * wmag + E * np.abs(wref) + 1e-30)
+
+
+def test_norm_rotary_gradient_against_differences():
+    """d/ds of sum(G * norm_rotary(x + s d)) at 0 by central differences in 64 bits (the forward reference, checked
+    above); their own error is h^2 / 6 times a third derivative of about 40 here, and rounding 2^-52 / h of sums of
+    about 100: with h = 1e-4 below 1e-6."""
+    rng = np.random.default_rng(5)
+    x, G, d = rng.standard_normal((3, 2, 16)).astype(np.float32), rng.standard_normal((3, 2, 16)).astype(np.float32), rng.standard_normal((3, 2, 16))
+    w, dw = rng.standard_normal(16).astype(np.float32), rng.standard_normal(16)
+    table, pos = dbs.rotary_table(20, 16), ints([4, 0, 19])
+    eps, t, p, h = np.float64(np.float32(1e-5)), f64(table), pos.cpu().numpy(), 1e-4
+
+    def value(s, u):
+        return (G.astype(np.float64) * norm_ref(x + s * d, w + u * dw, t, p, False, eps)[0]).sum()
+
+    dx, _, dwt, _ = dbs.norm_rotary_gradient(*(torch.from_numpy(a).to(DEV) if a is not None else None for a in (G, None, x, None, w, None)),
+                                             table, pos, eps=1e-5)
+    for got, want in (((f64(dx) * d).sum(), (value(h, 0) - value(-h, 0)) / (2 * h)), ((f64(dwt) * dw).sum(), (value(0, h) - value(0, -h)) / (2 * h))):
+        assert abs(got - want) < 1e-4                                         # 96 and 16 products of fp32 results of magnitude below 10
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("page,D,odd", [(1, 64, False), (16, 128, False), (24, 80, False), (5, 33, True)])
+def test_norm_rotary_append(dt, page, D, odd):
+    rng = np.random.default_rng(page * 100 + D)
+    n, hq, hkv, pages = 11, 6, 2, -(-20 // page)
+    q, k, v = (heads_of(rng, dt, (n,), h, D, "odd" if odd else "plain") for h in (hq, hkv, hkv))
+    kc, vc = rnd(rng, dt, pages, page, hkv, D), rnd(rng, dt, pages, page, hkv, D)
+    before = kc.clone(), vc.clone()
+    slots = rng.permutation(pages * page)[:n].astype(np.int32)
+    slots[3], slots[7] = -1, pages * page
+    table, pos = dbs.rotary_table(64, D // 2 * 2), torch.from_numpy(rng.integers(0, 64, n).astype(np.int32)).to(DEV)
+    qw, kw = rnd(rng, dt, D), rnd(rng, dt, D)
+    out = dbs.norm_rotary_append(q, k, v, qw, kw, table, pos, kc, vc, ints(slots), eps=1e-6)
+    qo, ko = dbs.norm_rotary(q, k, qw, kw, table, pos, eps=1e-6)
+    assert torch.equal(out, qo)
+    for got, base, new in ((kc, before[0], ko), (vc, before[1], v)):
+        ref = base.clone().flatten(0, 1)
+        for i, s in enumerate(slots):
+            if 0 <= s < pages * page:
+                ref[s] = new[i]
+        assert torch.equal(got.flatten(0, 1), ref)
+
+
+def test_norm_rotary_outside_the_table_and_what_is_not_finite():
+    rng = np.random.default_rng(8)
+    q, w, table = rnd(rng, "f32", 6, 2, 32), rnd(rng, "f32", 32), dbs.rotary_table(10, 16)
+    ok = dbs.norm_rotary(q, None, w, None, table, ints([0, 1, 2, 3, 4, 5]))[0]
+    out = dbs.norm_rotary(q, None, w, None, table, ints([0, 10, -1, 3, 4, 5]))[0]
+    assert torch.isnan(out[1:3, :, :16]).all() and torch.equal(out[1:3, :, 16:], ok[1:3, :, 16:])
+    assert torch.equal(out[[0, 3, 4, 5]], ok[[0, 3, 4, 5]])
+    q[2, 1, 5], q[4, 0, 31] = NAN, INF
+    out = dbs.norm_rotary(q, None, w, None, table, ints([0, 1, 2, 3, 4, 5]))[0]
+    assert torch.isnan(out[2, 1]).all() and torch.isnan(out[4, 0, 31])
+    rest = torch.ones(6, 2, dtype=torch.bool, device=DEV)
+    rest[2, 1] = rest[4, 0] = False
+    assert torch.equal(out[rest], ok[rest])
+    zero = dbs.norm_rotary(torch.zeros_like(q), None, w, None, table, ints([0, 1, 2, 3, 4, 5]))[0]
+    assert (zero == 0).all()
+    g = dbs.norm_rotary_gradient(ok, None, torch.zeros_like(q), None, w, None, table, ints([0, 1, 2, 3, 4, 5]))
+    assert torch.isfinite(g[0]).all() and (g[2] == 0).all()
+
+
+# ---- attention with a window and sinks ----
+
+
+def window_ref(q, k, v, kv, tl, window, sinks, scale, table=None, page=0):
+    """out, the sum of p |v|, and lse, in 64 bits."""
+    B, T, H, D = q.shape
+    G = H // k.shape[2]
+    o, mag, lse = np.zeros((B, T, H, D)), np.zeros((B, T, H, D)), np.full((B, T, H), -INF)
+    for b in range(B):
+        n, first = kv[b], kv[b] - tl[b]
+        if table is None:
+            kb, vb = k[b, :n], v[b, :n]
+        else:
+            at = np.clip(table[b], 0, k.shape[0] - 1)
+            kb, vb = k[at].reshape(-1, *k.shape[2:])[:n], v[at].reshape(-1, *v.shape[2:])[:n]
+        for t in range(tl[b]):
+            p = first + t
+            if p < 0:
+                continue
+            j = np.arange(p + 1)
+            j = j[(p - j < window) | (j < sinks)]
+            for h in range(H):
+                x = kb[j, h // G] @ q[b, t, h] * scale
+                top = x.max()
+                e = np.exp(x - top)
+                o[b, t, h], mag[b, t, h] = e @ vb[j, h // G] / e.sum(), e @ np.abs(vb[j, h // G]) / e.sum()
+                lse[b, t, h] = top + np.log(e.sum())
+    return o, mag, lse
+
+
+def window_inputs(rng, dt, B, T, hq, hkv, D, S, page, extra=2):
+    q = rnd(rng, dt, B, T, hq, D)
+    if not page:
+        return q, rnd(rng, dt, B, S, hkv, D), rnd(rng, dt, B, S, hkv, D), None
+    per = -(-S // page)
+    pages = B * per + extra
+    table = rng.permutation(pages)[:B * per].astype(np.int32).reshape(B, per)
+    return q, rnd(rng, dt, pages, page, hkv, D), rnd(rng, dt, pages, page, hkv, D), table
+
+
+def check_window(dt, q, k, v, table, kv, tl, window, sinks, scale=None, **kw):
+    out, lse = dbs.window_attention(q, k, v, ints(kv), window, sinks=sinks, q_lens=ints(tl), page_table=None if table is None else ints(table),
+                                    scale=scale, return_lse=True, **kw)
+    s = 1 / np.sqrt(q.shape[-1]) if scale is None else scale
+    ref, mag, rl = window_ref(f64(q), f64(k), f64(v), kv, tl, window, sinks, s, table)
+    close(out, ref, (U[dt] + 3e-4) * mag + U[dt] * np.abs(ref) + ETA[dt])
+    close(lse, rl, 4e-4)
+    again = dbs.window_attention(q, k, v, ints(kv), window, sinks=sinks, q_lens=ints(tl), page_table=None if table is None else ints(table),
+                                 scale=scale)
+    assert torch.equal(again, out)
+    return out, lse
+
+
+WINDOW_CASES = [
+    # B, T, hq, hkv, D, S, page, window, sinks
+    (1, 1, 1, 1, 64, 1, 0, 1, 0), (1, 1, 4, 1, 128, 300, 0, 64, 4), (2, 1, 8, 2, 128, 513, 16, 100, 0), (3, 1, 5, 1, 96, 200, 24, 64, 70),
+    (2, 1, 16, 1, 64, 400, 8, 399, 3), (1, 1, 32, 2, 256, 150, 16, 33, 1), (2, 2, 8, 1, 128, 260, 16, 130, 5), (2, 3, 10, 2, 80, 77, 16, 20, 2),
+    (3, 4, 4, 4, 64, 300, 64, 128, 16), (2, 5, 12, 2, 128, 700, 16, 257, 4), (1, 17, 2, 2, 128, 333, 16, 50, 0), (2, 33, 6, 1, 128, 200, 32, 40, 9),
+    (1, 64, 8, 1, 64, 500, 16, 200, 4), (2, 130, 4, 2, 128, 130, 16, 1000, 0), (1, 300, 1, 1, 128, 300, 0, 64, 4), (1, 257, 3, 1, 64, 400, 128, 128, 130),
+    (2, 100, 7, 1, 128, 150, 16, 31, 1), (1, 200, 5, 1, 256, 200, 16, 90, 4), (2, 65, 2, 1, 256, 300, 0, 100, 20), (1, 140, 4, 4, 40, 140, 8, 17, 2),
+    (1, 9, 130, 1, 64, 40, 16, 16, 1), (2, 70, 4, 2, 128, 100, 5, 33, 3), (1, 50, 4, 2, 64, 100, 1, 33, 3), (1, 6, 3, 1, 33, 60, 16, 20, 2),
+    (2, 40, 2, 2, 7, 60, 3, 20, 2), (1, 600, 2, 1, 128, 700, 256, 1, 0), (1, 520, 8, 2, 128, 520, 16, 128, 0)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("B,T,hq,hkv,D,S,page,window,sinks", WINDOW_CASES)
+def test_window_attention(dt, B, T, hq, hkv, D, S, page, window, sinks):
+    rng = np.random.default_rng(B * 7 + T * 31 + hq + D + S)
+    q, k, v, table = window_inputs(rng, dt, B, T, hq, hkv, D, S, page)
+    check_window(dt, q, k, v, table, [S] * B, [min(T, S)] * B, window, sinks)
+    tl = [int(rng.integers(0, T + 1)) for _ in range(B)]
+    kv = [int(rng.integers(0, S + 1)) for _ in range(B)]
+    check_window(dt, q, k, v, table, kv, tl, window, sinks, scale=0.2)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,hq,page", [(1, 4, 16), (3, 2, 0), (40, 4, 16), (200, 2, 16), (150, 2, 5)])
+def test_window_what_is_not_seen_takes_no_part(dt, T, hq, page):
+    """NaN and infinities before the windows, behind the entries, in other tokens' places: rows that do not see them."""
+    rng = np.random.default_rng(T + hq)
+    B, D, S, window, sinks = 2, 128, 420, 60, 3
+    q, k, v, table = window_inputs(rng, dt, B, T, hq, 1, D, S, page)
+    kv, tl = [390, 300], [T, T - T // 3]
+    ref = check_window(dt, q, k, v, table, kv, tl, window, sinks)
+
+    def spoil(c, b, j, value):
+        if table is None:
+            c[b, j] = value
+        else:
+            c[int(table[b, j // page]), j % page] = value
+
+    k2, v2 = k.clone(), v.clone()
+    for b in range(B):
+        lo = max(0, kv[b] - tl[b] - window + 1)
+        for i, j in enumerate([*range(sinks, lo), *range(kv[b], S)]):          # seen by no token
+            for c in (k2, v2):
+                spoil(c, b, j, (NAN, INF, -INF)[(i + b) % 3])
+    out, lse = dbs.window_attention(q, k2, v2, ints(kv), window, sinks=sinks, q_lens=ints(tl), page_table=None if table is None else ints(table),
+                                    return_lse=True)
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    # the entry of one token (of sequence 0) is spoiled: rows before it, and rows whose window is past it, stay
+    t = T // 2
+    j = kv[0] - tl[0] + t
+    for value in (NAN, INF):
+        k3, v3 = k.clone(), v.clone()
+        spoil(v3, 0, j, value)
+        got = dbs.window_attention(q, k3, v3, ints(kv), window, sinks=sinks, q_lens=ints(tl), page_table=None if table is None else ints(table))
+        sees = torch.arange(T, device=DEV)
+        sees = (sees >= t) & (sees < t + window)
+        clean = torch.ones((B, T), dtype=torch.bool, device=DEV)
+        clean[0] = ~sees
+        o, mag, _ = window_ref(f64(q), f64(k), f64(v), kv, tl, window, sinks, D**-0.5, table)
+        at = clean.cpu().numpy()
+        close(got[clean], o[at], (U[dt] + 3e-4) * mag[at] + U[dt] * np.abs(o[at]))
+        hit = got[0][sees]
+        assert torch.isnan(hit).all() if value != value else (torch.isinf(hit) & (hit > 0)).all()
+        spoil(k3, 0, j, NAN)
+        got = dbs.window_attention(q, k3, v3, ints(kv), window, sinks=sinks, q_lens=ints(tl), page_table=None if table is None else ints(table))
+        close(got[clean], o[at], (U[dt] + 3e-4) * mag[at] + U[dt] * np.abs(o[at]))
+        assert torch.isnan(got[0][sees]).all()
+
+
+@pytest.mark.parametrize("T", [1, 5, 60, 300])
+def test_window_layouts_and_given_outputs(T):
+    """Strides other than the usual, an output among others, rows behind the last token, scales of any sign."""
+    rng = np.random.default_rng(T)
+    B, hq, hkv, D, S, page = 2, 4, 2, 64, 330, 16
+    q, k, v, table = window_inputs(rng, "bf16", B, T, hq, hkv, D, S, page)
+    kv, tl = [S, 321], [T, (T + 1) // 2]
+    ref = check_window("bf16", q, k, v, table, kv, tl, 50, 4)[0]
+    q2 = q.transpose(1, 2).contiguous().transpose(1, 2)
+    both = torch.empty((k.shape[0], hkv, 2, page, D), dtype=q.dtype, device=DEV)          # heads before entries, K and V side by side
+    both[:, :, 0], both[:, :, 1] = k.transpose(1, 2), v.transpose(1, 2)
+    k2, v2 = both[:, :, 0].transpose(1, 2), both[:, :, 1].transpose(1, 2)
+    wide = torch.full((B, T, hq, D + 8), 7.0, dtype=q.dtype, device=DEV)
+    out = dbs.window_attention(q2, k2, v2, ints(kv), 50, sinks=4, q_lens=ints(tl), page_table=ints(table), out=wide[..., :D])
+    assert torch.equal(out, ref) and (wide[..., D:] == 7.0).all() and (out[1, tl[1]:] == 0).all()
+    odd = torch.full((B, T, hq, D + 3), 7.0, dtype=q.dtype, device=DEV)
+    out = dbs.window_attention(q2, k2, v2, ints(kv), 50, sinks=4, q_lens=ints(tl), page_table=ints(table), out=odd[..., 1:D + 1])
+    assert torch.equal(out, ref) and (odd[..., D + 1:] == 7.0).all() and (odd[..., 0] == 7.0).all()
+    check_window("bf16", q, k, v, table, kv, tl, 50, 4, scale=-0.1)
+    check_window("bf16", q, k, v, table, kv, tl, 50, 4, scale=0.0)
+    # the page table's other numbers are clamped, and those that no token needs are not looked at
+    t2 = table.copy()
+    lo = min(kv[0] - T, kv[1] - tl[1]) - 50
+    t2[:, 1:max(1, lo // page)] = -5
+    out = dbs.window_attention(q, k, v, ints(kv), 50, sinks=4, q_lens=ints(tl), page_table=ints(t2))
+    assert torch.equal(out, ref)
+
+
+def test_window_of_everything_is_plain_attention():
+    rng = np.random.default_rng(12)
+    q, k, v, table = window_inputs(rng, "f16", 2, 24, 8, 2, 64, 300, 16)
+    a = dbs.window_attention(q, k, v, ints([300, 211]), 1 << 40, sinks=1 << 40, page_table=ints(table))
+    b = dbs.tree_attention(q, k, v, ints([300, 211]), page_table=ints(table))
+    o, mag, _ = window_ref(f64(q), f64(k), f64(v), [300, 211], [24, 24], 1 << 40, 0, 0.125, table)
+    for got in (a, b):
+        close(got, o, (U["f16"] + 3e-4) * mag + U["f16"] * np.abs(o))
+
+
+# ---- pages ----
+
+
+class Pool:
+    """The page table by the book, one sequence after another."""
+
+    def __init__(self, batch, per, pages, page):
+        self.table, self.kv, self.refs, self.page = np.full((batch, per), -7, np.int32), np.zeros(batch, np.int32), np.zeros(pages, np.int32), page
+
+    def device(self):
+        return [ints(self.table), ints(self.kv), ints(self.refs)]
+
+    def resize(self, lens, columns=0):
+        B, per = self.table.shape
+        page, old = self.page, self.kv.copy()
+        status, slots = np.zeros(B, np.int32), np.full((B, columns), -1, np.int32)
+        for b in range(B):
+            if 0 <= lens[b] < self.kv[b]:
+                for c in range(-(-lens[b] // page), -(-self.kv[b] // page)):
+                    self.refs[self.table[b, c]] -= 1
+                self.kv[b] = lens[b]
+        free, asked, cut = np.flatnonzero(self.refs == 0), 0, self.refs.copy()
+        for b in range(B):
+            n, had = lens[b], self.kv[b]
+            if n <= had:
+                continue
+            if n > per * page:
+                status[b] = 3
+                continue
+            if had % page and cut[self.table[b, had // page]] > 1:
+                status[b] = 2
+                continue
+            new = range(-(-had // page), -(-n // page))
+            asked += len(new)
+            if len(new) and asked > len(free):
+                status[b] = 1
+                continue
+            for c, p in zip(new, free[asked - len(new):asked]):
+                self.table[b, c], self.refs[p] = p, 1
+            self.kv[b] = n
+            for i in range(min(columns, n - old[b])):
+                j = old[b] + i
+                slots[b, i] = self.table[b, j // page] * page + j % page
+        return status, slots
+
+    def fork(self, parents, children, *caches):
+        lens, taken, asked, status = self.kv.copy(), set(), 0, []
+        free, page = np.flatnonzero(self.refs == 0), self.page
+        for p, c in zip(parents, children):
+            if not (0 <= p < len(lens) and 0 <= c < len(lens)) or lens[c] > 0 or c in taken:
+                status.append(2)
+                continue
+            taken.add(c)
+            n, rest = int(lens[p]) // page, int(lens[p]) % page
+            if rest:
+                asked += 1
+                if asked > len(free):
+                    status.append(1)
+                    continue
+            for i in range(n):
+                self.table[c, i] = self.table[p, i]
+                self.refs[self.table[p, i]] += 1
+            if rest:
+                f = int(free[asked - 1])
+                self.table[c, n], self.refs[f] = f, 1
+                for x in caches:
+                    x[:, f, :rest] = x[:, int(self.table[p, n]), :rest]
+            self.kv[c] = lens[p]
+            status.append(0)
+        return np.array(status, np.int32)
+
+    def same(self, state):
+        for got, want in zip(state, (self.table, self.kv, self.refs)):
+            assert np.array_equal(got.cpu().numpy(), want)
+
+    def consistent(self):
+        count = np.zeros(len(self.refs), np.int32)
+        for b, n in enumerate(self.kv):
+            for c in range(-(-int(n) // self.page)):
+                count[self.table[b, c]] += 1
+        assert np.array_equal(count, self.refs)
+
+
+@pytest.mark.parametrize("batch,per,pages,page", [(1, 4, 3, 1), (5, 9, 30, 16), (40, 12, 200, 7), (1500, 3, 3000, 4), (30, 64, 70000, 16), (6, 3, 4, 24)])
+def test_cache_resize_walk(batch, per, pages, page):
+    """Random growth, cuts and releases, short of pages now and then."""
+    rng = np.random.default_rng(batch + pages)
+    pool = Pool(batch, per, pages, page)
+    if pages > 60000:                                                      # pages far back: the first are taken by others
+        pool.refs[:50000] = 9
+    state = pool.device()
+    for turn in range(10):
+        kind = rng.integers(0, 5, batch)
+        lens = np.where(kind == 0, -1, np.where(kind == 1, 0, np.where(kind == 2, pool.kv + rng.integers(0, page + 2, batch),
+                                                                       rng.integers(0, per * page + 2, batch)))).astype(np.int32)
+        columns = [0, 1, 5, 300][turn % 4]
+        status, slots = dbs.cache_resize(*state, ints(lens), page, columns=columns)
+        want, where = pool.resize(lens, columns)
+        assert np.array_equal(status.cpu().numpy(), want) and np.array_equal(slots.cpu().numpy(), where)
+        pool.same(state)
+        if pages <= 60000:
+            pool.consistent()
+    assert dbs.cache_resize(*state, ints([0] * batch), page)[1] is None
+    pool.resize([0] * batch)
+    pool.same(state)
+
+
+CACHES = [(1, 2, 8, "bf16", 4), (3, 2, 64, "f16", 5), (2, 1, 33, "bf16", 5), (2, 3, 5, "u8", 5), (2, 2, 40, "f32", 5)]
+
+
+def make_caches(rng, layers, heads, D, dt, dims, pages, page):
+    shape = (layers, pages, page, heads, D)
+    if dt == "u8":
+        k, v = (torch.from_numpy(rng.integers(0, 256, shape, dtype=np.uint8)).to(DEV) for _ in range(2))
+    else:
+        k, v = rnd(rng, dt, *shape), rnd(rng, dt, *shape)
+    return (k[0], v[0]) if dims == 4 else (k, v)
+
+
+def plain(c):
+    """[layers, pages, page, heads, D] on the host."""
+    return (c if c.dim() == 5 else c[None]).cpu().clone()
+
+
+@pytest.mark.parametrize("layers,heads,D,dt,dims", CACHES)
+@pytest.mark.parametrize("page,pages", [(1, 40), (16, 40), (24, 40), (5, 25)])
+def test_cache_fork(layers, heads, D, dt, dims, page, pages):
+    rng = np.random.default_rng(layers + D + page)
+    pool = Pool(12, 9, pages, page)
+    pool.resize(np.array([3 * page, 2 * page + page // 2, 1, 0, 5 * page + max(page - 1, 0), 0, 0, 0, 0, 0, 0, 0]))
+    k, v = make_caches(rng, layers, heads, D, dt, dims, pages, page)
+    state, hk, hv = pool.device(), plain(k), plain(v)
+    for parents, children in (([1], [5]), ([0, 1, 1, 4, 2, 3], [6, 7, 8, 9, 10, 11]), ([1, 4], [1, 3])):
+        status = dbs.cache_fork(k, v, *state, ints(parents), ints(children))
+        assert np.array_equal(status.cpu().numpy(), pool.fork(parents, children, hk, hv))
+        pool.same(state)
+        pool.consistent()
+        assert torch.equal(plain(k), hk) and torch.equal(plain(v), hv)
+    # the same child twice, numbers outside, a child of an empty parent
+    lens = np.full(12, -1, np.int32)
+    lens[[5, 6, 7, 8]] = 0
+    dbs.cache_resize(*state, ints(lens), page)
+    pool.resize(lens)
+    for parents, children in (([1, 4, 0], [5, 5, 5]), ([-1, 12, 0, 1, 2, 3], [6, 6, -1, 12, 2**31 - 1, 7]), ([6, 1, 6], [6, 8, 7])):
+        status = dbs.cache_fork(k, v, *state, ints(parents), ints(children))
+        assert np.array_equal(status.cpu().numpy(), pool.fork(parents, children, hk, hv))
+        pool.same(state)
+        pool.consistent()
+        assert torch.equal(plain(k), hk) and torch.equal(plain(v), hv)
+    assert dbs.cache_fork(k, v, *state, ints([]), ints([])).shape == (0,)
+    pool.same(state)
+
+
+def test_cache_fork_short_of_pages_and_growth_into_a_shared_page():
+    pool = Pool(6, 4, 5, 8)
+    pool.resize([8, 13, 5, 0, 0, 0])
+    rng = np.random.default_rng(2)
+    k, v = make_caches(rng, 2, 1, 16, "f16", 5, 5, 8)
+    state, hk, hv = pool.device(), plain(k), plain(v)
+    status = dbs.cache_fork(k, v, *state, ints([1, 2, 0]), ints([3, 4, 5]))          # one free page: for the first of the two
+    want = pool.fork([1, 2, 0], [3, 4, 5], hk, hv)
+    assert want.tolist() == [0, 1, 0] and np.array_equal(status.cpu().numpy(), want)
+    pool.same(state)
+    assert torch.equal(plain(k), hk) and torch.equal(plain(v), hv)
+    # cut inside a shared full page, then grown: refused; once the other has gone it may grow
+    for lens, want in (([4, -1, -1, -1, -1, -1], [0] * 6), ([6, -1, -1, -1, -1, -1], [2, 0, 0, 0, 0, 0]), ([6, -1, -1, -1, -1, 0], [0] * 6)):
+        status, slots = dbs.cache_resize(*state, ints(lens), 8, columns=3)
+        s, w = pool.resize(lens, 3)
+        assert s.tolist() == want and np.array_equal(status.cpu().numpy(), s) and np.array_equal(slots.cpu().numpy(), w)
+        pool.same(state)
+
+
+@pytest.mark.parametrize("layers,heads,D,dt,dims", CACHES)
+@pytest.mark.parametrize("T,page", [(1, 16), (6, 16), (40, 5), (700, 24), (3, 0)])
+def test_cache_compact(layers, heads, D, dt, dims, T, page):
+    rng = np.random.default_rng(T + D + page)
+    B, S = 4, T + 50
+    per = -(-S // page) if page else 1
+    pages, size = (B * per + 1, page) if page else (B, S)
+    k, v = make_caches(rng, layers, heads, D, dt, dims, pages, size)
+    table = rng.permutation(pages)[:B * per].astype(np.int32).reshape(B, per) if page else np.arange(B, dtype=np.int32)[:, None]
+    kv, tree = [S, S - 7, min(20, T), 0], [T, max(T // 2, 1), T, T]
+    acc = np.full((B, T), -1, np.int32)
+    for b in range(B):
+        take = np.flatnonzero(rng.random(T) < [0.5, 0.9, 0.3, 1.0][b])
+        acc[b, :len(take)] = take
+    if T == 6:
+        acc[0], acc[1], acc[2] = [0, 2, 2, 3, 4, 5], [1, 0, 2, 3, 4, 5], [0, 3, 6, 7, 8, 9]      # ends where it does not ascend, or leaves the tree
+    lens = np.array([T if T == 40 else min(int((acc[b] >= 0).sum()), [T, T, 4, T][b]) for b in range(B)], np.int32)
+    hk, hv, want = plain(k), plain(v), []
+    for b in range(B):
+        tr = min(tree[b], kv[b])
+        first, n = kv[b] - tr, 0
+        for i in range(lens[b]):
+            a = acc[b, i]
+            if not 0 <= a < tr or (i and a <= acc[b, i - 1]):
+                break
+            for x in (hk, hv):
+                x[:, table[b, (first + i) // size], (first + i) % size] = x[:, table[b, (first + a) // size], (first + a) % size]
+            n += 1
+        want.append(first + n)
+    lens_in = ints(kv)
+    got = dbs.cache_compact(k, v, lens_in, ints(tree), ints(acc), ints(lens) if T != 40 else None, page_table=ints(table) if page else None)
+    assert got.tolist() == want and lens_in.tolist() == kv
+    assert torch.equal(plain(k), hk) and torch.equal(plain(v), hv)
+
+
+def test_caches_of_other_layouts():
+    """Heads before entries, layers between: forked and compacted as the plain layout is."""
+    rng = np.random.default_rng(9)
+    layers, pages, page, heads, D = 3, 20, 8, 2, 24
+    base = [make_caches(rng, layers, heads, D, "bf16", 5, pages, page) for _ in range(1)][0]
+    other = [torch.full((pages, heads, layers, page, D + 8), 3.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    views = [o[..., :D].permute(2, 0, 3, 1, 4) for o in other]
+    for a, b in zip(views, base):
+        a.copy_(b)
+    pools = [Pool(5, 4, pages, page) for _ in range(2)]
+    states = []
+    for p, c in zip(pools, (base, views)):
+        p.resize([11, 30, 5, 0, 0])
+        states.append(p.device())
+        dbs.cache_fork(*c, *states[-1], ints([1, 0]), ints([3, 4]))
+        dbs.cache_compact(*c, states[-1][1], ints([3, 6, 2, 6, 3]), ints([[0, 2, -1], [1, 3, 5], [1, -1, -1], [0, 1, 4], [1, 2, -1]]), page_table=states[-1][0])
+    assert all(torch.equal(a, b) for a, b in zip(*states)) and all(torch.equal(a, b) for a, b in zip(base, views))
+    assert all((o[..., D:] == 3.0).all() for o in other)
+
+
+# ---- a run of them together ----
+
+
+def test_a_step_of_drafted_tokens_forked_and_cut_back():
+    """Grow, append, attend, keep what was accepted, fork and go on: against a dense cache of each sequence's own."""
+    rng = np.random.default_rng(21)
+    B, hq, hkv, D, page, pages, window, sinks, dt = 4, 4, 2, 64, 8, 64, 20, 2, "bf16"
+    state = [torch.full((B, 12), -1, dtype=torch.int32, device=DEV), ints([0] * B), ints([0] * pages)]
+    kc, vc = (torch.full((pages, page, hkv, D), NAN, dtype=DT[dt], device=DEV) for _ in range(2))
+    table, w = dbs.rotary_table(128, D), rnd(rng, "f32", D)
+    kept = {b: [] for b in range(B)}                                       # (k, v) of every entry
+    live = [0, 1]
+
+    def step(counts, accepted):
+        T = max(counts)
+        lens = state[1].cpu().numpy()
+        want = np.array([lens[b] + counts[b] if b in live else -1 for b in range(B)], np.int32)
+        status, slots = dbs.cache_resize(*state, ints(want), page, columns=T)
+        assert (status == 0).all()
+        q, k, v = rnd(rng, dt, B, T, hq, D), rnd(rng, dt, B, T, hkv, D), rnd(rng, dt, B, T, hkv, D)
+        pos = ints(lens[:, None] + np.arange(T, dtype=np.int32))
+        qt = dbs.norm_rotary_append(q, k, v, w, w, table, pos, kc, vc, slots)
+        kt = dbs.norm_rotary(k, None, w, None, table, pos)[0]
+        tl = np.array([counts[b] if b in live else 0 for b in range(B)], np.int32)
+        out = dbs.window_attention(qt, kc, vc, state[1], window, sinks=sinks, q_lens=ints(tl), page_table=state[0])
+        for b in live:
+            kept[b] += [(f64(kt[b, i]), f64(v[b, i])) for i in range(counts[b])]
+            dense = [np.stack([e[i] for e in kept[b]])[None] for i in range(2)]
+            ref, mag, _ = window_ref(f64(qt[b:b + 1]), *dense, [len(kept[b])], [counts[b]], window, sinks, D**-0.5)
+            close(out[b], ref[0], (U[dt] + 3e-4) * mag[0] + U[dt] * np.abs(ref[0]))
+        acc = np.full((B, T), -1, np.int32)
+        for b in live:
+            acc[b, :len(accepted[b])] = accepted[b]
+            first = len(kept[b]) - counts[b]
+            kept[b] = kept[b][:first] + [kept[b][first + a] for a in accepted[b]]
+        new = dbs.cache_compact(kc, vc, state[1], ints(tl), ints(acc), page_table=state[0])
+        assert (dbs.cache_resize(*state, new, page)[0] == 0).all()
+        assert state[1].tolist() == [len(kept[b]) for b in range(B)]
+
+    step([37, 21, 0, 0], {0: range(37), 1: range(21)})
+    step([6, 4, 0, 0], {0: [0, 2, 5], 1: [0]})
+    assert dbs.cache_fork(kc, vc, *state, ints([0, 1]), ints([2, 3])).tolist() == [0, 0]
+    kept[2], kept[3], live = list(kept[0]), list(kept[1]), [0, 1, 2, 3]
+    step([5, 9, 7, 3], {0: [0, 1, 4], 1: [0, 3, 8], 2: [0, 6], 3: [0, 1, 2]})
+    step([1, 1, 1, 1], {b: [0] for b in range(4)})
+    assert dbs.cache_resize(*state, ints([0] * B), page)[0].tolist() == [0] * B and (state[2] == 0).all() and dbs.operators_check() == 0
+
+
+def test_captured_and_replayed_on_another_stream():
+    """One step captured in a graph and replayed gives what calls on a stream give."""
+    rng = np.random.default_rng(31)
+    B, T, hq, hkv, D, page = 3, 2, 8, 2, 128, 16
+    q, k, v = rnd(rng, "f16", B, T, hq, D), rnd(rng, "f16", B, T, hkv, D), rnd(rng, "f16", B, T, hkv, D)
+    w, table, pos = rnd(rng, "f16", D), dbs.rotary_table(200, D), ints(np.array([[50, 51], [9, 10], [120, 121]]))
+    pool = Pool(B + 1, 10, 40, page)
+    pool.resize([50, 9, 120, 0])
+    kc0, vc0 = make_caches(rng, 1, hkv, D, "f16", 4, 40, page)
+
+    def run(state, kc, vc):
+        grown, slots = dbs.cache_resize(*state, ints_grow, page, columns=T)
+        qt = dbs.norm_rotary_append(q, k, v, w, w, table, pos, kc, vc, slots[:B].contiguous())
+        out = dbs.window_attention(qt, kc, vc, state[1][:B], 40, sinks=4, page_table=state[0][:B])
+        forked = dbs.cache_fork(kc, vc, *state, one, three)
+        lens = dbs.cache_compact(kc, vc, state[1], trees, accepted, page_table=state[0])
+        cut, _ = dbs.cache_resize(*state, lens, page)
+        grads = dbs.norm_rotary_gradient(qt, k, q, k, w, w, table, pos)
+        return [grown, slots, qt, out, forked, lens, cut, *grads]
+
+    ints_grow, one, three = ints([52, 11, 122, -1]), ints([1]), ints([3])
+    trees, accepted = ints([2, 2, 2, 0]), ints([[1, -1], [0, 1], [0, -1], [-1, -1]])
+    state = pool.device()
+    kc, vc = kc0.clone(), vc0.clone()
+    want = [t.clone() for t in (*run(state, kc, vc), *state, kc, vc)]
+    side = torch.cuda.Stream()
+    state2, kc2, vc2 = pool.device(), kc0.clone(), vc0.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = run(state2, kc2, vc2)
+    for _ in range(3):
+        for t, f in zip((*state2, kc2, vc2), (*pool.device(), kc0, vc0)):
+            t.copy_(f)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((*got, *state2, kc2, vc2), want):
+            assert torch.equal(a, b)
