@@ -212,5 +212,5 @@ def test_argument_structs_have_the_header_s_size():
     sizes = {"dbs_norm_heads": struct.calcsize("@" + _lib.NORM_HEADS), "dbs_norm_gradient_heads": struct.calcsize("@" + _lib.NORM_GRADIENT_HEADS),
              "dbs_window_args": _lib.WINDOW_ARGS.size, "dbs_page_state": _lib.PAGE_STATE.size, "dbs_cache_data": _lib.CACHE_DATA.size}
     src = '#include <stddef.h>\n#include "include/dbspmspv.h"\n' + "".join(f'_Static_assert(sizeof({k}) == {v}, "size");\n' for k, v in sizes.items())
-    src += '_Static_assert(offsetof(dbs_window_args, scale) == 192 && offsetof(dbs_cache_data, k_layer) == 48, "places");\n'
+    src += '_Static_assert(offsetof(dbs_window_args, scale) == 200 && offsetof(dbs_cache_data, k_layer) == 48, "places");\n'
     assert subprocess.run(["gcc", "-x", "c", "-fsyntax-only", "-I", root, "-"], input=src.encode(), cwd=root).returncode == 0
