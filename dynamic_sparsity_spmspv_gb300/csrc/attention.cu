@@ -1783,8 +1783,12 @@ extern "C" {
 
 dbs_status dbs_operators_check(void *stream)
 {
-    const dbs_status here = waits_since((cudaStream_t)stream), w4 = w4_waits_since((cudaStream_t)stream);
-    return here == DBS_ERR_CUDA ? here : w4 != DBS_OK ? w4 : here;
+    // (each is asked, so that each forgets)
+    const dbs_status all[3] = {waits_since((cudaStream_t)stream), w4_waits_since((cudaStream_t)stream), window_waits_since((cudaStream_t)stream)};
+    dbs_status worst = DBS_OK;
+    for (const dbs_status s : all)
+        if (s != DBS_OK && worst != DBS_ERR_CUDA) worst = s;
+    return worst;
 }
 
 dbs_status dbs_debug_operator_waits(int64_t limit_ns, int32_t block)

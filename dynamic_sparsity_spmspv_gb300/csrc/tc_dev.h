@@ -1,4 +1,4 @@
-// The fifth-generation tensor cores (tcgen05) for attention.cu and w4.cu: matrix
+// The fifth-generation tensor cores (tcgen05) for attention.cu, window.cu and w4.cu: matrix
 // instructions of 16-bit operands, tensor memory, descriptors.
 #pragma once
 #include "ops_dev.h"
@@ -21,6 +21,7 @@ static dbs_status waits_since(cudaStream_t s)
     return was ? DBS_ERR_TIMEOUT : DBS_OK;
 }
 dbs_status w4_waits_since(cudaStream_t s);
+dbs_status window_waits_since(cudaStream_t s);
 
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
 {

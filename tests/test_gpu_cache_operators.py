@@ -377,6 +377,48 @@ def test_window_layouts_and_given_outputs(T):
     assert torch.equal(out, ref)
 
 
+class waits_run_out:
+    """Waits of that block of each kernel (-2: of all) run out, after a millisecond."""
+
+    def __init__(self, block):
+        self.block = block
+
+    def __enter__(self):
+        assert dbs._lib.load().dbs_debug_operator_waits(1_000_000, self.block) == 0
+
+    def __exit__(self, *_):
+        torch.cuda.synchronize()
+        assert dbs._lib.load().dbs_debug_operator_waits(2_000_000_000, -1) == 0
+
+
+@pytest.mark.parametrize("B,T,hq,hk,D,S,window", [(2, 1, 8, 2, 128, 900, 400), (40, 1, 4, 4, 64, 200, 100), (1, 3, 4, 2, 256, 300, 200),
+                                                  (2, 90, 8, 2, 128, 700, 150), (1, 300, 4, 1, 64, 300, 100), (2, 100, 2, 2, 256, 200, 90),
+                                                  (3, 1500, 2, 2, 128, 1500, 200)])
+def test_window_that_gives_up_leaves_nan(B, T, hq, hk, D, S, window):
+    """All rows that a block whose wait ran out had in hand or still ahead are NaN, the others as ever, and so is the
+    next call."""
+    rng = np.random.default_rng(B + T)
+    q, k, v, table = window_inputs(rng, "f16", B, T, hq, hk, D, S, 16)
+    dbs.operators_check()
+
+    def call():
+        return dbs.window_attention(q, k, v, ints([S] * B), window, sinks=3, page_table=ints(table), out=torch.full_like(q, 5.0), return_lse=True)
+
+    clean, lse = call()
+    assert dbs.operators_check() == 0
+    for block in (-2, 0, 1):
+        with waits_run_out(block):
+            got, gl = call()
+        assert dbs.operators_check() == 4 and dbs.operators_check() == 0
+        nan = torch.isnan(got)
+        assert (nan.all(3) == nan.any(3)).all() and (nan.any(3) == torch.isnan(gl)).all()
+        nan = nan.any(3)
+        assert nan.all() if block == -2 else nan.any()
+        assert torch.equal(got[~nan], clean[~nan]) and torch.equal(gl[~nan], lse[~nan])
+        again, al = call()
+        assert torch.equal(again, clean) and torch.equal(al, lse)
+
+
 def test_window_of_everything_is_plain_attention():
     rng = np.random.default_rng(12)
     q, k, v, table = window_inputs(rng, "f16", 2, 24, 8, 2, 64, 300, 16)
