@@ -53,7 +53,7 @@ ATTENTION_ARGS = struct.Struct("@4i2qP3q2P6q2qP2q3PfP3q2Pq")
 LOGITS_ARGS = struct.Struct("@PiqPiq2qP2q2P3P2P2qPq")
 NORM_HEADS = ROTARY_HEADS + "Pi4x"
 NORM_GRADIENT_HEADS = "3P9q2i2P"
-WINDOW_ARGS = struct.Struct("@4i2qP3q2P6q2qP2q2P2qfP3qP")
+WINDOW_ARGS = struct.Struct("@4i2qP3q2P6q2qP2q2P2qfP3q2Pq")
 PAGE_STATE = struct.Struct("@P3q2P2q")
 CACHE_DATA = struct.Struct("@2P3qi8q")
 
@@ -91,6 +91,7 @@ PROTOTYPES = {
     "dbs_norm_rotary": (I32, [P, I32, I32, I64, I64, I32, I32, ctypes.c_float, P, I64, P, P, I64, I64, I32, P]),
     "dbs_norm_rotary_gradient_scratch": (I32, [I32, I32, P]),
     "dbs_norm_rotary_gradient": (I32, [P, I32, I32, I64, I64, I32, I32, ctypes.c_float, P, I64, P, I32, P, I64, P]),
+    "dbs_window_attention_scratch": (I32, [P, P]),
     "dbs_window_attention": (I32, [P, P]),
     "dbs_cache_resize_scratch": (I32, [P, P]),
     "dbs_cache_resize": (I32, [P, P, P, P, I64, P, I64, P]),

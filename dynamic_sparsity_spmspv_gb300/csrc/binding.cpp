@@ -729,7 +729,7 @@ PyObject *window_attention(PyObject *, PyObject *const *args, Py_ssize_t nargs, 
         if (A.window < 1 || A.sinks < 0) bad(c.fn, "window has to be at least 1, sinks at least 0");
         A.scale = (float)real(a.v[8], 1.0 / std::sqrt((double)Q.d));
         c.on(a.v[11]);
-        at::Tensor out, lse;
+        at::Tensor out, lse, scratch;
         if (given) {
             out = *given;
             if (out.sizes() != q.sizes()) bad(c.fn, "out has to have q's shape");
@@ -742,6 +742,11 @@ PyObject *window_attention(PyObject *, PyObject *const *args, Py_ssize_t nargs, 
         if (want_lse) {
             lse = c.empty({Q.b, Q.n, Q.h}, at::kFloat);
             A.lse = lse.data_ptr<float>();
+        }
+        check(c.fn, dbs_window_attention_scratch(&A, &A.scratch_bytes));
+        if (A.scratch_bytes > 0) {
+            scratch = c.empty({A.scratch_bytes}, at::kByte);
+            A.scratch = scratch.data_ptr();
         }
         check(c.fn, dbs_window_attention(&A, c.stream));
         if (given) written(out);

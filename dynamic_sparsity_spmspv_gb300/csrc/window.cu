@@ -13,7 +13,7 @@ namespace {
 struct Win {
     dbs_window_args a;
     float scale_log2;          // scale * log2(e): probabilities are powers of two
-    int window, sinks;         // (at most 2^31 - 1)
+    int window, sinks;         // (at most 2^31 - 1024)
     int group;                 // query heads of a kv head
     bool wide_out;             // heads of out start on 16-byte boundaries
     Waits waits;
@@ -587,12 +587,569 @@ __global__ void __launch_bounds__(FEW_NT) k_window_few(Win A, int groups, int sp
     if (threadIdx.x == 0 && stop) ran_out = 1;
 }
 
+// ---- many rows: tcgen05 ----
+//
+// A unit is TILES tiles of rows of one kv head, each of as many tokens as fill 128 rows
+// with their heads; its entries come in tiles of KEYS, once for all its row tiles.  S = Q K^T and
+// O += P V have both accumulators in tensor memory (a row per lane), Q, K and V lie in
+// shared memory in the 128-byte swizzle (V as it lies, its entries as the contraction's dimension), and
+// P, rounded to the caches' type, is written over S, so that the second product reads only V from shared
+// memory.  Warps have roles: four for each row tile do the softmax, a thread a row; one fetches Q and
+// K, one V, one issues the products, one clears what no row of the unit sees in V.  While one
+// row tile's softmax runs, the products of the other do.
+//
+// A row tile skips the tiles that none of its rows sees.  Blocks walk over the units, long ones
+// first; of few units `split` blocks take a part each, and k_window_join joins their outputs.
+//
+// Every wait on a barrier has a limit; a block whose wait runs out stops, leaves NaN in
+// the rows of all units that it had not finished, and says so.
+
+template <int DP, int TILES> struct Many {
+    static constexpr int KEYS = DP == 256 ? 64 : 128;
+    static constexpr int STAGES = DP == 64 ? 3 : 2;                       // of K, and of V
+    static constexpr int SUBQ = 128 * 128, SUBK = KEYS * 128;             // 64 columns of a tile, in bytes
+    static constexpr int Q = DP / 64 * SUBQ, KV = DP / 64 * SUBK;
+    static constexpr int HELP = 4 * TILES, NT = 32 * (HELP + 4);          // first of the warps that fetch, issue and clear
+    // registers of a thread at launch (TILES = 2), and once the helping warps have left some to the softmax's
+    static constexpr int REGS = 168, FEW = 88, MANY = (3 * REGS - FEW) / 2;
+    static constexpr int S_COL = 0, O_COL = TILES * KEYS;
+    static constexpr int SMEM = TILES * Q + STAGES * 2 * KV + 1024;
+    static_assert(O_COL + TILES * DP <= 512, "tensor memory");
+};
+
+struct ManyMaps {
+    Maps kv;
+    CUtensorMap q;             // [batch, tokens, heads, head_dim], boxes of 64 columns of a row tile
+};
+
+// How the rows are cut: tokens of a row tile (its rows: tokens * G <= 128), units of a kv head and of all.
+struct Cut {
+    int tokens, groups, units, split;
+    float *scratch;            // of split > 1
+};
+
+struct Unit {
+    Seq s;
+    Range r;
+    int64_t b;
+    int hk, t0;                // kv head, first token
+    int begin, end;            // tiles of the line that this block takes
+};
+
+template <int KEYS, int TILES>
+__device__ __forceinline__ Unit unit_of(const Win &A, const Cut &C, int u, int rank, int box)
+{
+    Unit U;
+    const uint32_t heads = (uint32_t)A.a.kv_heads, per = (uint32_t)A.a.batch * heads;
+    // (the last tokens first: their lines are the longest)
+    const uint32_t g = (uint32_t)u / per, bh = (uint32_t)u - g * per;
+    U.b = bh / heads;
+    U.hk = (int)(bh - (uint32_t)U.b * heads);
+    U.t0 = (C.groups - 1 - (int)g) * TILES * C.tokens;
+    U.s = sequence(A, U.b);
+    U.r = range_of(A, U.s, U.t0, U.t0 + TILES * C.tokens - 1, box);
+    const int n = (U.r.n + KEYS - 1) / KEYS;
+    U.begin = (int)((int64_t)n * rank / C.split);
+    U.end = (int)((int64_t)n * (rank + 1) / C.split);
+    return U;
+}
+
+// Positions of a row tile's tokens that see anything; none: last < 0.
+struct Span {
+    int first, last;
+};
+__device__ __forceinline__ Span span_of(const Unit &U, const Cut &C, int r)
+{
+    const int ta = U.t0 + r * C.tokens, tb = ta + C.tokens < U.s.tokens ? ta + C.tokens - 1 : U.s.tokens - 1;
+    Span p{U.s.first + ta, U.s.first + tb};
+    if (p.first < 0) p.first = 0;
+    if (ta > tb || p.last < 0) p.last = -1;
+    return p;
+}
+// Whether one of them sees an entry of the line's [v, v + size).
+__device__ __forceinline__ bool reaches(const Win &A, const Range &r, const Span &p, int v, int size)
+{
+    if (p.last < 0) return false;
+    if (v < r.sinks) return true;
+    const int j = r.real(v);
+    return j <= p.last && (j + size > p.first - A.window + 1 || j < A.sinks);
+}
+// Whether every row sees all of them, and whether some row sees each.
+__device__ __forceinline__ bool all_see(const Win &A, const Range &r, const Span &p, int v, int size)
+{
+    const Range mine{r.sinks, r.lo, r.n, r.hi, p.first, p.last};
+    return v + size <= r.n && seen_by_all(A, mine, v, size);
+}
+__device__ __forceinline__ bool none_idle(const Win &A, const Range &r, int v, int size)
+{
+    if (v + size > r.n) return false;
+    const int lo = window_start(A, r.first);                  // sinks <= j < lo: idle
+    if (v < r.sinks && v + size > A.sinks && A.sinks < r.sinks) return false;
+    if (v + size <= r.sinks) return true;
+    const int j = r.real(v < r.sinks ? r.sinks : v), end = r.real(v + size - 1);
+    return j >= lo || end < A.sinks;
+}
+
+// 128-byte rows of P and S in tensor memory, 32 columns at once (see tc_ld_begin).
+__device__ __forceinline__ float pow2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 32 bytes, a whole sector, at once.
+__device__ __forceinline__ void store32(float *p, float a, float b, float c, float d, float e, float f, float g, float h)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d), "f"(e), "f"(f), "f"(g), "f"(h) : "memory");
+}
+// A part's place in scratch: the rows' outputs, maxima and sums.
+template <int DP, int TILES> __host__ __device__ constexpr int64_t part_floats() { return TILES * 128 * (int64_t)(DP + 2); }
+template <int DP, int TILES> __device__ __forceinline__ float *part_of(const Cut &C, int u, int rank)
+{
+    return C.scratch + ((int64_t)u * C.split + rank) * part_floats<DP, TILES>();
+}
+
+template <class T, int DP, int TILES>
+__global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, Cut C, const __grid_constant__ ManyMaps maps)
+{
+    using M = Many<DP, TILES>;
+    constexpr int KEYS = M::KEYS, ST = M::STAGES;
+    const dbs_window_args &a = A.a;
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(8) uint64_t bars[5 * ST + 6 * TILES + 1];
+    __shared__ uint32_t tmem_at;
+    __shared__ int stop;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t sq = base, sk = base + TILES * M::Q, sv = sk + ST * M::KV;
+    const uint32_t k_full = smem_addr(bars), k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST, v_fixed = v_empty + 8 * ST;
+    const uint32_t q_full = v_fixed + 8 * ST, q_empty = q_full + 8 * TILES, s_full = q_empty + 8 * TILES, p_half = s_full + 8 * TILES;
+    const uint32_t p_full = p_half + 8 * TILES, o_done = p_full + 8 * TILES, last_bar = o_done + 8 * TILES;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // (a join waits for this grid's end)
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            bar_init(k_full + 8 * i, 1);
+            bar_init(k_empty + 8 * i, 1);
+            bar_init(v_full + 8 * i, 1);
+            bar_init(v_empty + 8 * i, 2);
+            bar_init(v_fixed + 8 * i, 1);
+        }
+        for (int i = 0; i < TILES; ++i) {
+            bar_init(q_full + 8 * i, 1);
+            bar_init(q_empty + 8 * i, 1);
+            bar_init(s_full + 8 * i, 1);
+            bar_init(p_half + 8 * i, 128);
+            bar_init(p_full + 8 * i, 128);
+            bar_init(o_done + 8 * i, 1);
+        }
+        bar_init(last_bar, 1);
+        stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == M::HELP + 2) tc_alloc(smem_addr(&tmem_at));
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = tmem_at;
+    const int rank = C.split > 1 ? (int)(blockIdx.x % (uint32_t)C.split) : 0;
+    const int u0 = (int)(blockIdx.x / (uint32_t)C.split), step = (int)(gridDim.x / (uint32_t)C.split), box = maps.kv.box;
+    const uint32_t limit = A.waits.limit;
+
+    if (warp < M::HELP) {
+        // ---- softmax: a thread has a row ----
+        more_registers<TILES == 2 ? M::MANY : 0>();
+        const int r = warp >> 2, row = (warp & 3) * 32 + lane, tile_row = r * 128 + row;
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+        const uint32_t s_at = tmem + lanes + M::S_COL + r * KEYS, o_at = tmem + lanes + M::O_COL + r * DP;
+        const int dt = row / A.group, dh = row - dt * A.group;             // its token in the row tile, its head
+        int count = 0;                                                     // tiles done
+        bool ok = true;
+        for (int u = u0; u < C.units; u += step) {
+            const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
+            const Span span = span_of(U, C, r);
+            const int t = U.t0 + r * C.tokens + dt, h = U.hk * A.group + dh;
+            const bool inside = dt < C.tokens && t < a.tokens;
+            const int p = inside && t < U.s.tokens && U.s.first + t >= 0 ? U.s.first + t : -1;
+            const bool busy = __any_sync(~0u, inside);
+            float m = -INFINITY, l = 0.f;
+            bool some = false;
+            for (int i = U.begin; ok && i < U.end; ++i) {
+                const int v0 = i * KEYS;
+                if (!reaches(A, U.r, span, v0, KEYS)) continue;
+                // (the scores come after the product before them: O is at rest)
+                ok = __all_sync(~0u, bar_wait(s_full + 8 * r, count & 1, &stop, limit));
+                if (!ok) break;
+                tc_after();
+                ++count;
+                if (busy) {
+                    constexpr int PARTS = KEYS / 32;
+                    uint32_t x[PARTS][32];
+#pragma unroll
+                    for (int c = 0; c < PARTS; ++c) tc_ld_begin(x[c], s_at + 32 * c);
+#pragma unroll
+                    for (int c = 0; c < PARTS; ++c) tc_ld_end(x[c]);
+                    if (!all_see(A, U.r, span, v0, KEYS)) {
+                        // columns that the row sees: up to `to`, and from behind `from` on or below `sinks`
+                        const int from_v = p - (v0 - U.r.sinks + U.r.lo), to = from_v, sinks = A.sinks - v0;
+                        const int from = from_v - A.window;
+#pragma unroll
+                        for (int c = 0; c < PARTS; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int at = 32 * c + e;
+                                if (!(at <= to && (at > from || at < sinks))) x[c][e] = 0xff800000u;
+                            }
+                    }
+                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < PARTS; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(x[c][e]));
+                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * A.scale_log2;      // (scale > 0 here)
+                    // replace the maximum only when it grew by more than 2^8
+                    const bool grew = top > m + 8.f || (m == -INFINITY && top > m);
+                    if (__any_sync(~0u, grew)) {
+                        const float f = grew ? (m == -INFINITY ? 0.f : exp2f(m - top)) : 1.f;
+                        if (grew) m = top;
+                        l *= f;
+                        if (some) {
+#pragma unroll 1
+                            for (int c = 0; c < DP / 32; ++c) {
+                                float o[32];
+                                uint32_t w[32];
+                                tc_ld(o, o_at + 32 * c);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
+                                tc_st(o_at + 32 * c, w);
+                            }
+                        }
+                    }
+                    const float shift = m == -INFINITY ? 0.f : m;
+                    float l4[4] = {l, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < PARTS / 2; ++c) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int e = 0; e < 64; e += 2) {
+                            const uint32_t *y = x[2 * c + e / 32] + e % 32;
+                            const float y0 = pow2(fmaf(__uint_as_float(y[0]), A.scale_log2, -shift)), y1 = pow2(fmaf(__uint_as_float(y[1]), A.scale_log2, -shift));
+                            l4[(e & 2)] += y0;
+                            l4[(e & 2) + 1] += y1;
+                            w[e / 2] = pack2<T>(y0, y1);
+                        }
+                        tc_st(s_at + 32 * c, w);
+                        tc_wait_st();
+                        tc_before();
+                        if (PARTS == 4) bar_arrive((c == 0 ? p_half : p_full) + 8 * r);
+                    }
+                    l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    if (PARTS == 2) {
+                        bar_arrive(p_half + 8 * r);
+                        bar_arrive(p_full + 8 * r);
+                    }
+                } else {
+                    tc_before();
+                    bar_arrive(p_half + 8 * r);
+                    bar_arrive(p_full + 8 * r);
+                }
+                some = true;
+            }
+            // the unit's (or the part's) output
+            if (ok && some) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (count - 1) & 1, &stop, limit));
+            tc_after();
+            const float nan = nanf("");
+            const bool none = p < 0 || l == 0.f, whole = C.split == 1;
+            const float by = !ok ? nan : !whole ? 1.f : none ? 0.f : 1.f / l;
+            float *const part = whole ? nullptr : part_of<DP, TILES>(C, u, rank);
+            T *out = (T *)a.out + U.b * a.o_batch + t * a.o_token + h * a.o_head;
+            bool odd = false;
+            if (busy)
+#pragma unroll 1
+                for (int c = 0; c < DP / 32; ++c) {
+                    float v[32];
+                    if (some && ok) tc_ld(v, o_at + 32 * c);
+                    if (!inside) continue;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = !ok ? nan : none ? 0.f : v[e] * by;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        const int d = 32 * c + e;
+                        if (d >= a.head_dim) break;
+                        if (!whole) {
+                            store32(part + tile_row * DP + d, v[e], v[e + 1], v[e + 2], v[e + 3], v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+                            continue;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) odd |= !isfinite(v[e + k]);
+                        if (A.wide_out) {
+                            *(uint4 *)(out + d) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]), pack2<T>(v[e + 4], v[e + 5]),
+                                                             pack2<T>(v[e + 6], v[e + 7]));
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) out[d + k] = from_f32<T>(v[e + k]);
+                        }
+                    }
+                }
+            tc_before();
+            if (inside && !whole) {
+                part[TILES * 128 * DP + tile_row] = m;
+                part[TILES * 128 * (DP + 1) + tile_row] = ok ? l : nan;
+            } else if (inside && a.lse) {
+                a.lse[(U.b * a.tokens + t) * a.q_heads + h] = !ok ? nan : none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            }
+            for (unsigned again = __ballot_sync(~0u, odd && ok && l == l); again; again &= again - 1) {
+                const int k = __ffs(again) - 1, tk = __shfl_sync(~0u, t, k), hh = __shfl_sync(~0u, h, k);
+                float ol[8], m1, l1;
+                row_by_warp<T>(A, U.s, U.b, tk, hh, 0, 1, m1, l1, ol);
+                store_row<T>(A, U.b, tk, hh, m1, l1, ol);
+            }
+        }
+    } else {
+        fewer_registers<TILES == 2 ? M::FEW : 0>();
+        if (warp <= M::HELP + 1) {
+            // ---- fetch: one warp Q and K, one V, a lane a box ----
+            const bool is_v = warp > M::HELP;
+            const uint32_t store = is_v ? sv : sk, full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
+            const CUtensorMap *const map = is_v ? &maps.kv.v : &maps.kv.k;
+            const int boxes = KEYS / box;                                  // (boxes of 8 to 128 entries; 1 to 16 of them)
+            const uint32_t vain = vain_bytes(A.waits);
+            int n = 0, nq[TILES] = {};
+            bool ok = true;
+            for (int u = u0; ok && u < C.units; u += step) {
+                const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
+                if (!is_v)
+#pragma unroll
+                    for (int r = 0; r < TILES; ++r) {
+                        if (!ok || span_of(U, C, r).last < 0) continue;
+                        ok = __all_sync(~0u, bar_wait(q_empty + 8 * r, (nq[r] + 1) & 1, &stop, limit));   // the first round finds it free
+                        if (!ok) continue;
+                        if (elected()) {
+                            bar_expect(q_full + 8 * r, (uint32_t)(C.tokens * A.group * 128 * (DP / 64)));
+#pragma unroll
+                            for (int c = 0; c < DP / 64; ++c)
+                                box_load(sq + r * M::Q + c * M::SUBQ, &maps.q, 64 * c, U.hk * A.group, U.t0 + r * C.tokens, (int)U.b, q_full + 8 * r);
+                        }
+                        __syncwarp();
+                        ++nq[r];
+                    }
+                Place at = {0, 0};
+                auto find = [&](int i) {
+                    const int v = i * KEYS + lane * box;
+                    if (lane < boxes && v < U.r.n) at = place_of(a, U.b, U.r.real(v));
+                };
+                if (U.begin < U.end) find(U.begin);
+                for (int i = U.begin; i < U.end && ok; ++i, ++n) {
+                    const int st = n % ST;
+                    ok = __all_sync(~0u, bar_wait(empty + 8 * st, (n / ST + 1) & 1, &stop, limit));
+                    if (!ok) break;
+                    const bool mine = lane < boxes && i * KEYS + lane * box < U.r.n;
+                    const int count = __popc(__ballot_sync(~0u, mine));
+                    if (lane == 0) bar_expect(full + 8 * st, (uint32_t)(count * box * 128 * (DP / 64)) + vain);
+                    __syncwarp();
+                    if (mine)
+#pragma unroll
+                        for (int c = 0; c < DP / 64; ++c)
+                            box_load(store + st * M::KV + c * M::SUBK + lane * box * 128, map, 64 * c, U.hk, (int)at.in, (int)at.page, full + 8 * st);
+                    __syncwarp();
+                    if (i + 1 < U.end) find(i + 1);
+                }
+            }
+            // copies under way end before their memory is given back
+            for (int i = n > ST ? n - ST : 0; i < n; ++i) {
+                int last = 0;
+                bar_wait(full + 8 * (i % ST), i / ST & 1, &last, limit);
+            }
+#pragma unroll
+            for (int r = 0; r < TILES; ++r)
+                if (nq[r] > 0) {
+                    int last = 0;
+                    bar_wait(q_full + 8 * r, (nq[r] - 1) & 1, &last, limit);
+                }
+        } else if (warp == M::HELP + 2) {
+            // ---- issue the products ----
+            constexpr uint32_t FMT = __is_same(T, __nv_bfloat16) ? 1u : 0u;
+            constexpr uint32_t DESC = 1u << 4 | FMT << 7 | FMT << 10 | (128u >> 4) << 24;
+            constexpr uint32_t DESC_S = DESC | (uint32_t)(KEYS >> 3) << 17, DESC_O = DESC | 1u << 16 | (uint32_t)(DP >> 3) << 17;
+            uint32_t fixes = 0;                                            // parity of v_fixed of a stage, a bit each
+            int n = 0, nq[TILES] = {}, count[TILES] = {};                  // tiles before this unit's; its row tiles' units, products
+            bool ok = true;
+            for (int u = u0; ok && u < C.units; u += step) {
+                const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
+                Span span[TILES];
+                bool more[TILES] = {};                                     // O has a product of this unit
+#pragma unroll
+                for (int r = 0; r < TILES; ++r) {
+                    span[r] = span_of(U, C, r);
+                    if (span[r].last >= 0 && ok) ok = __all_sync(~0u, bar_wait(q_full + 8 * r, nq[r]++ & 1, &stop, limit));
+                }
+                for (int i = U.begin - 1; i < U.end && ok; ++i) {
+                    const int t = n + i - U.begin, sv_ = (t + ST) % ST, sk_ = (t + 1) % ST;   // (t = -1: there is no V)
+#pragma unroll
+                    for (int r = 0; r < TILES; ++r) {
+                        if (i >= U.begin && reaches(A, U.r, span[r], i * KEYS, KEYS)) {
+                            const uint32_t d = __shfl_sync(~0u, tmem + M::O_COL + r * DP, 0), pa = __shfl_sync(~0u, tmem + M::S_COL + r * KEYS, 0);
+                            const uint32_t va = desc_lo(sv + sv_ * M::KV, M::SUBK), acc = __shfl_sync(~0u, (uint32_t)more[r], 0);
+                            uint64_t vd[KEYS / 16];
+#pragma unroll
+                            for (int k = 0; k < KEYS / 16; ++k) vd[k] = desc_of(va + k * 2048 / 16);
+                            ok = ok && __all_sync(~0u, bar_wait(v_full + 8 * sv_, t / ST & 1, &stop, limit));
+                            if (ok && !none_idle(A, U.r, i * KEYS, KEYS)) ok = __all_sync(~0u, bar_wait(v_fixed + 8 * sv_, fixes >> sv_ & 1u, &stop, limit));
+                            if (ok) ok = __all_sync(~0u, bar_wait(p_half + 8 * r, count[r] & 1, &stop, limit));
+                            if (!ok) break;
+                            tc_after();
+                            if (elected()) {
+#pragma unroll
+                                for (int k = 0; k < KEYS / 32; ++k) tc_mma_ts(d, pa + 8 * k, vd[k], DESC_O, k > 0 ? 1u : acc);
+                            }
+                            __syncwarp();
+                            ok = __all_sync(~0u, bar_wait(p_full + 8 * r, count[r] & 1, &stop, limit));
+                            if (!ok) break;
+                            tc_after();
+                            if (elected()) {
+#pragma unroll
+                                for (int k = KEYS / 32; k < KEYS / 16; ++k) tc_mma_ts(d, pa + 8 * k, vd[k], DESC_O, 1u);
+                                tc_commit(o_done + 8 * r);
+                            }
+                            __syncwarp();
+                            ++count[r];
+                            more[r] = true;
+                        }
+                        if (i + 1 < U.end && reaches(A, U.r, span[r], (i + 1) * KEYS, KEYS)) {
+                            const uint32_t d = __shfl_sync(~0u, tmem + M::S_COL + r * KEYS, 0);
+                            const uint32_t qa = desc_lo(sq + r * M::Q, 16), ka = desc_lo(sk + sk_ * M::KV, 16);
+                            uint64_t qd[DP / 16], kd[DP / 16];
+#pragma unroll
+                            for (int k = 0; k < DP / 16; ++k) {
+                                qd[k] = desc_of(qa + ((k >> 2) * M::SUBQ + (k & 3) * 32) / 16);
+                                kd[k] = desc_of(ka + ((k >> 2) * M::SUBK + (k & 3) * 32) / 16);
+                            }
+                            ok = ok && __all_sync(~0u, bar_wait(k_full + 8 * sk_, (t + 1) / ST & 1, &stop, limit));
+                            // P of the tile before, in these columns, has been read
+                            if (ok && count[r] > 0) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (count[r] - 1) & 1, &stop, limit));
+                            if (!ok) break;
+                            tc_after();
+                            if (elected()) {
+#pragma unroll
+                                for (int k = 0; k < DP / 16; ++k) tc_mma_ss(d, qd[k], kd[k], DESC_S, k > 0);
+                                tc_commit(s_full + 8 * r);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (!ok) break;
+                    if (i >= U.begin && !none_idle(A, U.r, i * KEYS, KEYS)) fixes ^= 1u << sv_;
+                    if (elected()) {
+                        if (i >= U.begin) tc_commit(v_empty + 8 * sv_);
+                        if (i + 1 < U.end) tc_commit(k_empty + 8 * sk_);
+                        if (i + 1 == U.end - 1 || U.begin == U.end)
+#pragma unroll
+                            for (int r = 0; r < TILES; ++r)
+                                if (span[r].last >= 0) tc_commit(q_empty + 8 * r);
+                    }
+                    __syncwarp();
+                }
+                n += U.end - U.begin;
+            }
+            // products under way end before their memory is given back
+            if (elected()) tc_commit(last_bar);
+            __syncwarp();
+            int last = 0;
+            bar_wait(last_bar, 0, &last, limit);
+        } else {
+            // ---- clear what no row of the unit sees in V: copied with a box, or behind the line ----
+            int n = 0;
+            bool ok = true;
+            for (int u = u0; ok && u < C.units; u += step) {
+                const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
+                for (int i = U.begin; i < U.end && ok; ++i, ++n) {
+                    const int st = n % ST;
+                    ok = __all_sync(~0u, bar_wait(v_full + 8 * st, n / ST & 1, &stop, limit));
+                    if (!ok) break;
+                    if (!none_idle(A, U.r, i * KEYS, KEYS)) {
+                        for (int k0 = 0; k0 < KEYS; k0 += 32) {
+                            const int v = i * KEYS + k0 + lane;
+                            unsigned clear = __ballot_sync(~0u, v >= U.r.n || !seen_by_any(A, U.r, U.r.real(v)));
+                            for (; clear; clear &= clear - 1) {
+                                const uint32_t at = sv + st * M::KV + (k0 + __ffs(clear) - 1) * 128;
+                                if (lane < DP / 8)
+                                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at + (lane >> 3) * M::SUBK + ((lane & 7) << 4)), "r"(0) : "memory");
+                            }
+                        }
+                        async_fence();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(v_fixed + 8 * st);
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(v_empty + 8 * st);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    if (warp == M::HELP + 2) {
+        tc_after();
+        tc_free(tmem);
+    }
+    if (tid == 0 && stop) ran_out = 1;
+}
+
+constexpr int JOIN_NT = 128, JOIN_SPLIT = 16;
+
+// Joins the parts of a unit, a row by each warp: the lanes read the parts' maxima and sums, then
+// all add up the parts' outputs in order, several loads at a time.
+template <class T, int DP, int TILES>
+__global__ void __launch_bounds__(JOIN_NT) k_window_join(Win A, Cut C)
+{
+    const dbs_window_args &a = A.a;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, i = (int)(blockIdx.x * (JOIN_NT / 32) + (threadIdx.x >> 5)), u = i / (TILES * 128), tile_row = i % (TILES * 128);
+    const uint32_t heads = (uint32_t)a.kv_heads, per = (uint32_t)a.batch * heads, g = (uint32_t)u / per, bh = (uint32_t)u - g * per;
+    const int64_t b = bh / heads;
+    const int hk = (int)(bh % heads), row = tile_row % 128, dt = row / A.group;
+    const int t = (C.groups - 1 - (int)g) * TILES * C.tokens + tile_row / 128 * C.tokens + dt, h = hk * A.group + row - dt * A.group;
+    if (dt >= C.tokens || t >= a.tokens) return;
+    const Seq s = sequence(A, b);
+    const float *const parts = part_of<DP, TILES>(C, u, 0);
+    constexpr int64_t PART = part_floats<DP, TILES>();
+    const bool in = lane < C.split;
+    const float m = in ? __ldcg(parts + lane * PART + TILES * 128 * DP + tile_row) : -INFINITY;
+    float l = in ? __ldcg(parts + lane * PART + TILES * 128 * (DP + 1) + tile_row) : 0.f, top = m;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    const float f = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2f(m - top);
+    l = f == 0.f ? 0.f : f * l;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+    if (t >= s.tokens || s.first + t < 0) l = 0.f;
+    float o[8] = {};
+#pragma unroll 4
+    for (int k = 0; k < C.split; ++k) {
+        const float fk = __shfl_sync(~0u, f, k);
+#pragma unroll
+        for (int e = 0; e < DP / 32; ++e) {
+            const float x = lane + 32 * e < a.head_dim ? __ldcg(parts + k * PART + tile_row * DP + lane + 32 * e) : 0.f;
+            o[e] += fk == 0.f ? 0.f : fk * x;
+        }
+    }
+    float m1 = top;
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (l == 0.f) o[e] = 0.f;
+        odd |= !isfinite(o[e]);
+    }
+    if (l == l && __any_sync(~0u, odd)) row_by_warp<T>(A, s, b, t, h, 0, 1, m1, l, o);
+    store_row<T>(A, b, t, h, m1, l, o);
+}
+
 bool args_ok(const dbs_window_args *a)
 {
     constexpr int64_t INTS = int64_t(1) << 31;
     if (!a || (a->dtype != DBS_F16 && a->dtype != DBS_BF16) || a->head_dim < 1 || a->head_dim > 256 || a->kv_heads < 1 ||
         a->kv_heads > 65536 || a->q_heads < a->kv_heads || a->q_heads > 65536 || a->q_heads % a->kv_heads || a->batch < 0 ||
-        a->batch >= INTS || a->tokens < 0 || a->tokens >= INTS || a->pages < 0 || a->page_size < 0 || a->max_pages < 0 ||
+        a->batch >= INTS || a->tokens < 0 || a->tokens > INTS - 1024 || a->pages < 0 || a->page_size < 0 || a->max_pages < 0 ||
         a->page_size >= INTS || a->max_pages >= INTS || a->pages >= INTS || a->window < 1 || a->sinks < 0 || !std::isfinite(a->scale))
         return false;
     if (a->batch == 0 || a->tokens == 0) return true;
@@ -692,22 +1249,102 @@ dbs_status launch_few(const Win &A, const Maps &maps, cudaStream_t s)
     return launched();
 }
 
-template <class T, int DP>
-dbs_status launch_size(const Win &A, cudaStream_t s)
+// Q's rows as boxes of a row tile: 64 columns of a kv head's query heads of `tokens` tokens.
+bool make_q_map(const dbs_window_args &a, int group, int tokens, CUtensorMap &map)
 {
-    Maps maps{};
-    return make_maps(A.a, FEW_STEP, maps) ? launch_few<T, DP, true>(A, maps, s) : launch_few<T, DP, false>(A, maps, s);
+    const encode_tiled_fn encode = encode_tiled();
+    const cuuint64_t dims[4] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.q_heads, (cuuint64_t)a.tokens, (cuuint64_t)a.batch};
+    const int64_t by[3] = {a.q_head, a.q_token, a.q_batch};
+    const cuuint32_t box[4] = {64, (cuuint32_t)group, (cuuint32_t)tokens, 1}, ones[4] = {1, 1, 1, 1};
+    cuuint64_t strides[3];
+    for (int d = 0; d < 3; ++d) {
+        const int64_t bytes = dims[d + 1] == 1 ? 16 * a.head_dim : by[d] * 2;
+        if (bytes <= 0 || bytes >= int64_t(1) << 40) return false;
+        strides[d] = (cuuint64_t)bytes;
+    }
+    return encode && encode(&map, a.dtype == DBS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                            const_cast<void *>(a.q), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, int DP, int TILES>
+dbs_status launch_many(const Win &A, Cut C, const ManyMaps &maps, cudaStream_t s)
+{
+    using M = Many<DP, TILES>;
+    static Once once;
+    if (!room_for(once, k_window_many<T, DP, TILES>, M::SMEM, false, TILES == 2 ? M::REGS : 0)) return DBS_ERR_CUDA;
+    const int sms = multiprocessors();
+    k_window_many<T, DP, TILES><<<C.split > 1 ? C.units * C.split : C.units < sms ? C.units : sms, M::NT, M::SMEM, s>>>(A, C, maps);
+    const dbs_status st = launched();
+    if (st != DBS_OK || C.split == 1) return st;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(C.units * TILES * 128 / (JOIN_NT / 32)));
+    c.blockDim = JOIN_NT;
+    c.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, k_window_join<T, DP, TILES>, A, C) == cudaSuccess ? DBS_OK : (cudaGetLastError(), DBS_ERR_CUDA);
+}
+
+// How a call runs.
+struct Plan {
+    bool rows, many;           // any alignment; 128 rows at a time
+    ManyMaps maps;             // of `many`, with Q; of the kernel for few rows without
+    bool boxes;                // there are maps
+    Cut cut;                   // of `many`
+    int64_t scratch;           // bytes
+};
+
+dbs_status plan_of(const dbs_window_args &a, Plan &P)
+{
+    P.rows = !on_vectors(a);
+    P.many = P.boxes = false;
+    P.scratch = 0;
+    if (P.rows) return DBS_OK;
+    const int sms = multiprocessors(), group = a.q_heads / a.kv_heads, dp = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256;
+    if (sms == 0) return DBS_ERR_CUDA;
+    // Many rows of a kv head: 128 at a time, if K, V and Q can be copied as boxes (sinks and the
+    // window's start round to them).
+    if (a.tokens * group > FEW_ROWS && group <= 128 && a.scale > 0 && make_maps(a, a.sinks > 0 ? 16 : dp == 256 ? 64 : 128, P.maps.kv) &&
+        make_q_map(a, group, 128 / group, P.maps.q)) {
+        const int tiles = dp == 256 ? 1 : 2, keys = dp == 256 ? 64 : 128;
+        Cut &C = P.cut;
+        C.tokens = 128 / group;
+        C.groups = (int)((a.tokens + tiles * C.tokens - 1) / (tiles * C.tokens));
+        C.units = (int)(a.batch * a.kv_heads * C.groups);
+        C.scratch = nullptr;
+        // Blocks of a unit: as many as find room at once, with two tiles each at least.
+        const int64_t line = (line_of(a, tiles * C.tokens) + keys - 1) / keys;
+        int64_t split = sms / C.units;
+        split = split < line / 2 ? split : line / 2;
+        C.split = (int)(split < 1 ? 1 : split < JOIN_SPLIT ? split : JOIN_SPLIT);
+        if (C.split > 1) P.scratch = (int64_t)C.units * C.split * tiles * 128 * (dp + 2) * (int64_t)sizeof(float);
+        P.many = P.boxes = true;
+        return DBS_OK;
+    }
+    P.boxes = make_maps(a, FEW_STEP, P.maps.kv);
+    return DBS_OK;
+}
+
+template <class T, int DP>
+dbs_status launch_size(const Win &A, const Plan &P, cudaStream_t s)
+{
+    if (P.many) return launch_many<T, DP, DP == 256 ? 1 : 2>(A, P.cut, P.maps, s);
+    return P.boxes ? launch_few<T, DP, true>(A, P.maps.kv, s) : launch_few<T, DP, false>(A, P.maps.kv, s);
 }
 
 template <class T>
-dbs_status launch(const Win &A, cudaStream_t s)
+dbs_status launch(const Win &A, const Plan &P, cudaStream_t s)
 {
-    if (!on_vectors(A.a)) {
+    if (P.rows) {
         k_window_rows<T><<<(unsigned)(A.a.batch * A.a.tokens * A.a.q_heads), ROW_NT, 0, s>>>(A);
         return launched();
     }
     const int d = A.a.head_dim;
-    return d <= 64 ? launch_size<T, 64>(A, s) : d <= 128 ? launch_size<T, 128>(A, s) : launch_size<T, 256>(A, s);
+    return d <= 64 ? launch_size<T, 64>(A, P, s) : d <= 128 ? launch_size<T, 128>(A, P, s) : launch_size<T, 256>(A, P, s);
 }
 
 }  // namespace
@@ -716,13 +1353,33 @@ namespace dbs::ops {
 dbs_status window_waits_since(cudaStream_t s) { return waits_since(s); }
 }  // namespace dbs::ops
 
-extern "C" dbs_status dbs_window_attention(const dbs_window_args *a, void *stream)
+extern "C" {
+
+dbs_status dbs_window_attention_scratch(const dbs_window_args *a, int64_t *bytes)
+{
+    if (!bytes || !args_ok(a)) return DBS_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (a->batch == 0 || a->tokens == 0) return DBS_OK;
+    Plan P;
+    const dbs_status st = plan_of(*a, P);
+    if (st == DBS_OK) *bytes = P.scratch;
+    return st;
+}
+
+dbs_status dbs_window_attention(const dbs_window_args *a, void *stream)
 {
     if (!args_ok(a)) return DBS_ERR_INVALID_ARG;
     if (a->batch == 0 || a->tokens == 0) return DBS_OK;
-    constexpr int64_t MOST = 0x7fffffff;
+    Plan P;
+    const dbs_status st = plan_of(*a, P);
+    if (st != DBS_OK) return st;
+    if (P.scratch > 0 && (!a->scratch || (reinterpret_cast<uintptr_t>(a->scratch) & 31u) || a->scratch_bytes < P.scratch)) return DBS_ERR_INVALID_ARG;
+    P.cut.scratch = (float *)a->scratch;
+    constexpr int64_t MOST = 0x7fffffff - 1023;                          // (as many entries as there may be)
     const bool wide_out = aligned16(a->out) && aligned8(a->o_batch) && aligned8(a->o_token) && aligned8(a->o_head);
     const Win A{*a, a->scale * 1.4426950408889634f, (int)(a->window < MOST ? a->window : MOST), (int)(a->sinks < MOST ? a->sinks : MOST),
                 a->q_heads / a->kv_heads, wide_out, waits()};
-    return a->dtype == DBS_F16 ? launch<__half>(A, (cudaStream_t)stream) : launch<__nv_bfloat16>(A, (cudaStream_t)stream);
+    return a->dtype == DBS_F16 ? launch<__half>(A, P, (cudaStream_t)stream) : launch<__nv_bfloat16>(A, P, (cudaStream_t)stream);
 }
+
+}  // extern "C"

@@ -669,7 +669,13 @@ typedef struct {
     void *out;                 /* [batch, tokens, q_heads, head_dim], each head in a place of its own */
     int64_t o_batch, o_token, o_head;
     float *lse;                /* device [batch, tokens, q_heads], natural logarithm, or NULL */
+    void *scratch;             /* device, 32-byte aligned, dbs_window_attention_scratch bytes; the call
+                                  leaves nothing in it that a later call reads */
+    int64_t scratch_bytes;
 } dbs_window_args;
+/* Bytes of scratch that dbs_window_attention needs for this call (whose fields are
+ * checked, and set but for lse and scratch). */
+dbs_status dbs_window_attention_scratch(const dbs_window_args *a, int64_t *bytes);
 /* Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA.  Waits inside its kernels end after two seconds
  * (dbs_operators_check). */
 dbs_status dbs_window_attention(const dbs_window_args *a, void *stream);

@@ -87,7 +87,8 @@ def test_norm_gradient_nothing_to_do_and_scratch():
 
 
 WIN = dict(dtype=2, d=64, hq=8, hk=2, batch=2, tokens=3, q=A, q0=1536, q1=512, q2=64, k=A, v=A, k0=64, k1=64, k2=64, v0=64, v1=64, v2=64, pages=9,
-           page=16, pt=A, maxp=4, prow=4, kv=A, ql=0, window=5, sinks=0, scale=0.125, out=A, o0=1536, o1=512, o2=64, lse=0)
+           page=16, pt=A, maxp=4, prow=4, kv=A, ql=0, window=5, sinks=0, scale=0.125, out=A, o0=1536, o1=512, o2=64, lse=0,
+           scratch=A, bytes=1 << 40)
 
 
 def window(**kw):
@@ -104,12 +105,16 @@ def window(**kw):
                                 dict(batch=1 << 31), dict(tokens=1 << 31), dict(batch=1 << 16, tokens=1 << 15), dict(batch=1 << 14, tokens=1 << 14),
                                 dict(page=64, maxp=(1 << 25) - 1), dict(page=1 << 30, maxp=2), dict(page=(1 << 31) - 1, maxp=1), dict(pages=1 << 31)])
 def test_window_refusals(kw):
-    assert window(**kw) == BAD
+    a = dict(WIN)
+    a.update(kw)
+    need = ctypes.c_int64(-1)
+    assert window(**kw) == BAD and _lib.load().dbs_window_attention_scratch(_lib.WINDOW_ARGS.pack(*a.values()), ctypes.byref(need)) == BAD
 
 
 def test_window_nothing_to_do():
     assert window(batch=0, q=0, out=0, kv=0) == OK and window(tokens=0, q=0, out=0) == OK
-    assert _lib.load().dbs_window_attention(None, None) == BAD
+    assert _lib.load().dbs_window_attention(None, None) == BAD and _lib.load().dbs_window_attention_scratch(None, None) == BAD
+    assert _lib.load().dbs_window_attention_scratch(_lib.WINDOW_ARGS.pack(*WIN.values()), None) == BAD
 
 
 STATE = dict(table=A, batch=3, maxp=4, prow=4, kv=A, refs=A, pages=9, page=16)

@@ -288,7 +288,8 @@ WINDOW_CASES = [
     (1, 64, 8, 1, 64, 500, 16, 200, 4), (2, 130, 4, 2, 128, 130, 16, 1000, 0), (1, 300, 1, 1, 128, 300, 0, 64, 4), (1, 257, 3, 1, 64, 400, 128, 128, 130),
     (2, 100, 7, 1, 128, 150, 16, 31, 1), (1, 200, 5, 1, 256, 200, 16, 90, 4), (2, 65, 2, 1, 256, 300, 0, 100, 20), (1, 140, 4, 4, 40, 140, 8, 17, 2),
     (1, 9, 130, 1, 64, 40, 16, 16, 1), (2, 70, 4, 2, 128, 100, 5, 33, 3), (1, 50, 4, 2, 64, 100, 1, 33, 3), (1, 6, 3, 1, 33, 60, 16, 20, 2),
-    (2, 40, 2, 2, 7, 60, 3, 20, 2), (1, 600, 2, 1, 128, 700, 256, 1, 0), (1, 520, 8, 2, 128, 520, 16, 128, 0)]
+    (2, 40, 2, 2, 7, 60, 3, 20, 2), (1, 600, 2, 1, 128, 700, 256, 1, 0), (1, 520, 8, 2, 128, 520, 16, 128, 0),
+    (1, 40, 4, 1, 64, 2000, 16, 1500, 4), (2, 30, 4, 2, 128, 2100, 24, 2100, 0), (1, 20, 2, 2, 256, 1500, 0, 1000, 30), (3, 8, 8, 1, 128, 1300, 64, 1200, 64)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
