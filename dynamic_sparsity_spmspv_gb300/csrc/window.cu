@@ -605,14 +605,15 @@ __global__ void __launch_bounds__(FEW_NT) k_window_few(Win A, int groups, int sp
 // the rows of all units that it had not finished, and says so.
 
 template <int DP, int TILES> struct Many {
-    static constexpr int KEYS = DP == 256 ? 64 : 128;
-    static constexpr int STAGES = DP == 64 ? 3 : 2;                       // of K, and of V
+    static constexpr int KEYS = 64, SB = 2;                               // entries of a tile; score buffers of a row tile
+    static constexpr int STAGES = DP == 64 ? 6 : DP == 128 ? 4 : 2;       // of K, and of V
     static constexpr int SUBQ = 128 * 128, SUBK = KEYS * 128;             // 64 columns of a tile, in bytes
     static constexpr int Q = DP / 64 * SUBQ, KV = DP / 64 * SUBK;
-    static constexpr int HELP = 4 * TILES, NT = 32 * (HELP + 4);          // first of the warps that fetch, issue and clear
+    // first warps of the roles: fetch Q and K, fetch V, clear, issue (a warp for each row tile)
+    static constexpr int HELP = 4 * TILES, CLEAR = HELP + 2, ISSUE = HELP + 3, NT = 32 * (TILES == 2 ? 16 : 8);
     // registers of a thread at launch (TILES = 2), and once the helping warps have left some to the softmax's
-    static constexpr int REGS = 168, FEW = 88, MANY = (3 * REGS - FEW) / 2;
-    static constexpr int S_COL = 0, O_COL = TILES * KEYS;
+    static constexpr int REGS = 128, FEW = 80, MANY = 2 * REGS - FEW;
+    static constexpr int S_COL = 0, O_COL = TILES * SB * KEYS;
     static constexpr int SMEM = TILES * Q + STAGES * 2 * KV + 1024;
     static_assert(O_COL + TILES * DP <= 512, "tensor memory");
 };
@@ -666,37 +667,75 @@ __device__ __forceinline__ Span span_of(const Unit &U, const Cut &C, int r)
     if (ta > tb || p.last < 0) p.last = -1;
     return p;
 }
-// Whether one of them sees an entry of the line's [v, v + size).
-__device__ __forceinline__ bool reaches(const Win &A, const Range &r, const Span &p, int v, int size)
+// Which tiles of the line a row tile's tokens reach, those before `sinks` and from `from` to `to`,
+// and which all of them see whole, those before `all_sinks` and from `all_from` to `all_to`.
+struct Reach {
+    int sinks, from, to, all_sinks, all_from, all_to;
+    __device__ __forceinline__ bool some(int i) const { return i < sinks || (i >= from && i <= to); }
+    __device__ __forceinline__ bool all(int i) const { return i < all_sinks || (i >= all_from && i <= all_to); }
+};
+template <int KEYS> __device__ __forceinline__ Reach reach_of(const Win &A, const Range &r, const Span &p)
 {
-    if (p.last < 0) return false;
-    if (v < r.sinks) return true;
-    const int j = r.real(v);
-    return j <= p.last && (j + size > p.first - A.window + 1 || j < A.sinks);
+    if (p.last < 0) return {0, 1, 0, 0, 1, 0};
+    const int shift = r.sinks - r.lo;                                      // from an entry behind the sinks to its place in the line
+    const int begins = window_start(A, p.first) + shift, whole = window_start(A, p.last) + shift;
+    const int sinks = r.sinks ? r.sinks : A.sinks < p.last + 1 ? A.sinks : p.last + 1;
+    const int all = r.sinks || A.sinks < p.first + 1 ? A.sinks : p.first + 1;
+    return {(sinks + KEYS - 1) / KEYS, (begins > 0 ? begins : 0) / KEYS, (p.last + shift) / KEYS,
+            all / KEYS, (whole + KEYS - 1) / KEYS, (p.first + shift + 1) / KEYS - 1};
 }
-// Whether every row sees all of them, and whether some row sees each.
-__device__ __forceinline__ bool all_see(const Win &A, const Range &r, const Span &p, int v, int size)
+// Tiles with entries that no row of the unit sees: rounded to boxes between the sinks and the window,
+// and behind the line.
+struct Idle {
+    int from, to, last;
+    __device__ __forceinline__ bool any(int i) const { return (i >= from && i <= to) || i == last; }
+};
+template <int KEYS> __device__ __forceinline__ Idle idle_of(const Win &A, const Range &r)
 {
-    const Range mine{r.sinks, r.lo, r.n, r.hi, p.first, p.last};
-    return v + size <= r.n && seen_by_all(A, mine, v, size);
-}
-__device__ __forceinline__ bool none_idle(const Win &A, const Range &r, int v, int size)
-{
-    if (v + size > r.n) return false;
-    const int lo = window_start(A, r.first);                  // sinks <= j < lo: idle
-    if (v < r.sinks && v + size > A.sinks && A.sinks < r.sinks) return false;
-    if (v + size <= r.sinks) return true;
-    const int j = r.real(v < r.sinks ? r.sinks : v), end = r.real(v + size - 1);
-    return j >= lo || end < A.sinks;
+    const int end = r.sinks + window_start(A, r.first) - r.lo;
+    return {A.sinks < end ? A.sinks / KEYS : 1, A.sinks < end ? (end - 1) / KEYS : 0, r.n % KEYS ? r.n / KEYS : -1};
 }
 
-// 128-byte rows of P and S in tensor memory, 32 columns at once (see tc_ld_begin).
+// (to 2 units of the last place, and 0 below 2^-126: far below the 16 bits that P keeps)
 __device__ __forceinline__ float pow2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two fp32 values at once.
+__device__ __forceinline__ uint64_t two(float a, float b)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ float2 apart(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma_two(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ uint64_t add_two(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ float max_of(float a, float b, float c)
+{
+    float v;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
+    return v;
+}
+// The lowest n bits, for any n.
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 // 32 bytes, a whole sector, at once.
 __device__ __forceinline__ void store32(float *p, float a, float b, float c, float d, float e, float f, float g, float h)
 {
@@ -713,40 +752,41 @@ template <class T, int DP, int TILES>
 __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, Cut C, const __grid_constant__ ManyMaps maps)
 {
     using M = Many<DP, TILES>;
-    constexpr int KEYS = M::KEYS, ST = M::STAGES;
+    constexpr int KEYS = M::KEYS, ST = M::STAGES, SB = M::SB;
     const dbs_window_args &a = A.a;
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(8) uint64_t bars[5 * ST + 6 * TILES + 1];
+    __shared__ __align__(8) uint64_t bars[5 * ST + 7 * TILES + 1];
     __shared__ uint32_t tmem_at;
     __shared__ int stop;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t sq = base, sk = base + TILES * M::Q, sv = sk + ST * M::KV;
     const uint32_t k_full = smem_addr(bars), k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST, v_fixed = v_empty + 8 * ST;
-    const uint32_t q_full = v_fixed + 8 * ST, q_empty = q_full + 8 * TILES, s_full = q_empty + 8 * TILES, p_half = s_full + 8 * TILES;
-    const uint32_t p_full = p_half + 8 * TILES, o_done = p_full + 8 * TILES, last_bar = o_done + 8 * TILES;
+    const uint32_t q_full = v_fixed + 8 * ST, q_empty = q_full + 8 * TILES, s_full = q_empty + 8 * TILES, p_full = s_full + 8 * TILES * SB;
+    const uint32_t o_done = p_full + 8 * TILES * SB, last_bar = o_done + 8 * TILES;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // (a join waits for this grid's end)
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             bar_init(k_full + 8 * i, 1);
-            bar_init(k_empty + 8 * i, 1);
+            bar_init(k_empty + 8 * i, TILES);
             bar_init(v_full + 8 * i, 1);
-            bar_init(v_empty + 8 * i, 2);
+            bar_init(v_empty + 8 * i, TILES + 1);
             bar_init(v_fixed + 8 * i, 1);
         }
         for (int i = 0; i < TILES; ++i) {
             bar_init(q_full + 8 * i, 1);
             bar_init(q_empty + 8 * i, 1);
-            bar_init(s_full + 8 * i, 1);
-            bar_init(p_half + 8 * i, 128);
-            bar_init(p_full + 8 * i, 128);
             bar_init(o_done + 8 * i, 1);
         }
-        bar_init(last_bar, 1);
+        for (int i = 0; i < TILES * SB; ++i) {
+            bar_init(s_full + 8 * i, 1);
+            bar_init(p_full + 8 * i, 4);
+        }
+        bar_init(last_bar, TILES);
         stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == M::HELP + 2) tc_alloc(smem_addr(&tmem_at));
+    if (warp == M::ISSUE) tc_alloc(smem_addr(&tmem_at));
     tc_before();
     __syncthreads();
     tc_after();
@@ -760,59 +800,64 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
         more_registers<TILES == 2 ? M::MANY : 0>();
         const int r = warp >> 2, row = (warp & 3) * 32 + lane, tile_row = r * 128 + row;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
-        const uint32_t s_at = tmem + lanes + M::S_COL + r * KEYS, o_at = tmem + lanes + M::O_COL + r * DP;
+        const uint32_t s_at = tmem + lanes + M::S_COL + r * SB * KEYS, o_at = tmem + lanes + M::O_COL + r * DP;
         const int dt = row / A.group, dh = row - dt * A.group;             // its token in the row tile, its head
+        const uint64_t scale2 = two(A.scale_log2, A.scale_log2);
         int count = 0;                                                     // tiles done
         bool ok = true;
         for (int u = u0; u < C.units; u += step) {
             const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
-            const Span span = span_of(U, C, r);
+            const Reach reach = reach_of<KEYS>(A, U.r, span_of(U, C, r));
             const int t = U.t0 + r * C.tokens + dt, h = U.hk * A.group + dh;
             const bool inside = dt < C.tokens && t < a.tokens;
             const int p = inside && t < U.s.tokens && U.s.first + t >= 0 ? U.s.first + t : -1;
             const bool busy = __any_sync(~0u, inside);
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY;
+            uint64_t l2[2] = {0, 0};
             bool some = false;
             for (int i = U.begin; ok && i < U.end; ++i) {
-                const int v0 = i * KEYS;
-                if (!reaches(A, U.r, span, v0, KEYS)) continue;
-                // (the scores come after the product before them: O is at rest)
-                ok = __all_sync(~0u, bar_wait(s_full + 8 * r, count & 1, &stop, limit));
+                if (!reach.some(i)) continue;
+                const int buf = count & 1;
+                bool settled = !some;                                      // the product before this one is known to be in O
+                ok = __all_sync(~0u, bar_wait(s_full + 8 * (r * SB + buf), count >> 1 & 1, &stop, limit));
                 if (!ok) break;
                 tc_after();
-                ++count;
                 if (busy) {
-                    constexpr int PARTS = KEYS / 32;
-                    uint32_t x[PARTS][32];
+                    uint32_t x[2][32];
+                    tc_ld_begin(x[0], s_at + buf * KEYS);
+                    tc_ld_begin(x[1], s_at + buf * KEYS + 32);
+                    tc_ld_end(x[0]);
+                    tc_ld_end(x[1]);
+                    if (!reach.all(i)) {
+                        // columns that the row sees: up to `to`, and from behind `from` on or before `sinks`
+                        const int v0 = i * KEYS, to = p - (v0 - U.r.sinks + U.r.lo), from = to - A.window, sinks = A.sinks - v0;
 #pragma unroll
-                    for (int c = 0; c < PARTS; ++c) tc_ld_begin(x[c], s_at + 32 * c);
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t see = below(to + 1 - 32 * c) & (~below(from + 1 - 32 * c) | below(sinks - 32 * c));
 #pragma unroll
-                    for (int c = 0; c < PARTS; ++c) tc_ld_end(x[c]);
-                    if (!all_see(A, U.r, span, v0, KEYS)) {
-                        // columns that the row sees: up to `to`, and from behind `from` on or below `sinks`
-                        const int from_v = p - (v0 - U.r.sinks + U.r.lo), to = from_v, sinks = A.sinks - v0;
-                        const int from = from_v - A.window;
-#pragma unroll
-                        for (int c = 0; c < PARTS; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int at = 32 * c + e;
-                                if (!(at <= to && (at > from || at < sinks))) x[c][e] = 0xff800000u;
-                            }
+                            for (int e = 0; e < 32; ++e) x[c][e] = see >> e & 1u ? x[c][e] : 0xff800000u;
+                        }
                     }
                     float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < PARTS; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(x[c][e]));
+                    for (int e = 0; e < 64; e += 2) {
+                        const uint32_t *y = x[e / 32] + e % 32;
+                        t4[e / 2 & 3] = max_of(t4[e / 2 & 3], __uint_as_float(y[0]), __uint_as_float(y[1]));
+                    }
                     const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * A.scale_log2;      // (scale > 0 here)
                     // replace the maximum only when it grew by more than 2^8
                     const bool grew = top > m + 8.f || (m == -INFINITY && top > m);
                     if (__any_sync(~0u, grew)) {
                         const float f = grew ? (m == -INFINITY ? 0.f : exp2f(m - top)) : 1.f;
                         if (grew) m = top;
-                        l *= f;
+                        l2[0] = fma_two(l2[0], two(f, f), 0);
+                        l2[1] = fma_two(l2[1], two(f, f), 0);
                         if (some) {
+                            // the output so far, once the product before this one is in it
+                            ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (count - 1) & 1, &stop, limit));
+                            if (!ok) break;
+                            settled = true;
+                            tc_after();
 #pragma unroll 1
                             for (int c = 0; c < DP / 32; ++c) {
                                 float o[32];
@@ -824,36 +869,32 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                             }
                         }
                     }
-                    const float shift = m == -INFINITY ? 0.f : m;
-                    float l4[4] = {l, 0.f, 0.f, 0.f};
+                    const float shift = m == -INFINITY ? 0.f : -m;
+                    const uint64_t shift2 = two(shift, shift);
+                    uint32_t w[32];
 #pragma unroll
-                    for (int c = 0; c < PARTS / 2; ++c) {
-                        uint32_t w[32];
-#pragma unroll
-                        for (int e = 0; e < 64; e += 2) {
-                            const uint32_t *y = x[2 * c + e / 32] + e % 32;
-                            const float y0 = pow2(fmaf(__uint_as_float(y[0]), A.scale_log2, -shift)), y1 = pow2(fmaf(__uint_as_float(y[1]), A.scale_log2, -shift));
-                            l4[(e & 2)] += y0;
-                            l4[(e & 2) + 1] += y1;
-                            w[e / 2] = pack2<T>(y0, y1);
-                        }
-                        tc_st(s_at + 32 * c, w);
-                        tc_wait_st();
-                        tc_before();
-                        if (PARTS == 4) bar_arrive((c == 0 ? p_half : p_full) + 8 * r);
+                    for (int e = 0; e < 64; e += 2) {
+                        const uint32_t *y = x[e / 32] + e % 32;
+                        float2 f = apart(fma_two(two(__uint_as_float(y[0]), __uint_as_float(y[1])), scale2, shift2));
+                        f.x = pow2(f.x);
+                        f.y = pow2(f.y);
+                        l2[e / 2 & 1] = add_two(l2[e / 2 & 1], two(f.x, f.y));
+                        w[e / 2] = pack2<T>(f.x, f.y);
                     }
-                    l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-                    if (PARTS == 2) {
-                        bar_arrive(p_half + 8 * r);
-                        bar_arrive(p_full + 8 * r);
-                    }
-                } else {
-                    tc_before();
-                    bar_arrive(p_half + 8 * r);
-                    bar_arrive(p_full + 8 * r);
+                    tc_st(s_at + buf * KEYS, w);
+                    tc_wait_st();
                 }
+                // (every phase of o_done is waited for while the next cannot end)
+                if (!settled) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (count - 1) & 1, &stop, limit));
+                if (!ok) break;
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(p_full + 8 * (r * SB + buf));
+                ++count;
                 some = true;
             }
+            const float2 la = apart(l2[0]), lb = apart(l2[1]);
+            const float l = (la.x + la.y) + (lb.x + lb.y);
             // the unit's (or the part's) output
             if (ok && some) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (count - 1) & 1, &stop, limit));
             tc_after();
@@ -911,7 +952,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
             const bool is_v = warp > M::HELP;
             const uint32_t store = is_v ? sv : sk, full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
             const CUtensorMap *const map = is_v ? &maps.kv.v : &maps.kv.k;
-            const int boxes = KEYS / box;                                  // (boxes of 8 to 128 entries; 1 to 16 of them)
+            const int boxes = KEYS / box;                                  // (boxes of 8 to 64 entries; 1 to 8 of them)
             const uint32_t vain = vain_bytes(A.waits);
             int n = 0, nq[TILES] = {};
             bool ok = true;
@@ -965,107 +1006,112 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                     int last = 0;
                     bar_wait(q_full + 8 * r, (nq[r] - 1) & 1, &last, limit);
                 }
-        } else if (warp == M::HELP + 2) {
-            // ---- issue the products ----
+        } else if (warp >= M::ISSUE && warp < M::ISSUE + TILES) {
+            // ---- issue the products of a row tile ----
+            const int r = warp - M::ISSUE;
             constexpr uint32_t FMT = __is_same(T, __nv_bfloat16) ? 1u : 0u;
             constexpr uint32_t DESC = 1u << 4 | FMT << 7 | FMT << 10 | (128u >> 4) << 24;
             constexpr uint32_t DESC_S = DESC | (uint32_t)(KEYS >> 3) << 17, DESC_O = DESC | 1u << 16 | (uint32_t)(DP >> 3) << 17;
+            // (what the instructions take is the same in all lanes, and the compiler knows it)
+            auto same = [](uint32_t v) { return __shfl_sync(~0u, v, 0); };
+            const uint32_t qa = desc_lo(sq + r * M::Q, 16), k0 = desc_lo(sk, 16), va0 = desc_lo(sv, M::SUBK);
+            const uint32_t s_col = same(tmem + M::S_COL + r * SB * KEYS), o_col = same(tmem + M::O_COL + r * DP);
             uint32_t fixes = 0;                                            // parity of v_fixed of a stage, a bit each
-            int n = 0, nq[TILES] = {}, count[TILES] = {};                  // tiles before this unit's; its row tiles' units, products
+            uint32_t k_st = 0, k_par = 0, v_st = 0, v_par = 0;             // stages of the next scores and outputs, and their barriers' parities
+            uint32_t scores = 0, done = 0, nq = 0;                         // score tiles, products and units
             bool ok = true;
             for (int u = u0; ok && u < C.units; u += step) {
                 const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
-                Span span[TILES];
-                bool more[TILES] = {};                                     // O has a product of this unit
-#pragma unroll
-                for (int r = 0; r < TILES; ++r) {
-                    span[r] = span_of(U, C, r);
-                    if (span[r].last >= 0 && ok) ok = __all_sync(~0u, bar_wait(q_full + 8 * r, nq[r]++ & 1, &stop, limit));
-                }
-                for (int i = U.begin - 1; i < U.end && ok; ++i) {
-                    const int t = n + i - U.begin, sv_ = (t + ST) % ST, sk_ = (t + 1) % ST;   // (t = -1: there is no V)
-#pragma unroll
-                    for (int r = 0; r < TILES; ++r) {
-                        if (i >= U.begin && reaches(A, U.r, span[r], i * KEYS, KEYS)) {
-                            const uint32_t d = __shfl_sync(~0u, tmem + M::O_COL + r * DP, 0), pa = __shfl_sync(~0u, tmem + M::S_COL + r * KEYS, 0);
-                            const uint32_t va = desc_lo(sv + sv_ * M::KV, M::SUBK), acc = __shfl_sync(~0u, (uint32_t)more[r], 0);
-                            uint64_t vd[KEYS / 16];
-#pragma unroll
-                            for (int k = 0; k < KEYS / 16; ++k) vd[k] = desc_of(va + k * 2048 / 16);
-                            ok = ok && __all_sync(~0u, bar_wait(v_full + 8 * sv_, t / ST & 1, &stop, limit));
-                            if (ok && !none_idle(A, U.r, i * KEYS, KEYS)) ok = __all_sync(~0u, bar_wait(v_fixed + 8 * sv_, fixes >> sv_ & 1u, &stop, limit));
-                            if (ok) ok = __all_sync(~0u, bar_wait(p_half + 8 * r, count[r] & 1, &stop, limit));
-                            if (!ok) break;
+                const Span span = span_of(U, C, r);
+                const Reach reach = reach_of<KEYS>(A, U.r, span);
+                const Idle idle = idle_of<KEYS>(A, U.r);
+                const int begin = (int)same((uint32_t)U.begin), end = (int)same((uint32_t)U.end);
+                uint32_t more = 0;                                         // O has a product of this unit
+                if (span.last >= 0) ok = __all_sync(~0u, bar_wait(q_full + 8 * r, nq++ & 1, &stop, limit));
+                // the scores of tile i + 1, then the outputs of tile i
+                for (int i = begin - 1; i < end && ok; ++i) {
+                    if (i + 1 < end) {
+                        const bool some = reach.some(i + 1);
+                        ok = bar_wait(k_full + 8 * k_st, k_par, &stop, limit);
+                        // the last product that was issued is done: P in these columns has been read, in the tile
+                        // before the last or earlier
+                        if (some && done > 0) ok = ok && bar_wait(o_done + 8 * r, (done - 1) & 1, &stop, limit);
+                        ok = __all_sync(~0u, ok);
+                        if (!ok) break;
+                        if (some) {
+                            const uint32_t d = s_col + (scores & 1) * KEYS, ka = k0 + k_st * (M::KV / 16);
                             tc_after();
                             if (elected()) {
 #pragma unroll
-                                for (int k = 0; k < KEYS / 32; ++k) tc_mma_ts(d, pa + 8 * k, vd[k], DESC_O, k > 0 ? 1u : acc);
+                                for (int k = 0; k < DP / 16; ++k)
+                                    tc_mma_ss(d, desc_of(qa + ((k >> 2) * M::SUBQ + (k & 3) * 32) / 16), desc_of(ka + ((k >> 2) * M::SUBK + (k & 3) * 32) / 16),
+                                              DESC_S, k > 0);
+                                tc_commit(s_full + 8 * (r * SB + (scores & 1)));
+                                tc_commit(k_empty + 8 * k_st);
                             }
-                            __syncwarp();
-                            ok = __all_sync(~0u, bar_wait(p_full + 8 * r, count[r] & 1, &stop, limit));
-                            if (!ok) break;
-                            tc_after();
-                            if (elected()) {
-#pragma unroll
-                                for (int k = KEYS / 32; k < KEYS / 16; ++k) tc_mma_ts(d, pa + 8 * k, vd[k], DESC_O, 1u);
-                                tc_commit(o_done + 8 * r);
-                            }
-                            __syncwarp();
-                            ++count[r];
-                            more[r] = true;
+                            ++scores;
+                        } else if (lane == 0) {
+                            bar_arrive(k_empty + 8 * k_st);
                         }
-                        if (i + 1 < U.end && reaches(A, U.r, span[r], (i + 1) * KEYS, KEYS)) {
-                            const uint32_t d = __shfl_sync(~0u, tmem + M::S_COL + r * KEYS, 0);
-                            const uint32_t qa = desc_lo(sq + r * M::Q, 16), ka = desc_lo(sk + sk_ * M::KV, 16);
-                            uint64_t qd[DP / 16], kd[DP / 16];
-#pragma unroll
-                            for (int k = 0; k < DP / 16; ++k) {
-                                qd[k] = desc_of(qa + ((k >> 2) * M::SUBQ + (k & 3) * 32) / 16);
-                                kd[k] = desc_of(ka + ((k >> 2) * M::SUBK + (k & 3) * 32) / 16);
-                            }
-                            ok = ok && __all_sync(~0u, bar_wait(k_full + 8 * sk_, (t + 1) / ST & 1, &stop, limit));
-                            // P of the tile before, in these columns, has been read
-                            if (ok && count[r] > 0) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (count[r] - 1) & 1, &stop, limit));
-                            if (!ok) break;
-                            tc_after();
-                            if (elected()) {
-#pragma unroll
-                                for (int k = 0; k < DP / 16; ++k) tc_mma_ss(d, qd[k], kd[k], DESC_S, k > 0);
-                                tc_commit(s_full + 8 * r);
-                            }
-                            __syncwarp();
+                        __syncwarp();
+                        if (++k_st == ST) {
+                            k_st = 0;
+                            k_par ^= 1;
                         }
                     }
+                    if (i + 2 == end || begin == end) {
+                        if (span.last >= 0 && elected()) tc_commit(q_empty + 8 * r);
+                        __syncwarp();
+                    }
+                    if (i < begin) continue;
+                    const bool some = reach.some(i), cleared = idle.any(i);
+                    const uint32_t buf = done & 1;
+                    ok = bar_wait(v_full + 8 * v_st, v_par, &stop, limit);
+                    if (cleared) {
+                        ok = ok && bar_wait(v_fixed + 8 * v_st, fixes >> v_st & 1u, &stop, limit);
+                        fixes ^= 1u << v_st;
+                    }
+                    if (some) ok = ok && bar_wait(p_full + 8 * (r * SB + buf), done >> 1 & 1, &stop, limit);
+                    ok = __all_sync(~0u, ok);
                     if (!ok) break;
-                    if (i >= U.begin && !none_idle(A, U.r, i * KEYS, KEYS)) fixes ^= 1u << sv_;
-                    if (elected()) {
-                        if (i >= U.begin) tc_commit(v_empty + 8 * sv_);
-                        if (i + 1 < U.end) tc_commit(k_empty + 8 * sk_);
-                        if (i + 1 == U.end - 1 || U.begin == U.end)
+                    if (some) {
+                        const uint32_t pa = s_col + buf * KEYS, va = va0 + v_st * (M::KV / 16);
+                        tc_after();
+                        if (elected()) {
 #pragma unroll
-                            for (int r = 0; r < TILES; ++r)
-                                if (span[r].last >= 0) tc_commit(q_empty + 8 * r);
+                            for (int k = 0; k < KEYS / 16; ++k) tc_mma_ts(o_col, pa + 8 * k, desc_of(va + k * 2048 / 16), DESC_O, k > 0 ? 1u : more);
+                            tc_commit(o_done + 8 * r);
+                            tc_commit(v_empty + 8 * v_st);
+                        }
+                        ++done;
+                        more = 1;
+                    } else if (lane == 0) {
+                        bar_arrive(v_empty + 8 * v_st);
                     }
                     __syncwarp();
+                    if (++v_st == ST) {
+                        v_st = 0;
+                        v_par ^= 1;
+                    }
                 }
-                n += U.end - U.begin;
             }
             // products under way end before their memory is given back
             if (elected()) tc_commit(last_bar);
             __syncwarp();
             int last = 0;
             bar_wait(last_bar, 0, &last, limit);
-        } else {
+        } else if (warp == M::CLEAR) {
             // ---- clear what no row of the unit sees in V: copied with a box, or behind the line ----
             int n = 0;
             bool ok = true;
             for (int u = u0; ok && u < C.units; u += step) {
                 const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
+                const Idle idle = idle_of<KEYS>(A, U.r);
                 for (int i = U.begin; i < U.end && ok; ++i, ++n) {
                     const int st = n % ST;
                     ok = __all_sync(~0u, bar_wait(v_full + 8 * st, n / ST & 1, &stop, limit));
                     if (!ok) break;
-                    if (!none_idle(A, U.r, i * KEYS, KEYS)) {
+                    if (idle.any(i)) {
                         for (int k0 = 0; k0 < KEYS; k0 += 32) {
                             const int v = i * KEYS + k0 + lane;
                             unsigned clear = __ballot_sync(~0u, v >= U.r.n || !seen_by_any(A, U.r, U.r.real(v)));
@@ -1088,7 +1134,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
     __syncwarp();
     tc_before();
     __syncthreads();
-    if (warp == M::HELP + 2) {
+    if (warp == M::ISSUE) {
         tc_after();
         tc_free(tmem);
     }
@@ -1308,9 +1354,9 @@ dbs_status plan_of(const dbs_window_args &a, Plan &P)
     if (sms == 0) return DBS_ERR_CUDA;
     // Many rows of a kv head: 128 at a time, if K, V and Q can be copied as boxes (sinks and the
     // window's start round to them).
-    if (a.tokens * group > FEW_ROWS && group <= 128 && a.scale > 0 && make_maps(a, a.sinks > 0 ? 16 : dp == 256 ? 64 : 128, P.maps.kv) &&
+    if (a.tokens * group > FEW_ROWS && group <= 128 && a.scale > 0 && make_maps(a, a.sinks > 0 ? 16 : 64, P.maps.kv) &&
         make_q_map(a, group, 128 / group, P.maps.q)) {
-        const int tiles = dp == 256 ? 1 : 2, keys = dp == 256 ? 64 : 128;
+        const int tiles = dp == 256 ? 1 : 2, keys = 64;
         Cut &C = P.cut;
         C.tokens = 128 / group;
         C.groups = (int)((a.tokens + tiles * C.tokens - 1) / (tiles * C.tokens));
