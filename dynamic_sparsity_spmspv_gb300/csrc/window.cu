@@ -605,17 +605,19 @@ __global__ void __launch_bounds__(FEW_NT) k_window_few(Win A, int groups, int sp
 // the rows of all units that it had not finished, and says so.
 
 template <int DP, int TILES> struct Many {
-    static constexpr int KEYS = 64, SB = 2;                               // entries of a tile; score buffers of a row tile
-    static constexpr int STAGES = DP == 64 ? 6 : DP == 128 ? 4 : 2;       // of K, and of V
+    static constexpr int KEYS = DP == 64 ? 96 : DP == 128 ? 80 : 64;      // entries of a tile
+    static constexpr int STAGES = DP == 256 ? 2 : 4;       // of K, and of V
     static constexpr int SUBQ = 128 * 128, SUBK = KEYS * 128;             // 64 columns of a tile, in bytes
     static constexpr int Q = DP / 64 * SUBQ, KV = DP / 64 * SUBK;
     // first warps of the roles: fetch Q and K, fetch V, clear, issue (a warp for each row tile)
     static constexpr int HELP = 4 * TILES, CLEAR = HELP + 2, ISSUE = HELP + 3, NT = 32 * (TILES == 2 ? 16 : 8);
     // registers of a thread at launch (TILES = 2), and once the helping warps have left some to the softmax's
     static constexpr int REGS = 128, FEW = 80, MANY = 2 * REGS - FEW;
-    static constexpr int S_COL = 0, O_COL = TILES * SB * KEYS;
+    // columns of tensor memory: scores, P (two to a column) and outputs of each row tile
+    static constexpr int S_COL = 0, P_COL = TILES * KEYS, O_COL = (P_COL + TILES * KEYS / 2 + 63) / 64 * 64;
     static constexpr int SMEM = TILES * Q + STAGES * 2 * KV + 1024;
     static_assert(O_COL + TILES * DP <= 512, "tensor memory");
+    static_assert(SMEM <= 227 * 1024 && KEYS % 16 == 0, "shared memory");
 };
 
 struct ManyMaps {
@@ -734,6 +736,21 @@ __device__ __forceinline__ float max_of(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
     return v;
 }
+// 16 columns of tensor memory: with more, a tile's scores would not stay in registers beside them.
+__device__ __forceinline__ void ld16(uint32_t (&r)[16], uint32_t a)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\ntcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t a, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+__device__ __forceinline__ void st8(uint32_t a, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
 // The lowest n bits, for any n.
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 // 32 bytes, a whole sector, at once.
@@ -752,18 +769,18 @@ template <class T, int DP, int TILES>
 __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, Cut C, const __grid_constant__ ManyMaps maps)
 {
     using M = Many<DP, TILES>;
-    constexpr int KEYS = M::KEYS, ST = M::STAGES, SB = M::SB;
+    constexpr int KEYS = M::KEYS, ST = M::STAGES;
     const dbs_window_args &a = A.a;
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(8) uint64_t bars[5 * ST + 7 * TILES + 1];
+    __shared__ __align__(8) uint64_t bars[5 * ST + 6 * TILES + 1];
     __shared__ uint32_t tmem_at;
     __shared__ int stop;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t sq = base, sk = base + TILES * M::Q, sv = sk + ST * M::KV;
     const uint32_t k_full = smem_addr(bars), k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST, v_fixed = v_empty + 8 * ST;
-    const uint32_t q_full = v_fixed + 8 * ST, q_empty = q_full + 8 * TILES, s_full = q_empty + 8 * TILES, p_full = s_full + 8 * TILES * SB;
-    const uint32_t o_done = p_full + 8 * TILES * SB, last_bar = o_done + 8 * TILES;
+    const uint32_t q_full = v_fixed + 8 * ST, q_empty = q_full + 8 * TILES, s_full = q_empty + 8 * TILES, s_free = s_full + 8 * TILES;
+    const uint32_t p_full = s_free + 8 * TILES, o_done = p_full + 8 * TILES, last_bar = o_done + 8 * TILES;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // (a join waits for this grid's end)
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -776,11 +793,10 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
         for (int i = 0; i < TILES; ++i) {
             bar_init(q_full + 8 * i, 1);
             bar_init(q_empty + 8 * i, 1);
-            bar_init(o_done + 8 * i, 1);
-        }
-        for (int i = 0; i < TILES * SB; ++i) {
             bar_init(s_full + 8 * i, 1);
+            bar_init(s_free + 8 * i, 4);
             bar_init(p_full + 8 * i, 4);
+            bar_init(o_done + 8 * i, 1);
         }
         bar_init(last_bar, TILES);
         stop = 0;
@@ -800,7 +816,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
         more_registers<TILES == 2 ? M::MANY : 0>();
         const int r = warp >> 2, row = (warp & 3) * 32 + lane, tile_row = r * 128 + row;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
-        const uint32_t s_at = tmem + lanes + M::S_COL + r * SB * KEYS, o_at = tmem + lanes + M::O_COL + r * DP;
+        const uint32_t s_at = tmem + lanes + M::S_COL + r * KEYS, p_at = tmem + lanes + M::P_COL + r * KEYS / 2, o_at = tmem + lanes + M::O_COL + r * DP;
         const int dt = row / A.group, dh = row - dt * A.group;             // its token in the row tile, its head
         const uint64_t scale2 = two(A.scale_log2, A.scale_log2);
         int count = 0;                                                     // tiles done
@@ -817,33 +833,50 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
             bool some = false;
             for (int i = U.begin; ok && i < U.end; ++i) {
                 if (!reach.some(i)) continue;
-                const int buf = count & 1;
-                bool settled = !some;                                      // the product before this one is known to be in O
-                ok = __all_sync(~0u, bar_wait(s_full + 8 * (r * SB + buf), count >> 1 & 1, &stop, limit));
+                ok = __all_sync(~0u, bar_wait(s_full + 8 * r, count & 1, &stop, limit));
                 if (!ok) break;
                 tc_after();
-                if (busy) {
-                    uint32_t x[2][32];
-                    tc_ld_begin(x[0], s_at + buf * KEYS);
-                    tc_ld_begin(x[1], s_at + buf * KEYS + 32);
-                    tc_ld_end(x[0]);
-                    tc_ld_end(x[1]);
+                // the scores have been read: the next tile's may come
+                auto read = [&] {
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(s_free + 8 * r);
+                };
+                // the product before this one is done: O is at rest, and P's place is free (every phase of
+                // o_done is waited for, while the next cannot end)
+                bool settled = !some;
+                auto settle = [&] {
+                    if (!settled) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (count - 1) & 1, &stop, limit));
+                    settled = true;
+                    tc_after();
+                };
+                if (!busy) {
+                    read();
+                    settle();
+                } else {
+                    constexpr int C = KEYS / 32, REST = KEYS % 32;         // whole chunks of 32 columns, and 16 more
+                    static_assert(REST == 0 || REST == 16, "a half chunk");
+                    uint32_t x[C][32], z[16];
+#pragma unroll
+                    for (int c = 0; c < C; ++c) tc_ld_begin(x[c], s_at + 32 * c);
+                    if (REST) ld16(z, s_at + 32 * C);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) tc_ld_end(x[c]);
+                    read();
+                    auto at = [&](int e) -> uint32_t & { return e < 32 * C ? x[e / 32][e % 32] : z[e % 32]; };
                     if (!reach.all(i)) {
                         // columns that the row sees: up to `to`, and from behind `from` on or before `sinks`
                         const int v0 = i * KEYS, to = p - (v0 - U.r.sinks + U.r.lo), from = to - A.window, sinks = A.sinks - v0;
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const uint32_t see = below(to + 1 - 32 * c) & (~below(from + 1 - 32 * c) | below(sinks - 32 * c));
+                        for (int c = 0; c < KEYS; c += 32) {
+                            const uint32_t see = below(to + 1 - c) & (~below(from + 1 - c) | below(sinks - c));
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[c][e] = see >> e & 1u ? x[c][e] : 0xff800000u;
+                            for (int e = c; e < c + 32 && e < KEYS; ++e) at(e) = see >> (e - c) & 1u ? at(e) : 0xff800000u;
                         }
                     }
                     float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        const uint32_t *y = x[e / 32] + e % 32;
-                        t4[e / 2 & 3] = max_of(t4[e / 2 & 3], __uint_as_float(y[0]), __uint_as_float(y[1]));
-                    }
+                    for (int e = 0; e < KEYS; e += 2) t4[e / 2 & 3] = max_of(t4[e / 2 & 3], __uint_as_float(at(e)), __uint_as_float(at(e + 1)));
                     const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * A.scale_log2;      // (scale > 0 here)
                     // replace the maximum only when it grew by more than 2^8
                     const bool grew = top > m + 8.f || (m == -INFINITY && top > m);
@@ -853,43 +886,44 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                         l2[0] = fma_two(l2[0], two(f, f), 0);
                         l2[1] = fma_two(l2[1], two(f, f), 0);
                         if (some) {
-                            // the output so far, once the product before this one is in it
-                            ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (count - 1) & 1, &stop, limit));
+                            settle();
                             if (!ok) break;
-                            settled = true;
-                            tc_after();
 #pragma unroll 1
-                            for (int c = 0; c < DP / 32; ++c) {
-                                float o[32];
-                                uint32_t w[32];
-                                tc_ld(o, o_at + 32 * c);
+                            for (int c = 0; c < DP; c += 16) {
+                                uint32_t o[16];
+                                ld16(o, o_at + c);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
-                                tc_st(o_at + 32 * c, w);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                st16(o_at + c, o);
                             }
                         }
                     }
                     const float shift = m == -INFINITY ? 0.f : -m;
                     const uint64_t shift2 = two(shift, shift);
-                    uint32_t w[32];
 #pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        const uint32_t *y = x[e / 32] + e % 32;
-                        float2 f = apart(fma_two(two(__uint_as_float(y[0]), __uint_as_float(y[1])), scale2, shift2));
-                        f.x = pow2(f.x);
-                        f.y = pow2(f.y);
-                        l2[e / 2 & 1] = add_two(l2[e / 2 & 1], two(f.x, f.y));
-                        w[e / 2] = pack2<T>(f.x, f.y);
+                    for (int c = 0; c < KEYS; c += 32) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = c; e < c + 32 && e < KEYS; e += 2) {
+                            float2 f = apart(fma_two(two(__uint_as_float(at(e)), __uint_as_float(at(e + 1))), scale2, shift2));
+                            f.x = pow2(f.x);
+                            f.y = pow2(f.y);
+                            l2[e / 2 & 1] = add_two(l2[e / 2 & 1], two(f.x, f.y));
+                            w[(e - c) / 2] = pack2<T>(f.x, f.y);
+                        }
+                        if (c == 0) {
+                            settle();
+                            if (!ok) break;
+                        }
+                        if (KEYS - c >= 32) st16(p_at + c / 2, w);
+                        else st8(p_at + c / 2, w);
                     }
-                    tc_st(s_at + buf * KEYS, w);
-                    tc_wait_st();
+                    if (ok) tc_wait_st();
                 }
-                // (every phase of o_done is waited for while the next cannot end)
-                if (!settled) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (count - 1) & 1, &stop, limit));
                 if (!ok) break;
                 tc_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(p_full + 8 * (r * SB + buf));
+                if (lane == 0) bar_arrive(p_full + 8 * r);
                 ++count;
                 some = true;
             }
@@ -952,7 +986,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
             const bool is_v = warp > M::HELP;
             const uint32_t store = is_v ? sv : sk, full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
             const CUtensorMap *const map = is_v ? &maps.kv.v : &maps.kv.k;
-            const int boxes = KEYS / box;                                  // (boxes of 8 to 64 entries; 1 to 8 of them)
+            const int boxes = KEYS / box;                                  // (boxes of 8 to 64 entries; 1 to 12 of them)
             const uint32_t vain = vain_bytes(A.waits);
             int n = 0, nq[TILES] = {};
             bool ok = true;
@@ -1012,94 +1046,81 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
             constexpr uint32_t FMT = __is_same(T, __nv_bfloat16) ? 1u : 0u;
             constexpr uint32_t DESC = 1u << 4 | FMT << 7 | FMT << 10 | (128u >> 4) << 24;
             constexpr uint32_t DESC_S = DESC | (uint32_t)(KEYS >> 3) << 17, DESC_O = DESC | 1u << 16 | (uint32_t)(DP >> 3) << 17;
-            // (what the instructions take is the same in all lanes, and the compiler knows it)
-            auto same = [](uint32_t v) { return __shfl_sync(~0u, v, 0); };
-            const uint32_t qa = desc_lo(sq + r * M::Q, 16), k0 = desc_lo(sk, 16), va0 = desc_lo(sv, M::SUBK);
-            const uint32_t s_col = same(tmem + M::S_COL + r * SB * KEYS), o_col = same(tmem + M::O_COL + r * DP);
-            uint32_t fixes = 0;                                            // parity of v_fixed of a stage, a bit each
-            uint32_t k_st = 0, k_par = 0, v_st = 0, v_par = 0;             // stages of the next scores and outputs, and their barriers' parities
-            uint32_t scores = 0, done = 0, nq = 0;                         // score tiles, products and units
-            bool ok = true;
-            for (int u = u0; ok && u < C.units; u += step) {
-                const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
-                const Span span = span_of(U, C, r);
-                const Reach reach = reach_of<KEYS>(A, U.r, span);
-                const Idle idle = idle_of<KEYS>(A, U.r);
-                const int begin = (int)same((uint32_t)U.begin), end = (int)same((uint32_t)U.end);
-                uint32_t more = 0;                                         // O has a product of this unit
-                if (span.last >= 0) ok = __all_sync(~0u, bar_wait(q_full + 8 * r, nq++ & 1, &stop, limit));
-                // the scores of tile i + 1, then the outputs of tile i
-                for (int i = begin - 1; i < end && ok; ++i) {
-                    if (i + 1 < end) {
-                        const bool some = reach.some(i + 1);
-                        ok = bar_wait(k_full + 8 * k_st, k_par, &stop, limit);
-                        // the last product that was issued is done: P in these columns has been read, in the tile
-                        // before the last or earlier
-                        if (some && done > 0) ok = ok && bar_wait(o_done + 8 * r, (done - 1) & 1, &stop, limit);
-                        ok = __all_sync(~0u, ok);
-                        if (!ok) break;
-                        if (some) {
-                            const uint32_t d = s_col + (scores & 1) * KEYS, ka = k0 + k_st * (M::KV / 16);
-                            tc_after();
-                            if (elected()) {
+            const uint32_t qa = (sq + r * M::Q) >> 4 | 1u << 16, k0 = sk >> 4 | 1u << 16, v0 = sv >> 4 | (uint32_t)(M::SUBK / 16) << 16;
+            const uint32_t s_col = tmem + M::S_COL + r * KEYS, p_col = tmem + M::P_COL + r * KEYS / 2, o_col = tmem + M::O_COL + r * DP;
+            // One lane does it all: it is alone in what follows, so that nothing has to be agreed on
+            // between two instructions.
+            if (elected()) {
+                uint32_t fixes = 0;                                        // parity of v_fixed of a stage, a bit each
+                uint32_t k_st = 0, k_par = 0, v_st = 0, v_par = 0;         // stages of the next scores and outputs, and their barriers' parities
+                uint32_t scores = 0, done = 0, nq = 0;                     // score tiles, products and units
+                bool ok = true;
+                for (int u = u0; ok && u < C.units; u += step) {
+                    const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
+                    const Span span = span_of(U, C, r);
+                    const Reach reach = reach_of<KEYS>(A, U.r, span);
+                    const Idle idle = idle_of<KEYS>(A, U.r);
+                    uint32_t more = 0;                                     // O has a product of this unit
+                    if (span.last >= 0) ok = bar_wait(q_full + 8 * r, nq++ & 1, &stop, limit);
+                    // the scores of tile i + 1, then the outputs of tile i
+                    for (int i = U.begin - 1; i < U.end && ok; ++i) {
+                        if (i + 1 < U.end) {
+                            ok = bar_wait(k_full + 8 * k_st, k_par, &stop, limit);
+                            if (reach.some(i + 1)) {
+                                if (scores > 0) ok = ok && bar_wait(s_free + 8 * r, (scores - 1) & 1, &stop, limit);
+                                if (!ok) break;
+                                const uint32_t ka = k0 + k_st * (M::KV / 16);
+                                tc_after();
 #pragma unroll
                                 for (int k = 0; k < DP / 16; ++k)
-                                    tc_mma_ss(d, desc_of(qa + ((k >> 2) * M::SUBQ + (k & 3) * 32) / 16), desc_of(ka + ((k >> 2) * M::SUBK + (k & 3) * 32) / 16),
-                                              DESC_S, k > 0);
-                                tc_commit(s_full + 8 * (r * SB + (scores & 1)));
+                                    tc_mma_ss(s_col, desc_of(qa + ((k >> 2) * M::SUBQ + (k & 3) * 32) / 16),
+                                              desc_of(ka + ((k >> 2) * M::SUBK + (k & 3) * 32) / 16), DESC_S, k > 0);
+                                tc_commit(s_full + 8 * r);
                                 tc_commit(k_empty + 8 * k_st);
+                                ++scores;
+                            } else {
+                                if (!ok) break;
+                                bar_arrive(k_empty + 8 * k_st);
                             }
-                            ++scores;
-                        } else if (lane == 0) {
-                            bar_arrive(k_empty + 8 * k_st);
+                            if (++k_st == ST) {
+                                k_st = 0;
+                                k_par ^= 1;
+                            }
                         }
-                        __syncwarp();
-                        if (++k_st == ST) {
-                            k_st = 0;
-                            k_par ^= 1;
+                        if (span.last >= 0 && (i + 2 == U.end || U.begin == U.end)) tc_commit(q_empty + 8 * r);
+                        if (i < U.begin) continue;
+                        ok = bar_wait(v_full + 8 * v_st, v_par, &stop, limit);
+                        if (idle.any(i)) {
+                            ok = ok && bar_wait(v_fixed + 8 * v_st, fixes >> v_st & 1u, &stop, limit);
+                            fixes ^= 1u << v_st;
                         }
-                    }
-                    if (i + 2 == end || begin == end) {
-                        if (span.last >= 0 && elected()) tc_commit(q_empty + 8 * r);
-                        __syncwarp();
-                    }
-                    if (i < begin) continue;
-                    const bool some = reach.some(i), cleared = idle.any(i);
-                    const uint32_t buf = done & 1;
-                    ok = bar_wait(v_full + 8 * v_st, v_par, &stop, limit);
-                    if (cleared) {
-                        ok = ok && bar_wait(v_fixed + 8 * v_st, fixes >> v_st & 1u, &stop, limit);
-                        fixes ^= 1u << v_st;
-                    }
-                    if (some) ok = ok && bar_wait(p_full + 8 * (r * SB + buf), done >> 1 & 1, &stop, limit);
-                    ok = __all_sync(~0u, ok);
-                    if (!ok) break;
-                    if (some) {
-                        const uint32_t pa = s_col + buf * KEYS, va = va0 + v_st * (M::KV / 16);
-                        tc_after();
-                        if (elected()) {
+                        if (reach.some(i)) {
+                            ok = ok && bar_wait(p_full + 8 * r, done & 1, &stop, limit);
+                            if (!ok) break;
+                            const uint32_t va = v0 + v_st * (M::KV / 16);
+                            tc_after();
 #pragma unroll
-                            for (int k = 0; k < KEYS / 16; ++k) tc_mma_ts(o_col, pa + 8 * k, desc_of(va + k * 2048 / 16), DESC_O, k > 0 ? 1u : more);
+                            for (int k = 0; k < KEYS / 16; ++k) tc_mma_ts(o_col, p_col + 8 * k, desc_of(va + k * 2048 / 16), DESC_O, k > 0 ? 1u : more);
                             tc_commit(o_done + 8 * r);
                             tc_commit(v_empty + 8 * v_st);
+                            ++done;
+                            more = 1;
+                        } else {
+                            if (!ok) break;
+                            bar_arrive(v_empty + 8 * v_st);
                         }
-                        ++done;
-                        more = 1;
-                    } else if (lane == 0) {
-                        bar_arrive(v_empty + 8 * v_st);
-                    }
-                    __syncwarp();
-                    if (++v_st == ST) {
-                        v_st = 0;
-                        v_par ^= 1;
+                        if (++v_st == ST) {
+                            v_st = 0;
+                            v_par ^= 1;
+                        }
                     }
                 }
+                // products under way end before their memory is given back
+                tc_commit(last_bar);
+                int last = 0;
+                bar_wait(last_bar, 0, &last, limit);
             }
-            // products under way end before their memory is given back
-            if (elected()) tc_commit(last_bar);
             __syncwarp();
-            int last = 0;
-            bar_wait(last_bar, 0, &last, limit);
         } else if (warp == M::CLEAR) {
             // ---- clear what no row of the unit sees in V: copied with a box, or behind the line ----
             int n = 0;
@@ -1114,7 +1135,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                     if (idle.any(i)) {
                         for (int k0 = 0; k0 < KEYS; k0 += 32) {
                             const int v = i * KEYS + k0 + lane;
-                            unsigned clear = __ballot_sync(~0u, v >= U.r.n || !seen_by_any(A, U.r, U.r.real(v)));
+                            unsigned clear = __ballot_sync(~0u, k0 + lane < KEYS && (v >= U.r.n || !seen_by_any(A, U.r, U.r.real(v))));
                             for (; clear; clear &= clear - 1) {
                                 const uint32_t at = sv + st * M::KV + (k0 + __ffs(clear) - 1) * 128;
                                 if (lane < DP / 8)
@@ -1354,9 +1375,9 @@ dbs_status plan_of(const dbs_window_args &a, Plan &P)
     if (sms == 0) return DBS_ERR_CUDA;
     // Many rows of a kv head: 128 at a time, if K, V and Q can be copied as boxes (sinks and the
     // window's start round to them).
-    if (a.tokens * group > FEW_ROWS && group <= 128 && a.scale > 0 && make_maps(a, a.sinks > 0 ? 16 : 64, P.maps.kv) &&
+    if (a.tokens * group > FEW_ROWS && group <= 128 && a.scale > 0 && make_maps(a, a.sinks > 0 || dp == 128 ? 16 : dp == 256 ? 64 : 32, P.maps.kv) &&
         make_q_map(a, group, 128 / group, P.maps.q)) {
-        const int tiles = dp == 256 ? 1 : 2, keys = 64;
+        const int tiles = dp == 256 ? 1 : 2, keys = dp == 64 ? 96 : dp == 128 ? 80 : 64;
         Cut &C = P.cut;
         C.tokens = 128 / group;
         C.groups = (int)((a.tokens + tiles * C.tokens - 1) / (tiles * C.tokens));
