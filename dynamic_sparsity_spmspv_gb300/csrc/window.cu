@@ -174,11 +174,17 @@ __device__ __forceinline__ Range range_of(const Win &A, const Seq &s, int t0, in
         r.hi = 0;
         return r;
     }
-    r.lo = window_start(A, r.first) / grain * grain;
-    if (A.sinks < r.lo) r.sinks = (A.sinks + grain - 1) / grain * grain;
+    r.lo = window_start(A, r.first) & -grain;                              // (a power of two)
+    if (A.sinks < r.lo) r.sinks = (A.sinks + grain - 1) & -grain;
     if (A.sinks >= r.lo || r.sinks >= r.lo) r.sinks = r.lo = 0;
     r.n = r.sinks + r.hi - r.lo;
     return r;
+}
+
+// bar_wait, whose first look is all there is most of the time.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *stop, uint32_t limit)
+{
+    return __builtin_expect(bar_test(bar, parity), 1) || bar_wait(bar, parity, stop, limit);
 }
 
 // Whether all rows see the entries v .. v + size - 1 of the line, all of which it has.
@@ -652,8 +658,12 @@ __device__ __forceinline__ Unit unit_of(const Win &A, const Cut &C, int u, int r
     U.s = sequence(A, U.b);
     U.r = range_of(A, U.s, U.t0, U.t0 + TILES * C.tokens - 1, box);
     const int n = (U.r.n + KEYS - 1) / KEYS;
-    U.begin = (int)((int64_t)n * rank / C.split);
-    U.end = (int)((int64_t)n * (rank + 1) / C.split);
+    U.begin = 0;
+    U.end = n;
+    if (C.split > 1) {                                                     // (n < 2^26, split at most 16)
+        U.begin = n * rank / C.split;
+        U.end = n * (rank + 1) / C.split;
+    }
     return U;
 }
 
@@ -809,6 +819,9 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
     const uint32_t tmem = tmem_at;
     const int rank = C.split > 1 ? (int)(blockIdx.x % (uint32_t)C.split) : 0;
     const int u0 = (int)(blockIdx.x / (uint32_t)C.split), step = (int)(gridDim.x / (uint32_t)C.split), box = maps.kv.box;
+    // Rounds of a unit for each block, every second backwards: units get shorter, and the block that
+    // had the longest of one round has the shortest of the next.
+    auto unit_at = [&](int k) { return k * step + (k & 1 ? step - 1 - u0 : u0); };
     const uint32_t limit = A.waits.limit;
 
     if (warp < M::HELP) {
@@ -821,7 +834,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
         const uint64_t scale2 = two(A.scale_log2, A.scale_log2);
         int count = 0;                                                     // tiles done
         bool ok = true;
-        for (int u = u0; u < C.units; u += step) {
+        for (int k = 0, u; (u = unit_at(k)) < C.units; ++k) {
             const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
             const Reach reach = reach_of<KEYS>(A, U.r, span_of(U, C, r));
             const int t = U.t0 + r * C.tokens + dt, h = U.hk * A.group + dh;
@@ -833,7 +846,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
             bool some = false;
             for (int i = U.begin; ok && i < U.end; ++i) {
                 if (!reach.some(i)) continue;
-                ok = __all_sync(~0u, bar_wait(s_full + 8 * r, count & 1, &stop, limit));
+                ok = __all_sync(~0u, wait_for(s_full + 8 * r, count & 1, &stop, limit));
                 if (!ok) break;
                 tc_after();
                 // the scores have been read: the next tile's may come
@@ -846,7 +859,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                 // o_done is waited for, while the next cannot end)
                 bool settled = !some;
                 auto settle = [&] {
-                    if (!settled) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (count - 1) & 1, &stop, limit));
+                    if (!settled) ok = __all_sync(~0u, wait_for(o_done + 8 * r, (count - 1) & 1, &stop, limit));
                     settled = true;
                     tc_after();
                 };
@@ -883,8 +896,8 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                     if (__any_sync(~0u, grew)) {
                         const float f = grew ? (m == -INFINITY ? 0.f : exp2f(m - top)) : 1.f;
                         if (grew) m = top;
-                        l2[0] = fma_two(l2[0], two(f, f), 0);
-                        l2[1] = fma_two(l2[1], two(f, f), 0);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) l2[e] = fma_two(l2[e], two(f, f), 0);
                         if (some) {
                             settle();
                             if (!ok) break;
@@ -898,6 +911,8 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                             }
                         }
                     }
+                    settle();
+                    if (!ok) break;
                     const float shift = m == -INFINITY ? 0.f : -m;
                     const uint64_t shift2 = two(shift, shift);
 #pragma unroll
@@ -911,14 +926,10 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                             l2[e / 2 & 1] = add_two(l2[e / 2 & 1], two(f.x, f.y));
                             w[(e - c) / 2] = pack2<T>(f.x, f.y);
                         }
-                        if (c == 0) {
-                            settle();
-                            if (!ok) break;
-                        }
                         if (KEYS - c >= 32) st16(p_at + c / 2, w);
                         else st8(p_at + c / 2, w);
                     }
-                    if (ok) tc_wait_st();
+                    tc_wait_st();
                 }
                 if (!ok) break;
                 tc_before();
@@ -927,17 +938,17 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                 ++count;
                 some = true;
             }
-            const float2 la = apart(l2[0]), lb = apart(l2[1]);
-            const float l = (la.x + la.y) + (lb.x + lb.y);
+            const float2 lsum = apart(add_two(l2[0], l2[1]));
+            const float l = lsum.x + lsum.y;
             // the unit's (or the part's) output
-            if (ok && some) ok = __all_sync(~0u, bar_wait(o_done + 8 * r, (count - 1) & 1, &stop, limit));
+            if (ok && some) ok = __all_sync(~0u, wait_for(o_done + 8 * r, (count - 1) & 1, &stop, limit));
             tc_after();
             const float nan = nanf("");
             const bool none = p < 0 || l == 0.f, whole = C.split == 1;
             const float by = !ok ? nan : !whole ? 1.f : none ? 0.f : 1.f / l;
             float *const part = whole ? nullptr : part_of<DP, TILES>(C, u, rank);
             T *out = (T *)a.out + U.b * a.o_batch + t * a.o_token + h * a.o_head;
-            bool odd = false;
+            float odd = 0.f;                                               // NaN once a value was not finite
             if (busy)
 #pragma unroll 1
                 for (int c = 0; c < DP / 32; ++c) {
@@ -955,7 +966,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                             continue;
                         }
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) odd |= !isfinite(v[e + k]);
+                        for (int k = 0; k < 8; ++k) odd = fmaf(v[e + k], 0.f, odd);
                         if (A.wide_out) {
                             *(uint4 *)(out + d) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]), pack2<T>(v[e + 4], v[e + 5]),
                                                              pack2<T>(v[e + 6], v[e + 7]));
@@ -972,7 +983,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
             } else if (inside && a.lse) {
                 a.lse[(U.b * a.tokens + t) * a.q_heads + h] = !ok ? nan : none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             }
-            for (unsigned again = __ballot_sync(~0u, odd && ok && l == l); again; again &= again - 1) {
+            for (unsigned again = __ballot_sync(~0u, odd != odd && ok && l == l); again; again &= again - 1) {
                 const int k = __ffs(again) - 1, tk = __shfl_sync(~0u, t, k), hh = __shfl_sync(~0u, h, k);
                 float ol[8], m1, l1;
                 row_by_warp<T>(A, U.s, U.b, tk, hh, 0, 1, m1, l1, ol);
@@ -990,7 +1001,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
             const uint32_t vain = vain_bytes(A.waits);
             int n = 0, nq[TILES] = {};
             bool ok = true;
-            for (int u = u0; ok && u < C.units; u += step) {
+            for (int k = 0, u; ok && (u = unit_at(k)) < C.units; ++k) {
                 const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
                 if (!is_v)
 #pragma unroll
@@ -1055,7 +1066,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                 uint32_t k_st = 0, k_par = 0, v_st = 0, v_par = 0;         // stages of the next scores and outputs, and their barriers' parities
                 uint32_t scores = 0, done = 0, nq = 0;                     // score tiles, products and units
                 bool ok = true;
-                for (int u = u0; ok && u < C.units; u += step) {
+                for (int k = 0, u; ok && (u = unit_at(k)) < C.units; ++k) {
                     const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
                     const Span span = span_of(U, C, r);
                     const Reach reach = reach_of<KEYS>(A, U.r, span);
@@ -1065,9 +1076,9 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                     // the scores of tile i + 1, then the outputs of tile i
                     for (int i = U.begin - 1; i < U.end && ok; ++i) {
                         if (i + 1 < U.end) {
-                            ok = bar_wait(k_full + 8 * k_st, k_par, &stop, limit);
+                            ok = wait_for(k_full + 8 * k_st, k_par, &stop, limit);
                             if (reach.some(i + 1)) {
-                                if (scores > 0) ok = ok && bar_wait(s_free + 8 * r, (scores - 1) & 1, &stop, limit);
+                                if (scores > 0) ok = ok && wait_for(s_free + 8 * r, (scores - 1) & 1, &stop, limit);
                                 if (!ok) break;
                                 const uint32_t ka = k0 + k_st * (M::KV / 16);
                                 tc_after();
@@ -1089,13 +1100,13 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                         }
                         if (span.last >= 0 && (i + 2 == U.end || U.begin == U.end)) tc_commit(q_empty + 8 * r);
                         if (i < U.begin) continue;
-                        ok = bar_wait(v_full + 8 * v_st, v_par, &stop, limit);
+                        ok = wait_for(v_full + 8 * v_st, v_par, &stop, limit);
                         if (idle.any(i)) {
                             ok = ok && bar_wait(v_fixed + 8 * v_st, fixes >> v_st & 1u, &stop, limit);
                             fixes ^= 1u << v_st;
                         }
                         if (reach.some(i)) {
-                            ok = ok && bar_wait(p_full + 8 * r, done & 1, &stop, limit);
+                            ok = ok && wait_for(p_full + 8 * r, done & 1, &stop, limit);
                             if (!ok) break;
                             const uint32_t va = v0 + v_st * (M::KV / 16);
                             tc_after();
@@ -1125,7 +1136,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
             // ---- clear what no row of the unit sees in V: copied with a box, or behind the line ----
             int n = 0;
             bool ok = true;
-            for (int u = u0; ok && u < C.units; u += step) {
+            for (int k = 0, u; ok && (u = unit_at(k)) < C.units; ++k) {
                 const Unit U = unit_of<KEYS, TILES>(A, C, u, rank, box);
                 const Idle idle = idle_of<KEYS>(A, U.r);
                 for (int i = U.begin; i < U.end && ok; ++i, ++n) {
