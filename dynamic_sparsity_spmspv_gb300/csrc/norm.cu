@@ -9,52 +9,76 @@ using namespace dbs::ops;
 namespace {
 
 constexpr int NT = 256;
+// Blocks of a multiprocessor and heads whose loads are issued together, for heads of one unit a lane
+// (16,382 tokens of 40 heads of 128, bf16: 3 and 2 71 us, 2 and 4 81, 4 and 1 78; the gradient of 8192
+// tokens of 32 heads of 96, f32: 2 and 2 69 us, 3 and 1 79).
+constexpr int FORWARD_BLOCKS = 3, FORWARD_HEADS = 2, BACKWARD_BLOCKS = 2, BACKWARD_HEADS = 2;
 
-// A unit of a head is what one lane holds of it: two vectors of N values at `a` and
-// `b`.  Of the turned entries they are the halves of N pairs, or, interleaved, N
-// pairs one after another (the second vector is missing where the entries end); of
-// the rest two vectors in a row.  A head is spread over L lanes of a warp (a power of
-// two), K units each, so its sums need log2 L exchanges and no shared memory, and a
-// head is read once.
+// What a lane moves at once: N values, 16 or 8 bytes, or one where rows are not aligned for that.
+template <class T, int N> struct Piece {
+    using type = uint4;
+};
+template <class T> struct Piece<T, 1> {
+    using type = typename Vec<T, false>::type;
+};
+template <> struct Piece<__half, 4> {
+    using type = uint2;
+};
+template <> struct Piece<__nv_bfloat16, 4> {
+    using type = uint2;
+};
+using dbs::ops::open;
+using dbs::ops::shut;
+template <class T> __device__ __forceinline__ void open(const uint2 &w, float (&v)[4])
+{
+    open2<T>(w.x, v, 0);
+    open2<T>(w.y, v, 1);
+}
+template <class T> __device__ __forceinline__ void shut(const float (&v)[4], uint2 &w) { w = make_uint2(shut2<T>(v, 0), shut2<T>(v, 1)); }
+
+// A unit of a head is what one lane holds of it: two pieces, `a` and `b`.  Of the turned entries
+// they are the halves of N pairs, or, interleaved, a piece of pairs from the first half of the
+// turned entries and one from the second (none where their number is odd); of the rest likewise one
+// from each half.  So the lanes of each access are neighbours in memory (with both pieces in a row an
+// access has half of each sector).  A head is
+// spread over L lanes of a warp (a power of two), K units each: its sums need log2 L exchanges and no shared
+// memory, and it is read once.
 struct Head {
     int head_dim, dim;
-    int units, turned;                 // of a head; of its turned entries
+    int units, turned, rest;           // of a head, of its turned entries, of the others
     int lanes;                         // L
+    float part;                        // 1 / head_dim
 };
 
-template <class T, bool INTERLEAVED, bool WIDE> struct Unit {
-    static constexpr int N = Vec<T, WIDE>::n;
-    static constexpr bool RUNS = INTERLEAVED && WIDE;      // pairs within a vector
+template <class T, bool INTERLEAVED, int N> struct Unit {
+    static constexpr bool RUNS = INTERLEAVED && N > 1;     // pairs within a piece
     int a, b;
     bool some, both, turned;
-    int pair;                                              // first of its N pairs
     __device__ __forceinline__ Unit(const Head &H, int c)
     {
         some = c < H.units;
         turned = c < H.turned;
-        pair = c * N;
-        const int r = H.dim + 2 * (c - H.turned) * N;
-        a = !turned ? r : INTERLEAVED ? 2 * c * N : c * N;
-        b = !turned || RUNS ? a + N : INTERLEAVED ? a + 1 : a + H.dim / 2;
+        const int r = c - H.turned;
+        a = !turned ? H.dim + r * N : INTERLEAVED && N == 1 ? 2 * c : c * N;
+        b = !turned ? a + H.rest * N : RUNS ? a + H.turned * N : INTERLEAVED ? a + 1 : a + H.dim / 2;
         both = some && b < (turned ? H.dim : H.head_dim);
     }
+    // The pair whose angle value e of the N is (of pairs within pieces: half of them in each).
+    __device__ __forceinline__ int pair(int e) const { return RUNS ? (e < N / 2 ? a / 2 + e : b / 2 + e - N / 2) : INTERLEAVED ? a / 2 : a + e; }
 };
 
-template <class T, bool INTERLEAVED, bool WIDE> Head head_of(int head_dim, int dim)
+template <int N> Head head_of(int head_dim, int dim)
 {
-    constexpr int N = Vec<T, WIDE>::n;
-    Head H{head_dim, dim, 0, 0, 1};
-    H.turned = (dim + 2 * N - 1) / (2 * N);
-    H.units = H.turned + (head_dim - dim + 2 * N - 1) / (2 * N);
+    Head H{head_dim, dim, 0, (dim / N + 1) / 2, ((head_dim - dim) / N + 1) / 2, 1, 1.f / (float)head_dim};
+    H.units = H.turned + H.rest;
     while (H.lanes < 32 && H.lanes < H.units) H.lanes *= 2;
     return H;
 }
 
-template <class T, bool INTERLEAVED, bool WIDE, int K> struct Lane {
-    using V = Vec<T, WIDE>;
-    using VT = typename V::type;
-    static constexpr int N = V::n, F = !WIDE ? 1 : N < 4 ? N : 4;
-    using U = Unit<T, INTERLEAVED, WIDE>;
+template <class T, bool INTERLEAVED, int N, int K> struct Lane {
+    using VT = typename Piece<T, N>::type;
+    using U = Unit<T, INTERLEAVED, N>;
+    static constexpr int RUN = U::RUNS ? N / 2 : N, F = RUN < 4 ? RUN : 4;     // angles in a row, of one load
 
     // The units' cosines and sines (1 and 0 of what is not turned).
     static __device__ __forceinline__ void angles(const Head &H, int lane, const float *table, int64_t rows, int64_t pos, float sign,
@@ -71,9 +95,9 @@ template <class T, bool INTERLEAVED, bool WIDE, int K> struct Lane {
                     float v[F];
                 };
                 Floats c4, s4;
-                const bool in = u.turned && u.pair + q < half;
+                const bool in = u.turned && (q < RUN || u.both);
                 if (in && ok) {
-                    const float *row = table + pos * H.dim + u.pair + q;
+                    const float *row = table + pos * H.dim + u.pair(q);
                     c4 = *(const Floats *)row;
                     s4 = *(const Floats *)(row + half);
                 }
@@ -85,8 +109,16 @@ template <class T, bool INTERLEAVED, bool WIDE, int K> struct Lane {
             }
         }
     }
-    static __device__ __forceinline__ void weights(const Head &H, int lane, const void *w, dbs_dtype type, float (&v)[K][2 * N])
+    // (`vectors`: the weight is of the heads' type and on 16-byte boundaries)
+    static __device__ __forceinline__ void weights(const Head &H, int lane, const void *w, dbs_dtype type, bool vectors, float (&v)[K][2 * N])
     {
+        if (N > 1 && vectors) {
+            VT x[K][2];
+            load(H, lane, (const T *)w, x);
+#pragma unroll
+            for (int k = 0; k < K; ++k) opened(x[k], v[k]);
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const U u(H, lane + k * H.lanes);
@@ -131,9 +163,27 @@ template <class T, bool INTERLEAVED, bool WIDE, int K> struct Lane {
             v[N + e] = b[e];
         }
     }
-    static __device__ __forceinline__ void closed(const float (&v)[2 * N], VT (&x)[2])
+    // A unit's values two by two, so that an instruction works on two: N words.
+    static __device__ __forceinline__ void paired(const float (&v)[2 * N], uint64_t (&p)[N])
     {
-        float a[N], b[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) p[j] = two(v[2 * j], v[2 * j + 1]);
+    }
+    static __device__ __forceinline__ void opened(const VT (&x)[2], uint64_t (&p)[N])
+    {
+        float v[2 * N];
+        opened(x, v);
+        paired(v, p);
+    }
+    static __device__ __forceinline__ void closed(const uint64_t (&p)[N], VT (&x)[2])
+    {
+        float v[2 * N], a[N], b[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float2 f = apart(p[j]);
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+        }
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             a[e] = v[e];
@@ -142,16 +192,51 @@ template <class T, bool INTERLEAVED, bool WIDE, int K> struct Lane {
         shut<T>(a, x[0]);
         shut<T>(b, x[1]);
     }
-    // (a, b) of every pair becomes (a cos - b sin, a sin + b cos)
-    static __device__ __forceinline__ void turn(float (&v)[2 * N], const float (&cs)[N], const float (&sn)[N])
+    // What every value (of a pair that turns) takes of itself and of its partner: (a, b) becomes
+    // (a wa cos - b wb sin, a wa sin + b wb cos).
+    static constexpr bool WITHIN = U::RUNS || N == 1;      // a word holds both of a pair
+    static __device__ __forceinline__ void turns(const float (&cs)[N], const float (&sn)[N], const float (&w)[2 * N], uint64_t (&own)[N], uint64_t (&other)[N])
     {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            float &a = U::RUNS ? v[2 * e] : v[e], &b = U::RUNS ? v[2 * e + 1] : v[N + e];
-            const float a0 = a, b0 = b;
-            a = a0 * cs[e] - b0 * sn[e];
-            b = a0 * sn[e] + b0 * cs[e];
+        for (int j = 0; j < N; ++j) {
+            const int e = 2 * j;
+            if (WITHIN) {
+                own[j] = two(cs[j] * w[e], cs[j] * w[e + 1]);
+                other[j] = two(-sn[j] * w[e + 1], sn[j] * w[e]);
+            } else if (e < N) {
+                own[j] = two(cs[e] * w[e], cs[e + 1] * w[e + 1]);
+                other[j] = two(-sn[e] * w[N + e], -sn[e + 1] * w[N + e + 1]);
+            } else {
+                own[j] = two(cs[e - N] * w[e], cs[e - N + 1] * w[e + 1]);
+                other[j] = two(sn[e - N] * w[e - N], sn[e - N + 1] * w[e - N + 1]);
+            }
         }
+    }
+    // (what is not turned takes nothing of others, whatever they hold)
+    static __device__ __forceinline__ void turn(uint64_t (&p)[N], const uint64_t (&own)[N], const uint64_t (&other)[N], bool turned)
+    {
+        uint64_t q[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) q[j] = mul_two(p[j], own[j]);
+        if (turned)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float2 f = apart(p[j]);
+                q[j] = fma_two(WITHIN ? two(f.y, f.x) : p[(j + N / 2) % N], other[j], q[j]);
+            }
+#pragma unroll
+        for (int j = 0; j < N; ++j) p[j] = q[j];
+    }
+    static __device__ __forceinline__ float both(uint64_t v)
+    {
+        const float2 f = apart(v);
+        return f.x + f.y;
+    }
+    // (mean + eps)^(-1/2), the function's value with one step of Newton's method
+    static __device__ __forceinline__ float root(const Head &H, float sum, float eps)
+    {
+        const float v = fmaf(sum, H.part, eps), r = rsqrtf(v), better = r * fmaf(-0.5f * v * r, r, 1.5f);
+        return better == better ? better : r;              // (0 and infinity have no step)
     }
     // (every lane of the warp takes part; each head's lanes get their own sum)
     static __device__ __forceinline__ float sum(const Head &H, float v)
@@ -165,6 +250,7 @@ template <class T, bool INTERLEAVED, bool WIDE, int K> struct Lane {
 
 struct Norm {
     dbs_norm_heads part[3];
+    bool vectors[3];                   // of the weights
     int32_t nparts;
     Head head, copy;                   // of the groups that are normed, and copied
     int64_t tokens, total;             // tokens of a sequence, tokens of all
@@ -179,11 +265,11 @@ struct Norm {
 // lanes each.  A group of lanes keeps its token's angles and its weights for up to
 // `span` heads, HEADS of whose loads are issued together.  Bound by HBM: every entry is
 // read and written once.
-template <class T, bool INTERLEAVED, bool WIDE, int K>
-__global__ void __launch_bounds__(NT) k_norm_rotary(Norm A, int span)
+template <class T, bool INTERLEAVED, int N, int K>
+__global__ void __launch_bounds__(NT, K == 1 ? FORWARD_BLOCKS : 1) k_norm_rotary(Norm A, int span)
 {
-    using L = Lane<T, INTERLEAVED, WIDE, K>;
-    constexpr int N = L::N, HEADS = K == 1 ? 4 : 1;
+    using L = Lane<T, INTERLEAVED, N, K>;
+    constexpr int HEADS = K == 1 ? FORWARD_HEADS : 1;
     int y = blockIdx.y, p = 0;
     for (;; ++p) {
         const int chunks = (A.part[p].heads.heads + span - 1) / span;
@@ -210,48 +296,56 @@ __global__ void __launch_bounds__(NT) k_norm_rotary(Norm A, int span)
     } else {
         dst += b * P.out_batch + t * P.out_token;
     }
-    float cs[K][N], sn[K][N], w[K][2 * N];
-    if (norm) {
-        L::angles(H, lane, A.table, A.table_rows, H.dim && in ? A.positions[tok] : 0, 1.f, cs, sn);
-        L::weights(H, lane, A.part[p].weight, A.part[p].weight_dtype, w);
-    }
-    for (int h = 0; h < heads; h += HEADS) {
-        typename L::VT x[HEADS][K][2];
+    typename L::VT x[HEADS][K][2];
+    auto fetch = [&](int h) {
 #pragma unroll
         for (int k = 0; k < HEADS; ++k)
             if (h + k < heads) L::load(H, lane, src + k * P.in_head, x[k]);
+        src += HEADS * P.in_head;
+    };
+    fetch(0);
+    uint64_t own[K][N], other[K][N];
+    if (norm) {
+        float cs[K][N], sn[K][N], w[K][2 * N];
+        L::angles(H, lane, A.table, A.table_rows, H.dim && in ? A.positions[tok] : 0, 1.f, cs, sn);
+        L::weights(H, lane, A.part[p].weight, A.part[p].weight_dtype, A.vectors[p], w);
+#pragma unroll
+        for (int c = 0; c < K; ++c) L::turns(cs[c], sn[c], w[c], own[c], other[c]);
+    }
+    for (int h = 0; h < heads; h += HEADS) {
+        if (h) fetch(h);
 #pragma unroll
         for (int k = 0; k < HEADS; ++k) {
             if (h + k >= heads) break;
             if (norm) {
-                float v[K][2 * N], ss = 0.f;
+                uint64_t v[K][N], ss = 0;
 #pragma unroll
                 for (int c = 0; c < K; ++c) {
                     L::opened(x[k][c], v[c]);
 #pragma unroll
-                    for (int e = 0; e < 2 * N; ++e) ss = fmaf(v[c][e], v[c][e], ss);
+                    for (int j = 0; j < N; ++j) ss = fma_two(v[c][j], v[c][j], ss);
                 }
-                const float r = 1.f / sqrtf(L::sum(H, ss) / (float)H.head_dim + A.eps);
+                const float r = L::root(H, L::sum(H, L::both(ss)), A.eps);
+                const uint64_t r2 = two(r, r);
 #pragma unroll
                 for (int c = 0; c < K; ++c) {
 #pragma unroll
-                    for (int e = 0; e < 2 * N; ++e) v[c][e] = v[c][e] * r * w[c][e];
-                    L::turn(v[c], cs[c], sn[c]);
+                    for (int j = 0; j < N; ++j) v[c][j] = mul_two(v[c][j], r2);
+                    L::turn(v[c], own[c], other[c], lane + c * H.lanes < H.turned);
                     L::closed(v[c], x[k][c]);
                 }
             }
             if (write) L::store(H, lane, dst + k * P.out_head, x[k]);
         }
-        src += HEADS * P.in_head;
         dst += HEADS * P.out_head;
     }
 }
 
-template <class T, bool INTERLEAVED, bool WIDE, int K>
+template <class T, bool INTERLEAVED, int N, int K>
 dbs_status launch_norm(Norm &A, int head_dim, int dim, cudaStream_t s)
 {
-    A.head = head_of<T, INTERLEAVED, WIDE>(head_dim, dim);
-    A.copy = head_of<T, INTERLEAVED, WIDE>(head_dim, 0);
+    A.head = head_of<N>(head_dim, dim);
+    A.copy = head_of<N>(head_dim, 0);
     const int lanes = A.head.lanes > A.copy.lanes ? A.head.lanes : A.copy.lanes;
     const int64_t room = (int64_t)multiprocessors() * 2048;
     if (room == 0) return DBS_ERR_CUDA;
@@ -263,7 +357,7 @@ dbs_status launch_norm(Norm &A, int head_dim, int dim, cudaStream_t s)
         for (int p = 0; p < A.nparts; ++p) chunks += (A.part[p].heads.heads + span - 1) / span;
         if (span == 1 || A.total * lanes * chunks >= room || 2 * chunks > 65535) break;
     }
-    k_norm_rotary<T, INTERLEAVED, WIDE, K><<<dim3((unsigned)((A.total * lanes + NT - 1) / NT), (unsigned)chunks), NT, 0, s>>>(A, span);
+    k_norm_rotary<T, INTERLEAVED, N, K><<<dim3((unsigned)((A.total * lanes + NT - 1) / NT), (unsigned)chunks), NT, 0, s>>>(A, span);
     return launched();
 }
 
@@ -271,6 +365,7 @@ dbs_status launch_norm(Norm &A, int head_dim, int dim, cudaStream_t s)
 
 struct Gradient {
     dbs_norm_gradient_heads part[2];
+    bool vectors[2];
     int32_t nparts, blocks[2];         // blocks of each group of heads
     Head head;
     int64_t tokens, total;
@@ -286,11 +381,11 @@ struct Gradient {
 // the grid's turn; what the heads give to weight' stays in its registers.  In the end the block's
 // groups are added up in their order and written to scratch, and k_norm_weight adds the blocks.
 // Bound by HBM: two entries are read and one is written.
-template <class T, bool INTERLEAVED, bool WIDE, int K>
-__global__ void __launch_bounds__(NT) k_norm_gradient(Gradient A, int span)
+template <class T, bool INTERLEAVED, int N, int K>
+__global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradient(Gradient A, int span)
 {
-    using L = Lane<T, INTERLEAVED, WIDE, K>;
-    constexpr int N = L::N, HEADS = K == 1 ? 2 : 1;
+    using L = Lane<T, INTERLEAVED, N, K>;
+    constexpr int HEADS = K == 1 ? BACKWARD_HEADS : 1;
     extern __shared__ float sums[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int p = (int)blockIdx.x >= A.blocks[0], block = (int)blockIdx.x - (p ? A.blocks[0] : 0);
@@ -301,63 +396,78 @@ __global__ void __launch_bounds__(NT) k_norm_gradient(Gradient A, int span)
     const int64_t items = A.total * chunks, step = (int64_t)A.blocks[p] * groups;
     // (all lanes of a warp go the same number of turns)
     const int first = (threadIdx.x & ~31) / H.lanes;
-    float w[K][2 * N], dw[K][2 * N];
-    L::weights(H, lane, P.weight, P.weight_dtype, w);
+    uint64_t w[K][N], dw[K][N];
+    {
+        float f[K][2 * N];
+        L::weights(H, lane, P.weight, P.weight_dtype, A.vectors[p], f);
 #pragma unroll
-    for (int c = 0; c < K; ++c)
+        for (int c = 0; c < K; ++c) {
+            L::paired(f[c], w[c]);
 #pragma unroll
-        for (int e = 0; e < 2 * N; ++e) dw[c][e] = 0.f;
+            for (int j = 0; j < N; ++j) dw[c][j] = 0;
+        }
+    }
     for (int64_t i0 = (int64_t)block * groups + first; i0 < items; i0 += step) {
         const int64_t i = i0 + (group - first);
         const bool in = i < items;
         const uint32_t tok = in ? (uint32_t)(i / chunks) : 0u, chunk = in ? (uint32_t)(i - (int64_t)tok * chunks) : 0u;
         const uint32_t b = tok / (uint32_t)A.tokens, t = tok - b * (uint32_t)A.tokens;
         const int h0 = (int)chunk * span, heads = P.heads - h0 < span ? P.heads - h0 : span;
-        float cs[K][N], sn[K][N];
-        L::angles(H, lane, A.table, A.table_rows, H.dim ? A.positions[tok] : 0, -1.f, cs, sn);
         const T *g = (const T *)P.grad + b * P.grad_batch + t * P.grad_token + h0 * P.grad_head;
         const T *x = (const T *)P.in + b * P.in_batch + t * P.in_token + h0 * P.in_head;
         T *out = (T *)P.out + b * P.out_batch + t * P.out_token + h0 * P.out_head;
-        for (int h = 0; h < span; h += HEADS) {
-            typename L::VT gv[HEADS][K][2], xv[HEADS][K][2];
+        typename L::VT gv[HEADS][K][2], xv[HEADS][K][2];
+        auto fetch = [&](int h) {
 #pragma unroll
             for (int k = 0; k < HEADS; ++k)
                 if (in && h + k < heads) {
                     L::load(H, lane, g + k * P.grad_head, gv[k]);
                     L::load(H, lane, x + k * P.in_head, xv[k]);
                 }
+            g += HEADS * P.grad_head;
+            x += HEADS * P.in_head;
+        };
+        fetch(0);
+        uint64_t own[K][N], other[K][N];
+        {
+            float cs[K][N], sn[K][N], ones[2 * N];
+            L::angles(H, lane, A.table, A.table_rows, H.dim ? A.positions[tok] : 0, -1.f, cs, sn);
+#pragma unroll
+            for (int e = 0; e < 2 * N; ++e) ones[e] = 1.f;
+#pragma unroll
+            for (int c = 0; c < K; ++c) L::turns(cs[c], sn[c], ones, own[c], other[c]);
+        }
+        for (int h = 0; h < span; h += HEADS) {
+            if (h) fetch(h);
 #pragma unroll
             for (int k = 0; k < HEADS; ++k) {
                 const bool live = in && h + k < heads;
-                float gf[K][2 * N], xf[K][2 * N], ss = 0.f, dot = 0.f;
+                uint64_t gf[K][N], xf[K][N], ss = 0, dot = 0;
 #pragma unroll
                 for (int c = 0; c < K; ++c) {
                     L::opened(gv[k][c], gf[c]);
                     L::opened(xv[k][c], xf[c]);
-                    L::turn(gf[c], cs[c], sn[c]);
+                    L::turn(gf[c], own[c], other[c], lane + c * H.lanes < H.turned);
 #pragma unroll
-                    for (int e = 0; e < 2 * N; ++e) {
-                        ss = fmaf(xf[c][e], xf[c][e], ss);
-                        dot = fmaf(w[c][e] * gf[c][e], xf[c][e], dot);
+                    for (int j = 0; j < N; ++j) {
+                        ss = fma_two(xf[c][j], xf[c][j], ss);
+                        dot = fma_two(mul_two(w[c][j], gf[c][j]), xf[c][j], dot);
                     }
                 }
-                ss = L::sum(H, ss);
-                dot = L::sum(H, dot);
-                const float r = 1.f / sqrtf(ss / (float)H.head_dim + A.eps), f = dot * r * r / (float)H.head_dim;
+                const float r = L::root(H, L::sum(H, L::both(ss)), A.eps), f = -L::sum(H, L::both(dot)) * r * r * H.part;
                 if (!live) continue;
+                const uint64_t r2 = two(r, r), f2 = two(f, f);
 #pragma unroll
                 for (int c = 0; c < K; ++c) {
 #pragma unroll
-                    for (int e = 0; e < 2 * N; ++e) {
-                        dw[c][e] = fmaf(gf[c][e], xf[c][e] * r, dw[c][e]);
-                        gf[c][e] = r * (w[c][e] * gf[c][e] - xf[c][e] * f);
+                    for (int j = 0; j < N; ++j) {
+                        dw[c][j] = fma_two(gf[c][j], mul_two(xf[c][j], r2), dw[c][j]);
+                        gf[c][j] = mul_two(r2, fma_two(xf[c][j], f2, mul_two(w[c][j], gf[c][j])));
                     }
                     L::closed(gf[c], gv[k][c]);
                 }
                 L::store(H, lane, out + k * P.out_head, gv[k]);
             }
-            g += HEADS * P.grad_head;
-            x += HEADS * P.in_head;
             out += HEADS * P.out_head;
         }
     }
@@ -366,8 +476,10 @@ __global__ void __launch_bounds__(NT) k_norm_gradient(Gradient A, int span)
     for (int c = 0; c < K; ++c) {
         const typename L::U u(H, lane + c * H.lanes);
 #pragma unroll
-        for (int e = 0; e < 2 * N; ++e)
-            if (e < N ? u.some : u.both) sums[group * H.head_dim + (e < N ? u.a + e : u.b + e - N)] = dw[c][e];
+        for (int e = 0; e < 2 * N; ++e) {
+            const float2 f = apart(dw[c][e / 2]);
+            if (e < N ? u.some : u.both) sums[group * H.head_dim + (e < N ? u.a + e : u.b + e - N)] = e & 1 ? f.y : f.x;
+        }
     }
     __syncthreads();
     for (int d = threadIdx.x; d < H.head_dim; d += NT) {
@@ -388,7 +500,7 @@ __global__ void __launch_bounds__(1024) k_norm_weight(Gradient A, int head_dim)
     const float *from = A.scratch + (int64_t)blockIdx.y * A.room * head_dim;
     float s = 0.f;
     if (d < head_dim)
-#pragma unroll 4
+#pragma unroll 16
         for (int k = warp; k < A.blocks[blockIdx.y]; k += 32) s += __ldcg(from + (int64_t)k * head_dim + d);
     part[warp][lane] = s;
     __syncthreads();
@@ -400,15 +512,14 @@ __global__ void __launch_bounds__(1024) k_norm_weight(Gradient A, int head_dim)
     }
 }
 
-constexpr int GRADIENT_BLOCKS = 4;     // of a multiprocessor, at most
 
-template <class T, bool INTERLEAVED, bool WIDE, int K>
+template <class T, bool INTERLEAVED, int N, int K>
 dbs_status launch_gradient(Gradient &A, int head_dim, int dim, cudaStream_t s)
 {
-    A.head = head_of<T, INTERLEAVED, WIDE>(head_dim, dim);
+    A.head = head_of<N>(head_dim, dim);
     const int sms = multiprocessors(), groups = NT / A.head.lanes;
     if (sms == 0) return DBS_ERR_CUDA;
-    A.room = sms * GRADIENT_BLOCKS;
+    A.room = sms * BACKWARD_BLOCKS;
     // Heads of a turn: as for the forward pass
     int span = 8;
     int64_t heads = 0;
@@ -430,7 +541,7 @@ dbs_status launch_gradient(Gradient &A, int head_dim, int dim, cudaStream_t s)
     }
     if (blocks) {
         const int smem = groups * head_dim * (int)sizeof(float);
-        k_norm_gradient<T, INTERLEAVED, WIDE, K><<<blocks, NT, smem, s>>>(A, span);
+        k_norm_gradient<T, INTERLEAVED, N, K><<<blocks, NT, smem, s>>>(A, span);
         const dbs_status st = launched();
         if (st != DBS_OK) return st;
     }
@@ -447,60 +558,65 @@ dbs_status launch_gradient(Gradient &A, int head_dim, int dim, cudaStream_t s)
     return cudaLaunchKernelEx(&c, k_norm_weight, A, head_dim) == cudaSuccess ? DBS_OK : (cudaGetLastError(), DBS_ERR_CUDA);
 }
 
-// 16-byte accesses: every head on such a boundary, and whole vectors in each part of a head.
-template <class T> bool whole_vectors(int head_dim, int dim, bool interleaved, const float *table)
+// Pieces of N values: every head on such a boundary, and whole pieces in each part of a head.
+template <int N> bool whole_pieces(int head_dim, int dim, bool interleaved, const float *table)
 {
-    constexpr int N = 16 / (int)sizeof(T);
     return dim % (interleaved ? N : 2 * N) == 0 && head_dim % N == 0 && aligned16(table);
 }
-template <class T> bool on_vectors(const void *p, int64_t b, int64_t t, int64_t h)
+template <class T, int N> bool on_pieces(const void *p, int64_t b, int64_t t, int64_t h)
 {
-    constexpr int N = 16 / (int)sizeof(T);
-    return aligned16(p) && ((b | t | h) & (N - 1)) == 0;
+    return (reinterpret_cast<uintptr_t>(p) & (N * sizeof(T) - 1)) == 0 && ((b | t | h) & (N - 1)) == 0;
 }
 
-// The kernel for a head's size: units of a lane.
-template <class T, bool INTERLEAVED, class A>
-dbs_status choose(A &a, int head_dim, int dim, bool wide, cudaStream_t s, dbs_status (*const (&launch)[4])(A &, int, int, cudaStream_t))
-{
-    const int units = wide ? head_of<T, INTERLEAVED, true>(head_dim, dim).units : head_of<T, INTERLEAVED, false>(head_dim, dim).units;
-    if (wide) return launch[units <= 32 ? 0 : 1](a, head_dim, dim, s);
-    return launch[units <= 128 ? 2 : 3](a, head_dim, dim, s);
-}
+// Values of a piece.  Forward 16 bytes of them.  The gradient holds twice as much of a head
+// beside its weights and their sums, so it takes half as many of 16 bits.
+template <class T> constexpr int FORWARD = 16 / (int)sizeof(T);
+template <class T> constexpr int BACKWARD = 4;
+
+// The kernel for a head's size: units of a lane (at most 1024 entries, and the last piece of each part may
+// have no second).
 template <class T, bool INTERLEAVED> dbs_status norm_of(Norm &A, int head_dim, int dim, bool wide, cudaStream_t s)
 {
-    constexpr int MANY = sizeof(T) == 4 ? 5 : 3;           // (of 1024 entries at most, up to two vectors of which are short)
-    static constexpr dbs_status (*launch[4])(Norm &, int, int, cudaStream_t) = {
-        launch_norm<T, INTERLEAVED, true, 1>, launch_norm<T, INTERLEAVED, true, MANY>, launch_norm<T, INTERLEAVED, false, 4>,
-        launch_norm<T, INTERLEAVED, false, 16>};
-    return choose<T, INTERLEAVED, Norm>(A, head_dim, dim, wide, s, launch);
+    constexpr int N = FORWARD<T>;
+    if (wide) return head_of<N>(head_dim, dim).units <= 32 ? launch_norm<T, INTERLEAVED, N, 1>(A, head_dim, dim, s)
+                                                           : launch_norm<T, INTERLEAVED, N, 16 / N + 1>(A, head_dim, dim, s);
+    return head_of<1>(head_dim, dim).units <= 128 ? launch_norm<T, INTERLEAVED, 1, 4>(A, head_dim, dim, s)
+                                                  : launch_norm<T, INTERLEAVED, 1, 16>(A, head_dim, dim, s);
 }
 template <class T, bool INTERLEAVED> dbs_status gradient_of(Gradient &A, int head_dim, int dim, bool wide, cudaStream_t s)
 {
-    constexpr int MANY = sizeof(T) == 4 ? 5 : 3;
-    static constexpr dbs_status (*launch[4])(Gradient &, int, int, cudaStream_t) = {
-        launch_gradient<T, INTERLEAVED, true, 1>, launch_gradient<T, INTERLEAVED, true, MANY>, launch_gradient<T, INTERLEAVED, false, 4>,
-        launch_gradient<T, INTERLEAVED, false, 16>};
-    return choose<T, INTERLEAVED, Gradient>(A, head_dim, dim, wide, s, launch);
+    constexpr int N = BACKWARD<T>;
+    if (wide) return head_of<N>(head_dim, dim).units <= 32 ? launch_gradient<T, INTERLEAVED, N, 1>(A, head_dim, dim, s)
+                                                           : launch_gradient<T, INTERLEAVED, N, 16 / N + 1>(A, head_dim, dim, s);
+    return head_of<1>(head_dim, dim).units <= 128 ? launch_gradient<T, INTERLEAVED, 1, 4>(A, head_dim, dim, s)
+                                                  : launch_gradient<T, INTERLEAVED, 1, 16>(A, head_dim, dim, s);
 }
 
+template <class T> bool type_is(dbs_dtype t)
+{
+    return t == (sizeof(T) == 4 ? DBS_F32 : __is_same(T, __half) ? DBS_F16 : DBS_BF16);
+}
 template <class T> dbs_status norm(Norm &A, int head_dim, int dim, bool interleaved, cudaStream_t s)
 {
-    bool wide = whole_vectors<T>(head_dim, dim, interleaved, A.table);
+    constexpr int N = FORWARD<T>;
+    bool wide = whole_pieces<N>(head_dim, dim, interleaved, A.table);
     for (int p = 0; p < A.nparts; ++p) {
         const dbs_rotary_heads &P = A.part[p].heads;
-        wide = wide && on_vectors<T>(P.in, P.in_batch, P.in_token, P.in_head) && on_vectors<T>(P.out, P.out_batch, P.out_token, P.out_head);
+        wide = wide && on_pieces<T, N>(P.in, P.in_batch, P.in_token, P.in_head) && on_pieces<T, N>(P.out, P.out_batch, P.out_token, P.out_head);
+        A.vectors[p] = A.part[p].weight && type_is<T>(A.part[p].weight_dtype) && aligned16(A.part[p].weight);
     }
     return interleaved ? norm_of<T, true>(A, head_dim, dim, wide, s) : norm_of<T, false>(A, head_dim, dim, wide, s);
 }
 template <class T> dbs_status gradient(Gradient &A, int head_dim, int dim, bool interleaved, cudaStream_t s)
 {
-    bool wide = whole_vectors<T>(head_dim, dim, interleaved, A.table);
+    constexpr int N = BACKWARD<T>;
+    bool wide = whole_pieces<N>(head_dim, dim, interleaved, A.table);
     for (int p = 0; p < A.nparts; ++p) {
         const dbs_norm_gradient_heads &P = A.part[p];
-        wide = wide && (P.heads == 0 || (on_vectors<T>(P.grad, P.grad_batch, P.grad_token, P.grad_head) &&
-                                         on_vectors<T>(P.in, P.in_batch, P.in_token, P.in_head) &&
-                                         on_vectors<T>(P.out, P.out_batch, P.out_token, P.out_head)));
+        wide = wide && (P.heads == 0 || (on_pieces<T, N>(P.grad, P.grad_batch, P.grad_token, P.grad_head) &&
+                                         on_pieces<T, N>(P.in, P.in_batch, P.in_token, P.in_head) &&
+                                         on_pieces<T, N>(P.out, P.out_batch, P.out_token, P.out_head)));
+        A.vectors[p] = P.weight && type_is<T>(P.weight_dtype) && aligned16(P.weight);
     }
     return interleaved ? gradient_of<T, true>(A, head_dim, dim, wide, s) : gradient_of<T, false>(A, head_dim, dim, wide, s);
 }
@@ -571,7 +687,7 @@ dbs_status dbs_norm_rotary_gradient_scratch(int32_t nparts, int32_t head_dim, in
     if (!bytes || nparts < 1 || nparts > 2 || head_dim < 1 || head_dim > 1024) return DBS_ERR_INVALID_ARG;
     const int sms = multiprocessors();
     if (sms == 0) return DBS_ERR_CUDA;
-    *bytes = (int64_t)nparts * sms * GRADIENT_BLOCKS * head_dim * (int64_t)sizeof(float);
+    *bytes = (int64_t)nparts * sms * BACKWARD_BLOCKS * head_dim * (int64_t)sizeof(float);
     return DBS_OK;
 }
 
