@@ -133,6 +133,40 @@ template <class T, bool INTERLEAVED, int N, int K> struct Lane {
             }
         }
     }
+    // The lane's units: where its pieces are.
+    struct Units {
+        int a[K], b[K];
+        bool some[K], both[K], turned[K];
+        __device__ __forceinline__ Units(const Head &H, int lane)
+        {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const U u(H, lane + k * H.lanes);
+                a[k] = u.a;
+                b[k] = u.b;
+                some[k] = u.some;
+                both[k] = u.both;
+                turned[k] = u.turned;
+            }
+        }
+    };
+    static __device__ __forceinline__ void load(const Units &u, const T *p, VT (&x)[K][2])
+    {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            x[k][0] = x[k][1] = VT{};
+            if (u.some[k]) x[k][0] = *(const VT *)(p + u.a[k]);
+            if (u.both[k]) x[k][1] = *(const VT *)(p + u.b[k]);
+        }
+    }
+    static __device__ __forceinline__ void store(const Units &u, T *p, const VT (&x)[K][2])
+    {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (u.some[k]) *(VT *)(p + u.a[k]) = x[k][0];
+            if (u.both[k]) *(VT *)(p + u.b[k]) = x[k][1];
+        }
+    }
     static __device__ __forceinline__ void load(const Head &H, int lane, const T *p, VT (&x)[K][2])
     {
 #pragma unroll
@@ -141,15 +175,6 @@ template <class T, bool INTERLEAVED, int N, int K> struct Lane {
             x[k][0] = x[k][1] = VT{};
             if (u.some) x[k][0] = *(const VT *)(p + u.a);
             if (u.both) x[k][1] = *(const VT *)(p + u.b);
-        }
-    }
-    static __device__ __forceinline__ void store(const Head &H, int lane, T *p, const VT (&x)[K][2])
-    {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const U u(H, lane + k * H.lanes);
-            if (u.some) *(VT *)(p + u.a) = x[k][0];
-            if (u.both) *(VT *)(p + u.b) = x[k][1];
         }
     }
     static __device__ __forceinline__ void opened(const VT (&x)[2], float (&v)[2 * N])
@@ -241,7 +266,9 @@ template <class T, bool INTERLEAVED, int N, int K> struct Lane {
     // (every lane of the warp takes part; each head's lanes get their own sum)
     static __device__ __forceinline__ float sum(const Head &H, float v)
     {
-        for (int d = H.lanes >> 1; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1)
+            if (d < H.lanes) v += __shfl_xor_sync(~0u, v, d);
         return v;
     }
 };
@@ -296,11 +323,12 @@ __global__ void __launch_bounds__(NT, K == 1 ? FORWARD_BLOCKS : 1) k_norm_rotary
     } else {
         dst += b * P.out_batch + t * P.out_token;
     }
+    const typename L::Units units(H, lane);
     typename L::VT x[HEADS][K][2];
     auto fetch = [&](int h) {
 #pragma unroll
         for (int k = 0; k < HEADS; ++k)
-            if (h + k < heads) L::load(H, lane, src + k * P.in_head, x[k]);
+            if (h + k < heads) L::load(units, src + k * P.in_head, x[k]);
         src += HEADS * P.in_head;
     };
     fetch(0);
@@ -331,11 +359,11 @@ __global__ void __launch_bounds__(NT, K == 1 ? FORWARD_BLOCKS : 1) k_norm_rotary
                 for (int c = 0; c < K; ++c) {
 #pragma unroll
                     for (int j = 0; j < N; ++j) v[c][j] = mul_two(v[c][j], r2);
-                    L::turn(v[c], own[c], other[c], lane + c * H.lanes < H.turned);
+                    L::turn(v[c], own[c], other[c], units.turned[c]);
                     L::closed(v[c], x[k][c]);
                 }
             }
-            if (write) L::store(H, lane, dst + k * P.out_head, x[k]);
+            if (write) L::store(units, dst + k * P.out_head, x[k]);
         }
         dst += HEADS * P.out_head;
     }
@@ -396,6 +424,7 @@ __global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradi
     const int64_t items = A.total * chunks, step = (int64_t)A.blocks[p] * groups;
     // (all lanes of a warp go the same number of turns)
     const int first = (threadIdx.x & ~31) / H.lanes;
+    const typename L::Units units(H, lane);
     uint64_t w[K][N], dw[K][N];
     {
         float f[K][2 * N];
@@ -421,8 +450,8 @@ __global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradi
 #pragma unroll
             for (int k = 0; k < HEADS; ++k)
                 if (in && h + k < heads) {
-                    L::load(H, lane, g + k * P.grad_head, gv[k]);
-                    L::load(H, lane, x + k * P.in_head, xv[k]);
+                    L::load(units, g + k * P.grad_head, gv[k]);
+                    L::load(units, x + k * P.in_head, xv[k]);
                 }
             g += HEADS * P.grad_head;
             x += HEADS * P.in_head;
@@ -447,7 +476,7 @@ __global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradi
                 for (int c = 0; c < K; ++c) {
                     L::opened(gv[k][c], gf[c]);
                     L::opened(xv[k][c], xf[c]);
-                    L::turn(gf[c], own[c], other[c], lane + c * H.lanes < H.turned);
+                    L::turn(gf[c], own[c], other[c], units.turned[c]);
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
                         ss = fma_two(xf[c][j], xf[c][j], ss);
@@ -466,7 +495,7 @@ __global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradi
                     }
                     L::closed(gf[c], gv[k][c]);
                 }
-                L::store(H, lane, out + k * P.out_head, gv[k]);
+                L::store(units, out + k * P.out_head, gv[k]);
             }
             out += HEADS * P.out_head;
         }

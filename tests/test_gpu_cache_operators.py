@@ -166,6 +166,55 @@ def test_norm_rotary_gradient(dt, lead, heads, D, dim, il, layout):
     close(alone[2], wref, 192 * E * wmag + E * np.abs(wref) + 1e-30)
 
 
+MANY_TOKENS = [((2, 6000), 16, 8, 64, 64, False, "plain"), ((1, 12000), 8, 4, 128, 64, False, "first"), ((12001,), 8, 4, 96, 96, True, "plain"),
+               ((2, 5000), 17, 16, 128, 128, True, "plain"), ((10000,), 9, 5, 256, 0, False, "plain")]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("lead,hq,hk,D,dim,il,layout", MANY_TOKENS)
+def test_norm_rotary_of_many_tokens(dt, lead, hq, hk, D, dim, il, layout):
+    """Several turns of every warp; a few positions outside the table, a few slots outside the cache."""
+    rng = np.random.default_rng(hq + D)
+    n = int(np.prod(lead))
+    q, k, v = heads_of(rng, dt, lead, hq, D, layout, 2.0), heads_of(rng, dt, lead, hk, D, layout), heads_of(rng, dt, lead, hk, D, layout)
+    qw, kw = rnd(rng, dt, D), rnd(rng, "f32", D)
+    table = dbs.rotary_table(60, dim) if dim else torch.zeros((60, 0), device=DEV)
+    p = rng.integers(0, 60, lead).astype(np.int32)
+    p.reshape(-1)[::997] = [-1, 60, 5][n % 3]
+    pos = torch.from_numpy(p).to(DEV)
+    out = dbs.norm_rotary(q, k, qw, kw, table, pos, eps=1e-5, interleaved=il)
+    good = (p >= 0) & (p < 60)
+    eps, t, pc = np.float64(np.float32(1e-5)), f64(table), np.where(good, p, 0)
+    for got, x, w in ((out[0], q, qw), (out[1], k, kw)):
+        ref, mag = norm_ref(f64(x), f64(w), t, pc, il, eps)
+        ref[~good, :, :dim] = NAN
+        close(got, ref, 32 * E * mag + U[dt] * np.abs(ref) + ETA[dt])
+    x = q.clone()
+    assert torch.equal(dbs.norm_rotary(x, None, qw, None, table, pos, eps=1e-5, interleaved=il, q_out=x)[0].nan_to_num(7), out[0].nan_to_num(7))
+    # into a cache
+    page, slots = 16, rng.permutation(n + 40)[:n].astype(np.int32)
+    slots[::501] = -1
+    kc = torch.zeros((n // page + 4, page, hk, D), dtype=DT[dt], device=DEV)
+    vc = torch.ones_like(kc)
+    rk, rv = kc.flatten(0, 1).clone(), vc.flatten(0, 1).clone()
+    qo = dbs.norm_rotary_append(q, k, v, qw, kw, table, pos, kc, vc, ints(slots), eps=1e-5, interleaved=il)
+    assert torch.equal(qo.nan_to_num(7), out[0].nan_to_num(7))
+    take = torch.from_numpy(slots >= 0).to(DEV)
+    at = ints(slots).long()[take]
+    rk[at], rv[at] = out[1].reshape(-1, hk, D)[take], v.reshape(-1, hk, D)[take]
+    assert torch.equal(kc.flatten(0, 1).nan_to_num(7), rk.nan_to_num(7)) and torch.equal(vc.flatten(0, 1), rv)
+    # the gradient (its chains are no longer here: 17 heads of 10,000 tokens are 56 turns of 3040 groups of lanes)
+    qg, kg = heads_of(rng, dt, lead, hq, D, "plain"), heads_of(rng, dt, lead, hk, D, layout)
+    pos = torch.from_numpy(pc).to(DEV)
+    got = dbs.norm_rotary_gradient(qg, kg, q, k, qw, kw, table, pos, eps=1e-5, interleaved=il)
+    for dx, dw, g, y, w in ((got[0], got[2], qg, q, qw), (got[1], got[3], kg, k, kw)):
+        ref, mag, wref, wmag = grad_ref(f64(g), f64(y), f64(w), t, pc, il, eps)
+        close(dx, ref, 64 * E * mag + U[dt] * np.abs(ref) + ETA[dt])
+        close(dw, wref, 192 * E * wmag + E * np.abs(wref) + 1e-30)
+    again = dbs.norm_rotary_gradient(qg, kg, q, k, qw, kw, table, pos, eps=1e-5, interleaved=il)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
 def test_norm_rotary_gradient_against_differences():
     """d/ds of sum(G * norm_rotary(x + s d)) at 0 by central differences in 64 bits (the forward reference, checked
     above); their own error is h^2 / 6 times a third derivative of about 40 here, and rounding 2^-52 / h of sums of
