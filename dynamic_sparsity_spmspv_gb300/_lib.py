@@ -93,7 +93,7 @@ PROTOTYPES = {
     "dbs_norm_rotary_gradient": (I32, [P, I32, I32, I64, I64, I32, I32, ctypes.c_float, P, I64, P, I32, P, I64, P]),
     "dbs_window_attention_scratch": (I32, [P, P]),
     "dbs_window_attention": (I32, [P, P]),
-    "dbs_cache_resize_scratch": (I32, [P, P]),
+    "dbs_cache_resize_scratch": (I32, [P, I64, P]),
     "dbs_cache_resize": (I32, [P, P, P, P, I64, P, I64, P]),
     "dbs_cache_fork_scratch": (I32, [P, I64, P]),
     "dbs_cache_fork": (I32, [P, P, P, P, I64, P, P, I64, P]),

@@ -807,12 +807,13 @@ PyObject *cache_resize(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyOb
         const int32_t *want = (const int32_t *)c.vector("lens", &lens, S.batch, at::kInt);
         c.on(a.v[6]);
         int64_t bytes = 0;
-        check(c.fn, dbs_cache_resize_scratch(&S, &bytes));
-        const at::Tensor status = c.empty({S.batch}, at::kInt), scratch = c.empty({bytes}, at::kByte);
-        at::Tensor slots;
+        check(c.fn, dbs_cache_resize_scratch(&S, columns, &bytes));
+        const at::Tensor status = c.empty({S.batch}, at::kInt);
+        at::Tensor slots, scratch;
         if (a.v[5]) slots = c.empty({S.batch, columns}, at::kInt);
+        if (bytes > 0) scratch = c.empty({bytes}, at::kByte);
         check(c.fn, dbs_cache_resize(&S, want, status.data_ptr<int32_t>(), slots.defined() ? slots.data_ptr<int32_t>() : nullptr, columns,
-                                     scratch.data_ptr(), bytes, c.stream));
+                                     scratch.defined() ? scratch.data_ptr() : nullptr, bytes, c.stream));
         written(table);
         written(kv);
         written(refs);

@@ -173,6 +173,193 @@ __global__ void __launch_bounds__(PLAN_NT) k_resize(Resize A, int slots_here)
     write_slots(A, threadIdx.x, PLAN_NT);
 }
 
+// ---- the same for few sequences: a thread has one, and everything stays in shared memory ----
+
+constexpr int WORDS = PLAN_NT * RUN / 32;          // of a turn of pages, a bit each
+
+// Of the pages p0 .. p0 + 32 WORDS - 1: which are free, and how many before each word.
+struct Turn {
+    uint32_t free[WORDS];
+    int before[WORDS + 1];
+};
+// This thread's RUN pages of a turn; the bits of those that are free, and of those with two owners or more.
+struct Run {
+    uint32_t free, many;
+};
+__device__ __forceinline__ Run run_of(const dbs_page_state &s, int64_t p0)
+{
+    const int64_t mine = p0 + (int64_t)threadIdx.x * RUN;
+    Run r{0, 0};
+    int n[RUN];
+    if (mine + RUN <= s.pages && (reinterpret_cast<uintptr_t>(s.refs) & 15u) == 0) {
+#pragma unroll
+        for (int i = 0; i < RUN / 4; ++i) {
+            const int4 v = __ldcg((const int4 *)(s.refs + mine) + i);
+            n[4 * i] = v.x;
+            n[4 * i + 1] = v.y;
+            n[4 * i + 2] = v.z;
+            n[4 * i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) n[i] = mine + i < s.pages ? refs_of(s, (int)(mine + i)) : 1;
+    }
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+        r.free |= (uint32_t)(n[i] == 0) << i;
+        r.many |= (uint32_t)(n[i] > 1) << i;
+    }
+    return r;
+}
+// Two threads have a word.
+__device__ __forceinline__ uint32_t word_of(uint32_t half)
+{
+    return half | __shfl_down_sync(~0u, half, 1) << 16;
+}
+// Counts the free pages of a turn whose words are there; by the whole block.
+__device__ __forceinline__ int count_free(Turn &T, Sums &S)
+{
+    const int n = threadIdx.x < WORDS ? __popc(T.free[threadIdx.x]) : 0, at = (int)before(n, S);
+    if (threadIdx.x < WORDS) T.before[threadIdx.x] = at;
+    if (threadIdx.x == 0) T.before[WORDS] = (int)S.total;
+    __syncthreads();
+    return (int)S.total;
+}
+// The k-th free page of a turn (k below their number).
+__device__ __forceinline__ int nth_free(const Turn &T, int k)
+{
+    int lo = 0;
+#pragma unroll
+    for (int d = WORDS / 2; d; d >>= 1)
+        if (T.before[lo + d] <= k) lo += d;
+    uint32_t w = T.free[lo];
+    for (int i = k - T.before[lo]; i; --i) w &= w - 1;
+    return 32 * lo + __ffs(w) - 1;
+}
+// The last of n ascending offsets that is at most k (the first is 0; equal ones: the last).
+__device__ __forceinline__ int owner(const int *from, int n, int k)
+{
+    int lo = 0;
+    for (int d = PLAN_NT / 2; d; d >>= 1)
+        if (lo + d < n && from[lo + d] <= k) lo += d;
+    return lo;
+}
+
+// Free pages in order, as many as are asked for: of one turn in its bits, of more in `list`.  Returns how
+// many there are (all that exist, if they do not suffice); by the whole block, the first turn's bits being there.
+__device__ __forceinline__ int find_few(const dbs_page_state &s, int64_t asked, Turn &T, int *list, Sums &S)
+{
+    __syncthreads();
+    int found = asked > 0 ? count_free(T, S) : 0;
+    if (s.pages <= 32 * WORDS || asked == 0) return found;
+    const int total = (int)(asked < s.pages ? asked : s.pages);
+    for (int k = threadIdx.x; k < found && k < total; k += PLAN_NT) list[k] = nth_free(T, k);
+    for (int64_t p0 = 32 * WORDS; p0 < s.pages && found < total; p0 += 32 * WORDS) {
+        const uint32_t f = word_of(run_of(s, p0).free);
+        __syncthreads();                           // the bits of the turn before have been read
+        if (!(threadIdx.x & 1)) T.free[threadIdx.x >> 1] = f;
+        __syncthreads();
+        const int here = count_free(T, S);
+        for (int k = threadIdx.x; k < here && found + k < total; k += PLAN_NT) list[found + k] = (int)p0 + nth_free(T, k);
+        found += here;
+    }
+    __syncthreads();
+    return found;
+}
+__device__ __forceinline__ int found_page(const dbs_page_state &s, const Turn &T, const int *list, int k)
+{
+    return s.pages <= 32 * WORDS ? nth_free(T, k) : __ldcg(list + k);
+}
+
+// At most PLAN_NT sequences.  Cuts, new pages and slots are shared out among all threads one by one, so
+// that long sequences take no longer than short ones; refs are read beside the lengths.
+__global__ void __launch_bounds__(PLAN_NT) k_resize_few(Resize A, int slots_here)
+{
+    __shared__ Sums S;
+    __shared__ Turn T;
+    __shared__ uint32_t many[WORDS];
+    __shared__ int from[PLAN_NT], base[PLAN_NT], was[PLAN_NT], now[PLAN_NT];
+    const dbs_page_state &s = A.s;
+    const int t = threadIdx.x, n = (int)s.batch, page = (int)s.page_size;
+    const int64_t room = s.max_pages * s.page_size;
+    const bool mine = t < n;
+    const int old = mine ? length(s, t) : 0, want = mine ? A.lens[t] : -1;
+    const Run run = run_of(s, 0);
+    const int had = pages_of(old, page), have = want < 0 || want > room ? had : pages_of(want, page);
+    // the page that growth would go on in
+    const int last = mine && want > old && want <= room && old % page ? __ldcg(s.page_table + (int64_t)t * s.page_row + old / page) : -1;
+    const uint32_t free = word_of(run.free), shared = word_of(run.many);
+    if (!(t & 1)) {
+        T.free[t >> 1] = free;
+        many[t >> 1] = shared;
+    }
+    const int cut = want >= 0 && want < old ? had - have : 0;
+    const int64_t before_me = before(cut, S), cuts = S.total;
+    if (cuts > 0) {
+        // (owned pages are fewer than 2^31 in all, or the lengths are not a state: then the rest is passed over)
+        const int most = (int)(cuts < 0x7fffffff ? cuts : 0x7fffffff);
+        from[t] = before_me < most ? (int)before_me : most;
+        base[t] = have;
+        __syncthreads();
+        for (int64_t k = t; k < most; k += PLAN_NT) {
+            const int b = owner(from, n, (int)k), p = __ldcg(s.page_table + b * s.page_row + base[b] + ((int)k - from[b]));
+            if (!is_page(s, p)) continue;
+            const int left = atomicSub(s.refs + p, 1) - 1;
+            if (p >= 32 * WORDS) continue;
+            const uint32_t bit = 1u << (p & 31);
+            if (left == 0) atomicOr(T.free + (p >> 5), bit);
+            if (left == -1) atomicAnd(T.free + (p >> 5), ~bit);            // (a count that was wrong: not free)
+            if (left == 1) atomicAnd(many + (p >> 5), ~bit);
+        }
+        __syncthreads();
+    }
+    int status = want > room ? 3 : 0, need = 0;
+    if (status == 0 && want > old) {
+        need = have - had;
+        if (is_page(s, last) && (last < 32 * WORDS ? many[last >> 5] >> (last & 31) & 1u : refs_of(s, last) > 1)) {
+            status = 2;
+            need = 0;
+        }
+    }
+    const int64_t start = before(need, S), asked = S.total;
+    const int found = find_few(s, asked, T, A.list, S);
+    if (need > 0 && start + need > found) {
+        status = 1;
+        need = 0;
+    }
+    // (those that get their pages come before all that do not)
+    before(need, S);
+    const int taken = (int)S.total;
+    from[t] = start < taken ? (int)start : taken;
+    base[t] = had;
+    was[t] = old;
+    now[t] = status == 0 && want >= 0 ? want : old;
+    __syncthreads();
+    for (int k = t; k < taken; k += PLAN_NT) {
+        const int b = owner(from, n, k), p = found_page(s, T, A.list, k);
+        s.page_table[b * s.page_row + base[b] + (k - from[b])] = p;
+        s.refs[p] = 1;
+    }
+    if (mine) {
+        A.status[t] = status;
+        if (status == 0 && want >= 0) s.kv_lens[t] = want;
+        if (A.old) A.old[t] = old;
+    }
+    if (!slots_here) return;
+    __syncthreads();
+    const uint32_t columns = (uint32_t)A.columns, all = (uint32_t)n * columns;
+    for (uint32_t u = t; u < all; u += PLAN_NT) {
+        const uint32_t b = u / columns;
+        const int i = (int)(u - b * columns);
+        int slot = -1;
+        if (i < now[b] - was[b]) {
+            const int j = was[b] + i, p = __ldcg(s.page_table + b * s.page_row + j / page);
+            if (is_page(s, p)) slot = p * page + j % page;
+        }
+        A.slots[u] = slot;
+    }
+}
+
 // ---- copies of entries ----
 
 // Bytes of a row of one entry that lie together, and where rows lie.
@@ -195,6 +382,7 @@ __global__ void __launch_bounds__(PLAN_NT) k_fork_plan(dbs_page_state s, const i
                                                        int32_t *status, Fork *forks, int32_t *list)
 {
     __shared__ Sums S;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int page = (int)s.page_size;
     for (int i = threadIdx.x; i < n; i += PLAN_NT) {
         const int p = parents[i], c = children[i];
@@ -256,11 +444,54 @@ __global__ void __launch_bounds__(PLAN_NT) k_fork_plan(dbs_page_state s, const i
     }
 }
 
-// blockIdx.z: the fork; y: K and V of each layer, and before them the names of the
-// shared pages; x: the page's entries.
-template <class V>
-__global__ void __launch_bounds__(256) k_fork_copy(Data D, dbs_page_state s, const Fork *forks)
+// The same for at most PLAN_NT forks, in shared memory: a child is taken if no valid one before names it.
+__global__ void __launch_bounds__(PLAN_NT) k_fork_plan_few(dbs_page_state s, const int32_t *parents, const int32_t *children, int n,
+                                                           int32_t *status, Fork *forks, int32_t *list)
 {
+    __shared__ Sums S;
+    __shared__ Turn T;
+    __shared__ int named[PLAN_NT];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int t = threadIdx.x, page = (int)s.page_size;
+    const bool mine = t < n;
+    const int p = mine ? parents[t] : -1, c = mine ? children[t] : -1;
+    const Run run = run_of(s, 0);
+    bool good = p >= 0 && p < s.batch && c >= 0 && c < s.batch;
+    const int len = good ? length(s, p) : 0, taken = good ? length(s, c) : 1;
+    good = good && taken == 0;
+    Fork f{-1, -1, len % page, p, c, len / page};
+    if (good && f.entries) f.from = __ldcg(s.page_table + p * s.page_row + f.full);
+    const uint32_t free = word_of(run.free);
+    if (!(t & 1)) T.free[t >> 1] = free;
+    named[t] = good ? c : -1;
+    __syncthreads();
+    for (int i = 0; good && i < t; ++i) good = named[i] != c;
+    const int need = good && f.entries > 0, at = (int)before(need, S), asked = (int)S.total;
+    const int found = find_few(s, asked, T, list, S);
+    const bool fits = good && (!need || at < found);
+    if (mine) {
+        status[t] = fits ? 0 : good ? 1 : 2;
+        if (fits) {
+            s.kv_lens[c] = len;
+            if (need) {
+                f.to = found_page(s, T, list, at);
+                s.page_table[c * s.page_row + f.full] = f.to;
+                s.refs[f.to] = 1;
+                if (!is_page(s, f.from)) f.to = -1;            // (nothing to copy from)
+            }
+        } else {
+            f.child = -1;
+        }
+        forks[t] = f;
+    }
+}
+
+// blockIdx.z: the fork; y: K and V of each layer, and before them the names of the
+// shared pages; x: the page's entries, `across` threads (a power of two) to each, four entries a thread at once.
+template <class V>
+__global__ void __launch_bounds__(256) k_fork_copy(Data D, dbs_page_state s, const Fork *forks, int across)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const Fork f = forks[blockIdx.z];
     if (f.child < 0) return;
     const int64_t u0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
@@ -276,10 +507,22 @@ __global__ void __launch_bounds__(256) k_fork_copy(Data D, dbs_page_state s, con
     const int layer = (int)(blockIdx.y - 1) >> 1, is_v = (int)(blockIdx.y - 1) & 1;
     V *base = (V *)(is_v ? D.v : D.k) + layer * (is_v ? D.v_layer : D.k_layer);
     const int64_t by_page = is_v ? D.v_page : D.k_page, by_entry = is_v ? D.v_entry : D.k_entry, by_head = is_v ? D.v_head : D.k_head;
-    const int64_t per = D.heads * D.row, all = f.entries * per;
-    for (int64_t u = u0; u < all; u += step) {
-        const int64_t e = u / per, r = u - e * per, h = r / D.row, at = e * by_entry + h * by_head + (r - h * D.row);
-        base[f.to * by_page + at] = base[f.from * by_page + at];
+    const int down = 256 / across, e0 = (int)blockIdx.x * down + (int)threadIdx.x / across, turn = (int)gridDim.x * down;
+    const uint32_t per = (uint32_t)(D.heads * D.row), row = (uint32_t)D.row;           // (below 2^31)
+    V *const to = base + f.to * by_page;
+    const V *const from = base + f.from * by_page;
+    for (uint32_t u = threadIdx.x & (across - 1); u < per; u += across) {
+        const uint32_t h = D.heads == 1 ? 0u : u / row;
+        const int64_t at = h * by_head + (u - h * row);
+        for (int64_t e = e0; e < f.entries; e += 4 * (int64_t)turn) {
+            V x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (e + k * turn < f.entries) x[k] = from[(e + k * turn) * by_entry + at];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (e + k * turn < f.entries) to[(e + k * turn) * by_entry + at] = x[k];
+        }
     }
 }
 
@@ -316,8 +559,9 @@ __global__ void __launch_bounds__(MOVE_NT) k_compact(Compact A)
     const int64_t given = A.accepted_lens ? A.accepted_lens[b] : A.max_accepted;
     const int n = (int)(given < 0 ? 0 : given > A.max_accepted ? A.max_accepted : given);
     const int32_t *list = A.accepted + b * A.stride;
-    const int64_t u = (int64_t)blockIdx.x * MOVE_NT + threadIdx.x, per = D.heads * D.row;
-    const int64_t h = u / D.row, mine = h * by_head + (u - h * D.row);
+    const uint32_t u = blockIdx.x * MOVE_NT + threadIdx.x, per = (uint32_t)(D.heads * D.row), row = (uint32_t)D.row;    // (below 2^31)
+    const uint32_t h = D.heads == 1 ? 0u : u / row;
+    const int64_t mine = h * by_head + (u - h * row);
     int kept = 0;
     auto place = [&](int j) {
         int64_t page = b;
@@ -416,14 +660,24 @@ template <class F> dbs_status by_unit(int unit, F f)
 
 constexpr int64_t up16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
+// Slots that the one block writes; of more a second launch is through earlier.
+constexpr int64_t SLOTS_HERE = 8 * PLAN_NT;
+
+// Scratch of a resize: of few sequences only what does not stay in shared memory.
+int64_t scratch_of(const dbs_page_state &s, int64_t columns)
+{
+    if (s.batch > PLAN_NT) return up16(4 * (3 * s.batch + s.pages));
+    return up16(4 * ((s.batch * columns > SLOTS_HERE ? s.batch : 0) + (s.pages > 32 * WORDS ? s.pages : 0)));
+}
+
 }  // namespace
 
 extern "C" {
 
-dbs_status dbs_cache_resize_scratch(const dbs_page_state *s, int64_t *bytes)
+dbs_status dbs_cache_resize_scratch(const dbs_page_state *s, int64_t columns, int64_t *bytes)
 {
-    if (!bytes || !state_ok(s, false)) return DBS_ERR_INVALID_ARG;
-    *bytes = up16(4 * (3 * s->batch + s->pages));
+    if (!bytes || !state_ok(s, false) || columns < 0 || columns >= (int64_t(1) << 31)) return DBS_ERR_INVALID_ARG;
+    *bytes = scratch_of(*s, columns);
     return DBS_OK;
 }
 
@@ -432,18 +686,26 @@ dbs_status dbs_cache_resize(const dbs_page_state *s, const int32_t *lens, int32_
 {
     if (!state_ok(s, true) || columns < 0 || columns >= (int64_t(1) << 31)) return DBS_ERR_INVALID_ARG;
     if (s->batch == 0) return DBS_OK;
-    int64_t need = 0;
-    if (dbs_cache_resize_scratch(s, &need) != DBS_OK || !lens || !status || (s->pages > 0 && !s->refs) || !scratch || !aligned16(scratch) ||
-        scratch_bytes < need || lens == s->kv_lens)
+    const int64_t need = scratch_of(*s, columns), all = slots ? s->batch * columns : 0;
+    if (!lens || !status || (s->pages > 0 && !s->refs) || (need > 0 && (!scratch || !aligned16(scratch) || scratch_bytes < need)) || lens == s->kv_lens)
         return DBS_ERR_INVALID_ARG;
+    const bool here = all > 0 && all <= SLOTS_HERE;
     int32_t *at = (int32_t *)scratch;
-    const Resize A{*s, lens, status, columns ? slots : nullptr, columns, at, at + s->batch, at + 2 * s->batch, at + 3 * s->batch};
-    // Slots by the one block while it is through with them before a second launch would
-    // be.
-    const int64_t all = A.slots ? s->batch * columns : 0;
-    const bool here = all > 0 && all <= 8 * PLAN_NT;
     cudaStream_t st = (cudaStream_t)stream;
-    k_resize<<<1, PLAN_NT, 0, st>>>(A, here);
+    Resize A{*s, lens, status, all ? slots : nullptr, columns, nullptr, nullptr, nullptr, at};
+    if (s->batch <= PLAN_NT) {
+        if (s->batch * columns > SLOTS_HERE) {
+            A.old = at;
+            A.list = at + s->batch;
+        }
+        k_resize_few<<<1, PLAN_NT, 0, st>>>(A, here);
+    } else {
+        A.old = at;
+        A.need = at + s->batch;
+        A.end = at + 2 * s->batch;
+        A.list = at + 3 * s->batch;
+        k_resize<<<1, PLAN_NT, 0, st>>>(A, here);
+    }
     if (all > 0 && !here) {
         const int64_t blocks = (all + 255) / 256;
         k_slots<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(A);
@@ -470,18 +732,29 @@ dbs_status dbs_cache_fork(const dbs_cache_data *data, const dbs_page_state *s, c
     Fork *forks = (Fork *)scratch;
     int32_t *list = (int32_t *)(forks + n);
     cudaStream_t st = (cudaStream_t)stream;
-    k_fork_plan<<<1, PLAN_NT, 0, st>>>(*s, parents, children, (int)n, status, forks, list);
+    if (n <= PLAN_NT) k_fork_plan_few<<<1, PLAN_NT, 0, st>>>(*s, parents, children, (int)n, status, forks, list);
+    else k_fork_plan<<<1, PLAN_NT, 0, st>>>(*s, parents, children, (int)n, status, forks, list);
     dbs_status got = launched();
     if (got != DBS_OK || s->batch == 0) return got;
     Data D{};
     int unit = 16;
     const bool any = data->layers > 0 && data->heads > 0 && data->head_dim > 0;
     if (any) data_of(*data, D, unit);
-    const int64_t most = any ? s->page_size * D.heads * D.row : 1, blocks = (most + 1023) / 1024;
-    const dim3 grid((unsigned)(blocks < 256 ? blocks : 256), any ? (unsigned)(1 + 2 * data->layers) : 1u, (unsigned)n);
+    int across = 256;
+    while (across > 1 && any && across / 2 >= D.heads * D.row) across /= 2;
+    const int64_t each = 4 * (256 / across), blocks = (s->page_size + each - 1) / each;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(blocks < 256 ? blocks : 256), any ? (unsigned)(1 + 2 * data->layers) : 1u, (unsigned)n);
+    c.blockDim = 256;
+    c.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
     return by_unit(unit, [&](auto v) {
-        k_fork_copy<decltype(v)><<<grid, 256, 0, st>>>(D, *s, forks);
-        return launched();
+        return cudaLaunchKernelEx(&c, k_fork_copy<decltype(v)>, D, *s, (const Fork *)forks, across) == cudaSuccess ? DBS_OK
+                                                                                                                   : (cudaGetLastError(), DBS_ERR_CUDA);
     });
 }
 

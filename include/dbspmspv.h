@@ -704,9 +704,9 @@ typedef struct {
  *            max_pages * page_size
  *   slots    device int32[batch, columns], contiguous, or NULL: of the i-th new entry of b the slot
  *            (page * page_size + its place in the page), as dbs_rotary takes it; -1 where there is none
- *   scratch  device, 16-byte aligned, dbs_cache_resize_scratch bytes
+ *   scratch  device, 16-byte aligned, dbs_cache_resize_scratch bytes (which may be 0: then NULL)
  * Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */
-dbs_status dbs_cache_resize_scratch(const dbs_page_state *state, int64_t *bytes);
+dbs_status dbs_cache_resize_scratch(const dbs_page_state *state, int64_t columns, int64_t *bytes);
 dbs_status dbs_cache_resize(const dbs_page_state *state, const int32_t *lens, int32_t *status, int32_t *slots,
                             int64_t columns, void *scratch, int64_t scratch_bytes, void *stream);
 

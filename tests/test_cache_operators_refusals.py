@@ -147,13 +147,16 @@ def test_resize_refusals():
     def resize(s=state(), lens=2 * A, status=A, slots=0, columns=0, scratch=A, size=big):
         return lib.dbs_cache_resize(s, lens, status, slots, columns, scratch, size, None)
 
-    for kw in (dict(s=None), dict(lens=0), dict(status=0), dict(columns=-1), dict(columns=1 << 31), dict(scratch=0), dict(scratch=A + 4), dict(size=16),
-               dict(s=state(refs=0)), dict(lens=A)):
+    large = state(batch=2000)                                              # (few sequences need no scratch)
+    for kw in (dict(s=None), dict(lens=0), dict(status=0), dict(columns=-1), dict(columns=1 << 31), dict(s=large, scratch=0),
+               dict(s=large, scratch=A + 4), dict(s=large, size=16), dict(s=state(refs=0)), dict(lens=A)):
         assert resize(**kw) == BAD, kw
     assert resize(s=state(batch=0, kv=0, table=0), lens=0, status=0, scratch=0) == OK
     need = ctypes.c_int64(-1)
-    assert lib.dbs_cache_resize_scratch(state(), ctypes.byref(need)) == OK and need.value >= 4 * (3 * 3 + 9)
-    assert lib.dbs_cache_resize_scratch(state(), None) == BAD and lib.dbs_cache_resize_scratch(None, ctypes.byref(need)) == BAD
+    assert lib.dbs_cache_resize_scratch(large, 0, ctypes.byref(need)) == OK and need.value >= 4 * (3 * 2000 + 9)
+    assert lib.dbs_cache_resize_scratch(state(), 5, ctypes.byref(need)) == OK and need.value == 0
+    for bad in ((state(), 0, None), (None, 0, ctypes.byref(need)), (state(), -1, ctypes.byref(need)), (state(), 1 << 31, ctypes.byref(need))):
+        assert lib.dbs_cache_resize_scratch(*bad) == BAD
 
 
 def test_fork_refusals():

@@ -632,6 +632,44 @@ def test_cache_fork(layers, heads, D, dt, dims, page, pages):
     pool.same(state)
 
 
+@pytest.mark.parametrize("n,first", [(1023, 0), (1024, 0), (1025, 0), (1500, 0), (5, 17000), (700, 40000)])
+def test_cache_fork_of_many_and_far_pages(n, first):
+    """As many as one block has threads, and more; free pages behind those of `first` that others own; too few of them in the end."""
+    rng = np.random.default_rng(n)
+    pool = Pool(n + 60, 3, first + n // 2 + 90, 4)
+    pool.refs[:first] = 3
+    pool.resize(np.concatenate([rng.integers(1, 12, 40), np.zeros(n + 20, int)]))
+    k, v = make_caches(rng, 1, 1, 8, "f16", 5, len(pool.refs), 4)
+    state, hk, hv = pool.device(), plain(k), plain(v)
+    parents, children = rng.integers(0, 42, n), 40 + rng.permutation(n + 20)[:n]
+    children[rng.integers(0, n, 5)] = children[0]
+    status = dbs.cache_fork(k, v, *state, ints(parents.tolist()), ints(children.tolist()))
+    want = pool.fork(parents.tolist(), children.tolist(), hk, hv)
+    assert np.array_equal(status.cpu().numpy(), want) and (n < 100 or set(want.tolist()) == {0, 1, 2})
+    pool.same(state)
+    assert torch.equal(plain(k), hk) and torch.equal(plain(v), hv)
+    lens = np.where(rng.random(n + 60) < 0.3, 0, -1).astype(np.int32)
+    lens[40:50] = 11
+    status, slots = dbs.cache_resize(*state, ints(lens.tolist()), 4, columns=12)
+    s, w = pool.resize(lens, 12)
+    assert np.array_equal(status.cpu().numpy(), s) and np.array_equal(slots.cpu().numpy(), w)
+    pool.same(state)
+
+
+def test_cache_resize_of_long_sequences():
+    """Thousands of pages cut, and taken, by a few sequences; refs that start at an odd address."""
+    pages, page = 30000, 8
+    pool = Pool(5, 9000, pages, page)
+    base = torch.zeros(pages + 1, dtype=torch.int32, device=DEV)
+    state = [ints(pool.table), ints(pool.kv), base[1:]]
+    for lens in ([60000, 3, 0, 50001, -1], [100, 72000, 9, 0, 0], [0, 71999, 72001, 5, 72000], [0, 0, 0, 0, 0]):
+        status, slots = dbs.cache_resize(*state, ints(lens), page, columns=3000)
+        s, w = pool.resize(lens, 3000)
+        assert np.array_equal(status.cpu().numpy(), s) and np.array_equal(slots.cpu().numpy(), w)
+        pool.same(state)
+        pool.consistent()
+
+
 def test_cache_fork_short_of_pages_and_growth_into_a_shared_page():
     pool = Pool(6, 4, 5, 8)
     pool.resize([8, 13, 5, 0, 0, 0])
