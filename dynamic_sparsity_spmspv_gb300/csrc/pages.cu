@@ -536,7 +536,7 @@ struct Compact {
     int32_t *new_lens;
 };
 
-constexpr int MOVE_NT = 256;
+constexpr int MOVE_NT = 256;               // threads of a block, at most: as many as an entry has units
 
 // blockIdx.z: the sequence; y: K or V of a layer; x: units of an entry, one a thread.
 // Numbers ascend, so place i is behind no number that comes later: a thread may load any of its
@@ -548,6 +548,11 @@ __global__ void __launch_bounds__(MOVE_NT) k_compact(Compact A)
     __shared__ int64_t from[MOVE_NT], to[MOVE_NT];         // units
     __shared__ int ends;
     const int64_t b = blockIdx.z;
+    const int32_t *list = A.accepted + b * A.stride;
+    const int NT = (int)blockDim.x;
+    // (the list's first numbers are read beside the lengths)
+    auto number = [&](int64_t i) { return i >= 0 && i < A.max_accepted ? list[i] : -1; };
+    int a = number(threadIdx.x), prior = number((int64_t)threadIdx.x - 1);
     const int layer = (int)blockIdx.y >> 1, is_v = (int)blockIdx.y & 1;
     const Data &D = A.d;
     V *base = (V *)(is_v ? D.v : D.k) + layer * (is_v ? D.v_layer : D.k_layer);
@@ -558,8 +563,7 @@ __global__ void __launch_bounds__(MOVE_NT) k_compact(Compact A)
     const int first = kv - tree;
     const int64_t given = A.accepted_lens ? A.accepted_lens[b] : A.max_accepted;
     const int n = (int)(given < 0 ? 0 : given > A.max_accepted ? A.max_accepted : given);
-    const int32_t *list = A.accepted + b * A.stride;
-    const uint32_t u = blockIdx.x * MOVE_NT + threadIdx.x, per = (uint32_t)(D.heads * D.row), row = (uint32_t)D.row;    // (below 2^31)
+    const uint32_t u = blockIdx.x * NT + threadIdx.x, per = (uint32_t)(D.heads * D.row), row = (uint32_t)D.row;    // (below 2^31)
     const uint32_t h = D.heads == 1 ? 0u : u / row;
     const int64_t mine = h * by_head + (u - h * row);
     int kept = 0;
@@ -574,12 +578,15 @@ __global__ void __launch_bounds__(MOVE_NT) k_compact(Compact A)
         }
         return page * by_page + in * by_entry;
     };
-    for (int i0 = 0; i0 < n; i0 += MOVE_NT) {
-        const int i = i0 + threadIdx.x, most = n - i0 < MOVE_NT ? n - i0 : MOVE_NT;
+    for (int64_t i0 = 0; i0 < n; i0 += NT) {
+        const int i = (int)i0 + (int)threadIdx.x, most = n - i0 < NT ? (int)(n - i0) : NT;
+        if (i0) {
+            a = number(i0 + threadIdx.x);
+            prior = number(i0 + threadIdx.x - 1);
+        }
         if (threadIdx.x == 0) ends = most;
         __syncthreads();
-        if (i < n) {
-            const int a = list[i], prior = i ? list[i - 1] : -1;
+        if (i0 + threadIdx.x < n) {
             if (a < 0 || a >= tree || a <= prior) {
                 atomicMin(&ends, (int)threadIdx.x);
             } else {
@@ -774,9 +781,10 @@ dbs_status dbs_cache_compact(const dbs_cache_data *data, const dbs_page_state *s
     if (any) data_of(*data, A.d, unit);
     else A.d.row = 1;
     const int64_t per = any ? A.d.heads * A.d.row : 1;
-    const dim3 grid((unsigned)((per + MOVE_NT - 1) / MOVE_NT), any ? (unsigned)(2 * data->layers) : 1u, (unsigned)s->batch);
+    const int nt = per >= MOVE_NT ? MOVE_NT : (int)((per + 31) / 32 * 32);
+    const dim3 grid((unsigned)((per + nt - 1) / nt), any ? (unsigned)(2 * data->layers) : 1u, (unsigned)s->batch);
     return by_unit(unit, [&](auto v) {
-        k_compact<decltype(v)><<<grid, MOVE_NT, 0, (cudaStream_t)stream>>>(A);
+        k_compact<decltype(v)><<<grid, nt, 0, (cudaStream_t)stream>>>(A);
         return launched();
     });
 }

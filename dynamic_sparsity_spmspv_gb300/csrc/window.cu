@@ -238,6 +238,8 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap *map, i
     asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
                  "l"(map), "r"(bar), "r"(d), "r"(head), "r"(entry), "r"(page) : "memory");
 }
+// Fetches a map before its first copy asks for it.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
@@ -316,6 +318,10 @@ __global__ void __launch_bounds__(FEW_NT) k_window_few(Win A, int groups, int sp
     const int hk = (int)(bh % (uint32_t)a.kv_heads);
     const int64_t b = bh / (uint32_t)a.kv_heads, R0 = (int64_t)group * FEW_ROWS;
     if (threadIdx.x == 0) stop = 0;
+    if (BOXES && threadIdx.x == 0) {
+        prefetch_map(&maps.k);
+        prefetch_map(&maps.v);
+    }
     if (BOXES && lane == 0) {
         for (int i = 0; i < ST; ++i) bar_init(full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -767,6 +773,11 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
     const uint32_t q_full = v_fixed + 8 * ST, q_empty = q_full + 8 * TILES, s_full = q_empty + 8 * TILES, s_free = s_full + 8 * TILES;
     const uint32_t p_full = s_free + 8 * TILES, o_done = p_full + 8 * TILES, last_bar = o_done + 8 * TILES;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // (a join waits for this grid's end)
+    if (tid == 32) {
+        prefetch_map(&maps.q);
+        prefetch_map(&maps.kv.k);
+        prefetch_map(&maps.kv.v);
+    }
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             bar_init(k_full + 8 * i, 1);
