@@ -694,7 +694,8 @@ dbs_status dbs_cache_resize(const dbs_page_state *s, const int32_t *lens, int32_
     if (!state_ok(s, true) || columns < 0 || columns >= (int64_t(1) << 31)) return DBS_ERR_INVALID_ARG;
     if (s->batch == 0) return DBS_OK;
     const int64_t need = scratch_of(*s, columns), all = slots ? s->batch * columns : 0;
-    if (!lens || !status || (s->pages > 0 && !s->refs) || (need > 0 && (!scratch || !aligned16(scratch) || scratch_bytes < need)) || lens == s->kv_lens)
+    if (!lens || !status || (s->pages > 0 && !s->refs) || (need > 0 && (!scratch || !aligned16(scratch) || scratch_bytes < need)) || lens == s->kv_lens ||
+        status == s->kv_lens || status == lens)
         return DBS_ERR_INVALID_ARG;
     const bool here = all > 0 && all <= SLOTS_HERE;
     int32_t *at = (int32_t *)scratch;
@@ -772,7 +773,7 @@ dbs_status dbs_cache_compact(const dbs_cache_data *data, const dbs_page_state *s
         !data_ok(data, s, s->batch > 0))
         return DBS_ERR_INVALID_ARG;
     if (s->batch == 0) return DBS_OK;
-    if (!tree_lens || !new_lens || new_lens == s->kv_lens || (max_accepted > 0 && (!accepted || accepted_stride < 0)) ||
+    if (!tree_lens || !new_lens || new_lens == s->kv_lens || new_lens == tree_lens || new_lens == accepted_lens || (max_accepted > 0 && (!accepted || accepted_stride < 0)) ||
         (!s->page_table && (s->max_pages > 1 || s->pages < s->batch)) || (s->max_pages > 0 && s->pages < 1))
         return DBS_ERR_INVALID_ARG;
     Compact A{{}, *s, tree_lens, accepted, accepted_lens, max_accepted, accepted_stride, new_lens};

@@ -55,8 +55,9 @@ __device__ __forceinline__ Place place_of(const dbs_window_args &a, int64_t b, i
 __device__ __forceinline__ int window_start(const Win &A, int p) { return p >= A.window ? p - A.window + 1 : 0; }
 
 // One query row by one warp, entry by entry (every step-th of those it sees, from the
-// part-th on), touching only what the row sees.
-template <class T>
+// part-th on), touching only what the row sees.  OUT_ONLY: it ends once all of the output is NaN, so that l may
+// lack entries then.
+template <class T, bool OUT_ONLY = false>
 __device__ __forceinline__ void row_by_warp(const Win &A, const Seq &s, int64_t b, int t, int h, int part, int step, float &m, float &l,
                                             float (&o)[8])
 {
@@ -94,12 +95,18 @@ __device__ __forceinline__ void row_by_warp(const Win &A, const Seq &s, int64_t 
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (lane + 32 * e < a.head_dim) o[e] = fmaf(pr, to_f32(v[lane + 32 * e]), o[e] * keep);
+        if (OUT_ONLY) {
+            bool rest = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) rest |= lane + 32 * e < a.head_dim && o[e] == o[e];
+            if (!__any_sync(~0u, rest)) break;
+        }
     }
 }
 
 // Writes a row from its sums: out = o / l, lse = (m + log2 l) ln 2.
 template <class T>
-__device__ __forceinline__ void store_row(const Win &A, int64_t b, int t, int h, float m, float l, const float (&o)[8])
+__device__ __forceinline__ void store_out(const Win &A, int64_t b, int t, int h, float l, const float (&o)[8])
 {
     const dbs_window_args &a = A.a;
     const int lane = threadIdx.x & 31;
@@ -107,7 +114,13 @@ __device__ __forceinline__ void store_row(const Win &A, int64_t b, int t, int h,
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         if (lane + 32 * e < a.head_dim) out[lane + 32 * e] = from_f32<T>(l == 0.f ? 0.f : o[e] / l);
-    if (a.lse && lane == 0) a.lse[(b * a.tokens + t) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+template <class T>
+__device__ __forceinline__ void store_row(const Win &A, int64_t b, int t, int h, float m, float l, const float (&o)[8])
+{
+    const dbs_window_args &a = A.a;
+    store_out<T>(A, b, t, h, l, o);
+    if (a.lse && (threadIdx.x & 31) == 0) a.lse[(b * a.tokens + t) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 constexpr int ROW_NT = 128;
@@ -221,8 +234,27 @@ __device__ __forceinline__ Row row_of(const Win &A, const Seq &s, int hk, int64_
 
 // The matrix products give every row every entry of a tile, with probability 0 where it
 // is not seen, and 0 * NaN is NaN.  What no row of a unit sees is replaced by 0 on its way
-// through shared memory; a row whose result is not finite, because of an entry that others see or
-// of one of its own, is made anew by a warp from what it sees alone.
+// through shared memory; a row whose result is not finite, and of whose unit V has such a value at an entry that
+// others see and it does not, is made anew by a warp from what it sees alone.  (Those are the rows near such an
+// entry: what they all see costs them nothing more.)
+
+// Whether there is such a value for the row at position p (p >= 0), by a warp; heads in pieces of 16 bytes.
+template <class T> __device__ __forceinline__ bool spoiled(const Win &A, const Range &r, int64_t b, int hk, int p)
+{
+    const dbs_window_args &a = A.a;
+    const int lane = threadIdx.x & 31, chunks = a.head_dim / 8, begins = window_start(A, r.first), mine = window_start(A, p);
+    // entries lo .. mine - 1, which the row's window has passed, and p + 1 .. hi - 1, which come after it
+    const int lo = begins < A.sinks ? A.sinks : begins, past = mine > lo ? mine - lo : 0, n = past + r.hi - 1 - p;
+    constexpr uint32_t TOP = __is_same(T, __half) ? 0x7c00u : 0x7f80u;     // the exponent of infinity and NaN
+    bool bad = false;
+    for (int i = lane; i < n * chunks; i += 32) {
+        const int e = i / chunks;
+        const Place at = place_of(a, b, e < past ? lo + e : p + 1 + e - past);
+        const uint4 v = *((const uint4 *)((const T *)a.v + at.page * a.v_page + at.in * a.v_entry + hk * a.v_head) + (i - e * chunks));
+        for (uint32_t w : {v.x, v.y, v.z, v.w}) bad |= (w & TOP) == TOP || (w >> 16 & TOP) == TOP;
+    }
+    return __any_sync(~0u, bad);
+}
 
 // ---- few rows: every warp streams its own entries ----
 
@@ -583,15 +615,14 @@ __global__ void __launch_bounds__(FEW_NT) k_window_few(Win A, int groups, int sp
             out += fk == 0.f ? 0.f : fk * v[k];
         }
         if (row.p < 0) l = out = 0.f;
-        if (l == l && __any_sync(~0u, col < a.head_dim && !isfinite(out))) {
-            float ol[8], m1, l1;
-            row_by_warp<T>(A, s, b, row.t, row.h, 0, 1, m1, l1, ol);
+        float lo = l;                                                      // the output's divisor
+        if (l == l && __any_sync(~0u, col < a.head_dim && !isfinite(out)) && spoiled<T>(A, range, b, hk, row.p)) {
+            float ol[8], m1;
+            row_by_warp<T, true>(A, s, b, row.t, row.h, 0, 1, m1, lo, ol);
 #pragma unroll
             for (int e = 0; e < 8; ++e) out = e == e0 ? ol[e] : out;
-            l = l1;
-            top = m1;
         }
-        if (col < a.head_dim) ((T *)a.out + b * a.o_batch + row.t * a.o_token + row.h * a.o_head)[col] = from_f32<T>(l == 0.f ? 0.f : out / l);
+        if (col < a.head_dim) ((T *)a.out + b * a.o_batch + row.t * a.o_token + row.h * a.o_head)[col] = from_f32<T>(lo == 0.f ? 0.f : out / lo);
         if (a.lse && e0 == 0 && lane == 0) a.lse[(b * a.tokens + row.t) * a.q_heads + row.h] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
     }
     // (no block ends while another one reads its shared memory)
@@ -979,10 +1010,11 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
             }
             __syncwarp();                                                  // (what follows is written over it)
             for (unsigned again = __ballot_sync(~0u, odd != odd && ok && l == l); again; again &= again - 1) {
-                const int k = __ffs(again) - 1, tk = __shfl_sync(~0u, t, k), hh = __shfl_sync(~0u, h, k);
+                const int k = __ffs(again) - 1, tk = __shfl_sync(~0u, t, k), hh = __shfl_sync(~0u, h, k), pk = __shfl_sync(~0u, p, k);
+                if (!spoiled<T>(A, U.r, U.b, U.hk, pk)) continue;
                 float ol[8], m1, l1;
-                row_by_warp<T>(A, U.s, U.b, tk, hh, 0, 1, m1, l1, ol);
-                store_row<T>(A, U.b, tk, hh, m1, l1, ol);
+                row_by_warp<T, true>(A, U.s, U.b, tk, hh, 0, 1, m1, l1, ol);
+                store_out<T>(A, U.b, tk, hh, l1, ol);
             }
         }
     } else {
@@ -1181,7 +1213,7 @@ __global__ void __launch_bounds__(JOIN_NT) k_window_join(Win A, Cut C)
     const uint32_t heads = (uint32_t)a.kv_heads, per = (uint32_t)a.batch * heads, g = (uint32_t)u / per, bh = (uint32_t)u - g * per;
     const int64_t b = bh / heads;
     const int hk = (int)(bh % heads), row = tile_row % 128, dt = row / A.group;
-    const int t = (C.groups - 1 - (int)g) * TILES * C.tokens + tile_row / 128 * C.tokens + dt, h = hk * A.group + row - dt * A.group;
+    const int t0 = (C.groups - 1 - (int)g) * TILES * C.tokens, t = t0 + tile_row / 128 * C.tokens + dt, h = hk * A.group + row - dt * A.group;
     if (dt >= C.tokens || t >= a.tokens) return;
     const Seq s = sequence(A, b);
     const float *const parts = part_of<DP, TILES>(C, u, 0);
@@ -1206,15 +1238,18 @@ __global__ void __launch_bounds__(JOIN_NT) k_window_join(Win A, Cut C)
             o[e] += fk == 0.f ? 0.f : fk * x;
         }
     }
-    float m1 = top;
     bool odd = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         if (l == 0.f) o[e] = 0.f;
         odd |= !isfinite(o[e]);
     }
-    if (l == l && __any_sync(~0u, odd)) row_by_warp<T>(A, s, b, t, h, 0, 1, m1, l, o);
-    store_row<T>(A, b, t, h, m1, l, o);
+    store_row<T>(A, b, t, h, top, l, o);
+    if (l == l && __any_sync(~0u, odd) && spoiled<T>(A, range_of(A, s, t0, t0 + TILES * C.tokens - 1, 1), b, hk, s.first + t)) {
+        float m1, l1;
+        row_by_warp<T, true>(A, s, b, t, h, 0, 1, m1, l1, o);
+        store_out<T>(A, b, t, h, l1, o);
+    }
 }
 
 bool args_ok(const dbs_window_args *a)
@@ -1234,7 +1269,8 @@ bool args_ok(const dbs_window_args *a)
     for (int64_t stride : {a->q_batch, a->q_token, a->q_head, a->k_page, a->k_entry, a->k_head, a->v_page, a->v_entry, a->v_head,
                            a->page_row, a->o_batch, a->o_token, a->o_head})
         if (stride < 0) return false;
-    // heads of out that share memory
+    // out over the inputs, or heads of it that share memory
+    if (a->out == a->q || (entries > 0 && (a->out == a->k || a->out == a->v))) return false;
     if ((a->q_heads > 1 && a->o_head < a->head_dim) || (a->tokens > 1 && a->o_token < a->head_dim) ||
         (a->batch > 1 && a->o_batch < a->head_dim))
         return false;
@@ -1299,7 +1335,6 @@ dbs_status launch_few(const Win &A, const Maps &maps, cudaStream_t s)
     const int sms = multiprocessors();
     if (sms == 0) return DBS_ERR_CUDA;
     const int64_t rows = A.a.tokens * A.group, groups = (rows + FEW_ROWS - 1) / FEW_ROWS, units = A.a.batch * A.a.kv_heads * groups;
-    if (units * FEW_SPLIT >= int64_t(1) << 31) return DBS_ERR_INVALID_ARG;
     // Blocks of a unit: enough to fill the GPU's multiprocessors twice, with two turns of
     // its entries each at least.
     const int64_t turns = (line_of(A.a, FEW_ROWS) + FEW_KEYS - 1) / FEW_KEYS;

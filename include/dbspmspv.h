@@ -666,7 +666,8 @@ typedef struct {
     const int32_t *q_lens;     /* device [batch]; clamped to [0, tokens]; NULL = tokens */
     int64_t window, sinks;     /* window >= 1, sinks >= 0 */
     float scale;               /* finite */
-    void *out;                 /* [batch, tokens, q_heads, head_dim], each head in a place of its own */
+    void *out;                 /* [batch, tokens, q_heads, head_dim], each head in a place of its own, apart
+                                  from q and the caches */
     int64_t o_batch, o_token, o_head;
     float *lse;                /* device [batch, tokens, q_heads], natural logarithm, or NULL */
     void *scratch;             /* device, 32-byte aligned, dbs_window_attention_scratch bytes; the call
@@ -697,7 +698,7 @@ typedef struct {
 /* Gives every sequence a new length: cut (pages that it no longer owns lose a
  * reference; 0 frees it), or grown by free pages.  All cuts come before all growth;
  * then pages go to the sequences in their order.
- *   lens     device int32[batch]; below 0: the sequence stays as it is
+ *   lens     device int32[batch]; below 0: the sequence stays as it is (not kv_lens itself)
  *   status   device int32[batch]: 0, or why a sequence kept its length: 1 the free pages
  *            do not suffice for it and those before it that asked for pages, 2 it would
  *            grow into a page that others own too (fork it first), 3 it is longer than
@@ -740,7 +741,7 @@ dbs_status dbs_cache_fork(const dbs_cache_data *data, const dbs_page_state *stat
  *   accepted       device int32[batch, max_accepted], rows accepted_stride apart: ascending
  *                  numbers below tree_lens[b]; the first that is not (-1, say) ends the list
  *   accepted_lens  device int32[batch], or NULL = max_accepted
- *   new_lens       device int32[batch]: kv_lens[b] - tree_lens[b] + those kept (kv_lens stays; not its address)
+ *   new_lens       device int32[batch]: kv_lens[b] - tree_lens[b] + those kept (kv_lens stays); apart from the lists
  * Of `state` refs is not used; page_table may be NULL: sequence b is page b.  Drafted
  * entries have to lie in pages that b alone owns.  batch < 2^16, layers < 2^15.
  * Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */

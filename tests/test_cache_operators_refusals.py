@@ -87,7 +87,7 @@ def test_norm_gradient_nothing_to_do_and_scratch():
 
 
 WIN = dict(dtype=2, d=64, hq=8, hk=2, batch=2, tokens=3, q=A, q0=1536, q1=512, q2=64, k=A, v=A, k0=64, k1=64, k2=64, v0=64, v1=64, v2=64, pages=9,
-           page=16, pt=A, maxp=4, prow=4, kv=A, ql=0, window=5, sinks=0, scale=0.125, out=A, o0=1536, o1=512, o2=64, lse=0,
+           page=16, pt=A, maxp=4, prow=4, kv=A, ql=0, window=5, sinks=0, scale=0.125, out=2 * A, o0=1536, o1=512, o2=64, lse=0,
            scratch=A, bytes=1 << 40)
 
 
@@ -103,7 +103,8 @@ def window(**kw):
                                 dict(scale=float("inf")), dict(q0=-1), dict(q1=-1), dict(q2=-1), dict(k0=-1), dict(k1=-1), dict(k2=-1), dict(v0=-1),
                                 dict(v1=-1), dict(v2=-1), dict(prow=-1), dict(o2=63), dict(o1=0), dict(o0=0), dict(pt=0), dict(pt=0, maxp=1, pages=1),
                                 dict(batch=1 << 31), dict(tokens=1 << 31), dict(batch=1 << 16, tokens=1 << 15), dict(batch=1 << 14, tokens=1 << 14),
-                                dict(page=64, maxp=(1 << 25) - 1), dict(page=1 << 30, maxp=2), dict(page=(1 << 31) - 1, maxp=1), dict(pages=1 << 31)])
+                                dict(page=64, maxp=(1 << 25) - 1), dict(page=1 << 30, maxp=2), dict(page=(1 << 31) - 1, maxp=1), dict(pages=1 << 31),
+                                dict(out=A)])
 def test_window_refusals(kw):
     a = dict(WIN)
     a.update(kw)
@@ -144,12 +145,12 @@ def data(k=A, v=A, layers=2, heads=2, d=64, e=2, strides=(18432, 2048, 128, 64) 
 def test_resize_refusals():
     lib, big = _lib.load(), 1 << 40
 
-    def resize(s=state(), lens=2 * A, status=A, slots=0, columns=0, scratch=A, size=big):
+    def resize(s=state(), lens=2 * A, status=3 * A, slots=0, columns=0, scratch=A, size=big):
         return lib.dbs_cache_resize(s, lens, status, slots, columns, scratch, size, None)
 
     large = state(batch=2000)                                              # (few sequences need no scratch)
     for kw in (dict(s=None), dict(lens=0), dict(status=0), dict(columns=-1), dict(columns=1 << 31), dict(s=large, scratch=0),
-               dict(s=large, scratch=A + 4), dict(s=large, size=16), dict(s=state(refs=0)), dict(lens=A)):
+               dict(s=large, scratch=A + 4), dict(s=large, size=16), dict(s=state(refs=0)), dict(lens=A), dict(status=A), dict(status=2 * A)):
         assert resize(**kw) == BAD, kw
     assert resize(s=state(batch=0, kv=0, table=0), lens=0, status=0, scratch=0) == OK
     need = ctypes.c_int64(-1)
@@ -188,7 +189,7 @@ def test_compact_refusals():
     def compact(d=data(), s=state(), tree=A, acc=A, most=4, stride=4, lens=0, new=2 * A):
         return lib.dbs_cache_compact(d, s, tree, acc, most, stride, lens, new, None)
 
-    cases = [dict(d=None), dict(s=None), dict(tree=0), dict(acc=0), dict(most=-1), dict(most=1 << 31), dict(stride=-1), dict(new=0), dict(new=A),
+    cases = [dict(d=None), dict(s=None), dict(tree=0), dict(acc=0), dict(most=-1), dict(most=1 << 31), dict(stride=-1), dict(new=0), dict(new=A), dict(tree=2 * A), dict(lens=2 * A),
              dict(s=state(batch=65536)), dict(s=state(table=0)), dict(s=state(table=0, maxp=1, pages=2)), dict(s=state(pages=0))]
     cases += [dict(d=data(**kw)) for kw in BAD_DATA]
     for kw in cases:

@@ -830,3 +830,164 @@ def test_captured_and_replayed_on_another_stream():
         torch.cuda.synchronize()
         for a, b in zip((*got, *state2, kc2, vc2), want):
             assert torch.equal(a, b)
+
+
+# ---- what is not finite and seen, calls at once, far and many places ----
+
+
+@pytest.mark.parametrize("T,hq,hk,D,S,page", [(1, 8, 2, 128, 4000, 16), (1, 4, 4, 64, 300, 5), (7, 4, 2, 256, 900, 0), (40, 4, 1, 64, 2000, 16),
+                                              (600, 8, 2, 128, 1500, 16), (900, 2, 1, 256, 960, 64), (20, 3, 1, 40, 500, 3)])
+def test_window_not_finite_values_that_all_rows_see(T, hq, hk, D, S, page):
+    """Values are taken column by column, and sums (lse) do not take them at all."""
+    rng = np.random.default_rng(T + D)
+    q, k, v, table = window_inputs(rng, "bf16", 1, T, hq, hk, D, S, page)
+    kw = dict(sinks=2, page_table=None if table is None else ints(table), return_lse=True)
+    out, lse = dbs.window_attention(q, k, v, ints([S]), S, **kw)
+    at = (0, 1) if table is None else (int(table[0, 0]), 1) if page > 1 else (int(table[0, 1]), 0)     # entry 1, a sink
+    for column, value in ((3, NAN), (D - 1, INF)):
+        v2 = v.clone()
+        v2[at][..., column] = value
+        got, gl = dbs.window_attention(q, k, v2, ints([S]), S, **kw)
+        rest = [c for c in range(D) if c != column]
+        assert torch.equal(gl, lse) and torch.equal(got[..., rest], out[..., rest])
+        assert not torch.isfinite(got[..., column]).any()
+    got, gl = dbs.window_attention(q, k, torch.full_like(v, NAN), ints([S]), S, **kw)
+    assert torch.equal(gl, lse) and torch.isnan(got).all()
+    # from the middle on: rows before it stay, the others have NaN
+    v2, p = v.clone(), S - (T + 1) // 2
+    flat = v2 if table is None else v2[torch.from_numpy(table[0]).long().to(DEV)].reshape(1, -1, hk, D)
+    flat[:, p:] = NAN
+    if table is not None:
+        v2[torch.from_numpy(table[0]).long().to(DEV)] = flat.reshape(-1, page, hk, D)
+    got, gl = dbs.window_attention(q, k, v2, ints([S]), S, **kw)
+    before = p - (S - T)
+    o, mag, _ = window_ref(f64(q), f64(k), f64(v), [S], [T], S, 2, D**-0.5, table)
+    close(got[:, :before], o[:, :before], (U["bf16"] + 3e-4) * mag[:, :before] + U["bf16"] * np.abs(o[:, :before]))
+    assert torch.isnan(got[:, before:]).all() and torch.equal(gl, lse)
+
+
+def test_calls_at_once_on_two_streams_and_in_two_graphs():
+    """Two sets of tensors, their calls on two streams and as two graphs replayed at once, give what each gives alone."""
+    rng = np.random.default_rng(41)
+    page, D = 16, 128
+    sets = []
+    for B, T, hq, hkv, S in ((2, 90, 8, 2, 700), (5, 1, 8, 1, 1500)):
+        q, k, v, table = window_inputs(rng, "f16", B, T, hq, hkv, D, S, page)
+        x = rnd(rng, "f16", B, T, hkv, D)
+        pool = Pool(B + 1, k.shape[0] // B, 3 * k.shape[0], page)
+        pool.resize([100 + 7 * b for b in range(B)] + [0])
+        sets.append(dict(q=q, k=k, v=v, table=ints(table), kv=ints([S - 3 * b for b in range(B)]), x=x, w=rnd(rng, "f16", D),
+                         rot=dbs.rotary_table(256, D), pos=ints(rng.integers(0, 256, (B, T))), state=pool.device(), start=pool.device(),
+                         lens=ints([100 + 20 * b for b in range(B)] + [-1]), caches=make_caches(rng, 1, hkv, D, "f16", 4, 3 * k.shape[0], page),
+                         parents=ints([B - 1]), children=ints([B])))
+
+    def run(s, **kw):
+        for a, b in zip(s["state"], s["start"]):
+            a.copy_(b)
+        out = dbs.window_attention(s["q"], s["k"], s["v"], s["kv"], 600, sinks=4, page_table=s["table"], return_lse=True, **kw)
+        grads = dbs.norm_rotary_gradient(s["q"], s["x"], s["q"], s["x"], s["w"], s["w"], s["rot"], s["pos"], **kw)
+        turned_ = dbs.norm_rotary(s["q"], s["x"], s["w"], s["w"], s["rot"], s["pos"], **kw)
+        grown = dbs.cache_resize(*s["state"], s["lens"], page, columns=40, **kw)
+        forked = dbs.cache_fork(*s["caches"], *s["state"], s["parents"], s["children"], **kw)
+        return [*out, *grads, *turned_, *grown, forked, *s["state"]]
+
+    want = [[t.clone() for t in run(s)] for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for s, stream in zip(sets, streams):
+            with torch.cuda.stream(stream):
+                got.append([t.clone() for t in run(s)])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+    # a stream given by hand
+    out = dbs.window_attention(sets[0]["q"], sets[0]["k"], sets[0]["v"], sets[0]["kv"], 600, sinks=4, page_table=sets[0]["table"], stream=streams[1])
+    streams[1].synchronize()
+    assert torch.equal(out, want[0][0])
+    graphs, got = [], []
+    for s, stream in zip(sets, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            got.append(run(s))
+        graphs.append(g)
+    for _ in range(5):
+        for g, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+    assert dbs.operators_check() == 0
+
+
+def test_caches_past_32_bits():
+    """Entries behind 2^32 elements: appended, seen, forked and compacted as those of a small cache are."""
+    rng = np.random.default_rng(51)
+    page, heads, D, hq, dt = 16, 8, 128, 16, "bf16"
+    per, far = 4, (1 << 32) // (16 * 8 * 128) + 5                          # the numbers of the pages in use begin there
+    big = [torch.empty((far + 12, page, heads, D), dtype=DT[dt], device=DEV) for _ in range(2)]
+    small = [torch.zeros((12, page, heads, D), dtype=DT[dt], device=DEV) for _ in range(2)]
+    for c in big:
+        c[far:] = 0
+    B, T, w, table = 2, 40, rnd(rng, "f32", D), dbs.rotary_table(64, D)
+    q, k, v = rnd(rng, dt, B, T, hq, D), rnd(rng, dt, B, T, heads, D), rnd(rng, dt, B, T, heads, D)
+    pos = ints(np.tile(np.arange(T), (B, 1)))
+    results = []
+    for caches, first in ((small, 0), (big, far)):
+        refs = torch.zeros(first + 12, dtype=torch.int32, device=DEV)
+        refs[:first] = 1                                                   # (taken by others)
+        state = [torch.full((B + 1, per), -1, dtype=torch.int32, device=DEV), ints([0] * (B + 1)), refs]
+        status, slots = dbs.cache_resize(*state, ints([T, T, -1]), page, columns=T)
+        qt = dbs.norm_rotary_append(q, k, v, w, w, table, pos, *caches, slots[:B])
+        outs = [dbs.window_attention(qt, *caches, state[1][:B], 25, sinks=2, page_table=state[0][:B]),
+                dbs.window_attention(qt[:, -1:], *caches, state[1][:B], 25, sinks=2, page_table=state[0][:B])]
+        forked = dbs.cache_fork(*caches, *state, ints([1]), ints([2]))
+        lens = dbs.cache_compact(*caches, state[1], ints([7, 8, 0]), ints([[0, 2, 5], [3, 4, 7], [-1, -1, -1]]), page_table=state[0])
+        results.append([status, torch.where(slots < 0, -1, slots - first * page), torch.where(state[0] < 0, -1, state[0] - first), state[1], refs[first:],
+                        qt, *outs, forked, lens, *(c[first:] for c in caches)])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    del big, caches, results
+    torch.cuda.empty_cache()
+
+
+def test_many_sequences():
+    """More sequences than a grid's second and third dimension have blocks, or one less where that is the limit."""
+    rng = np.random.default_rng(61)
+    B, D = 70000, 64
+    q, k, v, _ = window_inputs(rng, "f16", B, 1, 2, 1, D, 3, 0)
+    kv = rng.integers(0, 4, B)
+    out = dbs.window_attention(q, k, v, ints(kv), 2, sinks=1)
+    some = np.r_[0:20, 32760:32780, 65530:65545, B - 20:B]
+    at = torch.from_numpy(some).to(DEV)
+    o, mag, _ = window_ref(f64(q[at]), f64(k[at]), f64(v[at]), kv[some], [1] * len(some), 2, 1, D**-0.5)
+    close(out[at], o, (U["f16"] + 3e-4) * mag + U["f16"] * np.abs(o) + ETA["f16"])
+    n, page = 65535, 2
+    pool = Pool(2 * n + 1, 1, n + 5, page)
+    pool.resize([1] + [0] * (2 * n))
+    state = pool.device()
+    caches = make_caches(rng, 1, 1, 8, "f16", 4, n + 5, page)
+    host = [plain(c).clone() for c in caches]
+    parents, children = np.zeros(n, np.int32), np.arange(1, n + 1, dtype=np.int32)
+    assert np.array_equal(dbs.cache_fork(*caches, *state, ints(parents), ints(children)).cpu().numpy(), pool.fork(parents, children, *host))
+    pool.same(state)
+    assert all(torch.equal(plain(c), h) for c, h in zip(caches, host))
+    lens = np.where(np.arange(2 * n + 1) < 3, 2, -1).astype(np.int32)
+    lens[n:] = 1
+    want = pool.resize(lens)
+    assert np.array_equal(dbs.cache_resize(*state, ints(lens), page)[0].cpu().numpy(), want[0])
+    pool.same(state)
+
+
+def test_inputs_that_require_a_gradient_are_refused():
+    q = torch.zeros((1, 2, 2, 64), dtype=torch.float16, device=DEV, requires_grad=True)
+    x, w, table, i = q.detach(), torch.ones(64, device=DEV, requires_grad=True), dbs.rotary_table(4, 64), ints([0, 1])
+    one = ints([2])
+    for call in (lambda: dbs.norm_rotary(q, None, None, None, table, i), lambda: dbs.norm_rotary(x, None, w, None, table, i),
+                 lambda: dbs.norm_rotary_gradient(x, None, x, None, w, None, table, i), lambda: dbs.window_attention(q, x, x, one, 4),
+                 lambda: dbs.window_attention(x, x, q, one, 4), lambda: dbs.cache_compact(q, x, one, one, ints([[0]]))):
+        with pytest.raises(dbs.DbsError, match="requires a gradient"):
+            call()
+    with torch.no_grad():
+        assert torch.equal(dbs.norm_rotary(q, None, w, None, table, i)[0], torch.zeros_like(x))
+    with pytest.raises(dbs.DbsError):
+        dbs.window_attention(x, x, x, one, 4, out=x)
