@@ -9,10 +9,12 @@ using namespace dbs::ops;
 namespace {
 
 constexpr int NT = 256;
-// Blocks of a multiprocessor and heads whose loads are issued together, for heads of one unit a lane
-// (16,382 tokens of 40 heads of 128, bf16: 3 and 2 71 us, 2 and 4 81, 4 and 1 78; the gradient of 8192
-// tokens of 32 heads of 96, f32: 2 and 2 69 us, 3 and 1 79).
-constexpr int FORWARD_BLOCKS = 3, FORWARD_HEADS = 2, BACKWARD_BLOCKS = 2, BACKWARD_HEADS = 2;
+// Blocks of a multiprocessor, heads whose loads are issued together, and heads of a thread at most, for
+// heads of one unit a lane.  Forward the next heads are loaded before these are worked on (16,382 tokens of 40 heads of
+// 128, bf16: 2, 3 and 12 60 us, 2, 3 and 8 61, 2, 2 and 8 66, 3, 1 and 8 67, 2, 4 and 16 78 (registers spilled);
+// without that 3, 2 and 8 71).  The gradient has no registers left for it (8192 tokens of 32 heads of 96, f32: 2, 2 and 8 66 us,
+// 2, 2 and 4 69, 3 and 1 79; loading ahead 68 with one head, 78 with two).
+constexpr int FORWARD_BLOCKS = 2, FORWARD_HEADS = 3, FORWARD_SPAN = 12, BACKWARD_BLOCKS = 2, BACKWARD_HEADS = 2, BACKWARD_SPAN = 8;
 
 // What a lane moves at once: N values, 16 or 8 bytes, or one where rows are not aligned for that.
 template <class T, int N> struct Piece {
@@ -290,8 +292,8 @@ struct Norm {
 
 // blockIdx.y: the chunks of `span` heads of every group; blockIdx.x: the tokens, L
 // lanes each.  A group of lanes keeps its token's angles and its weights for up to
-// `span` heads, HEADS of whose loads are issued together.  Bound by HBM: every entry is
-// read and written once.
+// `span` heads, HEADS of whose loads are issued together, while the HEADS before them are worked on.  Bound by HBM:
+// every entry is read and written once (338 MB in 60 us, 83% of the memory's rate).
 template <class T, bool INTERLEAVED, int N, int K>
 __global__ void __launch_bounds__(NT, K == 1 ? FORWARD_BLOCKS : 1) k_norm_rotary(Norm A, int span)
 {
@@ -324,14 +326,14 @@ __global__ void __launch_bounds__(NT, K == 1 ? FORWARD_BLOCKS : 1) k_norm_rotary
         dst += b * P.out_batch + t * P.out_token;
     }
     const typename L::Units units(H, lane);
-    typename L::VT x[HEADS][K][2];
-    auto fetch = [&](int h) {
+    typename L::VT x[HEADS][K][2], next[HEADS][K][2];
+    auto fetch = [&](int h, typename L::VT (&to)[HEADS][K][2]) {
 #pragma unroll
         for (int k = 0; k < HEADS; ++k)
-            if (h + k < heads) L::load(units, src + k * P.in_head, x[k]);
+            if (h + k < heads) L::load(units, src + k * P.in_head, to[k]);
         src += HEADS * P.in_head;
     };
-    fetch(0);
+    fetch(0, x);
     uint64_t own[K][N], other[K][N];
     if (norm) {
         float cs[K][N], sn[K][N], w[K][2 * N];
@@ -340,8 +342,9 @@ __global__ void __launch_bounds__(NT, K == 1 ? FORWARD_BLOCKS : 1) k_norm_rotary
 #pragma unroll
         for (int c = 0; c < K; ++c) L::turns(cs[c], sn[c], w[c], own[c], other[c]);
     }
+#pragma unroll 1
     for (int h = 0; h < heads; h += HEADS) {
-        if (h) fetch(h);
+        fetch(h + HEADS, next);
 #pragma unroll
         for (int k = 0; k < HEADS; ++k) {
             if (h + k >= heads) break;
@@ -365,6 +368,13 @@ __global__ void __launch_bounds__(NT, K == 1 ? FORWARD_BLOCKS : 1) k_norm_rotary
             }
             if (write) L::store(units, dst + k * P.out_head, x[k]);
         }
+#pragma unroll
+        for (int k = 0; k < HEADS; ++k)
+#pragma unroll
+            for (int c = 0; c < K; ++c) {
+                x[k][c][0] = next[k][c][0];
+                x[k][c][1] = next[k][c][1];
+            }
         dst += HEADS * P.out_head;
     }
 }
@@ -377,13 +387,13 @@ dbs_status launch_norm(Norm &A, int head_dim, int dim, cudaStream_t s)
     const int lanes = A.head.lanes > A.copy.lanes ? A.head.lanes : A.copy.lanes;
     const int64_t room = (int64_t)multiprocessors() * 2048;
     if (room == 0) return DBS_ERR_CUDA;
-    // Heads of a thread: eight, so that angles and weights are read once for all of them,
+    // Heads of a thread: many, so that angles and weights are read once for all of them,
     // and fewer while that leaves some of the GPU's threads idle.
-    int span = 8, chunks = 0;
+    int span = FORWARD_SPAN, chunks = 0;
     for (;; span /= 2) {
         chunks = 0;
         for (int p = 0; p < A.nparts; ++p) chunks += (A.part[p].heads.heads + span - 1) / span;
-        if (span == 1 || A.total * lanes * chunks >= room || 2 * chunks > 65535) break;
+        if (span == 1 || A.total * lanes * chunks >= room) break;          // (at most 3 * 16384 chunks)
     }
     k_norm_rotary<T, INTERLEAVED, N, K><<<dim3((unsigned)((A.total * lanes + NT - 1) / NT), (unsigned)chunks), NT, 0, s>>>(A, span);
     return launched();
@@ -408,7 +418,8 @@ struct Gradient {
 // A group of lanes takes a token's heads, HEADS at a time, then the next token that is
 // the grid's turn; what the heads give to weight' stays in its registers.  In the end the block's
 // groups are added up in their order and written to scratch, and k_norm_weight adds the blocks.
-// Bound by HBM: two entries are read and one is written.
+// Bound by HBM: two entries are read and one is written (303 MB in 66 us, 68% of the memory's rate: waiting
+// for it, with as many loads under way as registers hold).
 template <class T, bool INTERLEAVED, int N, int K>
 __global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradient(Gradient A, int span)
 {
@@ -439,7 +450,8 @@ __global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradi
     for (int64_t i0 = (int64_t)block * groups + first; i0 < items; i0 += step) {
         const int64_t i = i0 + (group - first);
         const bool in = i < items;
-        const uint32_t tok = in ? (uint32_t)(i / chunks) : 0u, chunk = in ? (uint32_t)(i - (int64_t)tok * chunks) : 0u;
+        // (neighbours have neighbouring tokens: 66 us, with a token's chunks side by side 68)
+        const uint32_t chunk = in ? (uint32_t)(i / A.total) : 0u, tok = in ? (uint32_t)(i - chunk * A.total) : 0u;
         const uint32_t b = tok / (uint32_t)A.tokens, t = tok - b * (uint32_t)A.tokens;
         const int h0 = (int)chunk * span, heads = P.heads - h0 < span ? P.heads - h0 : span;
         const T *g = (const T *)P.grad + b * P.grad_batch + t * P.grad_token + h0 * P.grad_head;
@@ -550,7 +562,7 @@ dbs_status launch_gradient(Gradient &A, int head_dim, int dim, cudaStream_t s)
     if (sms == 0) return DBS_ERR_CUDA;
     A.room = sms * BACKWARD_BLOCKS;
     // Heads of a turn: as for the forward pass
-    int span = 8;
+    int span = BACKWARD_SPAN;
     int64_t heads = 0;
     for (int p = 0; p < A.nparts; ++p) heads += A.part[p].heads;
     for (; span > 1; span /= 2) {
