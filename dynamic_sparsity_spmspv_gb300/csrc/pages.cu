@@ -272,7 +272,9 @@ __device__ __forceinline__ int found_page(const dbs_page_state &s, const Turn &T
 }
 
 // At most PLAN_NT sequences.  Cuts, new pages and slots are shared out among all threads one by one, so
-// that long sequences take no longer than short ones; refs are read beside the lengths.
+// that long sequences take no longer than short ones; refs are read beside the lengths.  Bound by the latency of
+// some twenty block-wide steps and three reads in a row (8, 256 and 1024 sequences, a slot each: 5.8, 6.5 and 7.1 us; by
+// k_resize 5.9, 15.6 and 46).
 __global__ void __launch_bounds__(PLAN_NT) k_resize_few(Resize A, int slots_here)
 {
     __shared__ Sums S;
@@ -444,18 +446,22 @@ __global__ void __launch_bounds__(PLAN_NT) k_fork_plan(dbs_page_state s, const i
     }
 }
 
-// The same for at most PLAN_NT forks, in shared memory: a child is taken if no valid one before names it.
+// The same for at most PLAN_NT forks, in shared memory: the children are kept in a table twice as large as they
+// are many, each with the first valid fork that names it.  (4, 256 and 1024 forks with the copies of two small
+// states 7.2, 8.5 and 13.4 us; by the other kernel 9.3, 10.7 and 16.6; with a comparison of every two children 7, 15 and 41.)
 __global__ void __launch_bounds__(PLAN_NT) k_fork_plan_few(dbs_page_state s, const int32_t *parents, const int32_t *children, int n,
                                                            int32_t *status, Fork *forks, int32_t *list)
 {
     __shared__ Sums S;
     __shared__ Turn T;
-    __shared__ int named[PLAN_NT];
+    __shared__ int child[2 * PLAN_NT], by[2 * PLAN_NT];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int t = threadIdx.x, page = (int)s.page_size;
     const bool mine = t < n;
     const int p = mine ? parents[t] : -1, c = mine ? children[t] : -1;
     const Run run = run_of(s, 0);
+    child[t] = child[t + PLAN_NT] = -1;
+    by[t] = by[t + PLAN_NT] = PLAN_NT;
     bool good = p >= 0 && p < s.batch && c >= 0 && c < s.batch;
     const int len = good ? length(s, p) : 0, taken = good ? length(s, c) : 1;
     good = good && taken == 0;
@@ -463,9 +469,18 @@ __global__ void __launch_bounds__(PLAN_NT) k_fork_plan_few(dbs_page_state s, con
     if (good && f.entries) f.from = __ldcg(s.page_table + p * s.page_row + f.full);
     const uint32_t free = word_of(run.free);
     if (!(t & 1)) T.free[t >> 1] = free;
-    named[t] = good ? c : -1;
     __syncthreads();
-    for (int i = 0; good && i < t; ++i) good = named[i] != c;
+    uint32_t at_child = (uint32_t)c * 2654435769u >> 21;           // (Fibonacci hashing: 2^32 over the golden ratio, 11 bits)
+    static_assert(2 * PLAN_NT == 1 << 11, "11 bits");
+    if (good) {
+        for (;; at_child = (at_child + 1) % (2 * PLAN_NT)) {       // (ends: at least half of the places stay free)
+            const int there = atomicCAS(child + at_child, -1, c);
+            if (there == -1 || there == c) break;
+        }
+        atomicMin(by + at_child, t);
+    }
+    __syncthreads();
+    good = good && by[at_child] == t;
     const int need = good && f.entries > 0, at = (int)before(need, S), asked = (int)S.total;
     const int found = find_few(s, asked, T, list, S);
     const bool fits = good && (!need || at < found);
@@ -539,7 +554,8 @@ struct Compact {
 constexpr int MOVE_NT = 256;               // threads of a block, at most: as many as an entry has units
 
 // blockIdx.z: the sequence; y: K or V of a layer; x: units of an entry, one a thread.
-// Numbers ascend, so place i is behind no number that comes later: a thread may load any of its
+// Bound by latency: lengths and lists, page table and entries are three reads in a row (16 layers, 32 sequences of up to
+// 48 drafted tokens: 18 MB in 8.2 us).  Numbers ascend, so place i is behind no number that comes later: a thread may load any of its
 // units before it stores those of earlier places, in the list's order.
 template <class V>
 __global__ void __launch_bounds__(MOVE_NT) k_compact(Compact A)
@@ -667,8 +683,9 @@ template <class F> dbs_status by_unit(int unit, F f)
 
 constexpr int64_t up16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
-// Slots that the one block writes; of more a second launch is through earlier.
-constexpr int64_t SLOTS_HERE = 8 * PLAN_NT;
+// Slots that the one block writes; of more a second launch is through earlier (64, 2048, 8192 and 32,768 slots: 5.8, 6.5, 9.6
+// and 18.4 us in the one block, 6.9, 7.2, 8.5 and 9.7 with a second).
+constexpr int64_t SLOTS_HERE = 4 * PLAN_NT;
 
 // Scratch of a resize: of few sequences only what does not stay in shared memory.
 int64_t scratch_of(const dbs_page_state &s, int64_t columns)

@@ -10,7 +10,8 @@ the same text.  A layer is
     x += w4_linear(a);  x += decode_layer(down, relu(w4_linear(norm(x))))
 
 with the last product on a sparse matrix in the dual-view blocked format, and the
-logits go through penalize_logits.
+logits go through penalize_logits.  cache_compact keeps the entries of the drafted
+tokens that were right.
 """
 import os
 import sys
@@ -71,8 +72,7 @@ class Sequence:
     def __init__(self, model, prompt, seed):
         self.model, self.tokens, self.prompt = model, [], len(prompt)
         self.pages = torch.from_numpy(np.random.default_rng(seed).permutation(PAGES).astype(np.int32)).to(DEV)[None]
-        shape = (PAGES, PAGE, KV_HEADS, DIM)
-        self.cache = [(torch.zeros(shape, dtype=DT, device=DEV), torch.zeros(shape, dtype=DT, device=DEV)) for _ in range(LAYERS)]
+        self.k, self.v = (torch.zeros((LAYERS, PAGES, PAGE, KV_HEADS, DIM), dtype=DT, device=DEV) for _ in range(2))
         self.step(prompt[:-1], list(range(-1, len(prompt) - 2)))            # a chain: each token's parent is the one before
         self.tokens = list(prompt[:-1])
         self.last = prompt[-1]
@@ -96,10 +96,11 @@ class Sequence:
         tree = torch.from_numpy(bits.view(np.int64)).to(DEV)
         positions = torch.tensor([before + len(p) - 1 for p in paths], dtype=torch.int32, device=DEV)
         slots = self.entries(np.arange(before, before + n))
-        lens = torch.tensor([before + n], dtype=torch.int32, device=DEV)
+        lens = self.lens = torch.tensor([before + n], dtype=torch.int32, device=DEV)
+        self.drafted = torch.tensor([n], dtype=torch.int32, device=DEV)
 
         x = m.embedding[torch.tensor(tokens, device=DEV)]
-        for (qkv, out, up, down, ws), (kc, vc) in zip(m.layers, self.cache):
+        for (qkv, out, up, down, ws), kc, vc in zip(m.layers, self.k, self.v):
             q, k, v = qkv(norm(x)).unflatten(1, (-1, DIM)).split([HEADS, KV_HEADS, KV_HEADS], 1)
             q = dbs.rotary_append(q, k, v, m.table, positions, kc, vc, slots)
             a = dbs.tree_attention(q[None], kc, vc, lens, tree, page_table=self.pages)
@@ -119,13 +120,8 @@ class Sequence:
                                    frequency=0.05 * rows)
 
     def keep(self, path):
-        """Takes the drafted tokens on `path` into the text: their entries move to its end."""
-        before = len(self.tokens)
-        src, dst = self.entries([before + t for t in path]).long(), self.entries([before + i for i in range(len(path))]).long()
-        for pair in self.cache:
-            for c in pair:
-                flat = c.view(-1, KV_HEADS, DIM)
-                flat[dst] = flat[src]
+        """Takes the drafted tokens on `path` into the text: their entries move to its end, in all layers."""
+        dbs.cache_compact(self.k, self.v, self.lens, self.drafted, torch.tensor([path], dtype=torch.int32, device=DEV), page_table=self.pages)
 
     def advance(self, drafts, parents):
         """One step: the last token and drafted ones behind it (a parent of 0: the last token).  Returns the tokens that

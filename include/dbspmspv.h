@@ -432,9 +432,9 @@ dbs_status dbs_spmspv_dense_noalloc_check(void *stream);
  * statistics and rotations are fp32; every result is rounded once, to its own type
  * (and attention's probabilities to the caches', see there).
  *
- * Waits inside the kernels of dbs_w4_linear and dbs_tree_attention end after two
- * seconds: the block gives up and leaves NaN in what it had not finished (in lse
- * too). */
+ * Waits inside the kernels of dbs_w4_linear, dbs_tree_attention and
+ * dbs_window_attention end after two seconds: the block gives up and leaves NaN in
+ * what it had not finished (in lse too). */
 
 /* Whether such a wait ran out on the current device since the last check, in
  * calls on `stream` or calls that have ended: synchronizes the stream and returns
@@ -648,7 +648,7 @@ dbs_status dbs_norm_rotary_gradient(const dbs_norm_gradient_heads *parts, int32_
  * G = q_heads / kv_heads.  A token that sees none gets 0 and lse -inf, and so do the tokens
  * t >= q_lens[b].  Entries that a token does not see take no part in its row, whatever they
  * hold (NaN included).  Each probability is rounded once to `dtype` before it meets v where the products
- * run on tensor cores (their sum, and so lse, takes them in fp32). */
+ * run on tensor cores (their sum, and so lse, takes them in fp32; one that rounds to 0 gives NaN with an infinite v). */
 typedef struct {
     dbs_dtype dtype;           /* DBS_F16 or DBS_BF16, of q, caches and out */
     int32_t head_dim;          /* 1..256 */
