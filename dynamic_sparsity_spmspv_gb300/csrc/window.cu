@@ -126,7 +126,8 @@ __device__ __forceinline__ void store_row(const Win &A, int64_t b, int t, int h,
 constexpr int ROW_NT = 128;
 
 // Any head size and alignment: one block per query row, its warps take every fourth
-// entry, a lane every 32nd value.
+// entry, a lane every 32nd value.  Bound by the latency of each entry's sum: one token, window 1024, 176 us; a prompt
+// of 8192 tokens, window 4096, 150 ms.
 template <class T>
 __global__ void __launch_bounds__(ROW_NT) k_window_rows(Win A)
 {
@@ -326,7 +327,8 @@ template <int DP> struct Few {
 //
 // BOXES: K and V come by tiled copies (TMA) of boxes of 16 entries, or of 8 where pages split
 // into eights only; else by 16-byte asynchronous copies.  Bound by HBM where many tokens'
-// windows are read, by latency for one.
+// windows are read (64 sequences of one token, 32/8 heads of 128, window 4096: 170 us, 93% of the memory's rate), by latency for
+// one (window 1024: 7.5 us on the device, 10.3 as a call).
 template <class T, int DP, bool BOXES>
 __global__ void __launch_bounds__(FEW_NT) k_window_few(Win A, int groups, int split, const __grid_constant__ Maps maps)
 {
@@ -639,17 +641,19 @@ __global__ void __launch_bounds__(FEW_NT) k_window_few(Win A, int groups, int sp
 // P, rounded to the caches' type, goes to tensor memory too, so that the second product reads only V from
 // shared memory.  It has columns of its own: the next tile's scores are made as soon as this one's have been read, and
 // wait for no product (with P over S and tiles of 128, or of 64 with two buffers: 463 and 376 us for the prompt
-// below, here 329).  That leaves room for tiles of 80 at head_dim 128.  Warps have roles: four for each row tile do
+// below, here 328).  That leaves room for tiles of 80 at head_dim 128.  Warps have roles: four for each row tile do
 // the softmax, a thread a row; one fetches Q and K, one V, one for each row tile issues its products (one for
 // both: 671), one clears what no row of the unit sees in V.
 //
 // A row tile skips the tiles that none of its rows sees.  Blocks walk over the units, long ones
 // first; of few units `split` blocks take a part each, and k_window_join joins their outputs.
 //
-// A prompt of 8192 tokens, window 4096, 32/8 heads of 128: 329 us, 66% of the tensor cores' rate, of whose cycles 56%
+// A prompt of 8192 tokens, window 4096, 32/8 heads of 128: 328 us, 66% of the tensor cores' rate, of whose cycles 56%
 // are busy.  A step of a pair of row tiles takes 2100 cycles of a softmax thread for 80 entries, most of them
 // latencies of its own chain (reading 200, maximum 400, powers of two 800, waits 400), with two such warps a
-// scheduler; two threads a row, which halve it, have to exchange maxima: 371 us.  8 sequences of 8 tokens,
+// scheduler.  Without its arithmetic 265 us are left: reading scores, storing P, and the products, whose Q comes anew from
+// shared memory for each tile.  Two threads a row, which halve the chain, have to exchange maxima: 371 us; powers taken
+// beside the maximum, with the one so far, and again where it grew: 330; waits that sleep: 330.  8 sequences of 8 tokens,
 // 32/4 heads, window 2047 and 64 sinks: 18.5 us in two launches, six tiles a block.
 //
 // Every wait on a barrier has a limit; a block whose wait runs out stops, leaves NaN in
@@ -1335,12 +1339,15 @@ dbs_status launch_few(const Win &A, const Maps &maps, cudaStream_t s)
     const int sms = multiprocessors();
     if (sms == 0) return DBS_ERR_CUDA;
     const int64_t rows = A.a.tokens * A.group, groups = (rows + FEW_ROWS - 1) / FEW_ROWS, units = A.a.batch * A.a.kv_heads * groups;
-    // Blocks of a unit: enough to fill the GPU's multiprocessors twice, with two turns of
-    // its entries each at least.
+    // Blocks of a unit: enough to fill the GPU's multiprocessors twice, up to four with a turn of its entries each,
+    // eight with more than one, more with four or more: a turn takes 1.2 us, a join of eight or sixteen blocks
+    // longer.  (One token, 8 kv heads of 128: 200 entries 6.8 us, in one block 8.1; 1024 in eight blocks 7.5, in
+    // sixteen 8.0; 8192 in sixteen 13.6, in four 30; 32768 34.9 and 105.)
     const int64_t turns = (line_of(A.a, FEW_ROWS) + FEW_KEYS - 1) / FEW_KEYS;
     const int most = DP == 256 ? 8 : FEW_SPLIT;
     int split = 1;
-    while (split < most && units * split * 2 <= 2 * sms && turns >= 4 * split) split *= 2;
+    while (split < most && units * split * 2 <= 2 * sms && (split < 4 ? turns > split : split < 8 ? turns > 2 * split : turns >= 4 * split))
+        split *= 2;
     if (!room_for(once, k_window_few<T, DP, BOXES>, F::SMEM, true)) return DBS_ERR_CUDA;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)(units * split));
@@ -1415,7 +1422,8 @@ dbs_status plan_of(const dbs_window_args &a, Plan &P)
     const int sms = multiprocessors(), group = a.q_heads / a.kv_heads, dp = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256;
     if (sms == 0) return DBS_ERR_CUDA;
     // Many rows of a kv head: 128 at a time, if K, V and Q can be copied as boxes (sinks and the
-    // window's start round to them).
+    // window's start round to them).  Heads of 128, 8 of kv, 16 rows, one sequence of 8192 entries and 32 of 4096: 16.8 us and 103, by
+    // 16 at a time 15.0 and 97; 24 rows 16.8 and 103, by 16 at a time 26 and 141; 64 rows 18.7 and 107, 22 and 277.
     if (a.tokens * group > FEW_ROWS && group <= 128 && a.scale > 0 && make_maps(a, a.sinks > 0 || dp == 128 ? 16 : dp == 256 ? 64 : 32, P.maps.kv) &&
         make_q_map(a, group, 128 / group, P.maps.q)) {
         const int tiles = dp == 256 ? 1 : 2, keys = dp == 64 ? 96 : dp == 128 ? 80 : 64;
@@ -1424,7 +1432,8 @@ dbs_status plan_of(const dbs_window_args &a, Plan &P)
         C.groups = (int)((a.tokens + tiles * C.tokens - 1) / (tiles * C.tokens));
         C.units = (int)(a.batch * a.kv_heads * C.groups);
         C.scratch = nullptr;
-        // Blocks of a unit: as many as find room at once, with two tiles each at least.
+        // Blocks of a unit: as many as find room at once, with two tiles each at least (64 tokens, 32/8 heads, window 4096:
+        // 22 us, in one block 62; 8 sequences of 8 tokens over 2111 entries 24 and 29).
         const int64_t line = (line_of(a, tiles * C.tokens) + keys - 1) / keys;
         int64_t split = sms / C.units;
         split = split < line / 2 ? split : line / 2;
