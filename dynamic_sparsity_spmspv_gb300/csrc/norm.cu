@@ -12,8 +12,9 @@ constexpr int NT = 256;
 // Blocks of a multiprocessor, heads whose loads are issued together, and heads of a thread at most, for
 // heads of one unit a lane.  Forward the next heads are loaded before these are worked on (16,382 tokens of 40 heads of
 // 128, bf16: 2, 3 and 12 60 us, 2, 3 and 8 61, 2, 2 and 8 66, 3, 1 and 8 67, 2, 4 and 16 78 (registers spilled);
-// without that 3, 2 and 8 71).  The gradient has no registers left for it (8192 tokens of 32 heads of 96, f32: 2, 2 and 8 66 us,
-// 2, 2 and 4 69, 3 and 1 79; loading ahead 68 with one head, 78 with two).
+// without that 3, 2 and 8 71).  The gradient has registers left for it in 16 bits only (8192 tokens of 32 heads of 96, f32: 2, 2 and
+// 8 66 us, 2, 2 and 4 69, 3 and 1 79; loading ahead 68 with one head, 78 with two; of 40 heads of 128, bf16: 95, without 116,
+// with 3 blocks 110, with 4 heads 128).
 constexpr int FORWARD_BLOCKS = 2, FORWARD_HEADS = 3, FORWARD_SPAN = 12, BACKWARD_BLOCKS = 2, BACKWARD_HEADS = 2, BACKWARD_SPAN = 8;
 
 // What a lane moves at once: N values, 16 or 8 bytes, or one where rows are not aligned for that.
@@ -418,13 +419,15 @@ struct Gradient {
 // A group of lanes takes a token's heads, HEADS at a time, then the next token that is
 // the grid's turn; what the heads give to weight' stays in its registers.  In the end the block's
 // groups are added up in their order and written to scratch, and k_norm_weight adds the blocks.
-// Bound by HBM: two entries are read and one is written (303 MB in 66 us, 68% of the memory's rate: waiting
-// for it, with as many loads under way as registers hold).
+// Two entries are read and one is written (f32, 303 MB in 66 us, 67% of the memory's rate; bf16, 8192 tokens of 40 heads of
+// 128, 252 MB in 95 us, 39%).  Bound by instructions, some 200 for a lane's eight values of a head with its two sums over
+// lanes, and by their latencies with 16 warps, more of which registers do not allow.
 template <class T, bool INTERLEAVED, int N, int K>
 __global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradient(Gradient A, int span)
 {
     using L = Lane<T, INTERLEAVED, N, K>;
     constexpr int HEADS = K == 1 ? BACKWARD_HEADS : 1;
+    constexpr bool AHEAD = sizeof(T) == 2;                 // (the next heads are loaded before these are worked on)
     extern __shared__ float sums[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int p = (int)blockIdx.x >= A.blocks[0], block = (int)blockIdx.x - (p ? A.blocks[0] : 0);
@@ -457,18 +460,19 @@ __global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradi
         const T *g = (const T *)P.grad + b * P.grad_batch + t * P.grad_token + h0 * P.grad_head;
         const T *x = (const T *)P.in + b * P.in_batch + t * P.in_token + h0 * P.in_head;
         T *out = (T *)P.out + b * P.out_batch + t * P.out_token + h0 * P.out_head;
-        typename L::VT gv[HEADS][K][2], xv[HEADS][K][2];
-        auto fetch = [&](int h) {
+        using Set = typename L::VT[HEADS][K][2];
+        Set gv, xv, gn, xn;
+        auto fetch = [&](int h, Set &to_g, Set &to_x) {
 #pragma unroll
             for (int k = 0; k < HEADS; ++k)
                 if (in && h + k < heads) {
-                    L::load(units, g + k * P.grad_head, gv[k]);
-                    L::load(units, x + k * P.in_head, xv[k]);
+                    L::load(units, g + k * P.grad_head, to_g[k]);
+                    L::load(units, x + k * P.in_head, to_x[k]);
                 }
             g += HEADS * P.grad_head;
             x += HEADS * P.in_head;
         };
-        fetch(0);
+        fetch(0, gv, xv);
         uint64_t own[K][N], other[K][N];
         {
             float cs[K][N], sn[K][N], ones[2 * N];
@@ -478,8 +482,10 @@ __global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradi
 #pragma unroll
             for (int c = 0; c < K; ++c) L::turns(cs[c], sn[c], ones, own[c], other[c]);
         }
+#pragma unroll 1
         for (int h = 0; h < span; h += HEADS) {
-            if (h) fetch(h);
+            if (AHEAD) fetch(h + HEADS, gn, xn);
+            else if (h) fetch(h, gv, xv);
 #pragma unroll
             for (int k = 0; k < HEADS; ++k) {
                 const bool live = in && h + k < heads;
@@ -509,6 +515,16 @@ __global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradi
                 }
                 L::store(units, out + k * P.out_head, gv[k]);
             }
+            if (AHEAD)
+#pragma unroll
+                for (int k = 0; k < HEADS; ++k)
+#pragma unroll
+                    for (int c = 0; c < K; ++c)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            gv[k][c][e] = gn[k][c][e];
+                            xv[k][c][e] = xn[k][c][e];
+                        }
             out += HEADS * P.out_head;
         }
     }
@@ -610,7 +626,8 @@ template <class T, int N> bool on_pieces(const void *p, int64_t b, int64_t t, in
 }
 
 // Values of a piece.  Forward 16 bytes of them.  The gradient holds twice as much of a head
-// beside its weights and their sums, so it takes half as many of 16 bits.
+// beside its weights and their sums, so it takes half as many of 16 bits (with 16 bytes of them, and one block of a
+// multiprocessor instead of two, 98 us for 95 above).
 template <class T> constexpr int FORWARD = 16 / (int)sizeof(T);
 template <class T> constexpr int BACKWARD = 4;
 
