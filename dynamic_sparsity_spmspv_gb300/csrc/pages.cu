@@ -583,13 +583,14 @@ __global__ void __launch_bounds__(MOVE_NT) k_compact(Compact A)
     const uint32_t h = D.heads == 1 ? 0u : u / row;
     const int64_t mine = h * by_head + (u - h * row);
     int kept = 0;
-    auto place = [&](int j) {
+    // Where entry j lies; -1 if its page is none.
+    auto place = [&](int j) -> int64_t {
         int64_t page = b;
         int in = j;
         if (s.page_table) {
-            const int size = (int)s.page_size;
-            const int64_t p = s.page_table[b * s.page_row + j / size];
-            page = p < 0 ? 0 : p >= s.pages ? s.pages - 1 : p;
+            const int size = (int)s.page_size, p = s.page_table[b * s.page_row + j / size];
+            if (!is_page(s, p)) return -1;
+            page = p;
             in = j % size;
         }
         return page * by_page + in * by_entry;
@@ -606,8 +607,10 @@ __global__ void __launch_bounds__(MOVE_NT) k_compact(Compact A)
             if (a < 0 || a >= tree || a <= prior) {
                 atomicMin(&ends, (int)threadIdx.x);
             } else {
-                from[threadIdx.x] = a == i ? -1 : place(first + a);
-                to[threadIdx.x] = place(first + i);        // (an ascending list: i <= a < tree)
+                // (what comes from no page, or would go to none, stays where it is)
+                const int64_t dst = place(first + i);      // (an ascending list: i <= a < tree)
+                from[threadIdx.x] = a == i || dst < 0 ? -1 : place(first + a);
+                to[threadIdx.x] = dst;
             }
         }
         __syncthreads();

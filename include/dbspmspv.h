@@ -742,6 +742,7 @@ dbs_status dbs_cache_fork(const dbs_cache_data *data, const dbs_page_state *stat
  *                  numbers below tree_lens[b]; the first that is not (-1, say) ends the list
  *   accepted_lens  device int32[batch], or NULL = max_accepted
  *   new_lens       device int32[batch]: kv_lens[b] - tree_lens[b] + those kept (kv_lens stays); apart from the lists
+ * An entry that lies in, or would move to, a page outside [0, pages) is kept and counted without being moved.
  * Of `state` refs is not used; page_table may be NULL: sequence b is page b.  Drafted
  * entries have to lie in pages that b alone owns.  batch < 2^16, layers < 2^15.
  * Errors: DBS_ERR_INVALID_ARG, DBS_ERR_CUDA. */

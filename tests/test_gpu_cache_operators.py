@@ -991,3 +991,26 @@ def test_inputs_that_require_a_gradient_are_refused():
         assert torch.equal(dbs.norm_rotary(q, None, w, None, table, i)[0], torch.zeros_like(x))
     with pytest.raises(dbs.DbsError):
         dbs.window_attention(x, x, x, one, 4, out=x)
+
+
+@pytest.mark.parametrize("outside", [-1, -7, 11, 2**31 - 1])
+def test_cache_compact_passes_over_pages_that_are_none(outside):
+    """Pages of a drafted tree that are none: nothing is read from or written to another page for them, and the lengths are as ever."""
+    rng = np.random.default_rng(31)
+    B, per, page, pages, T = 3, 3, 4, 11, 12
+    k, v = make_caches(rng, 2, 2, 24, "f16", 5, pages, page)
+    table = (1 + rng.permutation(9)).astype(np.int32).reshape(B, per)      # the first and the last page belong to others
+    table[0, 1] = table[1, 0] = table[2, 2] = outside
+    acc = np.array([[1, 2, 4, 5, 7, 8, 9, 11, -1, -1, -1, -1], [0, 2, 3, 5, 6, 9, 10, 11, -1, -1, -1, -1], [3, 4, 8, 9, 10, 11, -1, -1, -1, -1, -1, -1]], np.int32)
+    hk, hv, want = plain(k), plain(v), []
+    for b in range(B):
+        path = [a for a in acc[b] if a >= 0]
+        for i, a in enumerate(path):
+            src, dst = table[b, a // page], table[b, i // page]
+            if 0 <= src < pages and 0 <= dst < pages:
+                for x in (hk, hv):
+                    x[:, dst, i % page] = x[:, src, a % page]
+        want.append(len(path))
+    got = dbs.cache_compact(k, v, ints([T] * B), ints([T] * B), ints(acc), page_table=ints(table))
+    assert got.tolist() == want
+    assert torch.equal(plain(k), hk) and torch.equal(plain(v), hv)
