@@ -604,11 +604,13 @@ __global__ void __launch_bounds__(MOVE_NT) k_compact(Compact A)
         if (threadIdx.x == 0) ends = most;
         __syncthreads();
         if (i0 + threadIdx.x < n) {
-            if (a < 0 || a >= tree || a <= prior) {
+            // (in a list that ascends up to here a is i at least; behind its end, where anything may stand,
+            // the check keeps place i within the tree)
+            if (a < i || a >= tree || a <= prior) {
                 atomicMin(&ends, (int)threadIdx.x);
             } else {
                 // (what comes from no page, or would go to none, stays where it is)
-                const int64_t dst = place(first + i);      // (an ascending list: i <= a < tree)
+                const int64_t dst = place(first + i);
                 from[threadIdx.x] = a == i || dst < 0 ? -1 : place(first + a);
                 to[threadIdx.x] = dst;
             }

@@ -1014,3 +1014,28 @@ def test_cache_compact_passes_over_pages_that_are_none(outside):
     got = dbs.cache_compact(k, v, ints([T] * B), ints([T] * B), ints(acc), page_table=ints(table))
     assert got.tolist() == want
     assert torch.equal(plain(k), hk) and torch.equal(plain(v), hv)
+
+
+@pytest.mark.parametrize("page,T", [(1, 2), (16, 5), (4, 256), (1, 300)])
+def test_cache_compact_of_lists_with_anything_behind_their_end(page, T):
+    """Sequences that fill their rows of the table, lists far longer than the tree that ascend again behind their end: what stands
+    there asks for no entry (places behind the tree's lie behind the row, and of the last sequence behind the table)."""
+    rng = np.random.default_rng(page + T)
+    B, most = 3, 1000
+    per = -(-(T + 30) // page)
+    S, pages = per * page, 3 * per
+    k, v = make_caches(rng, 2, 1, 16, "bf16", 5, pages, page)
+    table = rng.permutation(pages).astype(np.int32).reshape(B, per)
+    acc = np.tile(np.arange(T, dtype=np.int32), (B, -(-most // T)))[:, :most]          # 0 .. T - 1, again and again
+    acc[1, min(1, T - 1)] = T - 1                                                      # 0, T - 1, then it no longer ascends
+    acc[2, 0] = 1
+    acc[2, 1:T] = np.arange(1, T)                                                      # 1, and that again
+    hk, hv = plain(k), plain(v)
+    kept = [T, 2, 1]
+    for b in range(B):
+        for i in range(kept[b]):
+            for x in (hk, hv):
+                x[:, table[b, (S - T + i) // page], (S - T + i) % page] = x[:, table[b, (S - T + acc[b, i]) // page], (S - T + acc[b, i]) % page]
+    got = dbs.cache_compact(k, v, ints([S] * B), ints([T] * B), ints(acc), page_table=ints(table))
+    assert got.tolist() == [S - T + n for n in kept]
+    assert torch.equal(plain(k), hk) and torch.equal(plain(v), hv)
