@@ -232,8 +232,7 @@ __global__ void __launch_bounds__(ROW_NT) k_attn_rows(Attn A)
             for (int e = 0; e < 8; ++e) o[e] = 0.f;
             for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w]);
             for (int w = 0; w < W; ++w) {
-                // a maximum of -inf: nothing there, or a NaN that has to stay
-                f = s_m[w] == -INFINITY ? (s_l[w] != s_l[w] ? 1.f : 0.f) : exp2f(s_m[w] - top);
+                f = weight_of(s_m[w], s_l[w], top);
                 sum += f * s_l[w];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o[e] += f == 0.f ? 0.f : f * s_o[w][lane + 32 * e];
@@ -807,7 +806,7 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
                 for (int w = 0; w < FEW_W; ++w) top = fmaxf(top, s_m[w][r]);
 #pragma unroll
                 for (int w = 0; w < FEW_W; ++w) {
-                    const float f = s_m[w][r] == -INFINITY ? (s_l[w][r] != s_l[w][r] ? 1.f : 0.f) : exp2f(s_m[w][r] - top);
+                    const float f = weight_of(s_m[w][r], s_l[w][r], top);
                     const float *po = (const float *)(ring + w * (FEW_STAGES * 2 * HALF)) + r * DP;
                     sum += f * s_l[w][r];
 #pragma unroll
@@ -868,8 +867,8 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
                     for (int k = 0; k < FEW_SPLIT; ++k) v[k] = k < split ? from((const float *)(ring + joined(r)) + lane + 32 * e0, k) : 0.f;
 #pragma unroll
                     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-                    const float f = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2f(m - top);
-                    l = f == 0.f ? 0.f : f * l;
+                    const float f = weight_of(m, l, top);
+                    l *= f;
 #pragma unroll
                     for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
 #pragma unroll

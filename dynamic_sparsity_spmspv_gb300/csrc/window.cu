@@ -153,11 +153,10 @@ __global__ void __launch_bounds__(ROW_NT) k_window_rows(Win A)
         for (int e = 0; e < 8; ++e) o[e] = 0.f;
         for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w]);
         for (int w = 0; w < W; ++w) {
-            // a maximum of -inf: nothing there, or a NaN that has to stay
-            const float f = s_m[w] == -INFINITY ? (s_l[w] != s_l[w] ? 1.f : 0.f) : exp2f(s_m[w] - top);
+            const float f = weight_of(s_m[w], s_l[w], top);
             sum += f * s_l[w];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] += f == 0.f ? 0.f : f * s_o[w][lane + 32 * e];
+            for (int e = 0; e < 8; ++e) o[e] += f * s_o[w][lane + 32 * e];
         }
         store_row<T>(A, b, t, (int)h, top, sum, o);
     }
@@ -578,11 +577,11 @@ __global__ void __launch_bounds__(FEW_NT) k_window_few(Win A, int groups, int sp
         for (int w = 0; w < FEW_W; ++w) top = fmaxf(top, s_m[w][r]);
 #pragma unroll
         for (int w = 0; w < FEW_W; ++w) {
-            const float f = s_m[w][r] == -INFINITY ? (s_l[w][r] != s_l[w][r] ? 1.f : 0.f) : exp2f(s_m[w][r] - top);
+            const float f = weight_of(s_m[w][r], s_l[w][r], top);
             const float *po = (const float *)(ring + w * F::RING) + r * DP;
             sum += f * s_l[w][r];
 #pragma unroll
-            for (int e = 0; e < DP / 32; ++e) oo[e] += f == 0.f ? 0.f : f * po[lane + 32 * e];
+            for (int e = 0; e < DP / 32; ++e) oo[e] += f * po[lane + 32 * e];
         }
 #pragma unroll
         for (int e = 0; e < DP / 32; ++e) joined(r)[lane + 32 * e] = oo[e];
@@ -607,14 +606,14 @@ __global__ void __launch_bounds__(FEW_NT) k_window_few(Win A, int groups, int sp
         for (int k = 0; k < FEW_SPLIT; ++k) v[k] = k < split ? remote(joined(r) + col, k) : 0.f;
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        const float f = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2f(m - top);
-        l = f == 0.f ? 0.f : f * l;
+        const float f = weight_of(m, l, top);
+        l *= f;
 #pragma unroll
         for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
 #pragma unroll
         for (int k = 0; k < FEW_SPLIT; ++k) {
             const float fk = __shfl_sync(~0u, f, k);
-            out += fk == 0.f ? 0.f : fk * v[k];
+            out += fk * v[k];
         }
         if (row.p < 0) l = out = 0.f;
         float lo = l;                                                      // the output's divisor
@@ -1227,8 +1226,8 @@ __global__ void __launch_bounds__(JOIN_NT) k_window_join(Win A, Cut C)
     float l = in ? __ldcg(parts + lane * PART + TILES * 128 * (DP + 1) + tile_row) : 0.f, top = m;
 #pragma unroll
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    const float f = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2f(m - top);
-    l = f == 0.f ? 0.f : f * l;
+    const float f = weight_of(m, l, top);
+    l *= f;
 #pragma unroll
     for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
     if (t >= s.tokens || s.first + t < 0) l = 0.f;
@@ -1239,7 +1238,7 @@ __global__ void __launch_bounds__(JOIN_NT) k_window_join(Win A, Cut C)
 #pragma unroll
         for (int e = 0; e < DP / 32; ++e) {
             const float x = lane + 32 * e < a.head_dim ? __ldcg(parts + k * PART + tile_row * DP + lane + 32 * e) : 0.f;
-            o[e] += fk == 0.f ? 0.f : fk * x;
+            o[e] += fk * x;
         }
     }
     bool odd = false;

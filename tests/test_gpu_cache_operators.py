@@ -1039,3 +1039,33 @@ def test_cache_compact_of_lists_with_anything_behind_their_end(page, T):
     got = dbs.cache_compact(k, v, ints([S] * B), ints([T] * B), ints(acc), page_table=ints(table))
     assert got.tolist() == [S - T + n for n in kept]
     assert torch.equal(plain(k), hk) and torch.equal(plain(v), hv)
+
+
+@pytest.mark.parametrize("T,hq,hk,D,S,page", [(1, 8, 2, 128, 4000, 16), (1, 4, 1, 64, 9000, 0), (1, 2, 1, 256, 3000, 16), (2, 4, 2, 64, 2500, 5), (1, 4, 2, 33, 600, 16),
+                                              (7, 4, 2, 128, 900, 16), (40, 4, 1, 64, 3000, 16), (100, 2, 2, 128, 2000, 24), (30, 4, 1, 256, 1500, 64)])
+@pytest.mark.parametrize("loud,odd", [(5, 2), (2, 5)])
+def test_what_a_row_sees_counts_however_little_it_weighs(T, hq, hk, D, S, page, loud, odd):
+    """One entry's score is some 300 above all others (320 or more in base e, so that their weights are 0 in fp32), another entry in
+    another part of the line has a NaN key, or a value that is not finite: the rows are NaN, and lse where the key is."""
+    q, one = torch.ones((1, T, hq, D), dtype=torch.bfloat16, device=DEV), dict(dtype=torch.bfloat16, device=DEV)
+    shape = (-(-S // page), page, hk, D) if page else (1, S, hk, D)
+    table = torch.arange(shape[0], dtype=torch.int32, device=DEV)[None] if page else None
+    loud, odd = loud * (S - T) // 6, odd * (S - T) // 6
+    k, v = torch.zeros(shape, **one), torch.ones(shape, **one)
+    k.view(-1, hk, D)[loud] = 64
+    kw = dict(page_table=table, return_lse=True)
+    attend = [lambda: dbs.window_attention(q, k, v, ints([S]), S, **kw), lambda: dbs.tree_attention(q, k, v, ints([S]), **kw)]
+    for f in attend:
+        out, lse = f()
+        assert (out == 1).all() and torch.isfinite(lse).all()
+    flat = v.view(-1, hk, D)
+    for value in (NAN, INF):
+        flat[odd, :, 1] = value
+        out, lse = attend[0]()
+        assert not torch.isfinite(out[..., 1]).any() and torch.isfinite(lse).all()
+        assert (out[..., [c for c in range(D) if c != 1]] == 1).all()
+    flat[odd] = 1
+    k.view(-1, hk, D)[odd] = NAN
+    for f in attend:
+        out, lse = f()
+        assert torch.isnan(out).all() and torch.isnan(lse).all()
