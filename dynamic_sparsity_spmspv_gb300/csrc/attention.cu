@@ -2,6 +2,7 @@
 // sm_103a): softmax over the entries a token sees, with the running maximum
 // and sum held in fp32.
 #include "ops_dev.h"
+#include "places.h"
 #include "tc_dev.h"
 
 #include <cmath>
@@ -1769,9 +1770,8 @@ bool args_ok(const dbs_attention_args *a)
                            a->page_row, a->o_batch, a->o_token, a->o_head})
         if (stride < 0) return false;
     // heads of out that share memory
-    if ((a->q_heads > 1 && a->o_head < a->head_dim) || (a->tokens > 1 && a->o_token < a->head_dim) ||
-        (a->batch > 1 && a->o_batch < a->head_dim))
-        return false;
+    const Places out(a->out, 2, a->head_dim, {{a->batch, a->o_batch}, {a->tokens, a->o_token}, {a->q_heads, a->o_head}});
+    if (!out.own()) return false;
     if (!a->page_table && (a->max_pages > 1 || (entries > 0 && a->pages < a->batch))) return false;
     return true;
 }

@@ -2,6 +2,7 @@
 // its gradient (dbs_norm_rotary_gradient, sm_103a).
 #include <cmath>
 
+#include "places.h"
 #include "vec_dev.h"
 
 using namespace dbs::ops;
@@ -689,10 +690,9 @@ bool sizes_ok(dbs_dtype dtype, int64_t batch, int64_t tokens, int32_t head_dim, 
     return batch <= (int64_t(1) << 31) && tokens <= (int64_t(1) << 31) && batch * tokens < (int64_t(1) << 31) &&
            batch * tokens * head_dim < (int64_t(1) << 32) - NT;
 }
-bool places_apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t size)
-{
-    return (n0 <= 1 || s0 >= size) && (n1 <= 1 || s1 >= size) && (n2 <= 1 || s2 >= size);
-}
+int64_t size_of(dbs_dtype dtype) { return dtype == DBS_F32 ? 4 : 2; }
+// A negative stride among those of a group's heads.
+bool backwards(int64_t batch, int64_t token, int64_t head) { return batch < 0 || token < 0 || head < 0; }
 
 }  // namespace
 
@@ -718,10 +718,10 @@ dbs_status dbs_norm_rotary(const dbs_norm_heads *parts, int32_t nparts, dbs_dtyp
         if (P.to_slots && pages == 0) continue;                                // no slot is inside: nothing is written
         if (!P.out) return DBS_ERR_INVALID_ARG;
         const int64_t n_batch = P.to_slots ? pages : batch, n_token = P.to_slots ? page_size : tokens;
-        const bool apart = places_apart(P.heads, P.out_head, n_token, P.out_token, n_batch, P.out_batch, head_dim);
+        const Places out(P.out, size_of(dtype), head_dim, {{n_batch, P.out_batch}, {n_token, P.out_token}, {P.heads, P.out_head}});
         const bool placed = P.in != P.out || (!P.to_slots && (P.heads == 1 || P.in_head == P.out_head) &&
                                               (tokens == 1 || P.in_token == P.out_token) && (batch == 1 || P.in_batch == P.out_batch));
-        if (P.in_head < 0 || P.in_token < 0 || P.in_batch < 0 || !apart || !placed) return DBS_ERR_INVALID_ARG;
+        if (backwards(P.in_batch, P.in_token, P.in_head) || !out.own() || !placed) return DBS_ERR_INVALID_ARG;
         A.part[A.nparts++] = parts[p];
     }
     if (!work || A.nparts == 0) return DBS_OK;
@@ -765,9 +765,9 @@ dbs_status dbs_norm_rotary_gradient(const dbs_norm_gradient_heads *parts, int32_
         if (!work) P.heads = 0;
         if (P.heads) {
             if (!P.grad || !P.in || !P.out || (dim > 0 && (!table || !positions))) return DBS_ERR_INVALID_ARG;
-            for (int64_t stride : {P.grad_batch, P.grad_token, P.grad_head, P.in_batch, P.in_token, P.in_head})
-                if (stride < 0) return DBS_ERR_INVALID_ARG;
-            if (!places_apart(P.heads, P.out_head, tokens, P.out_token, batch, P.out_batch, head_dim)) return DBS_ERR_INVALID_ARG;
+            const Places out(P.out, size_of(dtype), head_dim, {{batch, P.out_batch}, {tokens, P.out_token}, {P.heads, P.out_head}});
+            if (backwards(P.grad_batch, P.grad_token, P.grad_head) || backwards(P.in_batch, P.in_token, P.in_head) || !out.own())
+                return DBS_ERR_INVALID_ARG;
             auto same = [&](int64_t b, int64_t t, int64_t h) {
                 return (batch == 1 || b == P.out_batch) && (tokens == 1 || t == P.out_token) && (P.heads == 1 || h == P.out_head);
             };

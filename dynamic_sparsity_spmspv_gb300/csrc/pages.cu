@@ -1,5 +1,6 @@
 // Pages of a cache (dbs_cache_resize, dbs_cache_fork, dbs_cache_compact, sm_103a).
 #include "ops_dev.h"
+#include "places.h"
 
 using namespace dbs::ops;
 
@@ -672,12 +673,11 @@ bool data_ok(const dbs_cache_data *c, const dbs_page_state *s, bool work)
         return false;
     if (!work || c->layers == 0 || c->heads == 0 || c->head_dim == 0) return true;
     if (!c->k || !c->v) return false;
-    const int64_t entry[2][4] = {{c->k_layer, c->k_page, c->k_entry, c->k_head}, {c->v_layer, c->v_page, c->v_entry, c->v_head}};
-    const int64_t count[4] = {c->layers, s->pages, s->page_size, c->heads};
-    for (auto &by : entry)
-        for (int i = 0; i < 4; ++i)
-            if (by[i] < 0 || (count[i] > 1 && by[i] < c->head_dim) || by[i] >= int64_t(1) << 50) return false;
-    return true;
+    for (int64_t by : {c->k_layer, c->k_page, c->k_entry, c->k_head, c->v_layer, c->v_page, c->v_entry, c->v_head})
+        if (by < 0 || by >= int64_t(1) << 50) return false;
+    const Places k(c->k, c->element_bytes, c->head_dim, {{c->layers, c->k_layer}, {s->pages, c->k_page}, {s->page_size, c->k_entry}, {c->heads, c->k_head}}),
+        v(c->v, c->element_bytes, c->head_dim, {{c->layers, c->v_layer}, {s->pages, c->v_page}, {s->page_size, c->v_entry}, {c->heads, c->v_head}});
+    return k.own() && v.own();
 }
 
 // f(V) with V the unit's type.

@@ -513,7 +513,8 @@ typedef struct {
  *   batch * tokens < 2^31, and times head_dim < 2^32 - 256; at most 16384 heads
  *   in a group
  * Errors: DBS_ERR_INVALID_ARG (heads of an output that share memory among
- * them), DBS_ERR_CUDA. */
+ * them, and strides that do not each step over all that the smaller ones take),
+ * DBS_ERR_CUDA. */
 dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype dtype, int64_t batch, int64_t tokens,
                       int32_t head_dim, int32_t dim, const float *table, int64_t table_rows, const int32_t *positions,
                       const int32_t *slots, int64_t pages, int64_t page_size, int32_t interleaved,
@@ -597,7 +598,9 @@ dbs_status dbs_penalize_logits(const dbs_logits_args *a, void *stream);
  *
  * As above: ASYNC, nothing allocated, no state between calls, capturable, the same
  * bits when repeated; strides in elements, not negative, innermost dimension
- * contiguous. */
+ * contiguous.  Of outputs and caches every stride (but of a dimension of one) steps over
+ * all that the smaller ones take, as in any permuted or sliced part of a contiguous
+ * tensor: otherwise two places may be one, and the call is refused. */
 
 /* Norms of queries and keys, each head's own, and their rotation in the same pass:
  *     n = x * (sum_c x[c]^2 / head_dim + eps)^(-1/2) * weight

@@ -223,3 +223,39 @@ def test_argument_structs_have_the_header_s_size():
     src = '#include <stddef.h>\n#include "include/dbspmspv.h"\n' + "".join(f'_Static_assert(sizeof({k}) == {v}, "size");\n' for k, v in sizes.items())
     src += '_Static_assert(offsetof(dbs_window_args, scale) == 200 && offsetof(dbs_cache_data, k_layer) == 48, "places");\n'
     assert subprocess.run(["gcc", "-x", "c", "-fsyntax-only", "-I", root, "-"], input=src.encode(), cwd=root).returncode == 0
+
+
+# (heads, tokens, batch of 2, 4, 2 or pages of 16 entries) strides that are each a head's size, of places that meet all the same
+TANGLED = [(512, 64, 64), (64, 128, 64), (512, 128, 128), (512, 128, 65), (320, 128, 64), (256, 128, 100)]
+
+
+@pytest.mark.parametrize("by", TANGLED)
+def test_outputs_whose_strides_do_not_step_over_one_another_are_refused(by):
+    lib = _lib.load()
+    assert norm(batch=2, parts=part(strides=(512, 128, 64) + by)) == BAD
+    assert norm(batch=2, parts=part(slots=1, strides=(512, 128, 64) + (4 * by[0], *by[1:])), slots=A, pages=2, page=16) == BAD
+    assert gradient(batch=2, parts=gpart(strides=(512, 128, 64) * 2 + by)) == BAD
+    need = ctypes.c_int64(-1)
+    a = dict(WIN, hq=2, hk=1, tokens=4, out=1 << 20, o0=by[0], o1=by[1], o2=by[2])
+    assert lib.dbs_window_attention_scratch(_lib.WINDOW_ARGS.pack(*a.values()), ctypes.byref(need)) == BAD
+    heads = struct.pack("@" + _lib.ROTARY_HEADS, A, 1 << 20, 512, 128, 64, *by, 2, 1, 0)
+    assert lib.dbs_rotary(heads, 1, 2, 2, 4, 64, 64, A, 10, A, 0, 0, 1, 0, 0, None) == BAD
+    tree = _lib.ATTENTION_ARGS.pack(2, 64, 2, 1, 2, 4, A, 512, 128, 64, A, A, *[64] * 6, 9, 16, A, 4, 4, A, 0, 0, 0.125, 1 << 20, *by, 0, A, 1 << 40)
+    assert lib.dbs_tree_attention_scratch(tree, ctypes.byref(need)) == BAD
+
+
+@pytest.mark.parametrize("by", [(18432, 2048, 64, 64), (18432, 2048, 128, 65), (18432, 1984, 128, 64), (18431, 2048, 128, 64), (2048, 2048, 128, 64),
+                                (64, 128, 2304, 64), (18432, 2048, 64, 1000)])
+def test_caches_whose_places_meet_are_refused(by):
+    lib, big, plain, far = _lib.load(), 1 << 40, (18432, 2048, 128, 64), 1 << 30
+    for strides in (by + plain, plain + by):
+        d = data(k=A, v=far, strides=strides)
+        assert lib.dbs_cache_fork(d, state(), A, A, 2, A, A, big, None) == BAD
+        assert lib.dbs_cache_compact(d, state(), A, A, 4, 4, 0, 2 * A, None) == BAD
+
+
+def test_permuted_and_sliced_outputs_are_taken():
+    need = ctypes.c_int64(-1)
+    for by in ((1536, 512, 64), (1536, 64, 192), (64, 128, 384), (4096, 1024, 128), (192, 64, 384), (64, 1 << 40, 1 << 50), (1 << 60, 512, 64)):
+        a = dict(WIN, out=1 << 40, o0=by[0], o1=by[1], o2=by[2])
+        assert _lib.load().dbs_window_attention_scratch(_lib.WINDOW_ARGS.pack(*a.values()), ctypes.byref(need)) != BAD, by
