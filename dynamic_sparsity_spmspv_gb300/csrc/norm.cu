@@ -705,6 +705,7 @@ dbs_status dbs_norm_rotary(const dbs_norm_heads *parts, int32_t nparts, dbs_dtyp
 {
     if (!parts || nparts < 1 || nparts > 3 || !sizes_ok(dtype, batch, tokens, head_dim, dim, eps, table_rows)) return DBS_ERR_INVALID_ARG;
     Norm A{};
+    Places writes[3], reads[3];
     const bool work = batch > 0 && tokens > 0;
     for (int p = 0; p < nparts; ++p) {
         const dbs_rotary_heads &P = parts[p].heads;
@@ -719,12 +720,14 @@ dbs_status dbs_norm_rotary(const dbs_norm_heads *parts, int32_t nparts, dbs_dtyp
         if (!P.out) return DBS_ERR_INVALID_ARG;
         const int64_t n_batch = P.to_slots ? pages : batch, n_token = P.to_slots ? page_size : tokens;
         const Places out(P.out, size_of(dtype), head_dim, {{n_batch, P.out_batch}, {n_token, P.out_token}, {P.heads, P.out_head}});
-        const bool placed = P.in != P.out || (!P.to_slots && (P.heads == 1 || P.in_head == P.out_head) &&
-                                              (tokens == 1 || P.in_token == P.out_token) && (batch == 1 || P.in_batch == P.out_batch));
-        if (backwards(P.in_batch, P.in_token, P.in_head) || !out.own() || !placed) return DBS_ERR_INVALID_ARG;
+        if (backwards(P.in_batch, P.in_token, P.in_head) || !out.own() || (P.to_slots && P.in == P.out)) return DBS_ERR_INVALID_ARG;
+        // (of a cache only the slots are written, which the host does not know)
+        if (!P.to_slots) writes[A.nparts] = out;
+        reads[A.nparts] = {P.in, size_of(dtype), head_dim, {{batch, P.in_batch}, {tokens, P.in_token}, {P.heads, P.in_head}}};
         A.part[A.nparts++] = parts[p];
     }
     if (!work || A.nparts == 0) return DBS_OK;
+    if (clash(writes, A.nparts, reads, A.nparts, true)) return DBS_ERR_INVALID_ARG;
     A.tokens = tokens;
     A.total = batch * tokens;
     A.eps = eps;
@@ -758,6 +761,7 @@ dbs_status dbs_norm_rotary_gradient(const dbs_norm_gradient_heads *parts, int32_
     Gradient A{};
     const bool work = batch > 0 && tokens > 0;
     bool sum = false, any = false;
+    Places writes[4], grads[2], reads[2];              // x' and weight' of each group
     for (int p = 0; p < nparts; ++p) {
         dbs_norm_gradient_heads P = parts[p];
         if (P.heads < 0 || P.heads > 16384 || (P.weight && !dtype_ok(P.weight_dtype))) return DBS_ERR_INVALID_ARG;
@@ -768,15 +772,15 @@ dbs_status dbs_norm_rotary_gradient(const dbs_norm_gradient_heads *parts, int32_
             const Places out(P.out, size_of(dtype), head_dim, {{batch, P.out_batch}, {tokens, P.out_token}, {P.heads, P.out_head}});
             if (backwards(P.grad_batch, P.grad_token, P.grad_head) || backwards(P.in_batch, P.in_token, P.in_head) || !out.own())
                 return DBS_ERR_INVALID_ARG;
-            auto same = [&](int64_t b, int64_t t, int64_t h) {
-                return (batch == 1 || b == P.out_batch) && (tokens == 1 || t == P.out_token) && (P.heads == 1 || h == P.out_head);
-            };
-            if ((P.out == P.grad && !same(P.grad_batch, P.grad_token, P.grad_head)) || (P.out == P.in && !same(P.in_batch, P.in_token, P.in_head)))
-                return DBS_ERR_INVALID_ARG;
+            writes[p] = out;
+            grads[p] = {P.grad, size_of(dtype), head_dim, {{batch, P.grad_batch}, {tokens, P.grad_token}, {P.heads, P.grad_head}}};
+            reads[p] = {P.in, size_of(dtype), head_dim, {{batch, P.in_batch}, {tokens, P.in_token}, {P.heads, P.in_head}}};
             any = true;
         }
+        if (P.weight_grad) writes[2 + p] = {P.weight_grad, 4, head_dim, {}};
         A.part[A.nparts++] = P;
     }
+    if (clash(writes, 4, grads, 2, true) || clash(writes, 4, reads, 2, true)) return DBS_ERR_INVALID_ARG;
     if (!sum && !any) return DBS_OK;
     if (sum) {
         int64_t need = 0;

@@ -665,7 +665,8 @@ bool data_of(const dbs_cache_data &c, Data &D, int &unit)
     return true;
 }
 
-bool data_ok(const dbs_cache_data *c, const dbs_page_state *s, bool work)
+// (`same`: K and V may be one tensor)
+bool data_ok(const dbs_cache_data *c, const dbs_page_state *s, bool work, bool same)
 {
     if (!c || c->layers < 0 || c->layers >= 32768 || c->heads < 0 || c->heads >= (int64_t(1) << 31) || c->head_dim < 0 ||
         c->head_dim >= (int64_t(1) << 31) || c->heads * c->head_dim >= (int64_t(1) << 31) ||
@@ -677,7 +678,7 @@ bool data_ok(const dbs_cache_data *c, const dbs_page_state *s, bool work)
         if (by < 0 || by >= int64_t(1) << 50) return false;
     const Places k(c->k, c->element_bytes, c->head_dim, {{c->layers, c->k_layer}, {s->pages, c->k_page}, {s->page_size, c->k_entry}, {c->heads, c->k_head}}),
         v(c->v, c->element_bytes, c->head_dim, {{c->layers, c->v_layer}, {s->pages, c->v_page}, {s->page_size, c->v_entry}, {c->heads, c->v_head}});
-    return k.own() && v.own();
+    return k.own() && v.own() && (!k.meets(v) || (same && k.same(v)));
 }
 
 // f(V) with V the unit's type.
@@ -685,6 +686,10 @@ template <class F> dbs_status by_unit(int unit, F f)
 {
     return unit == 16 ? f(uint4{}) : unit == 8 ? f(uint64_t{}) : unit == 4 ? f(uint32_t{}) : unit == 2 ? f(uint16_t{}) : f(uint8_t{});
 }
+
+Places ints(const int32_t *p, int64_t n) { return p ? Places(p, 4, n, {}) : Places(); }
+Places rows(const int32_t *p, int64_t n, int64_t columns, int64_t stride) { return p ? Places(p, 4, columns, {{n, stride}}) : Places(); }
+Places table_of(const dbs_page_state &s) { return rows(s.page_table, s.batch, s.max_pages, s.page_row); }
 
 constexpr int64_t up16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
@@ -716,9 +721,10 @@ dbs_status dbs_cache_resize(const dbs_page_state *s, const int32_t *lens, int32_
     if (!state_ok(s, true) || columns < 0 || columns >= (int64_t(1) << 31)) return DBS_ERR_INVALID_ARG;
     if (s->batch == 0) return DBS_OK;
     const int64_t need = scratch_of(*s, columns), all = slots ? s->batch * columns : 0;
-    if (!lens || !status || (s->pages > 0 && !s->refs) || (need > 0 && (!scratch || !aligned16(scratch) || scratch_bytes < need)) || lens == s->kv_lens ||
-        status == s->kv_lens || status == lens)
+    if (!lens || !status || (s->pages > 0 && !s->refs) || (need > 0 && (!scratch || !aligned16(scratch) || scratch_bytes < need)))
         return DBS_ERR_INVALID_ARG;
+    const Places writes[5] = {ints(status, s->batch), ints(slots, all), ints(s->kv_lens, s->batch), ints(s->refs, s->pages), table_of(*s)}, want = ints(lens, s->batch);
+    if (clash(writes, 5, &want, 1, false)) return DBS_ERR_INVALID_ARG;
     const bool here = all > 0 && all <= SLOTS_HERE;
     int32_t *at = (int32_t *)scratch;
     cudaStream_t st = (cudaStream_t)stream;
@@ -753,12 +759,14 @@ dbs_status dbs_cache_fork_scratch(const dbs_page_state *s, int64_t n, int64_t *b
 dbs_status dbs_cache_fork(const dbs_cache_data *data, const dbs_page_state *s, const int32_t *parents, const int32_t *children, int64_t n,
                           int32_t *status, void *scratch, int64_t scratch_bytes, void *stream)
 {
-    if (!state_ok(s, true) || n < 0 || n >= 65536 || !data_ok(data, s, n > 0)) return DBS_ERR_INVALID_ARG;
+    if (!state_ok(s, true) || n < 0 || n >= 65536 || !data_ok(data, s, n > 0, true)) return DBS_ERR_INVALID_ARG;
     if (n == 0) return DBS_OK;
     int64_t need = 0;
     if (dbs_cache_fork_scratch(s, n, &need) != DBS_OK || !parents || !children || !status || (s->pages > 0 && !s->refs) || !scratch ||
         !aligned16(scratch) || scratch_bytes < need)
         return DBS_ERR_INVALID_ARG;
+    const Places writes[4] = {ints(status, n), ints(s->kv_lens, s->batch), ints(s->refs, s->pages), table_of(*s)}, reads[2] = {ints(parents, n), ints(children, n)};
+    if (clash(writes, 4, reads, 2, false)) return DBS_ERR_INVALID_ARG;
     Fork *forks = (Fork *)scratch;
     int32_t *list = (int32_t *)(forks + n);
     cudaStream_t st = (cudaStream_t)stream;
@@ -792,12 +800,15 @@ dbs_status dbs_cache_compact(const dbs_cache_data *data, const dbs_page_state *s
                              int64_t max_accepted, int64_t accepted_stride, const int32_t *accepted_lens, int32_t *new_lens, void *stream)
 {
     if (!state_ok(s, s && s->page_table) || s->batch >= 65536 || max_accepted < 0 || max_accepted >= (int64_t(1) << 31) ||
-        !data_ok(data, s, s->batch > 0))
+        !data_ok(data, s, s->batch > 0, false))
         return DBS_ERR_INVALID_ARG;
     if (s->batch == 0) return DBS_OK;
-    if (!tree_lens || !new_lens || new_lens == s->kv_lens || new_lens == tree_lens || new_lens == accepted_lens || (max_accepted > 0 && (!accepted || accepted_stride < 0)) ||
+    if (!tree_lens || !new_lens || (max_accepted > 0 && (!accepted || accepted_stride < 0)) ||
         (!s->page_table && (s->max_pages > 1 || s->pages < s->batch)) || (s->max_pages > 0 && s->pages < 1))
         return DBS_ERR_INVALID_ARG;
+    const Places writes = ints(new_lens, s->batch), reads[5] = {ints(s->kv_lens, s->batch), ints(tree_lens, s->batch), ints(accepted_lens, s->batch),
+                                                                rows(accepted, s->batch, max_accepted, accepted_stride), table_of(*s)};
+    if (clash(&writes, 1, reads, 5, false)) return DBS_ERR_INVALID_ARG;
     Compact A{{}, *s, tree_lens, accepted, accepted_lens, max_accepted, accepted_stride, new_lens};
     int unit = 16;
     const bool any = data->layers > 0 && data->heads > 0 && data->head_dim > 0;

@@ -17,8 +17,9 @@ struct Places {
     uintptr_t at;
     Big run, count[4], step[4];
     int n = 0;
-    bool none;                     // no run at all
+    bool none = true;              // no run at all
 
+    Places() : at(0), run(0) {}
     Places(const void *p, int64_t element, int64_t run_elements, std::initializer_list<Dim> dims)
         : at(reinterpret_cast<uintptr_t>(p)), run((Big)element * run_elements), none(run_elements <= 0)
     {
@@ -47,6 +48,82 @@ struct Places {
         }
         return true;
     }
+    Big extent() const             // bytes from the first run's begin to the last one's end
+    {
+        Big e = run;
+        for (int i = 0; i < n; ++i) e += (count[i] - 1) * step[i];
+        return e;
+    }
+    bool dense() const
+    {
+        Big all = run;
+        for (int i = 0; i < n; ++i) all *= count[i];
+        return own() && all == extent();
+    }
+    bool same(const Places &o) const
+    {
+        bool is = at == o.at && run == o.run && n == o.n;
+        for (int i = 0; is && i < n; ++i) is = count[i] == o.count[i] && step[i] == o.step[i];
+        return is;
+    }
+    // Whether some byte is surely in both: both are without gaps and their spans meet, or two runs are
+    // found that do (always, if there are any, where each larger step of the two goes over what the
+    // smaller ones take: tensors of one layout cut out of one buffer).
+    bool meets(const Places &o) const
+    {
+        if (none || o.none) return false;
+        const Big gap = (Big)o.at - (Big)at;
+        if (gap >= extent() || -gap >= o.extent()) return false;
+        if (dense() && o.dense()) return true;
+        // Run y of `o` begins gap + sum y step' - sum x step behind run x of this: from -o.run + 1 to run - 1
+        // they meet.  By steps, with the differences of index that there are of each:
+        Big by[8], lo[8], hi[8];
+        int k = 0;
+        for (int i = 0, j = 0; i < n || j < o.n;) {
+            const Big s = j == o.n || (i < n && step[i] < o.step[j]) ? step[i] : o.step[j];
+            by[k] = s;
+            lo[k] = hi[k] = 0;
+            for (; i < n && step[i] == s; ++i) lo[k] -= count[i] - 1;
+            for (; j < o.n && o.step[j] == s; ++j) hi[k] += o.count[j] - 1;
+            k += s > 0;
+        }
+        int tries = 1000;
+        return found(gap, by, lo, hi, k, o.run, tries);
+    }
+
+private:
+    bool found(Big gap, const Big *by, const Big *lo, const Big *hi, int k, Big other, int &tries) const
+    {
+        if (--tries < 0) return false;
+        if (k == 0) return gap > -other && gap < run;
+        // what is left of the gap has to be within reach of the smaller steps
+        Big down = other, up = run;
+        for (int i = 0; i < k - 1; ++i) {
+            down += hi[i] * by[i];
+            up -= lo[i] * by[i];
+        }
+        const Big s = by[k - 1];
+        auto floor_of = [&](Big v) { return v >= 0 ? v / s : -((-v + s - 1) / s); };
+        Big first = -floor_of(down + gap), last = floor_of(up - gap);
+        if (first < lo[k - 1]) first = lo[k - 1];
+        if (last > hi[k - 1]) last = hi[k - 1];
+        for (Big x = first; x <= last && tries > 0; ++x)
+            if (found(gap + x * s, by, lo, hi, k - 1, other, tries)) return true;
+        return false;
+    }
 };
+
+// Whether one of `writes` shares memory with another or with one of `reads`; in place: but the i-th
+// output may be the very same as the i-th input (each place is read before it is written, by the same threads).
+inline bool clash(const Places *writes, int n_writes, const Places *reads, int n_reads, bool in_place)
+{
+    for (int i = 0; i < n_writes; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (writes[i].meets(writes[j])) return true;
+        for (int j = 0; j < n_reads; ++j)
+            if (writes[i].meets(reads[j]) && !(in_place && i == j && writes[i].same(reads[j]))) return true;
+    }
+    return false;
+}
 
 }  // namespace dbs::ops

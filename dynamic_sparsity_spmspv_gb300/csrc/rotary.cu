@@ -256,6 +256,7 @@ dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype d
         head_dim > 1024 || dim < 0 || dim > head_dim || (dim & 1) || table_rows < 0)
         return DBS_ERR_INVALID_ARG;
     Rotary A{};
+    Places writes[3], reads[3];
     int64_t heads = 0;
     const bool work = batch > 0 && tokens > 0;
     if (work && (batch > (int64_t(1) << 31) || tokens > (int64_t(1) << 31) || batch * tokens >= (int64_t(1) << 31)))
@@ -269,16 +270,18 @@ dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype d
             return DBS_ERR_INVALID_ARG;
         if (work && P.to_slots && pages == 0) continue;                        // no slot is inside: nothing is written
         if (work && !P.out) return DBS_ERR_INVALID_ARG;
-        // heads of the output that share memory, or another head's place of the input
+        // heads of the output that share memory
         const int64_t n_batch = P.to_slots ? pages : batch, n_token = P.to_slots ? page_size : tokens;
         const Places out(P.out, dtype == DBS_F32 ? 4 : 2, head_dim, {{n_batch, P.out_batch}, {n_token, P.out_token}, {P.heads, P.out_head}});
-        const bool placed = P.in != P.out || (!P.to_slots && (P.heads == 1 || P.in_head == P.out_head) &&
-                                              (tokens == 1 || P.in_token == P.out_token) && (batch == 1 || P.in_batch == P.out_batch));
-        if (work && (P.in_head < 0 || P.in_token < 0 || P.in_batch < 0 || !out.own() || !placed)) return DBS_ERR_INVALID_ARG;
+        if (work && (P.in_head < 0 || P.in_token < 0 || P.in_batch < 0 || !out.own() || (P.to_slots && P.in == P.out))) return DBS_ERR_INVALID_ARG;
+        // (of a cache only the slots are written, which the host does not know)
+        if (work && !P.to_slots) writes[A.nparts] = out;
+        if (work) reads[A.nparts] = {P.in, dtype == DBS_F32 ? 4 : 2, head_dim, {{batch, P.in_batch}, {tokens, P.in_token}, {P.heads, P.in_head}}};
         A.part[A.nparts++] = P;
         heads += P.heads;
     }
     if (!work || heads == 0) return DBS_OK;
+    if (clash(writes, A.nparts, reads, A.nparts, true)) return DBS_ERR_INVALID_ARG;
     if (batch * tokens * head_dim >= (int64_t(1) << 32) - NT) return DBS_ERR_INVALID_ARG;
     A.head_dim = head_dim;
     A.dim = dim;

@@ -1273,10 +1273,13 @@ bool args_ok(const dbs_window_args *a)
     for (int64_t stride : {a->q_batch, a->q_token, a->q_head, a->k_page, a->k_entry, a->k_head, a->v_page, a->v_entry, a->v_head,
                            a->page_row, a->o_batch, a->o_token, a->o_head})
         if (stride < 0) return false;
-    // out over the inputs, or heads of it that share memory
-    if (a->out == a->q || (entries > 0 && (a->out == a->k || a->out == a->v))) return false;
+    // heads of out that share memory, or are the inputs'
+    const int64_t pages = entries > 0 ? a->pages : 0;
     const Places out(a->out, 2, a->head_dim, {{a->batch, a->o_batch}, {a->tokens, a->o_token}, {a->q_heads, a->o_head}});
-    if (!out.own()) return false;
+    if (!out.own() || out.meets({a->q, 2, a->head_dim, {{a->batch, a->q_batch}, {a->tokens, a->q_token}, {a->q_heads, a->q_head}}}) ||
+        out.meets({a->k, 2, a->head_dim, {{pages, a->k_page}, {a->page_size, a->k_entry}, {a->kv_heads, a->k_head}}}) ||
+        out.meets({a->v, 2, a->head_dim, {{pages, a->v_page}, {a->page_size, a->v_entry}, {a->kv_heads, a->v_head}}}))
+        return false;
     if (!a->page_table && (a->max_pages > 1 || (entries > 0 && a->pages < a->batch))) return false;
     return true;
 }

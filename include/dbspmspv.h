@@ -488,7 +488,9 @@ dbs_status dbs_rotary_table(int64_t positions, int32_t dim, double base, dbs_rot
  * ptr + b * batch_stride + t * token_stride + h * head_stride + c. */
 typedef struct {
     const void *in;
-    void *out;                 /* may be `in` (in place, with its strides), else must not overlap it */
+    void *out;                 /* may be `in` (in place, with its strides), else must not overlap it, nor
+                                  another group's; refused where it does for certain (not of slots, which the host
+                                  does not know) */
     int64_t in_batch, in_token, in_head;
     int64_t out_batch, out_token, out_head;
     int32_t heads;             /* 0 = absent */
@@ -625,7 +627,8 @@ dbs_status dbs_norm_rotary(const dbs_norm_heads *parts, int32_t nparts, dbs_dtyp
  * (a token whose position is outside the table: NaN in x' and weight'). */
 typedef struct {
     const void *grad, *in;     /* [batch, tokens, heads, head_dim] each */
-    void *out;                 /* x'; may be grad or in (with its strides), else must not overlap them */
+    void *out;                 /* x'; may be grad or in (with its strides), else must not overlap them, nor the
+                                  other group's (refused) */
     int64_t grad_batch, grad_token, grad_head;
     int64_t in_batch, in_token, in_head;
     int64_t out_batch, out_token, out_head;
@@ -670,7 +673,7 @@ typedef struct {
     int64_t window, sinks;     /* window >= 1, sinks >= 0 */
     float scale;               /* finite */
     void *out;                 /* [batch, tokens, q_heads, head_dim], each head in a place of its own, apart
-                                  from q and the caches */
+                                  from q and the caches (refused where it is not) */
     int64_t o_batch, o_token, o_head;
     float *lse;                /* device [batch, tokens, q_heads], natural logarithm, or NULL */
     void *scratch;             /* device, 32-byte aligned, dbs_window_attention_scratch bytes; the call
@@ -688,7 +691,8 @@ dbs_status dbs_window_attention(const dbs_window_args *a, void *stream);
  * page_size); refs[p] counts the owned entries of page_table that name page p (0: free).
  * These calls keep that, in place; what page_table holds behind a sequence's pages stays
  * as it is.  Page numbers outside [0, pages) are passed over.  What a call does is a
- * function of its inputs alone: free pages are taken in the order of their numbers. */
+ * function of its inputs alone: free pages are taken in the order of their numbers.
+ * Arrays that are written may not overlap one another, nor those that are read (refused). */
 typedef struct {
     int32_t *page_table;       /* device [batch, max_pages], rows page_row apart (>= max_pages) */
     int64_t batch, max_pages, page_row;
@@ -717,7 +721,8 @@ dbs_status dbs_cache_resize(const dbs_page_state *state, const int32_t *lens, in
 /* K and V of all layers: entry e of page p in layer l begins at l * layer + p * page +
  * e * entry, its heads `head` apart. */
 typedef struct {
-    void *k, *v;               /* device [layers, pages, page_size, heads, head_dim], places apart from one another */
+    void *k, *v;               /* device [layers, pages, page_size, heads, head_dim], places apart from one another
+                                  (in a fork k may be v) */
     int64_t layers, heads, head_dim;
     int32_t element_bytes;     /* 1, 2, 4 or 8: entries are copied as they are */
     int64_t k_layer, k_page, k_entry, k_head;
@@ -744,7 +749,7 @@ dbs_status dbs_cache_fork(const dbs_cache_data *data, const dbs_page_state *stat
  *   accepted       device int32[batch, max_accepted], rows accepted_stride apart: ascending
  *                  numbers below tree_lens[b]; the first that is not (-1, say) ends the list
  *   accepted_lens  device int32[batch], or NULL = max_accepted
- *   new_lens       device int32[batch]: kv_lens[b] - tree_lens[b] + those kept (kv_lens stays); apart from the lists
+ *   new_lens       device int32[batch]: kv_lens[b] - tree_lens[b] + those kept (kv_lens stays)
  * An entry that lies in, or would move to, a page outside [0, pages) is kept and counted without being moved.
  * Of `state` refs is not used; page_table may be NULL: sequence b is page b.  Drafted
  * entries have to lie in pages that b alone owns.  batch < 2^16, layers < 2^15.

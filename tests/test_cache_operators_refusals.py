@@ -259,3 +259,66 @@ def test_permuted_and_sliced_outputs_are_taken():
     for by in ((1536, 512, 64), (1536, 64, 192), (64, 128, 384), (4096, 1024, 128), (192, 64, 384), (64, 1 << 40, 1 << 50), (1 << 60, 512, 64)):
         a = dict(WIN, out=1 << 40, o0=by[0], o1=by[1], o2=by[2])
         assert _lib.load().dbs_window_attention_scratch(_lib.WINDOW_ARGS.pack(*a.values()), ctypes.byref(need)) != BAD, by
+
+
+FAR = 1 << 30
+
+
+def test_outputs_that_lie_on_inputs_in_part_are_refused():
+    """Shifted views, other strides of the same memory, an output on another group's input or output; places in between, and the very
+    same place where a call works in place, are not."""
+    need = ctypes.c_int64(-1)
+
+    def win(**kw):
+        return _lib.load().dbs_window_attention_scratch(_lib.WINDOW_ARGS.pack(*{**WIN, "q": FAR, "k": 2 * FAR, "v": 3 * FAR, "out": 4 * FAR, **kw}.values()), ctypes.byref(need))
+
+    size = 2 * 3 * 8 * 64 * 2                                              # of q
+    for shift in (-size + 2, -128, 128, 1024, size - 2):
+        assert win(out=FAR + shift) == BAD
+    assert win(out=FAR + size) != BAD and win(out=FAR - size) != BAD
+    k = dict(k0=2048, k1=128, k2=64, v0=2048, v1=128, v2=64)               # nine pages
+    assert win(out=2 * FAR + 9 * 4096 - 2, **k) == BAD and win(out=2 * FAR + 9 * 4096, **k) != BAD
+    assert win(out=3 * FAR + 4096 - size, **k) == BAD
+    fused = dict(q0=3 * 1024, q1=1024, q2=64, o0=3 * 1024, o1=1024, o2=64)  # q and another tensor of eight heads, side by side
+    assert win(out=FAR + 1024, **fused) != BAD and win(out=FAR + 1022, **fused) == BAD and win(out=FAR - 128, **fused) == BAD
+    q, k = part(inp=FAR, out=2 * FAR), part(inp=3 * FAR, out=4 * FAR)
+    for bad in (part(inp=3 * FAR, out=2 * FAR), part(inp=3 * FAR, out=2 * FAR + 1022), part(inp=3 * FAR, out=FAR), part(inp=3 * FAR, out=FAR + 512),
+                part(inp=3 * FAR, out=3 * FAR + 128), part(inp=2 * FAR, out=4 * FAR), part(inp=3 * FAR, out=3 * FAR - 1022)):
+        assert norm(parts=q + bad, n=2) == BAD and norm(parts=bad + q, n=2) == BAD
+        turn = q[:_rotary] + bad[:_rotary]
+        assert _lib.load().dbs_rotary(turn, 2, 2, 1, 4, 64, 64, A, 10, A, 0, 0, 1, 0, 0, None) == BAD
+    assert norm(parts=part(inp=FAR, out=2 * FAR, slots=1) + part(inp=3 * FAR, out=3 * FAR, slots=1), n=2, slots=A, pages=4, page=16) == BAD
+    g = dict(grad=FAR, inp=2 * FAR, out=3 * FAR, dw=4 * FAR)
+    other = dict(grad=5 * FAR, inp=6 * FAR, out=7 * FAR, dw=8 * FAR)
+    for kw in (dict(out=3 * FAR), dict(out=3 * FAR + 128), dict(out=FAR), dict(out=2 * FAR + 1022), dict(out=5 * FAR - 128), dict(out=6 * FAR + 128), dict(dw=4 * FAR),
+               dict(dw=4 * FAR - 252), dict(dw=3 * FAR), dict(inp=3 * FAR), dict(grad=3 * FAR + 256)):
+        assert gradient(parts=gpart(**g) + gpart(**{**other, **kw}), n=2) == BAD, kw
+
+
+_rotary = struct.calcsize("@" + _lib.ROTARY_HEADS)
+
+
+def test_arrays_of_a_cache_s_pages_that_overlap_are_refused():
+    lib, big = _lib.load(), 1 << 40
+    apart = dict(table=FAR, kv=2 * FAR, refs=3 * FAR)
+
+    def resize(lens=4 * FAR, status=5 * FAR, slots=6 * FAR, **kw):
+        return lib.dbs_cache_resize(state(**dict(apart, **kw)), lens, status, slots, 2, A, big, None)
+
+    for kw in (dict(lens=2 * FAR + 8), dict(status=4 * FAR - 8), dict(slots=4 * FAR - 20), dict(slots=2 * FAR + 4), dict(status=6 * FAR + 20), dict(refs=2 * FAR + 8),
+               dict(kv=FAR + 4), dict(lens=3 * FAR + 32), dict(status=FAR + 44), dict(refs=FAR - 32), dict(lens=FAR + 40)):
+        assert resize(**kw) == BAD, kw
+
+    def fork(parents=4 * FAR, children=5 * FAR, status=6 * FAR, d=data(k=7 * FAR, v=8 * FAR), **kw):
+        return lib.dbs_cache_fork(d, state(**dict(apart, **kw)), parents, children, 2, status, A, big, None)
+
+    for kw in (dict(status=4 * FAR + 4), dict(children=6 * FAR - 4), dict(parents=2 * FAR + 8), dict(children=3 * FAR), dict(refs=2 * FAR), dict(status=FAR),
+               dict(d=data(k=7 * FAR, v=7 * FAR + 128))):
+        assert fork(**kw) == BAD, kw
+
+    def compact(tree=4 * FAR, acc=5 * FAR, lens=6 * FAR, new=9 * FAR, d=data(k=7 * FAR, v=8 * FAR), **kw):
+        return lib.dbs_cache_compact(d, state(**dict(apart, **kw)), tree, acc, 4, 4, lens, new, None)
+
+    for kw in (dict(new=4 * FAR + 8), dict(new=5 * FAR + 44), dict(new=6 * FAR - 8), dict(new=2 * FAR - 8), dict(new=FAR + 12), dict(d=data(k=7 * FAR, v=7 * FAR)),
+               dict(d=data(k=7 * FAR, v=7 * FAR + 2 * 18432 * 2 - 2))):
+        assert compact(**kw) == BAD, kw

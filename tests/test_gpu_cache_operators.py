@@ -1069,3 +1069,36 @@ def test_what_a_row_sees_counts_however_little_it_weighs(T, hq, hk, D, S, page, 
     for f in attend:
         out, lse = f()
         assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+def test_outputs_within_the_inputs_buffers():
+    """Heads of q, k and v side by side in one buffer: turned in place and attended into v's place, bit for bit as with tensors of their own; views
+    that lie on an input in part are refused."""
+    rng = np.random.default_rng(8)
+    B, T, hq, hk, D = 2, 40, 4, 4, 64
+    fused = rnd(rng, "bf16", B, T, hq + 2 * hk, D)
+    q, k, v = fused.split([hq, hk, hk], 2)
+    w, table, pos = rnd(rng, "bf16", D), dbs.rotary_table(64, D), ints([list(range(T))] * B)
+    own = dbs.norm_rotary(q.clone(), k.clone(), w, w, table, pos)
+    kc, vc = own[1].contiguous(), v.clone()
+    want = dbs.window_attention(own[0], kc, vc, ints([T] * B), 17)
+    dbs.norm_rotary(q, k, w, w, table, pos, q_out=q, k_out=k)
+    assert torch.equal(q, own[0]) and torch.equal(k, own[1])
+    assert dbs.window_attention(q, kc, vc, ints([T] * B), 17, out=v) is v and torch.equal(v, want)
+    one, heads = fused.flatten(), (B, T, hq, D)
+    for bad in (fused[:, :, 1:1 + hq], fused[:, :, 2:2 + hq], one[64:].as_strided(heads, q.stride()), one.as_strided(heads, (T * hq * D, hq * D, D, 1))):
+        with pytest.raises(dbs.DbsError):
+            dbs.window_attention(q, kc, vc, ints([T] * B), 17, out=bad)
+        with pytest.raises(dbs.DbsError):
+            dbs.norm_rotary(q, None, w, None, table, pos, q_out=bad)
+        with pytest.raises(dbs.DbsError):
+            dbs.rotary(q, None, table, pos, q_out=bad)
+    with pytest.raises(dbs.DbsError):
+        dbs.norm_rotary(q, k, w, w, table, pos, q_out=k)
+    with pytest.raises(dbs.DbsError):
+        dbs.window_attention(q, kc, vc, ints([T] * B), 17, out=vc)
+    lens = ints([5, 6, 7, 8])
+    with pytest.raises(dbs.DbsError):
+        dbs.cache_resize(ints([[-1, -1]] * 3), lens[:3], ints([0] * 8), lens[1:], 4)
+    with pytest.raises(dbs.DbsError):
+        dbs.cache_compact(kc, kc, ints([T] * B), ints([2] * B), ints([[1]] * B))
