@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(PLAN_NT) k_resize(Resize A, int slots_here)
                 const int p = s.page_table[b * s.page_row + c];
                 if (is_page(s, p)) atomicSub(s.refs + p, 1);
             }
+        __syncwarp();                              // (every lane has read the length)
         if (lane == 0) {
             A.old[b] = old;
             if (n >= 0 && n <= old) s.kv_lens[b] = n;

@@ -1102,3 +1102,18 @@ def test_outputs_within_the_inputs_buffers():
         dbs.cache_resize(ints([[-1, -1]] * 3), lens[:3], ints([0] * 8), lens[1:], 4)
     with pytest.raises(dbs.DbsError):
         dbs.cache_compact(kc, kc, ints([T] * B), ints([2] * B), ints([[1]] * B))
+
+
+def test_cache_resize_of_many_long_sequences():
+    """More sequences than a block has threads, cut by numbers of pages that keep a warp's lanes busy for different times."""
+    rng = np.random.default_rng(12)
+    batch, per, page = 1100, 70, 1
+    pool = Pool(batch, per, 60000, page)
+    state = pool.device()
+    for turn in range(6):
+        lens = rng.integers(0, per + 2, batch) if turn % 2 == 0 else np.where(rng.random(batch) < 0.2, -1, rng.integers(0, 4, batch) * pool.kv // 4)
+        status, slots = dbs.cache_resize(*state, ints(lens.tolist()), page, columns=3)
+        want, where = pool.resize(lens, 3)
+        assert np.array_equal(status.cpu().numpy(), want) and np.array_equal(slots.cpu().numpy(), where)
+        pool.same(state)
+        pool.consistent()
