@@ -1117,3 +1117,138 @@ def test_cache_resize_of_many_long_sequences():
         assert np.array_equal(status.cpu().numpy(), want) and np.array_equal(slots.cpu().numpy(), where)
         pool.same(state)
         pool.consistent()
+
+
+# ---- more units than blocks, longer lines ----
+
+
+def window_ref_gpu(q, k, v, kv, tl, window, sinks, table):
+    """window_ref of all rows in 64 bits on the GPU, a kv head of a sequence and 512 tokens at a time."""
+    B, T, H, D = q.shape
+    hk = k.shape[2]
+    o, mag = (torch.zeros((B, T, H, D), dtype=torch.float64, device=DEV) for _ in range(2))
+    lse = torch.full((B, T, H), -INF, dtype=torch.float64, device=DEV)
+    for b in range(B):
+        n, first = int(kv[b]), int(kv[b] - tl[b])
+        kb, vb = (x[b] if table is None else x[torch.from_numpy(table[b]).long().to(DEV)].flatten(0, 1) for x in (k, v))
+        for t0 in range(max(0, -first), int(tl[b]), 512):
+            t1 = min(int(tl[b]), t0 + 512)
+            p, j = torch.arange(first + t0, first + t1, device=DEV)[:, None], torch.arange(n, device=DEV)
+            hide = (j > p) | ((p - j >= window) & (j >= sinks))
+            for h in range(hk):
+                G = slice(h * (H // hk), (h + 1) * (H // hk))
+                x = torch.einsum("tgd,jd->gtj", q[b, t0:t1, G].double(), kb[:n, h].double()) * D**-0.5
+                x.masked_fill_(hide, -INF)
+                lse[b, t0:t1, G] = torch.logsumexp(x, -1).T
+                e = torch.softmax(x, -1)
+                o[b, t0:t1, G] = torch.einsum("gtj,jd->tgd", e, vb[:n, h].double())
+                mag[b, t0:t1, G] = torch.einsum("gtj,jd->tgd", e, vb[:n, h].double().abs())
+    return o, mag, lse
+
+
+def check_window_gpu(dt, q, k, v, table, kv, tl, window, sinks):
+    out, lse = dbs.window_attention(q, k, v, ints(kv), window, sinks=sinks, q_lens=ints(tl), page_table=None if table is None else ints(table), return_lse=True)
+    o, mag, rl = window_ref_gpu(q, k, v, kv, tl, window, sinks, table)
+    assert ((out.double() - o).abs() <= (U[dt] + 3e-4) * mag + U[dt] * o.abs() + ETA[dt]).all()
+    assert ((lse == rl) | ((lse.double() - rl).abs() <= 4e-4)).all()
+
+
+MANY_UNITS = [
+    # B, T, hq, hkv, D, S, page, window, sinks: three units of rows and more for a multiprocessor
+    (64, 70, 32, 8, 64, 200, 16, 50, 3), (64, 70, 32, 8, 128, 230, 16, 90, 0), (40, 70, 32, 8, 256, 150, 64, 60, 5), (96, 40, 8, 8, 128, 300, 0, 1000, 0),
+    (1, 4100, 32, 8, 128, 4100, 16, 700, 4), (1, 4100, 32, 8, 64, 4200, 0, 1500, 70), (1, 2050, 16, 8, 256, 2050, 32, 300, 4), (1, 4100, 16, 8, 256, 4100, 16, 300, 4), (2, 3000, 40, 8, 128, 3300, 24, 64, 0)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("B,T,hq,hkv,D,S,page,window,sinks", MANY_UNITS)
+def test_window_of_more_units_than_blocks(dt, B, T, hq, hkv, D, S, page, window, sinks):
+    """Blocks go from unit to unit, some of them without tokens, without entries, or with fewer entries than tokens."""
+    rng = np.random.default_rng(B + T + D)
+    q, k, v, table = window_inputs(rng, dt, B, T, hq, hkv, D, S, page)
+    if B <= 2:
+        kv, tl = np.array([S, S - 100][:B]), np.array([T, T - 77][:B])
+    else:
+        kv, tl = rng.integers(0, S + 1, B), np.where(rng.random(B) < 0.2, 0, rng.integers(0, T + 1, B))
+        kv[:4], tl[:4] = [0, T // 2, S, 1], [T, T, T, 1]
+    check_window_gpu(dt, q, k, v, table, kv.tolist(), tl.tolist(), window, sinks)
+
+
+@pytest.mark.parametrize("B,T,hq,hk,D,S,window,least", [(1, 4100, 32, 8, 128, 4100, 200, 500), (64, 70, 32, 8, 64, 100, 60, 500), (1, 2050, 16, 8, 256, 2050, 100, 4),
+                                                        (1, 4100, 16, 8, 256, 4100, 100, 250)])
+def test_window_that_gives_up_among_its_units_leaves_nan(B, T, hq, hk, D, S, window, least):
+    """A block whose wait ran out leaves NaN in all units that it had ahead, the others have theirs.  Units are 256 rows, of heads of 256
+    128; the first of a call have the last tokens, which may be few.  With 152 blocks: 520 units, three and more a block, two of them
+    full; 1024 units, half of them of 6 tokens; 264 units, of which block 0 has the first alone, of 2050 - 32 * 64 tokens of 2 heads; 520."""
+    rng = np.random.default_rng(B + T)
+    q, k, v, table = window_inputs(rng, "bf16", B, T, hq, hk, D, S, 16)
+    dbs.operators_check()
+
+    def call():
+        return dbs.window_attention(q, k, v, ints([S] * B), window, sinks=3, page_table=ints(table), out=torch.full_like(q, 5.0), return_lse=True)
+
+    clean, lse = call()
+    assert dbs.operators_check() == 0
+    for block in (-2, 0, 70):
+        with waits_run_out(block):
+            got, gl = call()
+        assert dbs.operators_check() == 4 and dbs.operators_check() == 0
+        nan = torch.isnan(got)
+        assert (nan.all(3) == nan.any(3)).all() and (nan.any(3) == torch.isnan(gl)).all()
+        nan = nan.any(3)
+        assert nan.all() if block == -2 else least <= nan.sum().item() <= nan.numel() // 20
+        assert torch.equal(got[~nan], clean[~nan]) and torch.equal(gl[~nan], lse[~nan])
+        again, al = call()
+        assert torch.equal(again, clean) and torch.equal(al, lse)
+
+
+def test_window_values_that_are_not_finite_among_many_units():
+    """NaN in entries that only some rows see, in a prompt of more units than blocks: the rows that see them are NaN, the others as without."""
+    rng = np.random.default_rng(77)
+    T, hq, hk, D, window = 4100, 32, 8, 128, 300
+    q, k, v, _ = window_inputs(rng, "bf16", 1, T, hq, hk, D, T, 0)
+    clean, lse = dbs.window_attention(q, k, v, ints([T]), window, sinks=2, return_lse=True)
+    sees = torch.zeros(T, dtype=torch.bool, device=DEV)
+    for j in (700, 701, 2303, 4000):
+        v[:, j] = NAN
+        sees[j:j + window] = True
+    got, gl = dbs.window_attention(q, k, v, ints([T]), window, sinks=2, return_lse=True)
+    assert torch.equal(gl, lse) and torch.isnan(got[0, sees]).all()
+    # rows near them are made anew, without the rounding of probabilities (2^-8 of sum p |v|, which is below 2 here; both results are rounded)
+    assert ((got[0, ~sees].float() - clean[0, ~sees].float()).abs() <= 2**-7 * clean[0, ~sees].float().abs() + 2**-7).all()
+    far = ~sees
+    for j in (700, 701, 2303, 4000):
+        far[max(0, j - 300):j + window + 300] = False
+    assert torch.equal(got[0, far], clean[0, far])
+
+
+LONG_LINES = [
+    # B, T, hq, hkv, D, S, page, window, sinks: few rows, up to sixteen blocks to a line
+    (1, 1, 8, 1, 128, 2000, 16, 5000, 0), (1, 1, 8, 2, 128, 4001, 16, 3900, 4), (1, 1, 32, 8, 128, 9001, 0, 8192, 4), (1, 1, 16, 1, 64, 9001, 8, 9000, 0),
+    (1, 2, 8, 8, 64, 6000, 16, 5000, 100), (1, 1, 8, 1, 256, 5003, 16, 5003, 0), (2, 1, 16, 8, 256, 3001, 0, 2500, 7), (1, 3, 5, 1, 96, 7777, 5, 7000, 3),
+    (1, 1, 8, 2, 128, 4000, 1, 3000, 0), (3, 4, 4, 4, 128, 4500, 64, 4000, 1), (1, 16, 1, 1, 64, 8000, 24, 100000, 0)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("B,T,hq,hkv,D,S,page,window,sinks", LONG_LINES)
+def test_window_of_few_rows_over_long_lines(dt, B, T, hq, hkv, D, S, page, window, sinks):
+    rng = np.random.default_rng(T + D + S)
+    q, k, v, table = window_inputs(rng, dt, B, T, hq, hkv, D, S, page)
+    check_window_gpu(dt, q, k, v, table, [S] + [S - 1000 * b - 13 for b in range(1, B)], [T] * B, window, sinks)
+
+
+@pytest.mark.parametrize("T", [2, 7])
+def test_window_long_line_with_values_that_are_not_finite(T):
+    """Few rows over sixteen blocks: rows before the first entry that is not finite are as without it, the others NaN."""
+    rng = np.random.default_rng(T)
+    S, hq, hk, D = 4000, 8, 4, 128
+    q, k, v, table = window_inputs(rng, "bf16", 1, T, hq, hk, D, S, 16)
+    before = T // 2
+    v2, p = v.clone(), S - T + before
+    assert before > 0
+    flat = v2[torch.from_numpy(table[0]).long().to(DEV)].reshape(1, -1, hk, D)
+    flat[:, p:] = NAN
+    v2[torch.from_numpy(table[0]).long().to(DEV)] = flat.reshape(-1, 16, hk, D)
+    got, gl = dbs.window_attention(q, k, v2, ints([S]), S, sinks=2, page_table=ints(table), return_lse=True)
+    o, mag, lse = window_ref_gpu(q, k, v, [S], [T], S, 2, table)
+    assert torch.isnan(got[:, before:]).all() and ((gl - lse).abs() <= 4e-4).all()
+    assert ((got[:, :before].double() - o[:, :before]).abs() <= (U["bf16"] + 3e-4) * mag[:, :before] + U["bf16"] * o[:, :before].abs()).all()
