@@ -1,11 +1,9 @@
 // Attention of drafted tokens over a (paged) cache (dbs_tree_attention,
 // sm_103a): softmax over the entries a token sees, with the running maximum
 // and sum held in fp32.
-#include "ops_dev.h"
+#include "cache_dev.h"
 #include "places.h"
 #include "tc_dev.h"
-
-#include <cmath>
 
 using namespace dbs::ops;
 
@@ -36,20 +34,6 @@ __device__ __forceinline__ Seq sequence(const Attn &A, int64_t b)
     s.tree = (int)(t < 0 ? 0 : t > a.tokens ? a.tokens : t);
     s.first = s.kv - s.tree;
     return s;
-}
-
-// Where entry j of sequence b lies: its page, and its place in it.
-struct Place {
-    int64_t page;
-    uint32_t in;
-};
-
-__device__ __forceinline__ Place place_of(const dbs_attention_args &a, int64_t b, int j)
-{
-    if (!a.page_table) return {b, (uint32_t)j};
-    const uint32_t size = (uint32_t)a.page_size, n = (uint32_t)j / size;
-    const int64_t p = a.page_table[b * a.page_row + n];
-    return {p < 0 ? 0 : p >= a.pages ? a.pages - 1 : p, (uint32_t)j - n * size};
 }
 
 // Whether token t of sequence b sees drafted entry i (0 <= i < tree).
@@ -106,39 +90,13 @@ __device__ __forceinline__ void row_by_warp(const Attn &A, int64_t b, int t, int
                                          float (&o)[8])
 {
     const dbs_attention_args &a = A.a;
-    const int lane = threadIdx.x & 31, hk = h / (a.q_heads / a.kv_heads);
     const Seq s = sequence(A, b);
-    const T *q = (const T *)a.q + b * a.q_batch + t * a.q_token + h * a.q_head;
     float qr[8];
-    m = -INFINITY;
-    l = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        qr[e] = lane + 32 * e < a.head_dim ? to_f32(q[lane + 32 * e]) : 0.f;
-        o[e] = 0.f;
-    }
+    begin_row<T>(a, b, t, h, qr, m, l, o);
     if (t >= s.tree) return;
     for (int j = j0; j < s.kv; j += step) {
         if (j >= s.first && !sees(A, b, t, j - s.first)) continue;
-        const Place at = place_of(a, b, j);
-        const T *k = (const T *)a.k + at.page * a.k_page + at.in * a.k_entry + hk * a.k_head;
-        const T *v = (const T *)a.v + at.page * a.v_page + at.in * a.v_entry + hk * a.v_head;
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (lane + 32 * e < a.head_dim) x = fmaf(qr[e], to_f32(k[lane + 32 * e]), x);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
-        x *= A.scale_log2;
-        const float top = fmaxf(m, x);
-        // all scores -inf so far: nothing is carried and nothing counts
-        const float keep = m == -INFINITY ? 0.f : exp2f(m - top);
-        const float pr = x == -INFINITY ? 0.f : exp2f(x - top);
-        l = l * keep + pr;
-        m = top;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (lane + 32 * e < a.head_dim) o[e] = fmaf(pr, to_f32(v[lane + 32 * e]), o[e] * keep);
+        take_entry<T>(a, place_of(a, b, j), h / A.group, A.scale_log2, qr, m, l, o);
     }
 }
 
@@ -187,19 +145,6 @@ __device__ __noinline__ Eight add_odd(const Attn &A, int64_t b, int t, int hk, E
     return o;
 }
 
-// Writes a row from its sums: out = o / l, lse = (m + log2 l) ln 2.
-template <class T>
-__device__ __forceinline__ void store_row(const Attn &A, int64_t b, int t, int h, float m, float l, const float (&o)[8])
-{
-    const dbs_attention_args &a = A.a;
-    const int lane = threadIdx.x & 31;
-    T *out = (T *)a.out + b * a.o_batch + t * a.o_token + h * a.o_head;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (lane + 32 * e < a.head_dim) out[lane + 32 * e] = from_f32<T>(l == 0.f ? 0.f : o[e] / l);
-    if (a.lse && lane == 0) a.lse[(b * a.tokens + t) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-}
-
 constexpr int ROW_NT = 128;
 
 // Any head size and alignment: one block per query row, its warps take every
@@ -238,7 +183,7 @@ __global__ void __launch_bounds__(ROW_NT) k_attn_rows(Attn A)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o[e] += f == 0.f ? 0.f : f * s_o[w][lane + 32 * e];
             }
-            store_row<T>(A, b, t, h, top, sum, o);
+            store_row<T>(a, b, t, h, top, sum, o);
         }
     }
 }
@@ -540,42 +485,13 @@ __global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int rows
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = q.v[e];
         }
-        store_row<T>(A, b, row.t, row.h, top, sum, o);
+        store_row<T>(a, b, row.t, row.h, top, sum, o);
     }
 }
 
 // ---- few rows: every warp streams its own entries ----
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-template <class T> __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
-template <> __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <> __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-constexpr int FEW_NT = 128, FEW_W = FEW_NT / 32;
-constexpr int FEW_ROWS = 16;               // one matrix instruction's rows
-constexpr int FEW_STEP = 16;               // entries of a stage of a warp
-constexpr int FEW_KEYS = FEW_W * FEW_STEP;
 constexpr int FEW_STAGES = 3;
-constexpr int FEW_SPLIT = 16;      // blocks of a cluster, at most
 
 template <int DP> constexpr int few_smem() { return FEW_W * FEW_STAGES * 2 * FEW_STEP * DP * 2; }
 
@@ -831,7 +747,7 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
 #pragma unroll
                         for (int e = 0; e < 8; ++e) oo[e] = w.v[e];
                     }
-                    store_row<T>(A, b, row.t, row.h, top, sum, oo);
+                    store_row<T>(a, b, row.t, row.h, top, sum, oo);
                 } else {
 #pragma unroll
                     for (int e = 0; e < DP / 32; ++e)
@@ -845,27 +761,20 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
             }
             if constexpr (CLUSTER) {
                 if (threadIdx.x == 0) j_odd = odd;
-                asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+                cluster_sync();
                 // 32 columns of a row for each of the cluster's warps in turn
-                auto from = [&](const void *p, int block) {
-                    uint32_t at;
-                    float v;
-                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(block));
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-                    return v;
-                };
                 const int64_t left = (int64_t)a.tokens * A.group - R0;
                 const int rows = (int)(left < FEW_ROWS ? left : FEW_ROWS);
                 for (int i = rank * FEW_W + warp; i < rows * (DP / 32); i += split * FEW_W) {
                     const int r = i / (DP / 32), e0 = i % (DP / 32);
                     const Row row = row_of(A, hk, R0 + r);
                     const bool in = lane < split;
-                    const float m = in ? from(j_m + r, lane) : -INFINITY;
-                    float l = in ? from(j_l + r, lane) : 0.f;
-                    const bool found = in && __float_as_int(from(&j_odd, lane)) != 0;
+                    const float m = in ? remote(j_m + r, lane) : -INFINITY;
+                    float l = in ? remote(j_l + r, lane) : 0.f;
+                    const bool found = in && __float_as_int(remote(&j_odd, lane)) != 0;
                     float v[FEW_SPLIT], o = 0.f, top = m;
 #pragma unroll
-                    for (int k = 0; k < FEW_SPLIT; ++k) v[k] = k < split ? from((const float *)(ring + joined(r)) + lane + 32 * e0, k) : 0.f;
+                    for (int k = 0; k < FEW_SPLIT; ++k) v[k] = k < split ? remote((const float *)(ring + joined(r)) + lane + 32 * e0, k) : 0.f;
 #pragma unroll
                     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
                     const float f = weight_of(m, l, top);
@@ -888,10 +797,10 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
                         for (int e = 0; e < 8; ++e) o = e == e0 ? w.v[e] : o;
                     }
                     if (lane + 32 * e0 < a.head_dim) ((T *)a.out + b * a.o_batch + row.t * a.o_token + row.h * a.o_head)[lane + 32 * e0] = from_f32<T>(l == 0.f ? 0.f : o / l);
-                    if (a.lse && e0 == 0 && lane == 0) a.lse[(b * a.tokens + row.t) * a.q_heads + row.h] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+                    if (a.lse && e0 == 0 && lane == 0) store_lse(a, b, row.t, row.h, top, l);
                 }
                 // (no block ends while another one reads its shared memory)
-                asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+                cluster_sync();
                 break;
             }
             __syncthreads();       // the rings are free again
@@ -957,31 +866,6 @@ template <int DP, int TILES> struct Many {
 static_assert(!Many<128, 2>::PS || Many<128, 2>::KEYS == 64, "a row of P is a row of the swizzle");
 static_assert(Many<128, 2>::O_COL + 2 * 128 <= 512 && Many<256, 1>::O_COL + 256 <= 512, "tensor memory");
 
-// 32 bytes, a whole sector, at once.
-__device__ __forceinline__ void store32(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g, uint32_t h)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
-}
-// (to 2 units of the last place, and 0 below 2^-126: far below the 16 bits that P keeps)
-__device__ __forceinline__ float pow2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Tensor maps of K and V: [pages, entries, heads, head_dim], boxes of 64 columns
-// of one head of `box` entries.
-struct Maps {
-    CUtensorMap k, v;
-    int box;
-};
-
-__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap *map, int d, int head, int entry, int page, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-                 "l"(map), "r"(bar), "r"(d), "r"(head), "r"(entry), "r"(page) : "memory");
-}
 // After a wait ran out, for the units that are left of a block's piece: who works on
 // them, for the join, by one warp; and NaN in their rows, or, of a part, sums that the
 // join makes NaN of, a row by each softmax thread (row `row` of row tile `r`).  (The first is
@@ -1209,9 +1093,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_attn_many(Attn A, Sh
                     const int d = 32 * c + e;
                     if (d >= a.head_dim) break;
                     if (!seg.whole) {
-                        store32(part + (int64_t)slot_row * a.head_dim + d, __float_as_uint(v[e]), __float_as_uint(v[e + 1]), __float_as_uint(v[e + 2]),
-                                __float_as_uint(v[e + 3]), __float_as_uint(v[e + 4]), __float_as_uint(v[e + 5]), __float_as_uint(v[e + 6]),
-                                __float_as_uint(v[e + 7]));
+                        store32(part + (int64_t)slot_row * a.head_dim + d, v[e], v[e + 1], v[e + 2], v[e + 3], v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
                     } else if (A.wide_out) {
                         *(uint4 *)(out + d) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]), pack2<T>(v[e + 4], v[e + 5]),
                                                          pack2<T>(v[e + 6], v[e + 7]));
@@ -1581,16 +1463,11 @@ struct Plan {
     int64_t slots, scratch;    // bytes of scratch: the slots, and all
 };
 
-bool aligned8(int64_t v) { return (v & 7) == 0; }
-
 dbs_status plan_of(const dbs_attention_args &a, Plan &P)
 {
     P = Plan{};
     const int64_t entries = a.max_pages * a.page_size, rows = a.tokens * (a.q_heads / a.kv_heads);
-    // 16-byte copies of heads: every head starts on such a boundary
-    P.rows = a.head_dim % 8 || !aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned8(a.q_batch) ||
-             !aligned8(a.q_token) || !aligned8(a.q_head) || !aligned8(a.k_page) || !aligned8(a.k_entry) ||
-             !aligned8(a.k_head) || !aligned8(a.v_page) || !aligned8(a.v_entry) || !aligned8(a.v_head);
+    P.rows = !on_vectors(a);
     if (P.rows) return DBS_OK;
     const int sms = multiprocessors();
     if (sms == 0) return DBS_ERR_CUDA;
@@ -1688,35 +1565,6 @@ dbs_status launch_few(const Attn &A, const Plan &P, cudaStream_t s)
     k_attn_few<T, DP, false><<<P.blocks, FEW_NT, few_smem<DP>(), s>>>(A, P.share, 0);
     const dbs_status st = launched();
     return st == DBS_OK ? launch_join<T>(A, P, s) : st;
-}
-
-// Boxes of the caches, or false where pages or strides do not allow them.
-bool make_maps(const dbs_attention_args &a, int keys, Maps &M)
-{
-    const encode_tiled_fn encode = encode_tiled();
-    if (!encode || a.page_size < 1 || a.pages < 1) return false;
-    // a sequence's own page is one run of entries; pages of a table split into boxes
-    M.box = keys;
-    if (a.page_table)
-        while (M.box >= 8 && a.page_size % M.box) M.box /= 2;
-    if (M.box < 8) return false;
-    for (int i = 0; i < 2; ++i) {
-        const cuuint64_t dims[4] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.kv_heads, (cuuint64_t)a.page_size, (cuuint64_t)a.pages};
-        const int64_t by[3] = {i ? a.v_head : a.k_head, i ? a.v_entry : a.k_entry, i ? a.v_page : a.k_page};
-        const cuuint32_t box[4] = {64, 1, (cuuint32_t)M.box, 1}, ones[4] = {1, 1, 1, 1};
-        cuuint64_t strides[3];
-        for (int d = 0; d < 3; ++d) {
-            // (a dimension of one entry has any stride)
-            const int64_t bytes = dims[d + 1] == 1 ? 16 * a.head_dim : by[d] * 2;
-            if (bytes <= 0 || bytes >= int64_t(1) << 40 || dims[d + 1] >= cuuint64_t(1) << 31) return false;
-            strides[d] = (cuuint64_t)bytes;
-        }
-        if (encode(i ? &M.v : &M.k, a.dtype == DBS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                   const_cast<void *>(i ? a.v : a.k), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return false;
-    }
-    return true;
 }
 
 template <class T, int DP, int TILES, bool BOXES>
@@ -1817,8 +1665,7 @@ dbs_status dbs_tree_attention(const dbs_attention_args *a, void *stream)
     const dbs_status st = plan_of(*a, P);
     if (st != DBS_OK) return st;
     if (P.scratch > 0 && (!a->scratch || (reinterpret_cast<uintptr_t>(a->scratch) & 31u) || a->scratch_bytes < P.scratch)) return DBS_ERR_INVALID_ARG;
-    const bool wide_out = aligned16(a->out) && aligned8(a->o_batch) && aligned8(a->o_token) && aligned8(a->o_head);
-    const Attn A{*a, a->scale * 1.4426950408889634f, (int)((a->tokens + 63) / 64), wide_out, a->q_heads / a->kv_heads, waits()};
+    const Attn A{*a, a->scale * 1.4426950408889634f, (int)((a->tokens + 63) / 64), wide_out(a->out, a->o_batch, a->o_token, a->o_head), a->q_heads / a->kv_heads, waits()};
     P.share.scratch = (float *)a->scratch;
     P.share.units = (int4 *)((char *)a->scratch + P.slots);
     return a->dtype == DBS_F16 ? launch<__half>(A, P, (cudaStream_t)stream) : launch<__nv_bfloat16>(A, P, (cudaStream_t)stream);

@@ -86,11 +86,6 @@ __device__ __forceinline__ uint64_t mul_two(uint64_t a, uint64_t b)
     return v;
 }
 
-// What a part of a softmax's row counts in the row, whose maximum (in powers of two) is `top`: its sum and its outputs
-// times that.  A part without a maximum has nothing, or a NaN that has to stay.  The product is taken even where the
-// weight is 0: a NaN in a part is one in the row, however little it weighs.
-__device__ __forceinline__ float weight_of(float m, float l, float top) { return m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2f(m - top); }
-
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 // ---- barriers in shared memory ----

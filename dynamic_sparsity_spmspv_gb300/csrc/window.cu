@@ -1,11 +1,9 @@
 // Attention with a sliding window and sinks over a (paged) cache
 // (dbs_window_attention, sm_103a): softmax over the entries a token sees, with the
 // running maximum and sum held in fp32.
-#include "ops_dev.h"
+#include "cache_dev.h"
 #include "places.h"
 #include "tc_dev.h"
-
-#include <cmath>
 
 using namespace dbs::ops;
 
@@ -38,20 +36,6 @@ __device__ __forceinline__ Seq sequence(const Win &A, int64_t b)
     return s;
 }
 
-// Where entry j of sequence b lies: its page, and its place in it.
-struct Place {
-    int64_t page;
-    uint32_t in;
-};
-
-__device__ __forceinline__ Place place_of(const dbs_window_args &a, int64_t b, int j)
-{
-    if (!a.page_table) return {b, (uint32_t)j};
-    const uint32_t size = (uint32_t)a.page_size, n = (uint32_t)j / size;
-    const int64_t p = a.page_table[b * a.page_row + n];
-    return {p < 0 ? 0 : p >= a.pages ? a.pages - 1 : p, (uint32_t)j - n * size};
-}
-
 // The first entry of the window of a token at position p (p >= 0).
 __device__ __forceinline__ int window_start(const Win &A, int p) { return p >= A.window ? p - A.window + 1 : 0; }
 
@@ -63,39 +47,14 @@ __device__ __forceinline__ void row_by_warp(const Win &A, const Seq &s, int64_t 
                                             float (&o)[8])
 {
     const dbs_window_args &a = A.a;
-    const int lane = threadIdx.x & 31, hk = h / A.group;
-    const T *q = (const T *)a.q + b * a.q_batch + t * a.q_token + h * a.q_head;
+    const int lane = threadIdx.x & 31;
     float qr[8];
-    m = -INFINITY;
-    l = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        qr[e] = lane + 32 * e < a.head_dim ? to_f32(q[lane + 32 * e]) : 0.f;
-        o[e] = 0.f;
-    }
+    begin_row<T>(a, b, t, h, qr, m, l, o);
     const int p = s.first + t;
     if (t >= s.tokens || p < 0) return;
     const int lo = window_start(A, p), sinks = A.sinks < lo ? A.sinks : lo, n = sinks + p + 1 - lo;
     for (int i = part; i < n; i += step) {
-        const Place at = place_of(a, b, i < sinks ? i : lo + i - sinks);
-        const T *k = (const T *)a.k + at.page * a.k_page + at.in * a.k_entry + hk * a.k_head;
-        const T *v = (const T *)a.v + at.page * a.v_page + at.in * a.v_entry + hk * a.v_head;
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (lane + 32 * e < a.head_dim) x = fmaf(qr[e], to_f32(k[lane + 32 * e]), x);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
-        x *= A.scale_log2;
-        const float top = fmaxf(m, x);
-        // all scores -inf so far: nothing is carried and nothing counts
-        const float keep = m == -INFINITY ? 0.f : exp2f(m - top);
-        const float pr = x == -INFINITY ? 0.f : exp2f(x - top);
-        l = l * keep + pr;
-        m = top;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (lane + 32 * e < a.head_dim) o[e] = fmaf(pr, to_f32(v[lane + 32 * e]), o[e] * keep);
+        take_entry<T>(a, place_of(a, b, i < sinks ? i : lo + i - sinks), h / A.group, A.scale_log2, qr, m, l, o);
         if (OUT_ONLY) {
             bool rest = false;
 #pragma unroll
@@ -103,25 +62,6 @@ __device__ __forceinline__ void row_by_warp(const Win &A, const Seq &s, int64_t 
             if (!__any_sync(~0u, rest)) break;
         }
     }
-}
-
-// Writes a row from its sums: out = o / l, lse = (m + log2 l) ln 2.
-template <class T>
-__device__ __forceinline__ void store_out(const Win &A, int64_t b, int t, int h, float l, const float (&o)[8])
-{
-    const dbs_window_args &a = A.a;
-    const int lane = threadIdx.x & 31;
-    T *out = (T *)a.out + b * a.o_batch + t * a.o_token + h * a.o_head;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (lane + 32 * e < a.head_dim) out[lane + 32 * e] = from_f32<T>(l == 0.f ? 0.f : o[e] / l);
-}
-template <class T>
-__device__ __forceinline__ void store_row(const Win &A, int64_t b, int t, int h, float m, float l, const float (&o)[8])
-{
-    const dbs_window_args &a = A.a;
-    store_out<T>(A, b, t, h, l, o);
-    if (a.lse && (threadIdx.x & 31) == 0) a.lse[(b * a.tokens + t) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 constexpr int ROW_NT = 128;
@@ -159,7 +99,7 @@ __global__ void __launch_bounds__(ROW_NT) k_window_rows(Win A)
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] += f * s_o[w][lane + 32 * e];
         }
-        store_row<T>(A, b, t, (int)h, top, sum, o);
+        store_row<T>(a, b, t, (int)h, top, sum, o);
     }
 }
 
@@ -259,57 +199,8 @@ template <class T> __device__ __forceinline__ bool spoiled(const Win &A, const R
 
 // ---- few rows: every warp streams its own entries ----
 
-// Tensor maps of K and V: [pages, entries, heads, head_dim], boxes of 64 columns of one head
-// of `box` entries.
-struct Maps {
-    CUtensorMap k, v;
-    int box;
-};
-
-__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap *map, int d, int head, int entry, int page, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-                 "l"(map), "r"(bar), "r"(d), "r"(head), "r"(entry), "r"(page) : "memory");
-}
 // Fetches a map before its first copy asks for it.
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-template <class T> __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    if constexpr (__is_same(T, __half))
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float remote(const void *p, int block)
-{
-    uint32_t at;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(block));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
-}
-__device__ __forceinline__ void cluster_sync() { asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory"); }
-
-constexpr int FEW_NT = 128, FEW_W = FEW_NT / 32;
-constexpr int FEW_ROWS = 16;               // one matrix instruction's rows
-constexpr int FEW_STEP = 16;               // entries of a stage of a warp
-constexpr int FEW_KEYS = FEW_W * FEW_STEP;
-constexpr int FEW_SPLIT = 16;              // blocks of a cluster, at most
-
 template <int DP> struct Few {
     static constexpr int STAGES = DP == 64 ? 6 : 3;
     static constexpr int SUB = FEW_STEP * 128, HALF = DP / 64 * SUB;       // 64 columns of a stage's K; all of it
@@ -625,7 +516,7 @@ __global__ void __launch_bounds__(FEW_NT) k_window_few(Win A, int groups, int sp
             for (int e = 0; e < 8; ++e) out = e == e0 ? ol[e] : out;
         }
         if (col < a.head_dim) ((T *)a.out + b * a.o_batch + row.t * a.o_token + row.h * a.o_head)[col] = from_f32<T>(lo == 0.f ? 0.f : out / lo);
-        if (a.lse && e0 == 0 && lane == 0) a.lse[(b * a.tokens + row.t) * a.q_heads + row.h] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+        if (a.lse && e0 == 0 && lane == 0) store_lse(a, b, row.t, row.h, top, l);
     }
     // (no block ends while another one reads its shared memory)
     if (split > 1) cluster_sync();
@@ -757,13 +648,6 @@ template <int KEYS> __device__ __forceinline__ Idle idle_of(const Win &A, const 
     return {A.sinks < end ? A.sinks / KEYS : 1, A.sinks < end ? (end - 1) / KEYS : 0, r.n % KEYS ? r.n / KEYS : -1};
 }
 
-// (to 2 units of the last place, and 0 below 2^-126: far below the 16 bits that P keeps)
-__device__ __forceinline__ float pow2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float max_of(float a, float b, float c)
 {
     float v;
@@ -787,11 +671,6 @@ __device__ __forceinline__ void st8(uint32_t a, const uint32_t (&r)[16])
 }
 // The lowest n bits, for any n.
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
-// 32 bytes, a whole sector, at once.
-__device__ __forceinline__ void store32(float *p, float a, float b, float c, float d, float e, float f, float g, float h)
-{
-    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d), "f"(e), "f"(f), "f"(g), "f"(h) : "memory");
-}
 // A part's place in scratch: the rows' outputs, maxima and sums.
 template <int DP, int TILES> __host__ __device__ constexpr int64_t part_floats() { return TILES * 128 * (int64_t)(DP + 2); }
 template <int DP, int TILES> __device__ __forceinline__ float *part_of(const Cut &C, int u, int rank)
@@ -1018,7 +897,7 @@ __global__ void __launch_bounds__(Many<DP, TILES>::NT, 1) k_window_many(Win A, C
                 if (!spoiled<T>(A, U.r, U.b, U.hk, pk)) continue;
                 float ol[8], m1, l1;
                 row_by_warp<T, true>(A, U.s, U.b, tk, hh, 0, 1, m1, l1, ol);
-                store_out<T>(A, U.b, tk, hh, l1, ol);
+                store_out<T>(a, U.b, tk, hh, l1, ol);
             }
         }
     } else {
@@ -1248,11 +1127,11 @@ __global__ void __launch_bounds__(JOIN_NT) k_window_join(Win A, Cut C)
         if (l == 0.f) o[e] = 0.f;
         odd |= !isfinite(o[e]);
     }
-    store_row<T>(A, b, t, h, top, l, o);
+    store_row<T>(a, b, t, h, top, l, o);
     if (l == l && __any_sync(~0u, odd) && spoiled<T>(A, range_of(A, s, t0, t0 + TILES * C.tokens - 1, 1), b, hk, s.first + t)) {
         float m1, l1;
         row_by_warp<T, true>(A, s, b, t, h, 0, 1, m1, l1, o);
-        store_out<T>(A, b, t, h, l1, o);
+        store_out<T>(a, b, t, h, l1, o);
     }
 }
 
@@ -1285,46 +1164,6 @@ bool args_ok(const dbs_window_args *a)
 }
 
 // ---- host ----
-
-bool aligned8(int64_t v) { return (v & 7) == 0; }
-
-// 16-byte copies of heads: every head starts on such a boundary.
-bool on_vectors(const dbs_window_args &a)
-{
-    return a.head_dim % 8 == 0 && aligned16(a.q) && aligned16(a.k) && aligned16(a.v) && aligned8(a.q_batch) && aligned8(a.q_token) &&
-           aligned8(a.q_head) && aligned8(a.k_page) && aligned8(a.k_entry) && aligned8(a.k_head) && aligned8(a.v_page) &&
-           aligned8(a.v_entry) && aligned8(a.v_head);
-}
-
-// Boxes of the caches, of `most` entries or as many as divide a page, or false where pages or
-// strides do not allow them.
-bool make_maps(const dbs_window_args &a, int most, Maps &M)
-{
-    const encode_tiled_fn encode = encode_tiled();
-    if (!encode || a.page_size < 1 || a.pages < 1 || a.max_pages < 1) return false;
-    // a sequence's own page is one run of entries; pages of a table split into boxes
-    M.box = most;
-    if (a.page_table)
-        while (M.box >= 8 && a.page_size % M.box) M.box /= 2;
-    if (M.box < 8) return false;
-    for (int i = 0; i < 2; ++i) {
-        const cuuint64_t dims[4] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.kv_heads, (cuuint64_t)a.page_size, (cuuint64_t)a.pages};
-        const int64_t by[3] = {i ? a.v_head : a.k_head, i ? a.v_entry : a.k_entry, i ? a.v_page : a.k_page};
-        const cuuint32_t box[4] = {64, 1, (cuuint32_t)M.box, 1}, ones[4] = {1, 1, 1, 1};
-        cuuint64_t strides[3];
-        for (int d = 0; d < 3; ++d) {
-            // (a dimension of one entry has any stride)
-            const int64_t bytes = dims[d + 1] == 1 ? 16 * a.head_dim : by[d] * 2;
-            if (bytes <= 0 || bytes >= int64_t(1) << 40 || dims[d + 1] >= cuuint64_t(1) << 31) return false;
-            strides[d] = (cuuint64_t)bytes;
-        }
-        if (encode(i ? &M.v : &M.k, a.dtype == DBS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                   const_cast<void *>(i ? a.v : a.k), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return false;
-    }
-    return true;
-}
 
 // Entries that a unit of `tokens` tokens may have, all that the line may hold.
 int64_t line_of(const dbs_window_args &a, int64_t tokens)
@@ -1369,19 +1208,8 @@ dbs_status launch_few(const Win &A, const Maps &maps, cudaStream_t s)
 // Q's rows as boxes of a row tile: 64 columns of a kv head's query heads of `tokens` tokens.
 bool make_q_map(const dbs_window_args &a, int group, int tokens, CUtensorMap &map)
 {
-    const encode_tiled_fn encode = encode_tiled();
     const cuuint64_t dims[4] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.q_heads, (cuuint64_t)a.tokens, (cuuint64_t)a.batch};
-    const int64_t by[3] = {a.q_head, a.q_token, a.q_batch};
-    const cuuint32_t box[4] = {64, (cuuint32_t)group, (cuuint32_t)tokens, 1}, ones[4] = {1, 1, 1, 1};
-    cuuint64_t strides[3];
-    for (int d = 0; d < 3; ++d) {
-        const int64_t bytes = dims[d + 1] == 1 ? 16 * a.head_dim : by[d] * 2;
-        if (bytes <= 0 || bytes >= int64_t(1) << 40) return false;
-        strides[d] = (cuuint64_t)bytes;
-    }
-    return encode && encode(&map, a.dtype == DBS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                            const_cast<void *>(a.q), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return map_of(map, a.dtype, a.q, dims, {a.q_head, a.q_token, a.q_batch}, {64, (cuuint32_t)group, (cuuint32_t)tokens, 1});
 }
 
 template <class T, int DP, int TILES>
@@ -1495,9 +1323,8 @@ dbs_status dbs_window_attention(const dbs_window_args *a, void *stream)
     if (P.scratch > 0 && (!a->scratch || (reinterpret_cast<uintptr_t>(a->scratch) & 31u) || a->scratch_bytes < P.scratch)) return DBS_ERR_INVALID_ARG;
     P.cut.scratch = (float *)a->scratch;
     constexpr int64_t MOST = 0x7fffffff - 1023;                          // (as many entries as there may be)
-    const bool wide_out = aligned16(a->out) && aligned8(a->o_batch) && aligned8(a->o_token) && aligned8(a->o_head);
     const Win A{*a, a->scale * 1.4426950408889634f, (int)(a->window < MOST ? a->window : MOST), (int)(a->sinks < MOST ? a->sinks : MOST),
-                a->q_heads / a->kv_heads, wide_out, waits()};
+                a->q_heads / a->kv_heads, wide_out(a->out, a->o_batch, a->o_token, a->o_head), waits()};
     return a->dtype == DBS_F16 ? launch<__half>(A, P, (cudaStream_t)stream) : launch<__nv_bfloat16>(A, P, (cudaStream_t)stream);
 }
 
