@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
 #pragma unroll
                     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
                     const float f = weight_of(m, l, top);
-                    l *= f;
+                    l = weighed(f, l);
 #pragma unroll
                     for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
 #pragma unroll

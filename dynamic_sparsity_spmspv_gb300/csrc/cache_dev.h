@@ -85,6 +85,8 @@ __device__ __forceinline__ void store_row(const A &a, int64_t b, int t, int h, f
 // times that.  A part without a maximum has nothing, or a NaN that has to stay.  The product is taken even where the
 // weight is 0: a NaN in a part is one in the row, however little it weighs.
 __device__ __forceinline__ float weight_of(float m, float l, float top) { return m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2f(m - top); }
+// Its sum times that, rounded by itself: the lanes add theirs in pairs, and both of a pair have to come to the same.
+__device__ __forceinline__ float weighed(float f, float l) { return __fmul_rn(f, l); }
 
 // ---- 16 rows: asynchronous copies, fragments, matrix instructions ----
 

@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(FEW_NT) k_window_few(Win A, int groups, int sp
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
         const float f = weight_of(m, l, top);
-        l *= f;
+        l = weighed(f, l);
 #pragma unroll
         for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
 #pragma unroll
@@ -1107,7 +1107,7 @@ __global__ void __launch_bounds__(JOIN_NT) k_window_join(Win A, Cut C)
 #pragma unroll
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
     const float f = weight_of(m, l, top);
-    l *= f;
+    l = weighed(f, l);
 #pragma unroll
     for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
     if (t >= s.tokens || s.first + t < 0) l = 0.f;
