@@ -1619,7 +1619,7 @@ bool args_ok(const dbs_attention_args *a)
         if (stride < 0) return false;
     // heads of out that share memory
     const Places out(a->out, 2, a->head_dim, {{a->batch, a->o_batch}, {a->tokens, a->o_token}, {a->q_heads, a->o_head}});
-    if (!out.own()) return false;
+    if (!out.own) return false;
     if (!a->page_table && (a->max_pages > 1 || (entries > 0 && a->pages < a->batch))) return false;
     return true;
 }

@@ -720,7 +720,7 @@ dbs_status dbs_norm_rotary(const dbs_norm_heads *parts, int32_t nparts, dbs_dtyp
         if (!P.out) return DBS_ERR_INVALID_ARG;
         const int64_t n_batch = P.to_slots ? pages : batch, n_token = P.to_slots ? page_size : tokens;
         const Places out(P.out, size_of(dtype), head_dim, {{n_batch, P.out_batch}, {n_token, P.out_token}, {P.heads, P.out_head}});
-        if (backwards(P.in_batch, P.in_token, P.in_head) || !out.own() || (P.to_slots && P.in == P.out)) return DBS_ERR_INVALID_ARG;
+        if (backwards(P.in_batch, P.in_token, P.in_head) || !out.own || (P.to_slots && P.in == P.out)) return DBS_ERR_INVALID_ARG;
         // (of a cache only the slots are written, which the host does not know)
         if (!P.to_slots) writes[A.nparts] = out;
         reads[A.nparts] = {P.in, size_of(dtype), head_dim, {{batch, P.in_batch}, {tokens, P.in_token}, {P.heads, P.in_head}}};
@@ -770,7 +770,7 @@ dbs_status dbs_norm_rotary_gradient(const dbs_norm_gradient_heads *parts, int32_
         if (P.heads) {
             if (!P.grad || !P.in || !P.out || (dim > 0 && (!table || !positions))) return DBS_ERR_INVALID_ARG;
             const Places out(P.out, size_of(dtype), head_dim, {{batch, P.out_batch}, {tokens, P.out_token}, {P.heads, P.out_head}});
-            if (backwards(P.grad_batch, P.grad_token, P.grad_head) || backwards(P.in_batch, P.in_token, P.in_head) || !out.own())
+            if (backwards(P.grad_batch, P.grad_token, P.grad_head) || backwards(P.in_batch, P.in_token, P.in_head) || !out.own)
                 return DBS_ERR_INVALID_ARG;
             writes[p] = out;
             grads[p] = {P.grad, size_of(dtype), head_dim, {{batch, P.grad_batch}, {tokens, P.grad_token}, {P.heads, P.grad_head}}};

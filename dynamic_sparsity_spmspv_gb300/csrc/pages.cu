@@ -679,7 +679,7 @@ bool data_ok(const dbs_cache_data *c, const dbs_page_state *s, bool work, bool s
         if (by < 0 || by >= int64_t(1) << 50) return false;
     const Places k(c->k, c->element_bytes, c->head_dim, {{c->layers, c->k_layer}, {s->pages, c->k_page}, {s->page_size, c->k_entry}, {c->heads, c->k_head}}),
         v(c->v, c->element_bytes, c->head_dim, {{c->layers, c->v_layer}, {s->pages, c->v_page}, {s->page_size, c->v_entry}, {c->heads, c->v_head}});
-    return k.own() && v.own() && (!k.meets(v) || (same && k.same(v)));
+    return k.own && v.own && (!k.meets(v) || (same && k.same(v)));
 }
 
 // f(V) with V the unit's type.

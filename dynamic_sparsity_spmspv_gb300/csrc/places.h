@@ -8,25 +8,31 @@ namespace dbs::ops {
 
 // A strided tensor: runs of contiguous elements, in each of up to four dimensions
 // `count` of them, `step` bytes apart.  Dimensions of one run are left out, the others
-// lie by ascending steps.  (Wide numbers: a product of any two sizes fits.)
+// lie by ascending steps.  (In bytes; what no memory holds counts as MOST.)
 struct Places {
     using Big = __int128;
+    static constexpr int64_t MOST = int64_t(1) << 60;
     struct Dim {
         int64_t count, stride;     // in elements, 0 or more
     };
     uintptr_t at;
-    Big run, count[4], step[4];
+    int64_t run, extent;           // bytes of a run, and from the first one's begin to the last one's end
+    int64_t count[4], step[4];
     int n = 0;
     bool none = true;              // no run at all
+    // Whether every run has a place of its own: each dimension steps over all that the finer ones
+    // take.  (Dimensions permuted or cut out of a contiguous tensor do; strides whose runs lie
+    // apart without that are not known as such.)
+    bool own = true;
 
-    Places() : at(0), run(0) {}
+    Places() : at(0), run(0), extent(0) {}
     Places(const void *p, int64_t element, int64_t run_elements, std::initializer_list<Dim> dims)
-        : at(reinterpret_cast<uintptr_t>(p)), run((Big)element * run_elements), none(run_elements <= 0)
+        : at(reinterpret_cast<uintptr_t>(p)), run(product(element, run_elements)), extent(run), none(run_elements <= 0)
     {
         for (const Dim &d : dims) {
             none = none || d.count <= 0;
             if (d.count <= 1) continue;
-            const Big s = (Big)element * d.stride;
+            const int64_t s = product(element, d.stride);
             int i = n++;
             for (; i > 0 && step[i - 1] > s; --i) {
                 step[i] = step[i - 1];
@@ -35,30 +41,16 @@ struct Places {
             step[i] = s;
             count[i] = d.count;
         }
-    }
-    // Whether every run has a place of its own: each dimension steps over all that the finer ones
-    // take.  (Dimensions permuted or cut out of a contiguous tensor do; strides whose runs lie
-    // apart without that are not known as such.)
-    bool own() const
-    {
-        Big extent = run;
-        for (int i = 0; !none && i < n; ++i) {
-            if (step[i] < extent) return false;
-            extent += (count[i] - 1) * step[i];
+        for (int i = 0; i < n; ++i) {
+            own = own && (none || step[i] >= extent);
+            extent = capped(product(count[i] - 1, step[i]) + extent);
         }
-        return true;
-    }
-    Big extent() const             // bytes from the first run's begin to the last one's end
-    {
-        Big e = run;
-        for (int i = 0; i < n; ++i) e += (count[i] - 1) * step[i];
-        return e;
     }
     bool dense() const
     {
-        Big all = run;
-        for (int i = 0; i < n; ++i) all *= count[i];
-        return own() && all == extent();
+        int64_t all = run;
+        for (int i = 0; i < n; ++i) all = product(all, count[i]);
+        return own && all == extent && extent < MOST;
     }
     bool same(const Places &o) const
     {
@@ -72,15 +64,15 @@ struct Places {
     bool meets(const Places &o) const
     {
         if (none || o.none) return false;
-        const Big gap = (Big)o.at - (Big)at;
-        if (gap >= extent() || -gap >= o.extent()) return false;
+        const int64_t gap = (int64_t)(o.at - at);          // (addresses are below 2^62)
+        if (gap >= extent || -gap >= o.extent) return false;
         if (dense() && o.dense()) return true;
         // Run y of `o` begins gap + sum y step' - sum x step behind run x of this: from -o.run + 1 to run - 1
         // they meet.  By steps, with the differences of index that there are of each:
         Big by[8], lo[8], hi[8];
         int k = 0;
         for (int i = 0, j = 0; i < n || j < o.n;) {
-            const Big s = j == o.n || (i < n && step[i] < o.step[j]) ? step[i] : o.step[j];
+            const int64_t s = j == o.n || (i < n && step[i] < o.step[j]) ? step[i] : o.step[j];
             by[k] = s;
             lo[k] = hi[k] = 0;
             for (; i < n && step[i] == s; ++i) lo[k] -= count[i] - 1;
@@ -92,6 +84,12 @@ struct Places {
     }
 
 private:
+    static int64_t capped(int64_t v) { return v < MOST ? v : MOST; }
+    static int64_t product(int64_t a, int64_t b)
+    {
+        int64_t v;
+        return __builtin_mul_overflow(a, b, &v) ? MOST : capped(v);
+    }
     bool found(Big gap, const Big *by, const Big *lo, const Big *hi, int k, Big other, int &tries) const
     {
         if (--tries < 0) return false;

@@ -273,7 +273,7 @@ dbs_status dbs_rotary(const dbs_rotary_heads *parts, int32_t nparts, dbs_dtype d
         // heads of the output that share memory
         const int64_t n_batch = P.to_slots ? pages : batch, n_token = P.to_slots ? page_size : tokens;
         const Places out(P.out, dtype == DBS_F32 ? 4 : 2, head_dim, {{n_batch, P.out_batch}, {n_token, P.out_token}, {P.heads, P.out_head}});
-        if (work && (P.in_head < 0 || P.in_token < 0 || P.in_batch < 0 || !out.own() || (P.to_slots && P.in == P.out))) return DBS_ERR_INVALID_ARG;
+        if (work && (P.in_head < 0 || P.in_token < 0 || P.in_batch < 0 || !out.own || (P.to_slots && P.in == P.out))) return DBS_ERR_INVALID_ARG;
         // (of a cache only the slots are written, which the host does not know)
         if (work && !P.to_slots) writes[A.nparts] = out;
         if (work) reads[A.nparts] = {P.in, dtype == DBS_F32 ? 4 : 2, head_dim, {{batch, P.in_batch}, {tokens, P.in_token}, {P.heads, P.in_head}}};

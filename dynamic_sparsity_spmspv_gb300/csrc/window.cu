@@ -1155,7 +1155,7 @@ bool args_ok(const dbs_window_args *a)
     // heads of out that share memory, or are the inputs'
     const int64_t pages = entries > 0 ? a->pages : 0;
     const Places out(a->out, 2, a->head_dim, {{a->batch, a->o_batch}, {a->tokens, a->o_token}, {a->q_heads, a->o_head}});
-    if (!out.own() || out.meets({a->q, 2, a->head_dim, {{a->batch, a->q_batch}, {a->tokens, a->q_token}, {a->q_heads, a->q_head}}}) ||
+    if (!out.own || out.meets({a->q, 2, a->head_dim, {{a->batch, a->q_batch}, {a->tokens, a->q_token}, {a->q_heads, a->q_head}}}) ||
         out.meets({a->k, 2, a->head_dim, {{pages, a->k_page}, {a->page_size, a->k_entry}, {a->kv_heads, a->k_head}}}) ||
         out.meets({a->v, 2, a->head_dim, {{pages, a->v_page}, {a->page_size, a->v_entry}, {a->kv_heads, a->v_head}}}))
         return false;
