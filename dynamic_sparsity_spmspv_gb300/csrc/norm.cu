@@ -591,8 +591,9 @@ dbs_status launch_gradient(Gradient &A, int head_dim, int dim, cudaStream_t s)
     bool sum = false;
     for (int p = 0; p < A.nparts; ++p) {
         const int64_t items = A.total * ((A.part[p].heads + span - 1) / span), most = (items + groups - 1) / groups;
-        int64_t share = heads ? ((int64_t)A.room * A.part[p].heads + heads - 1) / heads : 0;
-        share = share < A.room ? share : A.room;
+        // (no more blocks than find room at once, in both groups together: one more would run when the others have ended)
+        int64_t share = heads ? (int64_t)A.room * A.part[p].heads / heads : 0;
+        if (share == 0) share = 1;
         A.blocks[p] = (int)(most < share ? most : share);
         blocks += A.blocks[p];
         sum = sum || A.part[p].weight_grad;
