@@ -14,8 +14,8 @@ constexpr int NT = 256;
 // heads of one unit a lane.  Forward the next heads are loaded before these are worked on (16,382 tokens of 40 heads of
 // 128, bf16: 2, 3 and 12 60 us, 2, 3 and 8 61, 2, 2 and 8 66, 3, 1 and 8 67, 2, 4 and 16 78 (registers spilled);
 // without that 3, 2 and 8 71).  The gradient has registers left for it in 16 bits only (8192 tokens of 32 heads of 96, f32: 2, 2 and
-// 8 66 us, 2, 2 and 4 69, 3 and 1 79; loading ahead 68 with one head, 78 with two; of 40 heads of 128, bf16: 95, without 116,
-// with 3 blocks 110, with 4 heads 128).
+// 8 64 us, 2, 2 and 4 66, 2, 4 and 8 72, 2, 1 and 8 79, 3, 2 and 8 89 (spilled); loading ahead 76; of 40 heads of 128, bf16: 62,
+// without loading ahead 74, with 1 head 72, 4 heads 90, 3 blocks 89, a span of 4 71).
 constexpr int FORWARD_BLOCKS = 2, FORWARD_HEADS = 3, FORWARD_SPAN = 12, BACKWARD_BLOCKS = 2, BACKWARD_HEADS = 2, BACKWARD_SPAN = 8;
 
 // What a lane moves at once: N values, 16 or 8 bytes, or one where rows are not aligned for that.
@@ -421,8 +421,10 @@ struct Gradient {
 // the grid's turn; what the heads give to weight' stays in its registers.  In the end the block's
 // groups are added up in their order and written to scratch, and k_norm_weight adds the blocks.
 // Two entries are read and one is written (f32, 303 MB in 66 us, 67% of the memory's rate; bf16, 8192 tokens of 40 heads of
-// 128, 252 MB in 95 us, 39%).  Bound by instructions, some 200 for a lane's eight values of a head with its two sums over
-// lanes, and by their latencies with 16 warps, more of which registers do not allow.
+// 128, 252 MB in 62 us, 60%).  Bound by latencies with 16 warps, more of which registers do not allow: in fp32 by the memory's,
+// whose loads wait for the heads before them (issue 37% of the active cycles, 4.5 warps waiting for memory at each instruction); in
+// 16 bits, with the next heads under way, by those of its instructions, 234 of a warp for two heads and their sums
+// over lanes (issue 58%; waiting for an instruction before 1.9, for exchanges 1.1, for memory 1.1).
 template <class T, bool INTERLEAVED, int N, int K>
 __global__ void __launch_bounds__(NT, K == 1 ? BACKWARD_BLOCKS : 1) k_norm_gradient(Gradient A, int span)
 {
@@ -629,12 +631,13 @@ template <class T, int N> bool on_pieces(const void *p, int64_t b, int64_t t, in
 
 // Values of a piece.  Forward 16 bytes of them.  The gradient holds twice as much of a head
 // beside its weights and their sums, so it takes half as many of 16 bits (with 16 bytes of them, and one block of a
-// multiprocessor instead of two, 98 us for 95 above).
+// multiprocessor instead of two: 59 us for 62 above, 53 for 55 with heads of 256, as many with heads of 96).
 template <class T> constexpr int FORWARD = 16 / (int)sizeof(T);
 template <class T> constexpr int BACKWARD = 4;
 
 // The kernel for a head's size: units of a lane (at most 1024 entries, and the last piece of each part may
-// have no second).
+// have no second).  The gradient's kernels of many units, for heads above 256 entries, spill registers (2048 tokens of 10 heads of
+// 512: bf16 81 us, f32 97, floors 9 and 18; of 1024 91 and 120).
 template <class T, bool INTERLEAVED> dbs_status norm_of(Norm &A, int head_dim, int dim, bool wide, cudaStream_t s)
 {
     constexpr int N = FORWARD<T>;

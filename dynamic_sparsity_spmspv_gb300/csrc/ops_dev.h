@@ -1,5 +1,5 @@
-// Device helpers shared by the decoding-step operators (w4.cu, rotary.cu,
-// attention.cu, logits.cu).
+// Device helpers shared by the operators of a decoding step and around a cache (w4.cu, rotary.cu,
+// norm.cu, attention.cu, window.cu, pages.cu, logits.cu).
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
