@@ -60,13 +60,13 @@ struct Places {
     }
     // Whether some byte is surely in both: both are without gaps and their spans meet, or two runs are
     // found that do (always, if there are any, where each larger step of the two goes over what the
-    // smaller ones take: tensors of one layout cut out of one buffer).
+    // smaller ones take: tensors of one layout cut out of one buffer; else among a thousand tries).
     bool meets(const Places &o) const
     {
         if (none || o.none) return false;
         const int64_t gap = (int64_t)(o.at - at);          // (addresses are below 2^62)
         if (gap >= extent || -gap >= o.extent) return false;
-        if (dense() && o.dense()) return true;
+        if ((gap < run && -gap < o.run) || (dense() && o.dense())) return true;        // (the first runs meet)
         // Run y of `o` begins gap + sum y step' - sum x step behind run x of this: from -o.run + 1 to run - 1
         // they meet.  By steps, with the differences of index that there are of each:
         Big by[8], lo[8], hi[8];

@@ -322,3 +322,18 @@ def test_arrays_of_a_cache_s_pages_that_overlap_are_refused():
     for kw in (dict(new=4 * FAR + 8), dict(new=5 * FAR + 44), dict(new=6 * FAR - 8), dict(new=2 * FAR - 8), dict(new=FAR + 12), dict(d=data(k=7 * FAR, v=7 * FAR)),
                dict(d=data(k=7 * FAR, v=7 * FAR + 2 * 18432 * 2 - 2))):
         assert compact(**kw) == BAD, kw
+
+
+@pytest.mark.parametrize("tokens,heads", [(4, 2), (300, 40), (2000, 128)])
+def test_outputs_at_an_input_s_address_with_other_strides_are_refused(tokens, heads):
+    """Heads before tokens and tokens before heads, with room between heads: places that meet in many ways or few, the first of them for certain."""
+    step = 72
+    plain, turned = (0, heads * step, step), (0, step, tokens * step)
+    for a, b in ((plain, turned), (turned, plain)):
+        assert norm(tokens=tokens, parts=part(inp=FAR, out=FAR, heads=heads, strides=a + b)) == BAD
+        assert gradient(tokens=tokens, parts=gpart(grad=FAR, inp=2 * FAR, out=FAR, dw=0, heads=heads, strides=a + a + b)) == BAD
+        need = ctypes.c_int64(-1)
+        w = {**WIN, "batch": 1, "tokens": tokens, "hq": heads, "hk": 2, "q": FAR, "out": FAR, "q1": a[1], "q2": a[2], "o1": b[1], "o2": b[2]}
+        assert _lib.load().dbs_window_attention_scratch(_lib.WINDOW_ARGS.pack(*w.values()), ctypes.byref(need)) == BAD
+        turn = struct.pack("@" + _lib.ROTARY_HEADS, FAR, FAR, *a, *b, heads, 1, 0)
+        assert _lib.load().dbs_rotary(turn, 1, 2, 1, tokens, 64, 64, A, 10, A, 0, 0, 1, 0, 0, None) == BAD
