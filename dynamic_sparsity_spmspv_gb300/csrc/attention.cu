@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(ROW_NT) k_attn_rows(Attn A)
                 f = weight_of(s_m[w], s_l[w], top);
                 sum += f * s_l[w];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] += f == 0.f ? 0.f : f * s_o[w][lane + 32 * e];
+                for (int e = 0; e < 8; ++e) o[e] += f * s_o[w][lane + 32 * e];
             }
             store_row<T>(a, b, t, h, top, sum, o);
         }
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(JOIN_NT) k_attn_join(Attn A, Share S, int rows
                         const float fi = __shfl_sync(~0u, f, (i + k * split) & 31);
                         if (i + k * split >= now_parts) break;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] += fi == 0.f ? 0.f : fi * v[k][e];
+                        for (int e = 0; e < 8; ++e) o[e] += fi * v[k][e];
                     }
                 }
             }
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
                     const float *po = (const float *)(ring + w * (FEW_STAGES * 2 * HALF)) + r * DP;
                     sum += f * s_l[w][r];
 #pragma unroll
-                    for (int e = 0; e < DP / 32; ++e) oo[e] += f == 0.f ? 0.f : f * po[lane + 32 * e];
+                    for (int e = 0; e < DP / 32; ++e) oo[e] += f * po[lane + 32 * e];
                 }
                 if (CLUSTER) {
 #pragma unroll
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(FEW_NT) k_attn_few(Attn A, Share S, int split)
 #pragma unroll
                     for (int k = 0; k < FEW_SPLIT; ++k) {
                         const float fk = __shfl_sync(~0u, f, k);
-                        o += fk == 0.f ? 0.f : fk * v[k];
+                        o += fk * v[k];
                     }
                     if (row.t >= s.tree) {
                         l = 0.f;

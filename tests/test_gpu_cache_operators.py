@@ -1252,3 +1252,24 @@ def test_window_long_line_with_values_that_are_not_finite(T):
     o, mag, lse = window_ref_gpu(q, k, v, [S], [T], S, 2, table)
     assert torch.isnan(got[:, before:]).all() and ((gl - lse).abs() <= 4e-4).all()
     assert ((got[:, :before].double() - o[:, :before]).abs() <= (U["bf16"] + 3e-4) * mag[:, :before] + U["bf16"] * o[:, :before].abs()).all()
+
+
+@pytest.mark.parametrize("B,T,hq,hk,D,S,page", [(1, 1, 8, 2, 128, 4000, 16), (1, 1, 4, 1, 64, 40000, 0), (1, 2, 4, 2, 64, 2500, 5), (1, 1, 4, 2, 33, 600, 16), (1, 40, 4, 1, 64, 3000, 16),
+                                                (2, 100, 2, 2, 128, 2000, 24), (1, 30, 4, 1, 256, 1500, 64), (3, 7, 2, 2, 128, 5000, 16)])
+@pytest.mark.parametrize("loud,odd", [(5, 2), (2, 5)])
+def test_tree_values_count_however_little_they_weigh(B, T, hq, hk, D, S, page, loud, odd):
+    """As above for drafted tokens: one value that is not finite, in the part that all see, in an entry whose weight is 0 in fp32."""
+    q, one = torch.ones((B, T, hq, D), dtype=torch.bfloat16, device=DEV), dict(dtype=torch.bfloat16, device=DEV)
+    per = -(-S // page) if page else 1
+    shape = (B * per, page, hk, D) if page else (B, S, hk, D)
+    table = torch.arange(B * per, dtype=torch.int32, device=DEV).view(B, per) if page else None
+    k, v = torch.zeros(shape, **one), torch.ones(shape, **one)
+    kb, vb = k.view(B, -1, hk, D), v.view(B, -1, hk, D)
+    kb[:, loud * (S - T) // 6] = 64
+    out, lse = dbs.tree_attention(q, k, v, ints([S] * B), page_table=table, return_lse=True)
+    assert (out == 1).all() and torch.isfinite(lse).all()
+    for value in (NAN, INF):
+        vb[:, odd * (S - T) // 6, :, 1] = value
+        got, gl = dbs.tree_attention(q, k, v, ints([S] * B), page_table=table, return_lse=True)
+        assert not torch.isfinite(got[..., 1]).any() and torch.equal(gl, lse)
+        assert (got[..., [c for c in range(D) if c != 1]] == 1).all()
