@@ -10,8 +10,7 @@ namespace dbs::ops {
 // `count` of them, `step` bytes apart.  Dimensions of one run are left out, the others
 // lie by ascending steps.  (In bytes; what no memory holds counts as MOST.)
 struct Places {
-    using Big = __int128;
-    static constexpr int64_t MOST = int64_t(1) << 60;
+    static constexpr int64_t MOST = int64_t(1) << 58;      // (sums of a few of it fit)
     struct Dim {
         int64_t count, stride;     // in elements, 0 or more
     };
@@ -67,9 +66,10 @@ struct Places {
         const int64_t gap = (int64_t)(o.at - at);          // (addresses are below 2^62)
         if (gap >= extent || -gap >= o.extent) return false;
         if ((gap < run && -gap < o.run) || (dense() && o.dense())) return true;        // (the first runs meet)
+        if (extent >= MOST || o.extent >= MOST) return false;
         // Run y of `o` begins gap + sum y step' - sum x step behind run x of this: from -o.run + 1 to run - 1
         // they meet.  By steps, with the differences of index that there are of each:
-        Big by[8], lo[8], hi[8];
+        int64_t by[8], lo[8], hi[8];
         int k = 0;
         for (int i = 0, j = 0; i < n || j < o.n;) {
             const int64_t s = j == o.n || (i < n && step[i] < o.step[j]) ? step[i] : o.step[j];
@@ -90,22 +90,22 @@ private:
         int64_t v;
         return __builtin_mul_overflow(a, b, &v) ? MOST : capped(v);
     }
-    bool found(Big gap, const Big *by, const Big *lo, const Big *hi, int k, Big other, int &tries) const
+    bool found(int64_t gap, const int64_t *by, const int64_t *lo, const int64_t *hi, int k, int64_t other, int &tries) const
     {
         if (--tries < 0) return false;
         if (k == 0) return gap > -other && gap < run;
         // what is left of the gap has to be within reach of the smaller steps
-        Big down = other, up = run;
+        int64_t down = other, up = run;
         for (int i = 0; i < k - 1; ++i) {
             down += hi[i] * by[i];
             up -= lo[i] * by[i];
         }
-        const Big s = by[k - 1];
-        auto floor_of = [&](Big v) { return v >= 0 ? v / s : -((-v + s - 1) / s); };
-        Big first = -floor_of(down + gap), last = floor_of(up - gap);
+        const int64_t s = by[k - 1];
+        auto floor_of = [&](int64_t v) { return v >= 0 ? v / s : -((-v + s - 1) / s); };
+        int64_t first = -floor_of(down + gap), last = floor_of(up - gap);
         if (first < lo[k - 1]) first = lo[k - 1];
         if (last > hi[k - 1]) last = hi[k - 1];
-        for (Big x = first; x <= last && tries > 0; ++x)
+        for (int64_t x = first; x <= last && tries > 0; ++x)
             if (found(gap + x * s, by, lo, hi, k - 1, other, tries)) return true;
         return false;
     }
