@@ -201,6 +201,7 @@ template <class T> __device__ __forceinline__ bool spoiled(const Win &A, const R
 
 // Fetches a map before its first copy asks for it.
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
+
 template <int DP> struct Few {
     static constexpr int STAGES = DP == 64 ? 6 : 3;
     static constexpr int SUB = FEW_STEP * 128, HALF = DP / 64 * SUB;       // 64 columns of a stage's K; all of it
